@@ -5,7 +5,9 @@ Argument marshalling only: every call goes straight to the C ABI declared in
 kernels. Arguments that are device arrays accept a torch CUDA tensor (its
 ``data_ptr()``) or a raw address; host pools accept a numpy array or a raw address;
 ``stream`` accepts a ``torch.cuda.Stream``, a raw ``cudaStream_t`` or None (the legacy
-default stream). A non-OK status raises :class:`HsError` carrying the status code.
+default stream). A non-OK status raises :class:`HsError` carrying the status code. The 4-bit
+cache's calls (``hs_fp4_*``, ``hs_pages_*``) also refuse, with ValueError, a tensor that is not on
+the current CUDA device.
 
 The in-tree ``libhs.so`` is loaded on first use; every entry point raises ImportError
 if it has not been built (``python -m hierarchical_sparse_attention_gb300.build``).
@@ -24,6 +26,7 @@ HS_OK, HS_ERR_INVALID_ARG, HS_ERR_INVALID_CONFIG, HS_ERR_CUDA, HS_ERR_DEVICE_FLA
 HS_FLAG_TOKEN, HS_FLAG_DUP, HS_FLAG_STATE, HS_FLAG_HOSTROW, HS_FLAG_DEVROW, HS_FLAG_SEQLEN = 1, 2, 4, 8, 16, 32
 HS_FLAG_ORDER = 64
 HS_FLAG_TIMEOUT = 128
+HS_FLAG_NOPAGE = 256
 HS_MAX_MLA_SPLITS = 16
 HS_MAX_TOP_K, HS_MAX_HOT_SLOTS, HS_MAX_LAYERS = 4096, 16384, 8
 
@@ -33,14 +36,28 @@ EXPORTS = ("hs_workspace_bytes", "hs_create", "hs_resolve", "hs_backup", "hs_get
            "hs_invalidate_tokens", "hs_invalidate_host_rows", "hs_resolve_layers", "hs_gather",
            "hs_resolve_spec", "hs_backup_spec", "hs_reset_hints", "hs_sparse_mla_workspace_bytes",
            "hs_sparse_mla_decode", "hs_launch_shape", "hs_resolve_spec_layers", "hs_gather_spec",
-           "hs_host_numa_node", "hs_host_bind_node", "hs_sparse_mla_launches")
+           "hs_host_numa_node", "hs_host_bind_node", "hs_sparse_mla_launches",
+           "hs_fp4_pack_rows", "hs_fp4_unpack_rows", "hs_fp4_mla_splits", "hs_fp4_mla_workspace_bytes",
+           "hs_fp4_sparse_mla_decode", "hs_fp4_window_mla_decode", "hs_pages_workspace_bytes", "hs_pages_init",
+           "hs_pages_extend", "hs_pages_fork", "hs_pages_free", "hs_pages_compact")
 HS_MAX_SPEC_QUERIES = 8
 HS_NOALLOC_MAX_LAYERS = 8
+HS_FP4_ROW_BYTES = 416
+HS_MAX_PAGE_REQUESTS = 65536
 
 
 class hs_config(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("max_requests", "top_k", "hot_slots", "row_bytes", "num_layers",
                                               "page_size", "max_context", "max_pages", "host_row_stride")]
+
+
+class hs_page_pool(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("num_requests", "max_pages", "num_pages", "page_size", "row_bytes",
+                                               "num_layers")] +
+                [("device_pools", ctypes.c_void_p * HS_MAX_LAYERS)] +
+                [(n, ctypes.c_void_p) for n in ("resident_pages", "page_refs", "free_pages", "free_count",
+                                                "error_flags", "workspace")] +
+                [("workspace_bytes", ctypes.c_size_t)])
 
 
 class HsError(RuntimeError):
@@ -106,6 +123,25 @@ def _load() -> ctypes.CDLL:
     lib.hs_host_bind_node.restype = ctypes.c_int
     lib.hs_resolve_noalloc.argtypes = [cfgp, P, P, i64, i64, i32] + [P] * 11 + [P]
     lib.hs_resolve_noalloc.restype = ctypes.c_int
+    f32, poolp = ctypes.c_float, ctypes.POINTER(hs_page_pool)
+    lib.hs_fp4_pack_rows.argtypes = [i32, P, i64, P, f32, P, i64, P, P]
+    lib.hs_fp4_unpack_rows.argtypes = [i32, P, i64, P, f32, P, i64, P, P]
+    lib.hs_fp4_mla_splits.argtypes = [i32, i32, i32, i64]
+    lib.hs_fp4_mla_splits.restype = i32
+    lib.hs_fp4_mla_workspace_bytes.argtypes = [i32, i32, i32, i32]
+    lib.hs_fp4_mla_workspace_bytes.restype = sz
+    lib.hs_fp4_sparse_mla_decode.argtypes = [i32] * 4 + [P, P, i64, P, f32, f32, P, P, P, sz, P, P]
+    lib.hs_fp4_window_mla_decode.argtypes = ([i32] * 6 + [P, P, i64, i32, i32, P, P, f32, f32, P, P, P, sz, P, P])
+    lib.hs_pages_workspace_bytes.argtypes = [i32, i32]
+    lib.hs_pages_workspace_bytes.restype = sz
+    lib.hs_pages_init.argtypes = [poolp, P]
+    lib.hs_pages_extend.argtypes = [poolp, i32, P, P, P, P, P]
+    lib.hs_pages_fork.argtypes = [poolp, i32, P, P, P, P, P]
+    lib.hs_pages_free.argtypes = [poolp, i32, P, P, P, P]
+    lib.hs_pages_compact.argtypes = [poolp, P]
+    for name in ("hs_fp4_pack_rows", "hs_fp4_unpack_rows", "hs_fp4_sparse_mla_decode", "hs_fp4_window_mla_decode",
+                 "hs_pages_init", "hs_pages_extend", "hs_pages_fork", "hs_pages_free", "hs_pages_compact"):
+        getattr(lib, name).restype = ctypes.c_int
     return lib
 
 
@@ -138,6 +174,29 @@ def _addr(x) -> Optional[int]:
             raise ValueError("arrays passed to libhs must be contiguous")
         return x.ctypes.data
     raise TypeError(f"cannot take the address of {type(x).__name__}")
+
+
+def _dev(x, rows: bool = False) -> Optional[int]:
+    """_addr of a device array, which has to be on the current device (a raw address is taken as it is).
+    rows: a 2-D array whose rows may be apart (the call says how far)."""
+    if x is None or isinstance(x, int):
+        return x
+    if not getattr(x, "is_cuda", False):
+        raise ValueError("this argument is read or written on the GPU: pass a CUDA tensor or a device address")
+    import torch
+    if x.device.index != torch.cuda.current_device():
+        raise ValueError(f"the tensor is on {x.device}, the current device is cuda:{torch.cuda.current_device()}")
+    if rows:
+        if x.dim() != 2 or x.stride(1) != 1:
+            raise ValueError("rows of consecutive values are needed")
+        return x.data_ptr()
+    return _addr(x)
+
+
+def _rows_of(x, stride: int) -> Optional[int]:
+    if not (x is None or isinstance(x, int)) and x.dim() == 2 and x.size(0) > 1 and x.stride(0) != stride:
+        raise ValueError(f"the rows are {x.stride(0)} values apart, not {stride}")
+    return _dev(x, rows=True)
 
 
 def _stream(s) -> Optional[int]:
@@ -284,6 +343,89 @@ def hs_sparse_mla_decode(num_requests: int, num_heads: int, top_k: int, splits: 
     _check(_lib.hs_sparse_mla_decode(num_requests, num_heads, top_k, splits, _addr(q), _addr(kv_pool), pool_rows,
                                      _addr(out_rows), float(sm_scale), _addr(o), _addr(lse), _addr(workspace),
                                      workspace_bytes, _addr(error_flags), _stream(stream)), "hs_sparse_mla_decode")
+
+
+def hs_fp4_pack_rows(n: int, kv, kv_stride: int, rows, latent_scale: float, pool, pool_rows: int, error_flags,
+                     stream=None) -> None:
+    """Quantise n tokens (bf16 [n, kv_stride], 576 used) into the 4-bit rows `rows` of the pool."""
+    _check(_lib.hs_fp4_pack_rows(n, _rows_of(kv, kv_stride), kv_stride, _dev(rows), latent_scale, _dev(pool),
+                                 pool_rows, _dev(error_flags), _stream(stream)), "hs_fp4_pack_rows")
+
+
+def hs_fp4_unpack_rows(n: int, pool, pool_rows: int, rows, latent_scale: float, kv, kv_stride: int, error_flags,
+                       stream=None) -> None:
+    """Read the 4-bit rows `rows` back as bf16 into kv ([n, kv_stride], 576 written)."""
+    _check(_lib.hs_fp4_unpack_rows(n, _dev(pool), pool_rows, _dev(rows), latent_scale, _rows_of(kv, kv_stride),
+                                   kv_stride, _dev(error_flags), _stream(stream)), "hs_fp4_unpack_rows")
+
+
+def hs_fp4_mla_splits(num_requests: int, num_heads: int, num_queries: int, rows: int) -> int:
+    """Splits that suit a call over up to `rows` rows per request on the current device."""
+    return int(_lib.hs_fp4_mla_splits(num_requests, num_heads, num_queries, rows))
+
+
+def hs_fp4_mla_workspace_bytes(num_requests: int, num_heads: int, num_queries: int, splits: int) -> int:
+    return int(_lib.hs_fp4_mla_workspace_bytes(num_requests, num_heads, num_queries, splits))
+
+
+def hs_fp4_sparse_mla_decode(num_requests: int, num_heads: int, top_k: int, splits: int, q, kv_pool, pool_rows: int,
+                             out_rows, sm_scale: float, latent_scale: float, o, lse, workspace, workspace_bytes: int,
+                             error_flags, stream=None) -> None:
+    _check(_lib.hs_fp4_sparse_mla_decode(num_requests, num_heads, top_k, splits, _dev(q), _dev(kv_pool), pool_rows,
+                                         _dev(out_rows), sm_scale, latent_scale, _dev(o), _dev(lse), _dev(workspace),
+                                         workspace_bytes, _dev(error_flags), _stream(stream)),
+           "hs_fp4_sparse_mla_decode")
+
+
+def hs_fp4_window_mla_decode(num_requests: int, num_heads: int, num_queries: int, window: int, sinks: int,
+                             splits: int, q, kv_pool, pool_rows: int, page_size: int, max_pages: int, seq_lens,
+                             resident_pages, sm_scale: float, latent_scale: float, o, lse, workspace,
+                             workspace_bytes: int, error_flags, stream=None) -> None:
+    _check(_lib.hs_fp4_window_mla_decode(num_requests, num_heads, num_queries, window, sinks, splits, _dev(q),
+                                         _dev(kv_pool), pool_rows, page_size, max_pages, _dev(seq_lens),
+                                         _dev(resident_pages), sm_scale, latent_scale, _dev(o), _dev(lse),
+                                         _dev(workspace), workspace_bytes, _dev(error_flags), _stream(stream)),
+           "hs_fp4_window_mla_decode")
+
+
+def hs_pages_workspace_bytes(num_requests: int, num_pages: int) -> int:
+    return int(_lib.hs_pages_workspace_bytes(num_requests, num_pages))
+
+
+def make_page_pool(device_pools: Sequence, num_requests: int, max_pages: int, num_pages: int, page_size: int,
+                   row_bytes: int, resident_pages, page_refs, free_pages, free_count, workspace, workspace_bytes: int,
+                   error_flags) -> hs_page_pool:
+    """The descriptor of the hs_pages_* calls. It keeps the tensors that it points to alive."""
+    if not 1 <= len(device_pools) <= HS_MAX_LAYERS:
+        raise ValueError(f"1 to {HS_MAX_LAYERS} device pools")
+    arrays = [_dev(x) for x in (resident_pages, page_refs, free_pages, free_count, error_flags, workspace)]
+    p = hs_page_pool(num_requests, max_pages, num_pages, page_size, row_bytes, len(device_pools),
+                     (ctypes.c_void_p * HS_MAX_LAYERS)(*[_dev(x) for x in device_pools]), *arrays, workspace_bytes)
+    p.kept = (list(device_pools), resident_pages, page_refs, free_pages, free_count, error_flags, workspace)
+    return p
+
+
+def hs_pages_init(pool: hs_page_pool, stream=None) -> None:
+    _check(_lib.hs_pages_init(pool, _stream(stream)), "hs_pages_init")
+
+
+def hs_pages_extend(pool: hs_page_pool, n: int, requests, old_lens, new_lens, granted=None, stream=None) -> None:
+    _check(_lib.hs_pages_extend(pool, n, _dev(requests), _dev(old_lens), _dev(new_lens), _dev(granted),
+                                _stream(stream)), "hs_pages_extend")
+
+
+def hs_pages_fork(pool: hs_page_pool, n: int, parents, children, lens, granted=None, stream=None) -> None:
+    _check(_lib.hs_pages_fork(pool, n, _dev(parents), _dev(children), _dev(lens), _dev(granted), _stream(stream)),
+           "hs_pages_fork")
+
+
+def hs_pages_free(pool: hs_page_pool, n: int, requests, first_pages=None, end_pages=None, stream=None) -> None:
+    _check(_lib.hs_pages_free(pool, n, _dev(requests), _dev(first_pages), _dev(end_pages), _stream(stream)),
+           "hs_pages_free")
+
+
+def hs_pages_compact(pool: hs_page_pool, stream=None) -> None:
+    _check(_lib.hs_pages_compact(pool, _stream(stream)), "hs_pages_compact")
 
 
 def hs_reset_hints(h: Handle, stream=None) -> None:

@@ -17,7 +17,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build", "hs")
 LIB = os.path.join(PKG, "libhs.so")
-SOURCES = ["hs_resolve.cu", "hs_backup.cu", "hs_gather.cu", "hs_invalidate.cu", "hs_sparse_mla.cu", "hs_api.cu", "hs_noalloc.cu"]
+SOURCES = ["hs_resolve.cu", "hs_backup.cu", "hs_gather.cu", "hs_invalidate.cu", "hs_sparse_mla.cu", "hs_fp4_rows.cu",
+           "hs_fp4_mla.cu", "hs_pages.cu", "hs_api.cu", "hs_noalloc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden",
               "-I", INCLUDE, "-I", CSRC]
@@ -37,7 +38,7 @@ def _stale(out: str, deps: List[str]) -> bool:
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
-    headers = [os.path.join(CSRC, "hs_internal.h"), os.path.join(INCLUDE, "hs.h")]
+    headers = [os.path.join(CSRC, "hs_internal.h"), os.path.join(CSRC, "hs_fp4.h"), os.path.join(INCLUDE, "hs.h")]
     objs, procs = [], []
     for src in SOURCES:
         s = os.path.join(CSRC, src)

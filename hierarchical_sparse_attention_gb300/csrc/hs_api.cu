@@ -4,10 +4,13 @@
 #include <sys/syscall.h>
 #include <unistd.h>
 
+#include <cmath>
+#include <cstdint>
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
 
+#include "hs_fp4.h"
 #include "hs_internal.h"
 
 struct hs_handle {
@@ -142,6 +145,77 @@ hs_status make_geometry(const hs_config* cfg, void* const* host_pools, void* con
 }
 
 }  // namespace hs
+
+namespace {
+
+// What the calls on 4-bit rows check alike. A power of two in [2^-32, 2^32].
+bool latent_scale_ok(float g) {
+  int e;
+  return std::isfinite(g) && g >= 0x1p-32f && g <= 0x1p32f && std::frexp(g, &e) == 0.5f;
+}
+
+bool fp4_rows_ok(int32_t n, const uint16_t* kv, int64_t kv_stride, const int32_t* rows, float latent_scale,
+                 const uint8_t* pool, int64_t pool_rows, const uint32_t* error_flags) {
+  if (n < 0 || kv_stride < hs::kFp4Dims || kv_stride % 8 || pool_rows < 1 || !latent_scale_ok(latent_scale)) return false;
+  if (n == 0) return true;
+  return kv && rows && pool && error_flags && (uintptr_t)kv % 16 == 0 && (uintptr_t)pool % 16 == 0;
+}
+
+// num_requests x num_queries x num_heads stays within 32-bit grids and tensor extents.
+bool fp4_mla_shape_ok(int32_t num_requests, int32_t num_heads, int32_t num_queries, int32_t splits) {
+  return num_requests >= 1 && num_requests <= (1 << 20) && num_heads >= 1 && num_heads <= 128 && num_queries >= 1 &&
+         num_queries <= HS_MAX_SPEC_QUERIES && splits >= 1 && splits <= HS_MAX_MLA_SPLITS;
+}
+
+// The rest of an attention call, whichever way its rows are found.
+hs_status fp4_mla(hs::Fp4MlaArgs a, int32_t num_requests, int32_t num_heads, int32_t num_queries, int32_t splits,
+                  const uint16_t* q, const uint8_t* kv_pool, int64_t pool_rows, float sm_scale, float latent_scale,
+                  uint16_t* o, float* lse, void* workspace, size_t workspace_bytes, uint32_t* error_flags,
+                  hs_stream_t stream) {
+  if (num_requests < 0 || !fp4_mla_shape_ok(num_requests ? num_requests : 1, num_heads, num_queries, splits) ||
+      pool_rows < 1 || pool_rows > INT32_MAX || !latent_scale_ok(latent_scale) || !std::isfinite(sm_scale))
+    return HS_ERR_INVALID_ARG;
+  if (num_requests == 0) return HS_OK;
+  if (!q || !kv_pool || !o || !lse || !error_flags) return HS_ERR_INVALID_ARG;
+  if ((uintptr_t)q % 16 || (uintptr_t)kv_pool % 16 || (uintptr_t)o % 16) return HS_ERR_INVALID_ARG;
+  const size_t need = hs::fp4_mla_workspace_bytes(num_requests, num_heads, num_queries, splits);
+  if (need && (!workspace || workspace_bytes < need || (uintptr_t)workspace % 16)) return HS_ERR_INVALID_ARG;
+  a.q = q;
+  a.pool = kv_pool;
+  a.pool_rows = pool_rows;
+  a.num_heads = num_heads;
+  a.num_queries = num_queries;
+  a.splits = splits;
+  a.sm_scale = sm_scale;
+  a.latent_scale = latent_scale;
+  a.o = o;
+  a.lse = lse;
+  return hs::launch_fp4_mla(a, num_requests, static_cast<float*>(workspace), error_flags, (cudaStream_t)stream) ==
+                 cudaSuccess
+             ? HS_OK
+             : HS_ERR_CUDA;
+}
+
+// Checks a page pool and finds the widest piece that every pool and row can be copied in.
+bool page_args(const hs_page_pool* p, hs::PageArgs* a) {
+  if (!p || p->num_requests < 1 || p->num_requests > HS_MAX_PAGE_REQUESTS || p->max_pages < 1 || p->num_pages < 1 ||
+      p->page_size < 1 || p->row_bytes < 1 || p->num_layers < 1 || p->num_layers > HS_MAX_LAYERS ||
+      (int64_t)p->num_pages * p->page_size > INT32_MAX || (int64_t)p->max_pages * p->page_size > INT32_MAX)
+    return false;
+  if (!p->resident_pages || !p->page_refs || !p->free_pages || !p->free_count || !p->error_flags || !p->workspace ||
+      (uintptr_t)p->workspace % 16 || p->workspace_bytes < hs::pages_workspace_bytes(p->num_requests, p->num_pages))
+    return false;
+  uintptr_t bits = (uintptr_t)p->row_bytes;
+  for (int l = 0; l < p->num_layers; ++l) {
+    if (!p->device_pools[l]) return false;
+    bits |= (uintptr_t)p->device_pools[l];
+  }
+  a->p = *p;
+  a->vec = bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 1;
+  return true;
+}
+
+}  // namespace
 
 extern "C" {
 
@@ -566,6 +640,116 @@ hs_status hs_host_unregister(void* ptr) {
     return HS_ERR_CUDA;
   }
   return HS_OK;
+}
+
+hs_status hs_fp4_pack_rows(int32_t n, const uint16_t* kv, int64_t kv_stride, const int32_t* rows, float latent_scale,
+                           uint8_t* pool, int64_t pool_rows, uint32_t* error_flags, hs_stream_t stream) {
+  if (!fp4_rows_ok(n, kv, kv_stride, rows, latent_scale, pool, pool_rows, error_flags)) return HS_ERR_INVALID_ARG;
+  if (n == 0) return HS_OK;
+  const hs::Fp4RowsArgs a{n, const_cast<uint16_t*>(kv), kv_stride, rows, latent_scale, pool, pool_rows};
+  return hs::launch_fp4_pack(a, error_flags, (cudaStream_t)stream) == cudaSuccess ? HS_OK : HS_ERR_CUDA;
+}
+
+hs_status hs_fp4_unpack_rows(int32_t n, const uint8_t* pool, int64_t pool_rows, const int32_t* rows,
+                             float latent_scale, uint16_t* kv, int64_t kv_stride, uint32_t* error_flags,
+                             hs_stream_t stream) {
+  if (!fp4_rows_ok(n, kv, kv_stride, rows, latent_scale, pool, pool_rows, error_flags)) return HS_ERR_INVALID_ARG;
+  if (n == 0) return HS_OK;
+  const hs::Fp4RowsArgs a{n, kv, kv_stride, rows, latent_scale, const_cast<uint8_t*>(pool), pool_rows};
+  return hs::launch_fp4_unpack(a, error_flags, (cudaStream_t)stream) == cudaSuccess ? HS_OK : HS_ERR_CUDA;
+}
+
+int32_t hs_fp4_mla_splits(int32_t num_requests, int32_t num_heads, int32_t num_queries, int64_t rows) {
+  if (!fp4_mla_shape_ok(num_requests, num_heads, num_queries, 1) || rows < 1) return 1;
+  return hs::fp4_mla_splits(num_requests, num_heads, num_queries, rows);
+}
+
+size_t hs_fp4_mla_workspace_bytes(int32_t num_requests, int32_t num_heads, int32_t num_queries, int32_t splits) {
+  if (!fp4_mla_shape_ok(num_requests, num_heads, num_queries, splits)) return 0;
+  return hs::fp4_mla_workspace_bytes(num_requests, num_heads, num_queries, splits);
+}
+
+hs_status hs_fp4_sparse_mla_decode(int32_t num_requests, int32_t num_heads, int32_t top_k, int32_t splits,
+                                   const uint16_t* q, const uint8_t* kv_pool, int64_t pool_rows,
+                                   const int32_t* out_rows, float sm_scale, float latent_scale, uint16_t* o,
+                                   float* lse, void* workspace, size_t workspace_bytes, uint32_t* error_flags,
+                                   hs_stream_t stream) {
+  if (top_k < 1 || top_k > HS_MAX_TOP_K) return HS_ERR_INVALID_ARG;
+  if (num_requests > 0 && !out_rows) return HS_ERR_INVALID_ARG;
+  hs::Fp4MlaArgs a = {};
+  a.out_rows = out_rows;
+  a.top_k = top_k;
+  return fp4_mla(a, num_requests, num_heads, 1, splits, q, kv_pool, pool_rows, sm_scale, latent_scale, o, lse,
+                 workspace, workspace_bytes, error_flags, stream);
+}
+
+hs_status hs_fp4_window_mla_decode(int32_t num_requests, int32_t num_heads, int32_t num_queries, int32_t window,
+                                   int32_t sinks, int32_t splits, const uint16_t* q, const uint8_t* kv_pool,
+                                   int64_t pool_rows, int32_t page_size, int32_t max_pages, const int32_t* seq_lens,
+                                   const int32_t* resident_pages, float sm_scale, float latent_scale, uint16_t* o,
+                                   float* lse, void* workspace, size_t workspace_bytes, uint32_t* error_flags,
+                                   hs_stream_t stream) {
+  if (window < 1 || sinks < 0 || page_size < 1 || max_pages < 1) return HS_ERR_INVALID_ARG;
+  if (num_requests > 0 && (!seq_lens || !resident_pages)) return HS_ERR_INVALID_ARG;
+  hs::Fp4MlaArgs a = {};
+  a.seq_lens = seq_lens;
+  a.pages = resident_pages;
+  a.page_size = page_size;
+  a.max_pages = max_pages;
+  a.window = window;
+  a.sinks = sinks;
+  return fp4_mla(a, num_requests, num_heads, num_queries, splits, q, kv_pool, pool_rows, sm_scale, latent_scale, o,
+                 lse, workspace, workspace_bytes, error_flags, stream);
+}
+
+size_t hs_pages_workspace_bytes(int32_t num_requests, int32_t num_pages) {
+  if (num_requests < 1 || num_requests > HS_MAX_PAGE_REQUESTS || num_pages < 1) return 0;
+  return hs::pages_workspace_bytes(num_requests, num_pages);
+}
+
+hs_status hs_pages_init(const hs_page_pool* pool, hs_stream_t stream) {
+  hs::PageArgs a;
+  if (!page_args(pool, &a)) return HS_ERR_INVALID_ARG;
+  return hs::launch_pages_init(a, (cudaStream_t)stream) == cudaSuccess ? HS_OK : HS_ERR_CUDA;
+}
+
+hs_status hs_pages_extend(const hs_page_pool* pool, int32_t n, const int32_t* requests, const int32_t* old_lens,
+                          const int32_t* new_lens, int32_t* granted, hs_stream_t stream) {
+  hs::PageArgs a;
+  if (!page_args(pool, &a) || n < 0) return HS_ERR_INVALID_ARG;
+  if (n == 0) return HS_OK;
+  if (!requests || !old_lens || !new_lens) return HS_ERR_INVALID_ARG;
+  return hs::launch_pages_extend(a, n, requests, old_lens, new_lens, granted, (cudaStream_t)stream) == cudaSuccess
+             ? HS_OK
+             : HS_ERR_CUDA;
+}
+
+hs_status hs_pages_fork(const hs_page_pool* pool, int32_t n, const int32_t* parents, const int32_t* children,
+                        const int32_t* lens, int32_t* granted, hs_stream_t stream) {
+  hs::PageArgs a;
+  if (!page_args(pool, &a) || n < 0 || n > a.p.num_requests) return HS_ERR_INVALID_ARG;
+  if (n == 0) return HS_OK;
+  if (!parents || !children || !lens) return HS_ERR_INVALID_ARG;
+  return hs::launch_pages_fork(a, n, parents, children, lens, granted, (cudaStream_t)stream) == cudaSuccess
+             ? HS_OK
+             : HS_ERR_CUDA;
+}
+
+hs_status hs_pages_free(const hs_page_pool* pool, int32_t n, const int32_t* requests, const int32_t* first_pages,
+                        const int32_t* end_pages, hs_stream_t stream) {
+  hs::PageArgs a;
+  if (!page_args(pool, &a) || n < 0) return HS_ERR_INVALID_ARG;
+  if (n == 0) return HS_OK;
+  if (!requests) return HS_ERR_INVALID_ARG;
+  return hs::launch_pages_free(a, n, requests, first_pages, end_pages, (cudaStream_t)stream) == cudaSuccess
+             ? HS_OK
+             : HS_ERR_CUDA;
+}
+
+hs_status hs_pages_compact(const hs_page_pool* pool, hs_stream_t stream) {
+  hs::PageArgs a;
+  if (!page_args(pool, &a)) return HS_ERR_INVALID_ARG;
+  return hs::launch_pages_compact(a, (cudaStream_t)stream) == cudaSuccess ? HS_OK : HS_ERR_CUDA;
 }
 
 }  // extern "C"

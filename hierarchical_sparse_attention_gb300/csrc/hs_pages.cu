@@ -1,0 +1,534 @@
+// Pages of a cache: tables of pages per request, reference counts, a stack of free pages, and the
+// page copies of a fork and of a compaction, in every layer's pool.
+//
+// State (the caller's, on the device): resident_pages [num_requests, max_pages] (page or -1),
+// page_refs [num_pages] (table entries that hold the page), free_pages [num_pages] with free_count
+// (the stack's entries 0 .. free_count - 1, its top last). Every result is a function of the
+// arguments and the state alone: grants go by prefix sums over the entries in their order, pages
+// are pushed and packed in the order of their numbers, and the atomics only add, clear or set.
+#include "hs_fp4.h"
+
+namespace hs {
+namespace {
+
+constexpr int kPlanThreads = 1024;  // the one-CTA plans
+constexpr int kPageThreads = 256;
+constexpr int kMaxRequests = HS_MAX_PAGE_REQUESTS;
+
+// Workspace: a header, then per page a bit (freed by this call; zero between calls) and the
+// compaction's lists, then per entry of a fork what the plan found and gave.
+struct PageWork {
+  uint32_t* ticket;    // CTAs of a fork's check that are done; zero between calls
+  int32_t* moves;      // pages that the compaction moves
+  int32_t* live;       // live pages
+  uint32_t* freed;     // [ceil(num_pages / 32)]
+  int32_t *src, *dst;  // [num_pages] the compaction's moves
+  int32_t* rank;       // [num_pages] of a page past the live count: its move, or -1
+  int32_t* used;       // [num_requests] entry i: its child's row holds a page
+  int32_t* fresh;      // [num_requests] entry i: its copy's page; -1 none needed; -2 refused
+};
+
+size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+PageWork work_of(const hs_page_pool& p) {
+  uint8_t* at = static_cast<uint8_t*>(p.workspace);
+  auto take = [&](size_t bytes) {
+    uint8_t* r = at;
+    at += up256(bytes);
+    return r;
+  };
+  PageWork w;
+  uint32_t* head = reinterpret_cast<uint32_t*>(take(256));
+  w.ticket = head;
+  w.moves = reinterpret_cast<int32_t*>(head + 1);
+  w.live = reinterpret_cast<int32_t*>(head + 2);
+  w.freed = reinterpret_cast<uint32_t*>(take(((size_t)p.num_pages + 31) / 32 * 4));
+  w.src = reinterpret_cast<int32_t*>(take((size_t)p.num_pages * 4));
+  w.dst = reinterpret_cast<int32_t*>(take((size_t)p.num_pages * 4));
+  w.rank = reinterpret_cast<int32_t*>(take((size_t)p.num_pages * 4));
+  w.used = reinterpret_cast<int32_t*>(take((size_t)p.num_requests * 4));
+  w.fresh = reinterpret_cast<int32_t*>(take((size_t)p.num_requests * 4));
+  return w;
+}
+
+// At the end of a kernel that changes tables or rows: hs_backup may be the next kernel of the
+// stream, and it reads both before its wait (a programmatic dependent), so each thread makes what
+// it wrote visible before it exits.
+__device__ __forceinline__ void show_writes() { __threadfence(); }
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Exclusive prefix sum of v over the CTA's kPlanThreads threads; *total gets the sum. Called by
+// every thread; sums are 64-bit (entries x pages passes 32).
+__device__ int64_t block_prefix(int64_t v, int64_t* total) {
+  __shared__ int64_t s_warp[kPlanThreads / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t x = v;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
+    if (lane >= d) x += y;
+  }
+  __syncthreads();  // the last call's readers are done with s_warp
+  if (lane == 31) s_warp[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    int64_t t = s_warp[lane];
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, t, d);
+      if (lane >= d) t += y;
+    }
+    s_warp[lane] = t;
+  }
+  __syncthreads();
+  *total = s_warp[31];
+  return x - v + (warp ? s_warp[warp - 1] : 0);
+}
+
+// The stack's height, kept inside its array whatever the state holds.
+__device__ __forceinline__ int32_t stack_height(const hs_page_pool& p) {
+  const int32_t c = *p.free_count;
+  if (c < 0 || c > p.num_pages) {
+    if (threadIdx.x == 0) atomicOr(p.error_flags, HS_FLAG_STATE);
+    return c < 0 ? 0 : p.num_pages;
+  }
+  return c;
+}
+// The k-th page from the top of a stack of `height` (k < height), taken into use; -1 if the stack
+// holds no page there.
+__device__ __forceinline__ int32_t pop(const hs_page_pool& p, int32_t height, int64_t k) {
+  const int32_t page = p.free_pages[height - 1 - k];
+  if (page < 0 || page >= p.num_pages || atomicCAS(&p.page_refs[page], 0, 1) != 0) {
+    atomicOr(p.error_flags, HS_FLAG_STATE);
+    return -1;
+  }
+  return page;
+}
+
+__global__ void pages_init_kernel(const hs_page_pool p, const PageWork w) {
+  const int64_t step = (int64_t)gridDim.x * blockDim.x, t = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  for (int64_t i = t; i < (int64_t)p.num_requests * p.max_pages; i += step) p.resident_pages[i] = -1;
+  for (int64_t i = t; i < p.num_pages; i += step) {
+    p.page_refs[i] = 0;
+    p.free_pages[i] = p.num_pages - 1 - (int32_t)i;  // page 0 on top
+  }
+  for (int64_t i = t; i < (p.num_pages + 31) / 32; i += step) w.freed[i] = 0;
+  if (t == 0) {
+    *p.free_count = p.num_pages;
+    *w.ticket = 0;
+  }
+  show_writes();
+}
+
+// One CTA. Entry i asks for the pages [ceil(old / page_size), ceil(new / page_size)) of its
+// request; it gets all of them if the running sum of what the entries ask for is within the stack.
+__global__ void __launch_bounds__(kPlanThreads)
+    pages_extend_kernel(const hs_page_pool p, int32_t n, const int32_t* __restrict__ requests,
+                        const int32_t* __restrict__ old_lens, const int32_t* __restrict__ new_lens,
+                        int32_t* __restrict__ granted) {
+  __shared__ uint32_t s_once[kMaxRequests / 32], s_twice[kMaxRequests / 32];
+  __shared__ int64_t s_at[kPlanThreads];                         // the chunk's prefix sums
+  __shared__ int32_t s_req[kPlanThreads], s_first[kPlanThreads];  // and where its pages go
+  __shared__ uint8_t s_bad[kPlanThreads];
+  const int tid = threadIdx.x;
+  const int words = (p.num_requests + 31) / 32;
+  for (int i = tid; i < words; i += kPlanThreads) s_once[i] = s_twice[i] = 0;
+  __syncthreads();
+  for (int i = tid; i < n; i += kPlanThreads) {
+    const int32_t r = requests[i];
+    if (r >= 0 && r < p.num_requests && (atomicOr(&s_once[r >> 5], 1u << (r & 31)) >> (r & 31) & 1u))
+      atomicOr(&s_twice[r >> 5], 1u << (r & 31));
+  }
+  __syncthreads();
+  const int32_t height = stack_height(p);
+  const int64_t most = (int64_t)p.max_pages * p.page_size;
+  int64_t asked = 0, taken = 0;  // by the entries so far
+  for (int base = 0; base < n; base += kPlanThreads) {
+    const int i = base + tid;
+    int64_t need = 0, first = 0;
+    int32_t r = -1;
+    uint32_t flag = 0;
+    if (i < n) {
+      r = requests[i];
+      const int64_t a = old_lens[i], b = new_lens[i];
+      if (r < 0) {  // a padding entry
+      } else if (r >= p.num_requests) {
+        flag = HS_FLAG_TOKEN;
+      } else if (s_twice[r >> 5] >> (r & 31) & 1u) {
+        flag = HS_FLAG_DUP;
+      } else if (a < 0 || b < a || b > most) {
+        flag = HS_FLAG_SEQLEN;
+      } else {
+        first = (a + p.page_size - 1) / p.page_size;
+        need = (b + p.page_size - 1) / p.page_size - first;
+      }
+    }
+    // the pages asked for, spread over the threads: is any of them there already?
+    int64_t sum;
+    s_at[tid] = block_prefix(need, &sum);
+    s_req[tid] = r;
+    s_first[tid] = (int32_t)first;
+    s_bad[tid] = 0;
+    __syncthreads();
+    auto entry_of = [&](int64_t k) {  // the last entry whose prefix is <= k
+      int lo = 0, hi = kPlanThreads - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (s_at[mid] <= k) lo = mid;
+        else hi = mid - 1;
+      }
+      return lo;
+    };
+    for (int64_t k = tid; k < sum; k += kPlanThreads) {
+      const int e = entry_of(k);
+      if (p.resident_pages[(size_t)s_req[e] * p.max_pages + s_first[e] + (k - s_at[e])] != -1) s_bad[e] = 1;
+    }
+    __syncthreads();
+    if (s_bad[tid]) {
+      flag = HS_FLAG_STATE;
+      need = 0;
+    }
+    const int64_t before = asked + block_prefix(need, &sum);
+    asked += sum;
+    const bool got = need == 0 || before + need <= height;
+    if (i < n) {
+      if (flag) atomicOr(p.error_flags, flag);
+      if (!got) atomicOr(p.error_flags, HS_FLAG_NOPAGE);
+      if (granted) granted[i] = flag || !got ? -1 : (int32_t)need;
+    }
+    const int64_t mine = block_prefix(got ? need : 0, &sum);
+    s_at[tid] = mine;
+    __syncthreads();
+    for (int64_t k = tid; k < sum; k += kPlanThreads) {
+      const int e = entry_of(k);
+      p.resident_pages[(size_t)s_req[e] * p.max_pages + s_first[e] + (k - s_at[e])] = pop(p, height, taken + k);
+    }
+    taken += sum;
+    __syncthreads();
+  }
+  if (tid == 0) *p.free_count = height - (int32_t)taken;
+  show_writes();
+}
+
+// A CTA per entry looks whether the child's row holds a page; the last one done plans every
+// entry: which are refused, and the page of each copy.
+__global__ void __launch_bounds__(kPlanThreads)
+    pages_fork_plan_kernel(const hs_page_pool p, const PageWork w, int32_t n, const int32_t* __restrict__ parents,
+                           const int32_t* __restrict__ children, const int32_t* __restrict__ lens,
+                           int32_t* __restrict__ granted) {
+  __shared__ uint32_t s_once[kMaxRequests / 32], s_twice[kMaxRequests / 32], s_parent[kMaxRequests / 32];
+  __shared__ uint32_t s_last;
+  const int tid = threadIdx.x;
+  {
+    const int32_t c = children[blockIdx.x];
+    int held = 0;
+    if (c >= 0 && c < p.num_requests)
+      for (int i = tid; i < p.max_pages; i += kPlanThreads)
+        held |= p.resident_pages[(size_t)c * p.max_pages + i] != -1;
+    held = __syncthreads_or(held);
+    if (tid == 0) {
+      w.used[blockIdx.x] = held;
+      __threadfence();
+      s_last = atomicAdd(w.ticket, 1u) == gridDim.x - 1;
+    }
+    __syncthreads();
+    if (!s_last) return;
+    __threadfence();
+  }
+  const int words = (p.num_requests + 31) / 32;
+  for (int i = tid; i < words; i += kPlanThreads) s_once[i] = s_twice[i] = s_parent[i] = 0;
+  __syncthreads();
+  for (int i = tid; i < n; i += kPlanThreads) {
+    const int32_t c = children[i], q = parents[i];
+    if (c < 0 || q < 0) continue;  // a padding entry
+    if (c < p.num_requests && (atomicOr(&s_once[c >> 5], 1u << (c & 31)) >> (c & 31) & 1u))
+      atomicOr(&s_twice[c >> 5], 1u << (c & 31));
+    if (q < p.num_requests) atomicOr(&s_parent[q >> 5], 1u << (q & 31));
+  }
+  __syncthreads();
+  const int32_t height = stack_height(p);
+  const int64_t most = (int64_t)p.max_pages * p.page_size;
+  int64_t asked = 0, taken = 0;
+  for (int base = 0; base < n; base += kPlanThreads) {
+    const int i = base + tid;
+    int64_t need = 0;
+    uint32_t flag = 0;
+    bool padding = true;
+    if (i < n) {
+      const int32_t c = children[i], q = parents[i];
+      const int64_t len = lens[i];
+      padding = c < 0 || q < 0;
+      if (padding) {
+      } else if (c >= p.num_requests || q >= p.num_requests) {
+        flag = HS_FLAG_TOKEN;
+      } else if ((s_twice[c >> 5] | s_parent[c >> 5]) >> (c & 31) & 1u) {
+        flag = HS_FLAG_DUP;
+      } else if (len < 0 || len > most) {
+        flag = HS_FLAG_SEQLEN;
+      } else if (__ldcg(&w.used[i])) {
+        flag = HS_FLAG_STATE;
+      } else if (len % p.page_size) {
+        const int32_t page = p.resident_pages[(size_t)q * p.max_pages + len / p.page_size];
+        if (page >= p.num_pages || page < -1) flag = HS_FLAG_STATE;
+        else need = page >= 0;
+      }
+    }
+    int64_t sum;
+    const int64_t before = asked + block_prefix(need, &sum);
+    asked += sum;
+    const bool got = need == 0 || before + need <= height;
+    const int64_t mine = block_prefix(got ? need : 0, &sum);
+    if (i < n) {
+      if (flag) atomicOr(p.error_flags, flag);
+      if (!got) atomicOr(p.error_flags, HS_FLAG_NOPAGE);
+      const bool refused = flag || !got;
+      w.fresh[i] = refused || padding ? -2 : need ? pop(p, height, taken + mine) : -1;
+      if (granted) granted[i] = refused ? -1 : (int32_t)need;
+    }
+    taken += sum;
+  }
+  if (tid == 0) {
+    *p.free_count = height - (int32_t)taken;
+    *w.ticket = 0;
+  }
+}
+
+// `bytes` from src to dst by the CTA, in pieces of `vec` bytes (both start on a multiple of it).
+template <typename V>
+__device__ __forceinline__ void copy_span_as(const uint8_t* src, uint8_t* dst, int64_t bytes) {
+  const V* s = reinterpret_cast<const V*>(src);
+  V* d = reinterpret_cast<V*>(dst);
+  const int64_t n = bytes / (int64_t)sizeof(V);
+  int64_t i = threadIdx.x;
+  for (; i + 3 * kPageThreads < n; i += 4 * kPageThreads) {
+    V x[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) x[u] = s[i + u * kPageThreads];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) d[i + u * kPageThreads] = x[u];
+  }
+  for (; i < n; i += kPageThreads) d[i] = s[i];
+}
+__device__ __forceinline__ void copy_span(const uint8_t* src, uint8_t* dst, int64_t bytes, int vec) {
+  if (vec == 16) copy_span_as<uint4>(src, dst, bytes);
+  else if (vec == 4) copy_span_as<uint32_t>(src, dst, bytes);
+  else copy_span_as<uint8_t>(src, dst, bytes);
+}
+
+// Per entry: blockIdx.y 0 gives the child its parent's whole pages and the copy's page, 1 + l
+// copies the rows of the page that is not full in layer l.
+__global__ void __launch_bounds__(kPageThreads)
+    pages_fork_kernel(const PageArgs a, const PageWork w, const int32_t* __restrict__ parents,
+                      const int32_t* __restrict__ children, const int32_t* __restrict__ lens) {
+  pdl_wait();
+  const hs_page_pool& p = a.p;
+  const int i = blockIdx.x;
+  const int32_t fresh = w.fresh[i];
+  if (fresh == -2) return;
+  const int32_t* src = p.resident_pages + (size_t)parents[i] * p.max_pages;
+  const int32_t full = lens[i] / p.page_size, rest = lens[i] % p.page_size;
+  if (blockIdx.y == 0) {
+    int32_t* dst = p.resident_pages + (size_t)children[i] * p.max_pages;
+    for (int k = threadIdx.x; k < full; k += kPageThreads) {
+      int32_t page = src[k];
+      if (page >= p.num_pages || page < -1) {
+        atomicOr(p.error_flags, HS_FLAG_STATE);
+        page = -1;
+      }
+      if (page >= 0) atomicAdd(&p.page_refs[page], 1);
+      dst[k] = page;
+    }
+    if (threadIdx.x == 0 && fresh >= 0) dst[full] = fresh;
+  } else if (fresh >= 0) {
+    uint8_t* pool = static_cast<uint8_t*>(p.device_pools[blockIdx.y - 1]);
+    const int64_t page = (int64_t)p.page_size * p.row_bytes;
+    copy_span(pool + src[full] * page, pool + fresh * page, (int64_t)rest * p.row_bytes, a.vec);
+  }
+  show_writes();
+}
+
+// Every entry of the ranges: out of the table, its page's count down by one; a page that nobody
+// holds any more is marked. An entry is taken out by one thread however often the call names it.
+__global__ void __launch_bounds__(kPageThreads)
+    pages_drop_kernel(const hs_page_pool p, const PageWork w, const int32_t* __restrict__ requests,
+                      const int32_t* __restrict__ first_pages, const int32_t* __restrict__ end_pages) {
+  const int i = blockIdx.x;
+  const int32_t r = requests[i];
+  if (r < 0) return;
+  if (r >= p.num_requests) {
+    if (threadIdx.x == 0 && blockIdx.y == 0) atomicOr(p.error_flags, HS_FLAG_TOKEN);
+    return;
+  }
+  const int32_t lo = first_pages ? max(first_pages[i], 0) : 0;
+  const int32_t hi = end_pages ? min(end_pages[i], p.max_pages) : p.max_pages;
+  int32_t* row = p.resident_pages + (size_t)r * p.max_pages;
+  for (int64_t k = lo + (int64_t)blockIdx.y * kPageThreads + threadIdx.x; k < hi; k += (int64_t)gridDim.y * kPageThreads) {
+    if (row[k] == -1) continue;
+    const int32_t page = atomicExch(&row[k], -1);
+    if (page == -1) continue;
+    if (page < 0 || page >= p.num_pages) {
+      atomicOr(p.error_flags, HS_FLAG_STATE);
+      continue;
+    }
+    const int32_t held = atomicSub(&p.page_refs[page], 1);
+    if (held == 1) {
+      atomicOr(&w.freed[page >> 5], 1u << (page & 31));
+    } else if (held <= 0) {  // the count did not cover this entry
+      atomicAdd(&p.page_refs[page], 1);
+      atomicOr(p.error_flags, HS_FLAG_STATE);
+    }
+  }
+}
+
+// One CTA: the marked pages onto the stack, the lowest on top, and the marks away.
+__global__ void __launch_bounds__(kPlanThreads) pages_push_kernel(const hs_page_pool p, const PageWork w) {
+  pdl_wait();
+  const int tid = threadIdx.x;
+  const int32_t height = stack_height(p);
+  const int words = (int)(((int64_t)p.num_pages + 31) / 32);
+  int64_t total = 0;
+  for (int base = 0; base < words; base += kPlanThreads) total += base + tid < words ? __popc(w.freed[base + tid]) : 0;
+  block_prefix(total, &total);
+  if (total == 0) return;
+  int64_t rank = 0;  // marked pages below this chunk's
+  for (int base = 0; base < words; base += kPlanThreads) {
+    uint32_t bits = base + tid < words ? w.freed[base + tid] : 0;
+    int64_t sum;
+    int64_t k = rank + block_prefix(__popc(bits), &sum);
+    rank += sum;
+    if (bits) w.freed[base + tid] = 0;
+    for (; bits; bits &= bits - 1, ++k) {
+      const int64_t at = height + total - 1 - k;
+      if (at < p.num_pages) p.free_pages[at] = 32 * (base + tid) + __ffs(bits) - 1;
+      else atomicOr(p.error_flags, HS_FLAG_STATE);  // more pages than the pool has
+    }
+  }
+  if (tid == 0) *p.free_count = (int32_t)min((int64_t)p.num_pages, height + total);
+}
+
+// One CTA, a strip of pages per warp: the live pages are counted, those past the live count get
+// the free pages among the first ones, both in the order of their numbers.
+__global__ void __launch_bounds__(kPlanThreads) pages_compact_plan_kernel(const hs_page_pool p, const PageWork w) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t strip = ((int64_t)p.num_pages + kPlanThreads - 1) / kPlanThreads * 32;
+  const int64_t lo = min(warp * strip, (int64_t)p.num_pages), hi = min(lo + strip, (int64_t)p.num_pages);
+  const uint32_t below = (1u << lane) - 1;
+  int64_t count = 0;
+  for (int64_t b = lo; b < hi; b += 32) count += __popc(__ballot_sync(~0u, b + lane < hi && p.page_refs[b + lane] > 0));
+  int64_t live;
+  int64_t before = block_prefix(lane == 0 ? count : 0, &live);  // live pages below the strip
+  before = __shfl_sync(~0u, before, 0);
+  // live pages among the first `live`: the rest of those are holes, as many as there are pages to move
+  count = 0;
+  for (int64_t b = lo; b < min(hi, live); b += 32)
+    count += __popc(__ballot_sync(~0u, b + lane < min(hi, live) && p.page_refs[b + lane] > 0));
+  int64_t kept;
+  block_prefix(lane == 0 ? count : 0, &kept);
+  for (int64_t b = lo; b < hi; b += 32) {
+    const int64_t page = b + lane;
+    const bool in = page < hi, used = in && p.page_refs[page] > 0;
+    const uint32_t m = __ballot_sync(~0u, used);
+    const int64_t k = before + __popc(m & below);  // live pages below this one
+    if (in && page < live && !used) w.dst[page - k] = (int32_t)page;
+    if (in && page >= live) {
+      w.rank[page] = used ? (int32_t)(k - kept) : -1;
+      if (used) w.src[k - kept] = (int32_t)page;
+    }
+    before += __popc(m);
+  }
+  if (threadIdx.x == 0) {
+    *w.moves = (int32_t)(live - kept);
+    *w.live = (int32_t)live;
+  }
+}
+
+constexpr int kSpan = 16384;  // bytes of a page that one CTA copies at a time
+
+// Pages move, their counts with them; every table entry that names a moved page names its new
+// one; the stack holds the pages past the live ones, the lowest on top.
+__global__ void __launch_bounds__(kPageThreads) pages_compact_kernel(const PageArgs a, const PageWork w) {
+  pdl_wait();
+  const hs_page_pool& p = a.p;
+  const int64_t t = (int64_t)blockIdx.x * kPageThreads + threadIdx.x, step = (int64_t)gridDim.x * kPageThreads;
+  const int32_t moves = *w.moves, live = *w.live;
+  const int64_t page = (int64_t)p.page_size * p.row_bytes;
+  const int spans = (int)((page + kSpan - 1) / kSpan);
+  const int64_t tasks = (int64_t)moves * p.num_layers * spans;
+  for (int64_t k = blockIdx.x; k < tasks; k += gridDim.x) {
+    const int64_t at = k % spans * kSpan, rest = k / spans;
+    const int l = (int)(rest % p.num_layers);
+    const int64_t m = rest / p.num_layers;
+    uint8_t* pool = static_cast<uint8_t*>(p.device_pools[l]);
+    copy_span(pool + w.src[m] * page + at, pool + w.dst[m] * page + at, min((int64_t)kSpan, page - at), a.vec);
+  }
+  for (int64_t k = t; k < moves; k += step) {
+    p.page_refs[w.dst[k]] = p.page_refs[w.src[k]];
+    p.page_refs[w.src[k]] = 0;
+  }
+  for (int64_t k = t; k < (int64_t)p.num_requests * p.max_pages; k += step) {
+    const int32_t old = p.resident_pages[k];
+    if (old < live) continue;
+    const int32_t m = old < p.num_pages ? w.rank[old] : -1;
+    if (m >= 0) p.resident_pages[k] = w.dst[m];
+    else atomicOr(p.error_flags, HS_FLAG_STATE);  // a page that nobody counted
+  }
+  for (int64_t k = t; k < p.num_pages - live; k += step) p.free_pages[k] = p.num_pages - 1 - (int32_t)k;
+  if (t == 0) *p.free_count = p.num_pages - live;
+  show_writes();
+}
+
+cudaError_t sm_count(int* n) {
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  return e != cudaSuccess ? e : cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev);
+}
+
+}  // namespace
+
+size_t pages_workspace_bytes(int32_t num_requests, int32_t num_pages) {
+  return 256 + up256(((size_t)num_pages + 31) / 32 * 4) + 3 * up256((size_t)num_pages * 4) +
+         2 * up256((size_t)num_requests * 4);
+}
+
+cudaError_t launch_pages_init(const PageArgs& a, cudaStream_t stream) {
+  const int64_t n = (int64_t)a.p.num_requests * a.p.max_pages;
+  const int64_t most = n > a.p.num_pages ? n : a.p.num_pages;
+  const unsigned grid = (unsigned)((most + kPageThreads - 1) / kPageThreads < 1216 ? (most + kPageThreads - 1) / kPageThreads : 1216);
+  return launch(pages_init_kernel, dim3(grid), kPageThreads, stream, false, a.p, work_of(a.p));
+}
+
+cudaError_t launch_pages_extend(const PageArgs& a, int32_t n, const int32_t* requests, const int32_t* old_lens,
+                                const int32_t* new_lens, int32_t* granted, cudaStream_t stream) {
+  return launch(pages_extend_kernel, dim3(1), kPlanThreads, stream, false, a.p, n, requests, old_lens, new_lens, granted);
+}
+
+cudaError_t launch_pages_fork(const PageArgs& a, int32_t n, const int32_t* parents, const int32_t* children,
+                              const int32_t* lens, int32_t* granted, cudaStream_t stream) {
+  const PageWork w = work_of(a.p);
+  const cudaError_t e = launch(pages_fork_plan_kernel, dim3((unsigned)n), kPlanThreads, stream, false, a.p, w, n, parents,
+                               children, lens, granted);
+  if (e != cudaSuccess) return e;
+  return launch(pages_fork_kernel, dim3((unsigned)n, 1u + (unsigned)a.p.num_layers), kPageThreads, stream, true, a, w,
+                parents, children, lens);
+}
+
+cudaError_t launch_pages_free(const PageArgs& a, int32_t n, const int32_t* requests, const int32_t* first_pages,
+                              const int32_t* end_pages, cudaStream_t stream) {
+  const PageWork w = work_of(a.p);
+  const int chunks = (a.p.max_pages + kPageThreads - 1) / kPageThreads;
+  const cudaError_t e = launch(pages_drop_kernel, dim3((unsigned)n, (unsigned)(chunks < 64 ? chunks : 64)), kPageThreads,
+                               stream, false, a.p, w, requests, first_pages, end_pages);
+  if (e != cudaSuccess) return e;
+  return launch(pages_push_kernel, dim3(1), kPlanThreads, stream, true, a.p, w);
+}
+
+cudaError_t launch_pages_compact(const PageArgs& a, cudaStream_t stream) {
+  const PageWork w = work_of(a.p);
+  int sms = 0;
+  cudaError_t e = sm_count(&sms);
+  if (e != cudaSuccess) return e;
+  if ((e = launch(pages_compact_plan_kernel, dim3(1), kPlanThreads, stream, false, a.p, w)) != cudaSuccess) return e;
+  return launch(pages_compact_kernel, dim3(4u * (unsigned)sms), kPageThreads, stream, true, a, w);
+}
+
+}  // namespace hs

@@ -128,12 +128,16 @@ typedef enum {
 #define HS_FLAG_ORDER 64u  /* hs_invalidate_host_rows: rows not ascending, nothing cleared */
 #define HS_FLAG_TIMEOUT 128u /* a bounded device wait ran out: that call's outputs are invalid */
 
+#define HS_FLAG_NOPAGE 256u  /* hs_pages_extend / hs_pages_fork: too few free pages for an entry */
+
 /* Limits of this build. */
 #define HS_MAX_TOP_K 4096
 #define HS_MAX_HOT_SLOTS 16384
 #define HS_MAX_LAYERS 8
 #define HS_MAX_SPEC_QUERIES 8 /* verify steps of one speculative batch (n_spec + 1) */
-#define HS_MAX_MLA_SPLITS 16  /* row splits of hs_sparse_mla_decode */
+#define HS_MAX_MLA_SPLITS 16  /* row splits of hs_sparse_mla_decode and of the hs_fp4_*_mla_decode calls */
+#define HS_FP4_ROW_BYTES 416  /* one token's 4-bit MLA row */
+#define HS_MAX_PAGE_REQUESTS 65536 /* num_requests of an hs_page_pool */
 
 /* Configuration of one layer group (layers that share one indexer top-k and therefore
  * one slot map; "vLLM Hybrid HiSparse source implementation analysis" 7.4).
@@ -496,6 +500,173 @@ HS_API hs_status hs_resolve_noalloc(const hs_config* cfg, void* const* host_pool
                                     int32_t* device_buffer_tokens, int32_t* lru_slots, int32_t* lru_clock,
                                     const int32_t* resident_pages, int32_t* out_rows, int32_t* miss_counts,
                                     uint32_t* error_flags, hs_stream_t stream);
+
+/* ---- The 4-bit MLA cache: rows written and read, attention over them, and their pages ----
+ *
+ * A 4-bit row ("vLLM Hybrid HiSparse source implementation analysis", 9, gives the fp8 row it
+ * stands beside: 512 latent dims, scales, 64 bf16 RoPE values, 656 B) is HS_FP4_ROW_BYTES = 416 B:
+ *   bytes   0..255  e2m1 codes, dim 2i in the low nibble of byte i, dim 2i + 1 in the high one
+ *   bytes 256..287  e4m3 scales, one per 16 consecutive dims
+ *   bytes 288..415  64 bf16 RoPE values
+ * latent[d] = e2m1(code[d]) x e4m3(scale[d / 16]) x latent_scale. latent_scale is the caller's, one
+ * per pool, a power of two in [2^-32, 2^32]: it brings the latents into the scales' range (block
+ * maxima from about 2^-6 x 6 to 448 x 6 keep full precision). A pool of such rows goes through
+ * hs_create (row_bytes = 416), hs_resolve and hs_backup like any other, at 0.63 of the fp8 row's bytes. */
+
+/* Write n tokens' rows: token i, kv + i * kv_stride (576 bf16 values: latent, then RoPE), is
+ * quantised into pool row rows[i]. Per block of 16 latent dims, y = x / latent_scale: the scale is
+ * max |y| / 6 and each code y / scale, both rounded to the nearest value of their type, halfway to
+ * the even code, saturating; a block whose scale rounds to zero has zero codes, a block with a NaN
+ * or an infinity reads back as NaN. rows[i] < 0 skips the token; rows[i] >= pool_rows skips it and
+ * sets HS_FLAG_DEVROW. Rows named once each (two tokens for one row in one call: not checked, that
+ * row's bytes are then unspecified).
+ *   kv [n, kv_stride] bf16 bits, device, 16-byte aligned, kv_stride >= 576 and a multiple of 8
+ *   rows [n] int32, pool [pool_rows, 416] device, 16-byte aligned; error_flags: device uint32
+ * One kernel launch; no allocation, no synchronisation; graph-capturable. n == 0 is a no-op. */
+HS_API hs_status hs_fp4_pack_rows(int32_t n, const uint16_t* kv, int64_t kv_stride, const int32_t* rows,
+                                  float latent_scale, uint8_t* pool, int64_t pool_rows, uint32_t* error_flags,
+                                  hs_stream_t stream);
+
+/* Read n rows back: kv + i * kv_stride gets row rows[i]'s 576 values in bf16 (exact, but for values
+ * that latent_scale takes out of bf16's range), zeros where rows[i] is negative, and zeros with
+ * HS_FLAG_DEVROW where it is >= pool_rows. Any row any number of times. Layouts, alignment and
+ * launch rules as in hs_fp4_pack_rows. */
+HS_API hs_status hs_fp4_unpack_rows(int32_t n, const uint8_t* pool, int64_t pool_rows, const int32_t* rows,
+                                    float latent_scale, uint16_t* kv, int64_t kv_stride, uint32_t* error_flags,
+                                    hs_stream_t stream);
+
+/* Splits (1..HS_MAX_MLA_SPLITS) that suit a call of num_queries queries per request (1 for
+ * hs_fp4_sparse_mla_decode) over up to `rows` rows each (top_k; or window + sinks + num_queries - 1)
+ * on the current device, and the workspace a call with that many splits needs (0 for one split, and
+ * for a shape that the calls refuse). Host only. */
+HS_API int32_t hs_fp4_mla_splits(int32_t num_requests, int32_t num_heads, int32_t num_queries, int64_t rows);
+HS_API size_t hs_fp4_mla_workspace_bytes(int32_t num_requests, int32_t num_heads, int32_t num_queries,
+                                         int32_t splits);
+
+/* Sparse-MLA decode attention over 4-bit rows through the resolver's row table: hs_sparse_mla_decode's
+ * formula with the latents above. For request r and head h over the rows j = out_rows[r][i] in
+ * [0, pool_rows) (a row named twice counts twice):
+ *   s[h, j] = sm_scale * (q[h, :512] . latent_j + q[h, 512:] . rope_j)
+ *   o[r, h] = softmax_j(s[h]) . latent,  lse[r, h] = log sum_j exp s[h, j]  (-inf, o = 0 if none)
+ *   q [R, num_heads, 576] bf16 bits (num_heads 1..128), kv_pool [pool_rows, 416] with pool_rows <
+ *   2^31, o [R, num_heads, 512] bf16 bits: device, 16-byte aligned; out_rows [R, top_k], top_k <=
+ *   HS_MAX_TOP_K, lse [R, num_heads] fp32: device
+ *   splits (1..HS_MAX_MLA_SPLITS) divides each request's rows over more CTAs; hs_fp4_mla_splits
+ *   suggests a number. workspace: hs_fp4_mla_workspace_bytes(R, num_heads, 1, splits) device bytes,
+ *   16-byte aligned; calls that share it must be ordered.
+ *   error_flags: device uint32, HS_FLAG_* bits OR-ed in.
+ * No allocation, no synchronisation; graph-capturable. num_requests == 0 is a no-op. */
+HS_API hs_status hs_fp4_sparse_mla_decode(int32_t num_requests, int32_t num_heads, int32_t top_k, int32_t splits,
+                                          const uint16_t* q, const uint8_t* kv_pool, int64_t pool_rows,
+                                          const int32_t* out_rows, float sm_scale, float latent_scale, uint16_t* o,
+                                          float* lse, void* workspace, size_t workspace_bytes,
+                                          uint32_t* error_flags, hs_stream_t stream);
+
+/* Sliding-window MLA decode attention with sinks, over 4-bit rows through the page table ("vLLM
+ * HiSparse local KV offload architecture", residency: the newest pages stay on the GPU). The last
+ * num_queries (1..HS_MAX_SPEC_QUERIES) of request r's seq_lens[r] tokens are its queries (one new
+ * token, or the verify steps of a speculative batch): query i is token p = seq_lens[r] -
+ * num_queries + i and sees the tokens t <= p with t < sinks or t > p - window, that is itself, the
+ * window - 1 tokens before it and the first `sinks` tokens of the sequence. Token t's row is
+ * resident_pages[r][t / page_size] * page_size + t % page_size; tokens whose page is negative or
+ * whose row is past the pool are left out, with HS_FLAG_DEVROW. A query with p < 0 (a padded
+ * request, or one shorter than num_queries) sees nothing: o = 0, lse = -inf. seq_lens[r] outside
+ * [0, max_pages * page_size] does the same for the whole request and sets HS_FLAG_SEQLEN.
+ * window >= 1, sinks >= 0.
+ *   q [R, num_queries, num_heads, 576], o [R, num_queries, num_heads, 512], lse [R, num_queries,
+ *   num_heads], seq_lens [R], resident_pages [R, max_pages]; workspace for (R, num_heads,
+ *   num_queries, splits); everything else, and the formula, as in hs_fp4_sparse_mla_decode. */
+HS_API hs_status hs_fp4_window_mla_decode(int32_t num_requests, int32_t num_heads, int32_t num_queries,
+                                          int32_t window, int32_t sinks, int32_t splits, const uint16_t* q,
+                                          const uint8_t* kv_pool, int64_t pool_rows, int32_t page_size,
+                                          int32_t max_pages, const int32_t* seq_lens,
+                                          const int32_t* resident_pages, float sm_scale, float latent_scale,
+                                          uint16_t* o, float* lse, void* workspace, size_t workspace_bytes,
+                                          uint32_t* error_flags, hs_stream_t stream);
+
+/* The pages of one layer group's device pools and who holds them. Page b is the pool rows
+ * b * page_size .. b * page_size + page_size - 1 of every layer. The struct is read during the
+ * call; the buffers are the caller's, on the current device:
+ *   device_pools    num_layers pools of at least num_pages * page_size rows of row_bytes
+ *   resident_pages  [num_requests, max_pages]  hs_resolve's table: page of the request's tokens
+ *                   b * page_size .., or -1
+ *   page_refs       [num_pages]  table entries that hold the page; 0 for a free page
+ *   free_pages      [num_pages]  stack of the free pages: entries 0 .. *free_count - 1, top last
+ *   free_count      [1]
+ *   error_flags     uint32, HS_FLAG_* bits OR-ed in
+ *   workspace       hs_pages_workspace_bytes(num_requests, num_pages) bytes, 16-byte aligned,
+ *                   zeroed once before its first call (hs_pages_init does that too)
+ * Calls that share any of these must be ordered (one stream, or events). A state that no sequence
+ * of these calls leaves (a page held but not counted, a stack entry out of range, ...) sets
+ * HS_FLAG_STATE where it is met; nothing outside the buffers is read or written. All calls: at
+ * most two kernel launches, no allocation, no synchronisation, graph-capturable; the same state
+ * and arguments give the same result. row_bytes is any (656, 416, ...). */
+typedef struct {
+  int32_t num_requests; /* 1..HS_MAX_PAGE_REQUESTS */
+  int32_t max_pages;
+  int32_t num_pages; /* num_pages * page_size < 2^31 */
+  int32_t page_size;
+  int32_t row_bytes;
+  int32_t num_layers; /* 1..HS_MAX_LAYERS */
+  void* device_pools[HS_MAX_LAYERS];
+  int32_t* resident_pages;
+  int32_t* page_refs;
+  int32_t* free_pages;
+  int32_t* free_count;
+  uint32_t* error_flags;
+  void* workspace;
+  size_t workspace_bytes;
+} hs_page_pool;
+
+/* Workspace bytes; 0 for a size out of range. Host only. */
+HS_API size_t hs_pages_workspace_bytes(int32_t num_requests, int32_t num_pages);
+
+/* Every page free (page 0 on top of the stack), every table entry -1, the workspace ready. The
+ * pools are not touched. One kernel launch. */
+HS_API hs_status hs_pages_init(const hs_page_pool* pool, hs_stream_t stream);
+
+/* Sequences grow: entry i gives request requests[i] fresh pages for its tokens old_lens[i] ..
+ * new_lens[i] - 1, that is the page indices [ceil(old / page_size), ceil(new / page_size)), popped
+ * from the stack in entry order, index ascending, each with one reference. All or nothing per
+ * entry: it gets its pages if they and those of the entries before it are on the stack (and then
+ * those of no later entry are), else none, with HS_FLAG_NOPAGE. Refused too: a request out of range
+ * (HS_FLAG_TOKEN), named twice (every one of them, HS_FLAG_DUP), lengths that are negative, fall,
+ * or pass max_pages * page_size (HS_FLAG_SEQLEN), an index that holds a page already
+ * (HS_FLAG_STATE). A negative request is padding.
+ *   requests, old_lens, new_lens [n] device; granted [n] device or NULL: pages given, -1 refused
+ * One kernel launch. n == 0 is a no-op. */
+HS_API hs_status hs_pages_extend(const hs_page_pool* pool, int32_t n, const int32_t* requests,
+                                 const int32_t* old_lens, const int32_t* new_lens, int32_t* granted,
+                                 hs_stream_t stream);
+
+/* Sequences branch: entry i makes request children[i], whose row holds no page, a copy of the
+ * first lens[i] tokens of request parents[i]. Whole pages are shared (one reference more each; an
+ * index without a page stays without); of a last page that is not full, the lens[i] % page_size
+ * rows are copied in every layer into a fresh page of the child's, whose other rows are left as
+ * they were. So a page that tokens are still appended to is never shared. Fresh pages go by entry
+ * order as in hs_pages_extend (HS_FLAG_NOPAGE). Refused: requests out of range (HS_FLAG_TOKEN), a
+ * child named twice or also a parent of the call (HS_FLAG_DUP), a length outside [0, max_pages *
+ * page_size] (HS_FLAG_SEQLEN), a child's row that holds a page (HS_FLAG_STATE). A negative parent
+ * or child is padding. A refused entry changes nothing.
+ *   parents, children, lens [n] device, n <= num_requests; granted [n] device or NULL: fresh pages
+ *   taken (0 or 1), -1 refused
+ * Two kernel launches. n == 0 is a no-op. */
+HS_API hs_status hs_pages_fork(const hs_page_pool* pool, int32_t n, const int32_t* parents, const int32_t* children,
+                               const int32_t* lens, int32_t* granted, hs_stream_t stream);
+
+/* Requests give pages back: the table entries [first_pages[i], end_pages[i]) of requests[i] (NULL
+ * arrays: from the start, to the end of the row; ranges are cut to the row) become -1 and each
+ * one's page loses a reference; the pages that nobody holds then go onto the stack in descending
+ * order, the lowest on top. Entries may overlap or repeat. A negative request is padding, one out
+ * of range is skipped (HS_FLAG_TOKEN). Two kernel launches. n == 0 is a no-op. */
+HS_API hs_status hs_pages_free(const hs_page_pool* pool, int32_t n, const int32_t* requests,
+                               const int32_t* first_pages, const int32_t* end_pages, hs_stream_t stream);
+
+/* The live pages move together: with V pages in use, the k-th page in use at or past page V moves,
+ * in every layer, to the k-th free page below V, every table entry follows, and the stack holds
+ * pages num_pages - 1 .. V, V on top: afterwards pages V .. num_pages - 1 are the caller's to use
+ * otherwise. Tables of rows made before (out_rows) are stale. Two kernel launches. */
+HS_API hs_status hs_pages_compact(const hs_page_pool* pool, hs_stream_t stream);
 
 #ifdef __cplusplus
 }
