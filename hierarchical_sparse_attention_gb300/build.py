@@ -19,6 +19,7 @@ BUILD_DIR = os.path.join(ROOT, "_build", "hs")
 LIB = os.path.join(PKG, "libhs.so")
 SOURCES = ["hs_resolve.cu", "hs_backup.cu", "hs_gather.cu", "hs_invalidate.cu", "hs_sparse_mla.cu", "hs_fp4_rows.cu",
            "hs_fp4_mla.cu", "hs_pages.cu", "hs_api.cu", "hs_noalloc.cu"]
+HEADERS = ["hs_internal.h", "hs_fp4.h", "hs_tcgen05.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden",
               "-I", INCLUDE, "-I", CSRC]
@@ -38,7 +39,7 @@ def _stale(out: str, deps: List[str]) -> bool:
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
-    headers = [os.path.join(CSRC, "hs_internal.h"), os.path.join(CSRC, "hs_fp4.h"), os.path.join(INCLUDE, "hs.h")]
+    headers = [os.path.join(INCLUDE, "hs.h")] + [os.path.join(CSRC, h) for h in HEADERS]
     objs, procs = [], []
     for src in SOURCES:
         s = os.path.join(CSRC, src)

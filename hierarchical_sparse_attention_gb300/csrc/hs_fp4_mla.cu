@@ -1,114 +1,778 @@
-// MLA decode attention over 4-bit rows: through a row table (hs_fp4_sparse_mla_decode) or through
-// a page table for the tokens of a sliding window and its sinks (hs_fp4_window_mla_decode).
+// MLA decode attention over 4-bit rows on the 5th-generation tensor cores (tcgen05, accumulators in
+// tensor memory): through a row table (hs_fp4_sparse_mla_decode) or through a page table for the
+// tokens of a sliding window and its sinks (hs_fp4_window_mla_decode).
 //
-// Per query (request r, query i, head h) over the rows j that it sees:
-//   s_j = sm_scale (q[:512] . latent_j + q[512:] . rope_j),   o = softmax(s) . latent,
+// Per query head over the rows j that it sees:
+//   s_j = sm_scale (q[:512] . latent_j + q[512:] . rope_j),  o = softmax(s) . latent,
 //   lse = log sum_j exp s_j
-// One CTA per query and head; each warp takes every eighth row and keeps the running maximum m,
-// the sum l and the output of what it has seen: a new maximum m' scales l and the output by
-// exp(m - m'). The warps' parts are joined in shared memory. All sums are in 32 bits.
+//
+// Tiles. The 128 rows of an MMA are query heads of one request: all heads of as many of its queries
+// as fit (one query of 65 heads or more, eight of 16). A pair of CTAs in a cluster takes (tile,
+// split of the tile's rows) and walks the split in blocks of 64 rows:
+//   - the S-CTA (even rank) holds Q in tensor memory and computes S = Q . K^T of each block into one
+//     of two buffers; its softmax warpgroups (each 32 of the block's rows, a query head per thread)
+//     run the online softmax and write P as f16 into the O-CTA's shared memory;
+//   - the O-CTA holds O (128 x 512 in 32 bits, all of its tensor memory) and adds P . V; its
+//     corrector rescales O in the rare blocks that raise a head's reference maximum.
+// In each CTA a loader warp gathers the records (four to a tensor copy) into a ring of half-blocks,
+// and dequantisation warps turn them into the CTA's f16 tile. The roles hand blocks over through
+// mbarriers with bounded waits.
+//
+// Precision. code x scale is exact in f16, so K and V hold the latents' exact values but for
+// latent_scale, which goes into the scores' scale and the outputs instead. Q's latent part is
+// rounded from bf16 to f16: exact between 2^-14 and 65504, off by at most 2^-25 below. RoPE values
+// meet Q's in bf16, exact (Q's divided by latent_scale, a power of two), in MMAs of their own type
+// that add to the same sums. P is rounded to f16 (2^-11 of each weight, against 2^-8 of bf16: P is
+// the one operand that has to be rounded, and bf16 would cost as much as the output's rounding);
+// the weights' sum takes them unrounded, so lse does not see it. Scores, maxima, sums and O are in
+// 32 bits.
+//
+// NaN and infinities. A row that a query does not see gets P = 0, and 0 x NaN must not reach O: V
+// holds zero for a block whose scale is NaN, while K keeps the NaN, which makes the score, the
+// weight and so the output NaN for the queries that see the row, and only for them.
 #include "hs_fp4.h"
+#include "hs_tcgen05.cuh"
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
-#include <cuda_fp4.h>
 #include <cuda_fp8.h>
 
+#include <cstring>
+
 namespace hs {
+
+using namespace tc;
+
 namespace {
 
-constexpr int kWarps = 8, kThreads = 32 * kWarps;
+constexpr int T = 576;          // threads per CTA: 18 warps
+constexpr int MH = 128;         // MMA M: query heads of a tile (padded with zero rows)
+constexpr int BJ = 64, HB = 32;  // rows per block and half-block
+constexpr int DQK = kFp4Dims, DL = kFp4Latent;
+constexpr int KATOMS = DQK / 64, VATOMS = DL / 64;  // swizzle atoms of 64 values in a K and a V tile
+constexpr int NT = 2;           // tiles in flight
+constexpr int NR = 6;           // raw half-blocks in flight
+constexpr uint32_t TMEM_COLS = 512, Q_COL = 0, S_COL = 288;
+constexpr int S_REC = kFp4Row, O_REC = kFp4RopeAt;  // bytes of a record that each CTA reads
+constexpr int S_GRP = 4 * S_REC, O_GRP = 4 * O_REC;  // a gather's four records
+static_assert(S_GRP % 128 == 0 && O_GRP % 128 == 0, "gathers land on 128-byte boundaries");
+constexpr int S_SLOT = HB / 4 * S_GRP, O_SLOT = HB / 4 * O_GRP;
+// S-CTA warps: 0-7 softmax, 8 issuer, 9 loader, 10-17 dequantisation; O-CTA: 0-3 corrector, 4
+// issuer, 5 loader, 6-13 dequantisation (14-17 only read out at the end)
+constexpr int S_ISSUER = 8, S_LOADER = 9, S_DEQ0 = 10;
+constexpr int O_ISSUER = 4, O_LOADER = 5, O_DEQ0 = 6;
+constexpr int NDEQ = 8;         // dequantisation warps of each CTA: two items of 32 codes per row each
+static_assert(NDEQ * 2 * 32 == DL, "the dequantisation warps cover a row");
+constexpr int MASKS = 32;       // half-blocks whose row masks are kept (the loader is at most 16 ahead)
 
-__global__ void __launch_bounds__(kThreads) fp4_mla_kernel(const Fp4MlaArgs a, uint32_t* __restrict__ err) {
-  __shared__ float s_o[kWarps][kFp4Latent], s_m[kWarps], s_l[kWarps];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int h = blockIdx.y, i = blockIdx.x % a.num_queries, r = blockIdx.x / a.num_queries;
-  int64_t n = 0, sinks = 0, start = 0;  // rows seen; the first `sinks` are tokens 0 .., the rest from `start`
-  if (a.seq_lens == nullptr) {
-    n = a.top_k;
+constexpr uint32_t KV_ATOM = BJ * 128, K_TILE = KATOMS * KV_ATOM, V_TILE = VATOMS * KV_ATOM;
+constexpr uint32_t QBOX = MH * 128;
+constexpr uint32_t S_TILES = 0, S_QSTAGE = 0;  // Q is staged over the K tiles before the first block
+constexpr uint32_t S_RAW = NT * K_TILE;
+static_assert(KATOMS * QBOX <= S_RAW, "Q's staging fits the K tiles");
+constexpr uint32_t S_MX = S_RAW + NR * S_SLOT;
+constexpr uint32_t S_L1 = S_MX + 2 * MH * 4;
+constexpr uint32_t S_END = S_L1 + MH * 4;
+constexpr uint32_t O_TILES = 0, O_RAW = NT * V_TILE;
+constexpr uint32_t O_P = (O_RAW + NR * O_SLOT + 1023u) & ~1023u;
+constexpr uint32_t P_BUF = MH * BJ * 2, P_BYTES = P_BUF + MH * 4;  // P and the rescale factors of a block
+constexpr uint32_t O_ALPHA = O_P + 2 * P_BUF;
+constexpr uint32_t O_FIN = O_ALPHA + 2 * MH * 4;
+constexpr uint32_t O_END = O_FIN + 2 * MH * 4;
+constexpr uint32_t SMASK = S_END > O_END ? S_END : O_END;
+constexpr uint32_t SMEM_BYTES = SMASK + MASKS * 4 + 1024;  // + alignment slack
+static_assert(SMEM_BYTES <= 227 * 1024 - 1024, "shared memory of a CTA");
+constexpr float kRescaleLog2 = 8.f;  // a reference maximum stays until it is passed by 2^8: P < 2^8
+constexpr int EPI_PITCH = 36;        // floats per staged row of the read-out
+static_assert(16 * 32 * EPI_PITCH * 4 <= NT * V_TILE, "the read-out staging fits the V tiles");
+
+constexpr uint32_t kIdescQK = idesc(BJ, MH, false);                              // f16 latents
+constexpr uint32_t kIdescRope = kIdescQK | (1u << 7) | (1u << 10);               // bf16 RoPE
+constexpr uint32_t kIdescPV = idesc(256, MH, true);
+
+struct Barriers {
+  uint64_t raw_full[NR], raw_free[NR];    // loader <-> dequantisation: a ring buffer's records
+  uint64_t tile_full[NT], tile_free[NT];  // dequantisation <-> issuer
+  uint64_t q_raw, q_full;                 // S-CTA: Q staged; Q in tensor memory
+  uint64_t s_full[2], s_free[2];          // S-CTA: S written; S read
+  uint64_t p_free[2];                     // S-CTA, arrived by the O-CTA
+  uint64_t p_full[2];                     // O-CTA, completed by the S-CTA's stores
+  uint64_t pv_go[2];                      // O-CTA: O is ready for P . V of the block
+  uint64_t mma_done;                      // O-CTA: the MMAs issued so far are done
+  uint64_t fin;                           // O-CTA: the S-CTA's totals are here
+};
+
+// The rows of a tile's split, j = 0 .. n - 1, and who sees them.
+template <bool kWin>
+struct Rows {
+  const int32_t* table;  // the request's rows, or its pages
+  int64_t pool_rows;
+  int n, j0;             // rows of this split; the split's first row in the tile's list
+  // window: the list is tokens 0 .. kept - 1, then from `start`
+  int kept, start, page_size;
+
+  __device__ __forceinline__ int token(int j) const { return j0 + j < kept ? j0 + j : start + (j0 + j - kept); }
+  // what the table holds for row j (loaded ahead), and the pool row that it means (-1: none)
+  __device__ __forceinline__ int32_t raw(int j) const {
+    if (j >= n) return -1;
+    return __ldg(table + (kWin ? token(j) / page_size : j0 + j));
+  }
+  __device__ __forceinline__ int32_t row(int32_t raw, int j) const {
+    if (raw < 0) return -1;
+    const int64_t r = kWin ? (int64_t)raw * page_size + token(j) % page_size : raw;
+    return r < pool_rows ? (int32_t)r : -1;
+  }
+};
+
+// The loader warp: half-block k's 32 records into ring buffer k % NR, and the mask of its rows that
+// exist. Rows that do not are gathered as pool row 0 (every gather moves the same bytes; the
+// dequantisation writes zeros for them). The table is read three half-blocks ahead.
+template <bool kS, bool kWin>
+__device__ __forceinline__ void run_loader(const Rows<kWin>& rows, const CUtensorMap* tmap, int nblk, uint8_t* raw,
+                                           uint32_t* masks, Barriers& bs, int lane, uint32_t* err, volatile int* abort) {
+  constexpr int REC = kS ? S_REC : O_REC, GRP = kS ? S_GRP : O_GRP, SLOT = kS ? S_SLOT : O_SLOT;
+  const int halves = 2 * nblk;
+  int32_t t0 = rows.raw(lane), t1 = rows.raw(HB + lane), t2 = rows.raw(2 * HB + lane);
+  bool missing = false;
+  for (int k = 0; k < halves; ++k) {
+    const int j = HB * k + lane;
+    const int32_t pr = rows.row(t0, j);
+    t0 = t1;
+    t1 = t2;
+    t2 = rows.raw(j + 3 * HB);
+    const uint32_t mask = __ballot_sync(0xffffffffu, pr >= 0);
+    if (kS && kWin) missing |= j < rows.n && pr < 0;
+    const int32_t y = pr >= 0 ? pr : 0;
+    int32_t y4[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y4[i] = __shfl_sync(0xffffffffu, y, (4 * lane + i) & 31);
+    if (k >= NR && !__all_sync(0xffffffffu, pipe_wait(bs.raw_free, NR, k - NR, abort))) break;
+    if (lane == 0) {
+      masks[k % MASKS] = mask;
+      bar_arrive_tx(&bs.raw_full[k % NR], HB * REC);
+    }
+    __syncwarp();
+    if (lane < HB / 4)
+      asm volatile(
+          "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
+          "%4, %5, %6}], [%7];" ::"r"(smem_u32(raw + (k % NR) * SLOT + lane * GRP)),
+          "l"(tmap), "r"(0), "r"(y4[0]), "r"(y4[1]), "r"(y4[2]), "r"(y4[3]), "r"(smem_u32(&bs.raw_full[k % NR]))
+          : "memory");
+  }
+  if (kS && kWin && __any_sync(0xffffffffu, missing) && lane == 0) atomicOr(err, HS_FLAG_DEVROW);
+}
+
+// Four bytes of codes (a pair of dims each, low nibble first) to four f16 pairs.
+__device__ __forceinline__ uint4 codes_to_f16(uint32_t w) {
+  uint4 h;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\tcvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(h.x), "=r"(h.y), "=r"(h.z), "=r"(h.w)
+      : "r"(w));
+  return h;
+}
+__device__ __forceinline__ uint4 times(uint4 v, __half2 s) {
+  uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&x[i]), s);
+    x[i] = *reinterpret_cast<const uint32_t*>(&r);
+  }
+  return make_uint4(x[0], x[1], x[2], x[3]);
+}
+
+// One dequantisation warp's part of a half-block, lane = row: items 2 wq and 2 wq + 1 of 32 codes,
+// and in the S-CTA RoPE chunk wq. Rows four apart start at the same bank, so those with bit 2 set
+// take the two items in the other order; the tile's swizzle spreads the stores.
+template <bool kS>
+__device__ __forceinline__ void dequant_half(const uint8_t* __restrict__ rec, uint8_t* __restrict__ tile, int row,
+                                             bool valid, int wq) {
+  const uint32_t rb = (uint32_t)((row >> 3) * 1024 + (row & 7) * 128);
+  const int x = row & 7;
+  const auto at = [&](int d) {  // byte offset of (row, dim d) in the tile
+    return (uint32_t)((d >> 6) * KV_ATOM) + rb + ((uint32_t)(((d & 63) >> 3) ^ x) << 4);
+  };
+  uint32_t scales = *reinterpret_cast<const uint32_t*>(rec + kFp4Scales + 4 * wq);
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int odd = u ^ ((row >> 2) & 1), it = 2 * wq + odd;
+    const uint4 c = *reinterpret_cast<const uint4*>(rec + 16 * it);
+    const uint32_t sc = scales >> (16 * odd);
+    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {  // a scale's 16 dims
+      const uint8_t code = (uint8_t)(sc >> (8 * h));
+      // V: no NaN (see above); K keeps it
+      const bool zero = !valid || (!kS && (code & 0x7F) == 0x7F);
+      const __half2 s = __half2half2(__half(__nv_cvt_fp8_to_halfraw(code, __NV_E4M3)));
+      const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+      const uint4 a = zero ? none : times(codes_to_f16(w[2 * h]), s), b = zero ? none : times(codes_to_f16(w[2 * h + 1]), s);
+      *reinterpret_cast<uint4*>(tile + at(32 * it + 16 * h)) = a;
+      *reinterpret_cast<uint4*>(tile + at(32 * it + 16 * h + 8)) = b;
+    }
+  }
+  if (kS) {
+    uint4 v = *reinterpret_cast<const uint4*>(rec + kFp4RopeAt + 16 * wq);
+    if (!valid) v = make_uint4(0u, 0u, 0u, 0u);
+    *reinterpret_cast<uint4*>(tile + at(DL + 8 * wq)) = v;
+  }
+}
+
+// A dequantisation warp's loop. In the S-CTA it waits, before its first tile store, until Q has
+// left the staging area (which the K tiles overlay).
+template <bool kS>
+__device__ __forceinline__ void run_dequant(int nblk, const uint8_t* raw, const uint32_t* masks, uint8_t* tiles,
+                                            Barriers& bs, int wq, int lane, volatile int* abort) {
+  constexpr int REC = kS ? S_REC : O_REC, GRP = kS ? S_GRP : O_GRP, SLOT = kS ? S_SLOT : O_SLOT;
+  constexpr uint32_t TB = kS ? K_TILE : V_TILE;
+  for (int k = 0; k < 2 * nblk; ++k) {
+    const int b = k >> 1;
+    bool ok = true;
+    if (kS && k == 0) ok = pipe_wait(&bs.q_full, 1, 0, abort);
+    if ((k & 1) == 0 && b >= NT) ok = ok && pipe_wait(bs.tile_free, NT, b - NT, abort);
+    ok = ok && pipe_wait(bs.raw_full, NR, k, abort);
+    if (!__all_sync(0xffffffffu, ok)) break;
+    const uint32_t mask = *(volatile const uint32_t*)&masks[k % MASKS];
+    dequant_half<kS>(raw + (k % NR) * SLOT + (lane >> 2) * GRP + (lane & 3) * REC, tiles + (b % NT) * TB,
+                     (k & 1) * HB + lane, (mask >> lane) & 1u, wq);
+    fence_async_smem();  // the tile's generic writes before the tensor core reads it
+    __syncwarp();
+    if (lane == 0) {
+      bar_arrive(&bs.raw_free[k % NR]);
+      if (k & 1) bar_arrive(&bs.tile_full[b % NT]);
+    }
+  }
+}
+
+// Bits lo .. hi - 1 of a 32-bit mask.
+__device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
+  lo = min(max(lo, 0), 32);
+  hi = min(max(hi, 0), 32);
+  if (hi <= lo) return 0u;
+  return (0xFFFFFFFFu >> (32 - (hi - lo))) << lo;
+}
+
+template <bool kWin>
+__global__ void __launch_bounds__(T, 1)
+    fp4_mla_kernel(const Fp4MlaArgs a, int tiles_per_request, int queries_per_tile,
+                   const __grid_constant__ CUtensorMap tm_s, const __grid_constant__ CUtensorMap tm_o,
+                   const __grid_constant__ CUtensorMap tm_q, float* __restrict__ part_o, float* __restrict__ part_lse,
+                   uint32_t* __restrict__ err) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  __shared__ uint32_t s_taddr;
+  __shared__ __align__(8) Barriers bs;
+  __shared__ int s_abort;
+  __shared__ int s_issued;  // blocks whose MMAs the issuer started (the last commit to wait for)
+  volatile int* abort = &s_abort;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = blockIdx.x & 1u, partner = rank ^ 1u;  // 0: S-CTA, 1: O-CTA
+  const int tile = blockIdx.x >> 1, r = tile / tiles_per_request;
+  const int q0 = (tile - r * tiles_per_request) * queries_per_tile;  // the tile's first query
+  const int nq = min(queries_per_tile, a.num_queries - q0);
+  const int live_heads = nq * a.num_heads;
+  const size_t row0 = ((size_t)r * a.num_queries + q0) * a.num_heads;  // its first row of q, o and lse
+
+  // the tile's rows: every row that some query of the tile sees
+  Rows<kWin> rows;
+  rows.pool_rows = a.pool_rows;
+  int64_t S = 0;
+  int total;
+  if (kWin) {
+    rows.table = a.pages + (size_t)r * a.max_pages;
+    rows.page_size = a.page_size;
+    S = a.seq_lens[r];
+    const bool bad = S < 0 || S > (int64_t)a.max_pages * a.page_size;
+    if (bad && tid == 0) atomicOr(err, HS_FLAG_SEQLEN);
+    // tokens up to the tile's last query, from the first one of its first query
+    const int64_t end = bad ? 0 : max((int64_t)0, S - a.num_queries + q0 + nq);
+    const int64_t first = max((int64_t)0, S - a.num_queries + q0);
+    rows.kept = (int)min((int64_t)a.sinks, end);
+    rows.start = (int)max((int64_t)rows.kept, first + 1 - a.window);
+    total = rows.kept + (int)max((int64_t)0, end - rows.start);
   } else {
-    const int64_t S = a.seq_lens[r];
-    if (S < 0 || S > (int64_t)a.max_pages * a.page_size) {
-      if (threadIdx.x == 0) atomicOr(err, HS_FLAG_SEQLEN);
-    } else if (S - a.num_queries + i >= 0) {
-      const int64_t p = S - a.num_queries + i;
-      sinks = min((int64_t)a.sinks, p + 1);
-      start = max(sinks, p + 1 - a.window);
-      n = sinks + p + 1 - start;
-    }
+    rows.table = a.out_rows + (size_t)r * a.top_k;
+    total = a.top_k;
   }
-  const size_t at = ((size_t)r * a.num_queries + i) * a.num_heads + h;
-  float q[16], q_rope[2];
-#pragma unroll
-  for (int k = 0; k < 16; ++k) q[k] = __uint_as_float((uint32_t)a.q[at * kFp4Dims + 16 * lane + k] << 16);
-#pragma unroll
-  for (int k = 0; k < 2; ++k) q_rope[k] = __uint_as_float((uint32_t)a.q[at * kFp4Dims + kFp4Latent + 2 * lane + k] << 16);
-  float m = -INFINITY, l = 0.f, o[16] = {};
-  for (int64_t j = warp; j < n; j += kWarps) {
-    int64_t row;
-    if (a.seq_lens == nullptr) {
-      row = a.out_rows[(size_t)r * a.top_k + j];
-    } else {
-      const int64_t t = j < sinks ? j : start + j - sinks;
-      const int32_t page = a.pages[(size_t)r * a.max_pages + t / a.page_size];
-      row = page < 0 ? -1 : (int64_t)page * a.page_size + t % a.page_size;
-      if ((row < 0 || row >= a.pool_rows) && lane == 0) atomicOr(err, HS_FLAG_DEVROW);
+  const int all_blocks = (int)(((int64_t)total + BJ - 1) / BJ), per = (all_blocks + a.splits - 1) / a.splits;
+  const int p = blockIdx.y;
+  const int nblk = max(0, min(per, all_blocks - p * per));
+  rows.j0 = p * per * BJ;
+  rows.n = nblk > 0 ? min(total - rows.j0, nblk * BJ) : 0;
+
+  if (tid == 0) {
+    for (int k = 0; k < NR; ++k) {
+      bar_init(&bs.raw_full[k], 1);  // the loader's arrival with the gathers' bytes
+      bar_init(&bs.raw_free[k], NDEQ);
     }
-    if (row < 0 || row >= a.pool_rows) continue;
-    const uint8_t* rec = a.pool + row * kFp4Row;
-    const uint2 c = *reinterpret_cast<const uint2*>(rec + 8 * lane);
-    const float sc = __half2float(__half(__nv_cvt_fp8_to_halfraw(rec[kFp4Scales + lane], __NV_E4M3))) * a.latent_scale;
-    const uint32_t rope = *reinterpret_cast<const uint32_t*>(rec + kFp4RopeAt + 4 * lane);
-    float v[16], s = 0.f;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const uint32_t b = ((k < 4 ? c.x : c.y) >> (8 * (k & 3))) & 0xFFu;
-      const float2 x = __half22float2(__half2(__nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)b, __NV_E2M1)));
-      v[2 * k] = x.x * sc;
-      v[2 * k + 1] = x.y * sc;
-      s += q[2 * k] * v[2 * k] + q[2 * k + 1] * v[2 * k + 1];
+    for (int k = 0; k < NT; ++k) {
+      bar_init(&bs.tile_full[k], NDEQ);
+      bar_init(&bs.tile_free[k], 1);
     }
-    s += q_rope[0] * __uint_as_float(rope << 16) + q_rope[1] * __uint_as_float(rope & 0xFFFF0000u);
-#pragma unroll
-    for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-    s *= a.sm_scale;
-    const float mn = fmaxf(m, s), f = m == -INFINITY ? 0.f : expf(m - mn), p = s == -INFINITY ? 0.f : expf(s - mn);
-    l = l * f + p;
-#pragma unroll
-    for (int k = 0; k < 16; ++k) o[k] = o[k] * f + p * v[k];
-    m = mn;
+    bar_init(&bs.q_raw, 1);
+    bar_init(&bs.q_full, 8);  // one arrival per softmax warp
+    bar_init(&bs.mma_done, 1);
+    for (int k = 0; k < 2; ++k) {
+      bar_init(&bs.s_full[k], 1);
+      bar_init(&bs.s_free[k], 8);
+      bar_init(&bs.p_free[k], 1);
+      bar_init(&bs.p_full[k], 1);  // the O-CTA's expect_tx; the S-CTA's stores complete it
+      bar_init(&bs.pv_go[k], 4);
+    }
+    bar_init(&bs.fin, 4);
+    s_abort = 0;
+    s_issued = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    if (rank == 0 && nblk > 0) {
+      // Q's 128 rows as nine tensor boxes of 64 dims (rows past the tile's are not used)
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // q_raw's init, seen by the copies
+      bar_arrive_tx(&bs.q_raw, KATOMS * QBOX);
+      for (int bx = 0; bx < KATOMS; ++bx)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+            "[%4];" ::"r"(smem_u32(base + S_QSTAGE + bx * QBOX)),
+            "l"(&tm_q), "r"(64 * bx), "r"((int)row0), "r"(smem_u32(&bs.q_raw))
+            : "memory");
+    }
+    if (rank == 1)
+      for (int k = 0; k < 2 && k < nblk; ++k) bar_arrive_tx(&bs.p_full[k], P_BYTES);
   }
-#pragma unroll
-  for (int k = 0; k < 16; ++k) s_o[warp][16 * lane + k] = o[k];
-  if (lane == 0) {
-    s_m[warp] = m;
-    s_l[warp] = l;
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_taddr)),
+                 "r"(TMEM_COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  tc_before();
   __syncthreads();
-  float top = -INFINITY, sum = 0.f;
-  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w]);
-  for (int w = 0; w < kWarps; ++w) sum += s_m[w] == -INFINITY && s_l[w] == 0.f ? 0.f : s_l[w] * expf(s_m[w] - top);
-  for (int d = threadIdx.x; d < kFp4Latent; d += kThreads) {
-    float x = 0.f;
-    for (int w = 0; w < kWarps; ++w) x += s_m[w] == -INFINITY && s_l[w] == 0.f ? 0.f : s_o[w][d] * expf(s_m[w] - top);
-    const __nv_bfloat16 b = __float2bfloat16_rn(sum == 0.f ? 0.f : x / sum);
-    a.o[at * kFp4Latent + d] = *reinterpret_cast<const uint16_t*>(&b);
+  tc_after();
+  cluster_sync_all();  // both CTAs' barriers are initialised before either arrives on the other's
+  const uint32_t tbase = s_taddr;
+  const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+  const int head = (warp & 3) * 32 + lane;  // this thread's row of the tile = its tensor-memory lane
+  uint32_t* masks = reinterpret_cast<uint32_t*>(base + SMASK);
+
+  if (rank == 0) {
+    // ================================ S-CTA ================================
+    uint8_t* tiles = base + S_TILES;
+    uint8_t* raw = base + S_RAW;
+    if (warp < 8) {
+      const int wg = warp >> 2;
+      if (nblk > 0) {
+        // Q into tensor memory (warpgroup wg the columns [144 wg, 144 wg + 144)), column c holding
+        // dims 2c, 2c + 1: the latent part as f16, the RoPE part as bf16 over latent_scale
+        const uint8_t* qs = base + S_QSTAGE;
+        const bool landed = sync_and(pipe_wait(&bs.q_raw, 1, 0, abort), 2 * MH);
+        const bool live = landed && head < live_heads;
+        const uint8_t* src = qs + head * 128;
+        const float inv = 1.f / a.latent_scale;
+#pragma unroll 6
+        for (int c = 36 * wg; c < 36 * wg + 36; c += 2) {  // two 16-B chunks: 16 dims, 8 columns
+          uint32_t x[8] = {};
+          if (live) {
+            *reinterpret_cast<uint4*>(x) =
+                *reinterpret_cast<const uint4*>(src + (c >> 3) * QBOX + (((c & 7) ^ (head & 7)) << 4));
+            *reinterpret_cast<uint4*>(x + 4) =
+                *reinterpret_cast<const uint4*>(src + ((c + 1) >> 3) * QBOX + ((((c + 1) & 7) ^ (head & 7)) << 4));
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            if (c < DL / 8) {
+              x[i] = bf16x2_to_f16x2(x[i]);
+            } else {
+              const __nv_bfloat162 v =
+                  __floats2bfloat162_rn(__uint_as_float(x[i] << 16) * inv, __uint_as_float(x[i] & 0xFFFF0000u) * inv);
+              x[i] = *reinterpret_cast<const uint32_t*>(&v);
+            }
+          }
+          asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(
+                           tbase + lane_off + Q_COL + 4 * c),
+                       "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+                       : "memory");
+        }
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        tc_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(&bs.q_full);
+      }
+      // window: this query sees the list's rows [0, see_kept) and [see_lo, see_hi)
+      int see_kept = 0, see_lo = 0, see_hi = 0;
+      if (kWin) {
+        const int64_t at = S - a.num_queries + q0 + head / a.num_heads;  // its token
+        see_kept = (int)min((int64_t)rows.kept, at + 1) - rows.j0;
+        see_lo = (int)(rows.kept + max((int64_t)0, at + 1 - a.window - rows.start)) - rows.j0;
+        see_hi = (int)(rows.kept + max((int64_t)0, at + 1 - rows.start)) - rows.j0;
+      }
+      float* s_mx = reinterpret_cast<float*>(base + S_MX);
+      const uint32_t r_pbuf = remote(base + O_P, partner), r_alpha = remote(base + O_ALPHA, partner);
+      const float sl2 = a.sm_scale * a.latent_scale * 1.4426950408889634f;  // scores in log2 units
+      float m_run = -INFINITY, l_run = 0.f;
+      for (int b = 0; b < nblk; ++b) {
+        // every exit is taken by both warpgroups together (they meet at named barrier 1)
+        if (!sync_and(pipe_wait(bs.s_full, 2, b, abort), 2 * MH)) break;
+        tc_after();
+        uint32_t vm = *(volatile const uint32_t*)&masks[(2 * b + wg) % MASKS];
+        if (kWin) {
+          const int j = BJ * b + HB * wg;
+          vm &= bit_range(0, see_kept - j) | bit_range(see_lo - j, see_hi - j);
+        }
+        float s[HB];
+#pragma unroll
+        for (int q = 0; q < HB / 16; ++q) {
+          float t[16];
+          tmem_ld16(tbase + lane_off + S_COL + BJ * (b & 1) + HB * wg + 16 * q, t);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) s[16 * q + i] = ((vm >> (16 * q + i)) & 1u) ? t[i] * sl2 : -INFINITY;
+        }
+        tc_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(&bs.s_free[b & 1]);  // S is in registers
+        float bm = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < HB; ++i) bm = fmaxf(bm, s[i]);
+        s_mx[wg * MH + head] = bm;
+        sync_n(2 * MH);
+        bm = fmaxf(s_mx[head], s_mx[MH + head]);
+        const float m_new = bm > m_run + kRescaleLog2 || m_run == -INFINITY ? fmaxf(m_run, bm) : m_run;
+        const float alpha = m_new == -INFINITY ? 1.f : exp2f(m_run - m_new);  // m_run = -inf: O is still 0
+        const float ref = m_new == -INFINITY ? 0.f : m_new;  // a NaN score stays one, an unseen row's weight is 0
+        // the O-CTA's P buffer b & 1 is free once its P . V of block b - 2 is done
+        if (!sync_and(b < 2 || pipe_wait<true>(bs.p_free, 2, b - 2, abort), 2 * MH)) break;
+        float psum = 0.f;
+        const uint32_t pbuf = r_pbuf + (b & 1) * P_BUF;
+        const uint32_t rbar = remote(&bs.p_full[b & 1], partner);
+#pragma unroll
+        for (int c = 0; c < HB / 8; ++c) {  // four 16-B chunks of 8 f16: rows 32 wg + 8c ..
+          uint32_t w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float p0 = exp2f(s[8 * c + 2 * i] - ref), p1 = exp2f(s[8 * c + 2 * i + 1] - ref);
+            const __half2 pb = __floats2half2_rn(p0, p1);
+            psum += p0 + p1;
+            w[i] = *reinterpret_cast<const uint32_t*>(&pb);
+          }
+          st_async16(pbuf + sw128(head, HB * wg + 8 * c), make_uint4(w[0], w[1], w[2], w[3]), rbar);
+        }
+        if (wg == 0) st_async_f32(r_alpha + 4 * ((b & 1) * MH + head), alpha, rbar);
+        l_run = l_run * alpha + psum;
+        m_run = m_new;
+      }
+      // the row sums of both warpgroups, and the reference maxima, to the O-CTA
+      float* s_l1 = reinterpret_cast<float*>(base + S_L1);
+      if (wg == 1) s_l1[head] = l_run;
+      sync_n(2 * MH);
+      if (wg == 0) {
+        const uint32_t fin = remote(base + O_FIN, partner);
+        st_remote_f32(fin + 4 * head, l_run + s_l1[head]);
+        st_remote_f32(fin + 4 * (MH + head), m_run);
+        __syncwarp();
+        if (lane == 0) bar_arrive_remote(remote(&bs.fin, partner));
+      }
+    } else if (warp == S_ISSUER) {
+      bool go = __all_sync(0xffffffffu, nblk == 0 || pipe_wait(&bs.q_full, 1, 0, abort));
+      for (int b = 0; go && b < nblk; ++b) {
+        bool ok = pipe_wait(bs.tile_full, NT, b, abort);
+        ok = ok && (b < 2 || pipe_wait(bs.s_free, 2, b - 2, abort));
+        if (!__all_sync(0xffffffffu, ok)) break;
+        tc_after();
+        if (lane == 0) {
+          const uint64_t dk0 = mdesc(smem_u32(tiles + (b % NT) * K_TILE), 16, 1024);
+#pragma unroll
+          for (int kk = 0; kk < KATOMS * 4; ++kk) {
+            const int at = kk >> 2, w = kk & 3;
+            mma_ta(tbase + S_COL + BJ * (b & 1), tbase + Q_COL + 8 * kk,
+                   dk0 + (uint64_t)((at * KV_ATOM + w * 32) >> 4), kk < DL / 16 ? kIdescQK : kIdescRope, kk > 0);
+          }
+          commit(&bs.s_full[b & 1]);
+          commit(&bs.tile_free[b % NT]);
+          s_issued = b + 1;
+        }
+        __syncwarp();
+      }
+    } else if (warp == S_LOADER) {
+      run_loader<true, kWin>(rows, &tm_s, nblk, raw, masks, bs, lane, err, abort);
+    } else {
+      run_dequant<true>(nblk, raw, masks, tiles, bs, warp - S_DEQ0, lane, abort);
+    }
+  } else {
+    // ================================ O-CTA ================================
+    uint8_t* tiles = base + O_TILES;
+    uint8_t* raw = base + O_RAW;
+    const float* alpha_buf = reinterpret_cast<const float*>(base + O_ALPHA);
+    if (warp < 4) {
+      // corrector: if a head's reference maximum rose, rescale O once P . V of block b - 1 is done
+      for (int b = 0; b < nblk; ++b) {
+        if (!sync_and(pipe_wait<true>(bs.p_full, 2, b, abort), MH)) break;
+        const float f = alpha_buf[(b & 1) * MH + head];
+        // this buffer's next phase is block b + 2: its bytes come only after P . V of block b
+        if (tid == 0 && b + 2 < nblk) bar_arrive_tx(&bs.p_full[b & 1], P_BYTES);
+        if (sync_or(b > 0 && f != 1.f, MH)) {
+          if (!sync_and(pipe_wait(bs.tile_free, NT, b - 1, abort), MH)) break;
+          tc_after();
+          for (int c = 0; c < DL; c += 16) {
+            float v[16];
+            tmem_ld16(tbase + lane_off + c, v);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] *= f;
+            tmem_st16(tbase + lane_off + c, v);
+          }
+          tc_before();
+        }
+        __syncwarp();
+        if (lane == 0) bar_arrive(&bs.pv_go[b & 1]);
+      }
+    } else if (warp == O_ISSUER) {
+      for (int b = 0; b < nblk; ++b) {
+        bool ok = pipe_wait(bs.tile_full, NT, b, abort);
+        ok = ok && pipe_wait(bs.pv_go, 2, b, abort);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        tc_after();
+        fence_async_smem();
+        if (lane == 0) {
+          const uint64_t dp0 = mdesc(smem_u32(base + O_P + (b & 1) * P_BUF), 16, 1024);
+          const uint64_t dv0 = mdesc(smem_u32(tiles + (b % NT) * V_TILE), KV_ATOM, 1024);
+#pragma unroll
+          for (int kk = 0; kk < BJ / 16; ++kk)
+#pragma unroll
+            for (int nh = 0; nh < 2; ++nh)
+              mma_ss(tbase + 256 * nh, dp0 + (uint64_t)((kk * 32) >> 4),
+                     dv0 + (uint64_t)((nh * 4 * KV_ATOM + kk * 2048) >> 4), kIdescPV, (b > 0 || kk > 0) ? 1u : 0u);
+          commit(&bs.tile_free[b % NT]);
+          commit_multicast(&bs.p_free[b & 1], (uint16_t)(1u << partner));
+          commit(&bs.mma_done);
+          s_issued = b + 1;
+        }
+        __syncwarp();
+      }
+    } else if (warp == O_LOADER) {
+      run_loader<false, kWin>(rows, &tm_o, nblk, raw, masks, bs, lane, err, abort);
+    } else if (warp < O_DEQ0 + NDEQ) {
+      run_dequant<false>(nblk, raw, masks, tiles, bs, warp - O_DEQ0, lane, abort);
+    }
   }
-  if (threadIdx.x == 0) a.lse[at] = sum == 0.f ? -INFINITY : top + logf(sum);
+
+  __syncthreads();
+  // this CTA's MMAs of every block are done; the O-CTA also has the S-CTA's totals, the S-CTA
+  // the O-CTA's last P-buffer releases (its last arrivals here)
+  bool ok = !*abort && (nblk == 0 || pipe_wait(bs.tile_free, NT, nblk - 1, abort));
+  if (rank == 1) {
+    ok = ok && pipe_wait<true>(&bs.fin, 1, 0, abort);
+  } else {
+    for (int b = nblk >= 2 ? nblk - 2 : 0; b < nblk; ++b) ok = ok && pipe_wait<true>(bs.p_free, 2, b, abort);
+  }
+  ok = __syncthreads_and(ok && !*abort);
+  tc_after();
+  if (rank == 1 && ok && warp < 16) {
+    // O out, normalised: warp w holds rows 32 (w & 3) .. + 31 and takes a quarter of the columns,
+    // 32 at a time through its own staging rows, so that global stores write whole lines
+    const float* fin = reinterpret_cast<const float*>(base + O_FIN);
+    const float l = fin[head], m = fin[MH + head];
+    const float inv = l == 0.f ? 0.f : a.latent_scale / l;  // l is NaN where a weight is
+    const float lse = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+    const int head0 = (warp & 3) * 32;
+    float* stg = reinterpret_cast<float*>(base + O_TILES) + warp * (32 * EPI_PITCH);
+    const bool direct = a.splits == 1;
+    const size_t out0 = direct ? row0 : (size_t)p * ((size_t)(gridDim.x >> 1) / tiles_per_request) * a.num_queries * a.num_heads + row0;
+    const int c0 = (warp >> 2) * (DL / 4);
+    for (int c = c0; c < c0 + DL / 4; c += 32) {
+      float v[32];
+      if (nblk > 0) {
+        tmem_ld16(tbase + lane_off + c, *reinterpret_cast<float(*)[16]>(v));
+        tmem_ld16(tbase + lane_off + c + 16, *reinterpret_cast<float(*)[16]>(v + 16));
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < 32; i += 4)
+        *reinterpret_cast<float4*>(stg + lane * EPI_PITCH + i) =
+            make_float4(v[i] * inv, v[i + 1] * inv, v[i + 2] * inv, v[i + 3] * inv);
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int rr = 4 * i + (lane >> 3), q4 = lane & 7;
+        if (head0 + rr < live_heads) {
+          const float4 x = *reinterpret_cast<const float4*>(stg + rr * EPI_PITCH + 4 * q4);
+          const size_t at = (out0 + head0 + rr) * DL + c + 4 * q4;
+          if (direct) {
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(x.x, x.y), hi = __floats2bfloat162_rn(x.z, x.w);
+            *reinterpret_cast<uint2*>(a.o + at) =
+                make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+          } else {
+            *reinterpret_cast<float4*>(part_o + at) = x;
+          }
+        }
+      }
+      __syncwarp();
+    }
+    if (head < live_heads && warp < 4) (direct ? a.lse : part_lse)[out0 + head] = lse;
+  }
+  if (!ok) {
+    // outputs are not valid: flag it, and give any MMA still in flight one more bound before
+    // the tensor memory is released
+    if (tid == 0) atomicOr(err, HS_FLAG_TIMEOUT);
+    __syncthreads();
+    if (tid == 0) s_abort = 0;
+    __syncthreads();
+    const int n = s_issued;
+    if (n > 0) {
+      if (rank == 0)
+        pipe_wait(bs.s_full, 2, n - 1, abort);
+      else
+        pipe_wait(&bs.mma_done, 1, n - 1, abort);
+    }
+  }
+  tc_before();
+  __syncthreads();
+  if (warp == 0)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tbase), "r"(TMEM_COLS) : "memory");
+  // the merge kernel (if any) may launch; it waits for this grid's completion before reading
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  cluster_sync_all();  // the partner no longer reads or arrives on this CTA's shared memory
+}
+
+// The splits of each query head joined: weights exp(lse_p - lse), lse = log sum exp lse_p, in
+// split order. A thread per four output dims.
+constexpr int COMBINE_T = 256;
+__global__ void __launch_bounds__(COMBINE_T)
+    fp4_combine_kernel(const Fp4MlaArgs a, int rows, const float* __restrict__ part_o, const float* __restrict__ part_lse) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t g = (int64_t)blockIdx.x * COMBINE_T + threadIdx.x;
+  const int64_t row = g >> 7;
+  const int c4 = (int)(g & 127);
+  if (row >= rows) return;
+  float mx = -INFINITY, nan = 0.f;
+  for (int p = 0; p < a.splits; ++p) {
+    const float x = __ldg(part_lse + (size_t)p * rows + row);
+    mx = fmaxf(mx, x);
+    if (x != x) nan = x;
+  }
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float lse = nan != nan ? nan : mx;
+  if (lse != -INFINITY) {
+    float z = 0.f;
+    for (int p = 0; p < a.splits; ++p) z += expf(__ldg(part_lse + (size_t)p * rows + row) - mx);
+    const float inv = 1.f / z;
+    for (int p = 0; p < a.splits; ++p) {
+      const float w = expf(__ldg(part_lse + (size_t)p * rows + row) - mx) * inv;
+      const float4 v = __ldg(reinterpret_cast<const float4*>(part_o + ((size_t)p * rows + row) * DL) + c4);
+      acc.x += w * v.x;
+      acc.y += w * v.y;
+      acc.z += w * v.z;
+      acc.w += w * v.w;
+    }
+    lse = mx + logf(z);
+  }
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x, acc.y), hi = __floats2bfloat162_rn(acc.z, acc.w);
+  reinterpret_cast<uint2*>(a.o + (size_t)row * DL)[c4] =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+  if (c4 == 0) a.lse[row] = lse;
+}
+
+// The pool as a 2-D tensor of 8-byte elements, one row per record, read `box_bytes` at a time from
+// the start of a row (one row per box: the gathers pick the rows).
+cudaError_t pool_map(CUtensorMap* m, const uint8_t* pool, int64_t rows, int box_bytes) {
+  EncodeTiled fn = encoder();
+  if (fn == nullptr) return cudaErrorNotSupported;
+  const cuuint64_t dims[2] = {(cuuint64_t)(kFp4Row / 8), (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)kFp4Row};
+  const cuuint32_t box[2] = {(cuuint32_t)(box_bytes / 8), 1u};
+  const cuuint32_t elem[2] = {1u, 1u};
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT64, 2, const_cast<uint8_t*>(pool), dims, strides, box, elem,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// Q ([rows][576] bf16) as a 2-D tensor read in boxes of 128 rows x 64 dims, its 16-B chunks XOR-ed
+// with the row % 8; rows past the end read as zeros.
+cudaError_t q_map(CUtensorMap* m, const uint16_t* q, int64_t rows) {
+  EncodeTiled fn = encoder();
+  if (fn == nullptr) return cudaErrorNotSupported;
+  const cuuint64_t dims[2] = {(cuuint64_t)DQK, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)DQK * 2};
+  const cuuint32_t box[2] = {64u, (cuuint32_t)MH};
+  const cuuint32_t elem[2] = {1u, 1u};
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<uint16_t*>(q), dims, strides, box, elem,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// Queries of one request whose heads share a tile, and the tiles that its queries make.
+int queries_per_tile(int num_heads, int num_queries) {
+  const int fit = MH / num_heads;
+  return fit < num_queries ? (fit > 1 ? fit : 1) : num_queries;
+}
+int tiles_per_request(int num_heads, int num_queries) {
+  const int g = queries_per_tile(num_heads, num_queries);
+  return (num_queries + g - 1) / g;
 }
 
 }  // namespace
 
-int32_t fp4_mla_splits(int32_t, int32_t, int32_t, int64_t) { return 1; }
+int32_t fp4_mla_splits(int32_t num_requests, int32_t num_heads, int32_t num_queries, int64_t rows) {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return 1;
+  }
+  const int64_t pairs = (int64_t)num_requests * tiles_per_request(num_heads, num_queries), slots = sms / 2 ? sms / 2 : 1;
+  const int64_t blocks = (rows + BJ - 1) / BJ;
+  int64_t best = 1, best_cost = INT64_MAX;
+  for (int64_t s = 1; s <= HS_MAX_MLA_SPLITS && s <= blocks; ++s) {
+    const int64_t waves = (pairs * s + slots - 1) / slots;
+    const int64_t cost = waves * ((blocks + s - 1) / s + 6) + (s > 1 ? 3 + s : 0);
+    if (cost < best_cost) {
+      best = s;
+      best_cost = cost;
+    }
+  }
+  return (int32_t)best;
+}
+
 size_t fp4_mla_workspace_bytes(int32_t num_requests, int32_t num_heads, int32_t num_queries, int32_t splits) {
-  return splits == 1 ? 0 : (size_t)splits * num_requests * num_queries * num_heads * (kFp4Latent + 1) * sizeof(float);
+  return splits == 1 ? 0 : (size_t)splits * num_requests * num_queries * num_heads * (DL + 1) * sizeof(float);
 }
 
 cudaError_t launch_fp4_mla(const Fp4MlaArgs& a, int32_t num_requests, float* part, uint32_t* err,
                            cudaStream_t stream) {
-  (void)part;
-  return launch(fp4_mla_kernel, dim3((unsigned)num_requests * a.num_queries, (unsigned)a.num_heads), kThreads, stream,
-                false, a, err);
+  const bool win = a.seq_lens != nullptr;
+  const auto kernel = win ? fp4_mla_kernel<true> : fp4_mla_kernel<false>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+  const int rows = num_requests * a.num_queries * a.num_heads;
+  CUtensorMap tm_s, tm_o, tm_q;
+  if (e == cudaSuccess) e = q_map(&tm_q, a.q, rows);
+  if (e == cudaSuccess) e = pool_map(&tm_s, a.pool, a.pool_rows, S_REC);
+  if (e == cudaSuccess) e = pool_map(&tm_o, a.pool, a.pool_rows, O_REC);
+  if (e != cudaSuccess) {
+    (void)cudaGetLastError();
+    return e;
+  }
+  const int tiles = tiles_per_request(a.num_heads, a.num_queries), g = queries_per_tile(a.num_heads, a.num_queries);
+  float* part_lse = part ? part + (size_t)a.splits * rows * DL : nullptr;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2u * (unsigned)num_requests * (unsigned)tiles, (unsigned)a.splits);
+  cfg.blockDim = dim3(T);
+  cfg.dynamicSmemBytes = SMEM_BYTES;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kernel, a, tiles, g, tm_s, tm_o, tm_q, part, part_lse, err);
+  if (e != cudaSuccess) {
+    (void)cudaGetLastError();
+    return e;
+  }
+  if (a.splits == 1) return cudaSuccess;
+  return launch(fp4_combine_kernel, dim3((unsigned)(((int64_t)rows * (DL / 4) + COMBINE_T - 1) / COMBINE_T)), COMBINE_T,
+                stream, true, a, rows, (const float*)part, (const float*)part_lse);
 }
 
 }  // namespace hs

@@ -43,8 +43,8 @@
 // cluster fits the device at once); otherwise, and for other split counts, in a small second
 // kernel. Clusters of two CTAs serve one split and the fallback.
 #include "hs_internal.h"
+#include "hs_tcgen05.cuh"
 
-#include <cuda.h>  // CUtensorMap and its encoder's types (the encoder is fetched through the runtime)
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -52,6 +52,9 @@
 #include <mutex>
 
 namespace hs {
+
+using namespace tc;
+
 namespace {
 
 constexpr int T = 512;           // threads per CTA
@@ -106,99 +109,14 @@ constexpr int ROWS_CAP = 2048;                          // a split's row-table e
 constexpr uint32_t SROWS = (S_END > O_END ? S_END : O_END);  // both: the split's rows of the row table
 constexpr uint32_t SMEM_USED = SROWS + ROWS_CAP * 4;
 constexpr uint32_t SMEM_BYTES = SMEM_USED + 1024;       // + alignment slack
-constexpr uint64_t kWaitNs = 100000000ull;              // 100 ms bound on an mbarrier wait
-constexpr uint32_t kSuspendNs = 20000;                  // a waiting thread sleeps up to this long per try
-                                                        // (it wakes when the phase completes), so waiting
-                                                        // warps leave the issue slots to the working ones
 constexpr float kRescaleLog2 = 8.f;                     // reference-maximum slack (log2 units)
 constexpr int EPI_PITCH = 36;                           // floats per staged row of the read-out (16-B aligned,
                                                         // and 8 lanes' 16-B stores hit distinct banks)
 static_assert(16 * 32 * EPI_PITCH * 4 <= NT * V_TILE, "the read-out staging fits the V tiles' space");
 static_assert(S_RAW >= NT * K_TILE, "the staged Q covers the K tiles only");
 
-__device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-
-// Byte offset of (row, k) in a K-major tile whose rows are 128 B (64 f16), swizzled in
-// 8-row groups of 1024 B: the 16-B chunk index is XOR-ed with row % 8.
-__device__ __forceinline__ uint32_t sw128(int row, int k) {
-  return (uint32_t)((row >> 3) * 1024 + (row & 7) * 128 + ((((k * 2) >> 4) ^ (row & 7)) << 4) + ((k * 2) & 15));
-}
-
-// Shared-memory matrix descriptor: start, leading / stride byte offsets, 128-B swizzle.
-__device__ __forceinline__ uint64_t mdesc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-  return (uint64_t)((saddr >> 4) & 0x3FFF) | ((uint64_t)((lbo >> 4) & 0x3FFF) << 16) |
-         ((uint64_t)((sbo >> 4) & 0x3FFF) << 32) | (1ull << 46) | (2ull << 61);
-}
-// Instruction descriptor, kind::f16: fp32 accumulator, f16 A and B, A K-major, B K- or
-// MN-major, N and M.
-__host__ __device__ constexpr uint32_t idesc(int n, int m, bool b_mn_major) {
-  return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
-}
 constexpr uint32_t kIdescS = idesc(BJ, MH, false);  // S = Q . K^T
 constexpr uint32_t kIdescO = idesc(256, MH, true);  // O[:, n0:n0+256] += P . V (V read MN-major)
-
-__device__ __forceinline__ void commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-               : "memory");
-}
-__device__ __forceinline__ uint64_t gtime() {
-  uint64_t t;
-  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-  return t;
-}
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
-  uint32_t r[16];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-}
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&v)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
-          taddr),
-      "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])), "r"(__float_as_uint(v[3])),
-      "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])), "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7])),
-      "r"(__float_as_uint(v[8])), "r"(__float_as_uint(v[9])), "r"(__float_as_uint(v[10])),
-      "r"(__float_as_uint(v[11])), "r"(__float_as_uint(v[12])), "r"(__float_as_uint(v[13])),
-      "r"(__float_as_uint(v[14])), "r"(__float_as_uint(v[15]))
-      : "memory");
-  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-
-// OR / AND of a predicate over the first n threads of the CTA (named barrier 1; n a multiple of 32).
-// Named barrier 1 serves the softmax / corrector warpgroups, 2 the dequantisation warps.
-template <int id = 1>
-__device__ __forceinline__ int sync_or(bool pred, int n) {
-  int r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, %3, %2, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"((uint32_t)pred), "r"(n), "n"(id)
-      : "memory");
-  return r;
-}
-template <int id = 1>
-__device__ __forceinline__ int sync_and(bool pred, int n) {
-  int r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, %3, %2, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"((uint32_t)pred), "r"(n), "n"(id)
-      : "memory");
-  return r;
-}
-template <int id = 1>
-__device__ __forceinline__ void sync_n(int n) {
-  asm volatile("bar.sync %1, %0;" ::"r"(n), "n"(id) : "memory");
-}
 
 // Two e4m3 codes (low byte first) to an f16 pair, exactly (e4m3 is a subset of f16), times the
 // row's scale in f16.
@@ -208,105 +126,6 @@ __device__ __forceinline__ uint32_t to_f16x2(uint16_t codes, __half2 sc) {
   const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&h2), sc);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
-// A bf16 pair (low half first) to an f16 pair, rounded to nearest.
-__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t w) {
-  const __half2 h = __floats2half2_rn(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-// MMA with A in tensor memory (Q of S): lane m = row m, column c = A[m][2c], A[m][2c + 1].
-__device__ __forceinline__ void mma_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t id, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b), "r"(id), "r"(acc)
-      : "memory");
-}
-// MMA with A and B in shared memory (P of P . V, and V).
-__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a), "l"(b), "r"(id), "r"(acc)
-      : "memory");
-}
-__device__ __forceinline__ void bar_init(uint64_t* bar, uint32_t count) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count) : "memory");
-}
-__device__ __forceinline__ void bar_arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-__device__ __forceinline__ void bar_arrive_tx(uint64_t* bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
-}
-// The partner CTA's copy of a shared-memory address (distributed shared memory).
-__device__ __forceinline__ uint32_t remote(const void* local, uint32_t rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(local)), "r"(rank));
-  return r;
-}
-__device__ __forceinline__ void bar_arrive_remote(uint32_t raddr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(raddr) : "memory");
-}
-__device__ __forceinline__ void st_remote_f32(uint32_t raddr, float v) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(raddr), "f"(v) : "memory");
-}
-// Asynchronous stores into the partner CTA's shared memory that complete their bytes on the
-// partner's mbarrier (no fence or arrival of the storing thread needed).
-__device__ __forceinline__ void st_async16(uint32_t raddr, uint4 v, uint32_t rbar) {
-  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
-                   raddr),
-               "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w), "r"(rbar)
-               : "memory");
-}
-__device__ __forceinline__ void st_async_f32(uint32_t raddr, float v, uint32_t rbar) {
-  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(raddr),
-               "r"(__float_as_uint(v)), "r"(rbar)
-               : "memory");
-}
-// Arrive on the mbarrier at this shared-memory offset in the cluster CTAs of `mask` once the
-// MMAs issued so far are done.
-__device__ __forceinline__ void commit_multicast(uint64_t* bar, uint16_t mask) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::
-                   "r"(smem_u32(bar)),
-               "h"(mask)
-               : "memory");
-}
-__device__ __forceinline__ void cluster_sync_all() {
-  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
-}
-
-// Bounded wait for the completion of use k of a ring of `depth` barriers (barrier k % depth,
-// parity of k / depth); false when the bound ran out or another role gave up (abort set).
-// cluster: the barrier is arrived on from the partner CTA (acquire at cluster scope).
-template <bool cluster = false>
-__device__ __forceinline__ bool pipe_wait(uint64_t* ring, int depth, int k, volatile int* abort) {
-  uint64_t* bar = ring + (k % depth);
-  const uint32_t parity = (uint32_t)(k / depth) & 1u;
-  const uint64_t t0 = gtime();
-  for (;;) {
-    uint32_t done;
-    if (cluster)
-      asm volatile(
-          "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-          "selp.u32 %0, 1, 0, p;\n\t}"
-          : "=r"(done)
-          : "r"(smem_u32(bar)), "r"(parity), "n"(kSuspendNs)
-          : "memory");
-    else
-      asm volatile(
-          "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-          : "=r"(done)
-          : "r"(smem_u32(bar)), "r"(parity), "n"(kSuspendNs)
-          : "memory");
-    if (done) return true;
-    if (*abort || gtime() - t0 > kWaitNs) {
-      *abort = 1;
-      return false;
-    }
-  }
-}
-
 struct Barriers {
   uint64_t raw_full[NR];                // loader -> dequantisation: a ring buffer's records have landed
   uint64_t raw_free[NR];                // every dequantisation warp is done with a ring buffer
@@ -916,25 +735,6 @@ static_assert(SMEM_BYTES <= 227 * 1024, "the consumer's shared memory exceeds a 
 size_t sparse_mla_smem_bytes() { return SMEM_BYTES; }
 
 namespace {
-
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-// The driver's tensor-map encoder, fetched once through the runtime (no link against the
-// driver library).
-EncodeTiled encoder() {
-  static EncodeTiled fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiled>(p);
-  });
-  return fn;
-}
 
 // The pool as a 2-D tensor of 8-byte elements, one row per record (656 B = 82 elements), read
 // `box_bytes` at a time from the start of a row (one row per box: the gathers pick the rows).
