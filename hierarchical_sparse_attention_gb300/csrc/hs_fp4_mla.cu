@@ -14,9 +14,16 @@
 //     run the online softmax and write P as f16 into the O-CTA's shared memory;
 //   - the O-CTA holds O (128 x 512 in 32 bits, all of its tensor memory) and adds P . V; its
 //     corrector rescales O in the rare blocks that raise a head's reference maximum.
-// In each CTA a loader warp gathers the records (four to a tensor copy) into a ring of half-blocks,
-// and dequantisation warps turn them into the CTA's f16 tile. The roles hand blocks over through
+// In each CTA eight dequantisation warps bring the records they own (eight rows of each block) into
+// shared memory with 16-byte asynchronous copies, two blocks ahead, each in a ring of its own that no
+// other warp touches, and write them as f16 into the CTA's tiles. The roles hand blocks over through
 // mbarriers with bounded waits.
+//
+// Why these copies: a row is 416 bytes anywhere in the pool. Measured per SM, rows from HBM / L2:
+// four-row tensor gathers 16 / 24 GB/s from one warp and 20 / 33 from four, a bulk copy per row 24 /
+// 31 from four warps (the copy engine's requests in flight bound them), 16-byte asynchronous copies
+// 56 / 88 (76 SMs at once). Loads into registers blocks ahead are no faster than the gathers: a
+// thread's outstanding loads share a few scoreboards, so that waiting for a block waits for the next.
 //
 // Precision. code x scale is exact in f16, so K and V hold the latents' exact values but for
 // latent_scale, which goes into the scores' scale and the outputs instead. Q's latent part is
@@ -45,42 +52,40 @@ using namespace tc;
 
 namespace {
 
-constexpr int T = 576;          // threads per CTA: 18 warps
+constexpr int T = 544;          // threads per CTA: 17 warps
 constexpr int MH = 128;         // MMA M: query heads of a tile (padded with zero rows)
-constexpr int BJ = 64, HB = 32;  // rows per block and half-block
+constexpr int BJ = 64;          // rows per block
 constexpr int DQK = kFp4Dims, DL = kFp4Latent;
 constexpr int KATOMS = DQK / 64, VATOMS = DL / 64;  // swizzle atoms of 64 values in a K and a V tile
 constexpr int NT = 2;           // tiles in flight
-constexpr int NR = 6;           // raw half-blocks in flight
+constexpr int ND = 3;           // blocks of records in a dequantisation warp's ring: one read, two on their way
 constexpr uint32_t TMEM_COLS = 512, Q_COL = 0, S_COL = 288;
-constexpr int S_REC = kFp4Row, O_REC = kFp4RopeAt;  // bytes of a record that each CTA reads
-constexpr int S_GRP = 4 * S_REC, O_GRP = 4 * O_REC;  // a gather's four records
-static_assert(S_GRP % 128 == 0 && O_GRP % 128 == 0, "gathers land on 128-byte boundaries");
-constexpr int S_SLOT = HB / 4 * S_GRP, O_SLOT = HB / 4 * O_GRP;
-// S-CTA warps: 0-7 softmax, 8 issuer, 9 loader, 10-17 dequantisation; O-CTA: 0-3 corrector, 4
-// issuer, 5 loader, 6-13 dequantisation (14-17 only read out at the end)
-constexpr int S_ISSUER = 8, S_LOADER = 9, S_DEQ0 = 10;
-constexpr int O_ISSUER = 4, O_LOADER = 5, O_DEQ0 = 6;
-constexpr int NDEQ = 8;         // dequantisation warps of each CTA, a swizzle atom of every row each
-static_assert(NDEQ == VATOMS && NDEQ == kFp4Rope / 8, "a swizzle atom of latents and a RoPE chunk per dequantisation warp");
-constexpr int MASKS = 32;       // half-blocks whose row masks are kept (the loader is at most 16 ahead)
+// S-CTA warps: 0-7 softmax, 8 issuer, 9-16 dequantisation; O-CTA: 0-3 corrector, 4 issuer, 5-12
+// dequantisation (13-15 only read out at the end)
+constexpr int S_ISSUER = 8, S_DEQ0 = 9;
+constexpr int O_ISSUER = 4, O_DEQ0 = 5;
+constexpr int NDEQ = 8;         // dequantisation warps of each CTA, eight rows of a block each
+static_assert(NDEQ * 8 == BJ, "the dequantisation warps cover a block");
+constexpr int MASKS = 16;       // blocks whose row masks are kept (the copies are at most 7 blocks ahead of the softmax)
 
 constexpr uint32_t KV_ATOM = BJ * 128, K_TILE = KATOMS * KV_ATOM, V_TILE = VATOMS * KV_ATOM;
 constexpr uint32_t QBOX = MH * 128;
+constexpr int S_REC = kFp4Row, O_REC = kFp4RopeAt;  // bytes of a record that each CTA reads
+constexpr uint32_t S_RING = ND * 8 * S_REC, O_RING = ND * 8 * O_REC;  // a dequantisation warp's ring
 constexpr uint32_t S_TILES = 0, S_QSTAGE = 0;  // Q is staged over the K tiles before the first block
 constexpr uint32_t S_RAW = NT * K_TILE;
 static_assert(KATOMS * QBOX <= S_RAW, "Q's staging fits the K tiles");
-constexpr uint32_t S_MX = S_RAW + NR * S_SLOT;
-constexpr uint32_t S_L1 = S_MX + 2 * MH * 4;
-constexpr uint32_t S_END = S_L1 + MH * 4;
+constexpr uint32_t S_REF = S_RAW + NDEQ * S_RING;  // the reference maxima, handed from block to block
+constexpr uint32_t S_SUMS = S_REF + MH * 4;     // each softmax warpgroup's sums and their references
+constexpr uint32_t S_MASK = S_SUMS + 4 * MH * 4;  // a byte per block and dequantisation warp: its rows that exist
+constexpr uint32_t S_END = S_MASK + MASKS * NDEQ;
 constexpr uint32_t O_TILES = 0, O_RAW = NT * V_TILE;
-constexpr uint32_t O_P = (O_RAW + NR * O_SLOT + 1023u) & ~1023u;
+constexpr uint32_t O_P = (O_RAW + NDEQ * O_RING + 1023u) & ~1023u;
 constexpr uint32_t P_BUF = MH * BJ * 2, P_BYTES = P_BUF + MH * 4;  // P and the rescale factors of a block
 constexpr uint32_t O_ALPHA = O_P + 2 * P_BUF;
 constexpr uint32_t O_FIN = O_ALPHA + 2 * MH * 4;
 constexpr uint32_t O_END = O_FIN + 2 * MH * 4;
-constexpr uint32_t SMASK = S_END > O_END ? S_END : O_END;
-constexpr uint32_t SMEM_BYTES = SMASK + MASKS * 4 + 1024;  // + alignment slack
+constexpr uint32_t SMEM_BYTES = (S_END > O_END ? S_END : O_END) + 1024;  // + alignment slack
 static_assert(SMEM_BYTES <= 227 * 1024 - 1024, "shared memory of a CTA");
 constexpr float kRescaleLog2 = 8.f;  // a reference maximum stays until it is passed by 2^8: P < 2^8
 constexpr int EPI_PITCH = 36;        // floats per staged row of the read-out
@@ -91,16 +96,58 @@ constexpr uint32_t kIdescRope = kIdescQK | (1u << 7) | (1u << 10);              
 constexpr uint32_t kIdescPV = idesc(256, MH, true);
 
 struct Barriers {
-  uint64_t raw_full[NR], raw_free[NR];    // loader <-> dequantisation: a ring buffer's records
   uint64_t tile_full[NT], tile_free[NT];  // dequantisation <-> issuer
   uint64_t q_raw, q_full;                 // S-CTA: Q staged; Q in tensor memory
   uint64_t s_full[2], s_free[2];          // S-CTA: S written; S read
+  uint64_t m_set[2][4];                   // S-CTA: the block's reference maxima of a warp's heads are set
   uint64_t p_free[2];                     // S-CTA, arrived by the O-CTA
   uint64_t p_full[2];                     // O-CTA, completed by the S-CTA's stores
   uint64_t pv_go[2];                      // O-CTA: O is ready for P . V of the block
   uint64_t mma_done;                      // O-CTA: the MMAs issued so far are done
   uint64_t fin;                           // O-CTA: the S-CTA's totals are here
 };
+
+// pipe_wait for waits that are mostly over when they begin: the clock is read only once the first
+// try has failed (reading it first made every hand-over ~0.1 us longer).
+template <bool cluster = false>
+__device__ __forceinline__ bool ready_or_wait(uint64_t* ring, int depth, int k, volatile int* abort) {
+  uint64_t* bar = ring + (k % depth);
+  const uint32_t parity = (uint32_t)(k / depth) & 1u;
+  uint32_t done;
+  if (cluster)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity), "n"(kSuspendNs)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity), "n"(kSuspendNs)
+        : "memory");
+  return done || pipe_wait<cluster>(ring, depth, k, abort);
+}
+
+__device__ __forceinline__ float ex2(float x) {  // 2^x: -inf gives 0, NaN stays
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// 64 accumulator columns of this thread's row.
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, float (&v)[64]) {
+#pragma unroll
+  for (int h = 0; h < 64; h += 16) {
+    uint32_t* r = reinterpret_cast<uint32_t*>(v + h);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr + h));
+  }
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
 
 // The rows of a tile's split, j = 0 .. n - 1, and who sees them.
 template <bool kWin>
@@ -124,44 +171,6 @@ struct Rows {
   }
 };
 
-// The loader warp: half-block k's 32 records into ring buffer k % NR, and the mask of its rows that
-// exist. Rows that do not are gathered as pool row 0 (every gather moves the same bytes; the
-// dequantisation writes zeros for them). The table is read three half-blocks ahead.
-template <bool kS, bool kWin>
-__device__ __forceinline__ void run_loader(const Rows<kWin>& rows, const CUtensorMap* tmap, int nblk, uint8_t* raw,
-                                           uint32_t* masks, Barriers& bs, int lane, uint32_t* err, volatile int* abort) {
-  constexpr int REC = kS ? S_REC : O_REC, GRP = kS ? S_GRP : O_GRP, SLOT = kS ? S_SLOT : O_SLOT;
-  const int halves = 2 * nblk;
-  int32_t t0 = rows.raw(lane), t1 = rows.raw(HB + lane), t2 = rows.raw(2 * HB + lane);
-  bool missing = false;
-  for (int k = 0; k < halves; ++k) {
-    const int j = HB * k + lane;
-    const int32_t pr = rows.row(t0, j);
-    t0 = t1;
-    t1 = t2;
-    t2 = rows.raw(j + 3 * HB);
-    const uint32_t mask = __ballot_sync(0xffffffffu, pr >= 0);
-    if (kS && kWin) missing |= j < rows.n && pr < 0;
-    const int32_t y = pr >= 0 ? pr : 0;
-    int32_t y4[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) y4[i] = __shfl_sync(0xffffffffu, y, (4 * lane + i) & 31);
-    if (k >= NR && !__all_sync(0xffffffffu, pipe_wait(bs.raw_free, NR, k - NR, abort))) break;
-    if (lane == 0) {
-      masks[k % MASKS] = mask;
-      bar_arrive_tx(&bs.raw_full[k % NR], HB * REC);
-    }
-    __syncwarp();
-    if (lane < HB / 4)
-      asm volatile(
-          "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
-          "%4, %5, %6}], [%7];" ::"r"(smem_u32(raw + (k % NR) * SLOT + lane * GRP)),
-          "l"(tmap), "r"(0), "r"(y4[0]), "r"(y4[1]), "r"(y4[2]), "r"(y4[3]), "r"(smem_u32(&bs.raw_full[k % NR]))
-          : "memory");
-  }
-  if (kS && kWin && __any_sync(0xffffffffu, missing) && lane == 0) atomicOr(err, HS_FLAG_DEVROW);
-}
-
 // Four bytes of codes (a pair of dims each, low nibble first) to four f16 pairs.
 __device__ __forceinline__ uint4 codes_to_f16(uint32_t w) {
   uint4 h;
@@ -182,74 +191,132 @@ __device__ __forceinline__ uint4 times(uint4 v, __half2 s) {
   return make_uint4(x[0], x[1], x[2], x[3]);
 }
 
-// One dequantisation warp's part of a half-block, lane = row: 64 latent dims (one swizzle atom) as
-// four items of 16 codes and a scale, and in the S-CTA a RoPE chunk. A row's items come in the order
-// u ^ (row / 4 % 4) and its chunk is wq ^ (row / 4 % 2): records four rows apart start at the same
-// bank, and this moves their reads to other banks while the stores of eight rows stay spread over a
-// line by the swizzle (an order that exchanged items four chunks apart made them meet two by two:
-// 1,527 clocks per block for the S-CTA's share alone).
-struct Piece {  // what a lane reads of its record
-  uint2 codes[4];
-  uint32_t scales;
-  uint4 rope;
-};
-template <bool kS>
-__device__ __forceinline__ Piece read_piece(const uint8_t* rec, int row, int wq) {
-  Piece x;
+// A dequantisation warp's copies of a block: its eight rows' first REC bytes into a slot of its ring,
+// 16 bytes a lane; rows that do not exist become zeros. y: lane l has row l % 8 (-1: none).
+template <int REC>
+__device__ __forceinline__ void copy_rows(uint32_t slot, int32_t y, const uint8_t* __restrict__ pool, int lane) {
+  constexpr int PER = REC / 16, N = 8 * PER;
 #pragma unroll
-  for (int u = 0; u < 4; ++u) x.codes[u] = *reinterpret_cast<const uint2*>(rec + 32 * wq + 8 * (u ^ ((row >> 2) & 3)));
-  x.scales = *reinterpret_cast<const uint32_t*>(rec + kFp4Scales + 4 * wq);
-  if (kS) x.rope = *reinterpret_cast<const uint4*>(rec + kFp4RopeAt + 16 * (wq ^ ((row >> 2) & 1)));
-  return x;
-}
-template <bool kS>
-__device__ __forceinline__ void write_piece(const Piece& piece, uint8_t* tile, int row, bool valid, int wq) {
-  const uint32_t rb = (uint32_t)((row >> 3) * 1024 + (row & 7) * 128);
-  const int x = row & 7;
-  uint8_t* atom = tile + wq * KV_ATOM + rb;
-  const uint4 none = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    const int it = u ^ ((row >> 2) & 3);
-    const uint8_t code = (uint8_t)(piece.scales >> (8 * it));
-    // V: no NaN (see above); K keeps it
-    const bool zero = !valid || (!kS && (code & 0x7F) == 0x7F);
-    const __half2 s = __half2half2(__half(__nv_cvt_fp8_to_halfraw(code, __NV_E4M3)));
-    const uint4 a = zero ? none : times(codes_to_f16(piece.codes[u].x), s);
-    const uint4 b = zero ? none : times(codes_to_f16(piece.codes[u].y), s);
-    *reinterpret_cast<uint4*>(atom + (((2 * it) ^ x) << 4)) = a;
-    *reinterpret_cast<uint4*>(atom + (((2 * it + 1) ^ x) << 4)) = b;
+  for (int i = 0; i < (N + 31) / 32; ++i) {
+    const int c = 32 * i + lane, r = c / PER, o = c - r * PER;
+    const int32_t row = __shfl_sync(0xffffffffu, y, r & 7);
+    if (N % 32 == 0 || c < N)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(slot + 16 * c),
+                   "l"(pool + (int64_t)max(row, 0) * kFp4Row + 16 * o), "r"(row >= 0 ? 16 : 0)
+                   : "memory");
   }
-  if (kS)
-    *reinterpret_cast<uint4*>(tile + VATOMS * KV_ATOM + rb + (((wq ^ ((row >> 2) & 1)) ^ x) << 4)) = valid ? piece.rope : none;
 }
 
-// A dequantisation warp's loop. In the S-CTA it waits, before its first tile store, until Q has
-// left the staging area (which the K tiles overlay).
+// What a lane reads of its warp's eight rows. Step s covers four rows (4 (s / 2) ..) and half of
+// their latent dims: lane = (row of the four, 32 dims `it`), placed so that the eight lanes of a load
+// or store phase have four rows and both halves of a line: the reads (rows 416 or 288 bytes apart)
+// and, through the tile's swizzle, the writes then meet every bank once.
+struct Held {
+  uint4 codes[4];
+  uint16_t scales[4];
+  uint4 rope[2];
+};
 template <bool kS>
-__device__ __forceinline__ void run_dequant(int nblk, const uint8_t* raw, const uint32_t* masks, uint8_t* tiles,
-                                            Barriers& bs, int wq, int lane, volatile int* abort) {
-  constexpr int REC = kS ? S_REC : O_REC, GRP = kS ? S_GRP : O_GRP, SLOT = kS ? S_SLOT : O_SLOT;
+__device__ __forceinline__ Held read_rows(const uint8_t* slot, int lane) {
+  constexpr int REC = kS ? S_REC : O_REC;
+  Held h;
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    const uint8_t* rec = slot + (4 * (s >> 1) + ((lane >> 1) & 3)) * REC;
+    const int it = (lane & 1) + 2 * (lane >> 3) + 8 * (s & 1);
+    h.codes[s] = *reinterpret_cast<const uint4*>(rec + 16 * it);
+    h.scales[s] = *reinterpret_cast<const uint16_t*>(rec + kFp4Scales + 2 * it);
+  }
+  if (kS)
+#pragma unroll
+    for (int g = 0; g < 2; ++g)  // four rows' RoPE values, a chunk per lane
+      h.rope[g] = *reinterpret_cast<const uint4*>(slot + (4 * g + (lane >> 3)) * REC + kFp4RopeAt + 16 * (lane & 7));
+  return h;
+}
+
+// Writes them into the tile, as f16, at the warp's group of eight rows.
+template <bool kS>
+__device__ __forceinline__ void write_rows(const Held& h, uint8_t* group, int lane) {
+  const int in4 = (lane >> 1) & 3;
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    const int g = s >> 1, it = (lane & 1) + 2 * (lane >> 3) + 8 * (s & 1);
+    uint8_t* at = group + (it >> 1) * KV_ATOM + (4 * g + in4) * 128 + ((lane & 1) ^ g) * 64;
+    const uint32_t w[4] = {h.codes[s].x, h.codes[s].y, h.codes[s].z, h.codes[s].w};
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {  // a scale's 16 dims
+      uint32_t code = ((uint32_t)h.scales[s] >> (8 * b)) & 0xFFu;
+      if (!kS && (code & 0x7Fu) == 0x7Fu) code = 0;  // V: no NaN (see above); K keeps it
+      const __half2 sc = __half2half2(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)code, __NV_E4M3)));
+#pragma unroll
+      for (int u = 2 * b; u < 2 * b + 2; ++u)
+        *reinterpret_cast<uint4*>(at + ((u ^ in4) << 4)) = times(codes_to_f16(w[u]), sc);
+    }
+  }
+  if (kS)
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      const int row = 4 * g + (lane >> 3);
+      *reinterpret_cast<uint4*>(group + VATOMS * KV_ATOM + row * 128 + (((lane & 7) ^ row) << 4)) = h.rope[g];
+    }
+}
+
+// A dequantisation warp's loop: block b is written while the rows of the next ND - 1 blocks are on
+// their way, and two more blocks' row numbers. In the S-CTA it waits, before its first tile write,
+// until Q has left the staging area, and tells the softmax which of its rows exist.
+template <bool kS, bool kWin>
+__device__ __forceinline__ void run_dequant(const Rows<kWin>& rows, const uint8_t* __restrict__ pool, int nblk,
+                                            uint8_t* ring, uint8_t* masks, uint8_t* tiles, Barriers& bs, int wq,
+                                            int lane, uint32_t* err, volatile int* abort) {
+  constexpr int REC = kS ? S_REC : O_REC;
   constexpr uint32_t TB = kS ? K_TILE : V_TILE;
-  for (int k = 0; k < 2 * nblk; ++k) {
-    const int b = k >> 1;
-    if (!__all_sync(0xffffffffu, pipe_wait(bs.raw_full, NR, k, abort))) break;
-    const uint32_t mask = *(volatile const uint32_t*)&masks[k % MASKS];
-    const int row = (k & 1) * HB + lane;
-    const Piece piece = read_piece<kS>(raw + (k % NR) * SLOT + (lane >> 2) * GRP + (lane & 3) * REC, row, wq);
-    __syncwarp();
-    if (lane == 0) bar_arrive(&bs.raw_free[k % NR]);  // the records are in registers
-    bool ok = true;
-    if (kS && k == 0) ok = pipe_wait(&bs.q_full, 1, 0, abort);
-    if ((k & 1) == 0 && b >= NT) ok = ok && pipe_wait(bs.tile_free, NT, b - NT, abort);
-    if (!__all_sync(0xffffffffu, ok)) break;
-    write_piece<kS>(piece, tiles + (b % NT) * TB, row, (mask >> lane) & 1u, wq);
-    if (k & 1) {
+  const int own = 8 * wq + (lane & 7);
+  bool missing = false, ok = true;
+  auto start = [&](int32_t raw, int b) {  // the copies of block b (one group of copies, empty past the end)
+    if (b < nblk) {
+      const int j = BJ * b + own;
+      const int32_t y = rows.row(raw, j);
+      if (kS) {
+        if (kWin) missing |= j < rows.n && y < 0;
+        const uint32_t mask = __ballot_sync(0xffffffffu, y >= 0);
+        if (lane == 0) masks[(b % MASKS) * NDEQ + wq] = (uint8_t)mask;
+      }
+      copy_rows<REC>(smem_u32(ring + (b % ND) * (8 * REC)), y, pool, lane);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  {
+    int32_t first[ND - 1];
+#pragma unroll
+    for (int c = 0; c < ND - 1; ++c) first[c] = rows.raw(BJ * c + own);
+#pragma unroll
+    for (int c = 0; c < ND - 1; ++c) start(first[c], c);
+  }
+  int32_t next[2];  // of the next two blocks to start; the loop is unrolled so that none moves before its use
+#pragma unroll
+  for (int c = 0; c < 2; ++c) next[c] = rows.raw(BJ * (ND - 1 + c) + own);
+  for (int b0 = 0; ok && b0 < nblk; b0 += 2) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int b = b0 + c;
+      if (b >= nblk) break;
+      start(next[c], b + ND - 1);  // into the slot that block b - 1 was read from
+      next[c] = rows.raw(BJ * (b + ND + 1) + own);
+      asm volatile("cp.async.wait_group %0;" ::"n"(ND - 1) : "memory");
+      __syncwarp();
+      const Held held = read_rows<kS>(ring + (b % ND) * (8 * REC), lane);
+      if (kS && b == 0) ok = ready_or_wait(&bs.q_full, 1, 0, abort);
+      if (b >= NT) ok = ok && ready_or_wait(bs.tile_free, NT, b - NT, abort);
+      ok = __all_sync(0xffffffffu, ok);  // (and the slot has been read)
+      if (!ok) break;
+      write_rows<kS>(held, tiles + (b % NT) * TB + wq * 1024, lane);
       fence_async_smem();  // the tile's generic writes before the tensor core reads it
       __syncwarp();
       if (lane == 0) bar_arrive(&bs.tile_full[b % NT]);
     }
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");  // none is left in flight at the end
+  if (kS && kWin && __any_sync(0xffffffffu, missing) && lane == 0) atomicOr(err, HS_FLAG_DEVROW);
 }
 
 // Bits lo .. hi - 1 of a 32-bit mask.
@@ -263,7 +330,6 @@ __device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
 template <bool kWin>
 __global__ void __launch_bounds__(T, 1)
     fp4_mla_kernel(const Fp4MlaArgs a, int tiles_per_request, int queries_per_tile,
-                   const __grid_constant__ CUtensorMap tm_s, const __grid_constant__ CUtensorMap tm_o,
                    const __grid_constant__ CUtensorMap tm_q, float* __restrict__ part_o, float* __restrict__ part_lse,
                    uint32_t* __restrict__ err) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -309,10 +375,6 @@ __global__ void __launch_bounds__(T, 1)
   rows.n = nblk > 0 ? min(total - rows.j0, nblk * BJ) : 0;
 
   if (tid == 0) {
-    for (int k = 0; k < NR; ++k) {
-      bar_init(&bs.raw_full[k], 1);  // the loader's arrival with the gathers' bytes
-      bar_init(&bs.raw_free[k], NDEQ);
-    }
     for (int k = 0; k < NT; ++k) {
       bar_init(&bs.tile_full[k], NDEQ);
       bar_init(&bs.tile_free[k], 1);
@@ -322,7 +384,8 @@ __global__ void __launch_bounds__(T, 1)
     bar_init(&bs.mma_done, 1);
     for (int k = 0; k < 2; ++k) {
       bar_init(&bs.s_full[k], 1);
-      bar_init(&bs.s_free[k], 8);
+      bar_init(&bs.s_free[k], 4);  // the warps of the block's softmax warpgroup
+      for (int w = 0; w < 4; ++w) bar_init(&bs.m_set[k][w], 1);
       bar_init(&bs.p_free[k], 1);
       bar_init(&bs.p_full[k], 1);  // the O-CTA's expect_tx; the S-CTA's stores complete it
       bar_init(&bs.pv_go[k], 4);
@@ -358,12 +421,11 @@ __global__ void __launch_bounds__(T, 1)
   const uint32_t tbase = s_taddr;
   const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
   const int head = (warp & 3) * 32 + lane;  // this thread's row of the tile = its tensor-memory lane
-  uint32_t* masks = reinterpret_cast<uint32_t*>(base + SMASK);
+  uint8_t* masks = base + S_MASK;
 
   if (rank == 0) {
     // ================================ S-CTA ================================
     uint8_t* tiles = base + S_TILES;
-    uint8_t* raw = base + S_RAW;
     if (warp < 8) {
       const int wg = warp >> 2;
       if (nblk > 0) {
@@ -374,6 +436,7 @@ __global__ void __launch_bounds__(T, 1)
         const bool live = landed && head < live_heads;
         const uint8_t* src = qs + head * 128;
         const float inv = 1.f / a.latent_scale;
+        const uint32_t sign = a.sm_scale < 0.f ? 0x80008000u : 0u;  // so that scores scale by a positive factor
 #pragma unroll 6
         for (int c = 36 * wg; c < 36 * wg + 36; c += 2) {  // two 16-B chunks: 16 dims, 8 columns
           uint32_t x[8] = {};
@@ -392,6 +455,7 @@ __global__ void __launch_bounds__(T, 1)
                   __floats2bfloat162_rn(__uint_as_float(x[i] << 16) * inv, __uint_as_float(x[i] & 0xFFFF0000u) * inv);
               x[i] = *reinterpret_cast<const uint32_t*>(&v);
             }
+            x[i] ^= sign;
           }
           asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(
                            tbase + lane_off + Q_COL + 4 * c),
@@ -411,76 +475,87 @@ __global__ void __launch_bounds__(T, 1)
         see_lo = (int)(rows.kept + max((int64_t)0, at + 1 - a.window - rows.start)) - rows.j0;
         see_hi = (int)(rows.kept + max((int64_t)0, at + 1 - rows.start)) - rows.j0;
       }
-      float* s_mx = reinterpret_cast<float*>(base + S_MX);
+      // Warpgroup wg takes the blocks b with b % 2 = wg, a query head per thread. From one block
+      // to the next only the reference maximum goes over, from warp to warp (the two warps of the
+      // same heads): it is known once a block's scores are read, so the warpgroups' exponentials
+      // overlap. Each keeps the sum of its own blocks under the reference of its last one.
+      float* s_ref = reinterpret_cast<float*>(base + S_REF);
       const uint32_t r_pbuf = remote(base + O_P, partner), r_alpha = remote(base + O_ALPHA, partner);
-      const float sl2 = a.sm_scale * a.latent_scale * 1.4426950408889634f;  // scores in log2 units
-      float m_run = -INFINITY, l_run = 0.f;
-      for (int b = 0; b < nblk; ++b) {
-        // every exit is taken by both warpgroups together (they meet at named barrier 1)
-        if (!sync_and(pipe_wait(bs.s_full, 2, b, abort), 2 * MH)) break;
+      // scores in log2 units; a scale of zero stays above it, so that -inf stays -inf
+      const float sl2 = fmaxf(fabsf(a.sm_scale * a.latent_scale * 1.4426950408889634f), 1e-37f);
+      float m_own = -INFINITY, l_own = 0.f;
+      for (int b = wg; b < nblk; b += 2) {
+        if (!__all_sync(0xffffffffu, ready_or_wait(bs.s_full, 2, b, abort))) break;
         tc_after();
-        uint32_t vm = *(volatile const uint32_t*)&masks[(2 * b + wg) % MASKS];
-        if (kWin) {
-          const int j = BJ * b + HB * wg;
-          vm &= bit_range(0, see_kept - j) | bit_range(see_lo - j, see_hi - j);
-        }
-        float s[HB];
-#pragma unroll
-        for (int q = 0; q < HB / 16; ++q) {
-          float t[16];
-          tmem_ld16(tbase + lane_off + S_COL + BJ * (b & 1) + HB * wg + 16 * q, t);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) s[16 * q + i] = ((vm >> (16 * q + i)) & 1u) ? t[i] * sl2 : -INFINITY;
-        }
+        float t[BJ];
+        tmem_ld64(tbase + lane_off + S_COL + BJ * wg, t);
         tc_before();
         __syncwarp();
-        if (lane == 0) bar_arrive(&bs.s_free[b & 1]);  // S is in registers
-        float bm = -INFINITY;
+        if (lane == 0) bar_arrive(&bs.s_free[wg]);  // S is in registers
+        uint32_t vm[2];
+        bool all = true;
 #pragma unroll
-        for (int i = 0; i < HB; ++i) bm = fmaxf(bm, s[i]);
-        s_mx[wg * MH + head] = bm;
-        sync_n(2 * MH);
-        bm = fmaxf(s_mx[head], s_mx[MH + head]);
+        for (int h = 0; h < 2; ++h) {
+          vm[h] = *(volatile const uint32_t*)(masks + (b % MASKS) * NDEQ + 4 * h);
+          if (kWin) {
+            const int j = BJ * b + 32 * h;
+            vm[h] &= bit_range(0, see_kept - j) | bit_range(see_lo - j, see_hi - j);
+          }
+          all = all && vm[h] == 0xFFFFFFFFu;
+        }
+        if (!__all_sync(0xffffffffu, all)) {
+#pragma unroll
+          for (int i = 0; i < BJ; ++i) t[i] = ((vm[i / 32] >> (i % 32)) & 1u) ? t[i] : -INFINITY;
+        }
+        float bm = t[0];
+#pragma unroll
+        for (int i = 1; i < BJ; ++i) bm = fmaxf(bm, t[i]);
+        bm *= sl2;
+        float m_run = -INFINITY;
+        if (b > 0) {
+          if (!__all_sync(0xffffffffu, ready_or_wait(&bs.m_set[(b - 1) & 1][warp & 3], 1, (b - 1) >> 1, abort))) break;
+          m_run = s_ref[head];
+        }
+        // Lazy rescale: a head keeps its reference until a block's maximum passes it by 2^8, so P
+        // stays below 2^8 and O is rescaled only on those rare jumps. (bm is NaN if every score is:
+        // the reference then stays.)
         const float m_new = bm > m_run + kRescaleLog2 || m_run == -INFINITY ? fmaxf(m_run, bm) : m_run;
-        const float alpha = m_new == -INFINITY ? 1.f : exp2f(m_run - m_new);  // m_run = -inf: O is still 0
+        s_ref[head] = m_new;
+        __syncwarp();
+        if (lane == 0) bar_arrive(&bs.m_set[b & 1][warp & 3]);
+        const float alpha = m_new == -INFINITY ? 1.f : ex2(m_run - m_new);  // m_run = -inf: O is still 0
         const float ref = m_new == -INFINITY ? 0.f : m_new;  // a NaN score stays one, an unseen row's weight is 0
-        // the O-CTA's P buffer b & 1 is free once its P . V of block b - 2 is done
-        if (!sync_and(b < 2 || pipe_wait<true>(bs.p_free, 2, b - 2, abort), 2 * MH)) break;
-        float psum = 0.f;
-        const uint32_t pbuf = r_pbuf + (b & 1) * P_BUF;
-        const uint32_t rbar = remote(&bs.p_full[b & 1], partner);
+        l_own *= m_new == -INFINITY ? 1.f : ex2(m_own - m_new);
+        m_own = m_new;
+        // the O-CTA's P buffer wg is free once its P . V of block b - 2 is done
+        if (!__all_sync(0xffffffffu, b < 2 || ready_or_wait<true>(bs.p_free, 2, b - 2, abort))) break;
+        const uint32_t pbuf = r_pbuf + wg * P_BUF;
+        const uint32_t rbar = remote(&bs.p_full[wg], partner);
+        st_async_f32(r_alpha + 4 * (wg * MH + head), alpha, rbar);
+        float sum0 = 0.f, sum1 = 0.f;
 #pragma unroll
-        for (int c = 0; c < HB / 8; ++c) {  // four 16-B chunks of 8 f16: rows 32 wg + 8c ..
+        for (int c = 0; c < BJ / 8; ++c) {  // eight 16-B chunks of 8 f16
           uint32_t w[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float p0 = exp2f(s[8 * c + 2 * i] - ref), p1 = exp2f(s[8 * c + 2 * i + 1] - ref);
+            const float p0 = ex2(fmaf(t[8 * c + 2 * i], sl2, -ref)), p1 = ex2(fmaf(t[8 * c + 2 * i + 1], sl2, -ref));
             const __half2 pb = __floats2half2_rn(p0, p1);
-            psum += p0 + p1;
+            sum0 += p0;
+            sum1 += p1;
             w[i] = *reinterpret_cast<const uint32_t*>(&pb);
           }
-          st_async16(pbuf + sw128(head, HB * wg + 8 * c), make_uint4(w[0], w[1], w[2], w[3]), rbar);
+          st_async16(pbuf + sw128(head, 8 * c), make_uint4(w[0], w[1], w[2], w[3]), rbar);
         }
-        if (wg == 0) st_async_f32(r_alpha + 4 * ((b & 1) * MH + head), alpha, rbar);
-        l_run = l_run * alpha + psum;
-        m_run = m_new;
+        l_own += sum0 + sum1;
       }
-      // the row sums of both warpgroups, and the reference maxima, to the O-CTA
-      float* s_l1 = reinterpret_cast<float*>(base + S_L1);
-      if (wg == 1) s_l1[head] = l_run;
-      sync_n(2 * MH);
-      if (wg == 0) {
-        const uint32_t fin = remote(base + O_FIN, partner);
-        st_remote_f32(fin + 4 * head, l_run + s_l1[head]);
-        st_remote_f32(fin + 4 * (MH + head), m_run);
-        __syncwarp();
-        if (lane == 0) bar_arrive_remote(remote(&bs.fin, partner));
-      }
+      float* sums = reinterpret_cast<float*>(base + S_SUMS);
+      sums[2 * wg * MH + head] = l_own;
+      sums[(2 * wg + 1) * MH + head] = m_own;
     } else if (warp == S_ISSUER) {
       bool go = __all_sync(0xffffffffu, nblk == 0 || pipe_wait(&bs.q_full, 1, 0, abort));
       for (int b = 0; go && b < nblk; ++b) {
-        bool ok = pipe_wait(bs.tile_full, NT, b, abort);
-        ok = ok && (b < 2 || pipe_wait(bs.s_free, 2, b - 2, abort));
+        bool ok = ready_or_wait(bs.tile_full, NT, b, abort);
+        ok = ok && (b < 2 || ready_or_wait(bs.s_free, 2, b - 2, abort));
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_after();
         if (lane == 0) {
@@ -497,25 +572,24 @@ __global__ void __launch_bounds__(T, 1)
         }
         __syncwarp();
       }
-    } else if (warp == S_LOADER) {
-      run_loader<true, kWin>(rows, &tm_s, nblk, raw, masks, bs, lane, err, abort);
     } else {
-      run_dequant<true>(nblk, raw, masks, tiles, bs, warp - S_DEQ0, lane, abort);
+      run_dequant<true, kWin>(rows, a.pool, nblk, base + S_RAW + (warp - S_DEQ0) * S_RING, masks, tiles, bs, warp - S_DEQ0,
+                              lane, err, abort);
     }
   } else {
     // ================================ O-CTA ================================
     uint8_t* tiles = base + O_TILES;
-    uint8_t* raw = base + O_RAW;
     const float* alpha_buf = reinterpret_cast<const float*>(base + O_ALPHA);
     if (warp < 4) {
-      // corrector: if a head's reference maximum rose, rescale O once P . V of block b - 1 is done
+      // corrector: where a reference maximum of the warp's heads rose, rescale O once P . V of block
+      // b - 1 is done
       for (int b = 0; b < nblk; ++b) {
-        if (!sync_and(pipe_wait<true>(bs.p_full, 2, b, abort), MH)) break;
+        if (!__all_sync(0xffffffffu, ready_or_wait<true>(bs.p_full, 2, b, abort))) break;
         const float f = alpha_buf[(b & 1) * MH + head];
         // this buffer's next phase is block b + 2: its bytes come only after P . V of block b
         if (tid == 0 && b + 2 < nblk) bar_arrive_tx(&bs.p_full[b & 1], P_BYTES);
-        if (sync_or(b > 0 && f != 1.f, MH)) {
-          if (!sync_and(pipe_wait(bs.tile_free, NT, b - 1, abort), MH)) break;
+        if (__any_sync(0xffffffffu, b > 0 && f != 1.f)) {
+          if (!__all_sync(0xffffffffu, ready_or_wait(bs.tile_free, NT, b - 1, abort))) break;
           tc_after();
           for (int c = 0; c < DL; c += 16) {
             float v[16];
@@ -531,8 +605,8 @@ __global__ void __launch_bounds__(T, 1)
       }
     } else if (warp == O_ISSUER) {
       for (int b = 0; b < nblk; ++b) {
-        bool ok = pipe_wait(bs.tile_full, NT, b, abort);
-        ok = ok && pipe_wait(bs.pv_go, 2, b, abort);
+        bool ok = ready_or_wait(bs.tile_full, NT, b, abort);
+        ok = ok && ready_or_wait(bs.pv_go, 2, b, abort);
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_after();
         fence_async_smem();
@@ -552,14 +626,25 @@ __global__ void __launch_bounds__(T, 1)
         }
         __syncwarp();
       }
-    } else if (warp == O_LOADER) {
-      run_loader<false, kWin>(rows, &tm_o, nblk, raw, masks, bs, lane, err, abort);
     } else if (warp < O_DEQ0 + NDEQ) {
-      run_dequant<false>(nblk, raw, masks, tiles, bs, warp - O_DEQ0, lane, abort);
+      run_dequant<false, kWin>(rows, a.pool, nblk, base + O_RAW + (warp - O_DEQ0) * O_RING, masks, tiles, bs, warp - O_DEQ0,
+                               lane, err, abort);
     }
   }
 
   __syncthreads();
+  if (rank == 0 && warp < 4) {
+    // the sums of both warpgroups under the last block's reference, and that, to the O-CTA
+    const float* sums = reinterpret_cast<const float*>(base + S_SUMS);
+    const float l0 = sums[head], m0 = sums[MH + head], l1 = sums[2 * MH + head], m1 = sums[3 * MH + head];
+    const float m = nblk > 0 ? reinterpret_cast<const float*>(base + S_REF)[head] : -INFINITY;
+    const auto part = [&](float l, float mo) { return m == -INFINITY ? l : l * ex2(mo - m); };
+    const uint32_t fin = remote(base + O_FIN, partner);
+    st_remote_f32(fin + 4 * head, part(l0, m0) + part(l1, m1));
+    st_remote_f32(fin + 4 * (MH + head), m);
+    __syncwarp();
+    if (lane == 0) bar_arrive_remote(remote(&bs.fin, partner));
+  }
   // this CTA's MMAs of every block are done; the O-CTA also has the S-CTA's totals, the S-CTA
   // the O-CTA's last P-buffer releases (its last arrivals here)
   bool ok = !*abort && (nblk == 0 || pipe_wait(bs.tile_free, NT, nblk - 1, abort));
@@ -677,21 +762,6 @@ __global__ void __launch_bounds__(COMBINE_T)
   if (c4 == 0) a.lse[row] = lse;
 }
 
-// The pool as a 2-D tensor of 8-byte elements, one row per record, read `box_bytes` at a time from
-// the start of a row (one row per box: the gathers pick the rows).
-cudaError_t pool_map(CUtensorMap* m, const uint8_t* pool, int64_t rows, int box_bytes) {
-  EncodeTiled fn = encoder();
-  if (fn == nullptr) return cudaErrorNotSupported;
-  const cuuint64_t dims[2] = {(cuuint64_t)(kFp4Row / 8), (cuuint64_t)rows};
-  const cuuint64_t strides[1] = {(cuuint64_t)kFp4Row};
-  const cuuint32_t box[2] = {(cuuint32_t)(box_bytes / 8), 1u};
-  const cuuint32_t elem[2] = {1u, 1u};
-  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT64, 2, const_cast<uint8_t*>(pool), dims, strides, box, elem,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
 // Q ([rows][576] bf16) as a 2-D tensor read in boxes of 128 rows x 64 dims, its 16-B chunks XOR-ed
 // with the row % 8; rows past the end read as zeros.
 cudaError_t q_map(CUtensorMap* m, const uint16_t* q, int64_t rows) {
@@ -750,10 +820,8 @@ cudaError_t launch_fp4_mla(const Fp4MlaArgs& a, int32_t num_requests, float* par
   const auto kernel = win ? fp4_mla_kernel<true> : fp4_mla_kernel<false>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
   const int rows = num_requests * a.num_queries * a.num_heads;
-  CUtensorMap tm_s, tm_o, tm_q;
+  CUtensorMap tm_q;
   if (e == cudaSuccess) e = q_map(&tm_q, a.q, rows);
-  if (e == cudaSuccess) e = pool_map(&tm_s, a.pool, a.pool_rows, S_REC);
-  if (e == cudaSuccess) e = pool_map(&tm_o, a.pool, a.pool_rows, O_REC);
   if (e != cudaSuccess) {
     (void)cudaGetLastError();
     return e;
@@ -772,7 +840,7 @@ cudaError_t launch_fp4_mla(const Fp4MlaArgs& a, int32_t num_requests, float* par
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kernel, a, tiles, g, tm_s, tm_o, tm_q, part, part_lse, err);
+  e = cudaLaunchKernelEx(&cfg, kernel, a, tiles, g, tm_q, part, part_lse, err);
   if (e != cudaSuccess) {
     (void)cudaGetLastError();
     return e;
