@@ -107,8 +107,16 @@ struct Barriers {
   uint64_t fin;                           // O-CTA: the S-CTA's totals are here
 };
 
+// The kernel's roles run side by side from one instruction cache, and much of their time goes into
+// handing over: so their loops are short (not unrolled over blocks: at 165 KB of code the same loops
+// took up to twice as long as at 70 KB), and the wait that has to look at the clock is a call.
+template <bool cluster>
+__device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  return pipe_wait<cluster>(bar, 1, (int)parity, abort);
+}
 // pipe_wait for waits that are mostly over when they begin: the clock is read only once the first
-// try has failed (reading it first made every hand-over ~0.1 us longer).
+// try has failed (reading it first made every hand-over ~0.1 us longer). Use k of a ring of `depth`
+// barriers; a waiter has to have seen the ring's use k - depth over (parities repeat).
 template <bool cluster = false>
 __device__ __forceinline__ bool ready_or_wait(uint64_t* ring, int depth, int k, volatile int* abort) {
   uint64_t* bar = ring + (k % depth);
@@ -127,7 +135,15 @@ __device__ __forceinline__ bool ready_or_wait(uint64_t* ring, int depth, int k, 
         : "=r"(done)
         : "r"(smem_u32(bar)), "r"(parity), "n"(kSuspendNs)
         : "memory");
-  return done || pipe_wait<cluster>(ring, depth, k, abort);
+  return done || wait_on<cluster>(bar, parity, abort);
+}
+// One lane of the (converged) warp. The MMAs are issued by it from code that the whole warp runs, so
+// that their operands stay in uniform registers: 33 clocks an MMA of N = 64 with A in tensor memory,
+// where `if (lane == 0)` around the loop made it 58.
+__device__ __forceinline__ bool elected() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
 }
 
 __device__ __forceinline__ float ex2(float x) {  // 2^x: -inf gives 0, NaN stays
@@ -271,7 +287,7 @@ __device__ __forceinline__ void run_dequant(const Rows<kWin>& rows, const uint8_
   constexpr int REC = kS ? S_REC : O_REC;
   constexpr uint32_t TB = kS ? K_TILE : V_TILE;
   const int own = 8 * wq + (lane & 7);
-  bool missing = false, ok = true;
+  bool missing = false;
   auto start = [&](int32_t raw, int b) {  // the copies of block b (one group of copies, empty past the end)
     if (b < nblk) {
       const int j = BJ * b + own;
@@ -285,35 +301,25 @@ __device__ __forceinline__ void run_dequant(const Rows<kWin>& rows, const uint8_
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  {
-    int32_t first[ND - 1];
-#pragma unroll
-    for (int c = 0; c < ND - 1; ++c) first[c] = rows.raw(BJ * c + own);
-#pragma unroll
-    for (int c = 0; c < ND - 1; ++c) start(first[c], c);
-  }
-  int32_t next[2];  // of the next two blocks to start; the loop is unrolled so that none moves before its use
-#pragma unroll
-  for (int c = 0; c < 2; ++c) next[c] = rows.raw(BJ * (ND - 1 + c) + own);
-  for (int b0 = 0; ok && b0 < nblk; b0 += 2) {
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int b = b0 + c;
-      if (b >= nblk) break;
-      start(next[c], b + ND - 1);  // into the slot that block b - 1 was read from
-      next[c] = rows.raw(BJ * (b + ND + 1) + own);
-      asm volatile("cp.async.wait_group %0;" ::"n"(ND - 1) : "memory");
-      __syncwarp();
-      const Held held = read_rows<kS>(ring + (b % ND) * (8 * REC), lane);
-      if (kS && b == 0) ok = ready_or_wait(&bs.q_full, 1, 0, abort);
-      if (b >= NT) ok = ok && ready_or_wait(bs.tile_free, NT, b - NT, abort);
-      ok = __all_sync(0xffffffffu, ok);  // (and the slot has been read)
-      if (!ok) break;
-      write_rows<kS>(held, tiles + (b % NT) * TB + wq * 1024, lane);
-      fence_async_smem();  // the tile's generic writes before the tensor core reads it
-      __syncwarp();
-      if (lane == 0) bar_arrive(&bs.tile_full[b % NT]);
-    }
+  static_assert(ND == 3, "two blocks' copies are started here");
+  int32_t t0 = rows.raw(own), t1 = rows.raw(BJ + own), t2 = rows.raw(2 * BJ + own), t3 = rows.raw(3 * BJ + own);
+  start(t0, 0);
+  start(t1, 1);
+#pragma unroll 1
+  for (int b = 0; b < nblk; ++b) {
+    start(t2, b + ND - 1);  // into the slot that block b - 1 was read from
+    t2 = t3;
+    t3 = rows.raw(BJ * (b + ND + 1) + own);
+    asm volatile("cp.async.wait_group %0;" ::"n"(ND - 1) : "memory");
+    __syncwarp();
+    const Held held = read_rows<kS>(ring + (b % ND) * (8 * REC), lane);
+    bool ok = true;
+    if (kS && b == 0) ok = ready_or_wait(&bs.q_full, 1, 0, abort);
+    if (b >= NT) ok = ready_or_wait(bs.tile_free, NT, b - NT, abort);
+    if (!__all_sync(0xffffffffu, ok)) break;  // (and the slot has been read)
+    write_rows<kS>(held, tiles + (b % NT) * TB + wq * 1024, lane);
+    __syncwarp();  // (the issuer has the proxy fence: here it would wait for the copies in flight too)
+    if (lane == 0) bar_arrive(&bs.tile_full[b % NT]);
   }
   asm volatile("cp.async.wait_all;" ::: "memory");  // none is left in flight at the end
   if (kS && kWin && __any_sync(0xffffffffu, missing) && lane == 0) atomicOr(err, HS_FLAG_DEVROW);
@@ -437,7 +443,7 @@ __global__ void __launch_bounds__(T, 1)
         const uint8_t* src = qs + head * 128;
         const float inv = 1.f / a.latent_scale;
         const uint32_t sign = a.sm_scale < 0.f ? 0x80008000u : 0u;  // so that scores scale by a positive factor
-#pragma unroll 6
+#pragma unroll 2
         for (int c = 36 * wg; c < 36 * wg + 36; c += 2) {  // two 16-B chunks: 16 dims, 8 columns
           uint32_t x[8] = {};
           if (live) {
@@ -552,20 +558,24 @@ __global__ void __launch_bounds__(T, 1)
       sums[2 * wg * MH + head] = l_own;
       sums[(2 * wg + 1) * MH + head] = m_own;
     } else if (warp == S_ISSUER) {
+      // (tensor memory starts at 0: all of it is allocated here)
+      const bool one = elected();
+      const uint64_t k0 = mdesc(smem_u32(base + S_TILES), 16, 1024);
       bool go = __all_sync(0xffffffffu, nblk == 0 || pipe_wait(&bs.q_full, 1, 0, abort));
+#pragma unroll 1
       for (int b = 0; go && b < nblk; ++b) {
         bool ok = ready_or_wait(bs.tile_full, NT, b, abort);
         ok = ok && (b < 2 || ready_or_wait(bs.s_free, 2, b - 2, abort));
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_after();
-        if (lane == 0) {
-          const uint64_t dk0 = mdesc(smem_u32(tiles + (b % NT) * K_TILE), 16, 1024);
+        fence_async_smem();  // the tile's generic writes, seen through its barrier, before the tensor core's reads
+        const uint64_t dk0 = k0 + (uint64_t)((b % NT) * (K_TILE >> 4));
+        const uint32_t d = S_COL + BJ * (b & 1);
+        if (one) {
 #pragma unroll
-          for (int kk = 0; kk < KATOMS * 4; ++kk) {
-            const int at = kk >> 2, w = kk & 3;
-            mma_ta(tbase + S_COL + BJ * (b & 1), tbase + Q_COL + 8 * kk,
-                   dk0 + (uint64_t)((at * KV_ATOM + w * 32) >> 4), kk < DL / 16 ? kIdescQK : kIdescRope, kk > 0);
-          }
+          for (int kk = 0; kk < KATOMS * 4; ++kk)
+            mma_ta(d, Q_COL + 8 * kk, dk0 + (uint64_t)(((kk >> 2) * KV_ATOM + (kk & 3) * 32) >> 4),
+                   kk < DL / 16 ? kIdescQK : kIdescRope, kk > 0);
           commit(&bs.s_full[b & 1]);
           commit(&bs.tile_free[b % NT]);
           s_issued = b + 1;
@@ -591,6 +601,7 @@ __global__ void __launch_bounds__(T, 1)
         if (__any_sync(0xffffffffu, b > 0 && f != 1.f)) {
           if (!__all_sync(0xffffffffu, ready_or_wait(bs.tile_free, NT, b - 1, abort))) break;
           tc_after();
+#pragma unroll 1
           for (int c = 0; c < DL; c += 16) {
             float v[16];
             tmem_ld16(tbase + lane_off + c, v);
@@ -604,21 +615,23 @@ __global__ void __launch_bounds__(T, 1)
         if (lane == 0) bar_arrive(&bs.pv_go[b & 1]);
       }
     } else if (warp == O_ISSUER) {
+      const bool one = elected();
+      const uint64_t p0 = mdesc(smem_u32(base + O_P), 16, 1024), v0 = mdesc(smem_u32(base + O_TILES), KV_ATOM, 1024);
+#pragma unroll 1
       for (int b = 0; b < nblk; ++b) {
         bool ok = ready_or_wait(bs.tile_full, NT, b, abort);
         ok = ok && ready_or_wait(bs.pv_go, 2, b, abort);
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_after();
-        fence_async_smem();
-        if (lane == 0) {
-          const uint64_t dp0 = mdesc(smem_u32(base + O_P + (b & 1) * P_BUF), 16, 1024);
-          const uint64_t dv0 = mdesc(smem_u32(tiles + (b % NT) * V_TILE), KV_ATOM, 1024);
+        fence_async_smem();  // V's and P's writes, seen through their barriers, before the tensor core's reads
+        const uint64_t dp0 = p0 + (uint64_t)((b & 1) * (P_BUF >> 4)), dv0 = v0 + (uint64_t)((b % NT) * (V_TILE >> 4));
+        if (one) {
 #pragma unroll
           for (int kk = 0; kk < BJ / 16; ++kk)
 #pragma unroll
             for (int nh = 0; nh < 2; ++nh)
-              mma_ss(tbase + 256 * nh, dp0 + (uint64_t)((kk * 32) >> 4),
-                     dv0 + (uint64_t)((nh * 4 * KV_ATOM + kk * 2048) >> 4), kIdescPV, (b > 0 || kk > 0) ? 1u : 0u);
+              mma_ss(256 * nh, dp0 + (uint64_t)((kk * 32) >> 4), dv0 + (uint64_t)((nh * 4 * KV_ATOM + kk * 2048) >> 4),
+                     kIdescPV, (b > 0 || kk > 0) ? 1u : 0u);
           commit(&bs.tile_free[b % NT]);
           commit_multicast(&bs.p_free[b & 1], (uint16_t)(1u << partner));
           commit(&bs.mma_done);
@@ -667,6 +680,7 @@ __global__ void __launch_bounds__(T, 1)
     const bool direct = a.splits == 1;
     const size_t out0 = direct ? row0 : (size_t)p * ((size_t)(gridDim.x >> 1) / tiles_per_request) * a.num_queries * a.num_heads + row0;
     const int c0 = (warp >> 2) * (DL / 4);
+#pragma unroll 1
     for (int c = c0; c < c0 + DL / 4; c += 32) {
       float v[32];
       if (nblk > 0) {
