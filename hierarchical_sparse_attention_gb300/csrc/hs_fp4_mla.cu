@@ -52,32 +52,35 @@ using namespace tc;
 
 namespace {
 
-constexpr int T = 544;          // threads per CTA: 17 warps
+constexpr int T = 736;          // threads per CTA: 23 warps
 constexpr int MH = 128;         // MMA M: query heads of a tile (padded with zero rows)
 constexpr int BJ = 64;          // rows per block
 constexpr int DQK = kFp4Dims, DL = kFp4Latent;
 constexpr int KATOMS = DQK / 64, VATOMS = DL / 64;  // swizzle atoms of 64 values in a K and a V tile
 constexpr int NT = 2;           // tiles in flight
 constexpr int ND = 3;           // blocks of records in a dequantisation warp's ring: one read, two on their way
+constexpr int NS = 3;           // S buffers, and softmax warpgroups: one block each in turn
 constexpr uint32_t TMEM_COLS = 512, Q_COL = 0, S_COL = 288;
-// S-CTA warps: 0-7 softmax, 8 issuer, 9-16 dequantisation; O-CTA: 0-3 corrector, 4 issuer, 5-12
-// dequantisation (13-15 only read out at the end)
-constexpr int S_ISSUER = 8, S_DEQ0 = 9;
+static_assert(S_COL + NS * BJ <= TMEM_COLS, "Q and the S buffers fit tensor memory");
+// S-CTA warps: 0-11 softmax, 12 issuer, 13-22 dequantisation; O-CTA: 0-3 corrector, 4 issuer, 5-14
+// dequantisation (0-15 read out at the end). Dequantisation leaves out the warps w % 4 = 0: an issuer
+// whose MMAs wait for the tensor core holds up the shared-memory instructions of the warps on its
+// scheduler (they took up to 1.2 us longer over a block than the others).
+constexpr int S_ISSUER = 12, S_DEQ0 = 13;
 constexpr int O_ISSUER = 4, O_DEQ0 = 5;
-constexpr int NDEQ = 8;         // dequantisation warps of each CTA, eight rows of a block each
-static_assert(NDEQ * 8 == BJ, "the dequantisation warps cover a block");
-constexpr int MASKS = 16;       // blocks whose row masks are kept (the copies are at most 7 blocks ahead of the softmax)
+constexpr int NDEQ = 8, RW = BJ / NDEQ;  // dequantisation warps of each CTA, eight rows of a block each
+constexpr int MASKS = 16;       // blocks whose row masks are kept (the copies are at most 8 ahead of the softmax)
 
 constexpr uint32_t KV_ATOM = BJ * 128, K_TILE = KATOMS * KV_ATOM, V_TILE = VATOMS * KV_ATOM;
 constexpr uint32_t QBOX = MH * 128;
 constexpr int S_REC = kFp4Row, O_REC = kFp4RopeAt;  // bytes of a record that each CTA reads
-constexpr uint32_t S_RING = ND * 8 * S_REC, O_RING = ND * 8 * O_REC;  // a dequantisation warp's ring
+constexpr uint32_t S_RING = ND * RW * S_REC, O_RING = ND * RW * O_REC;  // a dequantisation warp's ring
 constexpr uint32_t S_TILES = 0, S_QSTAGE = 0;  // Q is staged over the K tiles before the first block
 constexpr uint32_t S_RAW = NT * K_TILE;
 static_assert(KATOMS * QBOX <= S_RAW, "Q's staging fits the K tiles");
 constexpr uint32_t S_REF = S_RAW + NDEQ * S_RING;  // the reference maxima, handed from block to block
-constexpr uint32_t S_SUMS = S_REF + MH * 4;     // each softmax warpgroup's sums and their references
-constexpr uint32_t S_MASK = S_SUMS + 4 * MH * 4;  // a byte per block and dequantisation warp: its rows that exist
+constexpr uint32_t S_SUMS = S_RAW;              // at the end: each softmax warpgroup's sums and their references
+constexpr uint32_t S_MASK = S_REF + MH * 4;     // a byte per block and dequantisation warp: its rows that exist
 constexpr uint32_t S_END = S_MASK + MASKS * NDEQ;
 constexpr uint32_t O_TILES = 0, O_RAW = NT * V_TILE;
 constexpr uint32_t O_P = (O_RAW + NDEQ * O_RING + 1023u) & ~1023u;
@@ -98,9 +101,10 @@ constexpr uint32_t kIdescPV = idesc(256, MH, true);
 struct Barriers {
   uint64_t tile_full[NT], tile_free[NT];  // dequantisation <-> issuer
   uint64_t q_raw, q_full;                 // S-CTA: Q staged; Q in tensor memory
-  uint64_t s_full[2], s_free[2];          // S-CTA: S written; S read
-  uint64_t m_set[2][4];                   // S-CTA: the block's reference maxima of a warp's heads are set
-  uint64_t p_free[2];                     // S-CTA, arrived by the O-CTA
+  // per softmax warpgroup, so that whoever waits on one waits on every phase of it (parities repeat):
+  uint64_t s_full[NS], s_free[NS];        // S-CTA: S written; S read
+  uint64_t m_set[NS][4];                  // S-CTA: the block's reference maxima of a warp's heads are set
+  uint64_t p_free[NS];                    // S-CTA, arrived by the O-CTA: P . V of the block is done
   uint64_t p_full[2];                     // O-CTA, completed by the S-CTA's stores
   uint64_t pv_go[2];                      // O-CTA: O is ready for P . V of the block
   uint64_t mma_done;                      // O-CTA: the MMAs issued so far are done
@@ -111,16 +115,7 @@ struct Barriers {
 // handing over: so their loops are short (not unrolled over blocks: at 165 KB of code the same loops
 // took up to twice as long as at 70 KB), and the wait that has to look at the clock is a call.
 template <bool cluster>
-__device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  return pipe_wait<cluster>(bar, 1, (int)parity, abort);
-}
-// pipe_wait for waits that are mostly over when they begin: the clock is read only once the first
-// try has failed (reading it first made every hand-over ~0.1 us longer). Use k of a ring of `depth`
-// barriers; a waiter has to have seen the ring's use k - depth over (parities repeat).
-template <bool cluster = false>
-__device__ __forceinline__ bool ready_or_wait(uint64_t* ring, int depth, int k, volatile int* abort) {
-  uint64_t* bar = ring + (k % depth);
-  const uint32_t parity = (uint32_t)(k / depth) & 1u;
+__device__ __forceinline__ bool try_once(uint64_t* bar, uint32_t parity) {
   uint32_t done;
   if (cluster)
     asm volatile(
@@ -135,7 +130,32 @@ __device__ __forceinline__ bool ready_or_wait(uint64_t* ring, int depth, int k, 
         : "=r"(done)
         : "r"(smem_u32(bar)), "r"(parity), "n"(kSuspendNs)
         : "memory");
-  return done || wait_on<cluster>(bar, parity, abort);
+  return done != 0;
+}
+// Waits on, with pipe_wait's bound; looks at the clock and at the abort flag every few tries only (a
+// try ends after well under a microsecond whatever it is asked, and the waiting warps' looks were a
+// quarter of all instructions).
+template <bool cluster>
+__device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  const uint64_t t0 = gtime();
+  for (;;) {
+#pragma unroll 1
+    for (int i = 0; i < 16; ++i)
+      if (try_once<cluster>(bar, parity)) return true;
+    if (*abort || gtime() - t0 > kWaitNs) {
+      *abort = 1;
+      return false;
+    }
+  }
+}
+// pipe_wait for waits that are mostly over when they begin: the clock is read only once the first
+// try has failed (reading it first made every hand-over ~0.1 us longer). Use k of a ring of `depth`
+// barriers; a waiter has to have seen the ring's use k - depth over (parities repeat).
+template <bool cluster = false>
+__device__ __forceinline__ bool ready_or_wait(uint64_t* ring, int depth, int k, volatile int* abort) {
+  uint64_t* bar = ring + (k % depth);
+  const uint32_t parity = (uint32_t)(k / depth) & 1u;
+  return try_once<cluster>(bar, parity) || wait_on<cluster>(bar, parity, abort);
 }
 // One lane of the (converged) warp. The MMAs are issued by it from code that the whole warp runs, so
 // that their operands stay in uniform registers: 33 clocks an MMA of N = 64 with A in tensor memory,
@@ -151,10 +171,10 @@ __device__ __forceinline__ float ex2(float x) {  // 2^x: -inf gives 0, NaN stays
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// 64 accumulator columns of this thread's row.
-__device__ __forceinline__ void tmem_ld64(uint32_t taddr, float (&v)[64]) {
+// 32 accumulator columns of this thread's row.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
 #pragma unroll
-  for (int h = 0; h < 64; h += 16) {
+  for (int h = 0; h < 32; h += 16) {
     uint32_t* r = reinterpret_cast<uint32_t*>(v + h);
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
@@ -163,6 +183,23 @@ __device__ __forceinline__ void tmem_ld64(uint32_t taddr, float (&v)[64]) {
         : "r"(taddr + h));
   }
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+// Two 32-bit floats at a time.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tadd.rn.f32x2 x, x, y;\n\t"
+      "mov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
 }
 
 // The rows of a tile's split, j = 0 .. n - 1, and who sees them.
@@ -259,15 +296,16 @@ __device__ __forceinline__ void write_rows(const Held& h, uint8_t* group, int la
     const int g = s >> 1, it = (lane & 1) + 2 * (lane >> 3) + 8 * (s & 1);
     uint8_t* at = group + (it >> 1) * KV_ATOM + (4 * g + in4) * 128 + ((lane & 1) ^ g) * 64;
     const uint32_t w[4] = {h.codes[s].x, h.codes[s].y, h.codes[s].z, h.codes[s].w};
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {  // a scale's 16 dims
-      uint32_t code = ((uint32_t)h.scales[s] >> (8 * b)) & 0xFFu;
-      if (!kS && (code & 0x7Fu) == 0x7Fu) code = 0;  // V: no NaN (see above); K keeps it
-      const __half2 sc = __half2half2(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)code, __NV_E4M3)));
-#pragma unroll
-      for (int u = 2 * b; u < 2 * b + 2; ++u)
-        *reinterpret_cast<uint4*>(at + ((u ^ in4) << 4)) = times(codes_to_f16(w[u]), sc);
+    uint32_t two = h.scales[s];  // the scales of 16 dims each
+    if (!kS) {  // V: no NaN (see above); K keeps it
+      if ((two & 0x7Fu) == 0x7Fu) two &= 0xFF00u;
+      if ((two & 0x7F00u) == 0x7F00u) two &= 0xFFu;
     }
+    const __half2_raw raw = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
+    const __half2 pair = raw, sc[2] = {__low2half2(pair), __high2half2(pair)};
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      *reinterpret_cast<uint4*>(at + ((u ^ in4) << 4)) = times(codes_to_f16(w[u]), sc[u >> 1]);
   }
   if (kS)
 #pragma unroll
@@ -286,7 +324,7 @@ __device__ __forceinline__ void run_dequant(const Rows<kWin>& rows, const uint8_
                                             int lane, uint32_t* err, volatile int* abort) {
   constexpr int REC = kS ? S_REC : O_REC;
   constexpr uint32_t TB = kS ? K_TILE : V_TILE;
-  const int own = 8 * wq + (lane & 7);
+  const int own = RW * wq + (lane & 7);
   bool missing = false;
   auto start = [&](int32_t raw, int b) {  // the copies of block b (one group of copies, empty past the end)
     if (b < nblk) {
@@ -297,7 +335,7 @@ __device__ __forceinline__ void run_dequant(const Rows<kWin>& rows, const uint8_
         const uint32_t mask = __ballot_sync(0xffffffffu, y >= 0);
         if (lane == 0) masks[(b % MASKS) * NDEQ + wq] = (uint8_t)mask;
       }
-      copy_rows<REC>(smem_u32(ring + (b % ND) * (8 * REC)), y, pool, lane);
+      copy_rows<REC>(smem_u32(ring + (b % ND) * (RW * REC)), y, pool, lane);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
@@ -312,7 +350,7 @@ __device__ __forceinline__ void run_dequant(const Rows<kWin>& rows, const uint8_
     t3 = rows.raw(BJ * (b + ND + 1) + own);
     asm volatile("cp.async.wait_group %0;" ::"n"(ND - 1) : "memory");
     __syncwarp();
-    const Held held = read_rows<kS>(ring + (b % ND) * (8 * REC), lane);
+    const Held held = read_rows<kS>(ring + (b % ND) * (RW * REC), lane);
     bool ok = true;
     if (kS && b == 0) ok = ready_or_wait(&bs.q_full, 1, 0, abort);
     if (b >= NT) ok = ready_or_wait(bs.tile_free, NT, b - NT, abort);
@@ -323,6 +361,13 @@ __device__ __forceinline__ void run_dequant(const Rows<kWin>& rows, const uint8_
   }
   asm volatile("cp.async.wait_all;" ::: "memory");  // none is left in flight at the end
   if (kS && kWin && __any_sync(0xffffffffu, missing) && lane == 0) atomicOr(err, HS_FLAG_DEVROW);
+}
+
+// The dequantisation warp that CTA warp w is, of those that begin with warp `first` (first % 4 = 1);
+// -1 if none.
+__device__ __forceinline__ int deq_warp(int w, int first) {
+  const int i = w - first, q = 3 * (i >> 2) + (i & 3);
+  return i >= 0 && (i & 3) != 3 && q < NDEQ ? q : -1;
 }
 
 // Bits lo .. hi - 1 of a 32-bit mask.
@@ -388,11 +433,13 @@ __global__ void __launch_bounds__(T, 1)
     bar_init(&bs.q_raw, 1);
     bar_init(&bs.q_full, 8);  // one arrival per softmax warp
     bar_init(&bs.mma_done, 1);
-    for (int k = 0; k < 2; ++k) {
+    for (int k = 0; k < NS; ++k) {
       bar_init(&bs.s_full[k], 1);
       bar_init(&bs.s_free[k], 4);  // the warps of the block's softmax warpgroup
       for (int w = 0; w < 4; ++w) bar_init(&bs.m_set[k][w], 1);
       bar_init(&bs.p_free[k], 1);
+    }
+    for (int k = 0; k < 2; ++k) {
       bar_init(&bs.p_full[k], 1);  // the O-CTA's expect_tx; the S-CTA's stores complete it
       bar_init(&bs.pv_go[k], 4);
     }
@@ -429,12 +476,14 @@ __global__ void __launch_bounds__(T, 1)
   const int head = (warp & 3) * 32 + lane;  // this thread's row of the tile = its tensor-memory lane
   uint8_t* masks = base + S_MASK;
 
+  float m_own = -INFINITY, l_own = 0.f;  // softmax: the sum of this thread's blocks, under this reference
+
   if (rank == 0) {
     // ================================ S-CTA ================================
     uint8_t* tiles = base + S_TILES;
-    if (warp < 8) {
+    if (warp < 4 * NS) {
       const int wg = warp >> 2;
-      if (nblk > 0) {
+      if (nblk > 0 && warp < 8) {
         // Q into tensor memory (warpgroup wg the columns [144 wg, 144 wg + 144)), column c holding
         // dims 2c, 2c + 1: the latent part as f16, the RoPE part as bf16 over latent_scale
         const uint8_t* qs = base + S_QSTAGE;
@@ -481,82 +530,100 @@ __global__ void __launch_bounds__(T, 1)
         see_lo = (int)(rows.kept + max((int64_t)0, at + 1 - a.window - rows.start)) - rows.j0;
         see_hi = (int)(rows.kept + max((int64_t)0, at + 1 - rows.start)) - rows.j0;
       }
-      // Warpgroup wg takes the blocks b with b % 2 = wg, a query head per thread. From one block
-      // to the next only the reference maximum goes over, from warp to warp (the two warps of the
-      // same heads): it is known once a block's scores are read, so the warpgroups' exponentials
-      // overlap. Each keeps the sum of its own blocks under the reference of its last one.
+      // Warpgroup wg takes the blocks b with b % NS = wg, a query head per thread. From one block to
+      // the next only the reference maximum goes over, from warp to warp (the warps of the same
+      // heads): it is known once a block's scores have been read, so the warpgroups' exponentials
+      // overlap. Each keeps the sum of its own blocks under the reference of its last one. The scores
+      // are read twice, for the maximum and for the weights (64 of them do not fit a thread's 64
+      // registers).
       float* s_ref = reinterpret_cast<float*>(base + S_REF);
       const uint32_t r_pbuf = remote(base + O_P, partner), r_alpha = remote(base + O_ALPHA, partner);
+      const uint32_t rbar0 = remote(&bs.p_full[0], partner), rbar1 = remote(&bs.p_full[1], partner);
       // scores in log2 units; a scale of zero stays above it, so that -inf stays -inf
       const float sl2 = fmaxf(fabsf(a.sm_scale * a.latent_scale * 1.4426950408889634f), 1e-37f);
-      float m_own = -INFINITY, l_own = 0.f;
-      for (int b = wg; b < nblk; b += 2) {
-        if (!__all_sync(0xffffffffu, ready_or_wait(bs.s_full, 2, b, abort))) break;
+      const uint32_t s_at = tbase + lane_off + S_COL + BJ * wg;
+      uint32_t turn = 0;  // of this warpgroup: its barriers' phase
+#pragma unroll 1
+      for (int b = wg; b < nblk; b += NS, turn ^= 1u) {
+        if (!__all_sync(0xffffffffu, ready_or_wait(&bs.s_full[wg], 1, (int)turn, abort))) break;
         tc_after();
-        float t[BJ];
-        tmem_ld64(tbase + lane_off + S_COL + BJ * wg, t);
-        tc_before();
-        __syncwarp();
-        if (lane == 0) bar_arrive(&bs.s_free[wg]);  // S is in registers
-        uint32_t vm[2];
-        bool all = true;
+        // the rows that exist, and that this query sees
+        const volatile uint32_t* at = reinterpret_cast<const volatile uint32_t*>(masks + (b % MASKS) * NDEQ);
+        uint32_t sees0 = at[0], sees1 = at[1];
+        if (kWin) {
+          const int j = BJ * b;
+          sees0 &= bit_range(0, see_kept - j) | bit_range(see_lo - j, see_hi - j);
+          sees1 &= bit_range(0, see_kept - j - 32) | bit_range(see_lo - j - 32, see_hi - j - 32);
+        }
+        const bool every = __all_sync(0xffffffffu, (sees0 & sees1) == 0xFFFFFFFFu);
+        const auto scores = [&](int c, float (&t)[32]) {  // 32 c .. 32 c + 31 of the block, -inf where it does not look
+          tmem_ld32(s_at + 32 * c, t);
+          if (!every) {
+            const uint32_t sees = c ? sees1 : sees0;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          vm[h] = *(volatile const uint32_t*)(masks + (b % MASKS) * NDEQ + 4 * h);
-          if (kWin) {
-            const int j = BJ * b + 32 * h;
-            vm[h] &= bit_range(0, see_kept - j) | bit_range(see_lo - j, see_hi - j);
+            for (int i = 0; i < 32; ++i) t[i] = ((sees >> i) & 1u) ? t[i] : -INFINITY;
           }
-          all = all && vm[h] == 0xFFFFFFFFu;
-        }
-        if (!__all_sync(0xffffffffu, all)) {
+        };
+        float bm = -INFINITY;
+#pragma unroll 1
+        for (int c = 0; c < BJ / 32; ++c) {
+          float t[32];
+          scores(c, t);
+          float x0 = t[0], x1 = t[1];
 #pragma unroll
-          for (int i = 0; i < BJ; ++i) t[i] = ((vm[i / 32] >> (i % 32)) & 1u) ? t[i] : -INFINITY;
+          for (int i = 2; i < 32; i += 2) {
+            x0 = fmaxf(x0, t[i]);
+            x1 = fmaxf(x1, t[i + 1]);
+          }
+          bm = fmaxf(bm, fmaxf(x0, x1));
         }
-        float bm = t[0];
-#pragma unroll
-        for (int i = 1; i < BJ; ++i) bm = fmaxf(bm, t[i]);
         bm *= sl2;
         float m_run = -INFINITY;
         if (b > 0) {
-          if (!__all_sync(0xffffffffu, ready_or_wait(&bs.m_set[(b - 1) & 1][warp & 3], 1, (b - 1) >> 1, abort))) break;
+          // (the block before is the last warpgroup's block of this turn, or of the turn before)
+          const int before = wg == 0 ? NS - 1 : wg - 1;
+          if (!__all_sync(0xffffffffu, ready_or_wait(&bs.m_set[before][warp & 3], 1, (int)(wg == 0 ? turn ^ 1u : turn), abort)))
+            break;
           m_run = s_ref[head];
         }
         // Lazy rescale: a head keeps its reference until a block's maximum passes it by 2^8, so P
-        // stays below 2^8 and O is rescaled only on those rare jumps. (bm is NaN if every score is:
-        // the reference then stays.)
+        // stays below 2^8 and O is rescaled only on those rare jumps. (NaN scores leave it alone.)
         const float m_new = bm > m_run + kRescaleLog2 || m_run == -INFINITY ? fmaxf(m_run, bm) : m_run;
         s_ref[head] = m_new;
         __syncwarp();
-        if (lane == 0) bar_arrive(&bs.m_set[b & 1][warp & 3]);
+        if (lane == 0) bar_arrive(&bs.m_set[wg][warp & 3]);
         const float alpha = m_new == -INFINITY ? 1.f : ex2(m_run - m_new);  // m_run = -inf: O is still 0
         const float ref = m_new == -INFINITY ? 0.f : m_new;  // a NaN score stays one, an unseen row's weight is 0
         l_own *= m_new == -INFINITY ? 1.f : ex2(m_own - m_new);
         m_own = m_new;
-        // the O-CTA's P buffer wg is free once its P . V of block b - 2 is done
-        if (!__all_sync(0xffffffffu, b < 2 || ready_or_wait<true>(bs.p_free, 2, b - 2, abort))) break;
-        const uint32_t pbuf = r_pbuf + wg * P_BUF;
-        const uint32_t rbar = remote(&bs.p_full[wg], partner);
-        st_async_f32(r_alpha + 4 * (wg * MH + head), alpha, rbar);
-        float sum0 = 0.f, sum1 = 0.f;
+        // the O-CTA's P buffer is free once P . V of block b - 2 is done
+        if (!__all_sync(0xffffffffu, b < 2 || ready_or_wait<true>(bs.p_free, NS, b - 2, abort))) break;
+        const uint32_t pbuf = r_pbuf + (b & 1) * P_BUF, rbar = b & 1 ? rbar1 : rbar0;
+        st_async_f32(r_alpha + 4 * ((b & 1) * MH + head), alpha, rbar);
+        float2 sum = make_float2(0.f, 0.f);
+#pragma unroll 1
+        for (int c = 0; c < BJ / 32; ++c) {
+          float t[32];
+          scores(c, t);
 #pragma unroll
-        for (int c = 0; c < BJ / 8; ++c) {  // eight 16-B chunks of 8 f16
-          uint32_t w[4];
+          for (int q = 0; q < 4; ++q) {  // four 16-B chunks of 8 f16
+            uint32_t w[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float p0 = ex2(fmaf(t[8 * c + 2 * i], sl2, -ref)), p1 = ex2(fmaf(t[8 * c + 2 * i + 1], sl2, -ref));
-            const __half2 pb = __floats2half2_rn(p0, p1);
-            sum0 += p0;
-            sum1 += p1;
-            w[i] = *reinterpret_cast<const uint32_t*>(&pb);
+            for (int i = 0; i < 4; ++i) {
+              float2 e = fma2(make_float2(t[8 * q + 2 * i], t[8 * q + 2 * i + 1]), make_float2(sl2, sl2), make_float2(-ref, -ref));
+              e = make_float2(ex2(e.x), ex2(e.y));
+              const __half2 pb = __floats2half2_rn(e.x, e.y);
+              sum = add2(sum, e);
+              w[i] = *reinterpret_cast<const uint32_t*>(&pb);
+            }
+            st_async16(pbuf + sw128(head, 32 * c + 8 * q), make_uint4(w[0], w[1], w[2], w[3]), rbar);
           }
-          st_async16(pbuf + sw128(head, 8 * c), make_uint4(w[0], w[1], w[2], w[3]), rbar);
         }
-        l_own += sum0 + sum1;
+        tc_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(&bs.s_free[wg]);  // S has been read
+        l_own += sum.x + sum.y;
       }
-      float* sums = reinterpret_cast<float*>(base + S_SUMS);
-      sums[2 * wg * MH + head] = l_own;
-      sums[(2 * wg + 1) * MH + head] = m_own;
     } else if (warp == S_ISSUER) {
       // (tensor memory starts at 0: all of it is allocated here)
       const bool one = elected();
@@ -565,26 +632,25 @@ __global__ void __launch_bounds__(T, 1)
 #pragma unroll 1
       for (int b = 0; go && b < nblk; ++b) {
         bool ok = ready_or_wait(bs.tile_full, NT, b, abort);
-        ok = ok && (b < 2 || ready_or_wait(bs.s_free, 2, b - 2, abort));
+        ok = ok && (b < NS || ready_or_wait(bs.s_free, NS, b - NS, abort));
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_after();
         fence_async_smem();  // the tile's generic writes, seen through its barrier, before the tensor core's reads
         const uint64_t dk0 = k0 + (uint64_t)((b % NT) * (K_TILE >> 4));
-        const uint32_t d = S_COL + BJ * (b & 1);
+        const uint32_t d = S_COL + BJ * (b % NS);
         if (one) {
 #pragma unroll
           for (int kk = 0; kk < KATOMS * 4; ++kk)
             mma_ta(d, Q_COL + 8 * kk, dk0 + (uint64_t)(((kk >> 2) * KV_ATOM + (kk & 3) * 32) >> 4),
                    kk < DL / 16 ? kIdescQK : kIdescRope, kk > 0);
-          commit(&bs.s_full[b & 1]);
+          commit(&bs.s_full[b % NS]);
           commit(&bs.tile_free[b % NT]);
           s_issued = b + 1;
         }
         __syncwarp();
       }
-    } else {
-      run_dequant<true, kWin>(rows, a.pool, nblk, base + S_RAW + (warp - S_DEQ0) * S_RING, masks, tiles, bs, warp - S_DEQ0,
-                              lane, err, abort);
+    } else if (const int wq = deq_warp(warp, S_DEQ0); wq >= 0) {
+      run_dequant<true, kWin>(rows, a.pool, nblk, base + S_RAW + wq * S_RING, masks, tiles, bs, wq, lane, err, abort);
     }
   } else {
     // ================================ O-CTA ================================
@@ -633,27 +699,37 @@ __global__ void __launch_bounds__(T, 1)
               mma_ss(256 * nh, dp0 + (uint64_t)((kk * 32) >> 4), dv0 + (uint64_t)((nh * 4 * KV_ATOM + kk * 2048) >> 4),
                      kIdescPV, (b > 0 || kk > 0) ? 1u : 0u);
           commit(&bs.tile_free[b % NT]);
-          commit_multicast(&bs.p_free[b & 1], (uint16_t)(1u << partner));
+          commit_multicast(&bs.p_free[b % NS], (uint16_t)(1u << partner));
           commit(&bs.mma_done);
           s_issued = b + 1;
         }
         __syncwarp();
       }
-    } else if (warp < O_DEQ0 + NDEQ) {
-      run_dequant<false, kWin>(rows, a.pool, nblk, base + O_RAW + (warp - O_DEQ0) * O_RING, masks, tiles, bs, warp - O_DEQ0,
-                               lane, err, abort);
+    } else if (const int wq = deq_warp(warp, O_DEQ0); wq >= 0) {
+      run_dequant<false, kWin>(rows, a.pool, nblk, base + O_RAW + wq * O_RING, masks, tiles, bs, wq, lane, err, abort);
     }
   }
 
   __syncthreads();
+  if (rank == 0) {
+    float* sums = reinterpret_cast<float*>(base + S_SUMS);
+    if (warp < 4 * NS) {
+      sums[2 * (warp >> 2) * MH + head] = l_own;
+      sums[(2 * (warp >> 2) + 1) * MH + head] = m_own;
+    }
+    __syncthreads();
+  }
   if (rank == 0 && warp < 4) {
-    // the sums of both warpgroups under the last block's reference, and that, to the O-CTA
+    // the warpgroups' sums under the last block's reference, and that, to the O-CTA
     const float* sums = reinterpret_cast<const float*>(base + S_SUMS);
-    const float l0 = sums[head], m0 = sums[MH + head], l1 = sums[2 * MH + head], m1 = sums[3 * MH + head];
     const float m = nblk > 0 ? reinterpret_cast<const float*>(base + S_REF)[head] : -INFINITY;
-    const auto part = [&](float l, float mo) { return m == -INFINITY ? l : l * ex2(mo - m); };
+    float l = 0.f;
+    for (int g = 0; g < NS; ++g) {
+      const float x = sums[2 * g * MH + head], mo = sums[(2 * g + 1) * MH + head];
+      l += m == -INFINITY ? x : x * ex2(mo - m);
+    }
     const uint32_t fin = remote(base + O_FIN, partner);
-    st_remote_f32(fin + 4 * head, part(l0, m0) + part(l1, m1));
+    st_remote_f32(fin + 4 * head, l);
     st_remote_f32(fin + 4 * (MH + head), m);
     __syncwarp();
     if (lane == 0) bar_arrive_remote(remote(&bs.fin, partner));
@@ -664,7 +740,7 @@ __global__ void __launch_bounds__(T, 1)
   if (rank == 1) {
     ok = ok && pipe_wait<true>(&bs.fin, 1, 0, abort);
   } else {
-    for (int b = nblk >= 2 ? nblk - 2 : 0; b < nblk; ++b) ok = ok && pipe_wait<true>(bs.p_free, 2, b, abort);
+    for (int b = nblk >= 2 ? nblk - 2 : 0; b < nblk; ++b) ok = ok && pipe_wait<true>(bs.p_free, NS, b, abort);
   }
   ok = __syncthreads_and(ok && !*abort);
   tc_after();
@@ -724,7 +800,7 @@ __global__ void __launch_bounds__(T, 1)
     const int n = s_issued;
     if (n > 0) {
       if (rank == 0)
-        pipe_wait(bs.s_full, 2, n - 1, abort);
+        pipe_wait(bs.s_full, NS, n - 1, abort);
       else
         pipe_wait(&bs.mma_done, 1, n - 1, abort);
     }
