@@ -79,20 +79,20 @@ constexpr uint32_t S_TILES = 0, S_QSTAGE = 0;  // Q is staged over the K tiles b
 constexpr uint32_t S_RAW = NT * K_TILE;
 static_assert(KATOMS * QBOX <= S_RAW, "Q's staging fits the K tiles");
 constexpr uint32_t S_REF = S_RAW + NDEQ * S_RING;  // the reference maxima, handed from block to block
-constexpr uint32_t S_SUMS = S_RAW;              // at the end: each softmax warpgroup's sums and their references
-constexpr uint32_t S_MASK = S_REF + MH * 4;     // a byte per block and dequantisation warp: its rows that exist
+constexpr uint32_t S_SUMS = S_REF + MH * 4;     // the sums of the softmax warpgroups after the first, and their references
+constexpr uint32_t S_MASK = S_SUMS + 2 * (NS - 1) * MH * 4;  // a byte per block and dequantisation warp: its rows that exist
 constexpr uint32_t S_END = S_MASK + MASKS * NDEQ;
 constexpr uint32_t O_TILES = 0, O_RAW = NT * V_TILE;
 constexpr uint32_t O_P = (O_RAW + NDEQ * O_RING + 1023u) & ~1023u;
 constexpr uint32_t P_BUF = MH * BJ * 2, P_BYTES = P_BUF + MH * 4;  // P and the rescale factors of a block
 constexpr uint32_t O_ALPHA = O_P + 2 * P_BUF;
 constexpr uint32_t O_FIN = O_ALPHA + 2 * MH * 4;
-constexpr uint32_t O_END = O_FIN + 2 * MH * 4;
+constexpr uint32_t O_END = O_FIN + 2 * 2 * MH * 4;  // two tiles' totals
 constexpr uint32_t SMEM_BYTES = (S_END > O_END ? S_END : O_END) + 1024;  // + alignment slack
 static_assert(SMEM_BYTES <= 227 * 1024 - 1024, "shared memory of a CTA");
 constexpr float kRescaleLog2 = 8.f;  // a reference maximum stays until it is passed by 2^8: P < 2^8
-constexpr int EPI_PITCH = 36;        // floats per staged row of the read-out
-static_assert(16 * 32 * EPI_PITCH * 4 <= NT * V_TILE, "the read-out staging fits the V tiles");
+constexpr int EPI_PITCH = 1024 + 16;  // bytes of a staged output row: 512 bf16 or 256 partial sums
+static_assert(MH * EPI_PITCH <= O_P, "the read-out's staging fits the V tiles and the records after them");
 
 constexpr uint32_t kIdescQK = idesc(BJ, MH, false);                              // f16 latents
 constexpr uint32_t kIdescRope = kIdescQK | (1u << 7) | (1u << 10);               // bf16 RoPE
@@ -100,7 +100,7 @@ constexpr uint32_t kIdescPV = idesc(256, MH, true);
 
 struct Barriers {
   uint64_t tile_full[NT], tile_free[NT];  // dequantisation <-> issuer
-  uint64_t q_raw, q_full;                 // S-CTA: Q staged; Q in tensor memory
+  uint64_t q_raw[NS], q_full;             // S-CTA: a third of Q staged; Q in tensor memory
   // per softmax warpgroup, so that whoever waits on one waits on every phase of it (parities repeat):
   uint64_t s_full[NS], s_free[NS];        // S-CTA: S written; S read
   uint64_t m_set[NS][4];                  // S-CTA: the block's reference maxima of a warp's heads are set
@@ -108,7 +108,7 @@ struct Barriers {
   uint64_t p_full[2];                     // O-CTA, completed by the S-CTA's stores
   uint64_t pv_go[2];                      // O-CTA: O is ready for P . V of the block
   uint64_t mma_done;                      // O-CTA: the MMAs issued so far are done
-  uint64_t fin;                           // O-CTA: the S-CTA's totals are here
+  uint64_t fin[2];                        // O-CTA: the S-CTA's totals of a tile are here
 };
 
 // The kernel's roles run side by side from one instruction cache, and much of their time goes into
@@ -315,13 +315,14 @@ __device__ __forceinline__ void write_rows(const Held& h, uint8_t* group, int la
     }
 }
 
-// A dequantisation warp's loop: block b is written while the rows of the next ND - 1 blocks are on
-// their way, and two more blocks' row numbers. In the S-CTA it waits, before its first tile write,
-// until Q has left the staging area, and tells the softmax which of its rows exist.
+// A dequantisation warp's loop over a unit's blocks: block b is written while the rows of the next
+// ND - 1 blocks are on their way, and two more blocks' row numbers. `done`: blocks of the units before
+// (places in rings go on from unit to unit). In the S-CTA it waits, before its first tile write, until Q
+// has left the staging area, and tells the softmax which of its rows exist.
 template <bool kS, bool kWin>
-__device__ __forceinline__ void run_dequant(const Rows<kWin>& rows, const uint8_t* __restrict__ pool, int nblk,
-                                            uint8_t* ring, uint8_t* masks, uint8_t* tiles, Barriers& bs, int wq,
-                                            int lane, uint32_t* err, volatile int* abort) {
+__device__ __forceinline__ void run_dequant(const Rows<kWin>& rows, const uint8_t* __restrict__ pool, int nblk, int done,
+                                            uint32_t q_phase, uint8_t* ring, uint8_t* masks, uint8_t* tiles,
+                                            Barriers& bs, int wq, int lane, uint32_t* err, volatile int* abort) {
   constexpr int REC = kS ? S_REC : O_REC;
   constexpr uint32_t TB = kS ? K_TILE : V_TILE;
   const int own = RW * wq + (lane & 7);
@@ -333,9 +334,9 @@ __device__ __forceinline__ void run_dequant(const Rows<kWin>& rows, const uint8_
       if (kS) {
         if (kWin) missing |= j < rows.n && y < 0;
         const uint32_t mask = __ballot_sync(0xffffffffu, y >= 0);
-        if (lane == 0) masks[(b % MASKS) * NDEQ + wq] = (uint8_t)mask;
+        if (lane == 0) masks[((done + b) % MASKS) * NDEQ + wq] = (uint8_t)mask;
       }
-      copy_rows<REC>(smem_u32(ring + (b % ND) * (RW * REC)), y, pool, lane);
+      copy_rows<REC>(smem_u32(ring + ((done + b) % ND) * (RW * REC)), y, pool, lane);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
@@ -345,21 +346,23 @@ __device__ __forceinline__ void run_dequant(const Rows<kWin>& rows, const uint8_
   start(t1, 1);
 #pragma unroll 1
   for (int b = 0; b < nblk; ++b) {
+    const int g = done + b;
     start(t2, b + ND - 1);  // into the slot that block b - 1 was read from
     t2 = t3;
     t3 = rows.raw(BJ * (b + ND + 1) + own);
     asm volatile("cp.async.wait_group %0;" ::"n"(ND - 1) : "memory");
     __syncwarp();
-    const Held held = read_rows<kS>(ring + (b % ND) * (RW * REC), lane);
+    const Held held = read_rows<kS>(ring + (g % ND) * (RW * REC), lane);
     bool ok = true;
-    if (kS && b == 0) ok = ready_or_wait(&bs.q_full, 1, 0, abort);
-    if (b >= NT) ok = ready_or_wait(bs.tile_free, NT, b - NT, abort);
+    if (kS && b == 0) ok = ready_or_wait(&bs.q_full, 1, (int)q_phase, abort);
+    if (g >= NT) ok = ok && ready_or_wait(bs.tile_free, NT, g - NT, abort);
     if (!__all_sync(0xffffffffu, ok)) break;  // (and the slot has been read)
-    write_rows<kS>(held, tiles + (b % NT) * TB + wq * 1024, lane);
+    write_rows<kS>(held, tiles + (g % NT) * TB + wq * 1024, lane);
     __syncwarp();  // (the issuer has the proxy fence: here it would wait for the copies in flight too)
-    if (lane == 0) bar_arrive(&bs.tile_full[b % NT]);
+    if (lane == 0) bar_arrive(&bs.tile_full[g % NT]);
   }
   asm volatile("cp.async.wait_all;" ::: "memory");  // none is left in flight at the end
+  __syncwarp();
   if (kS && kWin && __any_sync(0xffffffffu, missing) && lane == 0) atomicOr(err, HS_FLAG_DEVROW);
 }
 
@@ -378,9 +381,71 @@ __device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
   return (0xFFFFFFFFu >> (32 - (hi - lo))) << lo;
 }
 
+// A unit of work: a tile's split. Every thread of a pair computes it from its number.
+template <bool kWin>
+struct Unit {
+  Rows<kWin> rows;
+  int nblk;          // blocks of this split
+  int live;          // query heads of the tile
+  size_t row0;       // the first one's row of q, o and lse
+  int p;             // the split
+  int first_query;
+  int64_t seq_len;   // window
+};
+template <bool kWin>
+__device__ __forceinline__ Unit<kWin> unit_of(const Fp4MlaArgs& a, int u, int tiles_per_request, int queries_per_tile,
+                                              bool flag, uint32_t* err) {
+  Unit<kWin> x;
+  const int tile = u / a.splits, r = tile / tiles_per_request;
+  x.p = u - tile * a.splits;
+  x.first_query = (tile - r * tiles_per_request) * queries_per_tile;
+  const int nq = min(queries_per_tile, a.num_queries - x.first_query);
+  x.live = nq * a.num_heads;
+  x.row0 = ((size_t)r * a.num_queries + x.first_query) * a.num_heads;
+  // the tile's rows: every row that some query of the tile sees
+  x.rows.pool_rows = a.pool_rows;
+  int total;
+  if (kWin) {
+    x.rows.table = a.pages + (size_t)r * a.max_pages;
+    x.rows.page_size = a.page_size;
+    x.seq_len = a.seq_lens[r];
+    const bool bad = x.seq_len < 0 || x.seq_len > (int64_t)a.max_pages * a.page_size;
+    if (bad && flag) atomicOr(err, HS_FLAG_SEQLEN);
+    // tokens up to the tile's last query, from the first one of its first query
+    const int64_t at = x.seq_len - a.num_queries + x.first_query;
+    const int64_t end = bad ? 0 : max((int64_t)0, at + nq), first = max((int64_t)0, at);
+    x.rows.kept = (int)min((int64_t)a.sinks, end);
+    x.rows.start = (int)max((int64_t)x.rows.kept, first + 1 - a.window);
+    total = x.rows.kept + (int)max((int64_t)0, end - x.rows.start);
+  } else {
+    x.rows.table = a.out_rows + (size_t)r * a.top_k;
+    total = a.top_k;
+  }
+  const int all = (int)(((int64_t)total + BJ - 1) / BJ), per = (all + a.splits - 1) / a.splits;
+  x.nblk = max(0, min(per, all - x.p * per));
+  x.rows.j0 = x.p * per * BJ;
+  x.rows.n = x.nblk > 0 ? min(total - x.rows.j0, x.nblk * BJ) : 0;
+  return x;
+}
+
+// Q's 128 rows from row0 as nine tensor boxes of 64 dims, three to a barrier (rows past the tile's are
+// not used).
+__device__ __forceinline__ void request_q(const CUtensorMap* tm_q, size_t row0, uint8_t* base, Barriers& bs) {
+  fence_async_smem();  // earlier generic accesses of the staging area and the barriers, before the copies
+  for (int g = 0; g < NS; ++g) {
+    bar_arrive_tx(&bs.q_raw[g], KATOMS / NS * QBOX);
+    for (int bx = KATOMS / NS * g; bx < KATOMS / NS * (g + 1); ++bx)
+      asm volatile(
+          "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+              smem_u32(base + S_QSTAGE + bx * QBOX)),
+          "l"(tm_q), "r"(64 * bx), "r"((int)row0), "r"(smem_u32(&bs.q_raw[g]))
+          : "memory");
+  }
+}
+
 template <bool kWin>
 __global__ void __launch_bounds__(T, 1)
-    fp4_mla_kernel(const Fp4MlaArgs a, int tiles_per_request, int queries_per_tile,
+    fp4_mla_kernel(const Fp4MlaArgs a, int tiles_per_request, int queries_per_tile, int units,
                    const __grid_constant__ CUtensorMap tm_q, float* __restrict__ part_o, float* __restrict__ part_lse,
                    uint32_t* __restrict__ err) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -388,78 +453,45 @@ __global__ void __launch_bounds__(T, 1)
   __shared__ uint32_t s_taddr;
   __shared__ __align__(8) Barriers bs;
   __shared__ int s_abort;
-  __shared__ int s_issued;  // blocks whose MMAs the issuer started (the last commit to wait for)
+  __shared__ int s_issued;     // blocks whose MMAs the issuer started (the last commit to wait for)
+  __shared__ int s_requested;  // units whose Q was requested
   volatile int* abort = &s_abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = blockIdx.x & 1u, partner = rank ^ 1u;  // 0: S-CTA, 1: O-CTA
-  const int tile = blockIdx.x >> 1, r = tile / tiles_per_request;
-  const int q0 = (tile - r * tiles_per_request) * queries_per_tile;  // the tile's first query
-  const int nq = min(queries_per_tile, a.num_queries - q0);
-  const int live_heads = nq * a.num_heads;
-  const size_t row0 = ((size_t)r * a.num_queries + q0) * a.num_heads;  // its first row of q, o and lse
-
-  // the tile's rows: every row that some query of the tile sees
-  Rows<kWin> rows;
-  rows.pool_rows = a.pool_rows;
-  int64_t S = 0;
-  int total;
-  if (kWin) {
-    rows.table = a.pages + (size_t)r * a.max_pages;
-    rows.page_size = a.page_size;
-    S = a.seq_lens[r];
-    const bool bad = S < 0 || S > (int64_t)a.max_pages * a.page_size;
-    if (bad && tid == 0) atomicOr(err, HS_FLAG_SEQLEN);
-    // tokens up to the tile's last query, from the first one of its first query
-    const int64_t end = bad ? 0 : max((int64_t)0, S - a.num_queries + q0 + nq);
-    const int64_t first = max((int64_t)0, S - a.num_queries + q0);
-    rows.kept = (int)min((int64_t)a.sinks, end);
-    rows.start = (int)max((int64_t)rows.kept, first + 1 - a.window);
-    total = rows.kept + (int)max((int64_t)0, end - rows.start);
-  } else {
-    rows.table = a.out_rows + (size_t)r * a.top_k;
-    total = a.top_k;
-  }
-  const int all_blocks = (int)(((int64_t)total + BJ - 1) / BJ), per = (all_blocks + a.splits - 1) / a.splits;
-  const int p = blockIdx.y;
-  const int nblk = max(0, min(per, all_blocks - p * per));
-  rows.j0 = p * per * BJ;
-  rows.n = nblk > 0 ? min(total - rows.j0, nblk * BJ) : 0;
+  const int pairs = gridDim.x >> 1;
 
   if (tid == 0) {
     for (int k = 0; k < NT; ++k) {
       bar_init(&bs.tile_full[k], NDEQ);
       bar_init(&bs.tile_free[k], 1);
     }
-    bar_init(&bs.q_raw, 1);
-    bar_init(&bs.q_full, 8);  // one arrival per softmax warp
-    bar_init(&bs.mma_done, 1);
     for (int k = 0; k < NS; ++k) {
+      bar_init(&bs.q_raw[k], 1);
       bar_init(&bs.s_full[k], 1);
       bar_init(&bs.s_free[k], 4);  // the warps of the block's softmax warpgroup
       for (int w = 0; w < 4; ++w) bar_init(&bs.m_set[k][w], 1);
       bar_init(&bs.p_free[k], 1);
     }
+    bar_init(&bs.q_full, 4 * NS);  // one arrival per softmax warp
+    bar_init(&bs.mma_done, 1);
     for (int k = 0; k < 2; ++k) {
       bar_init(&bs.p_full[k], 1);  // the O-CTA's expect_tx; the S-CTA's stores complete it
       bar_init(&bs.pv_go[k], 4);
+      bar_init(&bs.fin[k], 4);
     }
-    bar_init(&bs.fin, 4);
     s_abort = 0;
     s_issued = 0;
+    s_requested = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    if (rank == 0 && nblk > 0) {
-      // Q's 128 rows as nine tensor boxes of 64 dims (rows past the tile's are not used)
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // q_raw's init, seen by the copies
-      bar_arrive_tx(&bs.q_raw, KATOMS * QBOX);
-      for (int bx = 0; bx < KATOMS; ++bx)
-        asm volatile(
-            "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
-            "[%4];" ::"r"(smem_u32(base + S_QSTAGE + bx * QBOX)),
-            "l"(&tm_q), "r"(64 * bx), "r"((int)row0), "r"(smem_u32(&bs.q_raw))
-            : "memory");
+    if (rank == 0) {
+      const Unit<kWin> first = unit_of<kWin>(a, blockIdx.x >> 1, tiles_per_request, queries_per_tile, false, err);
+      if (first.nblk > 0) {
+        request_q(&tm_q, first.row0, base, bs);
+        s_requested = 1;
+      }
+    } else {
+      for (int k = 0; k < 2; ++k) bar_arrive_tx(&bs.p_full[k], P_BYTES);
     }
-    if (rank == 1)
-      for (int k = 0; k < 2 && k < nblk; ++k) bar_arrive_tx(&bs.p_full[k], P_BYTES);
   }
   if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_taddr)),
@@ -470,334 +502,390 @@ __global__ void __launch_bounds__(T, 1)
   tc_before();
   __syncthreads();
   tc_after();
-  cluster_sync_all();  // both CTAs' barriers are initialised before either arrives on the other's
+  // both CTAs' barriers are initialised before either arrives on the other's (the initialiser's fence
+  // makes them visible: the barrier itself need not wait for anything)
+  asm volatile("barrier.cluster.arrive.relaxed;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
   const uint32_t tbase = s_taddr;
   const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
   const int head = (warp & 3) * 32 + lane;  // this thread's row of the tile = its tensor-memory lane
   uint8_t* masks = base + S_MASK;
 
-  float m_own = -INFINITY, l_own = 0.f;  // softmax: the sum of this thread's blocks, under this reference
-
-  if (rank == 0) {
-    // ================================ S-CTA ================================
-    uint8_t* tiles = base + S_TILES;
-    if (warp < 4 * NS) {
-      const int wg = warp >> 2;
-      if (nblk > 0 && warp < 8) {
-        // Q into tensor memory (warpgroup wg the columns [144 wg, 144 wg + 144)), column c holding
-        // dims 2c, 2c + 1: the latent part as f16, the RoPE part as bf16 over latent_scale
-        const uint8_t* qs = base + S_QSTAGE;
-        const bool landed = sync_and(pipe_wait(&bs.q_raw, 1, 0, abort), 2 * MH);
-        const bool live = landed && head < live_heads;
-        const uint8_t* src = qs + head * 128;
-        const float inv = 1.f / a.latent_scale;
-        const uint32_t sign = a.sm_scale < 0.f ? 0x80008000u : 0u;  // so that scores scale by a positive factor
-#pragma unroll 2
-        for (int c = 36 * wg; c < 36 * wg + 36; c += 2) {  // two 16-B chunks: 16 dims, 8 columns
-          uint32_t x[8] = {};
-          if (live) {
-            *reinterpret_cast<uint4*>(x) =
-                *reinterpret_cast<const uint4*>(src + (c >> 3) * QBOX + (((c & 7) ^ (head & 7)) << 4));
-            *reinterpret_cast<uint4*>(x + 4) =
-                *reinterpret_cast<const uint4*>(src + ((c + 1) >> 3) * QBOX + ((((c + 1) & 7) ^ (head & 7)) << 4));
-          }
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            if (c < DL / 8) {
-              x[i] = bf16x2_to_f16x2(x[i]);
-            } else {
-              const __nv_bfloat162 v =
-                  __floats2bfloat162_rn(__uint_as_float(x[i] << 16) * inv, __uint_as_float(x[i] & 0xFFFF0000u) * inv);
-              x[i] = *reinterpret_cast<const uint32_t*>(&v);
-            }
-            x[i] ^= sign;
-          }
-          asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(
-                           tbase + lane_off + Q_COL + 4 * c),
-                       "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
-                       : "memory");
-        }
-        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-        tc_before();
-        __syncwarp();
-        if (lane == 0) bar_arrive(&bs.q_full);
-      }
-      // window: this query sees the list's rows [0, see_kept) and [see_lo, see_hi)
-      int see_kept = 0, see_lo = 0, see_hi = 0;
-      if (kWin) {
-        const int64_t at = S - a.num_queries + q0 + head / a.num_heads;  // its token
-        see_kept = (int)min((int64_t)rows.kept, at + 1) - rows.j0;
-        see_lo = (int)(rows.kept + max((int64_t)0, at + 1 - a.window - rows.start)) - rows.j0;
-        see_hi = (int)(rows.kept + max((int64_t)0, at + 1 - rows.start)) - rows.j0;
-      }
-      // Warpgroup wg takes the blocks b with b % NS = wg, a query head per thread. From one block to
-      // the next only the reference maximum goes over, from warp to warp (the warps of the same
-      // heads): it is known once a block's scores have been read, so the warpgroups' exponentials
-      // overlap. Each keeps the sum of its own blocks under the reference of its last one. The scores
-      // are read twice, for the maximum and for the weights (64 of them do not fit a thread's 64
-      // registers).
-      float* s_ref = reinterpret_cast<float*>(base + S_REF);
-      const uint32_t r_pbuf = remote(base + O_P, partner), r_alpha = remote(base + O_ALPHA, partner);
-      const uint32_t rbar0 = remote(&bs.p_full[0], partner), rbar1 = remote(&bs.p_full[1], partner);
-      // scores in log2 units; a scale of zero stays above it, so that -inf stays -inf
-      const float sl2 = fmaxf(fabsf(a.sm_scale * a.latent_scale * 1.4426950408889634f), 1e-37f);
-      const uint32_t s_at = tbase + lane_off + S_COL + BJ * wg;
-      uint32_t turn = 0;  // of this warpgroup: its barriers' phase
+  // The units of this pair, one after the other. The two CTAs run on by themselves: the S-CTA is at the
+  // next unit's first blocks while the O-CTA still writes the last one's output.
+  int done = 0, full = 0;  // blocks, and units with blocks, before this one
+  bool ok = true;
 #pragma unroll 1
-      for (int b = wg; b < nblk; b += NS, turn ^= 1u) {
-        if (!__all_sync(0xffffffffu, ready_or_wait(&bs.s_full[wg], 1, (int)turn, abort))) break;
-        tc_after();
-        // the rows that exist, and that this query sees
-        const volatile uint32_t* at = reinterpret_cast<const volatile uint32_t*>(masks + (b % MASKS) * NDEQ);
-        uint32_t sees0 = at[0], sees1 = at[1];
-        if (kWin) {
-          const int j = BJ * b;
-          sees0 &= bit_range(0, see_kept - j) | bit_range(see_lo - j, see_hi - j);
-          sees1 &= bit_range(0, see_kept - j - 32) | bit_range(see_lo - j - 32, see_hi - j - 32);
-        }
-        const bool every = __all_sync(0xffffffffu, (sees0 & sees1) == 0xFFFFFFFFu);
-        const auto scores = [&](int c, float (&t)[32]) {  // 32 c .. 32 c + 31 of the block, -inf where it does not look
-          tmem_ld32(s_at + 32 * c, t);
-          if (!every) {
-            const uint32_t sees = c ? sees1 : sees0;
-#pragma unroll
-            for (int i = 0; i < 32; ++i) t[i] = ((sees >> i) & 1u) ? t[i] : -INFINITY;
-          }
-        };
-        float bm = -INFINITY;
-#pragma unroll 1
-        for (int c = 0; c < BJ / 32; ++c) {
-          float t[32];
-          scores(c, t);
-          float x0 = t[0], x1 = t[1];
-#pragma unroll
-          for (int i = 2; i < 32; i += 2) {
-            x0 = fmaxf(x0, t[i]);
-            x1 = fmaxf(x1, t[i + 1]);
-          }
-          bm = fmaxf(bm, fmaxf(x0, x1));
-        }
-        bm *= sl2;
-        float m_run = -INFINITY;
-        if (b > 0) {
-          // (the block before is the last warpgroup's block of this turn, or of the turn before)
-          const int before = wg == 0 ? NS - 1 : wg - 1;
-          if (!__all_sync(0xffffffffu, ready_or_wait(&bs.m_set[before][warp & 3], 1, (int)(wg == 0 ? turn ^ 1u : turn), abort)))
-            break;
-          m_run = s_ref[head];
-        }
-        // Lazy rescale: a head keeps its reference until a block's maximum passes it by 2^8, so P
-        // stays below 2^8 and O is rescaled only on those rare jumps. (NaN scores leave it alone.)
-        const float m_new = bm > m_run + kRescaleLog2 || m_run == -INFINITY ? fmaxf(m_run, bm) : m_run;
-        s_ref[head] = m_new;
-        __syncwarp();
-        if (lane == 0) bar_arrive(&bs.m_set[wg][warp & 3]);
-        const float alpha = m_new == -INFINITY ? 1.f : ex2(m_run - m_new);  // m_run = -inf: O is still 0
-        const float ref = m_new == -INFINITY ? 0.f : m_new;  // a NaN score stays one, an unseen row's weight is 0
-        l_own *= m_new == -INFINITY ? 1.f : ex2(m_own - m_new);
-        m_own = m_new;
-        // the O-CTA's P buffer is free once P . V of block b - 2 is done
-        if (!__all_sync(0xffffffffu, b < 2 || ready_or_wait<true>(bs.p_free, NS, b - 2, abort))) break;
-        const uint32_t pbuf = r_pbuf + (b & 1) * P_BUF, rbar = b & 1 ? rbar1 : rbar0;
-        st_async_f32(r_alpha + 4 * ((b & 1) * MH + head), alpha, rbar);
-        float2 sum = make_float2(0.f, 0.f);
-#pragma unroll 1
-        for (int c = 0; c < BJ / 32; ++c) {
-          float t[32];
-          scores(c, t);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {  // four 16-B chunks of 8 f16
-            uint32_t w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              float2 e = fma2(make_float2(t[8 * q + 2 * i], t[8 * q + 2 * i + 1]), make_float2(sl2, sl2), make_float2(-ref, -ref));
-              e = make_float2(ex2(e.x), ex2(e.y));
-              const __half2 pb = __floats2half2_rn(e.x, e.y);
-              sum = add2(sum, e);
-              w[i] = *reinterpret_cast<const uint32_t*>(&pb);
-            }
-            st_async16(pbuf + sw128(head, 32 * c + 8 * q), make_uint4(w[0], w[1], w[2], w[3]), rbar);
-          }
-        }
-        tc_before();
-        __syncwarp();
-        if (lane == 0) bar_arrive(&bs.s_free[wg]);  // S has been read
-        l_own += sum.x + sum.y;
-      }
-    } else if (warp == S_ISSUER) {
-      // (tensor memory starts at 0: all of it is allocated here)
-      const bool one = elected();
-      const uint64_t k0 = mdesc(smem_u32(base + S_TILES), 16, 1024);
-      bool go = __all_sync(0xffffffffu, nblk == 0 || pipe_wait(&bs.q_full, 1, 0, abort));
-#pragma unroll 1
-      for (int b = 0; go && b < nblk; ++b) {
-        bool ok = ready_or_wait(bs.tile_full, NT, b, abort);
-        ok = ok && (b < NS || ready_or_wait(bs.s_free, NS, b - NS, abort));
-        if (!__all_sync(0xffffffffu, ok)) break;
-        tc_after();
-        fence_async_smem();  // the tile's generic writes, seen through its barrier, before the tensor core's reads
-        const uint64_t dk0 = k0 + (uint64_t)((b % NT) * (K_TILE >> 4));
-        const uint32_t d = S_COL + BJ * (b % NS);
-        if (one) {
-#pragma unroll
-          for (int kk = 0; kk < KATOMS * 4; ++kk)
-            mma_ta(d, Q_COL + 8 * kk, dk0 + (uint64_t)(((kk >> 2) * KV_ATOM + (kk & 3) * 32) >> 4),
-                   kk < DL / 16 ? kIdescQK : kIdescRope, kk > 0);
-          commit(&bs.s_full[b % NS]);
-          commit(&bs.tile_free[b % NT]);
-          s_issued = b + 1;
-        }
-        __syncwarp();
-      }
-    } else if (const int wq = deq_warp(warp, S_DEQ0); wq >= 0) {
-      run_dequant<true, kWin>(rows, a.pool, nblk, base + S_RAW + wq * S_RING, masks, tiles, bs, wq, lane, err, abort);
-    }
-  } else {
-    // ================================ O-CTA ================================
-    uint8_t* tiles = base + O_TILES;
-    const float* alpha_buf = reinterpret_cast<const float*>(base + O_ALPHA);
-    if (warp < 4) {
-      // corrector: where a reference maximum of the warp's heads rose, rescale O once P . V of block
-      // b - 1 is done
-      for (int b = 0; b < nblk; ++b) {
-        if (!__all_sync(0xffffffffu, ready_or_wait<true>(bs.p_full, 2, b, abort))) break;
-        const float f = alpha_buf[(b & 1) * MH + head];
-        // this buffer's next phase is block b + 2: its bytes come only after P . V of block b
-        if (tid == 0 && b + 2 < nblk) bar_arrive_tx(&bs.p_full[b & 1], P_BYTES);
-        if (__any_sync(0xffffffffu, b > 0 && f != 1.f)) {
-          if (!__all_sync(0xffffffffu, ready_or_wait(bs.tile_free, NT, b - 1, abort))) break;
+  for (int u = blockIdx.x >> 1; u < units; u += pairs) {
+    const Unit<kWin> un = unit_of<kWin>(a, u, tiles_per_request, queries_per_tile, tid == 0, err);
+    const int nblk = un.nblk;
+    if (rank == 0) {
+      // ================================ S-CTA ================================
+      uint8_t* tiles = base + S_TILES;
+      const uint32_t q_phase = (uint32_t)full & 1u;
+      float m_own = -INFINITY, l_own = 0.f;  // softmax: the sum of this thread's blocks, under this reference
+      if (warp < 4 * NS) {
+        const int wg = warp >> 2;
+        if (nblk > 0) {
+          // Q into tensor memory (warpgroup wg the columns [96 wg, 96 wg + 96)), column c holding dims
+          // 2c, 2c + 1: the latent part as f16, the RoPE part as bf16 over latent_scale. Q has landed
+          // only after the last unit's MMAs, which read the columns.
+          const bool landed = __all_sync(0xffffffffu, ready_or_wait(&bs.q_raw[wg], 1, (int)q_phase, abort));
           tc_after();
+          const bool live = landed && head < un.live;
+          const float inv = 1.f / a.latent_scale;
+          const uint32_t sign = a.sm_scale < 0.f ? 0x80008000u : 0u;  // so that scores scale by a positive factor
 #pragma unroll 1
-          for (int c = 0; c < DL; c += 16) {
-            float v[16];
-            tmem_ld16(tbase + lane_off + c, v);
+          for (int bx = KATOMS / NS * wg; bx < KATOMS / NS * (wg + 1); ++bx) {
+            const uint8_t* src = base + S_QSTAGE + bx * QBOX + head * 128;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] *= f;
-            tmem_st16(tbase + lane_off + c, v);
+            for (int h = 0; h < 4; ++h) {  // two 16-B chunks: 16 dims, 8 columns
+              uint32_t x[8] = {};
+              if (live) {
+                *reinterpret_cast<uint4*>(x) = *reinterpret_cast<const uint4*>(src + (((2 * h) ^ (head & 7)) << 4));
+                *reinterpret_cast<uint4*>(x + 4) = *reinterpret_cast<const uint4*>(src + (((2 * h + 1) ^ (head & 7)) << 4));
+              }
+              if (bx < VATOMS) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = bf16x2_to_f16x2(x[i]) ^ sign;
+              } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  const __nv_bfloat162 v =
+                      __floats2bfloat162_rn(__uint_as_float(x[i] << 16) * inv, __uint_as_float(x[i] & 0xFFFF0000u) * inv);
+                  x[i] = *reinterpret_cast<const uint32_t*>(&v) ^ sign;
+                }
+              }
+              asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(
+                               tbase + lane_off + Q_COL + 32 * bx + 8 * h),
+                           "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+                           : "memory");
+            }
+          }
+          asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+          tc_before();
+          __syncwarp();
+          if (lane == 0) bar_arrive(&bs.q_full);
+        }
+        // window: this query sees the list's rows [0, see_kept) and [see_lo, see_hi)
+        int see_kept = 0, see_lo = 0, see_hi = 0;
+        if (kWin) {
+          const int64_t at = un.seq_len - a.num_queries + un.first_query + head / a.num_heads;  // its token
+          see_kept = (int)min((int64_t)un.rows.kept, at + 1) - un.rows.j0;
+          see_lo = (int)(un.rows.kept + max((int64_t)0, at + 1 - a.window - un.rows.start)) - un.rows.j0;
+          see_hi = (int)(un.rows.kept + max((int64_t)0, at + 1 - un.rows.start)) - un.rows.j0;
+        }
+        // Warpgroup wg takes the blocks whose number g = done + b has g % NS = wg, a query head per
+        // thread. From one block to the next only the reference maximum goes over, from warp to warp
+        // (the warps of the same heads): it is known once a block's scores have been read, so the
+        // warpgroups' exponentials overlap. Each keeps the sum of its own blocks under the reference of
+        // its last one. The scores are read twice, for the maximum and for the weights.
+        float* s_ref = reinterpret_cast<float*>(base + S_REF);
+        const uint32_t r_pbuf = remote(base + O_P, partner), r_alpha = remote(base + O_ALPHA, partner);
+        const uint32_t rbar0 = remote(&bs.p_full[0], partner), rbar1 = remote(&bs.p_full[1], partner);
+        // scores in log2 units; a scale of zero stays above it, so that -inf stays -inf
+        const float sl2 = fmaxf(fabsf(a.sm_scale * a.latent_scale * 1.4426950408889634f), 1e-37f);
+        const uint32_t s_at = tbase + lane_off + S_COL + BJ * wg;
+        int b = wg - done % NS;
+        if (b < 0) b += NS;
+        uint32_t turn = (uint32_t)((done + b) / NS) & 1u;  // of this warpgroup: its barriers' phase
+#pragma unroll 1
+        for (; b < nblk; b += NS, turn ^= 1u) {
+          const int g = done + b;
+          if (!__all_sync(0xffffffffu, ready_or_wait(&bs.s_full[wg], 1, (int)turn, abort))) break;
+          tc_after();
+          // the rows that exist, and that this query sees
+          const volatile uint32_t* at = reinterpret_cast<const volatile uint32_t*>(masks + (g % MASKS) * NDEQ);
+          uint32_t sees0 = at[0], sees1 = at[1];
+          if (kWin) {
+            const int j = BJ * b;
+            sees0 &= bit_range(0, see_kept - j) | bit_range(see_lo - j, see_hi - j);
+            sees1 &= bit_range(0, see_kept - j - 32) | bit_range(see_lo - j - 32, see_hi - j - 32);
+          }
+          const bool every = __all_sync(0xffffffffu, (sees0 & sees1) == 0xFFFFFFFFu);
+          const auto scores = [&](int c, float (&t)[32]) {  // 32 c .. 32 c + 31 of the block, -inf where it does not look
+            tmem_ld32(s_at + 32 * c, t);
+            if (!every) {
+              const uint32_t sees = c ? sees1 : sees0;
+#pragma unroll
+              for (int i = 0; i < 32; ++i) t[i] = ((sees >> i) & 1u) ? t[i] : -INFINITY;
+            }
+          };
+          float bm = -INFINITY;
+#pragma unroll 1
+          for (int c = 0; c < BJ / 32; ++c) {
+            float t[32];
+            scores(c, t);
+            float x0 = t[0], x1 = t[1];
+#pragma unroll
+            for (int i = 2; i < 32; i += 2) {
+              x0 = fmaxf(x0, t[i]);
+              x1 = fmaxf(x1, t[i + 1]);
+            }
+            bm = fmaxf(bm, fmaxf(x0, x1));
+          }
+          bm *= sl2;
+          float m_run = -INFINITY;
+          if (b > 0) {
+            // (the block before is the last warpgroup's block of this turn, or of the turn before)
+            const int before = wg == 0 ? NS - 1 : wg - 1;
+            if (!__all_sync(0xffffffffu, ready_or_wait(&bs.m_set[before][warp & 3], 1, (int)(wg == 0 ? turn ^ 1u : turn), abort)))
+              break;
+            m_run = s_ref[head];
+          }
+          // Lazy rescale: a head keeps its reference until a block's maximum passes it by 2^8, so P
+          // stays below 2^8 and O is rescaled only on those rare jumps. (NaN scores leave it alone.)
+          const float m_new = bm > m_run + kRescaleLog2 || m_run == -INFINITY ? fmaxf(m_run, bm) : m_run;
+          s_ref[head] = m_new;
+          __syncwarp();
+          if (lane == 0) bar_arrive(&bs.m_set[wg][warp & 3]);
+          const float alpha = m_new == -INFINITY ? 1.f : ex2(m_run - m_new);  // m_run = -inf: O is still 0
+          const float ref = m_new == -INFINITY ? 0.f : m_new;  // a NaN score stays one, an unseen row's weight is 0
+          l_own *= m_new == -INFINITY ? 1.f : ex2(m_own - m_new);
+          m_own = m_new;
+          // the O-CTA's P buffer is free once P . V of block g - 2 is done
+          if (!__all_sync(0xffffffffu, g < 2 || ready_or_wait<true>(bs.p_free, NS, g - 2, abort))) break;
+          const uint32_t pbuf = r_pbuf + (g & 1) * P_BUF, rbar = g & 1 ? rbar1 : rbar0;
+          st_async_f32(r_alpha + 4 * ((g & 1) * MH + head), alpha, rbar);
+          float2 sum = make_float2(0.f, 0.f);
+#pragma unroll 1
+          for (int c = 0; c < BJ / 32; ++c) {
+            float t[32];
+            scores(c, t);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {  // four 16-B chunks of 8 f16
+              uint32_t w[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                float2 e = fma2(make_float2(t[8 * q + 2 * i], t[8 * q + 2 * i + 1]), make_float2(sl2, sl2), make_float2(-ref, -ref));
+                e = make_float2(ex2(e.x), ex2(e.y));
+                const __half2 pb = __floats2half2_rn(e.x, e.y);
+                sum = add2(sum, e);
+                w[i] = *reinterpret_cast<const uint32_t*>(&pb);
+              }
+              st_async16(pbuf + sw128(head, 32 * c + 8 * q), make_uint4(w[0], w[1], w[2], w[3]), rbar);
+            }
           }
           tc_before();
+          __syncwarp();
+          if (lane == 0) bar_arrive(&bs.s_free[wg]);  // S has been read
+          l_own += sum.x + sum.y;
         }
-        __syncwarp();
-        if (lane == 0) bar_arrive(&bs.pv_go[b & 1]);
-      }
-    } else if (warp == O_ISSUER) {
-      const bool one = elected();
-      const uint64_t p0 = mdesc(smem_u32(base + O_P), 16, 1024), v0 = mdesc(smem_u32(base + O_TILES), KV_ATOM, 1024);
-#pragma unroll 1
-      for (int b = 0; b < nblk; ++b) {
-        bool ok = ready_or_wait(bs.tile_full, NT, b, abort);
-        ok = ok && ready_or_wait(bs.pv_go, 2, b, abort);
-        if (!__all_sync(0xffffffffu, ok)) break;
-        tc_after();
-        fence_async_smem();  // V's and P's writes, seen through their barriers, before the tensor core's reads
-        const uint64_t dp0 = p0 + (uint64_t)((b & 1) * (P_BUF >> 4)), dv0 = v0 + (uint64_t)((b % NT) * (V_TILE >> 4));
-        if (one) {
-#pragma unroll
-          for (int kk = 0; kk < BJ / 16; ++kk)
-#pragma unroll
-            for (int nh = 0; nh < 2; ++nh)
-              mma_ss(256 * nh, dp0 + (uint64_t)((kk * 32) >> 4), dv0 + (uint64_t)((nh * 4 * KV_ATOM + kk * 2048) >> 4),
-                     kIdescPV, (b > 0 || kk > 0) ? 1u : 0u);
-          commit(&bs.tile_free[b % NT]);
-          commit_multicast(&bs.p_free[b % NS], (uint16_t)(1u << partner));
-          commit(&bs.mma_done);
-          s_issued = b + 1;
+        if (wg > 0) {
+          float* sums = reinterpret_cast<float*>(base + S_SUMS) + 2 * (wg - 1) * MH;
+          sums[head] = l_own;
+          sums[MH + head] = m_own;
         }
-        __syncwarp();
-      }
-    } else if (const int wq = deq_warp(warp, O_DEQ0); wq >= 0) {
-      run_dequant<false, kWin>(rows, a.pool, nblk, base + O_RAW + wq * O_RING, masks, tiles, bs, wq, lane, err, abort);
-    }
-  }
-
-  __syncthreads();
-  if (rank == 0) {
-    float* sums = reinterpret_cast<float*>(base + S_SUMS);
-    if (warp < 4 * NS) {
-      sums[2 * (warp >> 2) * MH + head] = l_own;
-      sums[(2 * (warp >> 2) + 1) * MH + head] = m_own;
-    }
-    __syncthreads();
-  }
-  if (rank == 0 && warp < 4) {
-    // the warpgroups' sums under the last block's reference, and that, to the O-CTA
-    const float* sums = reinterpret_cast<const float*>(base + S_SUMS);
-    const float m = nblk > 0 ? reinterpret_cast<const float*>(base + S_REF)[head] : -INFINITY;
-    float l = 0.f;
-    for (int g = 0; g < NS; ++g) {
-      const float x = sums[2 * g * MH + head], mo = sums[(2 * g + 1) * MH + head];
-      l += m == -INFINITY ? x : x * ex2(mo - m);
-    }
-    const uint32_t fin = remote(base + O_FIN, partner);
-    st_remote_f32(fin + 4 * head, l);
-    st_remote_f32(fin + 4 * (MH + head), m);
-    __syncwarp();
-    if (lane == 0) bar_arrive_remote(remote(&bs.fin, partner));
-  }
-  // this CTA's MMAs of every block are done; the O-CTA also has the S-CTA's totals, the S-CTA
-  // the O-CTA's last P-buffer releases (its last arrivals here)
-  bool ok = !*abort && (nblk == 0 || pipe_wait(bs.tile_free, NT, nblk - 1, abort));
-  if (rank == 1) {
-    ok = ok && pipe_wait<true>(&bs.fin, 1, 0, abort);
-  } else {
-    for (int b = nblk >= 2 ? nblk - 2 : 0; b < nblk; ++b) ok = ok && pipe_wait<true>(bs.p_free, NS, b, abort);
-  }
-  ok = __syncthreads_and(ok && !*abort);
-  tc_after();
-  if (rank == 1 && ok && warp < 16) {
-    // O out, normalised: warp w holds rows 32 (w & 3) .. + 31 and takes a quarter of the columns,
-    // 32 at a time through its own staging rows, so that global stores write whole lines
-    const float* fin = reinterpret_cast<const float*>(base + O_FIN);
-    const float l = fin[head], m = fin[MH + head];
-    const float inv = l == 0.f ? 0.f : a.latent_scale / l;  // l is NaN where a weight is
-    const float lse = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
-    const int head0 = (warp & 3) * 32;
-    float* stg = reinterpret_cast<float*>(base + O_TILES) + warp * (32 * EPI_PITCH);
-    const bool direct = a.splits == 1;
-    const size_t out0 = direct ? row0 : (size_t)p * ((size_t)(gridDim.x >> 1) / tiles_per_request) * a.num_queries * a.num_heads + row0;
-    const int c0 = (warp >> 2) * (DL / 4);
+      } else if (warp == S_ISSUER) {
+        // (tensor memory starts at 0: all of it is allocated here)
+        const bool one = elected();
+        const uint64_t k0 = mdesc(smem_u32(base + S_TILES), 16, 1024);
+        bool go = __all_sync(0xffffffffu, nblk == 0 || ready_or_wait(&bs.q_full, 1, (int)q_phase, abort));
 #pragma unroll 1
-    for (int c = c0; c < c0 + DL / 4; c += 32) {
-      float v[32];
-      if (nblk > 0) {
-        tmem_ld16(tbase + lane_off + c, *reinterpret_cast<float(*)[16]>(v));
-        tmem_ld16(tbase + lane_off + c + 16, *reinterpret_cast<float(*)[16]>(v + 16));
-      } else {
+        for (int b = 0; go && b < nblk; ++b) {
+          const int g = done + b;
+          go = ready_or_wait(bs.tile_full, NT, g, abort);
+          go = go && (g < NS || ready_or_wait(bs.s_free, NS, g - NS, abort));
+          go = __all_sync(0xffffffffu, go);
+          if (!go) break;
+          tc_after();
+          fence_async_smem();  // the tile's generic writes, seen through its barrier, before the tensor core's reads
+          const uint64_t dk0 = k0 + (uint64_t)((g % NT) * (K_TILE >> 4));
+          const uint32_t d = S_COL + BJ * (g % NS);
+          if (one) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = 0.f;
-      }
-#pragma unroll
-      for (int i = 0; i < 32; i += 4)
-        *reinterpret_cast<float4*>(stg + lane * EPI_PITCH + i) =
-            make_float4(v[i] * inv, v[i + 1] * inv, v[i + 2] * inv, v[i + 3] * inv);
-      __syncwarp();
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int rr = 4 * i + (lane >> 3), q4 = lane & 7;
-        if (head0 + rr < live_heads) {
-          const float4 x = *reinterpret_cast<const float4*>(stg + rr * EPI_PITCH + 4 * q4);
-          const size_t at = (out0 + head0 + rr) * DL + c + 4 * q4;
-          if (direct) {
-            const __nv_bfloat162 lo = __floats2bfloat162_rn(x.x, x.y), hi = __floats2bfloat162_rn(x.z, x.w);
-            *reinterpret_cast<uint2*>(a.o + at) =
-                make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-          } else {
-            *reinterpret_cast<float4*>(part_o + at) = x;
+            for (int kk = 0; kk < KATOMS * 4; ++kk)
+              mma_ta(d, Q_COL + 8 * kk, dk0 + (uint64_t)(((kk >> 2) * KV_ATOM + (kk & 3) * 32) >> 4),
+                     kk < DL / 16 ? kIdescQK : kIdescRope, kk > 0);
+            commit(&bs.s_full[g % NS]);
+            commit(&bs.tile_free[g % NT]);
+            s_issued = g + 1;
+          }
+          __syncwarp();
+        }
+        // the next unit's Q, once this one's MMAs have read the tiles that it is staged over
+        if (go && u + pairs < units) {
+          const Unit<kWin> next = unit_of<kWin>(a, u + pairs, tiles_per_request, queries_per_tile, false, err);
+          if (next.nblk > 0) {
+            const int last = done + nblk - 1;
+            go = __all_sync(0xffffffffu, last < 0 || ready_or_wait(bs.tile_free, NT, last, abort));
+            if (go && one) {
+              request_q(&tm_q, next.row0, base, bs);
+              ++s_requested;
+            }
+            __syncwarp();
           }
         }
+      } else if (const int wq = deq_warp(warp, S_DEQ0); wq >= 0) {
+        run_dequant<true, kWin>(un.rows, a.pool, nblk, done, q_phase, base + S_RAW + wq * S_RING, masks, tiles, bs, wq,
+                                lane, err, abort);
       }
-      __syncwarp();
+      __syncthreads();
+      if (nblk > 0 && warp < 4) {
+        // the warpgroups' sums under the last block's reference, and that, to the O-CTA
+        const float* sums = reinterpret_cast<const float*>(base + S_SUMS);
+        const float m = reinterpret_cast<const float*>(base + S_REF)[head];
+        const auto part = [&](float l, float mo) { return m == -INFINITY ? l : l * ex2(mo - m); };
+        float l = part(l_own, m_own);
+        for (int g = 0; g < NS - 1; ++g) l += part(sums[2 * g * MH + head], sums[(2 * g + 1) * MH + head]);
+        const uint32_t fin = remote(base + O_FIN, partner) + (full & 1) * (2 * MH * 4);
+        st_remote_f32(fin + 4 * head, l);
+        st_remote_f32(fin + 4 * (MH + head), m);
+        __syncwarp();
+        if (lane == 0) bar_arrive_remote(remote(&bs.fin[full & 1], partner));
+      }
+      ok = __syncthreads_and(!*abort);
+    } else {
+      // ================================ O-CTA ================================
+      uint8_t* tiles = base + O_TILES;
+      const float* alpha_buf = reinterpret_cast<const float*>(base + O_ALPHA);
+      if (warp < 4) {
+        // corrector: where a reference maximum of the warp's heads rose, rescale O once P . V of the
+        // block before is done
+#pragma unroll 1
+        for (int b = 0; b < nblk; ++b) {
+          const int g = done + b;
+          if (!__all_sync(0xffffffffu, ready_or_wait<true>(bs.p_full, 2, g, abort))) break;
+          const float f = alpha_buf[(g & 1) * MH + head];
+          // this buffer's next phase is block g + 2: its bytes come only after P . V of block g
+          if (tid == 0) bar_arrive_tx(&bs.p_full[g & 1], P_BYTES);
+          if (__any_sync(0xffffffffu, b > 0 && f != 1.f)) {
+            if (!__all_sync(0xffffffffu, ready_or_wait(bs.tile_free, NT, g - 1, abort))) break;
+            tc_after();
+#pragma unroll 1
+            for (int c = 0; c < DL; c += 16) {
+              float v[16];
+              tmem_ld16(tbase + lane_off + c, v);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) v[i] *= f;
+              tmem_st16(tbase + lane_off + c, v);
+            }
+            tc_before();
+          }
+          __syncwarp();
+          if (lane == 0) bar_arrive(&bs.pv_go[g & 1]);
+        }
+      } else if (warp == O_ISSUER) {
+        const bool one = elected();
+        const uint64_t p0 = mdesc(smem_u32(base + O_P), 16, 1024), v0 = mdesc(smem_u32(base + O_TILES), KV_ATOM, 1024);
+#pragma unroll 1
+        for (int b = 0; b < nblk; ++b) {
+          const int g = done + b;
+          bool go = ready_or_wait(bs.tile_full, NT, g, abort);
+          go = go && ready_or_wait(bs.pv_go, 2, g, abort);
+          if (!__all_sync(0xffffffffu, go)) break;
+          tc_after();
+          fence_async_smem();  // V's and P's writes, seen through their barriers, before the tensor core's reads
+          const uint64_t dp0 = p0 + (uint64_t)((g & 1) * (P_BUF >> 4)), dv0 = v0 + (uint64_t)((g % NT) * (V_TILE >> 4));
+          if (one) {
+#pragma unroll
+            for (int kk = 0; kk < BJ / 16; ++kk)
+#pragma unroll
+              for (int nh = 0; nh < 2; ++nh)
+                mma_ss(256 * nh, dp0 + (uint64_t)((kk * 32) >> 4), dv0 + (uint64_t)((nh * 4 * KV_ATOM + kk * 2048) >> 4),
+                       kIdescPV, (b > 0 || kk > 0) ? 1u : 0u);
+            commit(&bs.tile_free[g % NT]);
+            commit_multicast(&bs.p_free[g % NS], (uint16_t)(1u << partner));
+            commit(&bs.mma_done);
+            s_issued = g + 1;
+          }
+          __syncwarp();
+        }
+      } else if (const int wq = deq_warp(warp, O_DEQ0); wq >= 0) {
+        run_dequant<false, kWin>(un.rows, a.pool, nblk, done, 0u, base + O_RAW + wq * O_RING, masks, tiles, bs, wq, lane,
+                                 err, abort);
+      }
+      __syncthreads();
+      // this unit's MMAs are done, and its totals are here
+      ok = !*abort;
+      if (nblk > 0)
+        ok = ok && ready_or_wait(bs.tile_free, NT, done + nblk - 1, abort) &&
+             ready_or_wait<true>(&bs.fin[full & 1], 1, (full >> 1) & 1, abort);
+      ok = __syncthreads_and(ok && !*abort);
+      tc_after();
+      if (ok && warp < 16) {
+        // O out, normalised: warp w has rows 32 (w & 3) .. + 31 and a quarter of the columns. The rows
+        // are staged in shared memory, 1024 bytes of each (all of a bf16 row; half of a row of partial
+        // sums, in two passes) and leave by one bulk copy a row.
+        const bool direct = a.splits == 1;
+        const float* fin = reinterpret_cast<const float*>(base + O_FIN) + (full & 1) * 2 * MH;
+        const float l = nblk > 0 ? fin[head] : 0.f, m = nblk > 0 ? fin[MH + head] : -INFINITY;
+        const float inv = l == 0.f ? 0.f : a.latent_scale / l;  // l is NaN where a weight is
+        uint8_t* stg = base + O_TILES + head * EPI_PITCH + (warp >> 2) * 256;
+        const size_t out0 = un.row0 + (direct ? 0 : (size_t)un.p * (units / a.splits / tiles_per_request) * a.num_queries * a.num_heads);
+#pragma unroll 1
+        for (int pass = 0; pass < (direct ? 1 : 2); ++pass) {
+          const int per = direct ? DL / 4 : DL / 8, c0 = pass * (DL / 2) + (warp >> 2) * per;
+#pragma unroll 1
+          for (int c = 0; c < per; c += 32) {
+            float v[32];
+            if (nblk > 0) {
+              tmem_ld32(tbase + lane_off + c0 + c, v);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] *= inv;
+            if (direct) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 8) {
+                uint32_t w[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const __nv_bfloat162 x = __floats2bfloat162_rn(v[i + 2 * k], v[i + 2 * k + 1]);
+                  w[k] = *reinterpret_cast<const uint32_t*>(&x);
+                }
+                *reinterpret_cast<uint4*>(stg + 2 * (c + i)) = make_uint4(w[0], w[1], w[2], w[3]);
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; i += 4)
+                *reinterpret_cast<float4*>(stg + 4 * (c + i)) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+            }
+          }
+          fence_async_smem();  // the staged rows, before the copies read them
+          sync_n(512);
+          if (warp < 4) {
+            if (head < un.live) {
+              const void* dst = direct ? static_cast<const void*>(a.o + (out0 + head) * DL)
+                                       : static_cast<const void*>(part_o + (out0 + head) * DL + pass * (DL / 2));
+              asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst),
+                           "r"(smem_u32(base + O_TILES + head * EPI_PITCH)), "r"(1024)
+                           : "memory");
+            }
+            asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
+          }
+          sync_n(512);  // the staging may be written again
+        }
+        if (head < un.live && warp < 4)
+          (direct ? a.lse : part_lse)[out0 + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+      }
+      tc_before();
+      __syncthreads();  // O and the staging are free for the next unit
+      tc_after();
     }
-    if (head < live_heads && warp < 4) (direct ? a.lse : part_lse)[out0 + head] = lse;
+    if (!ok) break;
+    done += nblk;
+    full += nblk > 0;
   }
+
+  // the S-CTA's MMAs are done (the O-CTA's are, unit by unit), and it has the O-CTA's last P-buffer
+  // releases (its last arrivals here)
+  if (rank == 0 && ok) {
+    ok = done == 0 || pipe_wait(bs.tile_free, NT, done - 1, abort);
+    for (int b = done >= 2 ? done - 2 : 0; b < done; ++b) ok = ok && pipe_wait<true>(bs.p_free, NS, b, abort);
+  }
+  ok = __syncthreads_and(ok && !*abort);
+  if (rank == 1) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // the outputs are written
   if (!ok) {
-    // outputs are not valid: flag it, and give any MMA still in flight one more bound before
-    // the tensor memory is released
+    // outputs are not valid: flag it, and give copies and MMAs still in flight one more bound before
+    // the shared and tensor memory are released
     if (tid == 0) atomicOr(err, HS_FLAG_TIMEOUT);
     __syncthreads();
     if (tid == 0) s_abort = 0;
     __syncthreads();
-    const int n = s_issued;
+    const int n = s_issued, q = s_requested;
+    for (int g = 0; rank == 0 && q > 0 && g < NS; ++g) pipe_wait(&bs.q_raw[g], 1, q - 1, abort);
     if (n > 0) {
       if (rank == 0)
         pipe_wait(bs.s_full, NS, n - 1, abort);
@@ -867,6 +955,16 @@ cudaError_t q_map(CUtensorMap* m, const uint16_t* q, int64_t rows) {
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// CTA pairs that the device holds at once: a CTA takes an SM.
+cudaError_t pairs_resident(int* pairs) {
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) (void)cudaGetLastError();
+  *pairs = sms > 3 ? sms / 2 : 1;
+  return e;
+}
+
 // Queries of one request whose heads share a tile, and the tiles that its queries make.
 int queries_per_tile(int num_heads, int num_queries) {
   const int fit = MH / num_heads;
@@ -880,13 +978,9 @@ int tiles_per_request(int num_heads, int num_queries) {
 }  // namespace
 
 int32_t fp4_mla_splits(int32_t num_requests, int32_t num_heads, int32_t num_queries, int64_t rows) {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-    (void)cudaGetLastError();
-    return 1;
-  }
-  const int64_t pairs = (int64_t)num_requests * tiles_per_request(num_heads, num_queries), slots = sms / 2 ? sms / 2 : 1;
+  int slots = 0;
+  if (pairs_resident(&slots) != cudaSuccess) return 1;
+  const int64_t pairs = (int64_t)num_requests * tiles_per_request(num_heads, num_queries);
   const int64_t blocks = (rows + BJ - 1) / BJ;
   int64_t best = 1, best_cost = INT64_MAX;
   for (int64_t s = 1; s <= HS_MAX_MLA_SPLITS && s <= blocks; ++s) {
@@ -910,6 +1004,8 @@ cudaError_t launch_fp4_mla(const Fp4MlaArgs& a, int32_t num_requests, float* par
   const auto kernel = win ? fp4_mla_kernel<true> : fp4_mla_kernel<false>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
   const int rows = num_requests * a.num_queries * a.num_heads;
+  int pairs = 1;
+  if (e == cudaSuccess) e = pairs_resident(&pairs);
   CUtensorMap tm_q;
   if (e == cudaSuccess) e = q_map(&tm_q, a.q, rows);
   if (e != cudaSuccess) {
@@ -917,9 +1013,10 @@ cudaError_t launch_fp4_mla(const Fp4MlaArgs& a, int32_t num_requests, float* par
     return e;
   }
   const int tiles = tiles_per_request(a.num_heads, a.num_queries), g = queries_per_tile(a.num_heads, a.num_queries);
+  const int units = num_requests * tiles * a.splits;
   float* part_lse = part ? part + (size_t)a.splits * rows * DL : nullptr;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2u * (unsigned)num_requests * (unsigned)tiles, (unsigned)a.splits);
+  cfg.gridDim = dim3(2u * (unsigned)(units < pairs ? units : pairs));
   cfg.blockDim = dim3(T);
   cfg.dynamicSmemBytes = SMEM_BYTES;
   cfg.stream = stream;
@@ -930,7 +1027,7 @@ cudaError_t launch_fp4_mla(const Fp4MlaArgs& a, int32_t num_requests, float* par
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kernel, a, tiles, g, tm_q, part, part_lse, err);
+  e = cudaLaunchKernelEx(&cfg, kernel, a, tiles, g, units, tm_q, part, part_lse, err);
   if (e != cudaSuccess) {
     (void)cudaGetLastError();
     return e;
