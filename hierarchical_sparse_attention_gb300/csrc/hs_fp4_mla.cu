@@ -245,18 +245,22 @@ __device__ __forceinline__ uint4 times(uint4 v, __half2 s) {
 }
 
 // A dequantisation warp's copies of a block: its eight rows' first REC bytes into a slot of its ring,
-// 16 bytes a lane; rows that do not exist become zeros. y: lane l has row l % 8 (-1: none).
+// eight lanes of 16 bytes to a row, four rows at a time: 128 consecutive bytes of each, which meet
+// every bank once, and addresses that are one register and a constant. Rows that do not exist become
+// zeros. y: lane l has row l % 8 (-1: none); dst: this lane's place in the slot.
 template <int REC>
-__device__ __forceinline__ void copy_rows(uint32_t slot, int32_t y, const uint8_t* __restrict__ pool, int lane) {
-  constexpr int PER = REC / 16, N = 8 * PER;
+__device__ __forceinline__ void copy_rows(uint32_t dst, int32_t y, const uint8_t* __restrict__ pool, int lane) {
 #pragma unroll
-  for (int i = 0; i < (N + 31) / 32; ++i) {
-    const int c = 32 * i + lane, r = c / PER, o = c - r * PER;
-    const int32_t row = __shfl_sync(0xffffffffu, y, r & 7);
-    if (N % 32 == 0 || c < N)
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(slot + 16 * c),
-                   "l"(pool + (int64_t)max(row, 0) * kFp4Row + 16 * o), "r"(row >= 0 ? 16 : 0)
-                   : "memory");
+  for (int g = 0; g < 2; ++g) {
+    const int32_t row = __shfl_sync(0xffffffffu, y, 4 * g + (lane >> 3));
+    const uint8_t* src = pool + (int64_t)max(row, 0) * kFp4Row + 16 * (lane & 7);
+    const int size = row >= 0 ? 16 : 0;
+#pragma unroll
+    for (int i = 0; i < (REC + 127) / 128; ++i)
+      if (128 * (i + 1) <= REC || 128 * i + 16 * (lane & 7) < REC)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + 4 * g * REC + 128 * i), "l"(src + 128 * i),
+                     "r"(size)
+                     : "memory");
   }
 }
 
@@ -287,14 +291,15 @@ __device__ __forceinline__ Held read_rows(const uint8_t* slot, int lane) {
   return h;
 }
 
-// Writes them into the tile, as f16, at the warp's group of eight rows.
+// Writes them into the tile, as f16, at the warp's group of eight rows. The place of chunk c of row x
+// of a line's eight is c ^ x: of a lane's four chunks it is one address with two bits flipped.
 template <bool kS>
 __device__ __forceinline__ void write_rows(const Held& h, uint8_t* group, int lane) {
   const int in4 = (lane >> 1) & 3;
+  const uint32_t at0 = smem_u32(group) + (lane >> 3) * KV_ATOM + in4 * 128 + (lane & 1) * 64 + in4 * 16;
+  const uint32_t at1 = (at0 ^ 64u) + 512u;
 #pragma unroll
   for (int s = 0; s < 4; ++s) {
-    const int g = s >> 1, it = (lane & 1) + 2 * (lane >> 3) + 8 * (s & 1);
-    uint8_t* at = group + (it >> 1) * KV_ATOM + (4 * g + in4) * 128 + ((lane & 1) ^ g) * 64;
     const uint32_t w[4] = {h.codes[s].x, h.codes[s].y, h.codes[s].z, h.codes[s].w};
     uint32_t two = h.scales[s];  // the scales of 16 dims each
     if (!kS) {  // V: no NaN (see above); K keeps it
@@ -304,15 +309,20 @@ __device__ __forceinline__ void write_rows(const Held& h, uint8_t* group, int la
     const __half2_raw raw = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
     const __half2 pair = raw, sc[2] = {__low2half2(pair), __high2half2(pair)};
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
-      *reinterpret_cast<uint4*>(at + ((u ^ in4) << 4)) = times(codes_to_f16(w[u]), sc[u >> 1]);
+    for (int u = 0; u < 4; ++u) {
+      const uint4 v = times(codes_to_f16(w[u]), sc[u >> 1]);
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(((s >> 1 ? at1 : at0) ^ (uint32_t)(u << 4)) + (s & 1) * 4 * KV_ATOM),
+                   "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                   : "memory");
+    }
   }
-  if (kS)
+  if (kS) {
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
       const int row = 4 * g + (lane >> 3);
       *reinterpret_cast<uint4*>(group + VATOMS * KV_ATOM + row * 128 + (((lane & 7) ^ row) << 4)) = h.rope[g];
     }
+  }
 }
 
 // A dequantisation warp's loop over a unit's blocks: block b is written while the rows of the next
@@ -327,6 +337,10 @@ __device__ __forceinline__ void run_dequant(const Rows<kWin>& rows, const uint8_
   constexpr uint32_t TB = kS ? K_TILE : V_TILE;
   const int own = RW * wq + (lane & 7);
   bool missing = false;
+  // slots of the ring: the next one to fill, and the next one to read
+  const uint32_t ring0 = smem_u32(ring) + (lane >> 3) * REC + 16 * (lane & 7), ring_end = ring0 + ND * RW * REC;
+  uint32_t fill = ring0;
+  const uint8_t* read = ring;
   auto start = [&](int32_t raw, int b) {  // the copies of block b (one group of copies, empty past the end)
     if (b < nblk) {
       const int j = BJ * b + own;
@@ -336,7 +350,9 @@ __device__ __forceinline__ void run_dequant(const Rows<kWin>& rows, const uint8_
         const uint32_t mask = __ballot_sync(0xffffffffu, y >= 0);
         if (lane == 0) masks[((done + b) % MASKS) * NDEQ + wq] = (uint8_t)mask;
       }
-      copy_rows<REC>(smem_u32(ring + ((done + b) % ND) * (RW * REC)), y, pool, lane);
+      copy_rows<REC>(fill, y, pool, lane);
+      fill += RW * REC;
+      if (fill == ring_end) fill = ring0;
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
@@ -352,7 +368,8 @@ __device__ __forceinline__ void run_dequant(const Rows<kWin>& rows, const uint8_
     t3 = rows.raw(BJ * (b + ND + 1) + own);
     asm volatile("cp.async.wait_group %0;" ::"n"(ND - 1) : "memory");
     __syncwarp();
-    const Held held = read_rows<kS>(ring + (g % ND) * (RW * REC), lane);
+    const Held held = read_rows<kS>(read, lane);
+    read = read + RW * REC == ring + ND * RW * REC ? ring : read + RW * REC;
     bool ok = true;
     if (kS && b == 0) ok = ready_or_wait(&bs.q_full, 1, (int)q_phase, abort);
     if (g >= NT) ok = ok && ready_or_wait(bs.tile_free, NT, g - NT, abort);
