@@ -85,9 +85,11 @@ constexpr uint32_t S_END = S_MASK + MASKS * NDEQ;
 constexpr uint32_t O_TILES = 0, O_RAW = NT * V_TILE;
 constexpr uint32_t O_P = (O_RAW + NDEQ * O_RING + 1023u) & ~1023u;
 constexpr uint32_t P_BUF = MH * BJ * 2, P_BYTES = P_BUF + MH * 4;  // P and the rescale factors of a block
+constexpr uint32_t FIN_BYTES = 2 * MH * 4;       // a unit's sums and references
 constexpr uint32_t O_ALPHA = O_P + 2 * P_BUF;
 constexpr uint32_t O_FIN = O_ALPHA + 2 * MH * 4;
-constexpr uint32_t O_END = O_FIN + 2 * 2 * MH * 4;  // two tiles' totals
+constexpr int NF = 4;                           // units whose totals are kept: the S-CTA is at most two ahead (P's buffers)
+constexpr uint32_t O_END = O_FIN + NF * FIN_BYTES;
 constexpr uint32_t SMEM_BYTES = (S_END > O_END ? S_END : O_END) + 1024;  // + alignment slack
 static_assert(SMEM_BYTES <= 227 * 1024 - 1024, "shared memory of a CTA");
 constexpr float kRescaleLog2 = 8.f;  // a reference maximum stays until it is passed by 2^8: P < 2^8
@@ -108,7 +110,7 @@ struct Barriers {
   uint64_t p_full[2];                     // O-CTA, completed by the S-CTA's stores
   uint64_t pv_go[2];                      // O-CTA: O is ready for P . V of the block
   uint64_t mma_done;                      // O-CTA: the MMAs issued so far are done
-  uint64_t fin[2];                        // O-CTA: the S-CTA's totals of a tile are here
+  uint64_t fin[NF];                       // O-CTA: the S-CTA's totals of a unit are here
 };
 
 // The kernel's roles run side by side from one instruction cache, and much of their time goes into
@@ -330,13 +332,13 @@ __device__ __forceinline__ void write_rows(const Held& h, uint8_t* group, int la
 // (places in rings go on from unit to unit). In the S-CTA it waits, before its first tile write, until Q
 // has left the staging area, and tells the softmax which of its rows exist.
 template <bool kS, bool kWin>
-__device__ __forceinline__ void run_dequant(const Rows<kWin>& rows, const uint8_t* __restrict__ pool, int nblk, int done,
+__device__ __forceinline__ bool run_dequant(const Rows<kWin>& rows, const uint8_t* __restrict__ pool, int nblk, int done,
                                             uint32_t q_phase, uint8_t* ring, uint8_t* masks, uint8_t* tiles,
                                             Barriers& bs, int wq, int lane, uint32_t* err, volatile int* abort) {
   constexpr int REC = kS ? S_REC : O_REC;
   constexpr uint32_t TB = kS ? K_TILE : V_TILE;
   const int own = RW * wq + (lane & 7);
-  bool missing = false;
+  bool missing = false, ok = true;
   // slots of the ring: the next one to fill, and the next one to read
   const uint32_t ring0 = smem_u32(ring) + (lane >> 3) * REC + 16 * (lane & 7), ring_end = ring0 + ND * RW * REC;
   uint32_t fill = ring0;
@@ -370,10 +372,10 @@ __device__ __forceinline__ void run_dequant(const Rows<kWin>& rows, const uint8_
     __syncwarp();
     const Held held = read_rows<kS>(read, lane);
     read = read + RW * REC == ring + ND * RW * REC ? ring : read + RW * REC;
-    bool ok = true;
     if (kS && b == 0) ok = ready_or_wait(&bs.q_full, 1, (int)q_phase, abort);
     if (g >= NT) ok = ok && ready_or_wait(bs.tile_free, NT, g - NT, abort);
-    if (!__all_sync(0xffffffffu, ok)) break;  // (and the slot has been read)
+    ok = __all_sync(0xffffffffu, ok);  // (and the slot has been read)
+    if (!ok) break;
     write_rows<kS>(held, tiles + (g % NT) * TB + wq * 1024, lane);
     __syncwarp();  // (the issuer has the proxy fence: here it would wait for the copies in flight too)
     if (lane == 0) bar_arrive(&bs.tile_full[g % NT]);
@@ -381,6 +383,7 @@ __device__ __forceinline__ void run_dequant(const Rows<kWin>& rows, const uint8_
   asm volatile("cp.async.wait_all;" ::: "memory");  // none is left in flight at the end
   __syncwarp();
   if (kS && kWin && __any_sync(0xffffffffu, missing) && lane == 0) atomicOr(err, HS_FLAG_DEVROW);
+  return ok;
 }
 
 // The dequantisation warp that CTA warp w is, of those that begin with warp `first` (first % 4 = 1);
@@ -460,6 +463,13 @@ __device__ __forceinline__ void request_q(const CUtensorMap* tm_q, size_t row0, 
   }
 }
 
+// The same boxes into L2, a unit ahead.
+__device__ __forceinline__ void prefetch_q(const CUtensorMap* tm_q, size_t row0) {
+  for (int bx = 0; bx < KATOMS; ++bx)
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];" ::"l"(tm_q), "r"(64 * bx), "r"((int)row0)
+                 : "memory");
+}
+
 template <bool kWin>
 __global__ void __launch_bounds__(T, 1)
     fp4_mla_kernel(const Fp4MlaArgs a, int tiles_per_request, int queries_per_tile, int units,
@@ -494,8 +504,8 @@ __global__ void __launch_bounds__(T, 1)
     for (int k = 0; k < 2; ++k) {
       bar_init(&bs.p_full[k], 1);  // the O-CTA's expect_tx; the S-CTA's stores complete it
       bar_init(&bs.pv_go[k], 4);
-      bar_init(&bs.fin[k], 4);
     }
+    for (int k = 0; k < NF; ++k) bar_init(&bs.fin[k], 1);  // the same
     s_abort = 0;
     s_issued = 0;
     s_requested = 0;
@@ -508,6 +518,7 @@ __global__ void __launch_bounds__(T, 1)
       }
     } else {
       for (int k = 0; k < 2; ++k) bar_arrive_tx(&bs.p_full[k], P_BYTES);
+      for (int k = 0; k < NF; ++k) bar_arrive_tx(&bs.fin[k], FIN_BYTES);
     }
   }
   if (warp == 0) {
@@ -527,12 +538,13 @@ __global__ void __launch_bounds__(T, 1)
   const int head = (warp & 3) * 32 + lane;  // this thread's row of the tile = its tensor-memory lane
   uint8_t* masks = base + S_MASK;
 
-  // The units of this pair, one after the other. The two CTAs run on by themselves: the S-CTA is at the
-  // next unit's first blocks while the O-CTA still writes the last one's output.
-  int done = 0, full = 0;  // blocks, and units with blocks, before this one
+  // The units of this pair, one after the other. In the S-CTA each role goes through them by itself
+  // (what they hand each other carries on from unit to unit); the O-CTA reads out with all its warps
+  // between two units.
   bool ok = true;
+  int done = 0, full = 0;  // blocks, and units with blocks, before this one
 #pragma unroll 1
-  for (int u = blockIdx.x >> 1; u < units; u += pairs) {
+  for (int u = blockIdx.x >> 1; ok && u < units; u += pairs) {
     const Unit<kWin> un = unit_of<kWin>(a, u, tiles_per_request, queries_per_tile, tid == 0, err);
     const int nblk = un.nblk;
     if (rank == 0) {
@@ -687,15 +699,33 @@ __global__ void __launch_bounds__(T, 1)
           if (lane == 0) bar_arrive(&bs.s_free[wg]);  // S has been read
           l_own += sum.x + sum.y;
         }
+        // the warpgroups' sums under the last block's reference, and that, to the O-CTA
+        sync_n(4 * NS * 32);
+        float* sums = reinterpret_cast<float*>(base + S_SUMS);
+        const float m = s_ref[head];
         if (wg > 0) {
-          float* sums = reinterpret_cast<float*>(base + S_SUMS) + 2 * (wg - 1) * MH;
-          sums[head] = l_own;
-          sums[MH + head] = m_own;
+          sums[2 * (wg - 1) * MH + head] = l_own;
+          sums[(2 * wg - 1) * MH + head] = m_own;
+        }
+        ok = sync_and(!*abort, 4 * NS * 32);  // (all softmax warps leave together)
+        if (wg == 0 && nblk > 0) {
+          const auto part = [&](float l, float mo) { return m == -INFINITY ? l : l * ex2(mo - m); };
+          float l = part(l_own, m_own);
+          for (int k = 0; k < NS - 1; ++k) l += part(sums[2 * k * MH + head], sums[(2 * k + 1) * MH + head]);
+          const uint32_t fin = remote(base + O_FIN, partner) + (full % NF) * FIN_BYTES;
+          const uint32_t bar = remote(&bs.fin[full % NF], partner);
+          st_async_f32(fin + 4 * head, l, bar);
+          st_async_f32(fin + 4 * (MH + head), m, bar);
         }
       } else if (warp == S_ISSUER) {
         // (tensor memory starts at 0: all of it is allocated here)
         const bool one = elected();
         const uint64_t k0 = mdesc(smem_u32(base + S_TILES), 16, 1024);
+        const bool more = u + pairs < units;
+        Unit<kWin> next;
+        next.nblk = 0;
+        if (more) next = unit_of<kWin>(a, u + pairs, tiles_per_request, queries_per_tile, false, err);
+        if (one && next.nblk > 0) prefetch_q(&tm_q, next.row0);
         bool go = __all_sync(0xffffffffu, nblk == 0 || ready_or_wait(&bs.q_full, 1, (int)q_phase, abort));
 #pragma unroll 1
         for (int b = 0; go && b < nblk; ++b) {
@@ -720,37 +750,20 @@ __global__ void __launch_bounds__(T, 1)
           __syncwarp();
         }
         // the next unit's Q, once this one's MMAs have read the tiles that it is staged over
-        if (go && u + pairs < units) {
-          const Unit<kWin> next = unit_of<kWin>(a, u + pairs, tiles_per_request, queries_per_tile, false, err);
-          if (next.nblk > 0) {
-            const int last = done + nblk - 1;
-            go = __all_sync(0xffffffffu, last < 0 || ready_or_wait(bs.tile_free, NT, last, abort));
-            if (go && one) {
-              request_q(&tm_q, next.row0, base, bs);
-              ++s_requested;
-            }
-            __syncwarp();
+        if (go && next.nblk > 0) {
+          const int last = done + nblk - 1;
+          go = __all_sync(0xffffffffu, last < 0 || ready_or_wait(bs.tile_free, NT, last, abort));
+          if (go && one) {
+            request_q(&tm_q, next.row0, base, bs);
+            ++s_requested;
           }
+          __syncwarp();
         }
+        ok = go;
       } else if (const int wq = deq_warp(warp, S_DEQ0); wq >= 0) {
-        run_dequant<true, kWin>(un.rows, a.pool, nblk, done, q_phase, base + S_RAW + wq * S_RING, masks, tiles, bs, wq,
-                                lane, err, abort);
+        ok = run_dequant<true, kWin>(un.rows, a.pool, nblk, done, q_phase, base + S_RAW + wq * S_RING, masks, tiles, bs, wq,
+                                     lane, err, abort);
       }
-      __syncthreads();
-      if (nblk > 0 && warp < 4) {
-        // the warpgroups' sums under the last block's reference, and that, to the O-CTA
-        const float* sums = reinterpret_cast<const float*>(base + S_SUMS);
-        const float m = reinterpret_cast<const float*>(base + S_REF)[head];
-        const auto part = [&](float l, float mo) { return m == -INFINITY ? l : l * ex2(mo - m); };
-        float l = part(l_own, m_own);
-        for (int g = 0; g < NS - 1; ++g) l += part(sums[2 * g * MH + head], sums[(2 * g + 1) * MH + head]);
-        const uint32_t fin = remote(base + O_FIN, partner) + (full & 1) * (2 * MH * 4);
-        st_remote_f32(fin + 4 * head, l);
-        st_remote_f32(fin + 4 * (MH + head), m);
-        __syncwarp();
-        if (lane == 0) bar_arrive_remote(remote(&bs.fin[full & 1], partner));
-      }
-      ok = __syncthreads_and(!*abort);
     } else {
       // ================================ O-CTA ================================
       uint8_t* tiles = base + O_TILES;
@@ -816,7 +829,7 @@ __global__ void __launch_bounds__(T, 1)
       ok = !*abort;
       if (nblk > 0)
         ok = ok && ready_or_wait(bs.tile_free, NT, done + nblk - 1, abort) &&
-             ready_or_wait<true>(&bs.fin[full & 1], 1, (full >> 1) & 1, abort);
+             ready_or_wait<true>(bs.fin, NF, full, abort);
       ok = __syncthreads_and(ok && !*abort);
       tc_after();
       if (ok && warp < 16) {
@@ -824,7 +837,7 @@ __global__ void __launch_bounds__(T, 1)
         // are staged in shared memory, 1024 bytes of each (all of a bf16 row; half of a row of partial
         // sums, in two passes) and leave by one bulk copy a row.
         const bool direct = a.splits == 1;
-        const float* fin = reinterpret_cast<const float*>(base + O_FIN) + (full & 1) * 2 * MH;
+        const float* fin = reinterpret_cast<const float*>(base + O_FIN) + (full % NF) * 2 * MH;
         const float l = nblk > 0 ? fin[head] : 0.f, m = nblk > 0 ? fin[MH + head] : -INFINITY;
         const float inv = l == 0.f ? 0.f : a.latent_scale / l;  // l is NaN where a weight is
         uint8_t* stg = base + O_TILES + head * EPI_PITCH + (warp >> 2) * 256;
@@ -862,30 +875,30 @@ __global__ void __launch_bounds__(T, 1)
           }
           fence_async_smem();  // the staged rows, before the copies read them
           sync_n(512);
-          if (warp < 4) {
-            if (head < un.live) {
-              const void* dst = direct ? static_cast<const void*>(a.o + (out0 + head) * DL)
-                                       : static_cast<const void*>(part_o + (out0 + head) * DL + pass * (DL / 2));
-              asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst),
-                           "r"(smem_u32(base + O_TILES + head * EPI_PITCH)), "r"(1024)
-                           : "memory");
-            }
-            asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
+          const int row = 8 * warp + lane;
+          if (lane < 8 && row < un.live) {
+            const void* dst = direct ? static_cast<const void*>(a.o + (out0 + row) * DL)
+                                     : static_cast<const void*>(part_o + (out0 + row) * DL + pass * (DL / 2));
+            asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst),
+                         "r"(smem_u32(base + O_TILES + row * EPI_PITCH)), "r"(1024)
+                         : "memory");
           }
+          asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
           sync_n(512);  // the staging may be written again
         }
         if (head < un.live && warp < 4)
           (direct ? a.lse : part_lse)[out0 + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
       }
       tc_before();
-      __syncthreads();  // O and the staging are free for the next unit
+      __syncthreads();  // O, the totals and the staging are free for the next units
       tc_after();
+      if (tid == 0 && nblk > 0) bar_arrive_tx(&bs.fin[full % NF], FIN_BYTES);
     }
-    if (!ok) break;
     done += nblk;
     full += nblk > 0;
   }
 
+  __syncthreads();
   // the S-CTA's MMAs are done (the O-CTA's are, unit by unit), and it has the O-CTA's last P-buffer
   // releases (its last arrivals here)
   if (rank == 0 && ok) {
