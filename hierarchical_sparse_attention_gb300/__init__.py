@@ -176,27 +176,31 @@ def _addr(x) -> Optional[int]:
     raise TypeError(f"cannot take the address of {type(x).__name__}")
 
 
-def _dev(x, rows: bool = False) -> Optional[int]:
-    """_addr of a device array, which has to be on the current device (a raw address is taken as it is).
-    rows: a 2-D array whose rows may be apart (the call says how far)."""
-    if x is None or isinstance(x, int):
-        return x
-    if not getattr(x, "is_cuda", False):
-        raise ValueError("this argument is read or written on the GPU: pass a CUDA tensor or a device address")
-    import torch
-    if x.device.index != torch.cuda.current_device():
-        raise ValueError(f"the tensor is on {x.device}, the current device is cuda:{torch.cuda.current_device()}")
-    if rows:
-        if x.dim() != 2 or x.stride(1) != 1:
-            raise ValueError("rows of consecutive values are needed")
-        return x.data_ptr()
-    return _addr(x)
-
-
-def _rows_of(x, stride: int) -> Optional[int]:
-    if not (x is None or isinstance(x, int)) and x.dim() == 2 and x.size(0) > 1 and x.stride(0) != stride:
-        raise ValueError(f"the rows are {x.stride(0)} values apart, not {stride}")
-    return _dev(x, rows=True)
+def _on_gpu(*xs, stride: Optional[int] = None):
+    """Addresses of contiguous arrays, which have to be on the current device (None and raw addresses are taken
+    as they are). stride: the first one is 2-D with rows of consecutive values that far apart instead."""
+    out, here = [], None
+    for i, x in enumerate(xs):
+        if x is None or isinstance(x, int):
+            out.append(x)
+            continue
+        on = x.get_device() if hasattr(x, "get_device") else -1
+        if on < 0:
+            raise ValueError("this argument is read or written on the GPU: pass a CUDA tensor or a device address")
+        if here is None:
+            import torch
+            here = torch.cuda.current_device()
+        if on != here:
+            raise ValueError(f"the tensor is on cuda:{on}, the current device is cuda:{here}")
+        if i == 0 and stride is not None:
+            if x.dim() != 2 or x.stride(1) != 1:
+                raise ValueError("rows of consecutive values are needed")
+            if x.size(0) > 1 and x.stride(0) != stride:
+                raise ValueError(f"the rows are {x.stride(0)} values apart, not {stride}")
+        elif not x.is_contiguous():
+            raise ValueError("arrays passed to libhs must be contiguous")
+        out.append(x.data_ptr())
+    return out
 
 
 def _stream(s) -> Optional[int]:
@@ -348,15 +352,17 @@ def hs_sparse_mla_decode(num_requests: int, num_heads: int, top_k: int, splits: 
 def hs_fp4_pack_rows(n: int, kv, kv_stride: int, rows, latent_scale: float, pool, pool_rows: int, error_flags,
                      stream=None) -> None:
     """Quantise n tokens (bf16 [n, kv_stride], 576 used) into the 4-bit rows `rows` of the pool."""
-    _check(_lib.hs_fp4_pack_rows(n, _rows_of(kv, kv_stride), kv_stride, _dev(rows), latent_scale, _dev(pool),
-                                 pool_rows, _dev(error_flags), _stream(stream)), "hs_fp4_pack_rows")
+    kv, rows, pool, error_flags = _on_gpu(kv, rows, pool, error_flags, stride=kv_stride)
+    _check(_lib.hs_fp4_pack_rows(n, kv, kv_stride, rows, latent_scale, pool, pool_rows, error_flags, _stream(stream)),
+           "hs_fp4_pack_rows")
 
 
 def hs_fp4_unpack_rows(n: int, pool, pool_rows: int, rows, latent_scale: float, kv, kv_stride: int, error_flags,
                        stream=None) -> None:
     """Read the 4-bit rows `rows` back as bf16 into kv ([n, kv_stride], 576 written)."""
-    _check(_lib.hs_fp4_unpack_rows(n, _dev(pool), pool_rows, _dev(rows), latent_scale, _rows_of(kv, kv_stride),
-                                   kv_stride, _dev(error_flags), _stream(stream)), "hs_fp4_unpack_rows")
+    kv, pool, rows, error_flags = _on_gpu(kv, pool, rows, error_flags, stride=kv_stride)
+    _check(_lib.hs_fp4_unpack_rows(n, pool, pool_rows, rows, latent_scale, kv, kv_stride, error_flags,
+                                   _stream(stream)), "hs_fp4_unpack_rows")
 
 
 def hs_fp4_mla_splits(num_requests: int, num_heads: int, num_queries: int, rows: int) -> int:
@@ -371,21 +377,22 @@ def hs_fp4_mla_workspace_bytes(num_requests: int, num_heads: int, num_queries: i
 def hs_fp4_sparse_mla_decode(num_requests: int, num_heads: int, top_k: int, splits: int, q, kv_pool, pool_rows: int,
                              out_rows, sm_scale: float, latent_scale: float, o, lse, workspace, workspace_bytes: int,
                              error_flags, stream=None) -> None:
-    _check(_lib.hs_fp4_sparse_mla_decode(num_requests, num_heads, top_k, splits, _dev(q), _dev(kv_pool), pool_rows,
-                                         _dev(out_rows), sm_scale, latent_scale, _dev(o), _dev(lse), _dev(workspace),
-                                         workspace_bytes, _dev(error_flags), _stream(stream)),
-           "hs_fp4_sparse_mla_decode")
+    q, kv_pool, out_rows, o, lse, workspace, error_flags = _on_gpu(q, kv_pool, out_rows, o, lse, workspace, error_flags)
+    _check(_lib.hs_fp4_sparse_mla_decode(num_requests, num_heads, top_k, splits, q, kv_pool, pool_rows, out_rows,
+                                         sm_scale, latent_scale, o, lse, workspace, workspace_bytes, error_flags,
+                                         _stream(stream)), "hs_fp4_sparse_mla_decode")
 
 
 def hs_fp4_window_mla_decode(num_requests: int, num_heads: int, num_queries: int, window: int, sinks: int,
                              splits: int, q, kv_pool, pool_rows: int, page_size: int, max_pages: int, seq_lens,
                              resident_pages, sm_scale: float, latent_scale: float, o, lse, workspace,
                              workspace_bytes: int, error_flags, stream=None) -> None:
-    _check(_lib.hs_fp4_window_mla_decode(num_requests, num_heads, num_queries, window, sinks, splits, _dev(q),
-                                         _dev(kv_pool), pool_rows, page_size, max_pages, _dev(seq_lens),
-                                         _dev(resident_pages), sm_scale, latent_scale, _dev(o), _dev(lse),
-                                         _dev(workspace), workspace_bytes, _dev(error_flags), _stream(stream)),
-           "hs_fp4_window_mla_decode")
+    q, kv_pool, seq_lens, resident_pages, o, lse, workspace, error_flags = _on_gpu(
+        q, kv_pool, seq_lens, resident_pages, o, lse, workspace, error_flags)
+    _check(_lib.hs_fp4_window_mla_decode(num_requests, num_heads, num_queries, window, sinks, splits, q, kv_pool,
+                                         pool_rows, page_size, max_pages, seq_lens, resident_pages, sm_scale,
+                                         latent_scale, o, lse, workspace, workspace_bytes, error_flags,
+                                         _stream(stream)), "hs_fp4_window_mla_decode")
 
 
 def hs_pages_workspace_bytes(num_requests: int, num_pages: int) -> int:
@@ -398,9 +405,9 @@ def make_page_pool(device_pools: Sequence, num_requests: int, max_pages: int, nu
     """The descriptor of the hs_pages_* calls. It keeps the tensors that it points to alive."""
     if not 1 <= len(device_pools) <= HS_MAX_LAYERS:
         raise ValueError(f"1 to {HS_MAX_LAYERS} device pools")
-    arrays = [_dev(x) for x in (resident_pages, page_refs, free_pages, free_count, error_flags, workspace)]
+    arrays = _on_gpu(resident_pages, page_refs, free_pages, free_count, error_flags, workspace)
     p = hs_page_pool(num_requests, max_pages, num_pages, page_size, row_bytes, len(device_pools),
-                     (ctypes.c_void_p * HS_MAX_LAYERS)(*[_dev(x) for x in device_pools]), *arrays, workspace_bytes)
+                     (ctypes.c_void_p * HS_MAX_LAYERS)(*_on_gpu(*device_pools)), *arrays, workspace_bytes)
     p.kept = (list(device_pools), resident_pages, page_refs, free_pages, free_count, error_flags, workspace)
     return p
 
@@ -410,17 +417,17 @@ def hs_pages_init(pool: hs_page_pool, stream=None) -> None:
 
 
 def hs_pages_extend(pool: hs_page_pool, n: int, requests, old_lens, new_lens, granted=None, stream=None) -> None:
-    _check(_lib.hs_pages_extend(pool, n, _dev(requests), _dev(old_lens), _dev(new_lens), _dev(granted),
-                                _stream(stream)), "hs_pages_extend")
+    _check(_lib.hs_pages_extend(pool, n, *_on_gpu(requests, old_lens, new_lens, granted), _stream(stream)),
+           "hs_pages_extend")
 
 
 def hs_pages_fork(pool: hs_page_pool, n: int, parents, children, lens, granted=None, stream=None) -> None:
-    _check(_lib.hs_pages_fork(pool, n, _dev(parents), _dev(children), _dev(lens), _dev(granted), _stream(stream)),
+    _check(_lib.hs_pages_fork(pool, n, *_on_gpu(parents, children, lens, granted), _stream(stream)),
            "hs_pages_fork")
 
 
 def hs_pages_free(pool: hs_page_pool, n: int, requests, first_pages=None, end_pages=None, stream=None) -> None:
-    _check(_lib.hs_pages_free(pool, n, _dev(requests), _dev(first_pages), _dev(end_pages), _stream(stream)),
+    _check(_lib.hs_pages_free(pool, n, *_on_gpu(requests, first_pages, end_pages), _stream(stream)),
            "hs_pages_free")
 
 
