@@ -24,19 +24,22 @@ constexpr int kFp4RopeAt = kFp4Scales + kFp4Latent / kFp4Block;
 constexpr int kFp4Row = kFp4RopeAt + 2 * kFp4Rope;
 static_assert(kFp4Row == HS_FP4_ROW_BYTES, "the record and the header agree");
 
-// A launch that returns its own error (cudaGetLastError could hand back another call's).
-// pdl: a programmatic dependent of the kernel before it, which waits (griddepcontrol.wait) itself.
+// A launch as a programmatic dependent of the kernel before it, which saves the gap between the two:
+// every kernel launched so begins with pdl_wait(), in every thread. Returns its own error
+// (cudaGetLastError could hand back another call's).
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 template <typename... P, typename... A>
-cudaError_t launch(void (*kernel)(P...), dim3 grid, unsigned threads, cudaStream_t stream, bool pdl, A... args) {
+cudaError_t launch(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t stream, A... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = pdl ? 1 : 0;
+  cfg.numAttrs = 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
   if (e != cudaSuccess) (void)cudaGetLastError();
   return e;

@@ -510,6 +510,7 @@ __global__ void __launch_bounds__(T, 1)
     s_issued = 0;
     s_requested = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    pdl_wait();
     if (rank == 0) {
       const Unit<kWin> first = unit_of<kWin>(a, blockIdx.x >> 1, tiles_per_request, queries_per_tile, false, err);
       if (first.nblk > 0) {
@@ -521,7 +522,7 @@ __global__ void __launch_bounds__(T, 1)
       for (int k = 0; k < NF; ++k) bar_arrive_tx(&bs.fin[k], FIN_BYTES);
     }
   }
-  if (warp == 0) {
+  if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_taddr)),
                  "r"(TMEM_COLS)
                  : "memory");
@@ -533,6 +534,7 @@ __global__ void __launch_bounds__(T, 1)
   // both CTAs' barriers are initialised before either arrives on the other's (the initialiser's fence
   // makes them visible: the barrier itself need not wait for anything)
   asm volatile("barrier.cluster.arrive.relaxed;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+  pdl_wait();
   const uint32_t tbase = s_taddr;
   const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
   const int head = (warp & 3) * 32 + lane;  // this thread's row of the tile = its tensor-memory lane
@@ -925,7 +927,7 @@ __global__ void __launch_bounds__(T, 1)
   }
   tc_before();
   __syncthreads();
-  if (warp == 0)
+  if (warp == 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tbase), "r"(TMEM_COLS) : "memory");
   // the merge kernel (if any) may launch; it waits for this grid's completion before reading
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -937,7 +939,7 @@ __global__ void __launch_bounds__(T, 1)
 constexpr int COMBINE_T = 256;
 __global__ void __launch_bounds__(COMBINE_T)
     fp4_combine_kernel(const Fp4MlaArgs a, int rows, const float* __restrict__ part_o, const float* __restrict__ part_lse) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  pdl_wait();
   const int64_t g = (int64_t)blockIdx.x * COMBINE_T + threadIdx.x;
   const int64_t row = g >> 7;
   const int c4 = (int)(g & 127);
@@ -1007,15 +1009,21 @@ int tiles_per_request(int num_heads, int num_queries) {
 
 }  // namespace
 
+// In tenths of a block's time (1.3 us): a wave of units takes their blocks and 5 blocks' time around
+// them; splitting at all adds 4 (partial outputs in 32 bits, the merge kernel and its launch), and 4
+// more per unit and pair for the partials' traffic. Measured (us, 128 heads, 2,048 rows): one request
+// 51 whole, 28 in 4 splits, 23 in 12; 16 requests 53, 32 in 4, 46 in 6 (two waves); 32 requests 52,
+// 43 in 2, 59 in 3 (two waves); 64 requests 56, 78 in 2. Of 512 rows: 8 requests 24, 22 in 4; 32
+// requests 24, 28 in 2.
 int32_t fp4_mla_splits(int32_t num_requests, int32_t num_heads, int32_t num_queries, int64_t rows) {
   int slots = 0;
   if (pairs_resident(&slots) != cudaSuccess) return 1;
-  const int64_t pairs = (int64_t)num_requests * tiles_per_request(num_heads, num_queries);
+  const int64_t tiles = (int64_t)num_requests * tiles_per_request(num_heads, num_queries);
   const int64_t blocks = (rows + BJ - 1) / BJ;
   int64_t best = 1, best_cost = INT64_MAX;
   for (int64_t s = 1; s <= HS_MAX_MLA_SPLITS && s <= blocks; ++s) {
-    const int64_t waves = (pairs * s + slots - 1) / slots;
-    const int64_t cost = waves * ((blocks + s - 1) / s + 6) + (s > 1 ? 3 + s : 0);
+    const int64_t units = tiles * s, waves = (units + slots - 1) / slots;
+    const int64_t cost = 10 * waves * ((blocks + s - 1) / s + 5) + (s > 1 ? 40 + 40 * units / slots : 0);
     if (cost < best_cost) {
       best = s;
       best_cost = cost;
@@ -1050,13 +1058,15 @@ cudaError_t launch_fp4_mla(const Fp4MlaArgs& a, int32_t num_requests, float* par
   cfg.blockDim = dim3(T);
   cfg.dynamicSmemBytes = SMEM_BYTES;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.numAttrs = 2;
   e = cudaLaunchKernelEx(&cfg, kernel, a, tiles, g, units, tm_q, part, part_lse, err);
   if (e != cudaSuccess) {
     (void)cudaGetLastError();
@@ -1064,7 +1074,7 @@ cudaError_t launch_fp4_mla(const Fp4MlaArgs& a, int32_t num_requests, float* par
   }
   if (a.splits == 1) return cudaSuccess;
   return launch(fp4_combine_kernel, dim3((unsigned)(((int64_t)rows * (DL / 4) + COMBINE_T - 1) / COMBINE_T)), COMBINE_T,
-                stream, true, a, rows, (const float*)part, (const float*)part_lse);
+                0, stream, a, rows, (const float*)part, (const float*)part_lse);
 }
 
 }  // namespace hs

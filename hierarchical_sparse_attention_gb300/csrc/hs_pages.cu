@@ -7,6 +7,7 @@
 // arguments and the state alone: grants go by prefix sums over the entries in their order, pages
 // are pushed and packed in the order of their numbers, and the atomics only add, clear or set.
 #include "hs_fp4.h"
+#include "hs_tcgen05.cuh"
 
 namespace hs {
 namespace {
@@ -55,7 +56,6 @@ PageWork work_of(const hs_page_pool& p) {
 // stream, and it reads both before its wait (a programmatic dependent), so each thread makes what
 // it wrote visible before it exits.
 __device__ __forceinline__ void show_writes() { __threadfence(); }
-__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Exclusive prefix sum of v over the CTA's kPlanThreads threads; *total gets the sum. Called by
 // every thread; sums are 64-bit (entries x pages passes 32).
@@ -106,6 +106,7 @@ __device__ __forceinline__ int32_t pop(const hs_page_pool& p, int32_t height, in
 }
 
 __global__ void pages_init_kernel(const hs_page_pool p, const PageWork w) {
+  pdl_wait();
   const int64_t step = (int64_t)gridDim.x * blockDim.x, t = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   for (int64_t i = t; i < (int64_t)p.num_requests * p.max_pages; i += step) p.resident_pages[i] = -1;
   for (int64_t i = t; i < p.num_pages; i += step) {
@@ -133,6 +134,7 @@ __global__ void __launch_bounds__(kPlanThreads)
   const int tid = threadIdx.x;
   const int words = (p.num_requests + 31) / 32;
   for (int i = tid; i < words; i += kPlanThreads) s_once[i] = s_twice[i] = 0;
+  pdl_wait();
   __syncthreads();
   for (int i = tid; i < n; i += kPlanThreads) {
     const int32_t r = requests[i];
@@ -219,6 +221,7 @@ __global__ void __launch_bounds__(kPlanThreads)
   __shared__ uint32_t s_once[kMaxRequests / 32], s_twice[kMaxRequests / 32], s_parent[kMaxRequests / 32];
   __shared__ uint32_t s_last;
   const int tid = threadIdx.x;
+  pdl_wait();
   {
     const int32_t c = children[blockIdx.x];
     int held = 0;
@@ -352,6 +355,7 @@ __global__ void __launch_bounds__(kPageThreads)
 __global__ void __launch_bounds__(kPageThreads)
     pages_drop_kernel(const hs_page_pool p, const PageWork w, const int32_t* __restrict__ requests,
                       const int32_t* __restrict__ first_pages, const int32_t* __restrict__ end_pages) {
+  pdl_wait();
   const int i = blockIdx.x;
   const int32_t r = requests[i];
   if (r < 0) return;
@@ -409,17 +413,20 @@ __global__ void __launch_bounds__(kPlanThreads) pages_push_kernel(const hs_page_
 // One CTA, a strip of pages per warp: the live pages are counted, those past the live count get
 // the free pages among the first ones, both in the order of their numbers.
 __global__ void __launch_bounds__(kPlanThreads) pages_compact_plan_kernel(const hs_page_pool p, const PageWork w) {
+  pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t strip = ((int64_t)p.num_pages + kPlanThreads - 1) / kPlanThreads * 32;
   const int64_t lo = min(warp * strip, (int64_t)p.num_pages), hi = min(lo + strip, (int64_t)p.num_pages);
   const uint32_t below = (1u << lane) - 1;
   int64_t count = 0;
+#pragma unroll 8  // (the loads of a batch go out together)
   for (int64_t b = lo; b < hi; b += 32) count += __popc(__ballot_sync(~0u, b + lane < hi && p.page_refs[b + lane] > 0));
   int64_t live;
   int64_t before = block_prefix(lane == 0 ? count : 0, &live);  // live pages below the strip
   before = __shfl_sync(~0u, before, 0);
   // live pages among the first `live`: the rest of those are holes, as many as there are pages to move
   count = 0;
+#pragma unroll 8
   for (int64_t b = lo; b < min(hi, live); b += 32)
     count += __popc(__ballot_sync(~0u, b + lane < min(hi, live) && p.page_refs[b + lane] > 0));
   int64_t kept;
@@ -442,25 +449,114 @@ __global__ void __launch_bounds__(kPlanThreads) pages_compact_plan_kernel(const 
   }
 }
 
-constexpr int kSpan = 16384;  // bytes of a page that one CTA copies at a time
+constexpr int kSpan = 16384;  // bytes of a page that are copied at a time
+constexpr int kRing = 6;      // spans of a CTA's ring, two CTAs to an SM
 
-// Pages move, their counts with them; every table entry that names a moved page names its new
-// one; the stack holds the pages past the live ones, the lowest on top.
-__global__ void __launch_bounds__(kPageThreads) pages_compact_kernel(const PageArgs a, const PageWork w) {
-  pdl_wait();
-  const hs_page_pool& p = a.p;
-  const int64_t t = (int64_t)blockIdx.x * kPageThreads + threadIdx.x, step = (int64_t)gridDim.x * kPageThreads;
-  const int32_t moves = *w.moves, live = *w.live;
+// The copies of a compaction: span k of all of them.
+struct Span {
+  const uint8_t* src;
+  uint8_t* dst;
+  int bytes;
+};
+__device__ __forceinline__ Span span_of(const hs_page_pool& p, const PageWork& w, int64_t k) {
   const int64_t page = (int64_t)p.page_size * p.row_bytes;
   const int spans = (int)((page + kSpan - 1) / kSpan);
-  const int64_t tasks = (int64_t)moves * p.num_layers * spans;
-  for (int64_t k = blockIdx.x; k < tasks; k += gridDim.x) {
-    const int64_t at = k % spans * kSpan, rest = k / spans;
-    const int l = (int)(rest % p.num_layers);
-    const int64_t m = rest / p.num_layers;
-    uint8_t* pool = static_cast<uint8_t*>(p.device_pools[l]);
-    copy_span(pool + w.src[m] * page + at, pool + w.dst[m] * page + at, min((int64_t)kSpan, page - at), a.vec);
+  const int64_t at = k % spans * kSpan, rest = k / spans, m = rest / p.num_layers;
+  uint8_t* pool = static_cast<uint8_t*>(p.device_pools[rest % p.num_layers]);
+  return {pool + w.src[m] * page + at, pool + w.dst[m] * page + at, (int)min((int64_t)kSpan, page - at)};
+}
+
+// A warp's share of them through a ring in shared memory, by bulk copies in and out: nothing but
+// their issue costs instructions, and some 160 KB an SM are on their way.
+__device__ __forceinline__ void copy_through_ring(const hs_page_pool& p, const PageWork& w, uint8_t* ring, uint64_t* full,
+                                                  volatile int* abort, int64_t tasks, int lane) {
+  if (blockIdx.x >= tasks) return;
+  const int64_t n = (tasks - blockIdx.x + gridDim.x - 1) / gridDim.x;
+  int64_t loaded = 0;
+  Span ahead{};                    // lane l: span 32 (loaded / 32) + l of this CTA's
+  uint8_t* dst = nullptr;          // lane l: where the span in slot l goes
+  int bytes = 0;
+  auto load = [&](int64_t upto) {  // the loads of the spans before `upto`
+    for (; loaded < n && loaded < upto; ++loaded) {
+      const int from = (int)(loaded & 31), slot = (int)(loaded % kRing);
+      if (from == 0 && loaded + lane < n) ahead = span_of(p, w, blockIdx.x + (loaded + lane) * gridDim.x);
+      const uint64_t s = __shfl_sync(~0u, (uint64_t)ahead.src, from), d = __shfl_sync(~0u, (uint64_t)ahead.dst, from);
+      const int b = __shfl_sync(~0u, ahead.bytes, from);
+      if (lane == slot) {
+        dst = (uint8_t*)d;
+        bytes = b;
+      }
+      if (lane == 0) {
+        tc::bar_arrive_tx(&full[slot], (uint32_t)b);
+        asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                         tc::smem_u32(ring + slot * kSpan)),
+                     "l"(s), "r"(b), "r"(tc::smem_u32(&full[slot]))
+                     : "memory");
+      }
+    }
+  };
+  load(kRing);
+  for (int64_t i = 0; i < n; ++i) {
+    const int slot = (int)(i % kRing);
+    const bool here = __all_sync(~0u, tc::pipe_wait(&full[slot], 1, (int)(i / kRing & 1), abort));
+    const uint64_t d = __shfl_sync(~0u, (uint64_t)dst, slot);
+    const int b = __shfl_sync(~0u, bytes, slot);
+    if (!here) break;
+    if (lane == 0) {
+      asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(d), "r"(tc::smem_u32(ring + slot * kSpan)), "r"(b)
+                   : "memory");
+      // the span before has been read out of its slot, which takes the next one
+      asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 1;" ::: "memory");
+    }
+    __syncwarp();
+    load(i + kRing);  // (of slot (i - 1) % kRing, at most)
   }
+  if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+  if (*abort) {  // never met: the waits are bounded so that a kernel always ends
+    if (lane == 0) atomicOr(p.error_flags, HS_FLAG_TIMEOUT);
+    __syncwarp();
+    *abort = 0;
+    __syncwarp();
+    for (int64_t i = max((int64_t)0, loaded - kRing); i < loaded; ++i)  // copies in flight get one more bound
+      tc::pipe_wait(&full[i % kRing], 1, (int)(i / kRing & 1), abort);
+  }
+  __syncwarp();
+}
+
+// Pages move, their counts with them; every table entry that names a moved page names its new
+// one; the stack holds the pages past the live ones, the lowest on top. kBulk: pools and rows on
+// 16-byte boundaries; the first warp has the copies, the others the tables.
+template <bool kBulk>
+__global__ void __launch_bounds__(kPageThreads) pages_compact_kernel(const PageArgs a, const PageWork w) {
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ __align__(8) uint64_t full[kRing];
+  __shared__ int s_abort;
+  if (kBulk && threadIdx.x == 0) {
+    for (int k = 0; k < kRing; ++k) tc::bar_init(&full[k], 1);
+    s_abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  pdl_wait();
+  const hs_page_pool& p = a.p;
+  const int32_t moves = *w.moves, live = *w.live;
+  const int64_t page = (int64_t)p.page_size * p.row_bytes;
+  const int64_t tasks = (page + kSpan - 1) / kSpan * moves * p.num_layers;
+  int first = 0;  // the first thread of those that have the tables
+  if (kBulk) {
+    first = 32;
+    if (threadIdx.x < 32) {
+      __syncwarp();
+      copy_through_ring(p, w, ring, full, &s_abort, tasks, threadIdx.x);
+      show_writes();
+      return;
+    }
+  } else {
+    for (int64_t k = blockIdx.x; k < tasks; k += gridDim.x) {
+      const Span s = span_of(p, w, k);
+      copy_span(s.src, s.dst, s.bytes, a.vec);
+    }
+  }
+  const int64_t step = (int64_t)gridDim.x * (kPageThreads - first), t = (int64_t)blockIdx.x * (kPageThreads - first) + threadIdx.x - first;
   for (int64_t k = t; k < moves; k += step) {
     p.page_refs[w.dst[k]] = p.page_refs[w.src[k]];
     p.page_refs[w.src[k]] = 0;
@@ -494,21 +590,21 @@ cudaError_t launch_pages_init(const PageArgs& a, cudaStream_t stream) {
   const int64_t n = (int64_t)a.p.num_requests * a.p.max_pages;
   const int64_t most = n > a.p.num_pages ? n : a.p.num_pages;
   const unsigned grid = (unsigned)((most + kPageThreads - 1) / kPageThreads < 1216 ? (most + kPageThreads - 1) / kPageThreads : 1216);
-  return launch(pages_init_kernel, dim3(grid), kPageThreads, stream, false, a.p, work_of(a.p));
+  return launch(pages_init_kernel, dim3(grid), kPageThreads, 0, stream, a.p, work_of(a.p));
 }
 
 cudaError_t launch_pages_extend(const PageArgs& a, int32_t n, const int32_t* requests, const int32_t* old_lens,
                                 const int32_t* new_lens, int32_t* granted, cudaStream_t stream) {
-  return launch(pages_extend_kernel, dim3(1), kPlanThreads, stream, false, a.p, n, requests, old_lens, new_lens, granted);
+  return launch(pages_extend_kernel, dim3(1), kPlanThreads, 0, stream, a.p, n, requests, old_lens, new_lens, granted);
 }
 
 cudaError_t launch_pages_fork(const PageArgs& a, int32_t n, const int32_t* parents, const int32_t* children,
                               const int32_t* lens, int32_t* granted, cudaStream_t stream) {
   const PageWork w = work_of(a.p);
-  const cudaError_t e = launch(pages_fork_plan_kernel, dim3((unsigned)n), kPlanThreads, stream, false, a.p, w, n, parents,
+  const cudaError_t e = launch(pages_fork_plan_kernel, dim3((unsigned)n), kPlanThreads, 0, stream, a.p, w, n, parents,
                                children, lens, granted);
   if (e != cudaSuccess) return e;
-  return launch(pages_fork_kernel, dim3((unsigned)n, 1u + (unsigned)a.p.num_layers), kPageThreads, stream, true, a, w,
+  return launch(pages_fork_kernel, dim3((unsigned)n, 1u + (unsigned)a.p.num_layers), kPageThreads, 0, stream, a, w,
                 parents, children, lens);
 }
 
@@ -517,9 +613,9 @@ cudaError_t launch_pages_free(const PageArgs& a, int32_t n, const int32_t* reque
   const PageWork w = work_of(a.p);
   const int chunks = (a.p.max_pages + kPageThreads - 1) / kPageThreads;
   const cudaError_t e = launch(pages_drop_kernel, dim3((unsigned)n, (unsigned)(chunks < 64 ? chunks : 64)), kPageThreads,
-                               stream, false, a.p, w, requests, first_pages, end_pages);
+                               0, stream, a.p, w, requests, first_pages, end_pages);
   if (e != cudaSuccess) return e;
-  return launch(pages_push_kernel, dim3(1), kPlanThreads, stream, true, a.p, w);
+  return launch(pages_push_kernel, dim3(1), kPlanThreads, 0, stream, a.p, w);
 }
 
 cudaError_t launch_pages_compact(const PageArgs& a, cudaStream_t stream) {
@@ -527,8 +623,14 @@ cudaError_t launch_pages_compact(const PageArgs& a, cudaStream_t stream) {
   int sms = 0;
   cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return e;
-  if ((e = launch(pages_compact_plan_kernel, dim3(1), kPlanThreads, stream, false, a.p, w)) != cudaSuccess) return e;
-  return launch(pages_compact_kernel, dim3(4u * (unsigned)sms), kPageThreads, stream, true, a, w);
+  if ((e = launch(pages_compact_plan_kernel, dim3(1), kPlanThreads, 0, stream, a.p, w)) != cudaSuccess) return e;
+  if (a.vec < 16) return launch(pages_compact_kernel<false>, dim3(4u * (unsigned)sms), kPageThreads, 0, stream, a, w);
+  e = cudaFuncSetAttribute(pages_compact_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing * kSpan);
+  if (e != cudaSuccess) {
+    (void)cudaGetLastError();
+    return e;
+  }
+  return launch(pages_compact_kernel<true>, dim3(2u * (unsigned)sms), kPageThreads, kRing * kSpan, stream, a, w);
 }
 
 }  // namespace hs
