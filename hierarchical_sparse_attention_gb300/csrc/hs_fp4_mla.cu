@@ -93,7 +93,7 @@ constexpr uint32_t O_END = O_FIN + NF * FIN_BYTES;
 constexpr uint32_t SMEM_BYTES = (S_END > O_END ? S_END : O_END) + 1024;  // + alignment slack
 static_assert(SMEM_BYTES <= 227 * 1024 - 1024, "shared memory of a CTA");
 constexpr float kRescaleLog2 = 8.f;  // a reference maximum stays until it is passed by 2^8: P < 2^8
-constexpr int EPI_PITCH = 1024 + 16;  // bytes of a staged output row: 512 bf16 or 256 partial sums
+constexpr int EPI_PITCH = 2 * DL + 16;  // bytes of a staged output row
 static_assert(MH * EPI_PITCH <= O_P, "the read-out's staging fits the V tiles and the records after them");
 
 constexpr uint32_t kIdescQK = idesc(BJ, MH, false);                              // f16 latents
@@ -472,7 +472,7 @@ __device__ __forceinline__ void prefetch_q(const CUtensorMap* tm_q, size_t row0)
 
 template <bool kWin>
 __global__ void __launch_bounds__(T, 1)
-    fp4_mla_kernel(const Fp4MlaArgs a, int tiles_per_request, int queries_per_tile, int units,
+    fp4_mla_kernel(const Fp4MlaArgs a, int tiles_per_request, int queries_per_tile, int units, int all_rows,
                    const __grid_constant__ CUtensorMap tm_q, float* __restrict__ part_o, float* __restrict__ part_lse,
                    uint32_t* __restrict__ err) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -835,58 +835,54 @@ __global__ void __launch_bounds__(T, 1)
       ok = __syncthreads_and(ok && !*abort);
       tc_after();
       if (ok && warp < 16) {
-        // O out, normalised: warp w has rows 32 (w & 3) .. + 31 and a quarter of the columns. The rows
-        // are staged in shared memory, 1024 bytes of each (all of a bf16 row; half of a row of partial
-        // sums, in two passes) and leave by one bulk copy a row.
+        // O out, normalised: warp w has rows 32 (w & 3) .. + 31 and a quarter of the columns. A thread
+        // holds 32 columns of one row. Partial sums go straight to memory, four columns at a time, in a
+        // layout in which the rows' pieces are neighbours (the merge kernel reads it so). bf16 rows are
+        // staged in shared memory, so that a row's stores are consecutive.
         const bool direct = a.splits == 1;
         const float* fin = reinterpret_cast<const float*>(base + O_FIN) + (full % NF) * 2 * MH;
         const float l = nblk > 0 ? fin[head] : 0.f, m = nblk > 0 ? fin[MH + head] : -INFINITY;
         const float inv = l == 0.f ? 0.f : a.latent_scale / l;  // l is NaN where a weight is
-        uint8_t* stg = base + O_TILES + head * EPI_PITCH + (warp >> 2) * 256;
-        const size_t out0 = un.row0 + (direct ? 0 : (size_t)un.p * (units / a.splits / tiles_per_request) * a.num_queries * a.num_heads);
+        const size_t out0 = un.row0 + (direct ? 0 : (size_t)un.p * all_rows);
+        uint8_t* stg = base + O_TILES + head * EPI_PITCH;
+        float4* part = reinterpret_cast<float4*>(part_o) + out0 * (DL / 4) + head;
 #pragma unroll 1
-        for (int pass = 0; pass < (direct ? 1 : 2); ++pass) {
-          const int per = direct ? DL / 4 : DL / 8, c0 = pass * (DL / 2) + (warp >> 2) * per;
-#pragma unroll 1
-          for (int c = 0; c < per; c += 32) {
-            float v[32];
-            if (nblk > 0) {
-              tmem_ld32(tbase + lane_off + c0 + c, v);
-            } else {
+        for (int c = (warp >> 2) * (DL / 4); c < ((warp >> 2) + 1) * (DL / 4); c += 32) {
+          float v[32];
+          if (nblk > 0) {
+            tmem_ld32(tbase + lane_off + c, v);
+          } else {
 #pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = 0.f;
-            }
+            for (int i = 0; i < 32; ++i) v[i] = 0.f;
+          }
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] *= inv;
-            if (direct) {
+          for (int i = 0; i < 32; ++i) v[i] *= inv;
+          if (direct) {
 #pragma unroll
-              for (int i = 0; i < 32; i += 8) {
-                uint32_t w[4];
+            for (int i = 0; i < 32; i += 8) {
+              uint32_t w[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  const __nv_bfloat162 x = __floats2bfloat162_rn(v[i + 2 * k], v[i + 2 * k + 1]);
-                  w[k] = *reinterpret_cast<const uint32_t*>(&x);
-                }
-                *reinterpret_cast<uint4*>(stg + 2 * (c + i)) = make_uint4(w[0], w[1], w[2], w[3]);
+              for (int k = 0; k < 4; ++k) {
+                const __nv_bfloat162 x = __floats2bfloat162_rn(v[i + 2 * k], v[i + 2 * k + 1]);
+                w[k] = *reinterpret_cast<const uint32_t*>(&x);
               }
-            } else {
-#pragma unroll
-              for (int i = 0; i < 32; i += 4)
-                *reinterpret_cast<float4*>(stg + 4 * (c + i)) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+              *reinterpret_cast<uint4*>(stg + 2 * (c + i)) = make_uint4(w[0], w[1], w[2], w[3]);
             }
+          } else if (head < un.live) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+              part[(size_t)((c + i) >> 2) * un.live] = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
           }
-          fence_async_smem();  // the staged rows, before the copies read them
+        }
+        if (direct) {
           sync_n(512);
-          const int row = 8 * warp + lane;
-          if (lane < 8 && row < un.live) {
-            const void* dst = direct ? static_cast<const void*>(a.o + (out0 + row) * DL)
-                                     : static_cast<const void*>(part_o + (out0 + row) * DL + pass * (DL / 2));
-            asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst),
-                         "r"(smem_u32(base + O_TILES + row * EPI_PITCH)), "r"(1024)
-                         : "memory");
+#pragma unroll 4
+          for (int k = 0; k < 2 * MH / 16; ++k) {  // warp w has rows 8 w .. 8 w + 7, half a row at a time
+            const int row = (MH / 16) * warp + (k >> 1), at = 512 * (k & 1) + 16 * lane;
+            if (row < un.live)
+              *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(a.o + (out0 + row) * DL) + at) =
+                  *reinterpret_cast<const uint4*>(base + O_TILES + row * EPI_PITCH + at);
           }
-          asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
-          sync_n(512);  // the staging may be written again
         }
         if (head < un.live && warp < 4)
           (direct ? a.lse : part_lse)[out0 + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
@@ -908,7 +904,6 @@ __global__ void __launch_bounds__(T, 1)
     for (int b = done >= 2 ? done - 2 : 0; b < done; ++b) ok = ok && pipe_wait<true>(bs.p_free, NS, b, abort);
   }
   ok = __syncthreads_and(ok && !*abort);
-  if (rank == 1) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // the outputs are written
   if (!ok) {
     // outputs are not valid: flag it, and give copies and MMAs still in flight one more bound before
     // the shared and tensor memory are released
@@ -934,42 +929,57 @@ __global__ void __launch_bounds__(T, 1)
   cluster_sync_all();  // the partner no longer reads or arrives on this CTA's shared memory
 }
 
-// The splits of each query head joined: weights exp(lse_p - lse), lse = log sum exp lse_p, in
-// split order. A thread per four output dims.
-constexpr int COMBINE_T = 256;
+// The splits of each query head joined: weights exp(lse_p - lse), lse = log sum exp lse_p, in split
+// order. Grid (tile, part of it); a thread has 16 output dims (a sector) of a row, neighbours have
+// neighbouring rows, as the partial sums lie: [split][tile][512 / 4][rows of the tile][4].
+constexpr int COMBINE_T = 128, COMBINE_D = 16;
 __global__ void __launch_bounds__(COMBINE_T)
-    fp4_combine_kernel(const Fp4MlaArgs a, int rows, const float* __restrict__ part_o, const float* __restrict__ part_lse) {
+    fp4_combine_kernel(const Fp4MlaArgs a, int tiles_per_request, int queries_per_tile, int rows,
+                       const float* __restrict__ part_o, const float* __restrict__ part_lse) {
   pdl_wait();
-  const int64_t g = (int64_t)blockIdx.x * COMBINE_T + threadIdx.x;
-  const int64_t row = g >> 7;
-  const int c4 = (int)(g & 127);
-  if (row >= rows) return;
+  const int r = blockIdx.x / tiles_per_request, q0 = (blockIdx.x - r * tiles_per_request) * queries_per_tile;
+  const int live = min(queries_per_tile, a.num_queries - q0) * a.num_heads;
+  const size_t row0 = ((size_t)r * a.num_queries + q0) * a.num_heads;
+  const int e = blockIdx.y * COMBINE_T + threadIdx.x, head = e % live, d = e / live * COMBINE_D;
+  if (d >= DL) return;
+  const float* lses = part_lse + row0 + head;
   float mx = -INFINITY, nan = 0.f;
   for (int p = 0; p < a.splits; ++p) {
-    const float x = __ldg(part_lse + (size_t)p * rows + row);
+    const float x = __ldg(lses + (size_t)p * rows);
     mx = fmaxf(mx, x);
     if (x != x) nan = x;
   }
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float acc[COMBINE_D] = {};
   float lse = nan != nan ? nan : mx;
   if (lse != -INFINITY) {
     float z = 0.f;
-    for (int p = 0; p < a.splits; ++p) z += expf(__ldg(part_lse + (size_t)p * rows + row) - mx);
+    for (int p = 0; p < a.splits; ++p) z += expf(__ldg(lses + (size_t)p * rows) - mx);
     const float inv = 1.f / z;
+    const float4* src = reinterpret_cast<const float4*>(part_o) + row0 * (DL / 4) + (size_t)(d / 4) * live + head;
+#pragma unroll 2
     for (int p = 0; p < a.splits; ++p) {
-      const float w = expf(__ldg(part_lse + (size_t)p * rows + row) - mx) * inv;
-      const float4 v = __ldg(reinterpret_cast<const float4*>(part_o + ((size_t)p * rows + row) * DL) + c4);
-      acc.x += w * v.x;
-      acc.y += w * v.y;
-      acc.z += w * v.z;
-      acc.w += w * v.w;
+      const float w = expf(__ldg(lses + (size_t)p * rows) - mx) * inv;
+#pragma unroll
+      for (int i = 0; i < COMBINE_D / 4; ++i) {
+        const float4 v = __ldg(src + (size_t)p * rows * (DL / 4) + i * live);
+        acc[4 * i] += w * v.x;
+        acc[4 * i + 1] += w * v.y;
+        acc[4 * i + 2] += w * v.z;
+        acc[4 * i + 3] += w * v.w;
+      }
     }
     lse = mx + logf(z);
   }
-  const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x, acc.y), hi = __floats2bfloat162_rn(acc.z, acc.w);
-  reinterpret_cast<uint2*>(a.o + (size_t)row * DL)[c4] =
-      make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-  if (c4 == 0) a.lse[row] = lse;
+  uint32_t w[COMBINE_D / 2];
+#pragma unroll
+  for (int i = 0; i < COMBINE_D / 2; ++i) {
+    const __nv_bfloat162 x = __floats2bfloat162_rn(acc[2 * i], acc[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&x);
+  }
+  uint4* dst = reinterpret_cast<uint4*>(a.o + (row0 + head) * DL + d);
+  dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+  dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  if (d == 0) a.lse[row0 + head] = lse;
 }
 
 // Q ([rows][576] bf16) as a 2-D tensor read in boxes of 128 rows x 64 dims, its 16-B chunks XOR-ed
@@ -1067,14 +1077,15 @@ cudaError_t launch_fp4_mla(const Fp4MlaArgs& a, int32_t num_requests, float* par
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.numAttrs = 2;
-  e = cudaLaunchKernelEx(&cfg, kernel, a, tiles, g, units, tm_q, part, part_lse, err);
+  e = cudaLaunchKernelEx(&cfg, kernel, a, tiles, g, units, rows, tm_q, part, part_lse, err);
   if (e != cudaSuccess) {
     (void)cudaGetLastError();
     return e;
   }
   if (a.splits == 1) return cudaSuccess;
-  return launch(fp4_combine_kernel, dim3((unsigned)(((int64_t)rows * (DL / 4) + COMBINE_T - 1) / COMBINE_T)), COMBINE_T,
-                0, stream, a, rows, (const float*)part, (const float*)part_lse);
+  const unsigned parts = (unsigned)((g * a.num_heads * (DL / COMBINE_D) + COMBINE_T - 1) / COMBINE_T);
+  return launch(fp4_combine_kernel, dim3((unsigned)(num_requests * tiles), parts), COMBINE_T, 0, stream, a, tiles, g, rows,
+                (const float*)part, (const float*)part_lse);
 }
 
 }  // namespace hs
