@@ -56,46 +56,44 @@ constexpr int T = 736;          // threads per CTA: 23 warps
 constexpr int MH = 128;         // MMA M: query heads of a tile (padded with zero rows)
 constexpr int BJ = 64;          // rows per block
 constexpr int DQK = kFp4Dims, DL = kFp4Latent;
-constexpr int KATOMS = DQK / 64, VATOMS = DL / 64;  // swizzle atoms of 64 values in a K and a V tile
+constexpr int QATOMS = DQK / 64, ATOMS = DL / 64;  // swizzle atoms of 64 values in Q and in a tile of latents
 constexpr int NT = 2;           // tiles in flight
 constexpr int ND = 3;           // blocks of records in a dequantisation warp's ring: one read, two on their way
 constexpr int NS = 3;           // S buffers, and softmax warpgroups: one block each in turn
 constexpr uint32_t TMEM_COLS = 512, Q_COL = 0, S_COL = 288;
 static_assert(S_COL + NS * BJ <= TMEM_COLS, "Q and the S buffers fit tensor memory");
 // S-CTA warps: 0-11 softmax, 12 issuer, 13-22 dequantisation; O-CTA: 0-3 corrector, 4 issuer, 5-14
-// dequantisation (0-15 read out at the end). Dequantisation leaves out the warps w % 4 = 0: an issuer
+// dequantisation, 15-22 and the corrector's read out. Dequantisation leaves out the warps w % 4 = 0: an issuer
 // whose MMAs wait for the tensor core holds up the shared-memory instructions of the warps on its
 // scheduler (they took up to 1.2 us longer over a block than the others).
 constexpr int S_ISSUER = 12, S_DEQ0 = 13;
-constexpr int O_ISSUER = 4, O_DEQ0 = 5;
+constexpr int O_ISSUER = 4, O_DEQ0 = 5, O_OUT0 = 15, NOUT = 3;  // NOUT warps read out a quarter of the heads
 constexpr int NDEQ = 8, RW = BJ / NDEQ;  // dequantisation warps of each CTA, eight rows of a block each
 constexpr int MASKS = 16;       // blocks whose row masks are kept (the copies are at most 8 ahead of the softmax)
 
-constexpr uint32_t KV_ATOM = BJ * 128, K_TILE = KATOMS * KV_ATOM, V_TILE = VATOMS * KV_ATOM;
+constexpr uint32_t KV_ATOM = BJ * 128, TILE = ATOMS * KV_ATOM;
 constexpr uint32_t QBOX = MH * 128;
-constexpr int S_REC = kFp4Row, O_REC = kFp4RopeAt;  // bytes of a record that each CTA reads
-constexpr uint32_t S_RING = ND * RW * S_REC, O_RING = ND * RW * O_REC;  // a dequantisation warp's ring
-constexpr uint32_t S_TILES = 0, S_QSTAGE = 0;  // Q is staged over the K tiles before the first block
-constexpr uint32_t S_RAW = NT * K_TILE;
-static_assert(KATOMS * QBOX <= S_RAW, "Q's staging fits the K tiles");
-constexpr uint32_t S_REF = S_RAW + NDEQ * S_RING;  // the reference maxima, handed from block to block
-constexpr uint32_t S_SUMS = S_REF + MH * 4;     // the sums of the softmax warpgroups after the first, and their references
-constexpr uint32_t S_MASK = S_SUMS + 2 * (NS - 1) * MH * 4;  // a byte per block and dequantisation warp: its rows that exist
+constexpr int REC = kFp4RopeAt;                    // bytes of a record that go through the rings: codes and scales
+constexpr uint32_t RING = ND * RW * REC;           // a dequantisation warp's ring
+constexpr uint32_t S_TILES = 0;                    // latents of K; Q's are staged over them before the first block
+constexpr int NR = 5;                              // RoPE tiles, copied straight to their places
+constexpr uint32_t S_ROPE = NT * TILE;             // (Q's are staged over two of them)
+constexpr uint32_t S_RAW = S_ROPE + NR * KV_ATOM;
+static_assert(ATOMS * QBOX <= NT * TILE && QBOX == 2 * KV_ATOM, "Q's staging");
+constexpr uint32_t S_REF = S_RAW + NDEQ * RING;  // the reference maxima, handed from block to block
+constexpr uint32_t S_MASK = S_REF + MH * 4;     // a byte per block and dequantisation warp: its rows that exist
 constexpr uint32_t S_END = S_MASK + MASKS * NDEQ;
-constexpr uint32_t O_TILES = 0, O_RAW = NT * V_TILE;
-constexpr uint32_t O_P = (O_RAW + NDEQ * O_RING + 1023u) & ~1023u;
+constexpr uint32_t O_TILES = 0, O_RAW = NT * TILE;
+constexpr uint32_t O_P = (O_RAW + NDEQ * RING + 1023u) & ~1023u;
 constexpr uint32_t P_BUF = MH * BJ * 2, P_BYTES = P_BUF + MH * 4;  // P and the rescale factors of a block
-constexpr uint32_t FIN_BYTES = 2 * MH * 4;       // a unit's sums and references
+constexpr uint32_t FIN_WG = 2 * MH * 4;          // a softmax warpgroup's sums and references of a unit
 constexpr uint32_t O_ALPHA = O_P + 2 * P_BUF;
 constexpr uint32_t O_FIN = O_ALPHA + 2 * MH * 4;
-constexpr int NF = 4;                           // units whose totals are kept: the S-CTA is at most two ahead (P's buffers)
-constexpr uint32_t O_END = O_FIN + NF * FIN_BYTES;
+constexpr int NF = 3;  // units whose totals are kept: P's two buffers let the S-CTA be two units ahead, of one block each
+constexpr uint32_t O_END = O_FIN + NF * NS * FIN_WG;
 constexpr uint32_t SMEM_BYTES = (S_END > O_END ? S_END : O_END) + 1024;  // + alignment slack
 static_assert(SMEM_BYTES <= 227 * 1024 - 1024, "shared memory of a CTA");
-constexpr float kRescaleLog2 = 8.f;  // a reference maximum stays until it is passed by 2^8: P < 2^8
-constexpr int EPI_PITCH = 2 * DL + 16;  // bytes of a staged output row
-static_assert(MH * EPI_PITCH <= O_P, "the read-out's staging fits the V tiles and the records after them");
-
+constexpr float kRescaleLog2 = 15.f;
 constexpr uint32_t kIdescQK = idesc(BJ, MH, false);                              // f16 latents
 constexpr uint32_t kIdescRope = kIdescQK | (1u << 7) | (1u << 10);               // bf16 RoPE
 constexpr uint32_t kIdescPV = idesc(256, MH, true);
@@ -111,6 +109,7 @@ struct Barriers {
   uint64_t pv_go[2];                      // O-CTA: O is ready for P . V of the block
   uint64_t mma_done;                      // O-CTA: the MMAs issued so far are done
   uint64_t fin[NF];                       // O-CTA: the S-CTA's totals of a unit are here
+  uint64_t o_full, o_free;                // O-CTA: a unit's last P . V is done; O has been read out
 };
 
 // The kernel's roles run side by side from one instruction cache, and much of their time goes into
@@ -186,6 +185,31 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
   }
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
+// 32 accumulator columns of 32 rows, spread over the warp as matrix fragments are: v[h][4 j + 2 s + e]
+// is row 16 h + 8 s + lane / 4, column 8 j + 2 (lane % 4) + e.
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, float (&v)[2][16]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t* r = reinterpret_cast<uint32_t*>(v[h]);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr + ((uint32_t)(16 * h) << 16)));
+  }
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+// 32 consecutive bytes of a lane: one store (a whole sector) where they are aligned.
+__device__ __forceinline__ void store8(uint32_t* dst, const uint32_t (&w)[8], bool aligned) {
+  if (aligned) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
 // Two 32-bit floats at a time.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 d;
@@ -246,23 +270,25 @@ __device__ __forceinline__ uint4 times(uint4 v, __half2 s) {
   return make_uint4(x[0], x[1], x[2], x[3]);
 }
 
-// A dequantisation warp's copies of a block: its eight rows' first REC bytes into a slot of its ring,
+// A dequantisation warp's copies of a block: its eight rows' codes and scales into a slot of its ring,
 // eight lanes of 16 bytes to a row, four rows at a time: 128 consecutive bytes of each, which meet
-// every bank once, and addresses that are one register and a constant. Rows that do not exist become
-// zeros. y: lane l has row l % 8 (-1: none); dst: this lane's place in the slot.
-template <int REC>
-__device__ __forceinline__ void copy_rows(uint32_t dst, int32_t y, const uint8_t* __restrict__ pool, int lane) {
+// every bank once, and addresses that are one register and a constant. In the S-CTA the RoPE values go
+// straight to their places in their tile, chunk c of row x of eight at c ^ x. Rows that do not exist
+// become zeros. y: lane l has row l % 8 (-1: none); dst, rope: this lane's places.
+template <bool kS>
+__device__ __forceinline__ void copy_rows(uint32_t dst, uint32_t rope, int32_t y, const uint8_t* __restrict__ pool, int lane) {
+  const auto copy16 = [](uint32_t to, const uint8_t* from, int size) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(size) : "memory");
+  };
 #pragma unroll
   for (int g = 0; g < 2; ++g) {
     const int32_t row = __shfl_sync(0xffffffffu, y, 4 * g + (lane >> 3));
     const uint8_t* src = pool + (int64_t)max(row, 0) * kFp4Row + 16 * (lane & 7);
     const int size = row >= 0 ? 16 : 0;
-#pragma unroll
-    for (int i = 0; i < (REC + 127) / 128; ++i)
-      if (128 * (i + 1) <= REC || 128 * i + 16 * (lane & 7) < REC)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + 4 * g * REC + 128 * i), "l"(src + 128 * i),
-                     "r"(size)
-                     : "memory");
+    copy16(dst + 4 * g * REC, src, size);
+    copy16(dst + 4 * g * REC + 128, src + 128, size);
+    if ((lane & 7) < 2) copy16(dst + 4 * g * REC + 256, src + 256, size);
+    if (kS) copy16(g ? (rope ^ 64u) + 512u : rope, src + kFp4RopeAt, size);
   }
 }
 
@@ -273,11 +299,8 @@ __device__ __forceinline__ void copy_rows(uint32_t dst, int32_t y, const uint8_t
 struct Held {
   uint4 codes[4];
   uint16_t scales[4];
-  uint4 rope[2];
 };
-template <bool kS>
 __device__ __forceinline__ Held read_rows(const uint8_t* slot, int lane) {
-  constexpr int REC = kS ? S_REC : O_REC;
   Held h;
 #pragma unroll
   for (int s = 0; s < 4; ++s) {
@@ -286,10 +309,6 @@ __device__ __forceinline__ Held read_rows(const uint8_t* slot, int lane) {
     h.codes[s] = *reinterpret_cast<const uint4*>(rec + 16 * it);
     h.scales[s] = *reinterpret_cast<const uint16_t*>(rec + kFp4Scales + 2 * it);
   }
-  if (kS)
-#pragma unroll
-    for (int g = 0; g < 2; ++g)  // four rows' RoPE values, a chunk per lane
-      h.rope[g] = *reinterpret_cast<const uint4*>(slot + (4 * g + (lane >> 3)) * REC + kFp4RopeAt + 16 * (lane & 7));
   return h;
 }
 
@@ -310,37 +329,38 @@ __device__ __forceinline__ void write_rows(const Held& h, uint8_t* group, int la
     }
     const __half2_raw raw = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
     const __half2 pair = raw, sc[2] = {__low2half2(pair), __high2half2(pair)};
+    uint4 v[4];  // the lane's 32 dims, a chunk of eight each
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const uint4 v = times(codes_to_f16(w[u]), sc[u >> 1]);
+    for (int u = 0; u < 4; ++u) v[u] = times(codes_to_f16(w[u]), sc[u >> 1]);
+    if (!kS) {  // V: chunk j takes pair j of each, the order of columns that the read-out wants
+      const uint4 a = v[0], b = v[1], c = v[2], d = v[3];
+      v[0] = make_uint4(a.x, b.x, c.x, d.x);
+      v[1] = make_uint4(a.y, b.y, c.y, d.y);
+      v[2] = make_uint4(a.z, b.z, c.z, d.z);
+      v[3] = make_uint4(a.w, b.w, c.w, d.w);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
       asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(((s >> 1 ? at1 : at0) ^ (uint32_t)(u << 4)) + (s & 1) * 4 * KV_ATOM),
-                   "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                   "r"(v[u].x), "r"(v[u].y), "r"(v[u].z), "r"(v[u].w)
                    : "memory");
-    }
-  }
-  if (kS) {
-#pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      const int row = 4 * g + (lane >> 3);
-      *reinterpret_cast<uint4*>(group + VATOMS * KV_ATOM + row * 128 + (((lane & 7) ^ row) << 4)) = h.rope[g];
-    }
   }
 }
 
 // A dequantisation warp's loop over a unit's blocks: block b is written while the rows of the next
 // ND - 1 blocks are on their way, and two more blocks' row numbers. `done`: blocks of the units before
 // (places in rings go on from unit to unit). In the S-CTA it waits, before its first tile write, until Q
-// has left the staging area, and tells the softmax which of its rows exist.
+// has left the staging area, and tells the softmax which of its rows exist. A block's copies start once
+// the tensor core has read the block four before it, whose RoPE tile they go to.
 template <bool kS, bool kWin>
 __device__ __forceinline__ bool run_dequant(const Rows<kWin>& rows, const uint8_t* __restrict__ pool, int nblk, int done,
-                                            uint32_t q_phase, uint8_t* ring, uint8_t* masks, uint8_t* tiles,
+                                            uint32_t q_phase, uint8_t* ring, uint8_t* rope, uint8_t* masks, uint8_t* tiles,
                                             Barriers& bs, int wq, int lane, uint32_t* err, volatile int* abort) {
-  constexpr int REC = kS ? S_REC : O_REC;
-  constexpr uint32_t TB = kS ? K_TILE : V_TILE;
   const int own = RW * wq + (lane & 7);
   bool missing = false, ok = true;
   // slots of the ring: the next one to fill, and the next one to read
   const uint32_t ring0 = smem_u32(ring) + (lane >> 3) * REC + 16 * (lane & 7), ring_end = ring0 + ND * RW * REC;
+  const uint32_t rope0 = kS ? smem_u32(rope) + RW * wq * 128 + (lane >> 3) * 128 + (((lane & 7) ^ (lane >> 3)) << 4) : 0u;
   uint32_t fill = ring0;
   const uint8_t* read = ring;
   auto start = [&](int32_t raw, int b) {  // the copies of block b (one group of copies, empty past the end)
@@ -352,13 +372,13 @@ __device__ __forceinline__ bool run_dequant(const Rows<kWin>& rows, const uint8_
         const uint32_t mask = __ballot_sync(0xffffffffu, y >= 0);
         if (lane == 0) masks[((done + b) % MASKS) * NDEQ + wq] = (uint8_t)mask;
       }
-      copy_rows<REC>(fill, y, pool, lane);
+      copy_rows<kS>(fill, rope0 + (done + b) % NR * KV_ATOM, y, pool, lane);
       fill += RW * REC;
       if (fill == ring_end) fill = ring0;
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  static_assert(ND == 3, "two blocks' copies are started here");
+  static_assert(ND == 3 && NT == 2 && NR >= ND + NT, "two blocks' copies are started here");
   int32_t t0 = rows.raw(own), t1 = rows.raw(BJ + own), t2 = rows.raw(2 * BJ + own), t3 = rows.raw(3 * BJ + own);
   start(t0, 0);
   start(t1, 1);
@@ -370,13 +390,13 @@ __device__ __forceinline__ bool run_dequant(const Rows<kWin>& rows, const uint8_
     t3 = rows.raw(BJ * (b + ND + 1) + own);
     asm volatile("cp.async.wait_group %0;" ::"n"(ND - 1) : "memory");
     __syncwarp();
-    const Held held = read_rows<kS>(read, lane);
+    const Held held = read_rows(read, lane);
     read = read + RW * REC == ring + ND * RW * REC ? ring : read + RW * REC;
     if (kS && b == 0) ok = ready_or_wait(&bs.q_full, 1, (int)q_phase, abort);
     if (g >= NT) ok = ok && ready_or_wait(bs.tile_free, NT, g - NT, abort);
     ok = __all_sync(0xffffffffu, ok);  // (and the slot has been read)
     if (!ok) break;
-    write_rows<kS>(held, tiles + (g % NT) * TB + wq * 1024, lane);
+    write_rows<kS>(held, tiles + (g % NT) * TILE + wq * 1024, lane);
     __syncwarp();  // (the issuer has the proxy fence: here it would wait for the copies in flight too)
     if (lane == 0) bar_arrive(&bs.tile_full[g % NT]);
   }
@@ -448,25 +468,31 @@ __device__ __forceinline__ Unit<kWin> unit_of(const Fp4MlaArgs& a, int u, int ti
   return x;
 }
 
-// Q's 128 rows from row0 as nine tensor boxes of 64 dims, three to a barrier (rows past the tile's are
-// not used).
-__device__ __forceinline__ void request_q(const CUtensorMap* tm_q, size_t row0, uint8_t* base, Barriers& bs) {
+// Where half a box of Q (64 rows of 64 dims) is staged: the latents' over the K tiles, the RoPE values'
+// over the RoPE tiles of the unit's third and fourth block (g0: the number of its first one), whose
+// copies start when Q is in tensor memory; those of the first two may be on their way.
+__device__ __forceinline__ uint32_t q_stage(int bx, int half, int g0) {
+  return bx < ATOMS ? S_TILES + bx * QBOX + half * KV_ATOM : S_ROPE + (g0 + 3 + half) % NR * KV_ATOM;
+}
+// Q's 128 rows from row0 as tensor boxes of 64 rows and dims, a third of the dims to a barrier (rows past
+// the tile's are not used).
+__device__ __forceinline__ void request_q(const CUtensorMap* tm_q, size_t row0, int g0, uint8_t* base, Barriers& bs) {
   fence_async_smem();  // earlier generic accesses of the staging area and the barriers, before the copies
   for (int g = 0; g < NS; ++g) {
-    bar_arrive_tx(&bs.q_raw[g], KATOMS / NS * QBOX);
-    for (int bx = KATOMS / NS * g; bx < KATOMS / NS * (g + 1); ++bx)
+    bar_arrive_tx(&bs.q_raw[g], QATOMS / NS * QBOX);
+    for (int i = 2 * (QATOMS / NS) * g; i < 2 * (QATOMS / NS) * (g + 1); ++i)
       asm volatile(
           "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-              smem_u32(base + S_QSTAGE + bx * QBOX)),
-          "l"(tm_q), "r"(64 * bx), "r"((int)row0), "r"(smem_u32(&bs.q_raw[g]))
+              smem_u32(base + q_stage(i >> 1, i & 1, g0))),
+          "l"(tm_q), "r"(64 * (i >> 1)), "r"((int)row0 + BJ * (i & 1)), "r"(smem_u32(&bs.q_raw[g]))
           : "memory");
   }
 }
 
 // The same boxes into L2, a unit ahead.
 __device__ __forceinline__ void prefetch_q(const CUtensorMap* tm_q, size_t row0) {
-  for (int bx = 0; bx < KATOMS; ++bx)
-    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];" ::"l"(tm_q), "r"(64 * bx), "r"((int)row0)
+  for (int i = 0; i < 2 * QATOMS; ++i)
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];" ::"l"(tm_q), "r"(64 * (i >> 1)), "r"((int)row0 + BJ * (i & 1))
                  : "memory");
 }
 
@@ -506,6 +532,8 @@ __global__ void __launch_bounds__(T, 1)
       bar_init(&bs.pv_go[k], 4);
     }
     for (int k = 0; k < NF; ++k) bar_init(&bs.fin[k], 1);  // the same
+    bar_init(&bs.o_full, 1);
+    bar_init(&bs.o_free, 4 * NOUT);
     s_abort = 0;
     s_issued = 0;
     s_requested = 0;
@@ -514,12 +542,11 @@ __global__ void __launch_bounds__(T, 1)
     if (rank == 0) {
       const Unit<kWin> first = unit_of<kWin>(a, blockIdx.x >> 1, tiles_per_request, queries_per_tile, false, err);
       if (first.nblk > 0) {
-        request_q(&tm_q, first.row0, base, bs);
+        request_q(&tm_q, first.row0, 0, base, bs);
         s_requested = 1;
       }
     } else {
       for (int k = 0; k < 2; ++k) bar_arrive_tx(&bs.p_full[k], P_BYTES);
-      for (int k = 0; k < NF; ++k) bar_arrive_tx(&bs.fin[k], FIN_BYTES);
     }
   }
   if (warp == 1) {
@@ -540,9 +567,9 @@ __global__ void __launch_bounds__(T, 1)
   const int head = (warp & 3) * 32 + lane;  // this thread's row of the tile = its tensor-memory lane
   uint8_t* masks = base + S_MASK;
 
-  // The units of this pair, one after the other. In the S-CTA each role goes through them by itself
-  // (what they hand each other carries on from unit to unit); the O-CTA reads out with all its warps
-  // between two units.
+  // The units of this pair, one after the other. Each role goes through them by itself: what the roles
+  // hand each other carries on from unit to unit, so that a unit's first blocks are brought in while
+  // the last one's end is computed and read out.
   bool ok = true;
   int done = 0, full = 0;  // blocks, and units with blocks, before this one
 #pragma unroll 1
@@ -560,14 +587,14 @@ __global__ void __launch_bounds__(T, 1)
           // Q into tensor memory (warpgroup wg the columns [96 wg, 96 wg + 96)), column c holding dims
           // 2c, 2c + 1: the latent part as f16, the RoPE part as bf16 over latent_scale. Q has landed
           // only after the last unit's MMAs, which read the columns.
-          const bool landed = __all_sync(0xffffffffu, ready_or_wait(&bs.q_raw[wg], 1, (int)q_phase, abort));
+          ok = __all_sync(0xffffffffu, ready_or_wait(&bs.q_raw[wg], 1, (int)q_phase, abort));
           tc_after();
-          const bool live = landed && head < un.live;
+          const bool live = ok && head < un.live;
           const float inv = 1.f / a.latent_scale;
           const uint32_t sign = a.sm_scale < 0.f ? 0x80008000u : 0u;  // so that scores scale by a positive factor
 #pragma unroll 1
-          for (int bx = KATOMS / NS * wg; bx < KATOMS / NS * (wg + 1); ++bx) {
-            const uint8_t* src = base + S_QSTAGE + bx * QBOX + head * 128;
+          for (int bx = QATOMS / NS * wg; bx < QATOMS / NS * (wg + 1); ++bx) {
+            const uint8_t* src = base + q_stage(bx, head >> 6, done) + (head & 63) * 128;
 #pragma unroll
             for (int h = 0; h < 4; ++h) {  // two 16-B chunks: 16 dims, 8 columns
               uint32_t x[8] = {};
@@ -575,7 +602,7 @@ __global__ void __launch_bounds__(T, 1)
                 *reinterpret_cast<uint4*>(x) = *reinterpret_cast<const uint4*>(src + (((2 * h) ^ (head & 7)) << 4));
                 *reinterpret_cast<uint4*>(x + 4) = *reinterpret_cast<const uint4*>(src + (((2 * h + 1) ^ (head & 7)) << 4));
               }
-              if (bx < VATOMS) {
+              if (bx < ATOMS) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) x[i] = bf16x2_to_f16x2(x[i]) ^ sign;
               } else {
@@ -618,11 +645,13 @@ __global__ void __launch_bounds__(T, 1)
         const uint32_t s_at = tbase + lane_off + S_COL + BJ * wg;
         int b = wg - done % NS;
         if (b < 0) b += NS;
+        const bool mine = b < nblk;  // it has a block of this unit
         uint32_t turn = (uint32_t)((done + b) / NS) & 1u;  // of this warpgroup: its barriers' phase
 #pragma unroll 1
-        for (; b < nblk; b += NS, turn ^= 1u) {
+        for (; ok && b < nblk; b += NS, turn ^= 1u) {
           const int g = done + b;
-          if (!__all_sync(0xffffffffu, ready_or_wait(&bs.s_full[wg], 1, (int)turn, abort))) break;
+          ok = __all_sync(0xffffffffu, ready_or_wait(&bs.s_full[wg], 1, (int)turn, abort));
+          if (!ok) break;
           tc_after();
           // the rows that exist, and that this query sees
           const volatile uint32_t* at = reinterpret_cast<const volatile uint32_t*>(masks + (g % MASKS) * NDEQ);
@@ -656,12 +685,12 @@ __global__ void __launch_bounds__(T, 1)
           }
           bm *= sl2;
           float m_run = -INFINITY;
-          if (b > 0) {
+          if (g > 0) {
             // (the block before is the last warpgroup's block of this turn, or of the turn before)
             const int before = wg == 0 ? NS - 1 : wg - 1;
-            if (!__all_sync(0xffffffffu, ready_or_wait(&bs.m_set[before][warp & 3], 1, (int)(wg == 0 ? turn ^ 1u : turn), abort)))
-              break;
-            m_run = s_ref[head];
+            ok = __all_sync(0xffffffffu, ready_or_wait(&bs.m_set[before][warp & 3], 1, (int)(wg == 0 ? turn ^ 1u : turn), abort));
+            if (!ok) break;
+            if (b > 0) m_run = s_ref[head];
           }
           // Lazy rescale: a head keeps its reference until a block's maximum passes it by 2^8, so P
           // stays below 2^8 and O is rescaled only on those rare jumps. (NaN scores leave it alone.)
@@ -674,7 +703,8 @@ __global__ void __launch_bounds__(T, 1)
           l_own *= m_new == -INFINITY ? 1.f : ex2(m_own - m_new);
           m_own = m_new;
           // the O-CTA's P buffer is free once P . V of block g - 2 is done
-          if (!__all_sync(0xffffffffu, g < 2 || ready_or_wait<true>(bs.p_free, NS, g - 2, abort))) break;
+          ok = __all_sync(0xffffffffu, g < 2 || ready_or_wait<true>(bs.p_free, NS, g - 2, abort));
+          if (!ok) break;
           const uint32_t pbuf = r_pbuf + (g & 1) * P_BUF, rbar = g & 1 ? rbar1 : rbar0;
           st_async_f32(r_alpha + 4 * ((g & 1) * MH + head), alpha, rbar);
           float2 sum = make_float2(0.f, 0.f);
@@ -701,28 +731,17 @@ __global__ void __launch_bounds__(T, 1)
           if (lane == 0) bar_arrive(&bs.s_free[wg]);  // S has been read
           l_own += sum.x + sum.y;
         }
-        // the warpgroups' sums under the last block's reference, and that, to the O-CTA
-        sync_n(4 * NS * 32);
-        float* sums = reinterpret_cast<float*>(base + S_SUMS);
-        const float m = s_ref[head];
-        if (wg > 0) {
-          sums[2 * (wg - 1) * MH + head] = l_own;
-          sums[(2 * wg - 1) * MH + head] = m_own;
-        }
-        ok = sync_and(!*abort, 4 * NS * 32);  // (all softmax warps leave together)
-        if (wg == 0 && nblk > 0) {
-          const auto part = [&](float l, float mo) { return m == -INFINITY ? l : l * ex2(mo - m); };
-          float l = part(l_own, m_own);
-          for (int k = 0; k < NS - 1; ++k) l += part(sums[2 * k * MH + head], sums[(2 * k + 1) * MH + head]);
-          const uint32_t fin = remote(base + O_FIN, partner) + (full % NF) * FIN_BYTES;
+        // its sum, under the reference of its last block, to the O-CTA
+        if (ok && mine) {
+          const uint32_t fin = remote(base + O_FIN, partner) + ((full % NF) * NS + wg) * FIN_WG;
           const uint32_t bar = remote(&bs.fin[full % NF], partner);
-          st_async_f32(fin + 4 * head, l, bar);
-          st_async_f32(fin + 4 * (MH + head), m, bar);
+          st_async_f32(fin + 4 * head, l_own, bar);
+          st_async_f32(fin + 4 * (MH + head), m_own, bar);
         }
       } else if (warp == S_ISSUER) {
         // (tensor memory starts at 0: all of it is allocated here)
         const bool one = elected();
-        const uint64_t k0 = mdesc(smem_u32(base + S_TILES), 16, 1024);
+        const uint64_t k0 = mdesc(smem_u32(base + S_TILES), 16, 1024), r0 = mdesc(smem_u32(base + S_ROPE), 16, 1024);
         const bool more = u + pairs < units;
         Unit<kWin> next;
         next.nblk = 0;
@@ -738,12 +757,13 @@ __global__ void __launch_bounds__(T, 1)
           if (!go) break;
           tc_after();
           fence_async_smem();  // the tile's generic writes, seen through its barrier, before the tensor core's reads
-          const uint64_t dk0 = k0 + (uint64_t)((g % NT) * (K_TILE >> 4));
+          const uint64_t dk0 = k0 + (uint64_t)((g % NT) * (TILE >> 4)), dr0 = r0 + (uint64_t)((g % NR) * (KV_ATOM >> 4));
           const uint32_t d = S_COL + BJ * (g % NS);
           if (one) {
 #pragma unroll
-            for (int kk = 0; kk < KATOMS * 4; ++kk)
-              mma_ta(d, Q_COL + 8 * kk, dk0 + (uint64_t)(((kk >> 2) * KV_ATOM + (kk & 3) * 32) >> 4),
+            for (int kk = 0; kk < QATOMS * 4; ++kk)
+              mma_ta(d, Q_COL + 8 * kk,
+                     kk < DL / 16 ? dk0 + (uint64_t)(((kk >> 2) * KV_ATOM + (kk & 3) * 32) >> 4) : dr0 + (uint64_t)(((kk & 3) * 32) >> 4),
                      kk < DL / 16 ? kIdescQK : kIdescRope, kk > 0);
             commit(&bs.s_full[g % NS]);
             commit(&bs.tile_free[g % NT]);
@@ -756,32 +776,35 @@ __global__ void __launch_bounds__(T, 1)
           const int last = done + nblk - 1;
           go = __all_sync(0xffffffffu, last < 0 || ready_or_wait(bs.tile_free, NT, last, abort));
           if (go && one) {
-            request_q(&tm_q, next.row0, base, bs);
+            request_q(&tm_q, next.row0, done + nblk, base, bs);
             ++s_requested;
           }
           __syncwarp();
         }
         ok = go;
       } else if (const int wq = deq_warp(warp, S_DEQ0); wq >= 0) {
-        ok = run_dequant<true, kWin>(un.rows, a.pool, nblk, done, q_phase, base + S_RAW + wq * S_RING, masks, tiles, bs, wq,
+        ok = run_dequant<true, kWin>(un.rows, a.pool, nblk, done, q_phase, base + S_RAW + wq * RING, base + S_ROPE, masks, tiles, bs, wq,
                                      lane, err, abort);
       }
     } else {
       // ================================ O-CTA ================================
       uint8_t* tiles = base + O_TILES;
       const float* alpha_buf = reinterpret_cast<const float*>(base + O_ALPHA);
+      const bool out_warp = warp < 4 || warp >= O_OUT0;
       if (warp < 4) {
         // corrector: where a reference maximum of the warp's heads rose, rescale O once P . V of the
         // block before is done
 #pragma unroll 1
         for (int b = 0; b < nblk; ++b) {
           const int g = done + b;
-          if (!__all_sync(0xffffffffu, ready_or_wait<true>(bs.p_full, 2, g, abort))) break;
+          ok = __all_sync(0xffffffffu, ready_or_wait<true>(bs.p_full, 2, g, abort));
+          if (!ok) break;
           const float f = alpha_buf[(g & 1) * MH + head];
           // this buffer's next phase is block g + 2: its bytes come only after P . V of block g
           if (tid == 0) bar_arrive_tx(&bs.p_full[g & 1], P_BYTES);
           if (__any_sync(0xffffffffu, b > 0 && f != 1.f)) {
-            if (!__all_sync(0xffffffffu, ready_or_wait(bs.tile_free, NT, g - 1, abort))) break;
+            ok = __all_sync(0xffffffffu, ready_or_wait(bs.tile_free, NT, g - 1, abort));
+            if (!ok) break;
             tc_after();
 #pragma unroll 1
             for (int c = 0; c < DL; c += 16) {
@@ -804,10 +827,12 @@ __global__ void __launch_bounds__(T, 1)
           const int g = done + b;
           bool go = ready_or_wait(bs.tile_full, NT, g, abort);
           go = go && ready_or_wait(bs.pv_go, 2, g, abort);
-          if (!__all_sync(0xffffffffu, go)) break;
+          if (b == 0) go = go && (full == 0 || ready_or_wait(&bs.o_free, 1, full - 1, abort));
+          ok = __all_sync(0xffffffffu, go);
+          if (!ok) break;
           tc_after();
           fence_async_smem();  // V's and P's writes, seen through their barriers, before the tensor core's reads
-          const uint64_t dp0 = p0 + (uint64_t)((g & 1) * (P_BUF >> 4)), dv0 = v0 + (uint64_t)((g % NT) * (V_TILE >> 4));
+          const uint64_t dp0 = p0 + (uint64_t)((g & 1) * (P_BUF >> 4)), dv0 = v0 + (uint64_t)((g % NT) * (TILE >> 4));
           if (one) {
 #pragma unroll
             for (int kk = 0; kk < BJ / 16; ++kk)
@@ -818,79 +843,78 @@ __global__ void __launch_bounds__(T, 1)
             commit(&bs.tile_free[g % NT]);
             commit_multicast(&bs.p_free[g % NS], (uint16_t)(1u << partner));
             commit(&bs.mma_done);
+            if (b == nblk - 1) commit(&bs.o_full);
             s_issued = g + 1;
           }
           __syncwarp();
         }
       } else if (const int wq = deq_warp(warp, O_DEQ0); wq >= 0) {
-        run_dequant<false, kWin>(un.rows, a.pool, nblk, done, 0u, base + O_RAW + wq * O_RING, masks, tiles, bs, wq, lane,
+        ok = run_dequant<false, kWin>(un.rows, a.pool, nblk, done, 0u, base + O_RAW + wq * RING, nullptr, masks, tiles, bs, wq, lane,
                                  err, abort);
       }
-      __syncthreads();
-      // this unit's MMAs are done, and its totals are here
-      ok = !*abort;
-      if (nblk > 0)
-        ok = ok && ready_or_wait(bs.tile_free, NT, done + nblk - 1, abort) &&
-             ready_or_wait<true>(bs.fin, NF, full, abort);
-      ok = __syncthreads_and(ok && !*abort);
-      tc_after();
-      if (ok && warp < 16) {
-        // O out, normalised: warp w has rows 32 (w & 3) .. + 31 and a quarter of the columns. A thread
-        // holds 32 columns of one row. Partial sums go straight to memory, four columns at a time, in a
-        // layout in which the rows' pieces are neighbours (the merge kernel reads it so). bf16 rows are
-        // staged in shared memory, so that a row's stores are consecutive.
+      if (out_warp) {
+        // The read-out. Warps 0 - 3, 16 - 19 and (20, 21, 22, 15) have a quarter of the heads each, by
+        // their number % 4 as tensor memory has it, and every third 32 columns. The columns of V's tile
+        // are ordered so that a lane's fragments are eight consecutive dims of each of four rows, and
+        // four lanes have 32 dims of a row (a thread a row made the stores take twice as long). The
+        // warps that have nothing else to do wait at a barrier of the hardware, not at the mbarriers:
+        // their looks slowed the others down (about 1 us more from P to P . V).
+        ok = sync_and(ok, 32 * 4 * NOUT);
+        const int set = warp < 4 ? 0 : warp >= 16 && warp < 20 ? 1 : 2;
         const bool direct = a.splits == 1;
-        const float* fin = reinterpret_cast<const float*>(base + O_FIN) + (full % NF) * 2 * MH;
-        const float l = nblk > 0 ? fin[head] : 0.f, m = nblk > 0 ? fin[MH + head] : -INFINITY;
+        float l = 0.f, m = -INFINITY;
+        if (nblk > 0) {
+          const int k = full % NF;
+          if (tid == 0 && ok) bar_arrive_tx(&bs.fin[k], min(nblk, NS) * FIN_WG);
+          ok = ok && ready_or_wait<true>(bs.fin, NF, full, abort) && ready_or_wait(&bs.o_full, 1, full, abort);
+          ok = __all_sync(0xffffffffu, ok);
+          tc_after();
+          // the warpgroups' sums, from the reference of each to the last block's
+          const float* fin = reinterpret_cast<const float*>(base + O_FIN) + (size_t)k * NS * (FIN_WG / 4) + head;
+          m = fin[(done + nblk - 1) % NS * (FIN_WG / 4) + MH];
+          for (int b = 0; b < min(nblk, NS); ++b) {
+            const float* of = fin + (done + nblk - 1 - b) % NS * (FIN_WG / 4);
+            l += m == -INFINITY ? of[0] : of[0] * ex2(of[MH] - m);
+          }
+        }
         const float inv = l == 0.f ? 0.f : a.latent_scale / l;  // l is NaN where a weight is
         const size_t out0 = un.row0 + (direct ? 0 : (size_t)un.p * all_rows);
-        uint8_t* stg = base + O_TILES + head * EPI_PITCH;
-        float4* part = reinterpret_cast<float4*>(part_o) + out0 * (DL / 4) + head;
+        const int row = (warp & 3) * 32 + (lane >> 2);  // and 8, 16, 24 after it
+        const size_t at = (out0 + row) * DL + 8 * (lane & 3);
+        const bool aligned = ((uintptr_t)part_o & 31u) == 0;
 #pragma unroll 1
-        for (int c = (warp >> 2) * (DL / 4); c < ((warp >> 2) + 1) * (DL / 4); c += 32) {
-          float v[32];
-          if (nblk > 0) {
-            tmem_ld32(tbase + lane_off + c, v);
-          } else {
+        for (int c = 32 * set; ok && c < DL; c += 32 * NOUT) {
+          float v[2][16] = {};
+          if (nblk > 0) tmem_ld_frag(tbase + lane_off + c, v);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = 0.f;
-          }
+          for (int k = 0; k < 4; ++k) {  // rows 8 k after the first
+            const float f = __shfl_sync(0xffffffffu, inv, 8 * k + (lane >> 2));
+            uint32_t w[8];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] *= inv;
-          if (direct) {
+            for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(v[k >> 1][4 * (i >> 1) + 2 * (k & 1) + (i & 1)] * f);
+            if (row + 8 * k >= un.live) {  // no query head
+            } else if (direct) {
+              uint32_t h[4];
 #pragma unroll
-            for (int i = 0; i < 32; i += 8) {
-              uint32_t w[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const __nv_bfloat162 x = __floats2bfloat162_rn(v[i + 2 * k], v[i + 2 * k + 1]);
-                w[k] = *reinterpret_cast<const uint32_t*>(&x);
+              for (int i = 0; i < 4; ++i) {
+                const __nv_bfloat162 x = __floats2bfloat162_rn(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+                h[i] = *reinterpret_cast<const uint32_t*>(&x);
               }
-              *reinterpret_cast<uint4*>(stg + 2 * (c + i)) = make_uint4(w[0], w[1], w[2], w[3]);
+              *reinterpret_cast<uint4*>(a.o + at + 8 * k * DL + c) = make_uint4(h[0], h[1], h[2], h[3]);
+            } else {
+              store8(reinterpret_cast<uint32_t*>(part_o + at + 8 * k * DL + c), w, aligned);
             }
-          } else if (head < un.live) {
-#pragma unroll
-            for (int i = 0; i < 32; i += 4)
-              part[(size_t)((c + i) >> 2) * un.live] = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
           }
+          __syncwarp();
         }
-        if (direct) {
-          sync_n(512);
-#pragma unroll 4
-          for (int k = 0; k < 2 * MH / 16; ++k) {  // warp w has rows 8 w .. 8 w + 7, half a row at a time
-            const int row = (MH / 16) * warp + (k >> 1), at = 512 * (k & 1) + 16 * lane;
-            if (row < un.live)
-              *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(a.o + (out0 + row) * DL) + at) =
-                  *reinterpret_cast<const uint4*>(base + O_TILES + row * EPI_PITCH + at);
-          }
-        }
-        if (head < un.live && warp < 4)
+        if (ok && set == 0 && head < un.live)
           (direct ? a.lse : part_lse)[out0 + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+        __syncwarp();
+        if (nblk > 0 && ok) {
+          tc_before();
+          if (lane == 0) bar_arrive(&bs.o_free);
+        }
       }
-      tc_before();
-      __syncthreads();  // O, the totals and the staging are free for the next units
-      tc_after();
-      if (tid == 0 && nblk > 0) bar_arrive_tx(&bs.fin[full % NF], FIN_BYTES);
     }
     done += nblk;
     full += nblk > 0;
@@ -929,67 +953,54 @@ __global__ void __launch_bounds__(T, 1)
   cluster_sync_all();  // the partner no longer reads or arrives on this CTA's shared memory
 }
 
-// The splits of each query head joined: weights exp(lse_p - lse), lse = log sum exp lse_p, in split
-// order. Grid (tile, part of it); a thread has 16 output dims (a sector) of a row, neighbours have
-// neighbouring rows, as the partial sums lie: [split][tile][512 / 4][rows of the tile][4].
-constexpr int COMBINE_T = 128, COMBINE_D = 16;
+// The splits of each query head joined, in split order, as an online softmax over their log-sum-exps
+// (one pass, so that the loads of four splits go out together). A thread per eight output dims.
+constexpr int COMBINE_T = 256;
 __global__ void __launch_bounds__(COMBINE_T)
-    fp4_combine_kernel(const Fp4MlaArgs a, int tiles_per_request, int queries_per_tile, int rows,
-                       const float* __restrict__ part_o, const float* __restrict__ part_lse) {
+    fp4_combine_kernel(const Fp4MlaArgs a, int rows, const float* __restrict__ part_o, const float* __restrict__ part_lse) {
   pdl_wait();
-  const int r = blockIdx.x / tiles_per_request, q0 = (blockIdx.x - r * tiles_per_request) * queries_per_tile;
-  const int live = min(queries_per_tile, a.num_queries - q0) * a.num_heads;
-  const size_t row0 = ((size_t)r * a.num_queries + q0) * a.num_heads;
-  const int e = blockIdx.y * COMBINE_T + threadIdx.x, head = e % live, d = e / live * COMBINE_D;
-  if (d >= DL) return;
-  const float* lses = part_lse + row0 + head;
-  float mx = -INFINITY, nan = 0.f;
+  const int64_t g = (int64_t)blockIdx.x * COMBINE_T + threadIdx.x;
+  const int64_t row = g / (DL / 8);
+  const int c8 = (int)(g % (DL / 8));
+  if (row >= rows) return;
+  float acc[8] = {}, z = 0.f, m = -INFINITY;
+#pragma unroll 4
   for (int p = 0; p < a.splits; ++p) {
-    const float x = __ldg(lses + (size_t)p * rows);
-    mx = fmaxf(mx, x);
-    if (x != x) nan = x;
+    const float x = __ldg(part_lse + (size_t)p * rows + row);
+    const float4* src = reinterpret_cast<const float4*>(part_o + ((size_t)p * rows + row) * DL) + 2 * c8;
+    const float4 u = __ldg(src), v = __ldg(src + 1);
+    const float mx = fmaxf(m, x), ref = mx == -INFINITY ? 0.f : mx;  // (a NaN leaves the maximum alone)
+    const float keep = expf(m - ref), w = expf(x - ref);
+    m = mx;
+    z = z * keep + w;
+    acc[0] = acc[0] * keep + w * u.x;
+    acc[1] = acc[1] * keep + w * u.y;
+    acc[2] = acc[2] * keep + w * u.z;
+    acc[3] = acc[3] * keep + w * u.w;
+    acc[4] = acc[4] * keep + w * v.x;
+    acc[5] = acc[5] * keep + w * v.y;
+    acc[6] = acc[6] * keep + w * v.z;
+    acc[7] = acc[7] * keep + w * v.w;
   }
-  float acc[COMBINE_D] = {};
-  float lse = nan != nan ? nan : mx;
-  if (lse != -INFINITY) {
-    float z = 0.f;
-    for (int p = 0; p < a.splits; ++p) z += expf(__ldg(lses + (size_t)p * rows) - mx);
-    const float inv = 1.f / z;
-    const float4* src = reinterpret_cast<const float4*>(part_o) + row0 * (DL / 4) + (size_t)(d / 4) * live + head;
-#pragma unroll 2
-    for (int p = 0; p < a.splits; ++p) {
-      const float w = expf(__ldg(lses + (size_t)p * rows) - mx) * inv;
+  const float inv = z == 0.f ? 0.f : 1.f / z;
+  uint32_t h[4];
 #pragma unroll
-      for (int i = 0; i < COMBINE_D / 4; ++i) {
-        const float4 v = __ldg(src + (size_t)p * rows * (DL / 4) + i * live);
-        acc[4 * i] += w * v.x;
-        acc[4 * i + 1] += w * v.y;
-        acc[4 * i + 2] += w * v.z;
-        acc[4 * i + 3] += w * v.w;
-      }
-    }
-    lse = mx + logf(z);
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 y = __floats2bfloat162_rn(acc[2 * i] * inv, acc[2 * i + 1] * inv);
+    h[i] = *reinterpret_cast<const uint32_t*>(&y);
   }
-  uint32_t w[COMBINE_D / 2];
-#pragma unroll
-  for (int i = 0; i < COMBINE_D / 2; ++i) {
-    const __nv_bfloat162 x = __floats2bfloat162_rn(acc[2 * i], acc[2 * i + 1]);
-    w[i] = *reinterpret_cast<const uint32_t*>(&x);
-  }
-  uint4* dst = reinterpret_cast<uint4*>(a.o + (row0 + head) * DL + d);
-  dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-  dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
-  if (d == 0) a.lse[row0 + head] = lse;
+  reinterpret_cast<uint4*>(a.o + (size_t)row * DL)[c8] = make_uint4(h[0], h[1], h[2], h[3]);
+  if (c8 == 0) a.lse[row] = z == 0.f ? -INFINITY : m + logf(z);
 }
 
-// Q ([rows][576] bf16) as a 2-D tensor read in boxes of 128 rows x 64 dims, its 16-B chunks XOR-ed
+// Q ([rows][576] bf16) as a 2-D tensor read in boxes of 64 rows x 64 dims, its 16-B chunks XOR-ed
 // with the row % 8; rows past the end read as zeros.
 cudaError_t q_map(CUtensorMap* m, const uint16_t* q, int64_t rows) {
   EncodeTiled fn = encoder();
   if (fn == nullptr) return cudaErrorNotSupported;
   const cuuint64_t dims[2] = {(cuuint64_t)DQK, (cuuint64_t)rows};
   const cuuint64_t strides[1] = {(cuuint64_t)DQK * 2};
-  const cuuint32_t box[2] = {64u, (cuuint32_t)MH};
+  const cuuint32_t box[2] = {64u, (cuuint32_t)BJ};
   const cuuint32_t elem[2] = {1u, 1u};
   const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<uint16_t*>(q), dims, strides, box, elem,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
@@ -1083,9 +1094,8 @@ cudaError_t launch_fp4_mla(const Fp4MlaArgs& a, int32_t num_requests, float* par
     return e;
   }
   if (a.splits == 1) return cudaSuccess;
-  const unsigned parts = (unsigned)((g * a.num_heads * (DL / COMBINE_D) + COMBINE_T - 1) / COMBINE_T);
-  return launch(fp4_combine_kernel, dim3((unsigned)(num_requests * tiles), parts), COMBINE_T, 0, stream, a, tiles, g, rows,
-                (const float*)part, (const float*)part_lse);
+  return launch(fp4_combine_kernel, dim3((unsigned)(((int64_t)rows * (DL / 8) + COMBINE_T - 1) / COMBINE_T)), COMBINE_T,
+                0, stream, a, rows, (const float*)part, (const float*)part_lse);
 }
 
 }  // namespace hs
