@@ -7,17 +7,26 @@
 //   lse = log sum_j exp s_j
 //
 // Tiles. The 128 rows of an MMA are query heads of one request: all heads of as many of its queries
-// as fit (one query of 65 heads or more, eight of 16). A pair of CTAs in a cluster takes (tile,
-// split of the tile's rows) and walks the split in blocks of 64 rows:
+// as fit (one query of 65 heads or more, eight of 16). A pair of CTAs in a cluster takes units (tile,
+// split of the tile's rows), one after the other, and walks each in blocks of 64 rows:
 //   - the S-CTA (even rank) holds Q in tensor memory and computes S = Q . K^T of each block into one
-//     of two buffers; its softmax warpgroups (each 32 of the block's rows, a query head per thread)
-//     run the online softmax and write P as f16 into the O-CTA's shared memory;
+//     of three buffers; its softmax warpgroups (a block each in turn, a query head per thread) run the
+//     online softmax and write P as f16 into the O-CTA's shared memory;
 //   - the O-CTA holds O (128 x 512 in 32 bits, all of its tensor memory) and adds P . V; its
 //     corrector rescales O in the rare blocks that raise a head's reference maximum.
 // In each CTA eight dequantisation warps bring the records they own (eight rows of each block) into
 // shared memory with 16-byte asynchronous copies, two blocks ahead, each in a ring of its own that no
 // other warp touches, and write them as f16 into the CTA's tiles. The roles hand blocks over through
-// mbarriers with bounded waits.
+// mbarriers with bounded waits. The two halves are on two SMs because Q (288 columns), S and O (512) do
+// not fit one tensor memory, nor K, V, Q and P one shared memory; both read every row, the second one
+// from L2.
+//
+// What bounds it (256 requests, 128 heads, 2,048 rows: 176 us, against 74 for its bytes and for its
+// operations): a block takes a pair 1.2 us. The S-CTA's MMAs are 0.63 of that, and its dequantisation
+// warps' round (copies started, records read, tile written) all of it, as K's tile has to go through
+// shared memory three times (record, tile, tensor core) beside P: its pipe is busy three quarters of the
+// time. A unit has ~5 us around its blocks (Q, the first block's way through the pipeline, the
+// read-out), 8 us for a first one, 5 more with the merge of splits.
 //
 // Why these copies: a row is 416 bytes anywhere in the pool. Measured per SM, rows from HBM / L2:
 // four-row tensor gathers 16 / 24 GB/s from one warp and 20 / 33 from four, a bulk copy per row 24 /
@@ -76,12 +85,15 @@ constexpr uint32_t QBOX = MH * 128;
 constexpr int REC = kFp4RopeAt;                    // bytes of a record that go through the rings: codes and scales
 constexpr uint32_t RING = ND * RW * REC;           // a dequantisation warp's ring
 constexpr uint32_t S_TILES = 0;                    // latents of K; Q's are staged over them before the first block
-constexpr int NR = 5;                              // RoPE tiles, copied straight to their places
+// RoPE values are copied straight to their tiles: a block's copies start when the tensor core is known to
+// be done with the block five before it. (Through the rings like the rest: 182 us instead of 176; with
+// four tiles, and so later copies, 183.)
+constexpr int NR = 5;
 constexpr uint32_t S_ROPE = NT * TILE;             // (Q's are staged over two of them)
 constexpr uint32_t S_RAW = S_ROPE + NR * KV_ATOM;
 static_assert(ATOMS * QBOX <= NT * TILE && QBOX == 2 * KV_ATOM, "Q's staging");
 constexpr uint32_t S_REF = S_RAW + NDEQ * RING;  // the reference maxima, handed from block to block
-constexpr uint32_t S_MASK = S_REF + MH * 4;     // a byte per block and dequantisation warp: its rows that exist
+constexpr uint32_t S_MASK = S_REF + MH * 4;     // a byte per block and dequantisation warp: which of its rows exist
 constexpr uint32_t S_END = S_MASK + MASKS * NDEQ;
 constexpr uint32_t O_TILES = 0, O_RAW = NT * TILE;
 constexpr uint32_t O_P = (O_RAW + NDEQ * RING + 1023u) & ~1023u;
@@ -93,6 +105,9 @@ constexpr int NF = 3;  // units whose totals are kept: P's two buffers let the S
 constexpr uint32_t O_END = O_FIN + NF * NS * FIN_WG;
 constexpr uint32_t SMEM_BYTES = (S_END > O_END ? S_END : O_END) + 1024;  // + alignment slack
 static_assert(SMEM_BYTES <= 227 * 1024 - 1024, "shared memory of a CTA");
+// A reference maximum stays until it is passed by 2^15, so that P < 65504 in f16, whose precision is the
+// same there. (At 2^8 a few heads of a tile were rescaled in the course of 2,048 rows, 2 us each time:
+// 182 us instead of 189 for 256 requests.)
 constexpr float kRescaleLog2 = 15.f;
 constexpr uint32_t kIdescQK = idesc(BJ, MH, false);                              // f16 latents
 constexpr uint32_t kIdescRope = kIdescQK | (1u << 7) | (1u << 10);               // bf16 RoPE
@@ -236,16 +251,19 @@ struct Rows {
   int n, j0;             // rows of this split; the split's first row in the tile's list
   // window: the list is tokens 0 .. kept - 1, then from `start`
   int kept, start, page_size;
+  uint32_t page_mul, page_shift;  // t / page_size = t page_mul >> page_shift for 0 <= t < 2^31
 
   __device__ __forceinline__ int token(int j) const { return j0 + j < kept ? j0 + j : start + (j0 + j - kept); }
+  __device__ __forceinline__ int page_of(int t) const { return (int)((uint64_t)(uint32_t)t * page_mul >> page_shift); }
   // what the table holds for row j (loaded ahead), and the pool row that it means (-1: none)
   __device__ __forceinline__ int32_t raw(int j) const {
     if (j >= n) return -1;
-    return __ldg(table + (kWin ? token(j) / page_size : j0 + j));
+    return __ldg(table + (kWin ? page_of(token(j)) : j0 + j));
   }
   __device__ __forceinline__ int32_t row(int32_t raw, int j) const {
     if (raw < 0) return -1;
-    const int64_t r = kWin ? (int64_t)raw * page_size + token(j) % page_size : raw;
+    const int t = kWin ? token(j) : 0;
+    const int64_t r = kWin ? (int64_t)(raw - page_of(t)) * page_size + t : raw;
     return r < pool_rows ? (int32_t)r : -1;
   }
 };
@@ -294,8 +312,8 @@ __device__ __forceinline__ void copy_rows(uint32_t dst, uint32_t rope, int32_t y
 
 // What a lane reads of its warp's eight rows. Step s covers four rows (4 (s / 2) ..) and half of
 // their latent dims: lane = (row of the four, 32 dims `it`), placed so that the eight lanes of a load
-// or store phase have four rows and both halves of a line: the reads (rows 416 or 288 bytes apart)
-// and, through the tile's swizzle, the writes then meet every bank once.
+// or store phase have four rows and both halves of a line: the reads (rows 288 bytes apart) and,
+// through the tile's swizzle, the writes then meet every bank once.
 struct Held {
   uint4 codes[4];
   uint16_t scales[4];
@@ -448,6 +466,8 @@ __device__ __forceinline__ Unit<kWin> unit_of(const Fp4MlaArgs& a, int u, int ti
   if (kWin) {
     x.rows.table = a.pages + (size_t)r * a.max_pages;
     x.rows.page_size = a.page_size;
+    x.rows.page_mul = a.page_mul;
+    x.rows.page_shift = a.page_shift;
     x.seq_len = a.seq_lens[r];
     const bool bad = x.seq_len < 0 || x.seq_len > (int64_t)a.max_pages * a.page_size;
     if (bad && flag) atomicOr(err, HS_FLAG_SEQLEN);
@@ -573,7 +593,7 @@ __global__ void __launch_bounds__(T, 1)
   bool ok = true;
   int done = 0, full = 0;  // blocks, and units with blocks, before this one
 #pragma unroll 1
-  for (int u = blockIdx.x >> 1; ok && u < units; u += pairs) {
+  for (int u = blockIdx.x >> 1; u < units; u += pairs) {
     const Unit<kWin> un = unit_of<kWin>(a, u, tiles_per_request, queries_per_tile, tid == 0, err);
     const int nblk = un.nblk;
     if (rank == 0) {
@@ -692,8 +712,8 @@ __global__ void __launch_bounds__(T, 1)
             if (!ok) break;
             if (b > 0) m_run = s_ref[head];
           }
-          // Lazy rescale: a head keeps its reference until a block's maximum passes it by 2^8, so P
-          // stays below 2^8 and O is rescaled only on those rare jumps. (NaN scores leave it alone.)
+          // Lazy rescale: a head keeps its reference until a block's maximum passes it by 2^15, and O is
+          // rescaled only on those rare jumps. (NaN scores leave it alone.)
           const float m_new = bm > m_run + kRescaleLog2 || m_run == -INFINITY ? fmaxf(m_run, bm) : m_run;
           s_ref[head] = m_new;
           __syncwarp();
@@ -795,7 +815,7 @@ __global__ void __launch_bounds__(T, 1)
         // corrector: where a reference maximum of the warp's heads rose, rescale O once P . V of the
         // block before is done
 #pragma unroll 1
-        for (int b = 0; b < nblk; ++b) {
+        for (int b = 0; ok && b < nblk; ++b) {
           const int g = done + b;
           ok = __all_sync(0xffffffffu, ready_or_wait<true>(bs.p_full, 2, g, abort));
           if (!ok) break;
@@ -860,6 +880,7 @@ __global__ void __launch_bounds__(T, 1)
         // warps that have nothing else to do wait at a barrier of the hardware, not at the mbarriers:
         // their looks slowed the others down (about 1 us more from P to P . V).
         ok = sync_and(ok, 32 * 4 * NOUT);
+        if (!ok) break;  // (all of them: one that gave up further down comes here once more)
         const int set = warp < 4 ? 0 : warp >= 16 && warp < 20 ? 1 : 2;
         const bool direct = a.splits == 1;
         float l = 0.f, m = -INFINITY;
@@ -915,7 +936,9 @@ __global__ void __launch_bounds__(T, 1)
           if (lane == 0) bar_arrive(&bs.o_free);
         }
       }
+      if (!ok && !out_warp) break;
     }
+    if (!ok && rank == 0) break;
     done += nblk;
     full += nblk > 0;
   }
@@ -954,7 +977,7 @@ __global__ void __launch_bounds__(T, 1)
 }
 
 // The splits of each query head joined, in split order, as an online softmax over their log-sum-exps
-// (one pass, so that the loads of four splits go out together). A thread per eight output dims.
+// (one pass, and the loads of two splits go out together). A thread per eight output dims.
 constexpr int COMBINE_T = 256;
 __global__ void __launch_bounds__(COMBINE_T)
     fp4_combine_kernel(const Fp4MlaArgs a, int rows, const float* __restrict__ part_o, const float* __restrict__ part_lse) {
@@ -964,7 +987,7 @@ __global__ void __launch_bounds__(COMBINE_T)
   const int c8 = (int)(g % (DL / 8));
   if (row >= rows) return;
   float acc[8] = {}, z = 0.f, m = -INFINITY;
-#pragma unroll 4
+#pragma unroll 2
   for (int p = 0; p < a.splits; ++p) {
     const float x = __ldg(part_lse + (size_t)p * rows + row);
     const float4* src = reinterpret_cast<const float4*>(part_o + ((size_t)p * rows + row) * DL) + 2 * c8;
@@ -1030,12 +1053,12 @@ int tiles_per_request(int num_heads, int num_queries) {
 
 }  // namespace
 
-// In tenths of a block's time (1.3 us): a wave of units takes their blocks and 5 blocks' time around
+// In tenths of a block's time (1.2 us): a wave of units takes their blocks and 5 blocks' time around
 // them; splitting at all adds 4 (partial outputs in 32 bits, the merge kernel and its launch), and 4
 // more per unit and pair for the partials' traffic. Measured (us, 128 heads, 2,048 rows): one request
-// 51 whole, 28 in 4 splits, 23 in 12; 16 requests 53, 32 in 4, 46 in 6 (two waves); 32 requests 52,
-// 43 in 2, 59 in 3 (two waves); 64 requests 56, 78 in 2. Of 512 rows: 8 requests 24, 22 in 4; 32
-// requests 24, 28 in 2.
+// 48 whole, 25 in 4 splits, 20 in 16; 16 requests 49, 27 in 4, 38 in 6 (two waves); 32 requests 49,
+// 36 in 2, 50 in 3 (two waves); 64 requests 50, 63 in 2. Of 512 rows: 8 requests 20.5, 18 in 4; 32
+// requests 21, 22 in 2.
 int32_t fp4_mla_splits(int32_t num_requests, int32_t num_heads, int32_t num_queries, int64_t rows) {
   int slots = 0;
   if (pairs_resident(&slots) != cudaSuccess) return 1;
@@ -1057,8 +1080,17 @@ size_t fp4_mla_workspace_bytes(int32_t num_requests, int32_t num_heads, int32_t 
   return splits == 1 ? 0 : (size_t)splits * num_requests * num_queries * num_heads * (DL + 1) * sizeof(float);
 }
 
-cudaError_t launch_fp4_mla(const Fp4MlaArgs& a, int32_t num_requests, float* part, uint32_t* err,
+cudaError_t launch_fp4_mla(const Fp4MlaArgs& args, int32_t num_requests, float* part, uint32_t* err,
                            cudaStream_t stream) {
+  // division by the page size as a product: with 2^(s - 1) < d <= 2^s and m = floor(2^(31 + s) / d) + 1,
+  // m d is above 2^(31 + s) by at most d <= 2^s, so that t m / 2^(31 + s) is above t / d by less than
+  // 1 / d for every t < 2^31
+  Fp4MlaArgs a = args;
+  if (a.seq_lens != nullptr) {
+    a.page_shift = 31;
+    while (((int64_t)1 << (a.page_shift - 31)) < a.page_size) ++a.page_shift;
+    a.page_mul = (uint32_t)(((uint64_t)1 << a.page_shift) / (uint64_t)a.page_size + 1);
+  }
   const bool win = a.seq_lens != nullptr;
   const auto kernel = win ? fp4_mla_kernel<true> : fp4_mla_kernel<false>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
