@@ -70,7 +70,7 @@ struct Fp4MlaArgs {
   const int32_t* seq_lens;  // window: lengths [R], each with its last num_queries tokens the queries'
   const int32_t* pages;     // [R, max_pages], -1: not on the device
   int32_t page_size, max_pages, window, sinks;
-  uint32_t page_mul, page_shift;  // filled in by launch_fp4_mla
+  uint32_t page_mul, page_shift, pool_pages;  // filled in by launch_fp4_mla
 };
 
 cudaError_t launch_fp4_pack(const Fp4RowsArgs& a, uint32_t* err, cudaStream_t stream);

@@ -247,7 +247,7 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 template <bool kWin>
 struct Rows {
   const int32_t* table;  // the request's rows, or its pages
-  int64_t pool_rows;
+  uint32_t pool_rows, pool_pages;  // below 2^31; window: pages that begin inside the pool
   int n, j0;             // rows of this split; the split's first row in the tile's list
   // window: the list is tokens 0 .. kept - 1, then from `start`
   int kept, start, page_size;
@@ -261,10 +261,10 @@ struct Rows {
     return __ldg(table + (kWin ? page_of(token(j)) : j0 + j));
   }
   __device__ __forceinline__ int32_t row(int32_t raw, int j) const {
-    if (raw < 0) return -1;
-    const int t = kWin ? token(j) : 0;
-    const int64_t r = kWin ? (int64_t)(raw - page_of(t)) * page_size + t : raw;
-    return r < pool_rows ? (int32_t)r : -1;
+    if (!kWin) return (uint32_t)raw < pool_rows ? raw : -1;
+    const int t = token(j), page = page_of(t);
+    const uint32_t r = (uint32_t)(raw - page) * (uint32_t)page_size + (uint32_t)t;  // below 2^32 for a page inside
+    return (uint32_t)raw < pool_pages && r < pool_rows ? (int32_t)r : -1;
   }
 };
 
@@ -337,15 +337,21 @@ __device__ __forceinline__ void write_rows(const Held& h, uint8_t* group, int la
   const int in4 = (lane >> 1) & 3;
   const uint32_t at0 = smem_u32(group) + (lane >> 3) * KV_ATOM + in4 * 128 + (lane & 1) * 64 + in4 * 16;
   const uint32_t at1 = (at0 ^ 64u) + 512u;
+  uint32_t scales[4] = {h.scales[0], h.scales[1], h.scales[2], h.scales[3]};
+  if (!kS) {  // V: zeros for NaN (0x7F, 0xFF; see above), which are few: one look at all of them. K keeps it
+    const uint32_t x = (((scales[0] | scales[1] << 16) & 0x7F7F7F7Fu) + 0x01010101u) |
+                       (((scales[2] | scales[3] << 16) & 0x7F7F7F7Fu) + 0x01010101u);
+    if (x & 0x80808080u)
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        if ((scales[s] & 0x7Fu) == 0x7Fu) scales[s] &= 0xFF00u;
+        if ((scales[s] & 0x7F00u) == 0x7F00u) scales[s] &= 0xFFu;
+      }
+  }
 #pragma unroll
   for (int s = 0; s < 4; ++s) {
     const uint32_t w[4] = {h.codes[s].x, h.codes[s].y, h.codes[s].z, h.codes[s].w};
-    uint32_t two = h.scales[s];  // the scales of 16 dims each
-    if (!kS) {  // V: no NaN (see above); K keeps it
-      if ((two & 0x7Fu) == 0x7Fu) two &= 0xFF00u;
-      if ((two & 0x7F00u) == 0x7F00u) two &= 0xFFu;
-    }
-    const __half2_raw raw = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
+    const __half2_raw raw = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)scales[s], __NV_E4M3);  // of 16 dims each
     const __half2 pair = raw, sc[2] = {__low2half2(pair), __high2half2(pair)};
     uint4 v[4];  // the lane's 32 dims, a chunk of eight each
 #pragma unroll
@@ -379,7 +385,7 @@ __device__ __forceinline__ bool run_dequant(const Rows<kWin>& rows, const uint8_
   // slots of the ring: the next one to fill, and the next one to read
   const uint32_t ring0 = smem_u32(ring) + (lane >> 3) * REC + 16 * (lane & 7), ring_end = ring0 + ND * RW * REC;
   const uint32_t rope0 = kS ? smem_u32(rope) + RW * wq * 128 + (lane >> 3) * 128 + (((lane & 7) ^ (lane >> 3)) << 4) : 0u;
-  uint32_t fill = ring0;
+  uint32_t fill = ring0, rope_fill = rope0 + done % NR * KV_ATOM;
   const uint8_t* read = ring;
   auto start = [&](int32_t raw, int b) {  // the copies of block b (one group of copies, empty past the end)
     if (b < nblk) {
@@ -390,7 +396,9 @@ __device__ __forceinline__ bool run_dequant(const Rows<kWin>& rows, const uint8_
         const uint32_t mask = __ballot_sync(0xffffffffu, y >= 0);
         if (lane == 0) masks[((done + b) % MASKS) * NDEQ + wq] = (uint8_t)mask;
       }
-      copy_rows<kS>(fill, rope0 + (done + b) % NR * KV_ATOM, y, pool, lane);
+      copy_rows<kS>(fill, rope_fill, y, pool, lane);
+      rope_fill += KV_ATOM;
+      if (rope_fill == rope0 + NR * KV_ATOM) rope_fill = rope0;
       fill += RW * REC;
       if (fill == ring_end) fill = ring0;
     }
@@ -461,11 +469,12 @@ __device__ __forceinline__ Unit<kWin> unit_of(const Fp4MlaArgs& a, int u, int ti
   x.live = nq * a.num_heads;
   x.row0 = ((size_t)r * a.num_queries + x.first_query) * a.num_heads;
   // the tile's rows: every row that some query of the tile sees
-  x.rows.pool_rows = a.pool_rows;
+  x.rows.pool_rows = (uint32_t)a.pool_rows;
   int total;
   if (kWin) {
     x.rows.table = a.pages + (size_t)r * a.max_pages;
     x.rows.page_size = a.page_size;
+    x.rows.pool_pages = a.pool_pages;
     x.rows.page_mul = a.page_mul;
     x.rows.page_shift = a.page_shift;
     x.seq_len = a.seq_lens[r];
@@ -1087,6 +1096,7 @@ cudaError_t launch_fp4_mla(const Fp4MlaArgs& args, int32_t num_requests, float* 
   // 1 / d for every t < 2^31
   Fp4MlaArgs a = args;
   if (a.seq_lens != nullptr) {
+    a.pool_pages = (uint32_t)((a.pool_rows + a.page_size - 1) / a.page_size);
     a.page_shift = 31;
     while (((int64_t)1 << (a.page_shift - 31)) < a.page_size) ++a.page_shift;
     a.page_mul = (uint32_t)(((uint64_t)1 << a.page_shift) / (uint64_t)a.page_size + 1);
