@@ -173,7 +173,8 @@ hs_status fp4_mla(hs::Fp4MlaArgs a, int32_t num_requests, int32_t num_heads, int
                   uint16_t* o, float* lse, void* workspace, size_t workspace_bytes, uint32_t* error_flags,
                   hs_stream_t stream) {
   if (num_requests < 0 || !fp4_mla_shape_ok(num_requests ? num_requests : 1, num_heads, num_queries, splits) ||
-      pool_rows < 1 || pool_rows > INT32_MAX || !latent_scale_ok(latent_scale) || !std::isfinite(sm_scale))
+      pool_rows < 1 || pool_rows > INT32_MAX || !latent_scale_ok(latent_scale) ||
+      !std::isfinite(sm_scale * latent_scale * 1.4426950408889634f))
     return HS_ERR_INVALID_ARG;
   if (num_requests == 0) return HS_OK;
   if (!q || !kv_pool || !o || !lse || !error_flags) return HS_ERR_INVALID_ARG;

@@ -447,25 +447,33 @@ __device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
   return (0xFFFFFFFFu >> (32 - (hi - lo))) << lo;
 }
 
-// A unit of work: a tile's split. Every thread of a pair computes it from its number.
+// The tiles' numbers: the first `whole` tiles are a unit each, the others, whose query heads begin with
+// row `split_row` of q, o and lse and are `split_rows`, a unit per split.
+struct Tiles {
+  int per_request, queries;  // of a request; of a tile
+  int units, whole, split_row, split_rows;
+};
+
+// A unit of work: a tile or one of its splits. Every thread of a pair computes it from its number.
 template <bool kWin>
 struct Unit {
   Rows<kWin> rows;
   int nblk;          // blocks of this split
   int live;          // query heads of the tile
   size_t row0;       // the first one's row of q, o and lse
-  int p;             // the split
+  int splits, p;     // the tile's, and this one
   int first_query;
   int64_t seq_len;   // window
 };
 template <bool kWin>
-__device__ __forceinline__ Unit<kWin> unit_of(const Fp4MlaArgs& a, int u, int tiles_per_request, int queries_per_tile,
-                                              bool flag, uint32_t* err) {
+__device__ __forceinline__ Unit<kWin> unit_of(const Fp4MlaArgs& a, const Tiles& ts, int u, bool flag, uint32_t* err) {
   Unit<kWin> x;
-  const int tile = u / a.splits, r = tile / tiles_per_request;
-  x.p = u - tile * a.splits;
-  x.first_query = (tile - r * tiles_per_request) * queries_per_tile;
-  const int nq = min(queries_per_tile, a.num_queries - x.first_query);
+  x.splits = u < ts.whole ? 1 : a.splits;
+  const int v = u < ts.whole ? 0 : u - ts.whole, tile = u < ts.whole ? u : ts.whole + v / a.splits;
+  x.p = v - v / a.splits * a.splits;
+  const int r = tile / ts.per_request;
+  x.first_query = (tile - r * ts.per_request) * ts.queries;
+  const int nq = min(ts.queries, a.num_queries - x.first_query);
   x.live = nq * a.num_heads;
   x.row0 = ((size_t)r * a.num_queries + x.first_query) * a.num_heads;
   // the tile's rows: every row that some query of the tile sees
@@ -490,7 +498,7 @@ __device__ __forceinline__ Unit<kWin> unit_of(const Fp4MlaArgs& a, int u, int ti
     x.rows.table = a.out_rows + (size_t)r * a.top_k;
     total = a.top_k;
   }
-  const int all = (int)(((int64_t)total + BJ - 1) / BJ), per = (all + a.splits - 1) / a.splits;
+  const int all = (int)(((int64_t)total + BJ - 1) / BJ), per = (all + x.splits - 1) / x.splits;
   x.nblk = max(0, min(per, all - x.p * per));
   x.rows.j0 = x.p * per * BJ;
   x.rows.n = x.nblk > 0 ? min(total - x.rows.j0, x.nblk * BJ) : 0;
@@ -527,7 +535,7 @@ __device__ __forceinline__ void prefetch_q(const CUtensorMap* tm_q, size_t row0)
 
 template <bool kWin>
 __global__ void __launch_bounds__(T, 1)
-    fp4_mla_kernel(const Fp4MlaArgs a, int tiles_per_request, int queries_per_tile, int units, int all_rows,
+    fp4_mla_kernel(const Fp4MlaArgs a, const Tiles ts,
                    const __grid_constant__ CUtensorMap tm_q, float* __restrict__ part_o, float* __restrict__ part_lse,
                    uint32_t* __restrict__ err) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -569,7 +577,7 @@ __global__ void __launch_bounds__(T, 1)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     pdl_wait();
     if (rank == 0) {
-      const Unit<kWin> first = unit_of<kWin>(a, blockIdx.x >> 1, tiles_per_request, queries_per_tile, false, err);
+      const Unit<kWin> first = unit_of<kWin>(a, ts, blockIdx.x >> 1, false, err);
       if (first.nblk > 0) {
         request_q(&tm_q, first.row0, 0, base, bs);
         s_requested = 1;
@@ -602,8 +610,8 @@ __global__ void __launch_bounds__(T, 1)
   bool ok = true;
   int done = 0, full = 0;  // blocks, and units with blocks, before this one
 #pragma unroll 1
-  for (int u = blockIdx.x >> 1; u < units; u += pairs) {
-    const Unit<kWin> un = unit_of<kWin>(a, u, tiles_per_request, queries_per_tile, tid == 0, err);
+  for (int u = blockIdx.x >> 1; u < ts.units; u += pairs) {
+    const Unit<kWin> un = unit_of<kWin>(a, ts, u, tid == 0, err);
     const int nblk = un.nblk;
     if (rank == 0) {
       // ================================ S-CTA ================================
@@ -771,10 +779,10 @@ __global__ void __launch_bounds__(T, 1)
         // (tensor memory starts at 0: all of it is allocated here)
         const bool one = elected();
         const uint64_t k0 = mdesc(smem_u32(base + S_TILES), 16, 1024), r0 = mdesc(smem_u32(base + S_ROPE), 16, 1024);
-        const bool more = u + pairs < units;
+        const bool more = u + pairs < ts.units;
         Unit<kWin> next;
         next.nblk = 0;
-        if (more) next = unit_of<kWin>(a, u + pairs, tiles_per_request, queries_per_tile, false, err);
+        if (more) next = unit_of<kWin>(a, ts, u + pairs, false, err);
         if (one && next.nblk > 0) prefetch_q(&tm_q, next.row0);
         bool go = __all_sync(0xffffffffu, nblk == 0 || ready_or_wait(&bs.q_full, 1, (int)q_phase, abort));
 #pragma unroll 1
@@ -891,7 +899,7 @@ __global__ void __launch_bounds__(T, 1)
         ok = sync_and(ok, 32 * 4 * NOUT);
         if (!ok) break;  // (all of them: one that gave up further down comes here once more)
         const int set = warp < 4 ? 0 : warp >= 16 && warp < 20 ? 1 : 2;
-        const bool direct = a.splits == 1;
+        const bool direct = un.splits == 1;
         float l = 0.f, m = -INFINITY;
         if (nblk > 0) {
           const int k = full % NF;
@@ -908,7 +916,7 @@ __global__ void __launch_bounds__(T, 1)
           }
         }
         const float inv = l == 0.f ? 0.f : a.latent_scale / l;  // l is NaN where a weight is
-        const size_t out0 = un.row0 + (direct ? 0 : (size_t)un.p * all_rows);
+        const size_t out0 = direct ? un.row0 : un.row0 - ts.split_row + (size_t)un.p * ts.split_rows;
         const int row = (warp & 3) * 32 + (lane >> 2);  // and 8, 16, 24 after it
         const size_t at = (out0 + row) * DL + 8 * (lane & 3);
         const bool aligned = ((uintptr_t)part_o & 31u) == 0;
@@ -985,11 +993,11 @@ __global__ void __launch_bounds__(T, 1)
   cluster_sync_all();  // the partner no longer reads or arrives on this CTA's shared memory
 }
 
-// The splits of each query head joined, in split order, as an online softmax over their log-sum-exps
+// The splits of query heads row0 .. row0 + rows - 1 joined, in split order, as an online softmax over their log-sum-exps
 // (one pass, and the loads of two splits go out together). A thread per eight output dims.
 constexpr int COMBINE_T = 256;
 __global__ void __launch_bounds__(COMBINE_T)
-    fp4_combine_kernel(const Fp4MlaArgs a, int rows, const float* __restrict__ part_o, const float* __restrict__ part_lse) {
+    fp4_combine_kernel(const Fp4MlaArgs a, int row0, int rows, const float* __restrict__ part_o, const float* __restrict__ part_lse) {
   pdl_wait();
   const int64_t g = (int64_t)blockIdx.x * COMBINE_T + threadIdx.x;
   const int64_t row = g / (DL / 8);
@@ -1021,8 +1029,8 @@ __global__ void __launch_bounds__(COMBINE_T)
     const __nv_bfloat162 y = __floats2bfloat162_rn(acc[2 * i] * inv, acc[2 * i + 1] * inv);
     h[i] = *reinterpret_cast<const uint32_t*>(&y);
   }
-  reinterpret_cast<uint4*>(a.o + (size_t)row * DL)[c8] = make_uint4(h[0], h[1], h[2], h[3]);
-  if (c8 == 0) a.lse[row] = z == 0.f ? -INFINITY : m + logf(z);
+  reinterpret_cast<uint4*>(a.o + (size_t)(row0 + row) * DL)[c8] = make_uint4(h[0], h[1], h[2], h[3]);
+  if (c8 == 0) a.lse[row0 + row] = z == 0.f ? -INFINITY : m + logf(z);
 }
 
 // Q ([rows][576] bf16) as a 2-D tensor read in boxes of 64 rows x 64 dims, its 16-B chunks XOR-ed
@@ -1062,12 +1070,16 @@ int tiles_per_request(int num_heads, int num_queries) {
 
 }  // namespace
 
-// In tenths of a block's time (1.2 us): a wave of units takes their blocks and 5 blocks' time around
+// Tiles that are not split: all, or the rounds in which every pair takes one. (A round's units end
+// together, so that splitting them would only add partial outputs: 64 requests of 2,048 rows 50 us whole,
+// 63 in 2; it is the last, partly filled round that splits fill.)
+static int whole_tiles(int64_t tiles, int splits, int slots) { return (int)(splits == 1 ? tiles : tiles / slots * slots); }
+
+// In tenths of a block's time (1.2 us): a round of units takes their blocks and 5 blocks' time around
 // them; splitting at all adds 4 (partial outputs in 32 bits, the merge kernel and its launch), and 4
 // more per unit and pair for the partials' traffic. Measured (us, 128 heads, 2,048 rows): one request
-// 48 whole, 25 in 4 splits, 20 in 16; 16 requests 49, 27 in 4, 38 in 6 (two waves); 32 requests 49,
-// 36 in 2, 50 in 3 (two waves); 64 requests 50, 63 in 2. Of 512 rows: 8 requests 20.5, 18 in 4; 32
-// requests 21, 22 in 2.
+// 48 whole, 25 in 4 splits, 20 in 16; 16 requests 49, 27 in 4, 38 in 6 (two rounds); 32 requests 49,
+// 36 in 2, 50 in 3 (two rounds). Of 512 rows: 8 requests 20.5, 18 in 4; 32 requests 21, 22 in 2.
 int32_t fp4_mla_splits(int32_t num_requests, int32_t num_heads, int32_t num_queries, int64_t rows) {
   int slots = 0;
   if (pairs_resident(&slots) != cudaSuccess) return 1;
@@ -1075,8 +1087,10 @@ int32_t fp4_mla_splits(int32_t num_requests, int32_t num_heads, int32_t num_quer
   const int64_t blocks = (rows + BJ - 1) / BJ;
   int64_t best = 1, best_cost = INT64_MAX;
   for (int64_t s = 1; s <= HS_MAX_MLA_SPLITS && s <= blocks; ++s) {
-    const int64_t units = tiles * s, waves = (units + slots - 1) / slots;
-    const int64_t cost = 10 * waves * ((blocks + s - 1) / s + 5) + (s > 1 ? 40 + 40 * units / slots : 0);
+    const int64_t whole = whole_tiles(tiles, (int)s, slots), units = (tiles - whole) * s;
+    if (s > 1 && units == 0) break;
+    const int64_t rounds = (whole + slots - 1) / slots, more = (units + slots - 1) / slots;
+    const int64_t cost = 10 * (rounds * (blocks + 5) + more * ((blocks + s - 1) / s + 5)) + (s > 1 ? 40 + 40 * units / slots : 0);
     if (cost < best_cost) {
       best = s;
       best_cost = cost;
@@ -1085,8 +1099,13 @@ int32_t fp4_mla_splits(int32_t num_requests, int32_t num_heads, int32_t num_quer
   return (int32_t)best;
 }
 
+// (Fewer tiles are split than there are pairs.)
 size_t fp4_mla_workspace_bytes(int32_t num_requests, int32_t num_heads, int32_t num_queries, int32_t splits) {
-  return splits == 1 ? 0 : (size_t)splits * num_requests * num_queries * num_heads * (DL + 1) * sizeof(float);
+  if (splits == 1) return 0;
+  size_t rows = (size_t)num_requests * num_queries * num_heads;
+  int pairs = 0;
+  if (pairs_resident(&pairs) == cudaSuccess && rows > (size_t)pairs * MH) rows = (size_t)pairs * MH;
+  return splits * rows * (DL + 1) * sizeof(float);
 }
 
 cudaError_t launch_fp4_mla(const Fp4MlaArgs& args, int32_t num_requests, float* part, uint32_t* err,
@@ -1113,11 +1132,17 @@ cudaError_t launch_fp4_mla(const Fp4MlaArgs& args, int32_t num_requests, float* 
     (void)cudaGetLastError();
     return e;
   }
-  const int tiles = tiles_per_request(a.num_heads, a.num_queries), g = queries_per_tile(a.num_heads, a.num_queries);
-  const int units = num_requests * tiles * a.splits;
-  float* part_lse = part ? part + (size_t)a.splits * rows * DL : nullptr;
+  Tiles ts;
+  ts.per_request = tiles_per_request(a.num_heads, a.num_queries);
+  ts.queries = queries_per_tile(a.num_heads, a.num_queries);
+  const int tiles = num_requests * ts.per_request;
+  ts.whole = whole_tiles(tiles, a.splits, pairs);
+  ts.units = ts.whole + (tiles - ts.whole) * a.splits;
+  ts.split_row = (ts.whole / ts.per_request * a.num_queries + ts.whole % ts.per_request * ts.queries) * a.num_heads;
+  ts.split_rows = rows - ts.split_row;
+  float* part_lse = part ? part + (size_t)a.splits * ts.split_rows * DL : nullptr;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2u * (unsigned)(units < pairs ? units : pairs));
+  cfg.gridDim = dim3(2u * (unsigned)(ts.units < pairs ? ts.units : pairs));
   cfg.blockDim = dim3(T);
   cfg.dynamicSmemBytes = SMEM_BYTES;
   cfg.stream = stream;
@@ -1130,14 +1155,14 @@ cudaError_t launch_fp4_mla(const Fp4MlaArgs& args, int32_t num_requests, float* 
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.numAttrs = 2;
-  e = cudaLaunchKernelEx(&cfg, kernel, a, tiles, g, units, rows, tm_q, part, part_lse, err);
+  e = cudaLaunchKernelEx(&cfg, kernel, a, ts, tm_q, part, part_lse, err);
   if (e != cudaSuccess) {
     (void)cudaGetLastError();
     return e;
   }
-  if (a.splits == 1) return cudaSuccess;
-  return launch(fp4_combine_kernel, dim3((unsigned)(((int64_t)rows * (DL / 8) + COMBINE_T - 1) / COMBINE_T)), COMBINE_T,
-                0, stream, a, rows, (const float*)part, (const float*)part_lse);
+  if (ts.whole == tiles) return cudaSuccess;
+  return launch(fp4_combine_kernel, dim3((unsigned)(((int64_t)ts.split_rows * (DL / 8) + COMBINE_T - 1) / COMBINE_T)), COMBINE_T,
+                0, stream, a, ts.split_row, ts.split_rows, (const float*)part, (const float*)part_lse);
 }
 
 }  // namespace hs

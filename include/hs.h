@@ -538,7 +538,7 @@ HS_API hs_status hs_fp4_unpack_rows(int32_t n, const uint8_t* pool, int64_t pool
 /* Splits (1..HS_MAX_MLA_SPLITS) that suit a call of num_queries queries per request (1 for
  * hs_fp4_sparse_mla_decode) over up to `rows` rows each (top_k; or window + sinks + num_queries - 1)
  * on the current device, and the workspace a call with that many splits needs (0 for one split, and
- * for a shape that the calls refuse). Host only. */
+ * for a shape that the calls refuse), both for the current device. Host only. */
 HS_API int32_t hs_fp4_mla_splits(int32_t num_requests, int32_t num_heads, int32_t num_queries, int64_t rows);
 HS_API size_t hs_fp4_mla_workspace_bytes(int32_t num_requests, int32_t num_heads, int32_t num_queries,
                                          int32_t splits);
@@ -551,11 +551,18 @@ HS_API size_t hs_fp4_mla_workspace_bytes(int32_t num_requests, int32_t num_heads
  *   q [R, num_heads, 576] bf16 bits (num_heads 1..128), kv_pool [pool_rows, 416] with pool_rows <
  *   2^31, o [R, num_heads, 512] bf16 bits: device, 16-byte aligned; out_rows [R, top_k], top_k <=
  *   HS_MAX_TOP_K, lse [R, num_heads] fp32: device
- *   splits (1..HS_MAX_MLA_SPLITS) divides each request's rows over more CTAs; hs_fp4_mla_splits
- *   suggests a number. workspace: hs_fp4_mla_workspace_bytes(R, num_heads, 1, splits) device bytes,
- *   16-byte aligned; calls that share it must be ordered.
+ *   splits (1..HS_MAX_MLA_SPLITS) divides requests' rows over more CTA pairs where not every pair
+ *   has a request (or a tile of 128 of its queries' heads) of its own: all of them below as many
+ *   as there are pairs, those of the last round above. Their partial results, in 32 bits, are
+ *   merged by a second kernel. hs_fp4_mla_splits suggests a number. workspace:
+ *   hs_fp4_mla_workspace_bytes(R, num_heads, 1, splits) device bytes, 16-byte aligned, contents
+ *   of no matter; calls that share it must be ordered.
  *   error_flags: device uint32, HS_FLAG_* bits OR-ed in.
- * No allocation, no synchronisation; graph-capturable. num_requests == 0 is a no-op. */
+ *   q's latent part goes through f16: 65520 and more is infinite there, values below 2^-14 are off by
+ *   up to 2^-25. sm_scale x latent_scale x log2(e) has to be finite in fp32. An MMA pipeline that
+ *   stands still for 100 ms sets HS_FLAG_TIMEOUT and ends the call, its outputs not valid.
+ * One or two kernel launches (no second one where nothing is split); no allocation, no
+ * synchronisation; graph-capturable. num_requests == 0 is a no-op. */
 HS_API hs_status hs_fp4_sparse_mla_decode(int32_t num_requests, int32_t num_heads, int32_t top_k, int32_t splits,
                                           const uint16_t* q, const uint8_t* kv_pool, int64_t pool_rows,
                                           const int32_t* out_rows, float sm_scale, float latent_scale, uint16_t* o,

@@ -18,7 +18,8 @@ def ragged(rng, n):
 
 
 @pytest.mark.parametrize("H,Q,W,sinks,splits,R", [(128, 1, 5000, 0, 1, 260), (128, 1, 300, 5, 1, 400), (16, 4, 700, 3, 1, 300),
-                                                  (128, 2, 200, 4, 3, 90), (100, 1, 64, 0, 5, 150), (128, 1, 1, 0, 1, 500)])
+                                                  (128, 2, 200, 4, 3, 90), (100, 1, 64, 0, 5, 150), (128, 1, 1, 0, 1, 500),
+                                                  (128, 3, 200, 4, 3, 60), (40, 4, 300, 0, 2, 120)])
 def test_pairs_go_through_units_of_every_length(H, Q, W, sinks, splits, R):
     hs = T._gpu()
     rng = np.random.default_rng(R + W)
