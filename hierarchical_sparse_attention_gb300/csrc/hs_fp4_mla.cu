@@ -67,8 +67,8 @@ constexpr int BJ = 64;          // rows per block
 constexpr int DQK = kFp4Dims, DL = kFp4Latent;
 constexpr int QATOMS = DQK / 64, ATOMS = DL / 64;  // swizzle atoms of 64 values in Q and in a tile of latents
 constexpr int NT = 2;           // tiles in flight
-constexpr int ND = 3;           // blocks of records in a dequantisation warp's ring: one read, two on their way
-constexpr int NS = 3;           // S buffers, and softmax warpgroups: one block each in turn
+constexpr int S_ND = 3, O_ND = 2;  // blocks of records in a dequantisation warp's ring: one read, the others on their way
+constexpr int NS = 3;           // S buffers, softmax warpgroups and P buffers: a block each in turn
 constexpr uint32_t TMEM_COLS = 512, Q_COL = 0, S_COL = 288;
 static_assert(S_COL + NS * BJ <= TMEM_COLS, "Q and the S buffers fit tensor memory");
 // S-CTA warps: 0-11 softmax, 12 issuer, 13-22 dequantisation; O-CTA: 0-3 corrector, 4 issuer, 5-14
@@ -83,7 +83,7 @@ constexpr int MASKS = 16;       // blocks whose row masks are kept (the copies a
 constexpr uint32_t KV_ATOM = BJ * 128, TILE = ATOMS * KV_ATOM;
 constexpr uint32_t QBOX = MH * 128;
 constexpr int REC = kFp4RopeAt;                    // bytes of a record that go through the rings: codes and scales
-constexpr uint32_t RING = ND * RW * REC;           // a dequantisation warp's ring
+constexpr uint32_t S_RING = S_ND * RW * REC, O_RING = O_ND * RW * REC;  // a dequantisation warp's ring
 constexpr uint32_t S_TILES = 0;                    // latents of K; Q's are staged over them before the first block
 // RoPE values are copied straight to their tiles: a block's copies start when the tensor core is known to
 // be done with the block five before it. (Through the rings like the rest: 182 us instead of 176; with
@@ -92,19 +92,20 @@ constexpr int NR = 5;
 constexpr uint32_t S_ROPE = NT * TILE;             // (Q's are staged over two of them)
 constexpr uint32_t S_RAW = S_ROPE + NR * KV_ATOM;
 static_assert(ATOMS * QBOX <= NT * TILE && QBOX == 2 * KV_ATOM, "Q's staging");
-constexpr uint32_t S_REF = S_RAW + NDEQ * RING;  // the reference maxima, handed from block to block
+constexpr uint32_t S_REF = S_RAW + NDEQ * S_RING;  // the reference maxima, handed from block to block
 constexpr uint32_t S_MASK = S_REF + MH * 4;     // a byte per block and dequantisation warp: which of its rows exist
 constexpr uint32_t S_END = S_MASK + MASKS * NDEQ;
 constexpr uint32_t O_TILES = 0, O_RAW = NT * TILE;
-constexpr uint32_t O_P = (O_RAW + NDEQ * RING + 1023u) & ~1023u;
+constexpr uint32_t O_P = (O_RAW + NDEQ * O_RING + 1023u) & ~1023u;
 constexpr uint32_t P_BUF = MH * BJ * 2, P_BYTES = P_BUF + MH * 4;  // P and the rescale factors of a block
 constexpr uint32_t FIN_WG = 2 * MH * 4;          // a softmax warpgroup's sums and references of a unit
-constexpr uint32_t O_ALPHA = O_P + 2 * P_BUF;
-constexpr uint32_t O_FIN = O_ALPHA + 2 * MH * 4;
-constexpr int NF = 3;  // units whose totals are kept: P's two buffers let the S-CTA be two units ahead, of one block each
+constexpr uint32_t O_ALPHA = O_P + NS * P_BUF;
+constexpr uint32_t O_FIN = O_ALPHA + NS * MH * 4;
+constexpr int NF = NS + 1;  // units whose totals are kept: P's buffers let the S-CTA be three units ahead, of one block each
 constexpr uint32_t O_END = O_FIN + NF * NS * FIN_WG;
-constexpr uint32_t SMEM_BYTES = (S_END > O_END ? S_END : O_END) + 1024;  // + alignment slack
-static_assert(SMEM_BYTES <= 227 * 1024 - 1024, "shared memory of a CTA");
+constexpr uint32_t SMEM_BYTES = S_END > O_END ? S_END : O_END;
+constexpr uint32_t STATIC_BYTES = 1024;  // barriers and flags, one block of a tile's alignment
+static_assert(STATIC_BYTES + SMEM_BYTES <= 227 * 1024, "shared memory of a CTA");
 // A reference maximum stays until it is passed by 2^15, so that P < 65504 in f16, whose precision is the
 // same there. (At 2^8 a few heads of a tile were rescaled in the course of 2,048 rows, 2 us each time:
 // 182 us instead of 189 for 256 requests.)
@@ -120,12 +121,21 @@ struct Barriers {
   uint64_t s_full[NS], s_free[NS];        // S-CTA: S written; S read
   uint64_t m_set[NS][4];                  // S-CTA: the block's reference maxima of a warp's heads are set
   uint64_t p_free[NS];                    // S-CTA, arrived by the O-CTA: P . V of the block is done
-  uint64_t p_full[2];                     // O-CTA, completed by the S-CTA's stores
-  uint64_t pv_go[2];                      // O-CTA: O is ready for P . V of the block
+  uint64_t p_full[NS];                    // O-CTA, completed by the S-CTA's stores
+  uint64_t pv_go[NS];                     // O-CTA: O is ready for P . V of the block
   uint64_t mma_done;                      // O-CTA: the MMAs issued so far are done
   uint64_t fin[NF];                       // O-CTA: the S-CTA's totals of a unit are here
   uint64_t o_full, o_free;                // O-CTA: a unit's last P . V is done; O has been read out
 };
+
+struct __align__(STATIC_BYTES) Control {
+  Barriers bs;
+  uint32_t taddr;
+  int abort;
+  int issued;     // blocks whose MMAs the issuer started (the last commit to wait for)
+  int requested;  // units whose Q was requested
+};
+static_assert(sizeof(Control) == STATIC_BYTES, "one block");
 
 // The kernel's roles run side by side from one instruction cache, and much of their time goes into
 // handing over: so their loops are short (not unrolled over blocks: at 165 KB of code the same loops
@@ -380,6 +390,7 @@ template <bool kS, bool kWin>
 __device__ __forceinline__ bool run_dequant(const Rows<kWin>& rows, const uint8_t* __restrict__ pool, int nblk, int done,
                                             uint32_t q_phase, uint8_t* ring, uint8_t* rope, uint8_t* masks, uint8_t* tiles,
                                             Barriers& bs, int wq, int lane, uint32_t* err, volatile int* abort) {
+  constexpr int ND = kS ? S_ND : O_ND;
   const int own = RW * wq + (lane & 7);
   bool missing = false, ok = true;
   // slots of the ring: the next one to fill, and the next one to read
@@ -404,10 +415,12 @@ __device__ __forceinline__ bool run_dequant(const Rows<kWin>& rows, const uint8_
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  static_assert(ND == 3 && NT == 2 && NR >= ND + NT, "two blocks' copies are started here");
-  int32_t t0 = rows.raw(own), t1 = rows.raw(BJ + own), t2 = rows.raw(2 * BJ + own), t3 = rows.raw(3 * BJ + own);
+  static_assert(NT == 2 && NR >= S_ND + NT, "a block's RoPE tile is free when its copies start");
+  static_assert(S_ND == 3 && O_ND == 2, "so many blocks' copies are started here");
+  const int32_t t0 = rows.raw(own), t1 = kS ? rows.raw(BJ + own) : -1;
+  int32_t t2 = rows.raw(BJ * (ND - 1) + own), t3 = rows.raw(BJ * ND + own);  // the two blocks' after these
   start(t0, 0);
-  start(t1, 1);
+  if (kS) start(t1, 1);
 #pragma unroll 1
   for (int b = 0; b < nblk; ++b) {
     const int g = done + b;
@@ -538,13 +551,16 @@ __global__ void __launch_bounds__(T, 1)
     fp4_mla_kernel(const Fp4MlaArgs a, const Tiles ts,
                    const __grid_constant__ CUtensorMap tm_q, float* __restrict__ part_o, float* __restrict__ part_lse,
                    uint32_t* __restrict__ err) {
-  extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  __shared__ uint32_t s_taddr;
-  __shared__ __align__(8) Barriers bs;
-  __shared__ int s_abort;
-  __shared__ int s_issued;     // blocks whose MMAs the issuer started (the last commit to wait for)
-  __shared__ int s_requested;  // units whose Q was requested
+  // (what is static fills a block of the tiles' alignment, and the rest begins after it)
+  extern __shared__ __align__(STATIC_BYTES) uint8_t base[];
+  __shared__ __align__(STATIC_BYTES) Control ctl;
+  Barriers& bs = ctl.bs;
+  uint32_t& s_taddr = ctl.taddr;
+  int &s_abort = ctl.abort, &s_issued = ctl.issued, &s_requested = ctl.requested;
+  if ((smem_u32(base) & (STATIC_BYTES - 1)) != 0) {  // (never: the tiles' swizzle wants it)
+    if (threadIdx.x == 0) atomicOr(err, HS_FLAG_TIMEOUT);
+    return;
+  }
   volatile int* abort = &s_abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = blockIdx.x & 1u, partner = rank ^ 1u;  // 0: S-CTA, 1: O-CTA
@@ -564,7 +580,7 @@ __global__ void __launch_bounds__(T, 1)
     }
     bar_init(&bs.q_full, 4 * NS);  // one arrival per softmax warp
     bar_init(&bs.mma_done, 1);
-    for (int k = 0; k < 2; ++k) {
+    for (int k = 0; k < NS; ++k) {
       bar_init(&bs.p_full[k], 1);  // the O-CTA's expect_tx; the S-CTA's stores complete it
       bar_init(&bs.pv_go[k], 4);
     }
@@ -583,7 +599,7 @@ __global__ void __launch_bounds__(T, 1)
         s_requested = 1;
       }
     } else {
-      for (int k = 0; k < 2; ++k) bar_arrive_tx(&bs.p_full[k], P_BYTES);
+      for (int k = 0; k < NS; ++k) bar_arrive_tx(&bs.p_full[k], P_BYTES);
     }
   }
   if (warp == 1) {
@@ -675,8 +691,8 @@ __global__ void __launch_bounds__(T, 1)
         // warpgroups' exponentials overlap. Each keeps the sum of its own blocks under the reference of
         // its last one. The scores are read twice, for the maximum and for the weights.
         float* s_ref = reinterpret_cast<float*>(base + S_REF);
-        const uint32_t r_pbuf = remote(base + O_P, partner), r_alpha = remote(base + O_ALPHA, partner);
-        const uint32_t rbar0 = remote(&bs.p_full[0], partner), rbar1 = remote(&bs.p_full[1], partner);
+        const uint32_t pbuf = remote(base + O_P + wg * P_BUF, partner);  // (block g's buffer is g % NS = wg)
+        const uint32_t r_alpha = remote(base + O_ALPHA + 4 * (wg * MH + head), partner), rbar = remote(&bs.p_full[wg], partner);
         // scores in log2 units; a scale of zero stays above it, so that -inf stays -inf
         const float sl2 = fmaxf(fabsf(a.sm_scale * a.latent_scale * 1.4426950408889634f), 1e-37f);
         const uint32_t s_at = tbase + lane_off + S_COL + BJ * wg;
@@ -739,11 +755,10 @@ __global__ void __launch_bounds__(T, 1)
           const float ref = m_new == -INFINITY ? 0.f : m_new;  // a NaN score stays one, an unseen row's weight is 0
           l_own *= m_new == -INFINITY ? 1.f : ex2(m_own - m_new);
           m_own = m_new;
-          // the O-CTA's P buffer is free once P . V of block g - 2 is done
-          ok = __all_sync(0xffffffffu, g < 2 || ready_or_wait<true>(bs.p_free, NS, g - 2, abort));
+          // the O-CTA's P buffer is free once P . V of block g - 3 is done
+          ok = __all_sync(0xffffffffu, g < NS || ready_or_wait<true>(bs.p_free, NS, g - NS, abort));
           if (!ok) break;
-          const uint32_t pbuf = r_pbuf + (g & 1) * P_BUF, rbar = g & 1 ? rbar1 : rbar0;
-          st_async_f32(r_alpha + 4 * ((g & 1) * MH + head), alpha, rbar);
+          st_async_f32(r_alpha, alpha, rbar);
           float2 sum = make_float2(0.f, 0.f);
 #pragma unroll 1
           for (int c = 0; c < BJ / 32; ++c) {
@@ -820,7 +835,7 @@ __global__ void __launch_bounds__(T, 1)
         }
         ok = go;
       } else if (const int wq = deq_warp(warp, S_DEQ0); wq >= 0) {
-        ok = run_dequant<true, kWin>(un.rows, a.pool, nblk, done, q_phase, base + S_RAW + wq * RING, base + S_ROPE, masks, tiles, bs, wq,
+        ok = run_dequant<true, kWin>(un.rows, a.pool, nblk, done, q_phase, base + S_RAW + wq * S_RING, base + S_ROPE, masks, tiles, bs, wq,
                                      lane, err, abort);
       }
     } else {
@@ -834,11 +849,11 @@ __global__ void __launch_bounds__(T, 1)
 #pragma unroll 1
         for (int b = 0; ok && b < nblk; ++b) {
           const int g = done + b;
-          ok = __all_sync(0xffffffffu, ready_or_wait<true>(bs.p_full, 2, g, abort));
+          ok = __all_sync(0xffffffffu, ready_or_wait<true>(bs.p_full, NS, g, abort));
           if (!ok) break;
-          const float f = alpha_buf[(g & 1) * MH + head];
-          // this buffer's next phase is block g + 2: its bytes come only after P . V of block g
-          if (tid == 0) bar_arrive_tx(&bs.p_full[g & 1], P_BYTES);
+          const float f = alpha_buf[g % NS * MH + head];
+          // this buffer's next phase is block g + 3: its bytes come only after P . V of block g
+          if (tid == 0) bar_arrive_tx(&bs.p_full[g % NS], P_BYTES);
           if (__any_sync(0xffffffffu, b > 0 && f != 1.f)) {
             ok = __all_sync(0xffffffffu, ready_or_wait(bs.tile_free, NT, g - 1, abort));
             if (!ok) break;
@@ -854,7 +869,7 @@ __global__ void __launch_bounds__(T, 1)
             tc_before();
           }
           __syncwarp();
-          if (lane == 0) bar_arrive(&bs.pv_go[g & 1]);
+          if (lane == 0) bar_arrive(&bs.pv_go[g % NS]);
         }
       } else if (warp == O_ISSUER) {
         const bool one = elected();
@@ -863,13 +878,13 @@ __global__ void __launch_bounds__(T, 1)
         for (int b = 0; b < nblk; ++b) {
           const int g = done + b;
           bool go = ready_or_wait(bs.tile_full, NT, g, abort);
-          go = go && ready_or_wait(bs.pv_go, 2, g, abort);
+          go = go && ready_or_wait(bs.pv_go, NS, g, abort);
           if (b == 0) go = go && (full == 0 || ready_or_wait(&bs.o_free, 1, full - 1, abort));
           ok = __all_sync(0xffffffffu, go);
           if (!ok) break;
           tc_after();
           fence_async_smem();  // V's and P's writes, seen through their barriers, before the tensor core's reads
-          const uint64_t dp0 = p0 + (uint64_t)((g & 1) * (P_BUF >> 4)), dv0 = v0 + (uint64_t)((g % NT) * (TILE >> 4));
+          const uint64_t dp0 = p0 + (uint64_t)((g % NS) * (P_BUF >> 4)), dv0 = v0 + (uint64_t)((g % NT) * (TILE >> 4));
           if (one) {
 #pragma unroll
             for (int kk = 0; kk < BJ / 16; ++kk)
@@ -886,7 +901,7 @@ __global__ void __launch_bounds__(T, 1)
           __syncwarp();
         }
       } else if (const int wq = deq_warp(warp, O_DEQ0); wq >= 0) {
-        ok = run_dequant<false, kWin>(un.rows, a.pool, nblk, done, 0u, base + O_RAW + wq * RING, nullptr, masks, tiles, bs, wq, lane,
+        ok = run_dequant<false, kWin>(un.rows, a.pool, nblk, done, 0u, base + O_RAW + wq * O_RING, nullptr, masks, tiles, bs, wq, lane,
                                  err, abort);
       }
       if (out_warp) {
@@ -965,7 +980,7 @@ __global__ void __launch_bounds__(T, 1)
   // releases (its last arrivals here)
   if (rank == 0 && ok) {
     ok = done == 0 || pipe_wait(bs.tile_free, NT, done - 1, abort);
-    for (int b = done >= 2 ? done - 2 : 0; b < done; ++b) ok = ok && pipe_wait<true>(bs.p_free, NS, b, abort);
+    for (int b = done >= NS ? done - NS : 0; b < done; ++b) ok = ok && pipe_wait<true>(bs.p_free, NS, b, abort);
   }
   ok = __syncthreads_and(ok && !*abort);
   if (!ok) {
