@@ -717,7 +717,7 @@ hs_status hs_pages_init(const hs_page_pool* pool, hs_stream_t stream) {
 hs_status hs_pages_extend(const hs_page_pool* pool, int32_t n, const int32_t* requests, const int32_t* old_lens,
                           const int32_t* new_lens, int32_t* granted, hs_stream_t stream) {
   hs::PageArgs a;
-  if (!page_args(pool, &a) || n < 0) return HS_ERR_INVALID_ARG;
+  if (!page_args(pool, &a) || n < 0 || n > HS_MAX_PAGE_ENTRIES) return HS_ERR_INVALID_ARG;
   if (n == 0) return HS_OK;
   if (!requests || !old_lens || !new_lens) return HS_ERR_INVALID_ARG;
   return hs::launch_pages_extend(a, n, requests, old_lens, new_lens, granted, (cudaStream_t)stream) == cudaSuccess
@@ -739,7 +739,7 @@ hs_status hs_pages_fork(const hs_page_pool* pool, int32_t n, const int32_t* pare
 hs_status hs_pages_free(const hs_page_pool* pool, int32_t n, const int32_t* requests, const int32_t* first_pages,
                         const int32_t* end_pages, hs_stream_t stream) {
   hs::PageArgs a;
-  if (!page_args(pool, &a) || n < 0) return HS_ERR_INVALID_ARG;
+  if (!page_args(pool, &a) || n < 0 || n > HS_MAX_PAGE_ENTRIES) return HS_ERR_INVALID_ARG;
   if (n == 0) return HS_OK;
   if (!requests) return HS_ERR_INVALID_ARG;
   return hs::launch_pages_free(a, n, requests, first_pages, end_pages, (cudaStream_t)stream) == cudaSuccess

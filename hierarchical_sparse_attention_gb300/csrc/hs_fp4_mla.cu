@@ -15,18 +15,20 @@
 //   - the O-CTA holds O (128 x 512 in 32 bits, all of its tensor memory) and adds P . V; its
 //     corrector rescales O in the rare blocks that raise a head's reference maximum.
 // In each CTA eight dequantisation warps bring the records they own (eight rows of each block) into
-// shared memory with 16-byte asynchronous copies, two blocks ahead, each in a ring of its own that no
-// other warp touches, and write them as f16 into the CTA's tiles. The roles hand blocks over through
+// shared memory with 16-byte asynchronous copies, two blocks ahead (the O-CTA, whose rows are in L2 by
+// then, one), each in a ring of its own that no other warp touches, and write them as f16 into the CTA's tiles. The roles hand blocks over through
 // mbarriers with bounded waits. The two halves are on two SMs because Q (288 columns), S and O (512) do
 // not fit one tensor memory, nor K, V, Q and P one shared memory; both read every row, the second one
 // from L2.
 //
-// What bounds it (256 requests, 128 heads, 2,048 rows: 176 us, against 74 for its bytes and for its
-// operations): a block takes a pair 1.2 us. The S-CTA's MMAs are 0.63 of that, and its dequantisation
-// warps' round (copies started, records read, tile written) all of it, as K's tile has to go through
-// shared memory three times (record, tile, tensor core) beside P: its pipe is busy three quarters of the
-// time. A unit has ~5 us around its blocks (Q, the first block's way through the pipeline, the
-// read-out), 8 us for a first one, 5 more with the merge of splits.
+// What bounds it (256 requests, 128 heads, 2,048 rows: 159 us, against 42 for its bytes and 74 for its
+// operations): a block takes a pair 1.1 us, 0.63 of them the S-CTA's MMAs. The rest is hand-overs: a K
+// tile's round (written 0.5 us, handed over 0.3, multiplied 0.63, released 0.2) is 0.85 us a block with
+// two tiles, S's and P's 0.8 with three buffers, and shared memory has no room for more; they do not
+// overlap perfectly. Timed with parts left out: 155 us instead of 155 (a long window) with a quarter of
+// the MMAs, 141 with a quarter of the tiles' writes, 152 with all rows in L2. A unit has ~4 us around its
+// blocks (Q, the first block's way through the pipeline, the read-out), 8 us for a first one, 5 more
+// with the merge of splits.
 //
 // Why these copies: a row is 416 bytes anywhere in the pool. Measured per SM, rows from HBM / L2:
 // four-row tensor gathers 16 / 24 GB/s from one warp and 20 / 33 from four, a bulk copy per row 24 /
@@ -86,8 +88,8 @@ constexpr int REC = kFp4RopeAt;                    // bytes of a record that go 
 constexpr uint32_t S_RING = S_ND * RW * REC, O_RING = O_ND * RW * REC;  // a dequantisation warp's ring
 constexpr uint32_t S_TILES = 0;                    // latents of K; Q's are staged over them before the first block
 // RoPE values are copied straight to their tiles: a block's copies start when the tensor core is known to
-// be done with the block five before it. (Through the rings like the rest: 182 us instead of 176; with
-// four tiles, and so later copies, 183.)
+// be done with the block five before it. (Of 256 requests then 182 us through the rings like the rest, 176
+// so, 183 with four tiles and so later copies.)
 constexpr int NR = 5;
 constexpr uint32_t S_ROPE = NT * TILE;             // (Q's are staged over two of them)
 constexpr uint32_t S_RAW = S_ROPE + NR * KV_ATOM;
@@ -258,19 +260,22 @@ template <bool kWin>
 struct Rows {
   const int32_t* table;  // the request's rows, or its pages
   uint32_t pool_rows, pool_pages;  // below 2^31; window: pages that begin inside the pool
-  int n, j0;             // rows of this split; the split's first row in the tile's list
+  int n, j0;  // rows of this split; the split's first row in the tile's list (j unsigned: past n it may pass 2^31)
   // window: the list is tokens 0 .. kept - 1, then from `start`
   int kept, start, page_size;
   uint32_t page_mul, page_shift;  // t / page_size = t page_mul >> page_shift for 0 <= t < 2^31
 
-  __device__ __forceinline__ int token(int j) const { return j0 + j < kept ? j0 + j : start + (j0 + j - kept); }
+  __device__ __forceinline__ int token(uint32_t j) const {
+    const int i = (int)((uint32_t)j0 + j);
+    return i < kept ? i : (int)((uint32_t)start + (uint32_t)(i - kept));
+  }
   __device__ __forceinline__ int page_of(int t) const { return (int)((uint64_t)(uint32_t)t * page_mul >> page_shift); }
   // what the table holds for row j (loaded ahead), and the pool row that it means (-1: none)
-  __device__ __forceinline__ int32_t raw(int j) const {
-    if (j >= n) return -1;
-    return __ldg(table + (kWin ? page_of(token(j)) : j0 + j));
+  __device__ __forceinline__ int32_t raw(uint32_t j) const {
+    if (j >= (uint32_t)n) return -1;
+    return __ldg(table + (kWin ? page_of(token(j)) : j0 + (int)j));
   }
-  __device__ __forceinline__ int32_t row(int32_t raw, int j) const {
+  __device__ __forceinline__ int32_t row(int32_t raw, uint32_t j) const {
     if (!kWin) return (uint32_t)raw < pool_rows ? raw : -1;
     const int t = token(j), page = page_of(t);
     const uint32_t r = (uint32_t)(raw - page) * (uint32_t)page_size + (uint32_t)t;  // below 2^32 for a page inside
@@ -391,7 +396,8 @@ __device__ __forceinline__ bool run_dequant(const Rows<kWin>& rows, const uint8_
                                             uint32_t q_phase, uint8_t* ring, uint8_t* rope, uint8_t* masks, uint8_t* tiles,
                                             Barriers& bs, int wq, int lane, uint32_t* err, volatile int* abort) {
   constexpr int ND = kS ? S_ND : O_ND;
-  const int own = RW * wq + (lane & 7);
+  const uint32_t own = RW * wq + (lane & 7);
+  auto of_block = [own](int b) { return (uint32_t)b * BJ + own; };  // this lane's row
   bool missing = false, ok = true;
   // slots of the ring: the next one to fill, and the next one to read
   const uint32_t ring0 = smem_u32(ring) + (lane >> 3) * REC + 16 * (lane & 7), ring_end = ring0 + ND * RW * REC;
@@ -400,10 +406,10 @@ __device__ __forceinline__ bool run_dequant(const Rows<kWin>& rows, const uint8_
   const uint8_t* read = ring;
   auto start = [&](int32_t raw, int b) {  // the copies of block b (one group of copies, empty past the end)
     if (b < nblk) {
-      const int j = BJ * b + own;
+      const uint32_t j = of_block(b);
       const int32_t y = rows.row(raw, j);
       if (kS) {
-        if (kWin) missing |= j < rows.n && y < 0;
+        if (kWin) missing |= j < (uint32_t)rows.n && y < 0;
         const uint32_t mask = __ballot_sync(0xffffffffu, y >= 0);
         if (lane == 0) masks[((done + b) % MASKS) * NDEQ + wq] = (uint8_t)mask;
       }
@@ -417,8 +423,8 @@ __device__ __forceinline__ bool run_dequant(const Rows<kWin>& rows, const uint8_
   };
   static_assert(NT == 2 && NR >= S_ND + NT, "a block's RoPE tile is free when its copies start");
   static_assert(S_ND == 3 && O_ND == 2, "so many blocks' copies are started here");
-  const int32_t t0 = rows.raw(own), t1 = kS ? rows.raw(BJ + own) : -1;
-  int32_t t2 = rows.raw(BJ * (ND - 1) + own), t3 = rows.raw(BJ * ND + own);  // the two blocks' after these
+  const int32_t t0 = rows.raw(of_block(0)), t1 = kS ? rows.raw(of_block(1)) : -1;
+  int32_t t2 = rows.raw(of_block(ND - 1)), t3 = rows.raw(of_block(ND));  // the two blocks' after these
   start(t0, 0);
   if (kS) start(t1, 1);
 #pragma unroll 1
@@ -426,7 +432,7 @@ __device__ __forceinline__ bool run_dequant(const Rows<kWin>& rows, const uint8_
     const int g = done + b;
     start(t2, b + ND - 1);  // into the slot that block b - 1 was read from
     t2 = t3;
-    t3 = rows.raw(BJ * (b + ND + 1) + own);
+    t3 = rows.raw(of_block(b + ND + 1));
     asm volatile("cp.async.wait_group %0;" ::"n"(ND - 1) : "memory");
     __syncwarp();
     const Held held = read_rows(read, lane);
@@ -514,7 +520,7 @@ __device__ __forceinline__ Unit<kWin> unit_of(const Fp4MlaArgs& a, const Tiles& 
   const int all = (int)(((int64_t)total + BJ - 1) / BJ), per = (all + x.splits - 1) / x.splits;
   x.nblk = max(0, min(per, all - x.p * per));
   x.rows.j0 = x.p * per * BJ;
-  x.rows.n = x.nblk > 0 ? min(total - x.rows.j0, x.nblk * BJ) : 0;
+  x.rows.n = x.nblk > 0 ? (int)min((int64_t)total - x.rows.j0, (int64_t)x.nblk * BJ) : 0;
   return x;
 }
 

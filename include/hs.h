@@ -138,6 +138,7 @@ typedef enum {
 #define HS_MAX_MLA_SPLITS 16  /* row splits of hs_sparse_mla_decode and of the hs_fp4_*_mla_decode calls */
 #define HS_FP4_ROW_BYTES 416  /* one token's 4-bit MLA row */
 #define HS_MAX_PAGE_REQUESTS 65536 /* num_requests of an hs_page_pool */
+#define HS_MAX_PAGE_ENTRIES (1 << 20) /* entries of an hs_pages_extend or hs_pages_free call */
 
 /* Configuration of one layer group (layers that share one indexer top-k and therefore
  * one slot map; "vLLM Hybrid HiSparse source implementation analysis" 7.4).
@@ -640,7 +641,8 @@ HS_API hs_status hs_pages_init(const hs_page_pool* pool, hs_stream_t stream);
  * (HS_FLAG_TOKEN), named twice (every one of them, HS_FLAG_DUP), lengths that are negative, fall,
  * or pass max_pages * page_size (HS_FLAG_SEQLEN), an index that holds a page already
  * (HS_FLAG_STATE). A negative request is padding.
- *   requests, old_lens, new_lens [n] device; granted [n] device or NULL: pages given, -1 refused
+ *   requests, old_lens, new_lens [n] device, n <= HS_MAX_PAGE_ENTRIES; granted [n] device or NULL:
+ *   pages given, -1 refused
  * One kernel launch. n == 0 is a no-op. */
 HS_API hs_status hs_pages_extend(const hs_page_pool* pool, int32_t n, const int32_t* requests,
                                  const int32_t* old_lens, const int32_t* new_lens, int32_t* granted,
@@ -665,7 +667,8 @@ HS_API hs_status hs_pages_fork(const hs_page_pool* pool, int32_t n, const int32_
  * arrays: from the start, to the end of the row; ranges are cut to the row) become -1 and each
  * one's page loses a reference; the pages that nobody holds then go onto the stack in descending
  * order, the lowest on top. Entries may overlap or repeat. A negative request is padding, one out
- * of range is skipped (HS_FLAG_TOKEN). Two kernel launches. n == 0 is a no-op. */
+ * of range is skipped (HS_FLAG_TOKEN). n <= HS_MAX_PAGE_ENTRIES. Two kernel launches. n == 0 is a
+ * no-op. */
 HS_API hs_status hs_pages_free(const hs_page_pool* pool, int32_t n, const int32_t* requests,
                                const int32_t* first_pages, const int32_t* end_pages, hs_stream_t stream);
 

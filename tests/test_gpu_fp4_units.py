@@ -257,3 +257,21 @@ def test_the_most_requests():
     s.release(list(range(n)) + list(range(0, n, 7)))
     s.compact()
     assert int(s.count.item()) == n + 3000
+
+
+def test_strides_that_do_not_fit_are_refused():
+    hs = T._gpu()
+    kv, pool = torch.zeros(8, 640, dtype=torch.int16, device="cuda"), torch.zeros(100, 416, dtype=torch.uint8, device="cuda")
+    rows, err = torch.arange(8, dtype=torch.int32, device="cuda"), T.flags()
+    hs.hs_fp4_pack_rows(8, kv[:, :576], 640, rows, 1.0, pool, 100, err)
+    hs.hs_fp4_pack_rows(1, kv[:1, :576], 576, rows, 1.0, pool, 100, err)  # one row: its stride says nothing
+    q = torch.zeros(2, 16, 1152, dtype=torch.bfloat16, device="cuda")
+    o, lse = torch.zeros(2, 16, 512, dtype=torch.bfloat16, device="cuda"), torch.zeros(2, 16, device="cuda")
+    for call in (lambda: hs.hs_fp4_pack_rows(8, kv[:, :576], 576, rows, 1.0, pool, 100, err),
+                 lambda: hs.hs_fp4_pack_rows(8, kv.t(), 640, rows, 1.0, pool, 100, err),
+                 lambda: hs.hs_fp4_pack_rows(4, kv[:, :576], 640, rows[::2], 1.0, pool, 100, err),
+                 lambda: hs.hs_fp4_unpack_rows(8, pool[:, :400], 100, rows, 1.0, kv, 640, err),
+                 lambda: hs.hs_fp4_sparse_mla_decode(2, 16, 4, 1, q[:, :, :576], pool, 100, rows.view(2, 4), 0.1, 1.0, o, lse, None, 0, err)):
+        with pytest.raises(ValueError):
+            call()
+    assert int(err.item()) == 0
