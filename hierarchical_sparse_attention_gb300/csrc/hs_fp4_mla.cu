@@ -55,7 +55,7 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
-#include <cstring>
+#include <atomic>
 
 namespace hs {
 
@@ -1069,13 +1069,22 @@ cudaError_t q_map(CUtensorMap* m, const uint16_t* q, int64_t rows) {
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// CTA pairs that the device holds at once: a CTA takes an SM.
+// CTA pairs that the current device holds at once: a CTA takes an SM. What a device is asked is kept, and
+// the kernels are set up for it on the way (both take host time as long as a quarter of a launch).
+constexpr int kDevices = 64;
 cudaError_t pairs_resident(int* pairs) {
+  static std::atomic<int> known[kDevices];
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && dev < kDevices && (*pairs = known[dev].load(std::memory_order_acquire)) > 0) return e;
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) (void)cudaGetLastError();
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(fp4_mla_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(fp4_mla_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
   *pairs = sms > 3 ? sms / 2 : 1;
+  if (e != cudaSuccess)
+    (void)cudaGetLastError();
+  else if (dev < kDevices)
+    known[dev].store(*pairs, std::memory_order_release);
   return e;
 }
 
@@ -1143,10 +1152,9 @@ cudaError_t launch_fp4_mla(const Fp4MlaArgs& args, int32_t num_requests, float* 
   }
   const bool win = a.seq_lens != nullptr;
   const auto kernel = win ? fp4_mla_kernel<true> : fp4_mla_kernel<false>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
   const int rows = num_requests * a.num_queries * a.num_heads;
   int pairs = 1;
-  if (e == cudaSuccess) e = pairs_resident(&pairs);
+  cudaError_t e = pairs_resident(&pairs);
   CUtensorMap tm_q;
   if (e == cudaSuccess) e = q_map(&tm_q, a.q, rows);
   if (e != cudaSuccess) {
