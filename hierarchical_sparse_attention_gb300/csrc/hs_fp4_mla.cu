@@ -487,11 +487,22 @@ struct Unit {
 template <bool kWin>
 __device__ __forceinline__ Unit<kWin> unit_of(const Fp4MlaArgs& a, const Tiles& ts, int u, bool flag, uint32_t* err) {
   Unit<kWin> x;
-  x.splits = u < ts.whole ? 1 : a.splits;
-  const int v = u < ts.whole ? 0 : u - ts.whole, tile = u < ts.whole ? u : ts.whole + v / a.splits;
-  x.p = v - v / a.splits * a.splits;
-  const int r = tile / ts.per_request;
-  x.first_query = (tile - r * ts.per_request) * ts.queries;
+  // (divisions are long: none where there is nothing to divide)
+  int tile = u;
+  x.splits = 1;
+  x.p = 0;
+  if (u >= ts.whole) {
+    const int v = u - ts.whole, q = v / a.splits;
+    x.splits = a.splits;
+    x.p = v - q * a.splits;
+    tile = ts.whole + q;
+  }
+  int r = tile;
+  x.first_query = 0;
+  if (ts.per_request > 1) {
+    r = tile / ts.per_request;
+    x.first_query = (tile - r * ts.per_request) * ts.queries;
+  }
   const int nq = min(ts.queries, a.num_queries - x.first_query);
   x.live = nq * a.num_heads;
   x.row0 = ((size_t)r * a.num_queries + x.first_query) * a.num_heads;
@@ -517,7 +528,7 @@ __device__ __forceinline__ Unit<kWin> unit_of(const Fp4MlaArgs& a, const Tiles& 
     x.rows.table = a.out_rows + (size_t)r * a.top_k;
     total = a.top_k;
   }
-  const int all = (int)(((int64_t)total + BJ - 1) / BJ), per = (all + x.splits - 1) / x.splits;
+  const int all = (int)(((int64_t)total + BJ - 1) / BJ), per = x.splits == 1 ? all : (all + x.splits - 1) / x.splits;
   x.nblk = max(0, min(per, all - x.p * per));
   x.rows.j0 = x.p * per * BJ;
   x.rows.n = x.nblk > 0 ? (int)min((int64_t)total - x.rows.j0, (int64_t)x.nblk * BJ) : 0;
