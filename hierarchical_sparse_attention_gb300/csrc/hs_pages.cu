@@ -8,8 +8,8 @@
 // are pushed and packed in the order of their numbers, and the atomics only add, clear or set.
 //
 // What bounds the calls: extend, fork and free are chains of dependent loads and barriers of one CTA
-// over little data, 4 to 8 us a kernel for 4 as for 200 entries (7.5 us extend, 7.2 and 3.8 us fork's two
-// kernels, 2.8 and 4.0 us free's; from a host that launches them one by one its launches take as
+// over little data, 4 to 10 us a kernel for 4 as for 200 entries (7.5 us extend, 7.2 and 3.8 us fork's two
+// kernels, 7 to 10 us free's; from a host that launches them one by one its launches take as
 // long); compact is bound by memory once it moves more than some hundred pages (58 us for 379 MB).
 #include "hs_fp4.h"
 #include "hs_tcgen05.cuh"
@@ -24,7 +24,7 @@ constexpr int kMaxRequests = HS_MAX_PAGE_REQUESTS;
 // Workspace: a header, then per page a bit (freed by this call; zero between calls) and the
 // compaction's lists, then per entry of a fork what the plan found and gave.
 struct PageWork {
-  uint32_t* ticket;    // CTAs of a fork's check that are done; zero between calls
+  uint32_t* ticket;    // CTAs of a fork's check or of a free that are done; zero between calls
   int32_t* moves;      // pages that the compaction moves
   int32_t* live;       // live pages
   uint32_t* freed;     // [ceil(num_pages / 32)]
@@ -62,10 +62,12 @@ PageWork work_of(const hs_page_pool& p) {
 // it wrote visible before it exits.
 __device__ __forceinline__ void show_writes() { __threadfence(); }
 
-// Exclusive prefix sum of v over the CTA's kPlanThreads threads; *total gets the sum. Called by
-// every thread; sums are 64-bit (entries x pages passes 32).
+// Exclusive prefix sum of v over the CTA's threads; *total gets the sum. Called by every thread; sums
+// are 64-bit (entries x pages passes 32).
+template <int kThreads>
 __device__ int64_t block_prefix(int64_t v, int64_t* total) {
-  __shared__ int64_t s_warp[kPlanThreads / 32];
+  constexpr int kWarps = kThreads / 32;
+  __shared__ int64_t s_warp[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int64_t x = v;
 #pragma unroll
@@ -77,17 +79,32 @@ __device__ int64_t block_prefix(int64_t v, int64_t* total) {
   if (lane == 31) s_warp[warp] = x;
   __syncthreads();
   if (warp == 0) {
-    int64_t t = s_warp[lane];
+    int64_t t = lane < kWarps ? s_warp[lane] : 0;
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
+    for (int d = 1; d < kWarps; d <<= 1) {
       const int64_t y = __shfl_up_sync(0xffffffffu, t, d);
       if (lane >= d) t += y;
     }
-    s_warp[lane] = t;
+    if (lane < kWarps) s_warp[lane] = t;
   }
   __syncthreads();
-  *total = s_warp[31];
+  *total = s_warp[kWarps - 1];
   return x - v + (warp ? s_warp[warp - 1] : 0);
+}
+
+// In every thread of a CTA that has written what the grid's last CTA reads: is this that CTA? (With
+// __ldcg it sees what the others wrote. It leaves the ticket zero for the next call.)
+__device__ bool last_cta(uint32_t* ticket) {
+  __shared__ uint32_t s_last;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    __threadfence();
+    s_last = atomicAdd(ticket, 1u) == gridDim.x * gridDim.y - 1;
+    if (s_last) *ticket = 0;
+    __threadfence();
+  }
+  __syncthreads();
+  return s_last;
 }
 
 // The stack's height, kept inside its array whatever the state holds.
@@ -172,7 +189,7 @@ __global__ void __launch_bounds__(kPlanThreads)
     }
     // the pages asked for, spread over the threads: is any of them there already?
     int64_t sum;
-    s_at[tid] = block_prefix(need, &sum);
+    s_at[tid] = block_prefix<kPlanThreads>(need, &sum);
     s_req[tid] = r;
     s_first[tid] = (int32_t)first;
     s_bad[tid] = 0;
@@ -195,7 +212,7 @@ __global__ void __launch_bounds__(kPlanThreads)
       flag = HS_FLAG_STATE;
       need = 0;
     }
-    const int64_t before = asked + block_prefix(need, &sum);
+    const int64_t before = asked + block_prefix<kPlanThreads>(need, &sum);
     asked += sum;
     const bool got = need == 0 || before + need <= height;
     if (i < n) {
@@ -203,7 +220,7 @@ __global__ void __launch_bounds__(kPlanThreads)
       if (!got) atomicOr(p.error_flags, HS_FLAG_NOPAGE);
       if (granted) granted[i] = flag || !got ? -1 : (int32_t)need;
     }
-    const int64_t mine = block_prefix(got ? need : 0, &sum);
+    const int64_t mine = block_prefix<kPlanThreads>(got ? need : 0, &sum);
     s_at[tid] = mine;
     __syncthreads();
     for (int64_t k = tid; k < sum; k += kPlanThreads) {
@@ -224,7 +241,6 @@ __global__ void __launch_bounds__(kPlanThreads)
                            const int32_t* __restrict__ children, const int32_t* __restrict__ lens,
                            int32_t* __restrict__ granted) {
   __shared__ uint32_t s_once[kMaxRequests / 32], s_twice[kMaxRequests / 32], s_parent[kMaxRequests / 32];
-  __shared__ uint32_t s_last;
   const int tid = threadIdx.x;
   pdl_wait();
   {
@@ -234,14 +250,8 @@ __global__ void __launch_bounds__(kPlanThreads)
       for (int i = tid; i < p.max_pages; i += kPlanThreads)
         held |= p.resident_pages[(size_t)c * p.max_pages + i] != -1;
     held = __syncthreads_or(held);
-    if (tid == 0) {
-      w.used[blockIdx.x] = held;
-      __threadfence();
-      s_last = atomicAdd(w.ticket, 1u) == gridDim.x - 1;
-    }
-    __syncthreads();
-    if (!s_last) return;
-    __threadfence();
+    if (tid == 0) w.used[blockIdx.x] = held;
+    if (!last_cta(w.ticket)) return;
   }
   const int words = (p.num_requests + 31) / 32;
   for (int i = tid; i < words; i += kPlanThreads) s_once[i] = s_twice[i] = s_parent[i] = 0;
@@ -282,10 +292,10 @@ __global__ void __launch_bounds__(kPlanThreads)
       }
     }
     int64_t sum;
-    const int64_t before = asked + block_prefix(need, &sum);
+    const int64_t before = asked + block_prefix<kPlanThreads>(need, &sum);
     asked += sum;
     const bool got = need == 0 || before + need <= height;
-    const int64_t mine = block_prefix(got ? need : 0, &sum);
+    const int64_t mine = block_prefix<kPlanThreads>(got ? need : 0, &sum);
     if (i < n) {
       if (flag) atomicOr(p.error_flags, flag);
       if (!got) atomicOr(p.error_flags, HS_FLAG_NOPAGE);
@@ -295,10 +305,7 @@ __global__ void __launch_bounds__(kPlanThreads)
     }
     taken += sum;
   }
-  if (tid == 0) {
-    *p.free_count = height - (int32_t)taken;
-    *w.ticket = 0;
-  }
+  if (tid == 0) *p.free_count = height - (int32_t)taken;
 }
 
 // `bytes` from src to dst by the CTA, in pieces of `vec` bytes (both start on a multiple of it).
@@ -355,64 +362,73 @@ __global__ void __launch_bounds__(kPageThreads)
   show_writes();
 }
 
-// Every entry of the ranges: out of the table, its page's count down by one; a page that nobody
-// holds any more is marked. An entry is taken out by one thread however often the call names it.
-__global__ void __launch_bounds__(kPageThreads)
-    pages_drop_kernel(const hs_page_pool p, const PageWork w, const int32_t* __restrict__ requests,
-                      const int32_t* __restrict__ first_pages, const int32_t* __restrict__ end_pages) {
-  pdl_wait();
-  const int i = blockIdx.x;
-  const int32_t r = requests[i];
-  if (r < 0) return;
-  if (r >= p.num_requests) {
-    if (threadIdx.x == 0 && blockIdx.y == 0) atomicOr(p.error_flags, HS_FLAG_TOKEN);
-    return;
-  }
-  const int32_t lo = first_pages ? max(first_pages[i], 0) : 0;
-  const int32_t hi = end_pages ? min(end_pages[i], p.max_pages) : p.max_pages;
-  int32_t* row = p.resident_pages + (size_t)r * p.max_pages;
-  for (int64_t k = lo + (int64_t)blockIdx.y * kPageThreads + threadIdx.x; k < hi; k += (int64_t)gridDim.y * kPageThreads) {
-    if (row[k] == -1) continue;
-    const int32_t page = atomicExch(&row[k], -1);
-    if (page == -1) continue;
-    if (page < 0 || page >= p.num_pages) {
-      atomicOr(p.error_flags, HS_FLAG_STATE);
-      continue;
-    }
-    const int32_t held = atomicSub(&p.page_refs[page], 1);
-    if (held == 1) {
-      atomicOr(&w.freed[page >> 5], 1u << (page & 31));
-    } else if (held <= 0) {  // the count did not cover this entry
-      atomicAdd(&p.page_refs[page], 1);
-      atomicOr(p.error_flags, HS_FLAG_STATE);
-    }
-  }
-}
-
-// One CTA: the marked pages onto the stack, the lowest on top, and the marks away.
-__global__ void __launch_bounds__(kPlanThreads) pages_push_kernel(const hs_page_pool p, const PageWork w) {
-  pdl_wait();
-  const int tid = threadIdx.x;
+// The marked pages onto the stack, the lowest on top, and the marks away, by one CTA of kPlanThreads: a
+// word of marks to a thread for their ranks, then a bit to a thread.
+__device__ void push_freed(const hs_page_pool& p, const PageWork& w) {
+  __shared__ uint32_t s_bits[kPlanThreads];
+  __shared__ int64_t s_rank[kPlanThreads];
+  const int tid = threadIdx.x, lane = tid & 31;
   const int32_t height = stack_height(p);
   const int words = (int)(((int64_t)p.num_pages + 31) / 32);
   int64_t total = 0;
-  for (int base = 0; base < words; base += kPlanThreads) total += base + tid < words ? __popc(w.freed[base + tid]) : 0;
-  block_prefix(total, &total);
+#pragma unroll 4
+  for (int i = tid; i < words; i += kPlanThreads) total += __popc(__ldcg(w.freed + i));
+  block_prefix<kPlanThreads>(total, &total);
   if (total == 0) return;
   int64_t rank = 0;  // marked pages below this chunk's
   for (int base = 0; base < words; base += kPlanThreads) {
-    uint32_t bits = base + tid < words ? w.freed[base + tid] : 0;
+    const uint32_t bits = base + tid < words ? __ldcg(w.freed + base + tid) : 0u;
     int64_t sum;
-    int64_t k = rank + block_prefix(__popc(bits), &sum);
+    s_rank[tid] = rank + block_prefix<kPlanThreads>(__popc(bits), &sum);
+    s_bits[tid] = bits;
     rank += sum;
     if (bits) w.freed[base + tid] = 0;
-    for (; bits; bits &= bits - 1, ++k) {
-      const int64_t at = height + total - 1 - k;
-      if (at < p.num_pages) p.free_pages[at] = 32 * (base + tid) + __ffs(bits) - 1;
+    __syncthreads();
+    for (int k = tid >> 5; sum > 0 && k < min(kPlanThreads, words - base); k += kPlanThreads / 32) {
+      const uint32_t x = s_bits[k];
+      if (!(x >> lane & 1u)) continue;
+      const int64_t place = height + total - 1 - s_rank[k] - __popc(x & ((1u << lane) - 1));
+      if (place < p.num_pages) p.free_pages[place] = 32 * (base + k) + lane;
       else atomicOr(p.error_flags, HS_FLAG_STATE);  // more pages than the pool has
     }
   }
   if (tid == 0) *p.free_count = (int32_t)min((int64_t)p.num_pages, height + total);
+}
+
+// Every entry of the ranges: out of the table, its page's count down by one; a page that nobody
+// holds any more is marked. An entry is taken out by one thread however often the call names it. The
+// last CTA puts the marked pages onto the stack.
+__global__ void __launch_bounds__(kPlanThreads)
+    pages_free_kernel(const hs_page_pool p, const PageWork w, const int32_t* __restrict__ requests,
+                      const int32_t* __restrict__ first_pages, const int32_t* __restrict__ end_pages) {
+  pdl_wait();
+  const int i = blockIdx.x;
+  const int32_t r = requests[i];
+  if (r >= p.num_requests && threadIdx.x == 0 && blockIdx.y == 0) atomicOr(p.error_flags, HS_FLAG_TOKEN);
+  if (r >= 0 && r < p.num_requests) {
+    const int32_t lo = first_pages ? max(first_pages[i], 0) : 0;
+    const int32_t hi = end_pages ? min(end_pages[i], p.max_pages) : p.max_pages;
+    int32_t* row = p.resident_pages + (size_t)r * p.max_pages;
+    for (int64_t k = lo + (int64_t)blockIdx.y * kPlanThreads + threadIdx.x; k < hi; k += (int64_t)gridDim.y * kPlanThreads) {
+      if (row[k] == -1) continue;
+      const int32_t page = atomicExch(&row[k], -1);
+      if (page == -1) continue;
+      if (page < 0 || page >= p.num_pages) {
+        atomicOr(p.error_flags, HS_FLAG_STATE);
+        continue;
+      }
+      const int32_t held = atomicSub(&p.page_refs[page], 1);
+      if (held == 1) {
+        atomicOr(&w.freed[page >> 5], 1u << (page & 31));
+      } else if (held <= 0) {  // the count did not cover this entry
+        atomicAdd(&p.page_refs[page], 1);
+        atomicOr(p.error_flags, HS_FLAG_STATE);
+      }
+    }
+  }
+  show_writes();
+  if (last_cta(w.ticket)) push_freed(p, w);
+  show_writes();
 }
 
 // One CTA, a strip of pages per warp: the live pages are counted, those past the live count get
@@ -427,7 +443,7 @@ __global__ void __launch_bounds__(kPlanThreads) pages_compact_plan_kernel(const 
 #pragma unroll 8  // (the loads of a batch go out together)
   for (int64_t b = lo; b < hi; b += 32) count += __popc(__ballot_sync(~0u, b + lane < hi && p.page_refs[b + lane] > 0));
   int64_t live;
-  int64_t before = block_prefix(lane == 0 ? count : 0, &live);  // live pages below the strip
+  int64_t before = block_prefix<kPlanThreads>(lane == 0 ? count : 0, &live);  // live pages below the strip
   before = __shfl_sync(~0u, before, 0);
   // live pages among the first `live`: the rest of those are holes, as many as there are pages to move
   count = 0;
@@ -435,7 +451,7 @@ __global__ void __launch_bounds__(kPlanThreads) pages_compact_plan_kernel(const 
   for (int64_t b = lo; b < min(hi, live); b += 32)
     count += __popc(__ballot_sync(~0u, b + lane < min(hi, live) && p.page_refs[b + lane] > 0));
   int64_t kept;
-  block_prefix(lane == 0 ? count : 0, &kept);
+  block_prefix<kPlanThreads>(lane == 0 ? count : 0, &kept);
   for (int64_t b = lo; b < hi; b += 32) {
     const int64_t page = b + lane;
     const bool in = page < hi, used = in && p.page_refs[page] > 0;
@@ -620,11 +636,9 @@ cudaError_t launch_pages_fork(const PageArgs& a, int32_t n, const int32_t* paren
 cudaError_t launch_pages_free(const PageArgs& a, int32_t n, const int32_t* requests, const int32_t* first_pages,
                               const int32_t* end_pages, cudaStream_t stream) {
   const PageWork w = work_of(a.p);
-  const int chunks = (a.p.max_pages + kPageThreads - 1) / kPageThreads;
-  const cudaError_t e = launch(pages_drop_kernel, dim3((unsigned)n, (unsigned)(chunks < 64 ? chunks : 64)), kPageThreads,
-                               0, stream, a.p, w, requests, first_pages, end_pages);
-  if (e != cudaSuccess) return e;
-  return launch(pages_push_kernel, dim3(1), kPlanThreads, 0, stream, a.p, w);
+  const int chunks = (a.p.max_pages + kPlanThreads - 1) / kPlanThreads;
+  return launch(pages_free_kernel, dim3((unsigned)n, (unsigned)(chunks < 64 ? chunks : 64)), kPlanThreads, 0, stream, a.p, w,
+                requests, first_pages, end_pages);
 }
 
 cudaError_t launch_pages_compact(const PageArgs& a, cudaStream_t stream) {

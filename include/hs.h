@@ -667,7 +667,7 @@ HS_API hs_status hs_pages_fork(const hs_page_pool* pool, int32_t n, const int32_
  * arrays: from the start, to the end of the row; ranges are cut to the row) become -1 and each
  * one's page loses a reference; the pages that nobody holds then go onto the stack in descending
  * order, the lowest on top. Entries may overlap or repeat. A negative request is padding, one out
- * of range is skipped (HS_FLAG_TOKEN). n <= HS_MAX_PAGE_ENTRIES. Two kernel launches. n == 0 is a
+ * of range is skipped (HS_FLAG_TOKEN). n <= HS_MAX_PAGE_ENTRIES. One kernel launch. n == 0 is a
  * no-op. */
 HS_API hs_status hs_pages_free(const hs_page_pool* pool, int32_t n, const int32_t* requests,
                                const int32_t* first_pages, const int32_t* end_pages, hs_stream_t stream);
