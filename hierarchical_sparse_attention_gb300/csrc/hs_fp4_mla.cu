@@ -110,7 +110,7 @@ constexpr uint32_t STATIC_BYTES = 1024;  // barriers and flags, one block of a t
 static_assert(STATIC_BYTES + SMEM_BYTES <= 227 * 1024, "shared memory of a CTA");
 // A reference maximum stays until it is passed by 2^15, so that P < 65504 in f16, whose precision is the
 // same there. (At 2^8 a few heads of a tile were rescaled in the course of 2,048 rows, 2 us each time:
-// 182 us instead of 189 for 256 requests.)
+// 256 requests took 189 us instead of 182.)
 constexpr float kRescaleLog2 = 15.f;
 constexpr uint32_t kIdescQK = idesc(BJ, MH, false);                              // f16 latents
 constexpr uint32_t kIdescRope = kIdescQK | (1u << 7) | (1u << 10);               // bf16 RoPE
@@ -390,7 +390,7 @@ __device__ __forceinline__ void write_rows(const Held& h, uint8_t* group, int la
 // ND - 1 blocks are on their way, and two more blocks' row numbers. `done`: blocks of the units before
 // (places in rings go on from unit to unit). In the S-CTA it waits, before its first tile write, until Q
 // has left the staging area, and tells the softmax which of its rows exist. A block's copies start once
-// the tensor core has read the block four before it, whose RoPE tile they go to.
+// the tensor core has read the block five before it, whose RoPE tile they go to.
 template <bool kS, bool kWin>
 __device__ __forceinline__ bool run_dequant(const Rows<kWin>& rows, const uint8_t* __restrict__ pool, int nblk, int done,
                                             uint32_t q_phase, uint8_t* ring, uint8_t* rope, uint8_t* masks, uint8_t* tiles,
