@@ -79,6 +79,7 @@ static_assert(S_COL + NS * BJ <= TMEM_COLS, "Q and the S buffers fit tensor memo
 // scheduler (they took up to 1.2 us longer over a block than the others).
 constexpr int S_ISSUER = 12, S_DEQ0 = 13;
 constexpr int O_ISSUER = 4, O_DEQ0 = 5, O_OUT0 = 15, NOUT = 3;  // NOUT warps read out a quarter of the heads
+static_assert(4 + T / 32 - O_OUT0 == 4 * NOUT, "the warps that meet at the read-out's barrier");
 constexpr int NDEQ = 8, RW = BJ / NDEQ;  // dequantisation warps of each CTA, eight rows of a block each
 constexpr int MASKS = 16;       // blocks whose row masks are kept (the copies are at most 8 ahead of the softmax)
 
