@@ -74,9 +74,10 @@ constexpr int NS = 3;           // S buffers, softmax warpgroups and P buffers: 
 constexpr uint32_t TMEM_COLS = 512, Q_COL = 0, S_COL = 288;
 static_assert(S_COL + NS * BJ <= TMEM_COLS, "Q and the S buffers fit tensor memory");
 // S-CTA warps: 0-11 softmax, 12 issuer, 13-22 dequantisation; O-CTA: 0-3 corrector, 4 issuer, 5-14
-// dequantisation, 15-22 and the corrector's read out. Dequantisation leaves out the warps w % 4 = 0: an issuer
-// whose MMAs wait for the tensor core holds up the shared-memory instructions of the warps on its
-// scheduler (they took up to 1.2 us longer over a block than the others).
+// dequantisation, 15-22 and the corrector's read out. Dequantisation leaves out the warps w % 4 = 0: an
+// issuer whose MMAs wait for the tensor core holds up the shared-memory instructions of the warps on its
+// scheduler (a window of 8,192 rows took 173 us instead of 155 with one of the S-CTA's eight there, 182
+// with two).
 constexpr int S_ISSUER = 12, S_DEQ0 = 13;
 constexpr int O_ISSUER = 4, O_DEQ0 = 5, O_OUT0 = 15, NOUT = 3;  // NOUT warps read out a quarter of the heads
 static_assert(4 + T / 32 - O_OUT0 == 4 * NOUT, "the warps that meet at the read-out's barrier");
