@@ -127,7 +127,6 @@ struct Barriers {
   uint64_t p_free[NS];                    // S-CTA, arrived by the O-CTA: P . V of the block is done
   uint64_t p_full[NS];                    // O-CTA, completed by the S-CTA's stores
   uint64_t pv_go[NS];                     // O-CTA: O is ready for P . V of the block
-  uint64_t mma_done;                      // O-CTA: the MMAs issued so far are done
   uint64_t fin[NF];                       // O-CTA: the S-CTA's totals of a unit are here
   uint64_t o_full, o_free;                // O-CTA: a unit's last P . V is done; O has been read out
 };
@@ -598,7 +597,6 @@ __global__ void __launch_bounds__(T, 1)
       bar_init(&bs.p_free[k], 1);
     }
     bar_init(&bs.q_full, 4 * NS);  // one arrival per softmax warp
-    bar_init(&bs.mma_done, 1);
     for (int k = 0; k < NS; ++k) {
       bar_init(&bs.p_full[k], 1);  // the O-CTA's expect_tx; the S-CTA's stores complete it
       bar_init(&bs.pv_go[k], 4);
@@ -913,7 +911,6 @@ __global__ void __launch_bounds__(T, 1)
                        kIdescPV, (b > 0 || kk > 0) ? 1u : 0u);
             commit(&bs.tile_free[g % NT]);
             commit_multicast(&bs.p_free[g % NS], (uint16_t)(1u << partner));
-            commit(&bs.mma_done);
             if (b == nblk - 1) commit(&bs.o_full);
             s_issued = g + 1;
           }
@@ -1012,10 +1009,11 @@ __global__ void __launch_bounds__(T, 1)
     const int n = s_issued, q = s_requested;
     for (int g = 0; rank == 0 && q > 0 && g < NS; ++g) pipe_wait(&bs.q_raw[g], 1, q - 1, abort);
     if (n > 0) {
+      // (of a ring as deep as blocks can be in flight, so that the parity is block n - 1's and no earlier one's)
       if (rank == 0)
         pipe_wait(bs.s_full, NS, n - 1, abort);
       else
-        pipe_wait(&bs.mma_done, 1, n - 1, abort);
+        pipe_wait(bs.tile_free, NT, n - 1, abort);
     }
   }
   tc_before();
