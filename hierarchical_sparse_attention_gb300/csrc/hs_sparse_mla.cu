@@ -137,7 +137,6 @@ struct Barriers {
   uint64_t p_free[2];                   // S-CTA, arrived by the O-CTA: P buffer free again
   uint64_t p_full[2];                   // O-CTA, arrived by the S-CTA: P and the factors written
   uint64_t pv_go[2];                    // O-CTA: O rescaled (if needed); P . V may go
-  uint64_t mma_done;                    // O-CTA: the MMAs it issued so far are done
   uint64_t fin;                         // O-CTA, arrived by the S-CTA: final l and m written
   uint64_t xch;                         // fused merge, O-CTA: the other split's O-CTA wrote its half for this one
 };
@@ -291,7 +290,6 @@ __global__ void __launch_bounds__(T, 1) sparse_mla_kernel(const SparseMlaArgs a,
     }
     bar_init(&bs.q_raw, 1);   // the issuing thread's arrival with the boxes' bytes
     bar_init(&bs.q_full, 8);  // one arrival per warp of the two softmax warpgroups
-    bar_init(&bs.mma_done, 1);
     for (int k = 0; k < 2; ++k) {
       bar_init(&bs.s_full[k], 1);
       bar_init(&bs.s_free[k], 8);
@@ -527,7 +525,6 @@ __global__ void __launch_bounds__(T, 1) sparse_mla_kernel(const SparseMlaArgs a,
                      dv0 + (uint64_t)((nh * 4 * KV_ATOM + kk * 2048) >> 4), kIdescO, (b > 0 || kk > 0) ? 1u : 0u);
           commit(&bs.tile_free[b % NT]);
           commit_multicast(&bs.p_free[b & 1], (uint16_t)(1u << partner));  // the S-CTA's P buffer is free once these are done
-          commit(&bs.mma_done);
           s_issued = b + 1;
         }
         __syncwarp();
@@ -678,10 +675,11 @@ __global__ void __launch_bounds__(T, 1) sparse_mla_kernel(const SparseMlaArgs a,
     __syncthreads();
     const int n = s_issued;
     if (n > 0) {
+      // (of a ring as deep as blocks can be in flight, so that the parity is block n - 1's and no earlier one's)
       if (rank == 0)
         pipe_wait(bs.s_full, 2, n - 1, abort);
       else
-        pipe_wait(&bs.mma_done, 1, n - 1, abort);
+        pipe_wait(bs.tile_free, NT, n - 1, abort);
     }
   }
   tc_before();

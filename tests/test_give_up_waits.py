@@ -42,7 +42,7 @@ def test_the_model_of_a_parity_wait():
     assert not returns(2, 2, 1) and not returns(2, 2, 2) and returns(2, 2, 3)
 
 
-@pytest.mark.parametrize("name", ["hs_fp4_mla.cu"])
+@pytest.mark.parametrize("name", ["hs_fp4_mla.cu", "hs_sparse_mla.cu"])
 def test_mmas_in_flight_are_waited_for(name):
     """Block n - 1's MMAs are issued once those of block n - 1 - NT are over, so up to NT blocks are in flight
     when a CTA gives up; MMAs end in the order in which they were issued."""
