@@ -150,7 +150,7 @@ struct Barriers {
 template <bool kS>
 __device__ __forceinline__ void run_loader(const SparseMlaArgs& a, const CUtensorMap* tmap, const int32_t* rows,
                                            int n_rows, int nblk, uint8_t* raw, Barriers& bs, int lane,
-                                           volatile int* abort) {
+                                           volatile int* abort, int& requested) {
   constexpr int REC = kS ? S_REC : O_REC, GRP = kS ? S_GRP : O_GRP, SLOT = kS ? S_SLOT : O_SLOT;
   const bool any = a.pool_rows > 0;
   const int halves = 2 * nblk;
@@ -169,6 +169,7 @@ __device__ __forceinline__ void run_loader(const SparseMlaArgs& a, const CUtenso
           "%4, %5, %6}], [%7];" ::"r"(smem_u32(raw + (k % NR) * SLOT + lane * GRP)),
           "l"(tmap), "r"(0), "r"(y4[0]), "r"(y4[1]), "r"(y4[2]), "r"(y4[3]), "r"(smem_u32(&bs.raw_full[k % NR]))
           : "memory");
+    if (lane == 0) requested = k + 1;
   }
 }
 
@@ -266,6 +267,7 @@ __global__ void __launch_bounds__(T, 1) sparse_mla_kernel(const SparseMlaArgs a,
   __shared__ __align__(8) Barriers bs;
   __shared__ int s_abort;
   __shared__ int s_issued;  // blocks whose MMAs the issuer started (the last commit to wait for)
+  __shared__ int s_requested;  // half-blocks whose records the loader requested
   volatile int* abort = &s_abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint32_t crank;
@@ -301,6 +303,7 @@ __global__ void __launch_bounds__(T, 1) sparse_mla_kernel(const SparseMlaArgs a,
     bar_init(&bs.xch, 1);  // fused merge: one release by the other split's O-CTA
     s_abort = 0;
     s_issued = 0;
+    s_requested = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     if (rank == 0 && nblk > 0) {
       // S-CTA: Q of request r into the staging area (over the K tiles) as nine tensor boxes of
@@ -473,7 +476,7 @@ __global__ void __launch_bounds__(T, 1) sparse_mla_kernel(const SparseMlaArgs a,
         __syncwarp();
       }
     } else if (warp == S_LOADER) {
-      run_loader<true>(a, &tm_s, rows, n_rows, nblk, raw, bs, lane, abort);
+      run_loader<true>(a, &tm_s, rows, n_rows, nblk, raw, bs, lane, abort, s_requested);
     } else {
       run_dequant<true>(a, rows, n_rows, nblk, raw, tiles, bs, warp - S_DEQW0, lane, abort);
     }
@@ -530,7 +533,7 @@ __global__ void __launch_bounds__(T, 1) sparse_mla_kernel(const SparseMlaArgs a,
         __syncwarp();
       }
     } else if (warp == O_LOADER) {
-      run_loader<false>(a, &tm_o, rows, n_rows, nblk, raw, bs, lane, abort);
+      run_loader<false>(a, &tm_o, rows, n_rows, nblk, raw, bs, lane, abort, s_requested);
     } else {
       run_dequant<false>(a, rows, n_rows, nblk, raw, tiles, bs, warp - O_DEQW0, lane, abort);
     }
@@ -667,13 +670,15 @@ __global__ void __launch_bounds__(T, 1) sparse_mla_kernel(const SparseMlaArgs a,
     }
   }
   if (!ok) {
-    // outputs are not valid: flag it, and give any MMA still in flight one more bound before
-    // the tensor memory is released
+    // outputs are not valid: flag it, and give copies and MMAs still in flight one more bound before
+    // the shared and tensor memory are released
     if (tid == 0) atomicOr(err, HS_FLAG_TIMEOUT);
     __syncthreads();
     if (tid == 0) s_abort = 0;
     __syncthreads();
-    const int n = s_issued;
+    const int n = s_issued, m = s_requested;
+    if (rank == 0 && nblk > 0) pipe_wait(&bs.q_raw, 1, 0, abort);
+    for (int k = m >= NR ? m - NR : 0; k < m; ++k) pipe_wait(bs.raw_full, NR, k, abort);
     if (n > 0) {
       // (of a ring as deep as blocks can be in flight, so that the parity is block n - 1's and no earlier one's)
       if (rank == 0)

@@ -1,5 +1,5 @@
-"""The waits on the path by which an attention kernel gives up (a bounded wait ran out): its MMAs are over
-before the tensor memory is freed. A model of mbarrier phases on the CPU, with the rings, depths and tiles
+"""The waits on the path by which an attention kernel gives up (a bounded wait ran out): its copies and MMAs
+are over before shared and tensor memory are freed. A model of mbarrier phases on the CPU, with the rings, depths and tiles
 in flight as the kernels' sources have them; no GPU path is made to run out."""
 import os
 import re
@@ -56,3 +56,25 @@ def test_mmas_in_flight_are_waited_for(name):
             for over in range(max(0, n - in_flight), n):
                 assert not returns(depth, n - 1, over), f"{ring}: back with {n - over} of {n} blocks' MMAs in flight"
             assert returns(depth, n - 1, n)
+
+
+@pytest.mark.parametrize("name,rings", [("hs_fp4_mla.cu", ["q_raw"]), ("hs_sparse_mla.cu", ["q_raw", "raw_full"])])
+def test_copies_in_flight_are_waited_for(name, rings):
+    """Every ring on which copies of the copy engine complete."""
+    text = source(name)
+    copies = re.findall(r"complete_tx::bytes \[%0\].*?:\s*\"memory\"", text, re.S)
+    assert sorted({re.search(r"smem_u32\(&bs\.(\w+)", c).group(1) for c in copies}) == sorted(rings)
+    for ring in rings:
+        assert re.search(r"pipe_wait\(&?bs\.%s\b" % ring, give_up(text)), ring
+
+
+def test_the_gathers_last_uses_are_the_ones_waited_for():
+    """Half-block k is requested once half-block k - NR has been read, so the last NR of those requested may be on
+    their way, in any order."""
+    text = source("hs_sparse_mla.cu")
+    ring = number(text, "NR")
+    assert "for (int k = m >= NR ? m - NR : 0; k < m; ++k) pipe_wait(bs.raw_full, NR, k, abort);" in give_up(text)
+    for m in range(1, 30):
+        for k in range(max(0, m - ring), m):
+            assert not returns(ring, k, k)  # all but k itself are there
+            assert returns(ring, k, k + 1)
