@@ -1023,6 +1023,7 @@ __global__ void __launch_bounds__(T, 1)
   // the merge kernel (if any) may launch; it waits for this grid's completion before reading
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   cluster_sync_all();  // the partner no longer reads or arrives on this CTA's shared memory
+  if (!ok && tid == 0) stay();
 }
 
 // The splits of query heads row0 .. row0 + rows - 1 joined, in split order, as an online softmax over their log-sum-exps

@@ -694,6 +694,7 @@ __global__ void __launch_bounds__(T, 1) sparse_mla_kernel(const SparseMlaArgs a,
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // the partner no longer reads or arrives on this CTA's shared memory
   cluster_sync_all();
+  if (!ok && tid == 0) stay();
 }
 
 // Merge the splits of each (request, head): weights exp(lse_p - lse), lse = log sum exp lse_p.

@@ -199,6 +199,14 @@ __device__ __forceinline__ bool pipe_wait(uint64_t* ring, int depth, int k, vola
   }
 }
 
+// A CTA that gave up ends this much later than its partner's last instruction: the partner's st.async
+// stores into it and the arrivals of its MMAs, which nobody may be waiting for any more, take microseconds
+// and find its shared memory still there.
+constexpr uint64_t kStayNs = 1000000ull;
+__device__ __forceinline__ void stay() {
+  for (const uint64_t t0 = gtime(); gtime() - t0 < kStayNs;) __nanosleep(20000);
+}
+
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);

@@ -78,3 +78,14 @@ def test_the_gathers_last_uses_are_the_ones_waited_for():
         for k in range(max(0, m - ring), m):
             assert not returns(ring, k, k)  # all but k itself are there
             assert returns(ring, k, k + 1)
+
+
+@pytest.mark.parametrize("name", ["hs_fp4_mla.cu", "hs_sparse_mla.cu"])
+def test_a_cta_that_gave_up_outlives_its_partners_stores(name):
+    """A CTA that gave up takes no more P: the stores that its partner has issued complete on no wait of its own,
+    so it stays, after the cluster's last barrier, for longer than any store takes."""
+    text = source(name)
+    end = text[text.index("tcgen05.dealloc"):]
+    assert re.search(r"cluster_sync_all\(\);\s*if \(!ok && tid == 0\) stay\(\);\s*}", end)
+    header = source("hs_tcgen05.cuh")
+    assert int(re.search(r"kStayNs = (\d+)ull", header).group(1)) >= 1000000
