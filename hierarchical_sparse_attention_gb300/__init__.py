@@ -7,7 +7,7 @@ kernels. Arguments that are device arrays accept a torch CUDA tensor (its
 ``stream`` accepts a ``torch.cuda.Stream``, a raw ``cudaStream_t`` or None (the legacy
 default stream). A non-OK status raises :class:`HsError` carrying the status code. The 4-bit
 cache's calls (``hs_fp4_*``, ``hs_pages_*``) also refuse, with ValueError, a tensor that is not on
-the current CUDA device.
+the current CUDA device, and a page pool whose tensors are not.
 
 The in-tree ``libhs.so`` is loaded on first use; every entry point raises ImportError
 if it has not been built (``python -m hierarchical_sparse_attention_gb300.build``).
@@ -59,6 +59,7 @@ class hs_page_pool(ctypes.Structure):
                 [(n, ctypes.c_void_p) for n in ("resident_pages", "page_refs", "free_pages", "free_count",
                                                 "error_flags", "workspace")] +
                 [("workspace_bytes", ctypes.c_size_t)])
+    device = None  # the CUDA device of the tensors it was made of; None: raw addresses only
 
 
 class HsError(RuntimeError):
@@ -424,30 +425,37 @@ def make_page_pool(device_pools: Sequence, num_requests: int, max_pages: int, nu
     p = hs_page_pool(num_requests, max_pages, num_pages, page_size, row_bytes, len(device_pools),
                      (ctypes.c_void_p * HS_MAX_LAYERS)(*_on_gpu(*device_pools)), *arrays, workspace_bytes)
     p.kept = (list(device_pools), resident_pages, page_refs, free_pages, free_count, error_flags, workspace)
+    p.device = next((x.get_device() for x in (*device_pools, *p.kept[1:]) if hasattr(x, "get_device")), None)
     return p
 
 
+def _pool_here(pool: Optional[hs_page_pool]) -> Optional[hs_page_pool]:
+    if pool is not None and pool.device is not None:
+        _device_check(pool.device)
+    return pool
+
+
 def hs_pages_init(pool: hs_page_pool, stream=None) -> None:
-    _check(_lib.hs_pages_init(pool, _stream(stream)), "hs_pages_init")
+    _check(_lib.hs_pages_init(_pool_here(pool), _stream(stream)), "hs_pages_init")
 
 
 def hs_pages_extend(pool: hs_page_pool, n: int, requests, old_lens, new_lens, granted=None, stream=None) -> None:
-    _check(_lib.hs_pages_extend(pool, n, *_on_gpu(requests, old_lens, new_lens, granted), _stream(stream)),
+    _check(_lib.hs_pages_extend(_pool_here(pool), n, *_on_gpu(requests, old_lens, new_lens, granted), _stream(stream)),
            "hs_pages_extend")
 
 
 def hs_pages_fork(pool: hs_page_pool, n: int, parents, children, lens, granted=None, stream=None) -> None:
-    _check(_lib.hs_pages_fork(pool, n, *_on_gpu(parents, children, lens, granted), _stream(stream)),
+    _check(_lib.hs_pages_fork(_pool_here(pool), n, *_on_gpu(parents, children, lens, granted), _stream(stream)),
            "hs_pages_fork")
 
 
 def hs_pages_free(pool: hs_page_pool, n: int, requests, first_pages=None, end_pages=None, stream=None) -> None:
-    _check(_lib.hs_pages_free(pool, n, *_on_gpu(requests, first_pages, end_pages), _stream(stream)),
+    _check(_lib.hs_pages_free(_pool_here(pool), n, *_on_gpu(requests, first_pages, end_pages), _stream(stream)),
            "hs_pages_free")
 
 
 def hs_pages_compact(pool: hs_page_pool, stream=None) -> None:
-    _check(_lib.hs_pages_compact(pool, _stream(stream)), "hs_pages_compact")
+    _check(_lib.hs_pages_compact(_pool_here(pool), _stream(stream)), "hs_pages_compact")
 
 
 def hs_reset_hints(h: Handle, stream=None) -> None:
