@@ -7,7 +7,8 @@ kernels. Arguments that are device arrays accept a torch CUDA tensor (its
 ``stream`` accepts a ``torch.cuda.Stream``, a raw ``cudaStream_t`` or None (the legacy
 default stream). A non-OK status raises :class:`HsError` carrying the status code. The 4-bit
 cache's calls (``hs_fp4_*``, ``hs_pages_*``) also refuse, with ValueError, a tensor that is not on
-the current CUDA device, and a page pool whose tensors are not.
+the current CUDA device, a page pool whose tensors are not, and a tensor whose elements are of another
+type than the call's (bf16 arrays may be given as their 16-bit patterns).
 
 The in-tree ``libhs.so`` is loaded on first use; every entry point raises ImportError
 if it has not been built (``python -m hierarchical_sparse_attention_gb300.build``).
@@ -189,11 +190,26 @@ def _device_check(on: int) -> int:
     return on
 
 
+_kinds = {}  # dtype -> the letter that the calls below name it by
+
+
+def _type_check(kind: str, dtype) -> None:
+    """Elements of the type that the library reads: i 32-bit integers, h bf16 values or their bits, f fp32."""
+    if not _kinds:
+        import torch
+        _kinds.update({torch.int32: "i", torch.uint32: "i", torch.bfloat16: "h", torch.int16: "h", torch.uint16: "h",
+                       torch.float32: "f"})
+    if _kinds.get(dtype) != kind:
+        wanted = {"i": "32-bit integers", "h": "bf16 values or their 16-bit patterns", "f": "32-bit floats"}[kind]
+        raise ValueError(f"{wanted} are needed here, not {dtype}")
+
+
 def _rows_on_gpu(x, stride: int) -> Optional[int]:
-    """_on_gpu of a 2-D array with rows of consecutive values, `stride` values apart."""
+    """_on_gpu of a 2-D array with rows of consecutive bf16 values, `stride` values apart."""
     if x is None or isinstance(x, int):
         return x
     _device_check(x.get_device() if hasattr(x, "get_device") else -1)
+    _type_check("h", x.dtype)
     if x.dim() != 2 or x.stride(1) != 1:
         raise ValueError("rows of consecutive values are needed")
     if x.size(0) > 1 and x.stride(0) != stride:
@@ -201,17 +217,19 @@ def _rows_on_gpu(x, stride: int) -> Optional[int]:
     return x.data_ptr()
 
 
-def _on_gpu(*xs):
-    """Addresses of contiguous arrays, which have to be on the current device (None and raw addresses are taken
-    as they are). Short, as a call's host time is mostly this: 0.3 us an array."""
+def _on_gpu(kinds: str, *xs):
+    """Addresses of contiguous arrays, which have to be on the current device and of the types in `kinds` (a letter
+    an array, "." any; None and raw addresses are taken as they are). Short, as a call's host time is mostly this."""
     out, here = [], -1
-    for x in xs:
+    for kind, x in zip(kinds, xs):
         if x is not None and not isinstance(x, int):
             on = x.get_device() if hasattr(x, "get_device") else -1
             if on != here or on < 0:
                 here = _device_check(on)
             if not x.is_contiguous():
                 raise ValueError("arrays passed to libhs must be contiguous")
+            if kind != "." and _kinds.get(x.dtype) != kind:
+                _type_check(kind, x.dtype)
             x = x.data_ptr()
         out.append(x)
     return out
@@ -367,7 +385,7 @@ def hs_fp4_pack_rows(n: int, kv, kv_stride: int, rows, latent_scale: float, pool
                      stream=None) -> None:
     """Quantise n tokens (bf16 [n, kv_stride], 576 used) into the 4-bit rows `rows` of the pool."""
     kv = _rows_on_gpu(kv, kv_stride)
-    rows, pool, error_flags = _on_gpu(rows, pool, error_flags)
+    rows, pool, error_flags = _on_gpu("i.i", rows, pool, error_flags)
     _check(_lib.hs_fp4_pack_rows(n, kv, kv_stride, rows, latent_scale, pool, pool_rows, error_flags, _stream(stream)),
            "hs_fp4_pack_rows")
 
@@ -376,7 +394,7 @@ def hs_fp4_unpack_rows(n: int, pool, pool_rows: int, rows, latent_scale: float, 
                        stream=None) -> None:
     """Read the 4-bit rows `rows` back as bf16 into kv ([n, kv_stride], 576 written)."""
     kv = _rows_on_gpu(kv, kv_stride)
-    pool, rows, error_flags = _on_gpu(pool, rows, error_flags)
+    pool, rows, error_flags = _on_gpu(".ii", pool, rows, error_flags)
     _check(_lib.hs_fp4_unpack_rows(n, pool, pool_rows, rows, latent_scale, kv, kv_stride, error_flags,
                                    _stream(stream)), "hs_fp4_unpack_rows")
 
@@ -393,7 +411,8 @@ def hs_fp4_mla_workspace_bytes(num_requests: int, num_heads: int, num_queries: i
 def hs_fp4_sparse_mla_decode(num_requests: int, num_heads: int, top_k: int, splits: int, q, kv_pool, pool_rows: int,
                              out_rows, sm_scale: float, latent_scale: float, o, lse, workspace, workspace_bytes: int,
                              error_flags, stream=None) -> None:
-    q, kv_pool, out_rows, o, lse, workspace, error_flags = _on_gpu(q, kv_pool, out_rows, o, lse, workspace, error_flags)
+    q, kv_pool, out_rows, o, lse, workspace, error_flags = _on_gpu("h.ihf.i", q, kv_pool, out_rows, o, lse, workspace,
+                                                                   error_flags)
     _check(_lib.hs_fp4_sparse_mla_decode(num_requests, num_heads, top_k, splits, q, kv_pool, pool_rows, out_rows,
                                          sm_scale, latent_scale, o, lse, workspace, workspace_bytes, error_flags,
                                          _stream(stream)), "hs_fp4_sparse_mla_decode")
@@ -404,7 +423,7 @@ def hs_fp4_window_mla_decode(num_requests: int, num_heads: int, num_queries: int
                              resident_pages, sm_scale: float, latent_scale: float, o, lse, workspace,
                              workspace_bytes: int, error_flags, stream=None) -> None:
     q, kv_pool, seq_lens, resident_pages, o, lse, workspace, error_flags = _on_gpu(
-        q, kv_pool, seq_lens, resident_pages, o, lse, workspace, error_flags)
+        "h.iihf.i", q, kv_pool, seq_lens, resident_pages, o, lse, workspace, error_flags)
     _check(_lib.hs_fp4_window_mla_decode(num_requests, num_heads, num_queries, window, sinks, splits, q, kv_pool,
                                          pool_rows, page_size, max_pages, seq_lens, resident_pages, sm_scale,
                                          latent_scale, o, lse, workspace, workspace_bytes, error_flags,
@@ -421,9 +440,9 @@ def make_page_pool(device_pools: Sequence, num_requests: int, max_pages: int, nu
     """The descriptor of the hs_pages_* calls. It keeps the tensors that it points to alive."""
     if not 1 <= len(device_pools) <= HS_MAX_LAYERS:
         raise ValueError(f"1 to {HS_MAX_LAYERS} device pools")
-    arrays = _on_gpu(resident_pages, page_refs, free_pages, free_count, error_flags, workspace)
+    arrays = _on_gpu("iiiii.", resident_pages, page_refs, free_pages, free_count, error_flags, workspace)
     p = hs_page_pool(num_requests, max_pages, num_pages, page_size, row_bytes, len(device_pools),
-                     (ctypes.c_void_p * HS_MAX_LAYERS)(*_on_gpu(*device_pools)), *arrays, workspace_bytes)
+                     (ctypes.c_void_p * HS_MAX_LAYERS)(*_on_gpu("." * len(device_pools), *device_pools)), *arrays, workspace_bytes)
     p.kept = (list(device_pools), resident_pages, page_refs, free_pages, free_count, error_flags, workspace)
     p.device = next((x.get_device() for x in (*device_pools, *p.kept[1:]) if hasattr(x, "get_device")), None)
     return p
@@ -440,17 +459,17 @@ def hs_pages_init(pool: hs_page_pool, stream=None) -> None:
 
 
 def hs_pages_extend(pool: hs_page_pool, n: int, requests, old_lens, new_lens, granted=None, stream=None) -> None:
-    _check(_lib.hs_pages_extend(_pool_here(pool), n, *_on_gpu(requests, old_lens, new_lens, granted), _stream(stream)),
+    _check(_lib.hs_pages_extend(_pool_here(pool), n, *_on_gpu("iiii", requests, old_lens, new_lens, granted), _stream(stream)),
            "hs_pages_extend")
 
 
 def hs_pages_fork(pool: hs_page_pool, n: int, parents, children, lens, granted=None, stream=None) -> None:
-    _check(_lib.hs_pages_fork(_pool_here(pool), n, *_on_gpu(parents, children, lens, granted), _stream(stream)),
+    _check(_lib.hs_pages_fork(_pool_here(pool), n, *_on_gpu("iiii", parents, children, lens, granted), _stream(stream)),
            "hs_pages_fork")
 
 
 def hs_pages_free(pool: hs_page_pool, n: int, requests, first_pages=None, end_pages=None, stream=None) -> None:
-    _check(_lib.hs_pages_free(_pool_here(pool), n, *_on_gpu(requests, first_pages, end_pages), _stream(stream)),
+    _check(_lib.hs_pages_free(_pool_here(pool), n, *_on_gpu("iii", requests, first_pages, end_pages), _stream(stream)),
            "hs_pages_free")
 
 

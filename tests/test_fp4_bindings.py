@@ -72,3 +72,62 @@ def test_a_page_pool_of_another_device_is_refused(lib, call):
     call(page_pool(Array(1)), Array(1))
     call(page_pool(A), A)  # addresses only: theirs to know
     assert len(lib.names) == 3
+
+
+I, U, H, F, P = (Array(dtype=t) for t in (torch.int32, torch.uint32, torch.bfloat16, torch.float32, torch.uint8))
+ROWS = dict(kv=H, rows=I, pool=P, err=I)
+MLA = dict(q=H, pool=P, table=I, lens=I, o=H, lse=F, ws=P, err=I)
+POOL = dict(pools=P, table=I, refs=I, free=I, count=I, err=I, ws=P)
+
+
+def pack(kv, rows, pool, err):
+    hs.hs_fp4_pack_rows(8, kv, 576, rows, 1.0, pool, 100, err)
+
+
+def unpack(kv, rows, pool, err):
+    hs.hs_fp4_unpack_rows(8, pool, 100, rows, 1.0, kv, 576, err)
+
+
+def sparse(q, pool, table, lens, o, lse, ws, err):
+    hs.hs_fp4_sparse_mla_decode(2, 16, 4, 1, q, pool, 100, table, 0.1, 1.0, o, lse, ws, 0, err)
+
+
+def window(q, pool, table, lens, o, lse, ws, err):
+    hs.hs_fp4_window_mla_decode(2, 16, 1, 8, 1, 1, q, pool, 100, 16, 8, lens, table, 0.1, 1.0, o, lse, ws, 0, err)
+
+
+def make(pools, table, refs, free, count, err, ws):
+    hs.hs_pages_init(hs.make_page_pool([pools], 4, 8, 100, 16, 416, table, refs, free, count, ws, 1 << 20, err))
+
+
+def entries(a, b, c, granted):
+    p = page_pool(A)
+    hs.hs_pages_extend(p, 1, a, b, c, granted)
+    hs.hs_pages_fork(p, 1, a, b, c, granted)
+
+
+def ranges(a, b, c):
+    hs.hs_pages_free(page_pool(A), 1, a, b, c)
+
+
+@pytest.mark.parametrize("call,good", [(pack, ROWS), (unpack, ROWS), (sparse, MLA), (window, MLA), (make, POOL),
+                                       (entries, dict(a=I, b=I, c=I, granted=I)), (ranges, dict(a=I, b=I, c=I))])
+def test_arrays_of_another_type_are_refused(lib, call, good):
+    """torch makes int64 where nothing else is asked for: read as 32-bit numbers, every second one is 0."""
+    call(**good)
+    call(**{k: U if v is I else v for k, v in good.items()})
+    for bits in (torch.int16, torch.uint16):
+        call(**{k: Array(dtype=bits) if v is H else v for k, v in good.items()})
+    for name, of in good.items():
+        call(**dict(good, **{name: A}))  # an address has no type
+        if of is P:  # bytes of any kind
+            call(**dict(good, **{name: Array(dtype=torch.int32)}))
+            continue
+        if call is sparse and name == "lens":
+            continue
+        for other in (torch.int64, torch.float16, torch.float64, torch.int8, torch.bool,
+                      torch.float32 if of is not F else torch.int32, torch.int32 if of is H else torch.bfloat16):
+            seen = len(lib.names)
+            with pytest.raises(ValueError):
+                call(**dict(good, **{name: Array(dtype=other)}))
+            assert len(lib.names) == seen or call is entries
