@@ -135,7 +135,7 @@ __global__ void pages_init_kernel(const hs_page_pool p, const PageWork w) {
     p.page_refs[i] = 0;
     p.free_pages[i] = p.num_pages - 1 - (int32_t)i;  // page 0 on top
   }
-  for (int64_t i = t; i < (p.num_pages + 31) / 32; i += step) w.freed[i] = 0;
+  for (int64_t i = t; i < ((int64_t)p.num_pages + 31) / 32; i += step) w.freed[i] = 0;
   if (t == 0) {
     *p.free_count = p.num_pages;
     *w.ticket = 0;
