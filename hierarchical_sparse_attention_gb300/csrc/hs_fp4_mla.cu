@@ -238,13 +238,17 @@ __device__ __forceinline__ void store8(uint32_t* dst, const uint32_t (&w)[8], bo
     reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
   }
 }
+// What a unit of S is in log2 units (S leaves the scales out). A scale of zero stays above it, so that -inf stays -inf.
+__device__ __forceinline__ float score_log2(const Fp4MlaArgs& a) {
+  return fmaxf(fabsf(a.sm_scale * a.latent_scale * 1.4426950408889634f), 1e-37f);
+}
 // Two 32-bit floats at a time.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   float2 d;
-  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
-      "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 x, x, y;\n\t"
+      "mov.b64 {%0, %1}, x;\n\t}"
       : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
 }
 __device__ __forceinline__ float2 add2(float2 a, float2 b) {
@@ -706,12 +710,14 @@ __global__ void __launch_bounds__(T, 1)
         // thread. From one block to the next only the reference maximum goes over, from warp to warp
         // (the warps of the same heads): it is known once a block's scores have been read, so the
         // warpgroups' exponentials overlap. Each keeps the sum of its own blocks under the reference of
-        // its last one. The scores are read twice, for the maximum and for the weights.
+        // its last one. The scores are read twice, for the maximum and for the weights. References are
+        // scores as S holds them, and a weight's exponent is the difference, scaled: a score times the scale
+        // is rounded by whole units from 2^24 on, so that scaled scores less a scaled reference made a
+        // weight of its own reference 2^16 or 0 instead of 1.
         float* s_ref = reinterpret_cast<float*>(base + S_REF);
         const uint32_t pbuf = remote(base + O_P + wg * P_BUF, partner);  // (block g's buffer is g % NS = wg)
         const uint32_t r_alpha = remote(base + O_ALPHA + 4 * (wg * MH + head), partner), rbar = remote(&bs.p_full[wg], partner);
-        // scores in log2 units; a scale of zero stays above it, so that -inf stays -inf
-        const float sl2 = fmaxf(fabsf(a.sm_scale * a.latent_scale * 1.4426950408889634f), 1e-37f);
+        const float sl2 = score_log2(a);
         const uint32_t s_at = tbase + lane_off + S_COL + BJ * wg;
         int b = wg - done % NS;
         if (b < 0) b += NS;
@@ -753,7 +759,6 @@ __global__ void __launch_bounds__(T, 1)
             }
             bm = fmaxf(bm, fmaxf(x0, x1));
           }
-          bm *= sl2;
           float m_run = -INFINITY;
           if (g > 0) {
             // (the block before is the last warpgroup's block of this turn, or of the turn before)
@@ -764,13 +769,13 @@ __global__ void __launch_bounds__(T, 1)
           }
           // Lazy rescale: a head keeps its reference until a block's maximum passes it by 2^15, and O is
           // rescaled only on those rare jumps. (NaN scores leave it alone.)
-          const float m_new = bm > m_run + kRescaleLog2 || m_run == -INFINITY ? fmaxf(m_run, bm) : m_run;
+          const float m_new = (bm - m_run) * sl2 > kRescaleLog2 || m_run == -INFINITY ? fmaxf(m_run, bm) : m_run;
           s_ref[head] = m_new;
           __syncwarp();
           if (lane == 0) bar_arrive(&bs.m_set[wg][warp & 3]);
-          const float alpha = m_new == -INFINITY ? 1.f : ex2(m_run - m_new);  // m_run = -inf: O is still 0
+          const float alpha = m_new == -INFINITY ? 1.f : ex2((m_run - m_new) * sl2);  // m_run = -inf: O is still 0
           const float ref = m_new == -INFINITY ? 0.f : m_new;  // a NaN score stays one, an unseen row's weight is 0
-          l_own *= m_new == -INFINITY ? 1.f : ex2(m_own - m_new);
+          l_own *= m_new == -INFINITY ? 1.f : ex2((m_own - m_new) * sl2);
           m_own = m_new;
           // the O-CTA's P buffer is free once P . V of block g - 3 is done
           ok = __all_sync(0xffffffffu, g < NS || ready_or_wait<true>(bs.p_free, NS, g - NS, abort));
@@ -786,7 +791,7 @@ __global__ void __launch_bounds__(T, 1)
               uint32_t w[4];
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                float2 e = fma2(make_float2(t[8 * q + 2 * i], t[8 * q + 2 * i + 1]), make_float2(sl2, sl2), make_float2(-ref, -ref));
+                float2 e = mul2(add2(make_float2(t[8 * q + 2 * i], t[8 * q + 2 * i + 1]), make_float2(-ref, -ref)), make_float2(sl2, sl2));
                 e = make_float2(ex2(e.x), ex2(e.y));
                 const __half2 pb = __floats2half2_rn(e.x, e.y);
                 sum = add2(sum, e);
@@ -931,6 +936,7 @@ __global__ void __launch_bounds__(T, 1)
         if (!ok) break;  // (all of them: one that gave up further down comes here once more)
         const int set = warp < 4 ? 0 : warp >= 16 && warp < 20 ? 1 : 2;
         const bool direct = un.splits == 1;
+        const float sl2 = score_log2(a);
         float l = 0.f, m = -INFINITY;
         if (nblk > 0) {
           const int k = full % NF;
@@ -943,7 +949,7 @@ __global__ void __launch_bounds__(T, 1)
           m = fin[(done + nblk - 1) % NS * (FIN_WG / 4) + MH];
           for (int b = 0; b < min(nblk, NS); ++b) {
             const float* of = fin + (done + nblk - 1 - b) % NS * (FIN_WG / 4);
-            l += m == -INFINITY ? of[0] : of[0] * ex2(of[MH] - m);
+            l += m == -INFINITY ? of[0] : of[0] * ex2((of[MH] - m) * sl2);
           }
         }
         const float inv = l == 0.f ? 0.f : a.latent_scale / l;  // l is NaN where a weight is
@@ -977,7 +983,7 @@ __global__ void __launch_bounds__(T, 1)
           __syncwarp();
         }
         if (ok && set == 0 && head < un.live)
-          (direct ? a.lse : part_lse)[out0 + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+          (direct ? a.lse : part_lse)[out0 + head] = l == 0.f ? -INFINITY : (m * sl2 + log2f(l)) * 0.6931471805599453f;
         __syncwarp();
         if (nblk > 0 && ok) {
           tc_before();

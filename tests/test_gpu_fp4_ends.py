@@ -37,3 +37,67 @@ def test_the_most_pages_a_pool_can_have():
     hs.hs_pages_free(p, 1, i32(0), i32(1), None)
     assert table.tolist() == [[0, -1, -1, -1]] and int(count.item()) == n - 1 and free[n - 3:n - 1].tolist() == [2, 1]
     assert not marks.any() and int(err.item()) == 0
+
+
+def loud(rng, n, top):
+    """n rows whose RoPE values make scores of any sign up to about top^2 x 64, and their latents."""
+    kv = rng.standard_normal((n, 576))
+    kv[:, 512:] = rng.choice([-1.0, 1.0], (n, 64)) * top * rng.uniform(0.25, 1, (n, 64))
+    return F.pack(T.bf16_bits(kv), 1.0)
+
+
+@pytest.mark.parametrize("top", [2.0 ** 4, 2.0 ** 9, 2.0 ** 12, 2.0 ** 15, 2.0 ** 25])
+@pytest.mark.parametrize("sm", [T.SM, -1.0])
+@pytest.mark.parametrize("splits", [1, 3])
+def test_scores_of_any_size_average_the_rows(top, sm, splits):
+    """A score passes 2^28 where its rounding in 32 bits is whole powers of two of a weight. Whatever the scores
+    are off by (test_gpu_fp4's E), weights are positive and add up to one:
+    * of a single row the weight is exactly 1: o is its latent, off by the bf16 rounding, 2^-9 of it;
+    * of many rows, a weight is off by 2^-11 of itself by its rounding, and by 2^-25 of the largest: o lies between the
+      rows' least and largest latents, but for 2^-11 + 2^-16 (sums) + 2^-9 (bf16) < 2^-8 and n 2^-25 of the largest
+      magnitude."""
+    hs = T._gpu()
+    rng = np.random.default_rng(int(np.log2(top)))
+    pool = loud(rng, 400, top)
+    q = rng.standard_normal((6, 24, 576))
+    q[:, :, 512:] = rng.choice([-1.0, 1.0], (6, 24, 64)) * top * rng.uniform(0.25, 1, (6, 24, 64))
+    q = T.bf16_bits(q)
+    rows = np.full((6, 200), -1, np.int32)
+    rows[0, 0], rows[1, 199], rows[2, 70] = 3, 5, 8  # one row only
+    rows[3:] = rng.integers(0, 400, (3, 200))
+    rows[5, 3:] = rows[5, 0]  # three rows, one of them again and again
+    o, lse, err = T.sparse(hs, q, T.d(pool), T.d(rows), 1.0, splits, sm)
+    assert err == 0
+    lat, rope = F.unpack(pool, 1.0)
+    for r in range(6):
+        mine = rows[r][rows[r] >= 0]
+        if r < 3:
+            assert (np.abs(o[r] - lat[mine]) <= 2.0 ** -9 * np.abs(lat[mine])).all()
+        low, high = lat[mine].min(0), lat[mine].max(0)
+        slack = (2.0 ** -8 + mine.size * 2.0 ** -25) * np.abs(lat[mine]).max(0)
+        assert (o[r] >= low - slack).all() and (o[r] <= high + slack).all()
+        _, want, _, B = F.attend(F.bf16_decode(q[r]), lat[mine], rope[mine], sm)
+        assert (np.abs(lse[r] - want) <= 2.0 ** -16 * B + 2.0 ** -20 * (1 + np.abs(want))).all()
+
+
+@pytest.mark.parametrize("order", [1, -1])
+def test_one_score_far_above_all_others_takes_all(order):
+    """Scores 2^23 k for k = 0 .. 15, all of them exact (one RoPE value, powers of two times k) and so far apart that a
+    rounding does not move a weight off 0 or 1: every query sees the loudest row alone, rows rising or falling."""
+    hs = T._gpu()
+    rng = np.random.default_rng(5)
+    kv = np.zeros((16, 576))
+    kv[:, :512] = rng.standard_normal((16, 512))
+    kv[:, 512] = 2.0 ** 13 * np.arange(16)
+    rec = F.pack(T.bf16_bits(kv), 1.0)[::order].copy()
+    pool = np.repeat(rec, 60, 0)
+    q = np.zeros((1, 20, 576))
+    q[:, :, 512] = 2.0 ** 14
+    rows = np.arange(16 * 60, dtype=np.int32)[None]
+    o, lse, err = T.sparse(hs, T.bf16_bits(q), T.d(pool), T.d(rows), 1.0, 1, 2.0 ** -4)
+    lat, _ = F.unpack(rec, 1.0)
+    top = lat[15 if order > 0 else 0]
+    assert err == 0
+    # sixty equal rows' weights are 1 / 60 each: their sum in 32 bits is off by 2^-24 of it a term
+    assert (np.abs(o[0] - top) <= (2.0 ** -9 + 2.0 ** -16) * np.abs(top)).all()
+    assert (np.abs(lse - (15 * 2.0 ** 23 + np.log(60))) <= 2.0 ** -20 * 15 * 2.0 ** 23).all()
