@@ -40,10 +40,12 @@
 // latent_scale, which goes into the scores' scale and the outputs instead. Q's latent part is
 // rounded from bf16 to f16: exact between 2^-14 and 65504, off by at most 2^-25 below. RoPE values
 // meet Q's in bf16, exact (Q's divided by latent_scale, a power of two), in MMAs of their own type
-// that add to the same sums. P is rounded to f16 (2^-11 of each weight, against 2^-8 of bf16: P is
-// the one operand that has to be rounded, and bf16 would cost as much as the output's rounding);
-// the weights' sum takes them unrounded, so lse does not see it. Scores, maxima, sums and O are in
-// 32 bits.
+// that add to the same sums. P, the one operand that has to be rounded, is rounded to f16: by up to
+// 2^-11 of a weight (bf16 would cost 2^-8, as much as the output's rounding), and, as f16 has no more
+// than 40 binades, by up to 2^-32 of the largest weight where a weight is smaller than 2^-21 of it
+// (kRefLog2). Over N such rows, as behind a sink that outweighs each of them, the output may be off
+// by N 2^-32 of their latents; split rows have a largest weight per split. The weights' sum takes
+// them unrounded, so lse does not see it. Scores, maxima, sums and O are in 32 bits.
 //
 // NaN and infinities. A row that a query does not see gets P = 0, and 0 x NaN must not reach O: V
 // holds zero for a block whose scale is NaN, while K keeps the NaN, which makes the score, the
@@ -110,10 +112,12 @@ constexpr uint32_t O_END = O_FIN + NF * NS * FIN_WG;
 constexpr uint32_t SMEM_BYTES = S_END > O_END ? S_END : O_END;
 constexpr uint32_t STATIC_BYTES = 1024;  // barriers and flags, one block of a tile's alignment
 static_assert(STATIC_BYTES + SMEM_BYTES <= 227 * 1024, "shared memory of a CTA");
-// A reference maximum stays until it is passed by 2^15, so that P < 65504 in f16, whose precision is the
-// same there. (At 2^8 a few heads of a tile were rescaled in the course of 2,048 rows, 2 us each time:
-// 256 requests took 189 us instead of 182.)
-constexpr float kRescaleLog2 = 15.f;
+// P of a score that equals its reference is 2^7, and a reference stays until it is passed by 2^8.9, so that
+// P < 2^15.91 = 61,500 in f16, which then keeps a weight to 2^-11 of itself down to 2^-21 of the
+// reference's, and to 2^-32 of the reference's below that. Room below the reference is taken from the room
+// above it, where too little costs rescales, ~2 us each (us, 256 requests of 2,048 rows / a window of
+// 8,192): 161 / 156 with 0 and 15, 160 / 158 with 7 and 8.9, 167 / 162 with 8 and 7, 220 / 191 with 10 and 5.
+constexpr float kRefLog2 = 7.f, kRescaleLog2 = 8.9f;
 constexpr uint32_t kIdescQK = idesc(BJ, MH, false);                              // f16 latents
 constexpr uint32_t kIdescRope = kIdescQK | (1u << 7) | (1u << 10);               // bf16 RoPE
 constexpr uint32_t kIdescPV = idesc(256, MH, true);
@@ -243,12 +247,12 @@ __device__ __forceinline__ float score_log2(const Fp4MlaArgs& a) {
   return fmaxf(fabsf(a.sm_scale * a.latent_scale * 1.4426950408889634f), 1e-37f);
 }
 // Two 32-bit floats at a time.
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 d;
-  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 x, x, y;\n\t"
-      "mov.b64 {%0, %1}, x;\n\t}"
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
       : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
   return d;
 }
 __device__ __forceinline__ float2 add2(float2 a, float2 b) {
@@ -767,8 +771,8 @@ __global__ void __launch_bounds__(T, 1)
             if (!ok) break;
             if (b > 0) m_run = s_ref[head];
           }
-          // Lazy rescale: a head keeps its reference until a block's maximum passes it by 2^15, and O is
-          // rescaled only on those rare jumps. (NaN scores leave it alone.)
+          // Lazy rescale: a head keeps its reference until a block's maximum passes it by 2^kRescaleLog2,
+          // and O is rescaled only on those rare jumps. (NaN scores leave it alone.)
           const float m_new = (bm - m_run) * sl2 > kRescaleLog2 || m_run == -INFINITY ? fmaxf(m_run, bm) : m_run;
           s_ref[head] = m_new;
           __syncwarp();
@@ -791,7 +795,8 @@ __global__ void __launch_bounds__(T, 1)
               uint32_t w[4];
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                float2 e = mul2(add2(make_float2(t[8 * q + 2 * i], t[8 * q + 2 * i + 1]), make_float2(-ref, -ref)), make_float2(sl2, sl2));
+                float2 e = fma2(add2(make_float2(t[8 * q + 2 * i], t[8 * q + 2 * i + 1]), make_float2(-ref, -ref)),
+                                make_float2(sl2, sl2), make_float2(kRefLog2, kRefLog2));
                 e = make_float2(ex2(e.x), ex2(e.y));
                 const __half2 pb = __floats2half2_rn(e.x, e.y);
                 sum = add2(sum, e);
@@ -983,7 +988,7 @@ __global__ void __launch_bounds__(T, 1)
           __syncwarp();
         }
         if (ok && set == 0 && head < un.live)
-          (direct ? a.lse : part_lse)[out0 + head] = l == 0.f ? -INFINITY : (m * sl2 + log2f(l)) * 0.6931471805599453f;
+          (direct ? a.lse : part_lse)[out0 + head] = l == 0.f ? -INFINITY : (m * sl2 + (log2f(l) - kRefLog2)) * 0.6931471805599453f;
         __syncwarp();
         if (nblk > 0 && ok) {
           tc_before();

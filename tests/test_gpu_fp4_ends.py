@@ -101,3 +101,75 @@ def test_one_score_far_above_all_others_takes_all(order):
     # sixty equal rows' weights are 1 / 60 each: their sum in 32 bits is off by 2^-24 of it a term
     assert (np.abs(o[0] - top) <= (2.0 ** -9 + 2.0 ** -16) * np.abs(top)).all()
     assert (np.abs(lse - (15 * 2.0 ** 23 + np.log(60))) <= 2.0 ** -20 * 15 * 2.0 ** 23).all()
+
+
+def check_long(q, lat, rope, o, lse, what):
+    """test_gpu_fp4's bound for long sums and small weights. Per output element, with its A, B and C:
+    * scores as there, E; a weight is off by 2^-11 of itself, or, below 2^-21 of the largest weight, by 2^-32 of the
+      largest, which is at most the weights' sum: 2^-32 C;
+    * O's N / 16 accumulations are off by 2^-22 of the sum of magnitudes each, the N additions of the weights' sum by
+      2^-24 of it each, spread over six partial sums: N (2^-26 + 2^-26) A;
+    * 2^-8 of o, the bf16 result. lse: E, the N 2^-26 of the sum, and 2^-20 (1 + |lse|)."""
+    n = lat.shape[0]
+    want, wlse, A, B = F.attend(F.bf16_decode(q), lat, rope, T.SM)
+    E = 2.0 ** -16 * B
+    bound = ((2 * E[:, None] + 2.0 ** -11 + 2.0 ** -16 + n * 2.0 ** -25) * A + 2.0 ** -32 * np.abs(lat).sum(0) +
+             2.0 ** -8 * np.abs(want) + 1e-30)
+    off = np.abs(o - want)
+    assert (off <= bound).all(), f"{what}: {(off / bound).max()} of the bound, {np.linalg.norm(off) / np.linalg.norm(want)} of the norm"
+    assert (np.abs(lse - wlse) <= E + n * 2.0 ** -26 + 2.0 ** -20 * (1 + np.abs(wlse))).all(), what
+    return off, want
+
+
+def behind_a_sink(rng, n, nats, jitter):
+    """n rows of which the first is a sink: its score is `nats` above the others' (which differ by up to jitter), and it
+    has no value in half of the latents. The others' latents are positive, so that their errors add up."""
+    kv = np.zeros((n, 576))
+    kv[:, :512] = rng.uniform(0.25, 1, (n, 512))
+    kv[0, :256] = 0
+    kv[1:, 513] = rng.uniform(-jitter, jitter, n - 1) / T.SM
+    kv[0, 512] = nats / T.SM
+    q = np.zeros((20, 576))
+    q[:, 512:514] = 1
+    return F.pack(T.bf16_bits(kv), 1.0), T.bf16_bits(q)
+
+
+@pytest.mark.parametrize("nats", [10.0, 16.0, 18.0, 21.0])
+@pytest.mark.parametrize("jitter", [0.0, 1.0])
+def test_rows_behind_a_sink_keep_their_weight(nats, jitter):
+    """Each of the others' weights is 2^-14 to 2^-30 of the sink's, which is seen first and sets the reference; half of
+    the outputs are theirs alone. Through the row table and through the window, whole and split."""
+    hs = T._gpu()
+    rng = np.random.default_rng(int(nats))
+    rec, q = behind_a_sink(rng, 4096, nats, jitter)
+    lat, rope = F.unpack(rec, 1.0)
+    rows = np.arange(4096, dtype=np.int32)[None]
+    for splits in (1, 3):
+        o, lse, err = T.sparse(hs, q[None], T.d(rec), T.d(rows), 1.0, splits)
+        assert err == 0
+        off, want = check_long(q, lat, rope, o[0], lse[0], f"row table, {splits} splits")
+        if nats <= 18:
+            assert (off[:, :256] <= 2.0 ** -5 * want[:, :256]).all()
+    n = 32768
+    rec, q = behind_a_sink(rng, n, nats, jitter)
+    table, total = T.pages_for(rng, np.array([n], np.int32), 64, n // 64)
+    pool = np.zeros((total, 416), np.uint8)
+    pool[(table[0].astype(np.int64)[:, None] * 64 + np.arange(64)).reshape(-1)] = rec
+    lat, rope = F.unpack(rec, 1.0)
+    o, lse, err = T.window(hs, q[None, None], T.d(pool), 64, np.array([n], np.int32), table, n - 1, 1, 1.0, 1)
+    assert err == 0
+    check_long(q, lat, rope, o[0, 0], lse[0, 0], "window")
+
+
+def test_a_window_over_a_whole_context_behind_a_sink():
+    """131,072 rows of 2^-26 of the sink's weight each: together 2^-9 of the sum, and half of the outputs."""
+    hs = T._gpu()
+    rng = np.random.default_rng(1)
+    n = 1 << 17
+    rec, q = behind_a_sink(rng, n, 18.0, 0.0)
+    table = np.arange(n // 64, dtype=np.int32)[None]
+    o, lse, err = T.window(hs, q[None, None], T.d(rec), 64, np.array([n], np.int32), table, 2 ** 31 - 1, 1, 1.0, 1)
+    assert err == 0
+    lat, rope = F.unpack(rec, 1.0)
+    off, want = check_long(q, lat, rope, o[0, 0], lse[0, 0], "whole context")
+    assert (off[:, :256] <= 2.0 ** -5 * want[:, :256]).all()  # 2^-32 of 2^-25.97, 2^-8 twice, 2^-11: 0.024
