@@ -37,8 +37,10 @@
 // thread's outstanding loads share a few scoreboards, so that waiting for a block waits for the next.
 //
 // Precision. code x scale is exact in f16, so K and V hold the latents' exact values but for
-// latent_scale, which goes into the scores' scale and the outputs instead. Q's latent part is
-// rounded from bf16 to f16: exact between 2^-14 and 65504, off by at most 2^-25 below. RoPE values
+// latent_scale, which goes into the scores' scale and the outputs instead. Q's latent part goes
+// from bf16 to f16: exact but for values below 2^-14, off by at most 2^-25, which is 2^-19 of the head's
+// largest; a head whose largest is below 2^-6 or above 65504 is divided by a power of two, which goes
+// into its scores' scale (the values are exact then down to 2^-32 of the largest). RoPE values
 // meet Q's in bf16, exact (Q's divided by latent_scale, a power of two), in MMAs of their own type
 // that add to the same sums. P, the one operand that has to be rounded, is rounded to f16: by up to
 // 2^-11 of a weight (bf16 would cost 2^-8, as much as the output's rounding), and, as f16 has no more
@@ -58,6 +60,7 @@
 #include <cuda_fp8.h>
 
 #include <atomic>
+#include <type_traits>
 
 namespace hs {
 
@@ -100,7 +103,8 @@ constexpr uint32_t S_RAW = S_ROPE + NR * KV_ATOM;
 static_assert(ATOMS * QBOX <= NT * TILE && QBOX == 2 * KV_ATOM, "Q's staging");
 constexpr uint32_t S_REF = S_RAW + NDEQ * S_RING;  // the reference maxima, handed from block to block
 constexpr uint32_t S_MASK = S_REF + MH * 4;     // a byte per block and dequantisation warp: which of its rows exist
-constexpr uint32_t S_END = S_MASK + MASKS * NDEQ;
+constexpr uint32_t S_QTOP = S_MASK + MASKS * NDEQ;  // a head's largest latent in each third of Q, and RoPE value
+constexpr uint32_t S_END = S_QTOP + (NS + 1) * MH * 2;
 constexpr uint32_t O_TILES = 0, O_RAW = NT * TILE;
 constexpr uint32_t O_P = (O_RAW + NDEQ * O_RING + 1023u) & ~1023u;
 constexpr uint32_t P_BUF = MH * BJ * 2, P_BYTES = P_BUF + MH * 4;  // P and the rescale factors of a block
@@ -242,9 +246,23 @@ __device__ __forceinline__ void store8(uint32_t* dst, const uint32_t (&w)[8], bo
     reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
   }
 }
-// What a unit of S is in log2 units (S leaves the scales out). A scale of zero stays above it, so that -inf stays -inf.
-__device__ __forceinline__ float score_log2(const Fp4MlaArgs& a) {
-  return fmaxf(fabsf(a.sm_scale * a.latent_scale * 1.4426950408889634f), 1e-37f);
+// What a unit of S is in log2 units (S leaves the scales out, and `up`, what Q was divided by). A scale of zero
+// stays above it, so that -inf stays -inf.
+__device__ __forceinline__ float score_log2(const Fp4MlaArgs& a, float up = 1.f) {
+  return fminf(fmaxf(fabsf(a.sm_scale * a.latent_scale * 1.4426950408889634f) * up, 1e-37f), 3e38f);
+}
+// The power of two that a head's Q is divided by, given the bf16 bits of its largest latent and RoPE value. 1 where f16
+// holds its latents: none over 65504, and what is lost (2^-25 of values below 2^-14) at most 2^-19 of the largest.
+// Otherwise the largest becomes 2^15 .. 65280. RoPE values are divided too, in bf16: it is kept so large that none
+// overflows, over latent_scale >= 2^-32, unless they are 2^60 times the largest latent, whose part in a score is
+// lost then anyway.
+__device__ __forceinline__ float q_divisor(uint32_t top, uint32_t rope) {
+  if (top == 0 || (top >= 0x3C80u && top < 0x4780u)) return 1.f;  // 2^-6, 2^16
+  return __uint_as_float((uint32_t)max(max((int)(top >> 7) - 15, (int)(rope >> 7) - 75), 127 - 95) << 23);
+}
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t m, const uint4& x) {  // of magnitudes
+  constexpr uint32_t k = 0x7FFF7FFFu;
+  return __vmaxu2(m, __vmaxu2(__vmaxu2(x.x & k, x.y & k), __vmaxu2(x.z & k, x.w & k)));
 }
 // Two 32-bit floats at a time.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
@@ -661,43 +679,76 @@ __global__ void __launch_bounds__(T, 1)
       float m_own = -INFINITY, l_own = 0.f;  // softmax: the sum of this thread's blocks, under this reference
       if (warp < 4 * NS) {
         const int wg = warp >> 2;
+        float up = 1.f;  // what this head's Q is divided by
         if (nblk > 0) {
           // Q into tensor memory (warpgroup wg the columns [96 wg, 96 wg + 96)), column c holding dims
           // 2c, 2c + 1: the latent part as f16, the RoPE part as bf16 over latent_scale. Q has landed
-          // only after the last unit's MMAs, which read the columns.
+          // only after the last unit's MMAs, which read the columns. It is taken as it is first, and once
+          // more where some head's latents do not fit f16 so (3 us more a unit; the look costs nothing that shows).
           ok = __all_sync(0xffffffffu, ready_or_wait(&bs.q_raw[wg], 1, (int)q_phase, abort));
           tc_after();
           const bool live = ok && head < un.live;
-          const float inv = 1.f / a.latent_scale;
           const uint32_t sign = a.sm_scale < 0.f ? 0x80008000u : 0u;  // so that scores scale by a positive factor
+          const auto box = [&](int bx) { return base + q_stage(bx, head >> 6, done) + (head & 63) * 128; };
+          const auto take = [&](auto divide, float down) {  // the largest magnitude in f16 of this third's latents
+            constexpr bool kDivide = decltype(divide)::value;
+            const float inv = down / a.latent_scale;
+            __half2 top = __float2half2_rn(0.f);
 #pragma unroll 1
-          for (int bx = QATOMS / NS * wg; bx < QATOMS / NS * (wg + 1); ++bx) {
-            const uint8_t* src = base + q_stage(bx, head >> 6, done) + (head & 63) * 128;
+            for (int bx = QATOMS / NS * wg; bx < QATOMS / NS * (wg + 1); ++bx) {
+              const uint8_t* src = box(bx);
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {  // two 16-B chunks: 16 dims, 8 columns
-              uint32_t x[8] = {};
-              if (live) {
-                *reinterpret_cast<uint4*>(x) = *reinterpret_cast<const uint4*>(src + (((2 * h) ^ (head & 7)) << 4));
-                *reinterpret_cast<uint4*>(x + 4) = *reinterpret_cast<const uint4*>(src + (((2 * h + 1) ^ (head & 7)) << 4));
-              }
-              if (bx < ATOMS) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = bf16x2_to_f16x2(x[i]) ^ sign;
-              } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                  const __nv_bfloat162 v =
-                      __floats2bfloat162_rn(__uint_as_float(x[i] << 16) * inv, __uint_as_float(x[i] & 0xFFFF0000u) * inv);
-                  x[i] = *reinterpret_cast<const uint32_t*>(&v) ^ sign;
+              for (int h = 0; h < 4; ++h) {  // two 16-B chunks: 16 dims, 8 columns
+                uint32_t x[8] = {};
+                if (live) {
+                  *reinterpret_cast<uint4*>(x) = *reinterpret_cast<const uint4*>(src + (((2 * h) ^ (head & 7)) << 4));
+                  *reinterpret_cast<uint4*>(x + 4) = *reinterpret_cast<const uint4*>(src + (((2 * h + 1) ^ (head & 7)) << 4));
                 }
+                if (bx < ATOMS) {
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) {
+                    const float lo = __uint_as_float(x[i] << 16), hi = __uint_as_float(x[i] & 0xFFFF0000u);
+                    const __half2 v = kDivide ? __floats2half2_rn(lo * down, hi * down) : __floats2half2_rn(lo, hi);
+                    if (!kDivide) top = __hmax2(top, __habs2(v));
+                    x[i] = *reinterpret_cast<const uint32_t*>(&v) ^ sign;
+                  }
+                } else {
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) {
+                    const __nv_bfloat162 v =
+                        __floats2bfloat162_rn(__uint_as_float(x[i] << 16) * inv, __uint_as_float(x[i] & 0xFFFF0000u) * inv);
+                    x[i] = *reinterpret_cast<const uint32_t*>(&v) ^ sign;
+                  }
+                }
+                asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(
+                                 tbase + lane_off + Q_COL + 32 * bx + 8 * h),
+                             "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+                             : "memory");
               }
-              asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(
-                               tbase + lane_off + Q_COL + 32 * bx + 8 * h),
-                           "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
-                           : "memory");
             }
+            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+            return fmaxf(__low2float(top), __high2float(top));
+          };
+          const float top = take(std::false_type{}, 1.f);
+          // a third that is too large, or so small that the head may be: all of it is looked at (every softmax warp
+          // comes to these barriers, whether its wait ended well or not)
+          if (sync_or<2>(live && !(top >= 0x1p-6f && top < 65504.f), 4 * NS * 32)) {
+            uint16_t* tops = reinterpret_cast<uint16_t*>(base + S_QTOP) + head;
+            uint32_t lat = 0, rope = 0;  // two lanes of 16 bits
+#pragma unroll 1
+            for (int bx = QATOMS / NS * wg; bx < QATOMS / NS * (wg + 1); ++bx)
+#pragma unroll 1
+              for (int c = 0; c < 8; ++c) {
+                const uint4 x = *reinterpret_cast<const uint4*>(box(bx) + ((c ^ (head & 7)) << 4));
+                if (bx < ATOMS) lat = max_bf16x2(lat, x);
+                else rope = max_bf16x2(rope, x);
+              }
+            tops[MH * wg] = (uint16_t)max(lat & 0xFFFFu, lat >> 16);
+            if (wg == NS - 1) tops[MH * NS] = (uint16_t)max(rope & 0xFFFFu, rope >> 16);
+            sync_n<2>(4 * NS * 32);
+            up = q_divisor(max(max((uint32_t)tops[0], (uint32_t)tops[MH]), (uint32_t)tops[2 * MH]), tops[3 * MH]);
+            if (__any_sync(0xffffffffu, live && up != 1.f)) take(std::true_type{}, 1.f / up);
           }
-          asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
           tc_before();
           __syncwarp();
           if (lane == 0) bar_arrive(&bs.q_full);
@@ -721,7 +772,7 @@ __global__ void __launch_bounds__(T, 1)
         float* s_ref = reinterpret_cast<float*>(base + S_REF);
         const uint32_t pbuf = remote(base + O_P + wg * P_BUF, partner);  // (block g's buffer is g % NS = wg)
         const uint32_t r_alpha = remote(base + O_ALPHA + 4 * (wg * MH + head), partner), rbar = remote(&bs.p_full[wg], partner);
-        const float sl2 = score_log2(a);
+        const float sl2 = score_log2(a, up);
         const uint32_t s_at = tbase + lane_off + S_COL + BJ * wg;
         int b = wg - done % NS;
         if (b < 0) b += NS;
@@ -815,7 +866,7 @@ __global__ void __launch_bounds__(T, 1)
           const uint32_t fin = remote(base + O_FIN, partner) + ((full % NF) * NS + wg) * FIN_WG;
           const uint32_t bar = remote(&bs.fin[full % NF], partner);
           st_async_f32(fin + 4 * head, l_own, bar);
-          st_async_f32(fin + 4 * (MH + head), m_own, bar);
+          st_async_f32(fin + 4 * (MH + head), m_own * up, bar);  // a score again, exact
         }
       } else if (warp == S_ISSUER) {
         // (tensor memory starts at 0: all of it is allocated here)

@@ -559,8 +559,8 @@ HS_API size_t hs_fp4_mla_workspace_bytes(int32_t num_requests, int32_t num_heads
  *   hs_fp4_mla_workspace_bytes(R, num_heads, 1, splits) device bytes, 16-byte aligned, contents
  *   of no matter; calls that share it must be ordered.
  *   error_flags: device uint32, HS_FLAG_* bits OR-ed in.
- *   q's latent part goes through f16: 65520 and more is infinite there, values below 2^-14 are off by
- *   up to 2^-25. A row's weight goes through f16 too: off by up to 2^-11 of itself, and a weight below
+ *   q's latent part goes through f16: exact, but for values that are off by up to 2^-19 of their head's
+ *   largest (those below 2^-14). A row's weight goes through f16 too: off by up to 2^-11 of itself, and a weight below
  *   2^-21 of the query's largest by up to 2^-32 of the largest (of its split), so that N rows that one
  *   row outweighs so far, as a sink may, are off by up to N 2^-32 of their latents; lse takes weights
  *   as they are. sm_scale x latent_scale x log2(e) has to be finite in fp32. An MMA pipeline that

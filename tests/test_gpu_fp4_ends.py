@@ -76,7 +76,7 @@ def test_scores_of_any_size_average_the_rows(top, sm, splits):
         low, high = lat[mine].min(0), lat[mine].max(0)
         slack = (2.0 ** -8 + mine.size * 2.0 ** -25) * np.abs(lat[mine]).max(0)
         assert (o[r] >= low - slack).all() and (o[r] <= high + slack).all()
-        _, want, _, B = F.attend(F.bf16_decode(q[r]), lat[mine], rope[mine], sm)
+        _, want, _, B = F.attend(T.bf16_decode(q[r]), lat[mine], rope[mine], sm)
         assert (np.abs(lse[r] - want) <= 2.0 ** -16 * B + 2.0 ** -20 * (1 + np.abs(want))).all()
 
 
@@ -111,7 +111,7 @@ def check_long(q, lat, rope, o, lse, what):
       2^-24 of it each, spread over six partial sums: N (2^-26 + 2^-26) A;
     * 2^-8 of o, the bf16 result. lse: E, the N 2^-26 of the sum, and 2^-20 (1 + |lse|)."""
     n = lat.shape[0]
-    want, wlse, A, B = F.attend(F.bf16_decode(q), lat, rope, T.SM)
+    want, wlse, A, B = F.attend(T.bf16_decode(q), lat, rope, T.SM)
     E = 2.0 ** -16 * B
     bound = ((2 * E[:, None] + 2.0 ** -11 + 2.0 ** -16 + n * 2.0 ** -25) * A + 2.0 ** -32 * np.abs(lat).sum(0) +
              2.0 ** -8 * np.abs(want) + 1e-30)
@@ -173,3 +173,44 @@ def test_a_window_over_a_whole_context_behind_a_sink():
     lat, rope = F.unpack(rec, 1.0)
     off, want = check_long(q, lat, rope, o[0, 0], lse[0, 0], "whole context")
     assert (off[:, :256] <= 2.0 ** -5 * want[:, :256]).all()  # 2^-32 of 2^-25.97, 2^-8 twice, 2^-11: 0.024
+
+
+@pytest.mark.parametrize("k", [-60, -30, -17, 17, 60, 100])
+@pytest.mark.parametrize("splits", [1, 2])
+def test_queries_of_any_size(k, splits):
+    """A query times 2^k with a scale over 2^k has the same scores: the same bits, as nothing but exponents differ."""
+    hs = T._gpu()
+    q, pool, rows = T.case(13, 3, 40, 300, 500, g=0.5)
+    want = T.sparse(hs, q, T.d(pool), T.d(rows), 0.5, splits)
+    q2 = T.bf16_bits(T.bf16_decode(q) * 2.0 ** k)
+    got = T.sparse(hs, q2, T.d(pool), T.d(rows), 0.5, splits, T.SM * 2.0 ** -k)
+    for r in range(3):
+        T.check(q[r], pool[rows[r][rows[r] >= 0]], 0.5, want[0][r], want[1][r], f"request {r}")
+    assert np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1]) and got[2] == want[2] == 0
+
+
+def test_queries_whose_values_differ_in_size():
+    """Heads of 2^-20 beside heads of 2^40, latents from 2^-28 of a head's largest up to it, latents that are all zero,
+    RoPE values 2^30 below and above the latents': the scores to test_gpu_fp4's E."""
+    hs = T._gpu()
+    rng = np.random.default_rng(17)
+    _, pool, rows = T.case(19, 2, 1, 200, 300)
+    q = rng.standard_normal((2, 40, 576))
+    q[:, :, :512] *= 2.0 ** rng.integers(-28, 1, (2, 40, 512))
+    q[:, 10:20, 512:] *= 2.0 ** -30
+    q[:, 20:30, 512:] *= 2.0 ** 30
+    q[:, 30:35, :512] = 0
+    q *= 2.0 ** rng.integers(-20, 40, (2, 40, 1))
+    q = T.bf16_bits(q)
+    for sm in (T.SM, T.SM * 2.0 ** 20, T.SM * 2.0 ** -40):
+        o, lse, err = T.sparse(hs, q, T.d(pool), T.d(rows), 1.0, 1, sm)
+        assert err == 0
+        for r in range(2):
+            lat, rope = F.unpack(pool[rows[r][rows[r] >= 0]], 1.0)
+            want, wlse, A, B = F.attend(T.bf16_decode(q[r]), lat, rope, sm)
+            E = 2.0 ** -16 * B
+            assert (np.abs(lse[r] - wlse) <= E + 2.0 ** -20 * (1 + np.abs(wlse))).all()
+            sure = E < 2.0 ** -6  # where the scores decide anything
+            bound = (2 * E[:, None] + 2.0 ** -10) * A + 2.0 ** -32 * np.abs(lat).sum(0) + 2.0 ** -8 * np.abs(want) + 1e-30
+            assert (np.abs(o[r] - want) <= bound)[sure].all()
+            assert (np.abs(o[r]) <= np.abs(lat).max(0) * (1 + 2.0 ** -7)).all()
