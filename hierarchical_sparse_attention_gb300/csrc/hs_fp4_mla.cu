@@ -563,10 +563,11 @@ __device__ __forceinline__ Unit<kWin> unit_of(const Fp4MlaArgs& a, const Tiles& 
 }
 
 // Where half a box of Q (64 rows of 64 dims) is staged: the latents' over the K tiles, the RoPE values'
-// over the RoPE tiles of the unit's third and fourth block (g0: the number of its first one), whose
-// copies start when Q is in tensor memory; those of the first two may be on their way.
+// over the RoPE tiles of two of the unit's blocks (g0: the number of its first one), whose copies start
+// when Q is in tensor memory: those of the first S_ND blocks may be on their way before.
+static_assert(NR >= S_ND + 2, "Q's two staged tiles are none of those that a unit's first copies go to");
 __device__ __forceinline__ uint32_t q_stage(int bx, int half, int g0) {
-  return bx < ATOMS ? S_TILES + bx * QBOX + half * KV_ATOM : S_ROPE + (g0 + 3 + half) % NR * KV_ATOM;
+  return bx < ATOMS ? S_TILES + bx * QBOX + half * KV_ATOM : S_ROPE + (g0 + S_ND + half) % NR * KV_ATOM;
 }
 // Q's 128 rows from row0 as tensor boxes of 64 rows and dims, a third of the dims to a barrier (rows past
 // the tile's are not used).
