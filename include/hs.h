@@ -660,6 +660,13 @@ HS_API hs_status hs_pages_extend(const hs_page_pool* pool, int32_t n, const int3
  * child named twice or also a parent of the call (HS_FLAG_DUP), a length outside [0, max_pages *
  * page_size] (HS_FLAG_SEQLEN), a child's row that holds a page (HS_FLAG_STATE). A negative parent
  * or child is padding. A refused entry changes nothing.
+ * Tokens before lens[i] are final from then on: a request that falls back below it (drafts that were
+ * rejected) would write a page that it shares, so fork at accepted lengths.
+ * The rest of a child's state is the caller's, as for every request row that is taken into use: hot slots
+ * empty (device_buffer_tokens -1, lru_slots and lru_clock 0; where lens[i] <= H, its tokens off the pages in
+ * slots of their own, as hs_resolve wants it), hs_reset_hints for speed. host_cache_locs of the tokens
+ * before lens[i] may name the parent's host rows, which no call writes again but hs_backup of a request whose
+ * newest token they hold, with the same bytes; later tokens need host rows of the child's own.
  *   parents, children, lens [n] device, n <= num_requests; granted [n] device or NULL: fresh pages
  *   taken (0 or 1), -1 refused
  * Two kernel launches. n == 0 is a no-op. */
