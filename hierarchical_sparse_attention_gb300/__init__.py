@@ -44,6 +44,7 @@ EXPORTS = ("hs_workspace_bytes", "hs_create", "hs_resolve", "hs_backup", "hs_get
 HS_MAX_SPEC_QUERIES = 8
 HS_NOALLOC_MAX_LAYERS = 8
 HS_FP4_ROW_BYTES = 416
+HS_MAX_FP4_MLA_REQUESTS = 1 << 20
 HS_MAX_PAGE_REQUESTS = 65536
 HS_MAX_PAGE_ENTRIES = 1 << 20
 

@@ -163,7 +163,7 @@ bool fp4_rows_ok(int32_t n, const uint16_t* kv, int64_t kv_stride, const int32_t
 
 // num_requests x num_queries x num_heads stays within 32-bit grids and tensor extents.
 bool fp4_mla_shape_ok(int32_t num_requests, int32_t num_heads, int32_t num_queries, int32_t splits) {
-  return num_requests >= 1 && num_requests <= (1 << 20) && num_heads >= 1 && num_heads <= 128 && num_queries >= 1 &&
+  return num_requests >= 1 && num_requests <= HS_MAX_FP4_MLA_REQUESTS && num_heads >= 1 && num_heads <= 128 && num_queries >= 1 &&
          num_queries <= HS_MAX_SPEC_QUERIES && splits >= 1 && splits <= HS_MAX_MLA_SPLITS;
 }
 

@@ -137,6 +137,7 @@ typedef enum {
 #define HS_MAX_SPEC_QUERIES 8 /* verify steps of one speculative batch (n_spec + 1) */
 #define HS_MAX_MLA_SPLITS 16  /* row splits of hs_sparse_mla_decode and of the hs_fp4_*_mla_decode calls */
 #define HS_FP4_ROW_BYTES 416  /* one token's 4-bit MLA row */
+#define HS_MAX_FP4_MLA_REQUESTS (1 << 20) /* num_requests of the hs_fp4_*_mla_decode calls */
 #define HS_MAX_PAGE_REQUESTS 65536 /* num_requests of an hs_page_pool */
 #define HS_MAX_PAGE_ENTRIES (1 << 20) /* entries of an hs_pages_extend or hs_pages_free call */
 
@@ -549,6 +550,7 @@ HS_API size_t hs_fp4_mla_workspace_bytes(int32_t num_requests, int32_t num_heads
  * [0, pool_rows) (a row named twice counts twice):
  *   s[h, j] = sm_scale * (q[h, :512] . latent_j + q[h, 512:] . rope_j)
  *   o[r, h] = softmax_j(s[h]) . latent,  lse[r, h] = log sum_j exp s[h, j]  (-inf, o = 0 if none)
+ *   num_requests R <= HS_MAX_FP4_MLA_REQUESTS
  *   q [R, num_heads, 576] bf16 bits (num_heads 1..128), kv_pool [pool_rows, 416] with pool_rows <
  *   2^31, o [R, num_heads, 512] bf16 bits: device, 16-byte aligned; out_rows [R, top_k], top_k <=
  *   HS_MAX_TOP_K, lse [R, num_heads] fp32: device
