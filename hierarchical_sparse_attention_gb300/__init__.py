@@ -180,27 +180,33 @@ def _addr(x) -> Optional[int]:
     raise TypeError(f"cannot take the address of {type(x).__name__}")
 
 
+_torch = None  # imported with the first tensor
+_types = {}  # of a letter: the dtypes that the library can read as it (the first is the one that it is mostly given)
+_wants = {}  # of a call's letters: the first dtype of each, None for any
+
+
+def _import_torch():
+    global _torch
+    import torch
+    _types.update({"i": (torch.int32, torch.uint32), "h": (torch.bfloat16, torch.int16, torch.uint16),
+                   "f": (torch.float32,)})
+    _torch = torch
+    return torch
+
+
 def _device_check(on: int) -> int:
     """`on`, the device of an array (-1: none), where it is the current device."""
     if on < 0:
         raise ValueError("this argument is read or written on the GPU: pass a CUDA tensor or a device address")
-    import torch
-    here = torch.cuda.current_device()
+    here = (_torch or _import_torch()).cuda.current_device()
     if on != here:
         raise ValueError(f"the tensor is on cuda:{on}, the current device is cuda:{here}")
     return on
 
 
-_kinds = {}  # dtype -> the letter that the calls below name it by
-
-
 def _type_check(kind: str, dtype) -> None:
     """Elements of the type that the library reads: i 32-bit integers, h bf16 values or their bits, f fp32."""
-    if not _kinds:
-        import torch
-        _kinds.update({torch.int32: "i", torch.uint32: "i", torch.bfloat16: "h", torch.int16: "h", torch.uint16: "h",
-                       torch.float32: "f"})
-    if _kinds.get(dtype) != kind:
+    if dtype not in _types[kind]:
         wanted = {"i": "32-bit integers", "h": "bf16 values or their 16-bit patterns", "f": "32-bit floats"}[kind]
         raise ValueError(f"{wanted} are needed here, not {dtype}")
 
@@ -218,19 +224,26 @@ def _rows_on_gpu(x, stride: int) -> Optional[int]:
     return x.data_ptr()
 
 
-def _on_gpu(kinds: str, *xs):
-    """Addresses of contiguous arrays, which have to be on the current device and of the types in `kinds` (a letter
-    an array, "." any; None and raw addresses are taken as they are). Short, as a call's host time is mostly this."""
-    out, here = [], -1
-    for kind, x in zip(kinds, xs):
+def _on_gpu(kinds: str, *xs, here: int = -1):
+    """Addresses of contiguous arrays, which have to be on the current device (`here`, where that is known) and of the
+    types in `kinds` (a letter an array, "." any; None and raw addresses are taken as they are). Short, as a call's
+    host time is mostly this: 0.4 us an array."""
+    wants = _wants.get(kinds)
+    if wants is None:
+        if all(x is None or isinstance(x, int) for x in xs):
+            return xs  # addresses: torch need not be there
+        _torch or _import_torch()
+        wants = _wants[kinds] = tuple(None if k == "." else _types[k][0] for k in kinds)
+    out = []
+    for want, x in zip(wants, xs):
         if x is not None and not isinstance(x, int):
             on = x.get_device() if hasattr(x, "get_device") else -1
             if on != here or on < 0:
                 here = _device_check(on)
+            if want is not None and x.dtype is not want:
+                _type_check(kinds[len(out)], x.dtype)
             if not x.is_contiguous():
                 raise ValueError("arrays passed to libhs must be contiguous")
-            if kind != "." and _kinds.get(x.dtype) != kind:
-                _type_check(kind, x.dtype)
             x = x.data_ptr()
         out.append(x)
     return out
@@ -449,33 +462,34 @@ def make_page_pool(device_pools: Sequence, num_requests: int, max_pages: int, nu
     return p
 
 
-def _pool_here(pool: Optional[hs_page_pool]) -> Optional[hs_page_pool]:
-    if pool is not None and pool.device is not None:
-        _device_check(pool.device)
-    return pool
+def _pool_here(pool: Optional[hs_page_pool]) -> int:
+    """The pool's device, which has to be the current one; -1 if it has none."""
+    return -1 if pool is None or pool.device is None else _device_check(pool.device)
 
 
 def hs_pages_init(pool: hs_page_pool, stream=None) -> None:
-    _check(_lib.hs_pages_init(_pool_here(pool), _stream(stream)), "hs_pages_init")
+    _pool_here(pool)
+    _check(_lib.hs_pages_init(pool, _stream(stream)), "hs_pages_init")
 
 
 def hs_pages_extend(pool: hs_page_pool, n: int, requests, old_lens, new_lens, granted=None, stream=None) -> None:
-    _check(_lib.hs_pages_extend(_pool_here(pool), n, *_on_gpu("iiii", requests, old_lens, new_lens, granted), _stream(stream)),
-           "hs_pages_extend")
+    arrays = _on_gpu("iiii", requests, old_lens, new_lens, granted, here=_pool_here(pool))
+    _check(_lib.hs_pages_extend(pool, n, *arrays, _stream(stream)), "hs_pages_extend")
 
 
 def hs_pages_fork(pool: hs_page_pool, n: int, parents, children, lens, granted=None, stream=None) -> None:
-    _check(_lib.hs_pages_fork(_pool_here(pool), n, *_on_gpu("iiii", parents, children, lens, granted), _stream(stream)),
-           "hs_pages_fork")
+    arrays = _on_gpu("iiii", parents, children, lens, granted, here=_pool_here(pool))
+    _check(_lib.hs_pages_fork(pool, n, *arrays, _stream(stream)), "hs_pages_fork")
 
 
 def hs_pages_free(pool: hs_page_pool, n: int, requests, first_pages=None, end_pages=None, stream=None) -> None:
-    _check(_lib.hs_pages_free(_pool_here(pool), n, *_on_gpu("iii", requests, first_pages, end_pages), _stream(stream)),
-           "hs_pages_free")
+    arrays = _on_gpu("iii", requests, first_pages, end_pages, here=_pool_here(pool))
+    _check(_lib.hs_pages_free(pool, n, *arrays, _stream(stream)), "hs_pages_free")
 
 
 def hs_pages_compact(pool: hs_page_pool, stream=None) -> None:
-    _check(_lib.hs_pages_compact(_pool_here(pool), _stream(stream)), "hs_pages_compact")
+    _pool_here(pool)
+    _check(_lib.hs_pages_compact(pool, _stream(stream)), "hs_pages_compact")
 
 
 def hs_reset_hints(h: Handle, stream=None) -> None:

@@ -131,3 +131,17 @@ def test_arrays_of_another_type_are_refused(lib, call, good):
             with pytest.raises(ValueError):
                 call(**dict(good, **{name: Array(dtype=other)}))
             assert len(lib.names) == seen or call is entries
+
+
+def test_addresses_need_no_torch():
+    """The calls with raw addresses, in a process where torch cannot be imported."""
+    import subprocess
+    import sys
+    code = ("import sys; sys.modules['torch'] = None\n"
+            "import hierarchical_sparse_attention_gb300 as hs\nA = 1 << 20\n"
+            "hs.hs_fp4_pack_rows(0, A, 576, A, 1.0, A, 100, A)\n"
+            "hs.hs_fp4_sparse_mla_decode(0, 16, 64, 1, A, A, 100, A, 0.1, 1.0, A, A, None, 0, A)\n"
+            "p = hs.make_page_pool([A], 4, 8, 100, 16, 416, A, A, A, A, A, hs.hs_pages_workspace_bytes(4, 100), A)\n"
+            "hs.hs_pages_extend(p, 0, A, A, A)\nhs.hs_pages_fork(p, 0, None, None, None)\nhs.hs_pages_free(p, 0, A)\n")
+    root = hs.__file__.rsplit("/", 2)[0]
+    subprocess.run([sys.executable, "-c", code], cwd=root, check=True, timeout=120)
