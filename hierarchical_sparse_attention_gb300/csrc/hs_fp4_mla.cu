@@ -246,10 +246,9 @@ __device__ __forceinline__ void store8(uint32_t* dst, const uint32_t (&w)[8], bo
     reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
   }
 }
-// What a unit of S is in log2 units (S leaves the scales out, and `up`, what Q was divided by). A scale of zero
-// stays above it, so that -inf stays -inf.
-__device__ __forceinline__ float score_log2(const Fp4MlaArgs& a, float up = 1.f) {
-  return fminf(fmaxf(fabsf(a.sm_scale * a.latent_scale * 1.4426950408889634f) * up, 1e-37f), 3e38f);
+// What a unit of a score without its scales is in log2 units.
+__device__ __forceinline__ float score_log2(const Fp4MlaArgs& a) {
+  return fabsf(a.sm_scale * a.latent_scale * 1.4426950408889634f);
 }
 // The power of two that a head's Q is divided by, given the bf16 bits of its largest latent and RoPE value. 1 where f16
 // holds its latents: none over 65504, and what is lost (2^-25 of values below 2^-14) at most 2^-19 of the largest.
@@ -773,7 +772,8 @@ __global__ void __launch_bounds__(T, 1)
         float* s_ref = reinterpret_cast<float*>(base + S_REF);
         const uint32_t pbuf = remote(base + O_P + wg * P_BUF, partner);  // (block g's buffer is g % NS = wg)
         const uint32_t r_alpha = remote(base + O_ALPHA + 4 * (wg * MH + head), partner), rbar = remote(&bs.p_full[wg], partner);
-        const float sl2 = score_log2(a, up);
+        // what a unit of S is; a scale of zero stays above it, so that -inf stays -inf
+        const float sl2 = fminf(fmaxf(score_log2(a) * up, 1e-37f), 3e38f);
         const uint32_t s_at = tbase + lane_off + S_COL + BJ * wg;
         int b = wg - done % NS;
         if (b < 0) b += NS;
@@ -1006,7 +1006,7 @@ __global__ void __launch_bounds__(T, 1)
           m = fin[(done + nblk - 1) % NS * (FIN_WG / 4) + MH];
           for (int b = 0; b < min(nblk, NS); ++b) {
             const float* of = fin + (done + nblk - 1 - b) % NS * (FIN_WG / 4);
-            l += m == -INFINITY ? of[0] : of[0] * ex2((of[MH] - m) * sl2);
+            l += of[MH] == -INFINITY ? of[0] : of[0] * ex2((of[MH] - m) * sl2);  // (no score: 0, or NaN)
           }
         }
         const float inv = l == 0.f ? 0.f : a.latent_scale / l;  // l is NaN where a weight is

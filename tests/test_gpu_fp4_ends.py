@@ -214,3 +214,33 @@ def test_queries_whose_values_differ_in_size():
             bound = (2 * E[:, None] + 2.0 ** -10) * A + 2.0 ** -32 * np.abs(lat).sum(0) + 2.0 ** -8 * np.abs(want) + 1e-30
             assert (np.abs(o[r] - want) <= bound)[sure].all()
             assert (np.abs(o[r]) <= np.abs(lat).max(0) * (1 + 2.0 ** -7)).all()
+
+
+@pytest.mark.parametrize("k", [0, 60, 100])
+def test_a_scale_of_zero_weighs_rows_alike(k):
+    """Whatever the query's size: o is the rows' mean, off by the weights' 2^-11, sums and the bf16 result; lse = log n."""
+    hs = T._gpu()
+    q, pool, rows = T.case(23, 2, 30, 300, 400, masked=0.0)
+    q = T.bf16_bits(T.bf16_decode(q) * 2.0 ** k)
+    for splits in (1, 2):
+        o, lse, err = T.sparse(hs, q, T.d(pool), T.d(rows), 1.0, splits, 0.0)
+        assert err == 0
+        for r in range(2):
+            lat, _ = F.unpack(pool[rows[r]], 1.0)
+            mean, A = lat.mean(0), np.abs(lat).mean(0)
+            assert (np.abs(o[r] - mean) <= (2.0 ** -11 + 2.0 ** -16) * A + 2.0 ** -8 * np.abs(mean) + 1e-30).all()
+            assert (np.abs(lse[r] - np.log(300)) <= 2.0 ** -20 * 7).all()
+
+
+def test_nan_in_one_warpgroups_blocks_reaches_the_sum():
+    """A row whose score is NaN, alone in its block of 64 and so in one of three partial sums."""
+    hs = T._gpu()
+    q, pool, rows = T.case(29, 1, 20, 192, 300, masked=0.0)
+    pool[7, 256:288] = 0x7F
+    rows[rows == 7] = 8
+    for block in range(3):
+        named = rows.copy()
+        named[0, 64 * block:64 * block + 64] = -1
+        named[0, 64 * block + 5] = 7
+        o, lse, err = T.sparse(hs, q, T.d(pool), T.d(named), 1.0, 1)
+        assert err == 0 and np.isnan(o).all() and np.isnan(lse).all()
