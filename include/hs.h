@@ -565,7 +565,7 @@ HS_API size_t hs_fp4_mla_workspace_bytes(int32_t num_requests, int32_t num_heads
  *   largest (those below 2^-14). A row's weight goes through f16 too: off by up to 2^-11 of itself, and a weight below
  *   2^-21 of the query's largest by up to 2^-32 of the largest (of its split), so that N rows that one
  *   row outweighs so far, as a sink may, are off by up to N 2^-32 of their latents; lse takes weights
- *   as they are. sm_scale x latent_scale x log2(e) has to be finite in fp32. An MMA pipeline that
+ *   as they are. q . row / latent_scale and sm_scale x latent_scale x log2(e) have to be finite in fp32. An MMA pipeline that
  *   stands still for 100 ms sets HS_FLAG_TIMEOUT and ends the call, its outputs not valid.
  * One or two kernel launches (no second one where nothing is split); no allocation, no
  * synchronisation; graph-capturable. num_requests == 0 is a no-op. */

@@ -244,3 +244,53 @@ def test_nan_in_one_warpgroups_blocks_reaches_the_sum():
         named[0, 64 * block + 5] = 7
         o, lse, err = T.sparse(hs, q, T.d(pool), T.d(named), 1.0, 1)
         assert err == 0 and np.isnan(o).all() and np.isnan(lse).all()
+
+
+@pytest.mark.parametrize("splits", [1, 3])
+def test_the_most_requests_of_a_call(splits):
+    """2^20 requests of one head and up to two rows each (every third has one, every third none): o is the row where
+    there is one, to the bf16 rounding, between the rows where there are two."""
+    hs = T._gpu()
+    R = hs.HS_MAX_FP4_MLA_REQUESTS
+    rng = np.random.default_rng(37)
+    rec = F.pack(T.tokens(rng, 500), 1.0)
+    lat = torch.from_numpy(F.unpack(rec, 1.0)[0]).cuda().float()
+    rows = torch.randint(0, 500, (R, 2), dtype=torch.int32, device="cuda")
+    rows[0::3], rows[1::3, 1] = -1, -1
+    q = torch.randn(R, 1, 576, device="cuda").to(torch.bfloat16)
+    wsb = hs.hs_fp4_mla_workspace_bytes(R, 1, 1, splits)
+    ws = torch.empty(max(16, wsb), dtype=torch.uint8, device="cuda")
+    o, lse, err = torch.empty(R, 512, dtype=torch.bfloat16, device="cuda"), torch.empty(R, 1, device="cuda"), T.flags()
+    hs.hs_fp4_sparse_mla_decode(R, 1, 2, splits, q, T.d(rec), 500, rows, T.SM, 1.0, o, lse, ws, wsb, err)
+    assert int(err.item()) == 0
+    assert not o[0::3].any() and torch.isneginf(lse[0::3]).all()
+    one = lat[rows[1::3, 0].long()]
+    assert ((o[1::3].float() - one).abs() <= 2.0 ** -9 * one.abs()).all()
+    a, b = lat[rows[2::3, 0].long()], lat[rows[2::3, 1].long()]
+    slack = 2.0 ** -8 * torch.maximum(a.abs(), b.abs())
+    got = o[2::3].float()
+    assert ((got >= torch.minimum(a, b) - slack) & (got <= torch.maximum(a, b) + slack)).all()
+    assert torch.isfinite(lse[1::3]).all() and torch.isfinite(lse[2::3]).all()
+
+
+def test_the_most_entries_of_a_page_call():
+    """2^20 entries, most of them padding: requests that grow stand far apart, a request is named twice, and a free
+    names the same requests again and again."""
+    hs = T._gpu()
+    import test_gpu_pages as G
+    n = hs.HS_MAX_PAGE_ENTRIES
+    s = G.Pair(hs, 11, 40, 5, 120, 4)
+    rng = np.random.default_rng(4)
+    at = np.sort(rng.choice(n, 12, replace=False))
+    at[-1] = n - 1
+    r, new = np.full(n, -1, np.int32), np.zeros(n, np.int32)
+    r[at], new[at] = [3, 4, 5, 6, 7, 8, 9, 10, 11, 9, 39, 12], [20, 7, 1, 0, 8, 20, 20, 20, 16, 4, 20, 3]
+    got = torch.zeros(n, dtype=torch.int32, device="cuda")
+    hs.hs_pages_extend(s.pool, n, G.d(r), G.d(np.zeros(n)), G.d(new), got)
+    want, flags = s.orc.extend(r[at].tolist(), [0] * 12, new[at].tolist())
+    assert got.cpu().numpy()[at].tolist() == want and int(got.abs().sum()) == np.abs(want).sum()
+    s.same(flags)
+    r = np.full(n, -1, np.int32)
+    r[::7] = rng.choice([3, 5, 39, 2], r[::7].size)
+    hs.hs_pages_free(s.pool, n, G.d(r))
+    s.same(s.orc.release([3, 5, 39, 2]))
