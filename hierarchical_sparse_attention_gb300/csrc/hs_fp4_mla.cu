@@ -95,8 +95,8 @@ constexpr int REC = kFp4RopeAt;                    // bytes of a record that go 
 constexpr uint32_t S_RING = S_ND * RW * REC, O_RING = O_ND * RW * REC;  // a dequantisation warp's ring
 constexpr uint32_t S_TILES = 0;                    // latents of K; Q's are staged over them before the first block
 // RoPE values are copied straight to their tiles: a block's copies start when the tensor core is known to
-// be done with the block five before it. (Of 256 requests then 182 us through the rings like the rest, 176
-// so, 183 with four tiles and so later copies.)
+// be done with the block five before it. (Measured when 256 requests took 176 us so: 182 through the rings
+// like the rest, 183 with four tiles and so later copies.)
 constexpr int NR = 5;
 constexpr uint32_t S_ROPE = NT * TILE;             // (Q's are staged over two of them)
 constexpr uint32_t S_RAW = S_ROPE + NR * KV_ATOM;

@@ -9,8 +9,8 @@
 // scale NaN (0x7F) and zero codes, so that it reads back as NaN. RoPE values are copied.
 //
 // What bounds them: memory. Measured for 32,768 tokens written and 65,536 read back, one after the
-// other: 29.7 us, 155 MB, 0.77 of a copy's bandwidth (launches and the first loads' latency are a
-// fifth of so short a pass). On the way: 37.8 us with a division per code and the loads after the
+// other: 30.8 us, 155 MB, 0.74 of a copy's bandwidth (launches and the first loads' latency are a
+// fifth of so short a pass). On the way, when that was 29.7: 37.8 us with a division per code and the loads after the
 // row's number; two or four tokens of a warp at a time 29.1 and 33.3 us (and 1 and 2.5 us more for
 // 32 tokens).
 #include "hs_fp4.h"

@@ -470,8 +470,8 @@ __global__ void __launch_bounds__(kPlanThreads) pages_compact_plan_kernel(const 
   }
 }
 
-// Bytes of a page that are copied at a time, and the spans of a CTA's ring, two CTAs to an SM: 77 us for a
-// step that moves 379 MB (read and written) of 26-KB pages; spans of 16 KB and rings of 6 79 us, of 8
+// Bytes of a page that are copied at a time, and the spans of a CTA's ring, two CTAs to an SM: 78 to 80 us for a
+// step that moves 379 MB (read and written) of 26-KB pages. Beside 77: spans of 16 KB and rings of 6 79 us, of 8
 // and 12 83, one CTA with a ring of 12 to an SM 83, 256 threads that load and store 64 bytes each in
 // turn 96.
 constexpr int kSpan = 32768;

@@ -567,6 +567,7 @@ HS_API size_t hs_fp4_mla_workspace_bytes(int32_t num_requests, int32_t num_heads
  *   row outweighs so far, as a sink may, are off by up to N 2^-32 of their latents; lse takes weights
  *   as they are. q . row / latent_scale and sm_scale x latent_scale x log2(e) have to be finite in fp32. An MMA pipeline that
  *   stands still for 100 ms sets HS_FLAG_TIMEOUT and ends the call, its outputs not valid.
+ * Its time goes by requests and rows: one head takes a tile of up to 128 as long as 128 of them do.
  * One or two kernel launches (no second one where nothing is split); no allocation, no
  * synchronisation; graph-capturable. num_requests == 0 is a no-op. */
 HS_API hs_status hs_fp4_sparse_mla_decode(int32_t num_requests, int32_t num_heads, int32_t top_k, int32_t splits,
@@ -613,7 +614,9 @@ HS_API hs_status hs_fp4_window_mla_decode(int32_t num_requests, int32_t num_head
  * of these calls leaves (a page held but not counted, a stack entry out of range, ...) sets
  * HS_FLAG_STATE where it is met; nothing outside the buffers is read or written. All calls: at
  * most two kernel launches, no allocation, no synchronisation, graph-capturable; the same state
- * and arguments give the same result. row_bytes is any (656, 416, ...). */
+ * and arguments give the same result. row_bytes is any (656, 416, ...). More than HS_MAX_LAYERS layers
+ * are several groups, each with a descriptor, a table, counts and a stack of its own (a call changes its
+ * table as it copies, so that two descriptors cannot share one): the same calls keep them equal. */
 typedef struct {
   int32_t num_requests; /* 1..HS_MAX_PAGE_REQUESTS */
   int32_t max_pages;
