@@ -252,9 +252,9 @@ __device__ __forceinline__ float score_log2(const Fp4MlaArgs& a) {
 }
 // The power of two that a head's Q is divided by, given the bf16 bits of its largest latent and RoPE value. 1 where f16
 // holds its latents: none over 65504, and what is lost (2^-25 of values below 2^-14) at most 2^-19 of the largest.
-// Otherwise the largest becomes 2^15 .. 65280. RoPE values are divided too, in bf16: it is kept so large that none
-// overflows, over latent_scale >= 2^-32, unless they are 2^60 times the largest latent, whose part in a score is
-// lost then anyway.
+// Otherwise the largest becomes 2^15 .. 65280. RoPE values are divided too, in bf16, and over latent_scale >= 2^-32: so
+// that none of them overflows, the divisor is at least 2^-75 of the largest one, which takes room from latents
+// only where RoPE values are more than 2^60 times as large, and at least 2^-95.
 __device__ __forceinline__ float q_divisor(uint32_t top, uint32_t rope) {
   if (top == 0 || (top >= 0x3C80u && top < 0x4780u)) return 1.f;  // 2^-6, 2^16
   return __uint_as_float((uint32_t)max(max((int)(top >> 7) - 15, (int)(rope >> 7) - 75), 127 - 95) << 23);
