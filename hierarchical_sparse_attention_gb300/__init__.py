@@ -6,7 +6,8 @@ kernels. Arguments that are device arrays accept a torch CUDA tensor (its
 ``data_ptr()``) or a raw address; host pools accept a numpy array or a raw address;
 ``stream`` accepts a ``torch.cuda.Stream``, a raw ``cudaStream_t`` or None (the legacy
 default stream). A non-OK status raises :class:`HsError` carrying the status code. The 4-bit
-cache's calls (``hs_fp4_*``, ``hs_pages_*``) also refuse, with ValueError, a tensor that is not on
+cache's calls and the batches' (``hs_fp4_*``, ``hs_pages_*``, ``hs_batch_plan``, ``hs_fp8_*``,
+``hs_chunk_mla``) also refuse, with ValueError, a tensor that is not on
 the current CUDA device, a page pool whose tensors are not, and a tensor whose elements are of another
 type than the call's (bf16 arrays may be given as their 16-bit patterns).
 
@@ -28,6 +29,7 @@ HS_FLAG_TOKEN, HS_FLAG_DUP, HS_FLAG_STATE, HS_FLAG_HOSTROW, HS_FLAG_DEVROW, HS_F
 HS_FLAG_ORDER = 64
 HS_FLAG_TIMEOUT = 128
 HS_FLAG_NOPAGE = 256
+HS_FLAG_FULL = 512
 HS_MAX_MLA_SPLITS = 16
 HS_MAX_TOP_K, HS_MAX_HOT_SLOTS, HS_MAX_LAYERS = 4096, 16384, 8
 
@@ -40,13 +42,17 @@ EXPORTS = ("hs_workspace_bytes", "hs_create", "hs_resolve", "hs_backup", "hs_get
            "hs_host_numa_node", "hs_host_bind_node", "hs_sparse_mla_launches",
            "hs_fp4_pack_rows", "hs_fp4_unpack_rows", "hs_fp4_mla_splits", "hs_fp4_mla_workspace_bytes",
            "hs_fp4_sparse_mla_decode", "hs_fp4_window_mla_decode", "hs_pages_workspace_bytes", "hs_pages_init",
-           "hs_pages_extend", "hs_pages_fork", "hs_pages_free", "hs_pages_compact")
+           "hs_pages_extend", "hs_pages_fork", "hs_pages_free", "hs_pages_compact", "hs_batch_plan",
+           "hs_fp8_pack_rows", "hs_fp8_unpack_rows", "hs_chunk_mla_workspace_bytes", "hs_chunk_mla")
 HS_MAX_SPEC_QUERIES = 8
 HS_NOALLOC_MAX_LAYERS = 8
 HS_FP4_ROW_BYTES = 416
 HS_MAX_FP4_MLA_REQUESTS = 1 << 20
 HS_MAX_PAGE_REQUESTS = 65536
 HS_MAX_PAGE_ENTRIES = 1 << 20
+HS_FP8_ROW_BYTES = 656
+HS_MAX_BATCH_ENTRIES = 65536
+HS_MAX_BATCH_TOKENS = 1 << 20
 
 
 class hs_config(ctypes.Structure):
@@ -143,7 +149,14 @@ def _load() -> ctypes.CDLL:
     lib.hs_pages_fork.argtypes = [poolp, i32, P, P, P, P, P]
     lib.hs_pages_free.argtypes = [poolp, i32, P, P, P, P]
     lib.hs_pages_compact.argtypes = [poolp, P]
-    for name in ("hs_fp4_pack_rows", "hs_fp4_unpack_rows", "hs_fp4_sparse_mla_decode", "hs_fp4_window_mla_decode",
+    lib.hs_batch_plan.argtypes = [i32, P, P, P, i32, P, i32, i32, i64, i32] + [P] * 5 + [i32, P, P, P]
+    lib.hs_fp8_pack_rows.argtypes = [i32, P, i64, P, P, f32, P, P, i32, P, i64, P, P]
+    lib.hs_fp8_unpack_rows.argtypes = [i32, P, i64, P, P, i64, P, P]
+    lib.hs_chunk_mla_workspace_bytes.argtypes = [i32, i32, i32, i64]
+    lib.hs_chunk_mla_workspace_bytes.restype = sz
+    lib.hs_chunk_mla.argtypes = [i32, i32, i32, P, P, P, P, i64, i32, i32, P, f32, P, P, i64, P, sz, P, P]
+    for name in ("hs_batch_plan", "hs_fp8_pack_rows", "hs_fp8_unpack_rows", "hs_chunk_mla",
+                 "hs_fp4_pack_rows", "hs_fp4_unpack_rows", "hs_fp4_sparse_mla_decode", "hs_fp4_window_mla_decode",
                  "hs_pages_init", "hs_pages_extend", "hs_pages_fork", "hs_pages_free", "hs_pages_compact"):
         getattr(lib, name).restype = ctypes.c_int
     return lib
@@ -490,6 +503,51 @@ def hs_pages_free(pool: hs_page_pool, n: int, requests, first_pages=None, end_pa
 def hs_pages_compact(pool: hs_page_pool, stream=None) -> None:
     _pool_here(pool)
     _check(_lib.hs_pages_compact(pool, _stream(stream)), "hs_pages_compact")
+
+
+def hs_batch_plan(n: int, requests, old_lens, new_lens, num_requests: int, resident_pages, max_pages: int,
+                  page_size: int, pool_rows: int, max_tokens: int, token_offsets, seq_lens, entries, positions, rows,
+                  max_blocks: int, block_tables, error_flags, stream=None) -> None:
+    """A step's flat tokens, their positions and pool rows, and the entries' block tables."""
+    (requests, old_lens, new_lens, resident_pages, token_offsets, seq_lens, entries, positions, rows, block_tables,
+     error_flags) = _on_gpu("iiiiiiiiiii", requests, old_lens, new_lens, resident_pages, token_offsets, seq_lens, entries,
+                            positions, rows, block_tables, error_flags)
+    _check(_lib.hs_batch_plan(n, requests, old_lens, new_lens, num_requests, resident_pages, max_pages, page_size,
+                              pool_rows, max_tokens, token_offsets, seq_lens, entries, positions, rows, max_blocks,
+                              block_tables, error_flags, _stream(stream)), "hs_batch_plan")
+
+
+def hs_fp8_pack_rows(n: int, kv, kv_stride: int, rows, norm_weight, norm_eps: float, positions, rope_table,
+                     rope_positions: int, pool, pool_rows: int, error_flags, stream=None) -> None:
+    """Normalise, rotate and quantise n tokens (bf16 [n, kv_stride], 576 used) into the fp8 rows `rows` of the pool."""
+    kv = _rows_on_gpu(kv, kv_stride)
+    rows, norm_weight, positions, rope_table, pool, error_flags = _on_gpu("ihif.i", rows, norm_weight, positions,
+                                                                          rope_table, pool, error_flags)
+    _check(_lib.hs_fp8_pack_rows(n, kv, kv_stride, rows, norm_weight, norm_eps, positions, rope_table, rope_positions,
+                                 pool, pool_rows, error_flags, _stream(stream)), "hs_fp8_pack_rows")
+
+
+def hs_fp8_unpack_rows(n: int, pool, pool_rows: int, rows, kv, kv_stride: int, error_flags, stream=None) -> None:
+    """Read the fp8 rows `rows` back as bf16 into kv ([n, kv_stride], 576 written)."""
+    kv = _rows_on_gpu(kv, kv_stride)
+    pool, rows, error_flags = _on_gpu(".ii", pool, rows, error_flags)
+    _check(_lib.hs_fp8_unpack_rows(n, pool, pool_rows, rows, kv, kv_stride, error_flags, _stream(stream)),
+           "hs_fp8_unpack_rows")
+
+
+def hs_chunk_mla_workspace_bytes(n: int, num_heads: int, max_tokens: int, max_kv_tokens: int) -> int:
+    return int(_lib.hs_chunk_mla_workspace_bytes(n, num_heads, max_tokens, max_kv_tokens))
+
+
+def hs_chunk_mla(n: int, num_heads: int, max_tokens: int, token_offsets, seq_lens, q, kv_pool, pool_rows: int,
+                 page_size: int, max_blocks: int, block_tables, sm_scale: float, o, lse, max_kv_tokens: int, workspace,
+                 workspace_bytes: int, error_flags, stream=None) -> None:
+    """Causal attention of the batch's new tokens over the pages of their sequences."""
+    token_offsets, seq_lens, q, kv_pool, block_tables, o, lse, workspace, error_flags = _on_gpu(
+        "iih.ihf.i", token_offsets, seq_lens, q, kv_pool, block_tables, o, lse, workspace, error_flags)
+    _check(_lib.hs_chunk_mla(n, num_heads, max_tokens, token_offsets, seq_lens, q, kv_pool, pool_rows, page_size,
+                             max_blocks, block_tables, sm_scale, o, lse, max_kv_tokens, workspace, workspace_bytes,
+                             error_flags, _stream(stream)), "hs_chunk_mla")
 
 
 def hs_reset_hints(h: Handle, stream=None) -> None:

@@ -18,8 +18,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build", "hs")
 LIB = os.path.join(PKG, "libhs.so")
 SOURCES = ["hs_resolve.cu", "hs_backup.cu", "hs_gather.cu", "hs_invalidate.cu", "hs_sparse_mla.cu", "hs_fp4_rows.cu",
-           "hs_fp4_mla.cu", "hs_pages.cu", "hs_api.cu", "hs_noalloc.cu"]
-HEADERS = ["hs_internal.h", "hs_fp4.h", "hs_tcgen05.cuh"]
+           "hs_fp4_mla.cu", "hs_pages.cu", "hs_batch.cu", "hs_fp8_rows.cu", "hs_chunk_mla.cu", "hs_api.cu", "hs_noalloc.cu"]
+HEADERS = ["hs_internal.h", "hs_fp4.h", "hs_chunk.h", "hs_tcgen05.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden",
               "-I", INCLUDE, "-I", CSRC]

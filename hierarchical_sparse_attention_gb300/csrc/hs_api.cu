@@ -10,6 +10,7 @@
 #include <cstdlib>
 #include <cstring>
 
+#include "hs_chunk.h"
 #include "hs_fp4.h"
 #include "hs_internal.h"
 
@@ -152,6 +153,18 @@ namespace {
 bool latent_scale_ok(float g) {
   int e;
   return std::isfinite(g) && g >= 0x1p-32f && g <= 0x1p32f && std::frexp(g, &e) == 0.5f;
+}
+
+bool fp8_rows_ok(int32_t n, const uint16_t* kv, int64_t kv_stride, const int32_t* rows, const uint8_t* pool,
+                 int64_t pool_rows, const uint32_t* error_flags) {
+  if (n < 0 || kv_stride < hs::kFp8Dims || kv_stride % 8 || pool_rows < 1) return false;
+  if (n == 0) return true;
+  return kv && rows && pool && error_flags && aligned(kv, 16) && aligned(pool, 16);
+}
+
+bool chunk_shape_ok(int32_t n, int32_t num_heads, int32_t max_tokens, int64_t max_kv_tokens) {
+  return n >= 0 && n <= HS_MAX_BATCH_ENTRIES && num_heads >= 1 && num_heads <= 128 && max_tokens >= 0 &&
+         max_tokens <= HS_MAX_BATCH_TOKENS && max_kv_tokens >= 0 && max_kv_tokens % 64 == 0 && max_kv_tokens <= INT32_MAX;
 }
 
 bool fp4_rows_ok(int32_t n, const uint16_t* kv, int64_t kv_stride, const int32_t* rows, float latent_scale,
@@ -751,6 +764,76 @@ hs_status hs_pages_compact(const hs_page_pool* pool, hs_stream_t stream) {
   hs::PageArgs a;
   if (!page_args(pool, &a)) return HS_ERR_INVALID_ARG;
   return hs::launch_pages_compact(a, (cudaStream_t)stream) == cudaSuccess ? HS_OK : HS_ERR_CUDA;
+}
+
+hs_status hs_batch_plan(int32_t n, const int32_t* requests, const int32_t* old_lens, const int32_t* new_lens,
+                        int32_t num_requests, const int32_t* resident_pages, int32_t max_pages, int32_t page_size,
+                        int64_t pool_rows, int32_t max_tokens, int32_t* token_offsets, int32_t* seq_lens,
+                        int32_t* entries, int32_t* positions, int32_t* rows, int32_t max_blocks, int32_t* block_tables,
+                        uint32_t* error_flags, hs_stream_t stream) {
+  if (n < 0 || n > HS_MAX_BATCH_ENTRIES || num_requests < 1 || num_requests > HS_MAX_PAGE_REQUESTS || max_pages < 1 ||
+      page_size < 1 || (int64_t)max_pages * page_size > INT32_MAX || pool_rows < 1 || pool_rows > INT32_MAX ||
+      max_tokens < 0 || max_tokens > HS_MAX_BATCH_TOKENS || (block_tables && max_blocks < 1))
+    return HS_ERR_INVALID_ARG;
+  if (!token_offsets || !error_flags) return HS_ERR_INVALID_ARG;
+  if (n > 0 && (!requests || !old_lens || !new_lens || !resident_pages)) return HS_ERR_INVALID_ARG;
+  const hs::BatchArgs a{n,        num_requests, max_pages,      page_size,     max_tokens, max_blocks, pool_rows, requests,
+                        old_lens, new_lens,     resident_pages, token_offsets, seq_lens,   entries,    positions, rows,
+                        block_tables};
+  return hs::launch_batch_plan(a, error_flags, (cudaStream_t)stream) == cudaSuccess ? HS_OK : HS_ERR_CUDA;
+}
+
+hs_status hs_fp8_pack_rows(int32_t n, const uint16_t* kv, int64_t kv_stride, const int32_t* rows,
+                           const uint16_t* norm_weight, float norm_eps, const int32_t* positions,
+                           const float* rope_table, int32_t rope_positions, uint8_t* pool, int64_t pool_rows,
+                           uint32_t* error_flags, hs_stream_t stream) {
+  if (!fp8_rows_ok(n, kv, kv_stride, rows, pool, pool_rows, error_flags)) return HS_ERR_INVALID_ARG;
+  if (norm_weight && (!aligned(norm_weight, 16) || !(norm_eps >= 0.f) || std::isinf(norm_eps))) return HS_ERR_INVALID_ARG;
+  if ((rope_table != nullptr) != (positions != nullptr) || (rope_table && rope_positions < 1)) return HS_ERR_INVALID_ARG;
+  if (n == 0) return HS_OK;
+  const hs::Fp8RowsArgs a{n,           const_cast<uint16_t*>(kv), kv_stride, rows,       pool,
+                          pool_rows,   norm_weight,               norm_eps,  positions, rope_table,
+                          rope_positions};
+  return hs::launch_fp8_pack(a, error_flags, (cudaStream_t)stream) == cudaSuccess ? HS_OK : HS_ERR_CUDA;
+}
+
+hs_status hs_fp8_unpack_rows(int32_t n, const uint8_t* pool, int64_t pool_rows, const int32_t* rows, uint16_t* kv,
+                             int64_t kv_stride, uint32_t* error_flags, hs_stream_t stream) {
+  if (!fp8_rows_ok(n, kv, kv_stride, rows, pool, pool_rows, error_flags)) return HS_ERR_INVALID_ARG;
+  if (n == 0) return HS_OK;
+  hs::Fp8RowsArgs a = {};
+  a.n = n;
+  a.kv = kv;
+  a.kv_stride = kv_stride;
+  a.rows = rows;
+  a.pool = const_cast<uint8_t*>(pool);
+  a.pool_rows = pool_rows;
+  return hs::launch_fp8_unpack(a, error_flags, (cudaStream_t)stream) == cudaSuccess ? HS_OK : HS_ERR_CUDA;
+}
+
+size_t hs_chunk_mla_workspace_bytes(int32_t n, int32_t num_heads, int32_t max_tokens, int64_t max_kv_tokens) {
+  if (!chunk_shape_ok(n, num_heads, max_tokens, max_kv_tokens) || n == 0 || max_tokens == 0) return 0;
+  return hs::chunk_workspace_bytes(n, num_heads, max_tokens, max_kv_tokens);
+}
+
+hs_status hs_chunk_mla(int32_t n, int32_t num_heads, int32_t max_tokens, const int32_t* token_offsets,
+                       const int32_t* seq_lens, const uint16_t* q, const uint8_t* kv_pool, int64_t pool_rows,
+                       int32_t page_size, int32_t max_blocks, const int32_t* block_tables, float sm_scale, uint16_t* o,
+                       float* lse, int64_t max_kv_tokens, void* workspace, size_t workspace_bytes,
+                       uint32_t* error_flags, hs_stream_t stream) {
+  if (!chunk_shape_ok(n, num_heads, max_tokens, max_kv_tokens) || page_size < 1 || max_blocks < 1 ||
+      (int64_t)max_blocks * page_size > INT32_MAX || pool_rows < 1 || pool_rows > INT32_MAX || !std::isfinite(sm_scale) ||
+      !std::isfinite(sm_scale * 1.4426950408889634f))
+    return HS_ERR_INVALID_ARG;
+  if (n == 0 || max_tokens == 0) return HS_OK;
+  if (!token_offsets || !seq_lens || !q || !kv_pool || !block_tables || !o || !lse || !workspace || !error_flags)
+    return HS_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(kv_pool, 16) || !aligned(o, 16) || !aligned(workspace, 256)) return HS_ERR_INVALID_ARG;
+  if (workspace_bytes < hs::chunk_workspace_bytes(n, num_heads, max_tokens, max_kv_tokens)) return HS_ERR_INVALID_ARG;
+  const hs::ChunkArgs a{n,         num_heads, max_tokens, token_offsets, seq_lens,     q, kv_pool,
+                        pool_rows, page_size, max_blocks, block_tables,  sm_scale,     o, lse,
+                        max_kv_tokens};
+  return hs::launch_chunk_mla(a, workspace, error_flags, (cudaStream_t)stream) == cudaSuccess ? HS_OK : HS_ERR_CUDA;
 }
 
 }  // extern "C"

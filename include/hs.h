@@ -129,6 +129,7 @@ typedef enum {
 #define HS_FLAG_TIMEOUT 128u /* a bounded device wait ran out: that call's outputs are invalid */
 
 #define HS_FLAG_NOPAGE 256u  /* hs_pages_extend / hs_pages_fork: too few free pages for an entry */
+#define HS_FLAG_FULL 512u    /* hs_batch_plan / hs_chunk_mla: an entry does not fit max_tokens / max_kv_tokens */
 
 /* Limits of this build. */
 #define HS_MAX_TOP_K 4096
@@ -140,6 +141,9 @@ typedef enum {
 #define HS_MAX_FP4_MLA_REQUESTS (1 << 20) /* num_requests of the hs_fp4_*_mla_decode calls */
 #define HS_MAX_PAGE_REQUESTS 65536 /* num_requests of an hs_page_pool */
 #define HS_MAX_PAGE_ENTRIES (1 << 20) /* entries of an hs_pages_extend or hs_pages_free call */
+#define HS_FP8_ROW_BYTES 656  /* one token's fp8 MLA row */
+#define HS_MAX_BATCH_ENTRIES 65536 /* entries of hs_batch_plan and hs_chunk_mla */
+#define HS_MAX_BATCH_TOKENS (1 << 20) /* max_tokens of hs_batch_plan and hs_chunk_mla */
 
 /* Configuration of one layer group (layers that share one indexer top-k and therefore
  * one slot map; "vLLM Hybrid HiSparse source implementation analysis" 7.4).
@@ -692,6 +696,92 @@ HS_API hs_status hs_pages_free(const hs_page_pool* pool, int32_t n, const int32_
  * pages num_pages - 1 .. V, V on top: afterwards pages V .. num_pages - 1 are the caller's to use
  * otherwise. Tables of rows made before (out_rows) are stale. Two kernel launches. */
 HS_API hs_status hs_pages_compact(const hs_page_pool* pool, hs_stream_t stream);
+
+/* ---- Steps with several new tokens of a sequence: the batch, its fp8 rows, attention of the chunks ----
+ *
+ * A step's batch has n entries, each a request and the tokens that are new to it: one (a decode step), a few
+ * (the verify steps of a speculative batch), or a chunk of a prompt. The entries' new tokens stand one after the
+ * other, entry by entry, as the step's flat tokens. In stream order: hs_pages_extend gives the new tokens their
+ * pages, hs_batch_plan says where each stands, hs_fp8_pack_rows writes every layer's rows, hs_chunk_mla attends. */
+
+/* The batch of a step, from the requests' lengths and the page table. Entry i is request requests[i] with
+ * old_lens[i] tokens before the step and new_lens[i] with the new ones, as in hs_pages_extend.
+ *   token_offsets [n + 1]   entry i's flat tokens are token_offsets[i] .. token_offsets[i + 1] - 1
+ *   seq_lens      [n]       new_lens[i]; 0 for padding and for refused entries
+ *   entries, positions, rows [max_tokens]   of each flat token: its entry, its position in the sequence, and its
+ *                           pool row resident_pages[request][position / page_size] * page_size + position % page_size
+ *                           (-1 with HS_FLAG_DEVROW where the page is negative or the row past pool_rows);
+ *                           -1 behind the last token
+ *   block_tables  [n, max_blocks]   the pages of entry i's seq_lens[i] tokens as the page table has them, then -1
+ * entries, positions, rows, seq_lens and block_tables may each be NULL. A negative request is padding: no tokens. An entry
+ * gets its tokens, all of them, if they and those of the entries before it are at most max_tokens (and then those of
+ * no later entry that has any are), else none, with HS_FLAG_FULL. Refused too: a request out of range
+ * (HS_FLAG_TOKEN), one named twice (every one of them, HS_FLAG_DUP), lengths that are negative, fall, or pass
+ * max_pages or (where block_tables is given) max_blocks pages (HS_FLAG_SEQLEN).
+ *   requests, old_lens, new_lens [n], resident_pages [num_requests, max_pages]: device, read; n <=
+ *   HS_MAX_BATCH_ENTRIES, num_requests <= HS_MAX_PAGE_REQUESTS, max_tokens <= HS_MAX_BATCH_TOKENS, pool_rows < 2^31
+ * Whole numbers, the same for the same arguments. One kernel launch; no allocation, no synchronisation;
+ * graph-capturable. n == 0 writes token_offsets[0] and the rows behind the last token. */
+HS_API hs_status hs_batch_plan(int32_t n, const int32_t* requests, const int32_t* old_lens, const int32_t* new_lens,
+                               int32_t num_requests, const int32_t* resident_pages, int32_t max_pages,
+                               int32_t page_size, int64_t pool_rows, int32_t max_tokens, int32_t* token_offsets,
+                               int32_t* seq_lens, int32_t* entries, int32_t* positions, int32_t* rows,
+                               int32_t max_blocks, int32_t* block_tables, uint32_t* error_flags, hs_stream_t stream);
+
+/* Write n tokens' fp8 rows ("vLLM Hybrid HiSparse source implementation analysis", 9: 512 e4m3 latent codes, 4 fp32
+ * scales, one per 128 codes, 64 bf16 RoPE values): token i, kv + i * kv_stride (576 bf16 values: latent, then RoPE),
+ * goes to pool row rows[i].
+ *   norm_weight: y = x w / sqrt(mean of x^2 over the 512 + norm_eps) (norm_weight [512] bf16 bits, 16-byte
+ *     aligned); NULL: y = x.
+ *   scale: per 128 dims the least power of two, at least 2^-126, with max |y| / scale <= 448; code = y / scale,
+ *     rounded to the nearest e4m3 value, halfway to the even code. Both as exact arithmetic has it (y to 2^-44). A
+ *     block with a NaN or an infinity (with a norm: a token with one) reads back as NaN.
+ *   rope_table [rope_positions, 64] fp32: 32 cosines, then 32 sines. Values 2i and 2i + 1, a and b, of a token at
+ *     position p = positions[i] become a cos - b sin and a sin + b cos of entry i of the table's row p, rounded once
+ *     to bf16; NULL (with positions NULL): copied. A position outside the table skips the token (HS_FLAG_SEQLEN).
+ * rows[i] < 0 skips the token; rows[i] >= pool_rows skips it and sets HS_FLAG_DEVROW. Rows named once each (two tokens
+ * for one row in one call: not checked, that row's bytes are then unspecified).
+ *   kv [n, kv_stride] bf16 bits, device, 16-byte aligned, kv_stride >= 576 and a multiple of 8
+ *   rows [n], positions [n] int32, pool [pool_rows, 656] 16-byte aligned, rope_table 4-byte aligned: device
+ * One kernel launch; no allocation, no synchronisation; graph-capturable. n == 0 is a no-op. */
+HS_API hs_status hs_fp8_pack_rows(int32_t n, const uint16_t* kv, int64_t kv_stride, const int32_t* rows,
+                                  const uint16_t* norm_weight, float norm_eps, const int32_t* positions,
+                                  const float* rope_table, int32_t rope_positions, uint8_t* pool, int64_t pool_rows,
+                                  uint32_t* error_flags, hs_stream_t stream);
+
+/* Read n rows back: kv + i * kv_stride gets row rows[i]'s 576 values, code x scale rounded to bf16 (exact where the
+ * scale is a power of two, within bf16's range), zeros where rows[i] is negative, and zeros with HS_FLAG_DEVROW where
+ * it is >= pool_rows. Any row any number of times. Layouts, alignment and launch rules as in hs_fp8_pack_rows. */
+HS_API hs_status hs_fp8_unpack_rows(int32_t n, const uint8_t* pool, int64_t pool_rows, const int32_t* rows,
+                                    uint16_t* kv, int64_t kv_stride, uint32_t* error_flags, hs_stream_t stream);
+
+/* Attention of the batch's new tokens over their sequences' pages, causal: entry i's queries are the flat tokens
+ * token_offsets[i] .. token_offsets[i + 1] - 1, the last ones of its seq_lens[i] tokens, whose rows are in the pool
+ * (new tokens' rows too: hs_fp8_pack_rows comes before). The query at position p sees the tokens t <= p of its
+ * sequence; for each of num_heads (1..128) heads h
+ *   s[h, t] = sm_scale * (q[h, :512] . latent_t + q[h, 512:] . rope_t),  latent = e4m3 x scale
+ *   o[h] = softmax_t(s[h]) . latent,  lse[h] = log sum_t exp s[h, t]  (-inf, o = 0 if it sees nothing)
+ * Token t's row is block_tables[i][t / page_size] * page_size + t % page_size; tokens whose page is negative or whose
+ * row is past the pool are left out, with HS_FLAG_DEVROW. An entry with more queries than seq_lens[i] has first
+ * queries at negative positions, which see nothing. seq_lens[i] outside [0, max_blocks * page_size] makes its queries
+ * see nothing (HS_FLAG_SEQLEN); token_offsets that are negative, fall or pass max_tokens leave the entry out
+ * (HS_FLAG_SEQLEN). Flat tokens behind the last entry's keep what o and lse held.
+ *   q [max_tokens, num_heads, 576] bf16 bits, o [max_tokens, num_heads, 512] bf16 bits, kv_pool [pool_rows, 656] with
+ *   pool_rows < 2^31: device, 16-byte aligned; lse [max_tokens, num_heads] fp32; token_offsets [n + 1], seq_lens [n],
+ *   block_tables [n, max_blocks]: device; n <= HS_MAX_BATCH_ENTRIES, max_tokens <= HS_MAX_BATCH_TOKENS
+ *   max_kv_tokens: room for the sequences of a call, each rounded up to 64 tokens, that is at least the sum of
+ *   (seq_lens[i] + 63) / 64 * 64 over the entries with queries. An entry that does not fit, after those before it,
+ *   sees nothing, like every later one that has tokens (HS_FLAG_FULL). A multiple of 64.
+ *   workspace: hs_chunk_mla_workspace_bytes(n, num_heads, max_tokens, max_kv_tokens) device bytes, 256-byte aligned,
+ *   contents of no matter; calls that share it must be ordered. error_flags: device uint32, HS_FLAG_* bits OR-ed in.
+ * No allocation, no synchronisation; graph-capturable: lengths are read on the device, so that a captured call serves
+ * every batch that its sizes hold. n == 0 or max_tokens == 0 is a no-op. */
+HS_API size_t hs_chunk_mla_workspace_bytes(int32_t n, int32_t num_heads, int32_t max_tokens, int64_t max_kv_tokens);
+HS_API hs_status hs_chunk_mla(int32_t n, int32_t num_heads, int32_t max_tokens, const int32_t* token_offsets,
+                              const int32_t* seq_lens, const uint16_t* q, const uint8_t* kv_pool, int64_t pool_rows,
+                              int32_t page_size, int32_t max_blocks, const int32_t* block_tables, float sm_scale,
+                              uint16_t* o, float* lse, int64_t max_kv_tokens, void* workspace, size_t workspace_bytes,
+                              uint32_t* error_flags, hs_stream_t stream);
 
 #ifdef __cplusplus
 }
