@@ -1,47 +1,150 @@
-// Attention of a step's new tokens over the fp8 pages of their sequences, causal.
+// Attention of a step's new tokens over the fp8 pages of their sequences, causal, on the 5th-generation tensor cores
+// (tcgen05, accumulators in tensor memory).
 //
 // Per query head of the token at position p, over the tokens t <= p of its sequence:
 //   s_t = sm_scale (q[:512] . latent_t + q[512:] . rope_t),  o = softmax(s) . latent,  lse = log sum_t exp s_t
 //
-// A first kernel lists the entries with queries; the second has a warp per query head, which goes over its sequence in
-// blocks of 32 rows (values in 32 bits in shared memory) with the running maximum and sum of a softmax.
+// Four kernels:
+//   - chunk_list: the entries with queries, where each sequence's rows go in the workspace, and the work dealt out evenly;
+//   - chunk_rows: every sequence's rows once, from their pages, as f16 in blocks of 64 rows laid out as the tensor cores
+//     read them, so that the attention brings a block in with one bulk copy and no arithmetic;
+//   - chunk_mla: tiles of 128 query heads (all heads of as many tokens of an entry as fit) over their blocks;
+//   - chunk_merge: joins the parts of tiles that were cut.
+//
+// chunk_mla. The work of a call is one line: the entries' tiles, one after the other, each as long as its blocks. It is cut
+// into as many equal pieces as there are pairs of CTAs, so that every pair ends at the same time whatever the lengths are;
+// a piece's first and last tile may be parts, whose results (in 32 bits) chunk_merge joins. A pair, on two SMs, because Q
+// (288 columns), S and O (512) do not fit one tensor memory, nor K, V, Q and P one shared memory, takes a tile's blocks of
+// 64 rows in turn:
+//   - the S-CTA (even rank) holds Q in tensor memory and computes S = Q . K^T of each block into one of three buffers; its
+//     three softmax warpgroups (a block each in turn, a query head per thread) run the online softmax and write P as f16
+//     into the O-CTA's shared memory;
+//   - the O-CTA holds O (128 x 512 in 32 bits, all of its tensor memory) and adds P . V; its corrector rescales O in the
+//     rare blocks that raise a head's reference maximum.
+// The roles hand blocks over through mbarriers with bounded waits, and run on from tile to tile: Q comes through the ring of
+// K's slots (a slot holds a block of 64 rows of 576 values, or half of Q), V through a ring of half blocks.
+//
+// Precision. Latents (e4m3 x scale) and RoPE values go through f16: exact where the scale is a power of two, else off by 2^-11
+// of themselves, and by 2^-25 where they are below 2^-14. Q goes through f16 over a power of two of its head, which
+// goes into its scores' scale: off by 2^-40 of the head's largest. P, whose reference weighs 2^7, is rounded to f16: by up to
+// 2^-11 of a weight, and by 2^-32 of the largest weight where it is below 2^-21 of that; its sum takes weights
+// unrounded, so lse does not see it. Scores, maxima, sums and O are in 32 bits.
+//
+// NaN, infinities and values that f16 does not hold. A row that a query does not see gets P = 0, and 0 x NaN must not reach O:
+// such values are zeros in the blocks, and a mark for their row makes its score NaN for the queries that see it, and so
+// their outputs, and only theirs.
 #include "hs_chunk.h"
+#include "hs_tcgen05.cuh"
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include <atomic>
+
 namespace hs {
+
+using namespace tc;
+
 namespace {
 
-constexpr int MH = 128;  // query heads of a tile: all heads of as many tokens of an entry as fit
+constexpr int T = 448;   // threads per CTA: 14 warps
+constexpr int MH = 128;  // MMA M: query heads of a tile (what is there of the next tokens fills it up)
+constexpr int BJ = 64;   // rows per block
 constexpr int DQK = kFp8Dims, DL = kFp8Latent;
+constexpr int QATOMS = DQK / 64, ATOMS = DL / 64;  // swizzle atoms of 64 values in a block of K and of V
+constexpr int NS = 3;    // S buffers, softmax warpgroups and P buffers: a block each in turn
+constexpr int NK = 3, NV = 5;  // slots of the S-CTA's ring (a block, or half of Q) and of the O-CTA's (half of V's block)
+constexpr uint32_t TMEM_COLS = 512, Q_COL = 0, S_COL = 288;
+static_assert(S_COL + NS * BJ <= TMEM_COLS, "Q and the S buffers fit tensor memory");
+// S-CTA warps: 0-11 softmax; O-CTA: 0-3 corrector, which reads out with 4-11; both: 12 issuer, 13 copies.
+constexpr int ISSUER = 12, COPIER = 13, NOUT = 3;  // NOUT warps read out a quarter of the heads
+
+constexpr uint32_t ATOM = BJ * 128, BLOCK = QATOMS * ATOM, HALF_V = ATOMS / 2 * ATOM;
+constexpr uint32_t S_RING = 0;
+constexpr uint32_t S_REF = NK * BLOCK;             // the reference maxima, handed from block to block
+constexpr uint32_t S_QTOP = S_REF + MH * 4;        // a head's largest value in each third of Q
+constexpr uint32_t S_END = S_QTOP + NS * MH * 2;
+constexpr uint32_t O_RING = 0;
+constexpr uint32_t O_P = NV * HALF_V;
+constexpr uint32_t P_BUF = MH * BJ * 2, P_BYTES = P_BUF + MH * 4;  // P and the rescale factors of a block
+constexpr uint32_t FIN_WG = 2 * MH * 4;            // a softmax warpgroup's sums and references of a tile
+constexpr uint32_t O_ALPHA = O_P + NS * P_BUF;
+constexpr int NF = NS + 1;  // tiles whose totals are kept: P's buffers let the S-CTA be three tiles ahead, of one block each
+constexpr uint32_t FIN = NS * FIN_WG + MH * 4;     // of a tile: the warpgroups', and what a unit of a score is
+constexpr uint32_t O_FIN = O_ALPHA + NS * MH * 4;
+constexpr uint32_t O_END = O_FIN + NF * FIN;
+constexpr uint32_t SMEM_BYTES = S_END > O_END ? S_END : O_END;
+constexpr uint32_t STATIC_BYTES = 1024;  // barriers and flags, one block of a tile's alignment
+static_assert(STATIC_BYTES + SMEM_BYTES <= 227 * 1024, "shared memory of a CTA");
+static_assert(BLOCK % 1024 == 0 && HALF_V % 1024 == 0 && O_P % 1024 == 0, "the swizzle's alignment");
+// P of a score that equals its reference is 2^7, and a reference stays until it is passed by 2^8.9, so that
+// P < 2^15.91 = 61,500 in f16, which then keeps a weight to 2^-11 of itself down to 2^-21 of the reference's.
+constexpr float kRefLog2 = 7.f, kRescaleLog2 = 8.9f;
+constexpr uint32_t kIdescQK = idesc(BJ, MH, false);
+constexpr uint32_t kIdescPV = idesc(256, MH, true);
+
+// How the work is dealt out, in blocks: what a tile takes besides its blocks, and the least part of a tile.
+constexpr int kTileCost = 4, kLeastPart = 4;
+constexpr int kPairs = 76;  // of CTAs, at most
 constexpr int kListThreads = 512;
+static_assert(kPairs < kListThreads, "a thread per pair");
 
 // An entry with queries.
-struct Entry {
+struct __align__(16) Entry {
   int32_t q0, nq, seq;  // first flat token, queries, tokens (0: they see nothing)
   int32_t table;        // its number: the block table's row
-  int32_t tile0;        // tiles of the entries before it
+  int64_t cost;         // of the entries before it, in tokens (64 to a block)
+  int32_t block;        // its first block of rows in the workspace
+  int32_t none;
+};
+static_assert(sizeof(Entry) == 32, "two loads");
+struct Pos {
+  int32_t ent, tile, blk, none;
 };
 struct Work {
-  int32_t* count;  // entries listed
-  int32_t* tiles;
-  Entry* entries;  // [n]
+  int32_t* count;   // entries listed
+  int32_t* blocks;  // blocks of their sequences
+  Pos* starts;      // [kPairs + 1] where a pair's work begins
+  Entry* entries;   // [n]
+  uint4* state;     // [blocks] two words of rows that exist, two of rows with a value that f16 does not hold
+  uint8_t* kv;      // [blocks] x BLOCK bytes
+  float* part_lse;  // [2 kPairs, MH] of a pair's first tile, where that began before, and of one that goes on after it
+  float* part_o;    // [2 kPairs, MH, DL]
 };
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
-size_t work_of(Work* w, void* workspace, int32_t n) {
-  uint8_t* at = static_cast<uint8_t*>(workspace);
-  w->count = reinterpret_cast<int32_t*>(at);
-  w->tiles = w->count + 1;
-  w->entries = reinterpret_cast<Entry*>(at + 256);
-  return 256 + up256((size_t)n * sizeof(Entry));
+size_t work_of(Work* w, void* workspace, int32_t n, int64_t max_kv_tokens) {
+  size_t at = 0;
+  const auto take = [&](size_t bytes) {
+    uint8_t* r = workspace == nullptr ? nullptr : static_cast<uint8_t*>(workspace) + at;
+    at += up256(bytes);
+    return r;
+  };
+  const size_t blocks = (size_t)(max_kv_tokens / BJ);
+  w->count = reinterpret_cast<int32_t*>(take(8));
+  w->blocks = w->count + 1;
+  w->starts = reinterpret_cast<Pos*>(take((kPairs + 1) * sizeof(Pos)));
+  w->entries = reinterpret_cast<Entry*>(take((size_t)n * sizeof(Entry)));
+  w->state = reinterpret_cast<uint4*>(take(blocks * sizeof(uint4)));
+  w->kv = take(blocks * BLOCK);
+  w->part_lse = reinterpret_cast<float*>(take((size_t)2 * kPairs * MH * 4));
+  w->part_o = reinterpret_cast<float*>(take((size_t)2 * kPairs * MH * DL * 4));
+  return at;
 }
 
-__global__ void __launch_bounds__(kListThreads) chunk_list_kernel(const ChunkArgs a, const Work w, uint32_t* __restrict__ err) {
+// ---------------------------------------------------------------- the list
+
+// What tiles 0 .. t - 1 of an entry cost, in tokens: tile i reads the `before` tokens before the entry's queries and
+// (i + 1) per_tile of these (a little more than it does where the last tile is not full, or before is negative).
+__device__ __forceinline__ int64_t cost_of(int64_t before, int per_tile, int64_t t) {
+  return (max(before, (int64_t)0) + kTileCost * BJ) * t + per_tile * (t * (t + 1) / 2);
+}
+__device__ __forceinline__ int blocks_of(int64_t tokens) { return tokens > 0 ? (int)((tokens + BJ - 1) / BJ) : 0; }
+
+__global__ void __launch_bounds__(kListThreads) chunk_list_kernel(const ChunkArgs a, const Work w, int pairs, uint32_t* __restrict__ err) {
   pdl_wait();
   const int tid = threadIdx.x, per_tile = MH / a.num_heads;
-  int64_t blocks = 0, listed = 0, tiles = 0;
+  int64_t blocks = 0, listed = 0, cost = 0;
   uint32_t flags = 0;
   for (int base = 0; base < a.n; base += kListThreads) {
     const int i = base + tid;
@@ -57,130 +160,870 @@ __global__ void __launch_bounds__(kListThreads) chunk_list_kernel(const ChunkArg
         seq = 0;
       }
     }
-    const int64_t need = nq > 0 ? (seq + 63) / 64 : 0;
+    const int64_t need = nq > 0 ? blocks_of(seq) : 0;
     int64_t sum;
     const int64_t before = blocks + cta_prefix<kListThreads>(need, &sum);
     blocks += sum;
-    if (need > 0 && (before + need) * 64 > a.max_kv_tokens) {
+    if (need > 0 && (before + need) * BJ > a.max_kv_tokens) {
       flags |= HS_FLAG_FULL;
       seq = 0;
     }
     const int64_t slot = listed + cta_prefix<kListThreads>(nq > 0, &sum);
     listed += sum;
-    const int64_t tile0 = tiles + cta_prefix<kListThreads>((nq + per_tile - 1) / per_tile, &sum);
-    tiles += sum;
-    if (nq > 0) w.entries[slot] = {q0, nq, seq, i, (int32_t)tile0};
+    const int64_t mine = nq > 0 ? cost_of((int64_t)seq - nq, per_tile, (nq + per_tile - 1) / per_tile) : 0;
+    const int64_t cost0 = cost + cta_prefix<kListThreads>(mine, &sum);
+    cost += sum;
+    // (entries that fit are those before some entry: the sums over all that asked are theirs)
+    if (nq > 0) w.entries[slot] = {q0, nq, seq, i, cost0, (int32_t)min(before, a.max_kv_tokens / BJ), 0};
   }
   if (flags) atomicOr(err, flags);
   if (tid == 0) {
     *w.count = (int32_t)listed;
-    *w.tiles = (int32_t)tiles;
+    *w.blocks = (int32_t)min(blocks, a.max_kv_tokens / BJ);
   }
-}
-
-constexpr int kWarps = 8, BJ = 32, KS = DQK + 1;
-constexpr size_t kSmem = (size_t)(BJ * KS + kWarps * DQK + BJ) * 4;
-
-__global__ void __launch_bounds__(kWarps * 32) chunk_plain_kernel(const ChunkArgs a, const Work w, uint32_t* __restrict__ err) {
-  extern __shared__ float smem[];
-  float* k = smem;                                         // [BJ][KS]
-  float* qs = smem + BJ * KS;                              // [kWarps][DQK]
-  int* there = reinterpret_cast<int*>(qs + kWarps * DQK);  // [BJ]
-  pdl_wait();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, per_tile = MH / a.num_heads;
-  const int count = *w.count, groups = MH / kWarps;
-  for (int64_t u = blockIdx.x; u < (int64_t)*w.tiles * groups; u += gridDim.x) {
-    const int tile = (int)(u / groups);
-    int lo = 0, hi = count - 1;
+  __syncthreads();  // (the entries, which any thread reads now)
+  if (tid > pairs) return;
+  Pos at = {(int32_t)listed, 0, 0, 0};
+  if (tid < pairs && listed > 0) {
+    const int64_t x = cost / pairs * tid + cost % pairs * tid / pairs;
+    int lo = 0, hi = (int)listed - 1;  // the last entry that begins at or before x
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (w.entries[mid].tile0 <= tile) lo = mid;
+      if (w.entries[mid].cost <= x) lo = mid;
       else hi = mid - 1;
     }
     const Entry e = w.entries[lo];
-    const int first = (tile - e.tile0) * per_tile, tokens = min(per_tile, e.nq - first);
-    const int m = (int)(u % groups) * kWarps + warp;
-    const bool live = m < tokens * a.num_heads;
-    const int64_t row = ((int64_t)e.q0 + first) * a.num_heads + m;
-    const int64_t end = (int64_t)e.seq - e.nq + first + tokens;  // past the last position that some query of the tile sees
-    const int64_t mine = (int64_t)e.seq - e.nq + first + m / a.num_heads + 1;
-    __syncthreads();
-    if (live)
-      for (int d = lane; d < DQK; d += 32) qs[warp * DQK + d] = __uint_as_float((uint32_t)a.q[row * DQK + d] << 16);
-    float top = -INFINITY, sum = 0.f, o[DL / 32] = {};
-    for (int64_t j0 = 0; j0 < end; j0 += BJ) {
+    const int tiles = (e.nq + per_tile - 1) / per_tile;
+    const int64_t before = (int64_t)e.seq - e.nq, y = x - e.cost;
+    // the last tile that begins at or before y: the root of the cost, a quadratic, put right by what rounding took
+    const double b = (double)(max(before, (int64_t)0) + kTileCost * BJ) + 0.5 * per_tile;
+    int64_t t = (int64_t)(2.0 * (double)y / (b + sqrt(b * b + 2.0 * per_tile * (double)y)));
+    t = min(max(t, (int64_t)0), (int64_t)tiles - 1);
+    while (t > 0 && cost_of(before, per_tile, t) > y) --t;
+    while (t < tiles - 1 && cost_of(before, per_tile, t + 1) <= y) ++t;
+    const int all = blocks_of(before + min((t + 1) * per_tile, (int64_t)e.nq));
+    int64_t blk = max((y - cost_of(before, per_tile, t)) / BJ - kTileCost, (int64_t)0);
+    if (blk < kLeastPart) blk = 0;
+    if (blk > 0 && all - blk < kLeastPart) blk = 0, ++t;
+    if (tid == 0) t = blk = 0;
+    at.ent = lo;
+    at.tile = (int)t;
+    at.blk = (int)blk;
+    if (t == tiles) at = {lo + 1, 0, 0, 0};
+  }
+  w.starts[tid] = at;
+}
+
+// ---------------------------------------------------------------- the rows
+
+constexpr int kRowsThreads = 384;
+
+// Two values to an f16 pair; those that it does not hold become zeros and set `bad`.
+__device__ __forceinline__ uint32_t to_f16(float2 v, bool& bad) {
+  const __half2 h = __floats2half2_rn(v.x, v.y);
+  uint32_t x = *reinterpret_cast<const uint32_t*>(&h);
+  const bool lo = (x & 0x7C00u) == 0x7C00u, hi = (x & 0x7C000000u) == 0x7C000000u;
+  if (lo) x &= 0xFFFF0000u;
+  if (hi) x &= 0x0000FFFFu;
+  bad |= lo || hi;
+  return x;
+}
+
+// A CTA per block at a time. A thread has 32 values of a row, a warp eight rows of 128 (or 16 of 32) at a time, placed so
+// that eight lanes' stores meet every bank once. Within 32 values, chunk j of four takes pair j of each, the order of
+// columns that the read-out of O wants (and Q's values have); the place of chunk c of row x of a line's eight is c ^ x.
+__global__ void __launch_bounds__(kRowsThreads) chunk_rows_kernel(const ChunkArgs a, const Work w, uint32_t* __restrict__ err) {
+  extern __shared__ __align__(1024) uint8_t image[];
+  __shared__ int s_entry;
+  __shared__ int32_t s_row[BJ];
+  __shared__ uint32_t s_there[2], s_bad[2];
+  pdl_wait();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int count = *w.count, total = *w.blocks;
+  for (int b = blockIdx.x; b < total; b += gridDim.x) {
+    // the last entry whose first block is at or before b
+    int lo = 0;
+    for (int n = count; n > 1;) {
+      const int step = (n + kRowsThreads - 1) / kRowsThreads, i = lo + tid * step;
+      if (i < lo + n && w.entries[i].block <= b && (i + step >= lo + n || w.entries[i + step].block > b)) s_entry = i;
       __syncthreads();
-      for (int j = warp; j < BJ; j += kWarps) {
-        const int64_t t = j0 + j;
-        int64_t r = -1;
-        if (t < end) {
-          const int32_t page = a.block_tables[(int64_t)e.table * a.max_blocks + t / a.page_size];
-          r = (int64_t)page * a.page_size + t % a.page_size;
-          if (page < 0 || r >= a.pool_rows) {
-            r = -1;
-            if (lane == 0) atomicOr(err, HS_FLAG_DEVROW);
-          }
-        }
-        if (lane == 0) there[j] = r >= 0;
-        const uint8_t* src = a.pool + max(r, (int64_t)0) * kFp8Row;
-        for (int d = lane; d < DQK; d += 32) {
-          float v = 0.f;
-          if (r < 0) {
-          } else if (d < DL) {
-            v = __half2float(__half(__nv_cvt_fp8_to_halfraw(src[d], __NV_E4M3))) *
-                reinterpret_cast<const float*>(src + kFp8Scales)[d / kFp8Block];
-          } else {
-            v = __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(src + kFp8RopeAt)[d - DL] << 16);
-          }
-          k[j * KS + d] = v;
-        }
+      n = min(step, lo + n - s_entry);
+      lo = s_entry;
+      __syncthreads();
+    }
+    const Entry e = w.entries[lo];
+    if (tid < BJ) {
+      const int64_t t = (int64_t)(b - e.block) * BJ + tid;
+      int32_t row = -1;
+      if (t < e.seq) {
+        const int32_t p = (int32_t)t / a.page_size, page = a.block_tables[(int64_t)e.table * a.max_blocks + p];
+        const int64_t r = (int64_t)page * a.page_size + ((int32_t)t - p * a.page_size);
+        if (page >= 0 && r < a.pool_rows) row = (int32_t)r;
+        else atomicOr(err, HS_FLAG_DEVROW);
       }
-      __syncthreads();
-      if (live) {
-        float s = 0.f;
-        for (int d = 0; d < DQK; ++d) s += qs[warp * DQK + d] * k[lane * KS + d];
-        const bool sees = j0 + lane < mine && there[lane];
-        s = sees ? s * a.sm_scale : -INFINITY;
-        float bm = s;
-        for (int d = 16; d > 0; d >>= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, d));
-        const float m_new = fmaxf(top, bm), ref = m_new == -INFINITY ? 0.f : m_new;
-        const float keep = expf(top - ref), p = expf(s - ref);
-        float z = p;
-        for (int d = 16; d > 0; d >>= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
-        top = m_new;
-        sum = sum * keep + z;
-        for (int i = 0; i < DL / 32; ++i) o[i] *= keep;
-        for (int j = 0; j < BJ; ++j) {
-          const float pj = __shfl_sync(0xffffffffu, p, j);
-          if (pj == 0.f) continue;  // (a row that is not seen may hold a NaN)
-          for (int i = 0; i < DL / 32; ++i) o[i] += pj * k[j * KS + 32 * i + lane];
-        }
+      s_row[tid] = row;
+      const uint32_t there = __ballot_sync(0xffffffffu, row >= 0);
+      if (lane == 0) {
+        s_there[warp] = there;
+        s_bad[warp] = 0;
       }
     }
-    if (live) {
-      for (int i = 0; i < DL / 32; ++i) {
-        const __nv_bfloat16 h = __float2bfloat16(sum == 0.f ? 0.f : o[i] / sum);
-        a.o[row * DL + 32 * i + lane] = *reinterpret_cast<const uint16_t*>(&h);
+    if (tid == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the last block has left
+    __syncthreads();
+    const auto put = [&](int row, int g, int j, uint32_t x0, uint32_t x1, uint32_t x2, uint32_t x3) {
+      *reinterpret_cast<uint4*>(image + (g >> 1) * ATOM + (row >> 3) * 1024 + (row & 7) * 128 + ((((g & 1) * 4 + j) ^ (row & 7)) << 4)) =
+          make_uint4(x0, x1, x2, x3);
+    };
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      const int task = warp + k * (kRowsThreads / 32);
+      bool bad = false;
+      int row;
+      if (task < 32) {  // latents: rows 8 (task / 4) .., 128 values of scale task % 4
+        row = 8 * (task >> 2) + (lane & 7);
+        const int g = 4 * (task & 3) + (lane >> 3);
+        const int32_t r = s_row[row];
+        uint32_t c[8] = {};
+        float s = 0.f;
+        if (r >= 0) {
+          const uint8_t* src = a.pool + (int64_t)r * kFp8Row;
+          *reinterpret_cast<uint4*>(c) = __ldg(reinterpret_cast<const uint4*>(src + 32 * g));
+          *reinterpret_cast<uint4*>(c + 4) = __ldg(reinterpret_cast<const uint4*>(src + 32 * g) + 1);
+          s = __ldg(reinterpret_cast<const float*>(src + kFp8Scales) + (task & 3));
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint32_t x[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c[2 * u + (j >> 1)] >> (16 * (j & 1))), __NV_E4M3);
+            const float2 v = __half22float2(__half2(h));
+            x[u] = to_f16(make_float2(v.x * s, v.y * s), bad);
+          }
+          put(row, g, j, x[0], x[1], x[2], x[3]);
+        }
+      } else {  // RoPE: 16 rows, 64 values
+        row = 16 * (task - 32) + 8 * (lane >> 4) + (lane & 7);
+        const int g = 16 + ((lane >> 3) & 1);
+        const int32_t r = s_row[row];
+        uint32_t c[16] = {};
+        if (r >= 0) {
+          const uint4* src = reinterpret_cast<const uint4*>(a.pool + (int64_t)r * kFp8Row + kFp8RopeAt + 64 * (g - 16));
+#pragma unroll
+          for (int u = 0; u < 4; ++u) *reinterpret_cast<uint4*>(c + 4 * u) = __ldg(src + u);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint32_t x[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            x[u] = to_f16(make_float2(__uint_as_float(c[4 * u + j] << 16), __uint_as_float(c[4 * u + j] & 0xFFFF0000u)), bad);
+          put(row, g, j, x[0], x[1], x[2], x[3]);
+        }
       }
-      if (lane == 0) a.lse[row] = sum == 0.f ? -INFINITY : top + logf(sum);
+      if (bad) atomicOr(&s_bad[row >> 5], 1u << (row & 31));
+    }
+    fence_async_smem();
+    __syncthreads();
+    if (tid == 0) {
+      w.state[b] = make_uint4(s_there[0], s_there[1], s_bad[0], s_bad[1]);
+      asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n\tcp.async.bulk.commit_group;" ::"l"(
+                       w.kv + (size_t)b * BLOCK),
+                   "r"(smem_u32(image)), "r"(BLOCK)
+                   : "memory");
     }
   }
+  if (tid == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+static_assert(kRowsThreads / 32 * 3 == 32 + BJ / 16, "three tasks a warp");
+
+// ---------------------------------------------------------------- the attention
+
+struct Barriers {
+  uint64_t full[NV], free[NV];     // a ring slot's bytes are there; it has been read
+  uint64_t q_top, q_full, q_done;  // S-CTA: Q's largest values are known; Q in tensor memory; the tile's last S is done
+  // per softmax warpgroup, so that whoever waits on one waits on every phase of it (parities repeat):
+  uint64_t s_full[NS], s_free[NS]; // S-CTA: S written; S read
+  uint64_t m_set[NS][4];           // S-CTA: the block's reference maxima of a warp's heads are set
+  uint64_t p_free[NS];             // S-CTA, arrived by the O-CTA: P . V of the block is done
+  uint64_t p_full[NS];             // O-CTA, completed by the S-CTA's stores
+  uint64_t pv_go[NS], pv_done[NS]; // O-CTA: O is ready for P . V of the block; it is done
+  uint64_t fin[NF];                // O-CTA: the S-CTA's totals of a tile are here
+  uint64_t o_full, o_free;         // O-CTA: a tile's last P . V is done; O has been read out
+};
+static_assert(NK <= NV, "the rings' barriers");
+
+struct __align__(STATIC_BYTES) Control {
+  Barriers bs;
+  uint32_t taddr;
+  int abort;
+  int issued;     // blocks whose MMAs the issuer started (the last commit to wait for)
+  int requested;  // ring slots whose copies were started
+};
+static_assert(sizeof(Control) == STATIC_BYTES, "one block");
+
+// A tile, or a part of one: what a pair does next. Every role computes it by itself.
+struct Unit {
+  int nblk;        // its blocks
+  int first, kv;   // the first one's number in its sequence, and in the workspace
+  int live;        // query heads of the tile
+  size_t row0;     // the first one's row of q, o and lse
+  int64_t seen;    // tokens that the tile's first query sees
+  bool whole;
+};
+struct Walk {
+  Pos at, end;
+  Entry e;
+  int held;  // the entry that e is
+};
+__device__ __forceinline__ bool next_unit(const ChunkArgs& a, const Work& w, int per_tile, Walk& k, Unit& u) {
+  if (k.at.ent == k.end.ent && k.at.tile == k.end.tile && k.at.blk == k.end.blk) return false;
+  if (k.held != k.at.ent) {
+    k.e = w.entries[k.at.ent];
+    k.held = k.at.ent;
+  }
+  const int first = k.at.tile * per_tile, tokens = min(per_tile, k.e.nq - first);
+  u.seen = (int64_t)k.e.seq - k.e.nq + first + 1;
+  const int all = blocks_of(u.seen + tokens - 1);
+  const bool cut = k.at.ent == k.end.ent && k.at.tile == k.end.tile;
+  u.first = k.at.blk;
+  u.nblk = (cut ? k.end.blk : all) - u.first;
+  u.kv = k.e.block + u.first;
+  u.live = tokens * a.num_heads;
+  u.row0 = ((size_t)k.e.q0 + first) * a.num_heads;
+  u.whole = u.first == 0 && !cut;
+  if (cut) {
+    k.at = k.end;
+  } else {
+    k.at.blk = 0;
+    if (first + tokens >= k.e.nq) {
+      ++k.at.ent;
+      k.at.tile = 0;
+    } else {
+      ++k.at.tile;
+    }
+  }
+  return true;
+}
+
+// What a unit of q . row is in log2 units.
+__device__ __forceinline__ float score_log2(const ChunkArgs& a) { return fabsf(a.sm_scale * 1.4426950408889634f); }
+
+__global__ void __launch_bounds__(T, 1)
+    chunk_mla_kernel(const ChunkArgs a, const Work w, const __grid_constant__ CUtensorMap tm_q, uint32_t* __restrict__ err) {
+  // (what is static fills a block of the tiles' alignment, and the rest begins after it)
+  extern __shared__ __align__(STATIC_BYTES) uint8_t base[];
+  __shared__ __align__(STATIC_BYTES) Control ctl;
+  Barriers& bs = ctl.bs;
+  if ((smem_u32(base) & (STATIC_BYTES - 1)) != 0) {  // (never: the tiles' swizzle wants it)
+    if (threadIdx.x == 0) atomicOr(err, HS_FLAG_TIMEOUT);
+    return;
+  }
+  volatile int* abort = &ctl.abort;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = blockIdx.x & 1u, partner = rank ^ 1u;  // 0: S-CTA, 1: O-CTA
+  const int pair = blockIdx.x >> 1;
+
+  if (tid == 0) {
+    for (int k = 0; k < NV; ++k) {
+      bar_init(&bs.full[k], 1);
+      bar_init(&bs.free[k], 1);
+    }
+    bar_init(&bs.q_top, 4 * NS);  // one arrival per softmax warp
+    bar_init(&bs.q_full, 4 * NS);
+    bar_init(&bs.q_done, 1);
+    for (int k = 0; k < NS; ++k) {
+      bar_init(&bs.s_full[k], 1);
+      bar_init(&bs.s_free[k], 4);  // the warps of the block's softmax warpgroup
+      for (int x = 0; x < 4; ++x) bar_init(&bs.m_set[k][x], 1);
+      bar_init(&bs.p_free[k], 1);
+      bar_init(&bs.p_full[k], 1);  // the O-CTA's expect_tx; the S-CTA's stores complete it
+      bar_init(&bs.pv_go[k], 4);
+      bar_init(&bs.pv_done[k], 1);
+    }
+    for (int k = 0; k < NF; ++k) bar_init(&bs.fin[k], 1);  // the same
+    bar_init(&bs.o_full, 1);
+    bar_init(&bs.o_free, 4 * NOUT);
+    ctl.abort = 0;
+    ctl.issued = 0;
+    ctl.requested = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    if (rank == 1)
+      for (int k = 0; k < NS; ++k) bar_arrive_tx(&bs.p_full[k], P_BYTES);
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&ctl.taddr)),
+                 "r"(TMEM_COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_before();
+  __syncthreads();
+  tc_after();
+  // both CTAs' barriers are initialised before either arrives on the other's
+  asm volatile("barrier.cluster.arrive.relaxed;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+  pdl_wait();
+  const uint32_t tbase = ctl.taddr;
+  const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+  const int head = (warp & 3) * 32 + lane;  // this thread's row of the tile = its tensor-memory lane
+  const int per_tile = MH / a.num_heads, token = head / a.num_heads;
+  Walk walk;
+  walk.at = w.starts[pair];
+  walk.end = w.starts[pair + 1];
+  walk.held = -1;
+
+  // The units of this pair, one after the other. Each role goes through them by itself: what the roles
+  // hand each other carries on from unit to unit.
+  bool ok = true;
+  int done = 0, full = 0;  // blocks, and units with blocks, before this one
+  Unit un;
+#pragma unroll 1
+  for (; next_unit(a, w, per_tile, walk, un); done += un.nblk, full += un.nblk > 0) {
+    const int nblk = un.nblk;
+    const int use0 = done + 2 * full;  // the S-CTA's ring: Q's two slots, then a slot per block
+    if (rank == 0) {
+      // ================================ S-CTA ================================
+      if (nblk == 0) continue;
+      if (warp < 4 * NS) {
+        const int wg = warp >> 2;
+        // Q into tensor memory (warpgroup wg the columns [96 wg, 96 wg + 96)), column c holding the values of
+        // places 2c, 2c + 1 of a row, over a power of two that brings the head's largest to 2^14 .. 2^15.
+        ok = full == 0 || ready_or_wait(&bs.q_done, 1, full - 1, abort);
+        const int use = use0 + (head >> 6);
+        ok = ok && ready_or_wait(bs.full, NK, use, abort);
+        ok = __all_sync(0xffffffffu, ok);
+        tc_after();
+        const uint8_t* src = base + S_RING + (use % NK) * BLOCK + (head & 63) * 128;
+        uint32_t top = 0;
+        if (!ok) break;
+#pragma unroll 1
+        for (int bx = 3 * wg; bx < 3 * wg + 3; ++bx)
+#pragma unroll
+          for (int c = 0; c < 8; ++c) top = max_bf16x2(top, *reinterpret_cast<const uint4*>(src + bx * ATOM + ((c ^ (head & 7)) << 4)));
+        uint16_t* tops = reinterpret_cast<uint16_t*>(base + S_QTOP) + head;
+        tops[MH * wg] = (uint16_t)max(top & 0xFFFFu, top >> 16);
+        __syncwarp();
+        if (lane == 0) bar_arrive(&bs.q_top);
+        ok = __all_sync(0xffffffffu, ready_or_wait(&bs.q_top, 1, full, abort));
+        if (!ok) break;
+        top = max(max((uint32_t)tops[0], (uint32_t)tops[MH]), (uint32_t)tops[2 * MH]);
+        const int down = top == 0 ? 127 : min(127 + 14 + 127 - (int)(top >> 7), 253);  // biased
+        const float mul = __uint_as_float((uint32_t)down << 23), up = __uint_as_float((uint32_t)(254 - down) << 23);
+        const uint32_t sign = a.sm_scale < 0.f ? 0x80008000u : 0u;  // so that scores scale by a positive factor
+#pragma unroll 1
+        for (int h = 6 * wg; h < 6 * wg + 6; ++h) {  // 32 values: 16 columns
+          uint32_t x[16], y[16];
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            *reinterpret_cast<uint4*>(x + 4 * u) =
+                *reinterpret_cast<const uint4*>(src + (h >> 1) * ATOM + ((((h & 1) * 4 + u) ^ (head & 7)) << 4));
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const uint32_t v = x[4 * u + j];
+              const __half2 f = __floats2half2_rn(__uint_as_float(v << 16) * mul, __uint_as_float(v & 0xFFFF0000u) * mul);
+              y[4 * j + u] = *reinterpret_cast<const uint32_t*>(&f) ^ sign;
+            }
+          asm volatile(
+              "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+                  tbase + lane_off + Q_COL + 16 * h),
+              "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]), "r"(y[4]), "r"(y[5]), "r"(y[6]), "r"(y[7]), "r"(y[8]), "r"(y[9]),
+              "r"(y[10]), "r"(y[11]), "r"(y[12]), "r"(y[13]), "r"(y[14]), "r"(y[15])
+              : "memory");
+        }
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        tc_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(&bs.q_full);
+        // Warpgroup wg takes the blocks whose number g = done + b has g % NS = wg, a query head per
+        // thread. From one block to the next only the reference maximum goes over, from warp to warp
+        // (the warps of the same heads): it is known once a block's scores have been read, so the
+        // warpgroups' exponentials overlap. Each keeps the sum of its own blocks under the reference of
+        // its last one. The scores are read twice, for the maximum and for the weights. References are
+        // scores as S holds them, and a weight's exponent is the difference, scaled: a score times the scale
+        // is rounded by whole units from 2^24 on.
+        float m_own = -INFINITY, l_own = 0.f;  // the sum of this thread's blocks, under this reference
+        float* s_ref = reinterpret_cast<float*>(base + S_REF);
+        const uint32_t pbuf = remote(base + O_P + wg * P_BUF, partner);  // (block g's buffer is g % NS = wg)
+        const uint32_t r_alpha = remote(base + O_ALPHA + 4 * (wg * MH + head), partner), rbar = remote(&bs.p_full[wg], partner);
+        // what a unit of S is; a scale of zero stays above it, so that -inf stays -inf
+        const float sl2 = fminf(fmaxf(score_log2(a) * up, 1e-37f), 3e38f);
+        const uint32_t s_at = tbase + lane_off + S_COL + BJ * wg;
+        const int64_t sees_to = un.seen + token - (int64_t)un.first * BJ;  // rows of the unit that this query sees
+        int b = wg - done % NS;
+        if (b < 0) b += NS;
+        const bool mine = b < nblk, last = (done + nblk - 1) % NS == wg;
+        uint32_t turn = (uint32_t)((done + b) / NS) & 1u;  // of this warpgroup: its barriers' phase
+        uint4 state = {};
+        if (mine) state = __ldcg(w.state + un.kv + b);
+#pragma unroll 1
+        for (; ok && b < nblk; b += NS, turn ^= 1u) {
+          const int g = done + b;
+          const int64_t left = sees_to - (int64_t)b * BJ;
+          const int to = (int)min(max(left, (int64_t)0), (int64_t)BJ);
+          const uint32_t sees0 = state.x & bit_range(0, to), sees1 = state.y & bit_range(0, to - 32);
+          const uint32_t nan0 = state.z, nan1 = state.w;
+          if (b + NS < nblk) state = __ldcg(w.state + un.kv + b + NS);
+          ok = __all_sync(0xffffffffu, ready_or_wait(&bs.s_full[wg], 1, (int)turn, abort));
+          if (!ok) break;
+          tc_after();
+          const bool every = __all_sync(0xffffffffu, (sees0 & sees1) == 0xFFFFFFFFu && (nan0 | nan1) == 0u);
+          const auto scores = [&](int c, float (&t)[32]) {  // 32 c .. 32 c + 31 of the block, -inf where it does not look
+            tmem_ld32(s_at + 32 * c, t);
+            if (!every) {
+              const uint32_t sees = c ? sees1 : sees0, nan = c ? nan1 : nan0;
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                t[i] = ((sees >> i) & 1u) ? (((nan >> i) & 1u) ? __uint_as_float(0x7FC00000u) : t[i]) : -INFINITY;
+            }
+          };
+          float bm = -INFINITY;
+#pragma unroll 1
+          for (int c = 0; c < BJ / 32; ++c) {
+            float t[32];
+            scores(c, t);
+            float x0 = t[0], x1 = t[1];
+#pragma unroll
+            for (int i = 2; i < 32; i += 2) {
+              x0 = fmaxf(x0, t[i]);
+              x1 = fmaxf(x1, t[i + 1]);
+            }
+            bm = fmaxf(bm, fmaxf(x0, x1));
+          }
+          float m_run = -INFINITY;
+          if (g > 0) {
+            // (the block before is the last warpgroup's block of this turn, or of the turn before)
+            const int before = wg == 0 ? NS - 1 : wg - 1;
+            ok = __all_sync(0xffffffffu, ready_or_wait(&bs.m_set[before][warp & 3], 1, (int)(wg == 0 ? turn ^ 1u : turn), abort));
+            if (!ok) break;
+            if (b > 0) m_run = s_ref[head];
+          }
+          // Lazy rescale: a head keeps its reference until a block's maximum passes it by 2^kRescaleLog2,
+          // and O is rescaled only on those rare jumps. (NaN scores leave it alone.)
+          const float m_new = (bm - m_run) * sl2 > kRescaleLog2 || m_run == -INFINITY ? fmaxf(m_run, bm) : m_run;
+          s_ref[head] = m_new;
+          __syncwarp();
+          if (lane == 0) bar_arrive(&bs.m_set[wg][warp & 3]);
+          const float alpha = m_new == -INFINITY ? 1.f : ex2((m_run - m_new) * sl2);  // m_run = -inf: O is still 0
+          const float ref = m_new == -INFINITY ? 0.f : m_new;  // a NaN score stays one, an unseen row's weight is 0
+          l_own *= m_new == -INFINITY ? 1.f : ex2((m_own - m_new) * sl2);
+          m_own = m_new;
+          // the O-CTA's P buffer is free once P . V of block g - 3 is done
+          ok = __all_sync(0xffffffffu, g < NS || ready_or_wait<true>(bs.p_free, NS, g - NS, abort));
+          if (!ok) break;
+          st_async_f32(r_alpha, alpha, rbar);
+          float2 sum = make_float2(0.f, 0.f);
+#pragma unroll 1
+          for (int c = 0; c < BJ / 32; ++c) {
+            float t[32];
+            scores(c, t);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {  // four 16-B chunks of 8 f16
+              uint32_t v[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                float2 e = fma2(add2(make_float2(t[8 * q + 2 * i], t[8 * q + 2 * i + 1]), make_float2(-ref, -ref)),
+                                make_float2(sl2, sl2), make_float2(kRefLog2, kRefLog2));
+                e = make_float2(ex2(e.x), ex2(e.y));
+                const __half2 pb = __floats2half2_rn(e.x, e.y);
+                sum = add2(sum, e);
+                v[i] = *reinterpret_cast<const uint32_t*>(&pb);
+              }
+              st_async16(pbuf + sw128(head, 32 * c + 8 * q), make_uint4(v[0], v[1], v[2], v[3]), rbar);
+            }
+          }
+          tc_before();
+          __syncwarp();
+          if (lane == 0) bar_arrive(&bs.s_free[wg]);  // S has been read
+          l_own += sum.x + sum.y;
+        }
+        // its sum, under the reference of its last block, to the O-CTA
+        if (ok && mine) {
+          const uint32_t fin = remote(base + O_FIN, partner) + (full % NF) * FIN;
+          const uint32_t bar = remote(&bs.fin[full % NF], partner);
+          st_async_f32(fin + wg * FIN_WG + 4 * head, l_own, bar);
+          st_async_f32(fin + wg * FIN_WG + 4 * (MH + head), m_own, bar);
+          if (last) st_async_f32(fin + NS * FIN_WG + 4 * head, sl2, bar);
+        }
+      } else if (warp == ISSUER) {
+        // (tensor memory starts at 0: all of it is allocated here)
+        const bool one = elected();
+        const uint64_t k0 = mdesc(smem_u32(base + S_RING), 16, 1024);
+        bool go = __all_sync(0xffffffffu, ready_or_wait(&bs.q_full, 1, full, abort));
+        if (go && one) {  // Q has left its slots
+          bar_arrive(&bs.free[use0 % NK]);
+          bar_arrive(&bs.free[(use0 + 1) % NK]);
+        }
+        tc_after();
+#pragma unroll 1
+        for (int b = 0; go && b < nblk; ++b) {
+          const int g = done + b, use = use0 + 2 + b;
+          go = ready_or_wait(bs.full, NK, use, abort);
+          go = go && (g < NS || ready_or_wait(bs.s_free, NS, g - NS, abort));
+          go = __all_sync(0xffffffffu, go);
+          if (!go) break;
+          tc_after();
+          const uint64_t dk0 = k0 + (uint64_t)((use % NK) * (BLOCK >> 4));
+          const uint32_t d = S_COL + BJ * (g % NS);
+          if (one) {
+#pragma unroll
+            for (int kk = 0; kk < QATOMS * 4; ++kk)
+              mma_ta(d, Q_COL + 8 * kk, dk0 + (uint64_t)(((kk >> 2) * ATOM + (kk & 3) * 32) >> 4), kIdescQK, kk > 0);
+            commit(&bs.s_full[g % NS]);
+            commit(&bs.free[use % NK]);
+            if (b == nblk - 1) commit(&bs.q_done);
+            ctl.issued = g + 1;
+          }
+          __syncwarp();
+        }
+        ok = go;
+      } else if (warp == COPIER) {
+#pragma unroll 1
+        for (int i = 0; lane == 0 && ok && i < 2 + nblk; ++i) {
+          const int use = use0 + i;
+          ok = use < NK || ready_or_wait(bs.free, NK, use - NK, abort);
+          if (!ok) break;
+          uint64_t* bar = &bs.full[use % NK];
+          const uint32_t dst = smem_u32(base + S_RING + (use % NK) * BLOCK);
+          bar_arrive_tx(bar, BLOCK);
+          ctl.requested = use + 1;
+          if (i < 2) {  // half of Q: 64 rows, in boxes of 64 values
+            for (int bx = 0; bx < QATOMS; ++bx)
+              asm volatile(
+                  "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+                      dst + bx * ATOM),
+                  "l"(&tm_q), "r"(64 * bx), "r"((int)un.row0 + BJ * i), "r"(smem_u32(bar))
+                  : "memory");
+          } else {
+            asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                         "l"(w.kv + (size_t)(un.kv + i - 2) * BLOCK), "r"(BLOCK), "r"(smem_u32(bar))
+                         : "memory");
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+      }
+    } else {
+      // ================================ O-CTA ================================
+      const float* alpha_buf = reinterpret_cast<const float*>(base + O_ALPHA);
+      if (warp < 4) {
+        // corrector: where a reference maximum of the warp's heads rose, rescale O once P . V of the
+        // block before is done
+#pragma unroll 1
+        for (int b = 0; ok && b < nblk; ++b) {
+          const int g = done + b;
+          ok = __all_sync(0xffffffffu, ready_or_wait<true>(bs.p_full, NS, g, abort));
+          if (!ok) break;
+          const float f = alpha_buf[g % NS * MH + head];
+          // this buffer's next phase is block g + 3: its bytes come only after P . V of block g
+          if (tid == 0) bar_arrive_tx(&bs.p_full[g % NS], P_BYTES);
+          if (__any_sync(0xffffffffu, b > 0 && f != 1.f)) {
+            ok = __all_sync(0xffffffffu, ready_or_wait(bs.pv_done, NS, g - 1, abort));
+            if (!ok) break;
+            tc_after();
+#pragma unroll 1
+            for (int c = 0; c < DL; c += 16) {
+              float v[16];
+              tmem_ld16(tbase + lane_off + c, v);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) v[i] *= f;
+              tmem_st16(tbase + lane_off + c, v);
+            }
+            tc_before();
+          }
+          __syncwarp();
+          if (lane == 0) bar_arrive(&bs.pv_go[g % NS]);
+        }
+      } else if (warp == ISSUER) {
+        const bool one = elected();
+        const uint64_t p0 = mdesc(smem_u32(base + O_P), 16, 1024), v0 = mdesc(smem_u32(base + O_RING), ATOM, 1024);
+#pragma unroll 1
+        for (int b = 0; ok && b < nblk; ++b) {
+          const int g = done + b;
+          bool go = ready_or_wait(bs.pv_go, NS, g, abort);
+          if (b == 0) go = go && (full == 0 || ready_or_wait(&bs.o_free, 1, full - 1, abort));
+          const uint64_t dp0 = p0 + (uint64_t)((g % NS) * (P_BUF >> 4));
+#pragma unroll 1
+          for (int nh = 0; go && nh < 2; ++nh) {
+            const int use = 2 * g + nh;
+            go = __all_sync(0xffffffffu, ready_or_wait(bs.full, NV, use, abort));
+            if (!go) break;
+            tc_after();
+            fence_async_smem();  // P's writes, seen through their barrier, before the tensor core's reads
+            const uint64_t dv0 = v0 + (uint64_t)((use % NV) * (HALF_V >> 4));
+            if (one) {
+#pragma unroll
+              for (int kk = 0; kk < BJ / 16; ++kk)
+                mma_ss(256 * nh, dp0 + (uint64_t)((kk * 32) >> 4), dv0 + (uint64_t)((kk * 2048) >> 4), kIdescPV,
+                       (b > 0 || kk > 0) ? 1u : 0u);
+              commit(&bs.free[use % NV]);
+              if (nh == 1) {
+                commit(&bs.pv_done[g % NS]);
+                commit_multicast(&bs.p_free[g % NS], (uint16_t)(1u << partner));
+                if (b == nblk - 1) commit(&bs.o_full);
+                ctl.issued = g + 1;
+              }
+            }
+            __syncwarp();
+          }
+          ok = __all_sync(0xffffffffu, go);
+        }
+      } else if (warp == COPIER) {
+#pragma unroll 1
+        for (int i = 0; lane == 0 && ok && i < 2 * nblk; ++i) {
+          const int use = 2 * done + i;
+          ok = use < NV || ready_or_wait(bs.free, NV, use - NV, abort);
+          if (!ok) break;
+          bar_arrive_tx(&bs.full[use % NV], HALF_V);
+          ctl.requested = use + 1;
+          asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                           smem_u32(base + O_RING + (use % NV) * HALF_V)),
+                       "l"(w.kv + (size_t)(un.kv + (i >> 1)) * BLOCK + (i & 1) * HALF_V), "r"(HALF_V), "r"(smem_u32(&bs.full[use % NV]))
+                       : "memory");
+        }
+        ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+      }
+      if (warp < 4 * NOUT) {
+        // The read-out. Warps w, w + 4 and w + 8 have a quarter of the heads, as tensor memory has it, and every
+        // third 32 columns. The columns are ordered so that a lane's fragments are eight consecutive dims of each of
+        // four rows, and four lanes have 32 dims of a row. The warps that have nothing else to do wait at a barrier of
+        // the hardware, not at the mbarriers.
+        ok = sync_and(ok, 32 * 4 * NOUT);
+        if (!ok) break;  // (all of them: one that gave up further down comes here once more)
+        const int set = warp >> 2;
+        float l = 0.f, m = -INFINITY, sl2 = 0.f;
+        if (nblk > 0) {
+          const int k = full % NF;
+          if (tid == 0) bar_arrive_tx(&bs.fin[k], min(nblk, NS) * FIN_WG + MH * 4);
+          ok = ready_or_wait<true>(bs.fin, NF, full, abort) && ready_or_wait(&bs.o_full, 1, full, abort);
+          ok = __all_sync(0xffffffffu, ok);
+          tc_after();
+          // the warpgroups' sums, from the reference of each to the last block's
+          const float* fin = reinterpret_cast<const float*>(base + O_FIN + k * FIN) + head;
+          sl2 = fin[NS * (FIN_WG / 4)];
+          m = fin[(done + nblk - 1) % NS * (FIN_WG / 4) + MH];
+          for (int b = 0; b < min(nblk, NS); ++b) {
+            const float* of = fin + (done + nblk - 1 - b) % NS * (FIN_WG / 4);
+            l += of[MH] == -INFINITY ? of[0] : of[0] * ex2((of[MH] - m) * sl2);  // (no score: 0, or NaN)
+          }
+        }
+        const float inv = l == 0.f ? 0.f : 1.f / l;  // l is NaN where a weight is
+        const int part = 2 * pair + (un.first > 0 ? 0 : 1);
+        const size_t out0 = un.whole ? un.row0 : (size_t)part * MH;
+        const int row = (warp & 3) * 32 + (lane >> 2);  // and 8, 16, 24 after it
+        const size_t at = (out0 + row) * DL + 8 * (lane & 3);
+#pragma unroll 1
+        for (int c = 32 * set; ok && c < DL; c += 32 * NOUT) {
+          float v[2][16] = {};
+          if (nblk > 0) tmem_ld_frag(tbase + lane_off + c, v);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {  // rows 8 k after the first
+            const float f = __shfl_sync(0xffffffffu, inv, 8 * k + (lane >> 2));
+            uint32_t x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = __float_as_uint(v[k >> 1][4 * (i >> 1) + 2 * (k & 1) + (i & 1)] * f);
+            if (row + 8 * k >= un.live) {  // no query head
+            } else if (un.whole) {
+              uint32_t h[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const __nv_bfloat162 y = __floats2bfloat162_rn(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
+                h[i] = *reinterpret_cast<const uint32_t*>(&y);
+              }
+              *reinterpret_cast<uint4*>(a.o + at + 8 * k * DL + c) = make_uint4(h[0], h[1], h[2], h[3]);
+            } else {
+              store8(reinterpret_cast<uint32_t*>(w.part_o + at + 8 * k * DL + c), x, true);
+            }
+          }
+          __syncwarp();
+        }
+        if (ok && set == 0 && head < un.live)
+          (un.whole ? a.lse : w.part_lse)[out0 + head] = l == 0.f ? -INFINITY : (m * sl2 + (log2f(l) - kRefLog2)) * 0.6931471805599453f;
+        __syncwarp();
+        if (ok && nblk > 0) {
+          tc_before();
+          if (lane == 0) bar_arrive(&bs.o_free);
+        }
+      }
+      if (!ok && warp >= 4 * NOUT) break;
+    }
+    if (!ok && rank == 0) break;
+  }
+
+  __syncthreads();
+  // MMAs and their arrivals in this CTA are over, and the S-CTA has the O-CTA's last P-buffer releases
+  if (ok && done > 0) {
+    if (rank == 0) {
+      ok = pipe_wait(bs.free, NK, done + 2 * full - 1, abort) && pipe_wait(&bs.q_done, 1, full - 1, abort);
+      for (int b = done >= NS ? done - NS : 0; b < done; ++b) ok = ok && pipe_wait<true>(bs.p_free, NS, b, abort);
+    } else {
+      ok = pipe_wait(bs.free, NV, 2 * done - 2, abort) && pipe_wait(bs.free, NV, 2 * done - 1, abort) &&
+           pipe_wait(bs.pv_done, NS, done - 1, abort);
+    }
+  }
+  ok = __syncthreads_and(ok && !*abort);
+  if (!ok) {
+    // outputs are not valid: flag it, and give copies and MMAs still in flight one more bound before
+    // the shared and tensor memory are released
+    if (tid == 0) atomicOr(err, HS_FLAG_TIMEOUT);
+    __syncthreads();
+    if (tid == 0) ctl.abort = 0;
+    __syncthreads();
+    const int n = ctl.issued, m = ctl.requested;
+    if (rank == 0) {
+      for (int k = m >= NK ? m - NK : 0; k < m; ++k) pipe_wait(bs.full, NK, k, abort);
+      if (n > 0) pipe_wait(bs.s_full, NS, n - 1, abort);
+    } else {
+      for (int k = m >= NV ? m - NV : 0; k < m; ++k) pipe_wait(bs.full, NV, k, abort);
+      if (n > 0) pipe_wait(bs.pv_done, NS, n - 1, abort);
+    }
+  }
+  tc_before();
+  __syncthreads();
+  if (warp == 1)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tbase), "r"(TMEM_COLS) : "memory");
+  // the merge kernel may launch; it waits for this grid's completion before reading
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  cluster_sync_all();  // the partner no longer reads or arrives on this CTA's shared memory
+  if (!ok && tid == 0) stay();
+}
+
+// ---------------------------------------------------------------- the join
+
+// The parts of a tile that pair blockIdx.y began and did not end, joined in their order as an online softmax over their
+// log-sum-exps. A thread per eight output dims.
+constexpr int kMergeThreads = 256;
+__global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const ChunkArgs a, const Work w, int pairs) {
+  pdl_wait();
+  const int p = blockIdx.y;
+  const Pos from = w.starts[p], cut = w.starts[p + 1];
+  if (cut.blk == 0 || (from.ent == cut.ent && from.tile == cut.tile && from.blk > 0)) return;
+  const Entry e = w.entries[cut.ent];
+  const int per_tile = MH / a.num_heads, first = cut.tile * per_tile, live = min(per_tile, e.nq - first) * a.num_heads;
+  const int m = (blockIdx.x * kMergeThreads + threadIdx.x) / (DL / 8), c8 = threadIdx.x % (DL / 8);
+  if (m >= live) return;
+  float acc[8] = {}, z = 0.f, top = -INFINITY;
+  Pos at = cut;
+  for (int q = p; q < pairs;) {
+    const int slot = 2 * q + (q == p ? 1 : 0);
+    const float x = w.part_lse[slot * MH + m];
+    const float4* src = reinterpret_cast<const float4*>(w.part_o + ((size_t)slot * MH + m) * DL) + 2 * c8;
+    const float4 u = src[0], v = src[1];
+    const float mx = fmaxf(top, x), ref = mx == -INFINITY ? 0.f : mx;  // (a NaN leaves the maximum alone)
+    const float keep = expf(top - ref), f = expf(x - ref);
+    top = mx;
+    z = z * keep + f;
+    acc[0] = acc[0] * keep + f * u.x;
+    acc[1] = acc[1] * keep + f * u.y;
+    acc[2] = acc[2] * keep + f * u.z;
+    acc[3] = acc[3] * keep + f * u.w;
+    acc[4] = acc[4] * keep + f * v.x;
+    acc[5] = acc[5] * keep + f * v.y;
+    acc[6] = acc[6] * keep + f * v.z;
+    acc[7] = acc[7] * keep + f * v.w;
+    // the next pair with a part: one whose work begins here, and is not nothing
+    bool more = true;
+    do {
+      if (++q >= pairs) break;
+      const Pos next = w.starts[q + 1];
+      more = !(next.ent == at.ent && next.tile == at.tile && next.blk == at.blk);
+      if (more) {
+        // (pair q's part begins at `at`, inside the tile, if the part before it was cut there)
+        if (at.ent != cut.ent || at.tile != cut.tile || at.blk == 0) q = pairs;
+        at = next;
+      }
+    } while (!more);
+  }
+  const float inv = z == 0.f ? 0.f : 1.f / z;
+  uint32_t h[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 y = __floats2bfloat162_rn(acc[2 * i] * inv, acc[2 * i + 1] * inv);
+    h[i] = *reinterpret_cast<const uint32_t*>(&y);
+  }
+  const size_t row = ((size_t)e.q0 + first) * a.num_heads + m;
+  *reinterpret_cast<uint4*>(a.o + row * DL + 8 * c8) = make_uint4(h[0], h[1], h[2], h[3]);
+  if (c8 == 0) a.lse[row] = z == 0.f ? -INFINITY : top + logf(z);
+}
+
+// Q ([rows][576] bf16) as a 2-D tensor read in boxes of 64 rows x 64 dims, its 16-B chunks XOR-ed
+// with the row % 8; rows past the end read as zeros.
+cudaError_t q_map(CUtensorMap* m, const uint16_t* q, int64_t rows) {
+  EncodeTiled fn = encoder();
+  if (fn == nullptr) return cudaErrorNotSupported;
+  const cuuint64_t dims[2] = {(cuuint64_t)DQK, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)DQK * 2};
+  const cuuint32_t box[2] = {64u, (cuuint32_t)BJ};
+  const cuuint32_t elem[2] = {1u, 1u};
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<uint16_t*>(q), dims, strides, box, elem,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// CTA pairs that the current device holds at once: a CTA takes an SM. What a device is asked is kept, and the kernels are
+// set up for it on the way.
+constexpr int kDevices = 64;
+cudaError_t pairs_resident(int* pairs) {
+  static std::atomic<int> known[kDevices];
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && dev < kDevices && (*pairs = known[dev].load(std::memory_order_acquire)) > 0) return e;
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(chunk_mla_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(chunk_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, BLOCK);
+  *pairs = sms / 2 < 1 ? 1 : sms / 2 < kPairs ? sms / 2 : kPairs;
+  if (e != cudaSuccess)
+    (void)cudaGetLastError();
+  else if (dev < kDevices)
+    known[dev].store(*pairs, std::memory_order_release);
+  return e;
 }
 
 }  // namespace
 
 size_t chunk_workspace_bytes(int32_t n, int32_t num_heads, int32_t max_tokens, int64_t max_kv_tokens) {
   Work w;
-  return work_of(&w, nullptr, n);
+  return work_of(&w, nullptr, n, max_kv_tokens);
 }
 
 cudaError_t launch_chunk_mla(const ChunkArgs& a, void* workspace, uint32_t* err, cudaStream_t stream) {
   Work w;
-  work_of(&w, workspace, a.n);
-  cudaError_t e = cudaFuncSetAttribute(chunk_plain_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
-  if (e == cudaSuccess) e = launch(chunk_list_kernel, dim3(1), kListThreads, 0, stream, a, w, err);
-  if (e == cudaSuccess) e = launch(chunk_plain_kernel, dim3(152 * 2), kWarps * 32, kSmem, stream, a, w, err);
-  return e;
+  work_of(&w, workspace, a.n, a.max_kv_tokens);
+  int pairs = 1;
+  cudaError_t e = pairs_resident(&pairs);
+  CUtensorMap tm_q;
+  if (e == cudaSuccess) e = q_map(&tm_q, a.q, (int64_t)a.max_tokens * a.num_heads);
+  if (e == cudaSuccess) e = launch(chunk_list_kernel, dim3(1), kListThreads, 0, stream, a, w, pairs, err);
+  const int64_t blocks = a.max_kv_tokens / BJ, ctas = 6 * (int64_t)pairs;
+  if (e == cudaSuccess && blocks > 0)
+    e = launch(chunk_rows_kernel, dim3((unsigned)(blocks < ctas ? blocks : ctas)), kRowsThreads, BLOCK, stream, a, w, err);
+  if (e != cudaSuccess) {
+    (void)cudaGetLastError();
+    return e;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2u * (unsigned)pairs);
+  cfg.blockDim = dim3(T);
+  cfg.dynamicSmemBytes = SMEM_BYTES;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  e = cudaLaunchKernelEx(&cfg, chunk_mla_kernel, a, w, tm_q, err);
+  if (e != cudaSuccess) {
+    (void)cudaGetLastError();
+    return e;
+  }
+  const int rows = MH / a.num_heads * a.num_heads;
+  return launch(chunk_merge_kernel, dim3((unsigned)((rows * (DL / 8) + kMergeThreads - 1) / kMergeThreads), (unsigned)pairs),
+                kMergeThreads, 0, stream, a, w, pairs);
 }
 
 }  // namespace hs

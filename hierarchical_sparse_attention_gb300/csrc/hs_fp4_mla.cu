@@ -148,104 +148,6 @@ struct __align__(STATIC_BYTES) Control {
 };
 static_assert(sizeof(Control) == STATIC_BYTES, "one block");
 
-// The kernel's roles run side by side from one instruction cache, and much of their time goes into
-// handing over: so their loops are short (not unrolled over blocks: at 165 KB of code the same loops
-// took up to twice as long as at 70 KB), and the wait that has to look at the clock is a call.
-template <bool cluster>
-__device__ __forceinline__ bool try_once(uint64_t* bar, uint32_t parity) {
-  uint32_t done;
-  if (cluster)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(smem_u32(bar)), "r"(parity), "n"(kSuspendNs)
-        : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(smem_u32(bar)), "r"(parity), "n"(kSuspendNs)
-        : "memory");
-  return done != 0;
-}
-// Waits on, with pipe_wait's bound; looks at the clock and at the abort flag every few tries only (a
-// try ends after well under a microsecond whatever it is asked, and the waiting warps' looks were a
-// quarter of all instructions).
-template <bool cluster>
-__device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  const uint64_t t0 = gtime();
-  for (;;) {
-#pragma unroll 1
-    for (int i = 0; i < 16; ++i)
-      if (try_once<cluster>(bar, parity)) return true;
-    if (*abort || gtime() - t0 > kWaitNs) {
-      *abort = 1;
-      return false;
-    }
-  }
-}
-// pipe_wait for waits that are mostly over when they begin: the clock is read only once the first
-// try has failed (reading it first made every hand-over ~0.1 us longer). Use k of a ring of `depth`
-// barriers; a waiter has to have seen the ring's use k - depth over (parities repeat).
-template <bool cluster = false>
-__device__ __forceinline__ bool ready_or_wait(uint64_t* ring, int depth, int k, volatile int* abort) {
-  uint64_t* bar = ring + (k % depth);
-  const uint32_t parity = (uint32_t)(k / depth) & 1u;
-  return try_once<cluster>(bar, parity) || wait_on<cluster>(bar, parity, abort);
-}
-// One lane of the (converged) warp. The MMAs are issued by it from code that the whole warp runs, so
-// that their operands stay in uniform registers: 33 clocks an MMA of N = 64 with A in tensor memory,
-// where `if (lane == 0)` around the loop made it 58.
-__device__ __forceinline__ bool elected() {
-  uint32_t r;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-  return r != 0;
-}
-
-__device__ __forceinline__ float ex2(float x) {  // 2^x: -inf gives 0, NaN stays
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-// 32 accumulator columns of this thread's row.
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
-#pragma unroll
-  for (int h = 0; h < 32; h += 16) {
-    uint32_t* r = reinterpret_cast<uint32_t*>(v + h);
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr + h));
-  }
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-}
-// 32 accumulator columns of 32 rows, spread over the warp as matrix fragments are: v[h][4 j + 2 s + e]
-// is row 16 h + 8 s + lane / 4, column 8 j + 2 (lane % 4) + e.
-__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, float (&v)[2][16]) {
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    uint32_t* r = reinterpret_cast<uint32_t*>(v[h]);
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr + ((uint32_t)(16 * h) << 16)));
-  }
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-}
-// 32 consecutive bytes of a lane: one store (a whole sector) where they are aligned.
-__device__ __forceinline__ void store8(uint32_t* dst, const uint32_t (&w)[8], bool aligned) {
-  if (aligned) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                 : "memory");
-  } else {
-    reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-  }
-}
 // What a unit of a score without its scales is in log2 units.
 __device__ __forceinline__ float score_log2(const Fp4MlaArgs& a) {
   return fabsf(a.sm_scale * a.latent_scale * 1.4426950408889634f);
@@ -259,28 +161,6 @@ __device__ __forceinline__ float q_divisor(uint32_t top, uint32_t rope) {
   if (top == 0 || (top >= 0x3C80u && top < 0x4780u)) return 1.f;  // 2^-6, 2^16
   return __uint_as_float((uint32_t)max(max((int)(top >> 7) - 15, (int)(rope >> 7) - 75), 127 - 95) << 23);
 }
-__device__ __forceinline__ uint32_t max_bf16x2(uint32_t m, const uint4& x) {  // of magnitudes
-  constexpr uint32_t k = 0x7FFF7FFFu;
-  return __vmaxu2(m, __vmaxu2(__vmaxu2(x.x & k, x.y & k), __vmaxu2(x.z & k, x.w & k)));
-}
-// Two 32-bit floats at a time.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
-      "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return d;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tadd.rn.f32x2 x, x, y;\n\t"
-      "mov.b64 {%0, %1}, x;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
-
 // The rows of a tile's split, j = 0 .. n - 1, and who sees them.
 template <bool kWin>
 struct Rows {
@@ -482,14 +362,6 @@ __device__ __forceinline__ bool run_dequant(const Rows<kWin>& rows, const uint8_
 __device__ __forceinline__ int deq_warp(int w, int first) {
   const int i = w - first, q = 3 * (i >> 2) + (i & 3);
   return i >= 0 && (i & 3) != 3 && q < NDEQ ? q : -1;
-}
-
-// Bits lo .. hi - 1 of a 32-bit mask.
-__device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
-  lo = min(max(lo, 0), 32);
-  hi = min(max(hi, 0), 32);
-  if (hi <= lo) return 0u;
-  return (0xFFFFFFFFu >> (32 - (hi - lo))) << lo;
 }
 
 // The tiles' numbers: the first `whole` tiles are a unit each, the others, whose query heads begin with
