@@ -48,17 +48,23 @@ using namespace tc;
 
 namespace {
 
-constexpr int T = 448;   // threads per CTA: 14 warps
+constexpr int T = 512;   // threads per CTA: 16 warps
 constexpr int MH = 128;  // MMA M: query heads of a tile (what is there of the next tokens fills it up)
 constexpr int BJ = 64;   // rows per block
 constexpr int DQK = kFp8Dims, DL = kFp8Latent;
 constexpr int QATOMS = DQK / 64, ATOMS = DL / 64;  // swizzle atoms of 64 values in a block of K and of V
 constexpr int NS = 3;    // S buffers, softmax warpgroups and P buffers: a block each in turn
 constexpr int NK = 3, NV = 5;  // slots of the S-CTA's ring (a block, or half of Q) and of the O-CTA's (half of V's block)
+// Barriers of V's slots: two to a slot in turn, as a use of an odd slot count is the other half's use before, whose issuer
+// waits on the other barrier: so each issuer waits on every phase of its own.
+constexpr int NVF = 2 * NV;
 constexpr uint32_t TMEM_COLS = 512, Q_COL = 0, S_COL = 288;
 static_assert(S_COL + NS * BJ <= TMEM_COLS, "Q and the S buffers fit tensor memory");
-// S-CTA warps: 0-11 softmax; O-CTA: 0-3 corrector, which reads out with 4-11; both: 12 issuer, 13 copies.
-constexpr int ISSUER = 12, COPIER = 13, NOUT = 3;  // NOUT warps read out a quarter of the heads
+// S-CTA warps: 0-11 softmax, 12-14 issuers; O-CTA: 0-3 corrector, which reads out with 4-11, 12 issuer; both: 15 copies.
+// S has an issuer per buffer: a commit takes its thread some 500 clocks with a block's MMAs before it, and the waits for
+// the next block 300 more, in which another thread's MMAs keep the tensor core busy (one issuer for all of S: 2,050 clocks
+// a block, of which its 36 MMAs are 1,150).
+constexpr int ISSUER = 12, COPIER = 15, NOUT = 3;  // NOUT warps read out a quarter of the heads
 
 constexpr uint32_t ATOM = BJ * 128, BLOCK = QATOMS * ATOM, HALF_V = ATOMS / 2 * ATOM;
 constexpr uint32_t S_RING = 0;
@@ -130,6 +136,27 @@ size_t work_of(Work* w, void* workspace, int32_t n, int64_t max_kv_tokens) {
   w->part_lse = reinterpret_cast<float*>(take((size_t)2 * kPairs * MH * 4));
   w->part_o = reinterpret_cast<float*>(take((size_t)2 * kPairs * MH * DL * 4));
   return at;
+}
+
+// P's descriptor: no swizzle, chunk c (8 values) of row m at 16 (128 c + m), so that a warp's stores of a chunk are 512
+// consecutive bytes. (Between two SMs' shared memories 16 KB of P take 860 clocks so, 1,600 to 2,000 where each lane's 16
+// bytes go to a line of their own, as rows of 128 bytes want it, and a block's MMAs 1,150.)
+__device__ __forceinline__ uint64_t pdesc(uint32_t saddr) {
+  return (uint64_t)((saddr >> 4) & 0x3FFF) | ((uint64_t)((MH * 16) >> 4) << 16) | ((uint64_t)(128 >> 4) << 32) | (1ull << 46);
+}
+
+// 64 accumulator columns of this thread's row.
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, float (&v)[BJ]) {
+#pragma unroll
+  for (int h = 0; h < BJ; h += 16) {
+    uint32_t* r = reinterpret_cast<uint32_t*>(v + h);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr + h));
+  }
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
 // ---------------------------------------------------------------- the list
@@ -340,14 +367,14 @@ static_assert(kRowsThreads / 32 * 3 == 32 + BJ / 16, "three tasks a warp");
 // ---------------------------------------------------------------- the attention
 
 struct Barriers {
-  uint64_t full[NV], free[NV];     // a ring slot's bytes are there; it has been read
+  uint64_t full[NVF], free[NV];    // a ring slot's bytes are there; it has been read
   uint64_t q_top, q_full, q_done;  // S-CTA: Q's largest values are known; Q in tensor memory; the tile's last S is done
   // per softmax warpgroup, so that whoever waits on one waits on every phase of it (parities repeat):
   uint64_t s_full[NS], s_free[NS]; // S-CTA: S written; S read
   uint64_t m_set[NS][4];           // S-CTA: the block's reference maxima of a warp's heads are set
-  uint64_t p_free[NS];             // S-CTA, arrived by the O-CTA: P . V of the block is done
+  uint64_t p_free[NS];             // both, arrived by the O-CTA's issuers: P . V of the block is done
   uint64_t p_full[NS];             // O-CTA, completed by the S-CTA's stores
-  uint64_t pv_go[NS], pv_done[NS]; // O-CTA: O is ready for P . V of the block; it is done
+  uint64_t pv_go[NS];              // O-CTA: O is ready for P . V of the block
   uint64_t fin[NF];                // O-CTA: the S-CTA's totals of a tile are here
   uint64_t o_full, o_free;         // O-CTA: a tile's last P . V is done; O has been read out
 };
@@ -357,7 +384,7 @@ struct __align__(STATIC_BYTES) Control {
   Barriers bs;
   uint32_t taddr;
   int abort;
-  int issued;     // blocks whose MMAs the issuer started (the last commit to wait for)
+  int issued[NS];  // blocks whose MMAs each issuer started (the last commit to wait for)
   int requested;  // ring slots whose copies were started
 };
 static_assert(sizeof(Control) == STATIC_BYTES, "one block");
@@ -425,27 +452,24 @@ __global__ void __launch_bounds__(T, 1)
   const int pair = blockIdx.x >> 1;
 
   if (tid == 0) {
-    for (int k = 0; k < NV; ++k) {
-      bar_init(&bs.full[k], 1);
-      bar_init(&bs.free[k], 1);
-    }
+    for (int k = 0; k < NVF; ++k) bar_init(&bs.full[k], 1);
+    for (int k = 0; k < NV; ++k) bar_init(&bs.free[k], 1);
     bar_init(&bs.q_top, 4 * NS);  // one arrival per softmax warp
     bar_init(&bs.q_full, 4 * NS);
-    bar_init(&bs.q_done, 1);
+    bar_init(&bs.q_done, NS);
     for (int k = 0; k < NS; ++k) {
       bar_init(&bs.s_full[k], 1);
       bar_init(&bs.s_free[k], 4);  // the warps of the block's softmax warpgroup
       for (int x = 0; x < 4; ++x) bar_init(&bs.m_set[k][x], 1);
-      bar_init(&bs.p_free[k], 1);
+      bar_init(&bs.p_free[k], 2);
       bar_init(&bs.p_full[k], 1);  // the O-CTA's expect_tx; the S-CTA's stores complete it
       bar_init(&bs.pv_go[k], 4);
-      bar_init(&bs.pv_done[k], 1);
     }
     for (int k = 0; k < NF; ++k) bar_init(&bs.fin[k], 1);  // the same
-    bar_init(&bs.o_full, 1);
+    bar_init(&bs.o_full, 2);
     bar_init(&bs.o_free, 4 * NOUT);
     ctl.abort = 0;
-    ctl.issued = 0;
+    for (int k = 0; k < NS; ++k) ctl.issued[k] = 0;
     ctl.requested = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     if (rank == 1)
@@ -478,7 +502,8 @@ __global__ void __launch_bounds__(T, 1)
   int done = 0, full = 0;  // blocks, and units with blocks, before this one
   Unit un;
 #pragma unroll 1
-  for (; next_unit(a, w, per_tile, walk, un); done += un.nblk, full += un.nblk > 0) {
+  for (; __all_sync(0xffffffffu, next_unit(a, w, per_tile, walk, un)); done += un.nblk, full += un.nblk > 0) {
+    un.nblk = __reduce_max_sync(0xffffffffu, un.nblk);
     const int nblk = un.nblk;
     const int use0 = done + 2 * full;  // the S-CTA's ring: Q's two slots, then a slot per block
     if (rank == 0) {
@@ -540,12 +565,12 @@ __global__ void __launch_bounds__(T, 1)
         // thread. From one block to the next only the reference maximum goes over, from warp to warp
         // (the warps of the same heads): it is known once a block's scores have been read, so the
         // warpgroups' exponentials overlap. Each keeps the sum of its own blocks under the reference of
-        // its last one. The scores are read twice, for the maximum and for the weights. References are
+        // its last one. References are
         // scores as S holds them, and a weight's exponent is the difference, scaled: a score times the scale
         // is rounded by whole units from 2^24 on.
         float m_own = -INFINITY, l_own = 0.f;  // the sum of this thread's blocks, under this reference
         float* s_ref = reinterpret_cast<float*>(base + S_REF);
-        const uint32_t pbuf = remote(base + O_P + wg * P_BUF, partner);  // (block g's buffer is g % NS = wg)
+        const uint32_t pbuf = remote(base + O_P + wg * P_BUF + 16 * head, partner);  // (block g's buffer is g % NS = wg)
         const uint32_t r_alpha = remote(base + O_ALPHA + 4 * (wg * MH + head), partner), rbar = remote(&bs.p_full[wg], partner);
         // what a unit of S is; a scale of zero stays above it, so that -inf stays -inf
         const float sl2 = fminf(fmaxf(score_log2(a) * up, 1e-37f), 3e38f);
@@ -569,28 +594,27 @@ __global__ void __launch_bounds__(T, 1)
           if (!ok) break;
           tc_after();
           const bool every = __all_sync(0xffffffffu, (sees0 & sees1) == 0xFFFFFFFFu && (nan0 | nan1) == 0u);
-          const auto scores = [&](int c, float (&t)[32]) {  // 32 c .. 32 c + 31 of the block, -inf where it does not look
-            tmem_ld32(s_at + 32 * c, t);
-            if (!every) {
-              const uint32_t sees = c ? sees1 : sees0, nan = c ? nan1 : nan0;
+          float t[BJ];  // the scores; -inf where this query does not look
+          tmem_ld64(s_at, t);
+          tc_before();
+          __syncwarp();
+          if (lane == 0) bar_arrive(&bs.s_free[wg]);  // S has been read
+          if (!every) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
-                t[i] = ((sees >> i) & 1u) ? (((nan >> i) & 1u) ? __uint_as_float(0x7FC00000u) : t[i]) : -INFINITY;
+            for (int i = 0; i < BJ; ++i) {
+              const uint32_t sees = i < 32 ? sees0 : sees1, nan = i < 32 ? nan0 : nan1;
+              t[i] = ((sees >> (i & 31)) & 1u) ? (((nan >> (i & 31)) & 1u) ? __uint_as_float(0x7FC00000u) : t[i]) : -INFINITY;
             }
-          };
-          float bm = -INFINITY;
-#pragma unroll 1
-          for (int c = 0; c < BJ / 32; ++c) {
-            float t[32];
-            scores(c, t);
-            float x0 = t[0], x1 = t[1];
-#pragma unroll
-            for (int i = 2; i < 32; i += 2) {
-              x0 = fmaxf(x0, t[i]);
-              x1 = fmaxf(x1, t[i + 1]);
-            }
-            bm = fmaxf(bm, fmaxf(x0, x1));
           }
+          float x0 = t[0], x1 = t[1], x2 = t[2], x3 = t[3];
+#pragma unroll
+          for (int i = 4; i < BJ; i += 4) {
+            x0 = fmaxf(x0, t[i]);
+            x1 = fmaxf(x1, t[i + 1]);
+            x2 = fmaxf(x2, t[i + 2]);
+            x3 = fmaxf(x3, t[i + 3]);
+          }
+          const float bm = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3));
           float m_run = -INFINITY;
           if (g > 0) {
             // (the block before is the last warpgroup's block of this turn, or of the turn before)
@@ -614,28 +638,20 @@ __global__ void __launch_bounds__(T, 1)
           if (!ok) break;
           st_async_f32(r_alpha, alpha, rbar);
           float2 sum = make_float2(0.f, 0.f);
-#pragma unroll 1
-          for (int c = 0; c < BJ / 32; ++c) {
-            float t[32];
-            scores(c, t);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {  // four 16-B chunks of 8 f16
-              uint32_t v[4];
+          for (int q = 0; q < BJ / 8; ++q) {  // 16-B chunks of 8 f16
+            uint32_t v[4];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                float2 e = fma2(add2(make_float2(t[8 * q + 2 * i], t[8 * q + 2 * i + 1]), make_float2(-ref, -ref)),
-                                make_float2(sl2, sl2), make_float2(kRefLog2, kRefLog2));
-                e = make_float2(ex2(e.x), ex2(e.y));
-                const __half2 pb = __floats2half2_rn(e.x, e.y);
-                sum = add2(sum, e);
-                v[i] = *reinterpret_cast<const uint32_t*>(&pb);
-              }
-              st_async16(pbuf + sw128(head, 32 * c + 8 * q), make_uint4(v[0], v[1], v[2], v[3]), rbar);
+            for (int i = 0; i < 4; ++i) {
+              float2 e = fma2(add2(make_float2(t[8 * q + 2 * i], t[8 * q + 2 * i + 1]), make_float2(-ref, -ref)),
+                              make_float2(sl2, sl2), make_float2(kRefLog2, kRefLog2));
+              e = make_float2(ex2(e.x), ex2(e.y));
+              const __half2 pb = __floats2half2_rn(e.x, e.y);
+              sum = add2(sum, e);
+              v[i] = *reinterpret_cast<const uint32_t*>(&pb);
             }
+            st_async16(pbuf + q * (MH * 16), make_uint4(v[0], v[1], v[2], v[3]), rbar);
           }
-          tc_before();
-          __syncwarp();
-          if (lane == 0) bar_arrive(&bs.s_free[wg]);  // S has been read
           l_own += sum.x + sum.y;
         }
         // its sum, under the reference of its last block, to the O-CTA
@@ -646,34 +662,39 @@ __global__ void __launch_bounds__(T, 1)
           st_async_f32(fin + wg * FIN_WG + 4 * (MH + head), m_own, bar);
           if (last) st_async_f32(fin + NS * FIN_WG + 4 * head, sl2, bar);
         }
-      } else if (warp == ISSUER) {
+      } else if (warp < ISSUER + NS) {
         // (tensor memory starts at 0: all of it is allocated here)
+        const int wg = warp - ISSUER;
         const bool one = elected();
         const uint64_t k0 = mdesc(smem_u32(base + S_RING), 16, 1024);
         bool go = __all_sync(0xffffffffu, ready_or_wait(&bs.q_full, 1, full, abort));
-        if (go && one) {  // Q has left its slots
+        if (go && one && wg == 0) {  // Q has left its slots
           bar_arrive(&bs.free[use0 % NK]);
           bar_arrive(&bs.free[(use0 + 1) % NK]);
         }
         tc_after();
+        int b = wg - done % NS;
+        if (b < 0) b += NS;
+        if (go && one && b >= nblk) bar_arrive(&bs.q_done);  // nothing of this unit
+        int turn = (done + b) / NS;  // of this buffer
 #pragma unroll 1
-        for (int b = 0; go && b < nblk; ++b) {
-          const int g = done + b, use = use0 + 2 + b;
+        for (; go && b < nblk; b += NS, ++turn) {
+          const int use = use0 + 2 + b;
           go = ready_or_wait(bs.full, NK, use, abort);
-          go = go && (g < NS || ready_or_wait(bs.s_free, NS, g - NS, abort));
+          go = go && (turn == 0 || ready_or_wait(&bs.s_free[wg], 1, turn - 1, abort));
           go = __all_sync(0xffffffffu, go);
           if (!go) break;
           tc_after();
           const uint64_t dk0 = k0 + (uint64_t)((use % NK) * (BLOCK >> 4));
-          const uint32_t d = S_COL + BJ * (g % NS);
+          const uint32_t d = S_COL + BJ * wg;
           if (one) {
 #pragma unroll
             for (int kk = 0; kk < QATOMS * 4; ++kk)
               mma_ta(d, Q_COL + 8 * kk, dk0 + (uint64_t)(((kk >> 2) * ATOM + (kk & 3) * 32) >> 4), kIdescQK, kk > 0);
-            commit(&bs.s_full[g % NS]);
+            commit(&bs.s_full[wg]);
             commit(&bs.free[use % NK]);
-            if (b == nblk - 1) commit(&bs.q_done);
-            ctl.issued = g + 1;
+            if (b + NS >= nblk) commit(&bs.q_done);
+            ctl.issued[wg] = turn + 1;
           }
           __syncwarp();
         }
@@ -718,7 +739,7 @@ __global__ void __launch_bounds__(T, 1)
           // this buffer's next phase is block g + 3: its bytes come only after P . V of block g
           if (tid == 0) bar_arrive_tx(&bs.p_full[g % NS], P_BYTES);
           if (__any_sync(0xffffffffu, b > 0 && f != 1.f)) {
-            ok = __all_sync(0xffffffffu, ready_or_wait(bs.pv_done, NS, g - 1, abort));
+            ok = __all_sync(0xffffffffu, ready_or_wait(bs.p_free, NS, g - 1, abort));
             if (!ok) break;
             tc_after();
 #pragma unroll 1
@@ -734,39 +755,32 @@ __global__ void __launch_bounds__(T, 1)
           __syncwarp();
           if (lane == 0) bar_arrive(&bs.pv_go[g % NS]);
         }
-      } else if (warp == ISSUER) {
+      } else if (warp == ISSUER || warp == ISSUER + 1) {
+        const int nh = warp - ISSUER;  // this issuer's 256 columns
         const bool one = elected();
-        const uint64_t p0 = mdesc(smem_u32(base + O_P), 16, 1024), v0 = mdesc(smem_u32(base + O_RING), ATOM, 1024);
+        const uint64_t p0 = pdesc(smem_u32(base + O_P)), v0 = mdesc(smem_u32(base + O_RING), ATOM, 1024);
 #pragma unroll 1
         for (int b = 0; ok && b < nblk; ++b) {
-          const int g = done + b;
+          const int g = done + b, use = 2 * g + nh;
           bool go = ready_or_wait(bs.pv_go, NS, g, abort);
           if (b == 0) go = go && (full == 0 || ready_or_wait(&bs.o_free, 1, full - 1, abort));
-          const uint64_t dp0 = p0 + (uint64_t)((g % NS) * (P_BUF >> 4));
-#pragma unroll 1
-          for (int nh = 0; go && nh < 2; ++nh) {
-            const int use = 2 * g + nh;
-            go = __all_sync(0xffffffffu, ready_or_wait(bs.full, NV, use, abort));
-            if (!go) break;
-            tc_after();
-            fence_async_smem();  // P's writes, seen through their barrier, before the tensor core's reads
-            const uint64_t dv0 = v0 + (uint64_t)((use % NV) * (HALF_V >> 4));
-            if (one) {
-#pragma unroll
-              for (int kk = 0; kk < BJ / 16; ++kk)
-                mma_ss(256 * nh, dp0 + (uint64_t)((kk * 32) >> 4), dv0 + (uint64_t)((kk * 2048) >> 4), kIdescPV,
-                       (b > 0 || kk > 0) ? 1u : 0u);
-              commit(&bs.free[use % NV]);
-              if (nh == 1) {
-                commit(&bs.pv_done[g % NS]);
-                commit_multicast(&bs.p_free[g % NS], (uint16_t)(1u << partner));
-                if (b == nblk - 1) commit(&bs.o_full);
-                ctl.issued = g + 1;
-              }
-            }
-            __syncwarp();
-          }
+          go = go && ready_or_wait(bs.full, NVF, use, abort);
           ok = __all_sync(0xffffffffu, go);
+          if (!ok) break;
+          tc_after();
+          fence_async_smem();  // P's writes, seen through their barrier, before the tensor core's reads
+          const uint64_t dp0 = p0 + (uint64_t)((g % NS) * (P_BUF >> 4)), dv0 = v0 + (uint64_t)((use % NV) * (HALF_V >> 4));
+          if (one) {
+#pragma unroll
+            for (int kk = 0; kk < BJ / 16; ++kk)
+              mma_ss(256 * nh, dp0 + (uint64_t)((kk * 2 * MH * 16) >> 4), dv0 + (uint64_t)((kk * 2048) >> 4), kIdescPV,
+                     (b > 0 || kk > 0) ? 1u : 0u);
+            commit(&bs.free[use % NV]);
+            commit_multicast(&bs.p_free[g % NS], (uint16_t)3);
+            if (b == nblk - 1) commit(&bs.o_full);
+            ctl.issued[nh] = g + 1;
+          }
+          __syncwarp();
         }
       } else if (warp == COPIER) {
 #pragma unroll 1
@@ -774,11 +788,12 @@ __global__ void __launch_bounds__(T, 1)
           const int use = 2 * done + i;
           ok = use < NV || ready_or_wait(bs.free, NV, use - NV, abort);
           if (!ok) break;
-          bar_arrive_tx(&bs.full[use % NV], HALF_V);
+          uint64_t* bar = &bs.full[use % NVF];
+          bar_arrive_tx(bar, HALF_V);
           ctl.requested = use + 1;
           asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
                            smem_u32(base + O_RING + (use % NV) * HALF_V)),
-                       "l"(w.kv + (size_t)(un.kv + (i >> 1)) * BLOCK + (i & 1) * HALF_V), "r"(HALF_V), "r"(smem_u32(&bs.full[use % NV]))
+                       "l"(w.kv + (size_t)(un.kv + (i >> 1)) * BLOCK + (i & 1) * HALF_V), "r"(HALF_V), "r"(smem_u32(bar))
                        : "memory");
         }
         ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
@@ -854,11 +869,12 @@ __global__ void __launch_bounds__(T, 1)
   // MMAs and their arrivals in this CTA are over, and the S-CTA has the O-CTA's last P-buffer releases
   if (ok && done > 0) {
     if (rank == 0) {
-      ok = pipe_wait(bs.free, NK, done + 2 * full - 1, abort) && pipe_wait(&bs.q_done, 1, full - 1, abort);
+      for (int k = max(done + 2 * full - NK, 0); k < done + 2 * full; ++k) ok = ok && pipe_wait(bs.free, NK, k, abort);
+      ok = ok && pipe_wait(&bs.q_done, 1, full - 1, abort);
       for (int b = done >= NS ? done - NS : 0; b < done; ++b) ok = ok && pipe_wait<true>(bs.p_free, NS, b, abort);
     } else {
       ok = pipe_wait(bs.free, NV, 2 * done - 2, abort) && pipe_wait(bs.free, NV, 2 * done - 1, abort) &&
-           pipe_wait(bs.pv_done, NS, done - 1, abort);
+           pipe_wait(bs.p_free, NS, done - 1, abort);
     }
   }
   ok = __syncthreads_and(ok && !*abort);
@@ -869,13 +885,16 @@ __global__ void __launch_bounds__(T, 1)
     __syncthreads();
     if (tid == 0) ctl.abort = 0;
     __syncthreads();
-    const int n = ctl.issued, m = ctl.requested;
+    const int m = ctl.requested;
     if (rank == 0) {
       for (int k = m >= NK ? m - NK : 0; k < m; ++k) pipe_wait(bs.full, NK, k, abort);
-      if (n > 0) pipe_wait(bs.s_full, NS, n - 1, abort);
+      for (int k = 0; k < NS; ++k)
+        if (ctl.issued[k] > 0) pipe_wait(&bs.s_full[k], 1, ctl.issued[k] - 1, abort);
     } else {
-      for (int k = m >= NV ? m - NV : 0; k < m; ++k) pipe_wait(bs.full, NV, k, abort);
-      if (n > 0) pipe_wait(bs.pv_done, NS, n - 1, abort);
+      for (int k = m >= NV ? m - NV : 0; k < m; ++k) pipe_wait(bs.full, NVF, k, abort);
+      // (each issuer's last block; a block that only one of them issued completes no phase: its slot's does)
+      for (int k = 0; k < 2; ++k)
+        if (ctl.issued[k] > 0) pipe_wait(bs.free, NV, 2 * (ctl.issued[k] - 1) + k, abort);
     }
   }
   tc_before();
