@@ -25,8 +25,8 @@
 // K's slots (a slot holds a block of 64 rows of 576 values, or half of Q), V through a ring of half blocks.
 //
 // Precision. Latents (e4m3 x scale) and RoPE values go through f16: exact where the scale is a power of two, else off by 2^-11
-// of themselves, and by 2^-25 where they are below 2^-14. Q goes through f16 over a power of two of its head, which
-// goes into its scores' scale: off by 2^-40 of the head's largest. P, whose reference weighs 2^7, is rounded to f16: by up to
+// of themselves, and by 2^-25 where they are below 2^-14. Q goes through f16, over a power of two where its head's
+// largest value is below 1 or above 65504, which goes into its scores' scale: off by 2^-25 of the head's largest. P, whose reference weighs 2^7, is rounded to f16: by up to
 // 2^-11 of a weight, and by 2^-32 of the largest weight where it is below 2^-21 of that; its sum takes weights
 // unrounded, so lse does not see it. Scores, maxima, sums and O are in 32 bits.
 //
@@ -41,6 +41,7 @@
 #include <cuda_fp8.h>
 
 #include <atomic>
+#include <type_traits>
 
 namespace hs {
 
@@ -60,7 +61,8 @@ constexpr int NK = 3, NV = 5;  // slots of the S-CTA's ring (a block, or half of
 constexpr int NVF = 2 * NV;
 constexpr uint32_t TMEM_COLS = 512, Q_COL = 0, S_COL = 288;
 static_assert(S_COL + NS * BJ <= TMEM_COLS, "Q and the S buffers fit tensor memory");
-// S-CTA warps: 0-11 softmax, 12-14 issuers; O-CTA: 0-3 corrector, which reads out with 4-11, 12 issuer; both: 15 copies.
+// S-CTA warps: 0-11 softmax, 12-14 issuers, 15 copies, and 12-15 bring Q; O-CTA: 0-3 corrector, which reads out with 4-11,
+// 12 and 13 issuers, 15 copies.
 // S has an issuer per buffer: a commit takes its thread some 500 clocks with a block's MMAs before it, and the waits for
 // the next block 300 more, in which another thread's MMAs keep the tensor core busy (one issuer for all of S: 2,050 clocks
 // a block, of which its 36 MMAs are 1,150).
@@ -69,8 +71,12 @@ constexpr int ISSUER = 12, COPIER = 15, NOUT = 3;  // NOUT warps read out a quar
 constexpr uint32_t ATOM = BJ * 128, BLOCK = QATOMS * ATOM, HALF_V = ATOMS / 2 * ATOM;
 constexpr uint32_t S_RING = 0;
 constexpr uint32_t S_REF = NK * BLOCK;             // the reference maxima, handed from block to block
-constexpr uint32_t S_QTOP = S_REF + MH * 4;        // a head's largest value in each third of Q
-constexpr uint32_t S_END = S_QTOP + NS * MH * 2;
+constexpr uint32_t S_UP = S_REF + MH * 4;          // what a head's Q was divided by, of the last NQ tiles
+// A softmax warpgroup that is at a block may find S computed up to five blocks on (its next one and the two after that), and
+// so, of tiles of one block each, Q set six tiles on: it looks at those tiles' barriers later, each before its
+// next use.
+constexpr int NQ = 8;
+constexpr uint32_t S_END = S_UP + NQ * MH * 4;
 constexpr uint32_t O_RING = 0;
 constexpr uint32_t O_P = NV * HALF_V;
 constexpr uint32_t P_BUF = MH * BJ * 2, P_BYTES = P_BUF + MH * 4;  // P and the rescale factors of a block
@@ -91,7 +97,7 @@ constexpr uint32_t kIdescQK = idesc(BJ, MH, false);
 constexpr uint32_t kIdescPV = idesc(256, MH, true);
 
 // How the work is dealt out, in blocks: what a tile takes besides its blocks, and the least part of a tile.
-constexpr int kTileCost = 4, kLeastPart = 4;
+constexpr int kTileCost = 5, kLeastPart = 4;
 constexpr int kPairs = 76;  // of CTAs, at most
 constexpr int kListThreads = 512;
 static_assert(kPairs < kListThreads, "a thread per pair");
@@ -368,7 +374,7 @@ static_assert(kRowsThreads / 32 * 3 == 32 + BJ / 16, "three tasks a warp");
 
 struct Barriers {
   uint64_t full[NVF], free[NV];    // a ring slot's bytes are there; it has been read
-  uint64_t q_top, q_full, q_done;  // S-CTA: Q's largest values are known; Q in tensor memory; the tile's last S is done
+  uint64_t q_full[NQ], q_done;     // S-CTA: Q in tensor memory; the tile's last S is done
   // per softmax warpgroup, so that whoever waits on one waits on every phase of it (parities repeat):
   uint64_t s_full[NS], s_free[NS]; // S-CTA: S written; S read
   uint64_t m_set[NS][4];           // S-CTA: the block's reference maxima of a warp's heads are set
@@ -454,8 +460,7 @@ __global__ void __launch_bounds__(T, 1)
   if (tid == 0) {
     for (int k = 0; k < NVF; ++k) bar_init(&bs.full[k], 1);
     for (int k = 0; k < NV; ++k) bar_init(&bs.free[k], 1);
-    bar_init(&bs.q_top, 4 * NS);  // one arrival per softmax warp
-    bar_init(&bs.q_full, 4 * NS);
+    for (int k = 0; k < NQ; ++k) bar_init(&bs.q_full[k], 4);  // one arrival per warp that brings Q
     bar_init(&bs.q_done, NS);
     for (int k = 0; k < NS; ++k) {
       bar_init(&bs.s_full[k], 1);
@@ -511,56 +516,9 @@ __global__ void __launch_bounds__(T, 1)
       if (nblk == 0) continue;
       if (warp < 4 * NS) {
         const int wg = warp >> 2;
-        // Q into tensor memory (warpgroup wg the columns [96 wg, 96 wg + 96)), column c holding the values of
-        // places 2c, 2c + 1 of a row, over a power of two that brings the head's largest to 2^14 .. 2^15.
-        ok = full == 0 || ready_or_wait(&bs.q_done, 1, full - 1, abort);
-        const int use = use0 + (head >> 6);
-        ok = ok && ready_or_wait(bs.full, NK, use, abort);
-        ok = __all_sync(0xffffffffu, ok);
-        tc_after();
-        const uint8_t* src = base + S_RING + (use % NK) * BLOCK + (head & 63) * 128;
-        uint32_t top = 0;
+        ok = __all_sync(0xffffffffu, ready_or_wait(bs.q_full, NQ, full, abort));
         if (!ok) break;
-#pragma unroll 1
-        for (int bx = 3 * wg; bx < 3 * wg + 3; ++bx)
-#pragma unroll
-          for (int c = 0; c < 8; ++c) top = max_bf16x2(top, *reinterpret_cast<const uint4*>(src + bx * ATOM + ((c ^ (head & 7)) << 4)));
-        uint16_t* tops = reinterpret_cast<uint16_t*>(base + S_QTOP) + head;
-        tops[MH * wg] = (uint16_t)max(top & 0xFFFFu, top >> 16);
-        __syncwarp();
-        if (lane == 0) bar_arrive(&bs.q_top);
-        ok = __all_sync(0xffffffffu, ready_or_wait(&bs.q_top, 1, full, abort));
-        if (!ok) break;
-        top = max(max((uint32_t)tops[0], (uint32_t)tops[MH]), (uint32_t)tops[2 * MH]);
-        const int down = top == 0 ? 127 : min(127 + 14 + 127 - (int)(top >> 7), 253);  // biased
-        const float mul = __uint_as_float((uint32_t)down << 23), up = __uint_as_float((uint32_t)(254 - down) << 23);
-        const uint32_t sign = a.sm_scale < 0.f ? 0x80008000u : 0u;  // so that scores scale by a positive factor
-#pragma unroll 1
-        for (int h = 6 * wg; h < 6 * wg + 6; ++h) {  // 32 values: 16 columns
-          uint32_t x[16], y[16];
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-            *reinterpret_cast<uint4*>(x + 4 * u) =
-                *reinterpret_cast<const uint4*>(src + (h >> 1) * ATOM + ((((h & 1) * 4 + u) ^ (head & 7)) << 4));
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              const uint32_t v = x[4 * u + j];
-              const __half2 f = __floats2half2_rn(__uint_as_float(v << 16) * mul, __uint_as_float(v & 0xFFFF0000u) * mul);
-              y[4 * j + u] = *reinterpret_cast<const uint32_t*>(&f) ^ sign;
-            }
-          asm volatile(
-              "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
-                  tbase + lane_off + Q_COL + 16 * h),
-              "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]), "r"(y[4]), "r"(y[5]), "r"(y[6]), "r"(y[7]), "r"(y[8]), "r"(y[9]),
-              "r"(y[10]), "r"(y[11]), "r"(y[12]), "r"(y[13]), "r"(y[14]), "r"(y[15])
-              : "memory");
-        }
-        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-        tc_before();
-        __syncwarp();
-        if (lane == 0) bar_arrive(&bs.q_full);
+        const float up = reinterpret_cast<const float*>(base + S_UP)[full % NQ * MH + head];
         // Warpgroup wg takes the blocks whose number g = done + b has g % NS = wg, a query head per
         // thread. From one block to the next only the reference maximum goes over, from warp to warp
         // (the warps of the same heads): it is known once a block's scores have been read, so the
@@ -662,54 +620,16 @@ __global__ void __launch_bounds__(T, 1)
           st_async_f32(fin + wg * FIN_WG + 4 * (MH + head), m_own, bar);
           if (last) st_async_f32(fin + NS * FIN_WG + 4 * head, sl2, bar);
         }
-      } else if (warp < ISSUER + NS) {
-        // (tensor memory starts at 0: all of it is allocated here)
-        const int wg = warp - ISSUER;
-        const bool one = elected();
+      } else {
         const uint64_t k0 = mdesc(smem_u32(base + S_RING), 16, 1024);
-        bool go = __all_sync(0xffffffffu, ready_or_wait(&bs.q_full, 1, full, abort));
-        if (go && one && wg == 0) {  // Q has left its slots
-          bar_arrive(&bs.free[use0 % NK]);
-          bar_arrive(&bs.free[(use0 + 1) % NK]);
-        }
-        tc_after();
-        int b = wg - done % NS;
-        if (b < 0) b += NS;
-        if (go && one && b >= nblk) bar_arrive(&bs.q_done);  // nothing of this unit
-        int turn = (done + b) / NS;  // of this buffer
-#pragma unroll 1
-        for (; go && b < nblk; b += NS, ++turn) {
-          const int use = use0 + 2 + b;
-          go = ready_or_wait(bs.full, NK, use, abort);
-          go = go && (turn == 0 || ready_or_wait(&bs.s_free[wg], 1, turn - 1, abort));
-          go = __all_sync(0xffffffffu, go);
-          if (!go) break;
-          tc_after();
-          const uint64_t dk0 = k0 + (uint64_t)((use % NK) * (BLOCK >> 4));
-          const uint32_t d = S_COL + BJ * wg;
-          if (one) {
-#pragma unroll
-            for (int kk = 0; kk < QATOMS * 4; ++kk)
-              mma_ta(d, Q_COL + 8 * kk, dk0 + (uint64_t)(((kk >> 2) * ATOM + (kk & 3) * 32) >> 4), kIdescQK, kk > 0);
-            commit(&bs.s_full[wg]);
-            commit(&bs.free[use % NK]);
-            if (b + NS >= nblk) commit(&bs.q_done);
-            ctl.issued[wg] = turn + 1;
-          }
-          __syncwarp();
-        }
-        ok = go;
-      } else if (warp == COPIER) {
-#pragma unroll 1
-        for (int i = 0; lane == 0 && ok && i < 2 + nblk; ++i) {
+        const auto copy = [&](int i) {  // one thread: half of Q (64 rows, in boxes of 64 values), or a block
           const int use = use0 + i;
-          ok = use < NK || ready_or_wait(bs.free, NK, use - NK, abort);
-          if (!ok) break;
+          if (use >= NK && !ready_or_wait(bs.free, NK, use - NK, abort)) return false;
           uint64_t* bar = &bs.full[use % NK];
           const uint32_t dst = smem_u32(base + S_RING + (use % NK) * BLOCK);
           bar_arrive_tx(bar, BLOCK);
           ctl.requested = use + 1;
-          if (i < 2) {  // half of Q: 64 rows, in boxes of 64 values
+          if (i < 2) {
             for (int bx = 0; bx < QATOMS; ++bx)
               asm volatile(
                   "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
@@ -721,8 +641,111 @@ __global__ void __launch_bounds__(T, 1)
                          "l"(w.kv + (size_t)(un.kv + i - 2) * BLOCK), "r"(BLOCK), "r"(smem_u32(bar))
                          : "memory");
           }
+          return true;
+        };
+        bool go = true;
+        if (warp == COPIER) {  // Q and the first block, as far as the ring goes before Q has left it
+          for (int i = 0; lane == 0 && go && i < NK; ++i) go = copy(i);
+          go = __shfl_sync(0xffffffffu, (int)go, 0) != 0;
         }
-        ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+        // Q into tensor memory, a head per thread, column c holding the values of places 2c, 2c + 1 of a row, over a power
+        // of two that brings the head's largest to 2^14 .. 2^15 where it is below 1 or above 65504. The tile before may still
+        // be in the softmax: it needs its S only, all of which is done.
+        go = go && (full == 0 || ready_or_wait(&bs.q_done, 1, full - 1, abort));
+        const int q_use = use0 + (head >> 6);
+        go = go && ready_or_wait(bs.full, NK, q_use, abort);
+        go = __all_sync(0xffffffffu, go);
+        if (go) {
+          tc_after();
+          const uint8_t* src = base + S_RING + (q_use % NK) * BLOCK + (head & 63) * 128;
+          // It is taken as it is first, and once more where some head's values want a divisor.
+          const auto take = [&](auto scaled, float mul) {  // the largest magnitude in f16
+            constexpr bool kScaled = decltype(scaled)::value;
+            __half2 top = __float2half2_rn(0.f);
+#pragma unroll 3
+            for (int h = 0; h < 2 * QATOMS; ++h) {  // 32 values: 16 columns
+              uint32_t x[16], y[16];
+#pragma unroll
+              for (int u = 0; u < 4; ++u)
+                *reinterpret_cast<uint4*>(x + 4 * u) =
+                    *reinterpret_cast<const uint4*>(src + (h >> 1) * ATOM + ((((h & 1) * 4 + u) ^ (head & 7)) << 4));
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                  const float lo = __uint_as_float(x[4 * u + j] << 16), hi = __uint_as_float(x[4 * u + j] & 0xFFFF0000u);
+                  const __half2 f = kScaled ? __floats2half2_rn(lo * mul, hi * mul) : __floats2half2_rn(lo, hi);
+                  if (!kScaled) top = __hmax2(top, __habs2(f));
+                  y[4 * j + u] = *reinterpret_cast<const uint32_t*>(&f);
+                }
+              asm volatile(
+                  "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+                      tbase + lane_off + Q_COL + 16 * h),
+                  "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]), "r"(y[4]), "r"(y[5]), "r"(y[6]), "r"(y[7]), "r"(y[8]), "r"(y[9]),
+                  "r"(y[10]), "r"(y[11]), "r"(y[12]), "r"(y[13]), "r"(y[14]), "r"(y[15])
+                  : "memory");
+            }
+            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+            return fmaxf(__low2float(top), __high2float(top));
+          };
+          float up = 1.f;
+          const float largest = take(std::false_type{}, 1.f);
+          if (__any_sync(0xffffffffu, !(largest >= 1.f && largest < 65504.f)) || a.sm_scale < 0.f) {
+            uint32_t top = 0;
+#pragma unroll 1
+            for (int c = 0; c < 8 * QATOMS; ++c) top = max_bf16x2(top, *reinterpret_cast<const uint4*>(src + (c >> 3) * ATOM + ((c & 7) << 4)));
+            top = max(top & 0xFFFFu, top >> 16);
+            const int down = top == 0 ? 127 : min(127 + 14 + 127 - (int)(top >> 7), 253);  // biased
+            const float mul = __uint_as_float((uint32_t)down << 23);
+            up = __uint_as_float((uint32_t)(254 - down) << 23);
+            take(std::true_type{}, a.sm_scale < 0.f ? -mul : mul);  // (negative, so that scores scale by a positive factor)
+          }
+          reinterpret_cast<float*>(base + S_UP)[full % NQ * MH + head] = up;
+          tc_before();
+          __syncwarp();
+          if (lane == 0) bar_arrive(&bs.q_full[full % NQ]);
+        }
+        if (warp == COPIER) {
+#pragma unroll 1
+          for (int i = NK; lane == 0 && go && i < 2 + nblk; ++i) go = copy(i);
+          go = __shfl_sync(0xffffffffu, (int)go, 0) != 0;
+        } else {
+          // (tensor memory starts at 0: all of it is allocated here)
+          const int wg = warp - ISSUER;
+          const bool one = elected();
+          go = __all_sync(0xffffffffu, go && ready_or_wait(bs.q_full, NQ, full, abort));
+          if (go && one && wg == 0) {  // Q has left its slots
+            bar_arrive(&bs.free[use0 % NK]);
+            bar_arrive(&bs.free[(use0 + 1) % NK]);
+          }
+          tc_after();
+          int b = wg - done % NS;
+          if (b < 0) b += NS;
+          if (go && one && b >= nblk) bar_arrive(&bs.q_done);  // nothing of this unit
+          int turn = (done + b) / NS;  // of this buffer
+#pragma unroll 1
+          for (; go && b < nblk; b += NS, ++turn) {
+            const int use = use0 + 2 + b;
+            go = ready_or_wait(bs.full, NK, use, abort);
+            go = go && (turn == 0 || ready_or_wait(&bs.s_free[wg], 1, turn - 1, abort));
+            go = __all_sync(0xffffffffu, go);
+            if (!go) break;
+            tc_after();
+            const uint64_t dk0 = k0 + (uint64_t)((use % NK) * (BLOCK >> 4));
+            const uint32_t d = S_COL + BJ * wg;
+            if (one) {
+#pragma unroll
+              for (int kk = 0; kk < QATOMS * 4; ++kk)
+                mma_ta(d, Q_COL + 8 * kk, dk0 + (uint64_t)(((kk >> 2) * ATOM + (kk & 3) * 32) >> 4), kIdescQK, kk > 0);
+              commit(&bs.s_full[wg]);
+              commit(&bs.free[use % NK]);
+              if (b + NS >= nblk) commit(&bs.q_done);
+              ctl.issued[wg] = turn + 1;
+            }
+            __syncwarp();
+          }
+        }
+        ok = go;
       }
     } else {
       // ================================ O-CTA ================================
