@@ -61,12 +61,12 @@ constexpr int NK = 3, NV = 5;  // slots of the S-CTA's ring (a block, or half of
 constexpr int NVF = 2 * NV;
 constexpr uint32_t TMEM_COLS = 512, Q_COL = 0, S_COL = 288;
 static_assert(S_COL + NS * BJ <= TMEM_COLS, "Q and the S buffers fit tensor memory");
-// S-CTA warps: 0-11 softmax, 12-14 issuers, 15 copies, and 12-15 bring Q; O-CTA: 0-3 corrector, which reads out with 4-11,
-// 12 and 13 issuers, 15 copies.
+// S-CTA warps: 0-11 softmax, 12-14 issuers, 15 copies, and 12-15 bring Q; O-CTA: 0-3 corrector, 4-11 read out, 12 and 13
+// issuers, 15 copies.
 // S has an issuer per buffer: a commit takes its thread some 500 clocks with a block's MMAs before it, and the waits for
 // the next block 300 more, in which another thread's MMAs keep the tensor core busy (one issuer for all of S: 2,050 clocks
 // a block, of which its 36 MMAs are 1,150).
-constexpr int ISSUER = 12, COPIER = 15, NOUT = 3;  // NOUT warps read out a quarter of the heads
+constexpr int ISSUER = 12, COPIER = 15, OUT = 4, NOUT = 2;  // NOUT warps read out a quarter of the heads
 
 constexpr uint32_t ATOM = BJ * 128, BLOCK = QATOMS * ATOM, HALF_V = ATOMS / 2 * ATOM;
 constexpr uint32_t S_RING = 0;
@@ -382,7 +382,7 @@ struct Barriers {
   uint64_t p_full[NS];             // O-CTA, completed by the S-CTA's stores
   uint64_t pv_go[NS];              // O-CTA: O is ready for P . V of the block
   uint64_t fin[NF];                // O-CTA: the S-CTA's totals of a tile are here
-  uint64_t o_full, o_free;         // O-CTA: a tile's last P . V is done; O has been read out
+  uint64_t o_full, o_free[2];      // O-CTA: a tile's last P . V is done; a half of O has been read
 };
 static_assert(NK <= NV, "the rings' barriers");
 
@@ -472,7 +472,7 @@ __global__ void __launch_bounds__(T, 1)
     }
     for (int k = 0; k < NF; ++k) bar_init(&bs.fin[k], 1);  // the same
     bar_init(&bs.o_full, 2);
-    bar_init(&bs.o_free, 4 * NOUT);
+    for (int k = 0; k < 2; ++k) bar_init(&bs.o_free[k], 4 * NOUT);
     ctl.abort = 0;
     for (int k = 0; k < NS; ++k) ctl.issued[k] = 0;
     ctl.requested = 0;
@@ -786,7 +786,7 @@ __global__ void __launch_bounds__(T, 1)
         for (int b = 0; ok && b < nblk; ++b) {
           const int g = done + b, use = 2 * g + nh;
           bool go = ready_or_wait(bs.pv_go, NS, g, abort);
-          if (b == 0) go = go && (full == 0 || ready_or_wait(&bs.o_free, 1, full - 1, abort));
+          if (b == 0) go = go && (full == 0 || ready_or_wait(&bs.o_free[nh], 1, full - 1, abort));
           go = go && ready_or_wait(bs.full, NVF, use, abort);
           ok = __all_sync(0xffffffffu, go);
           if (!ok) break;
@@ -821,18 +821,19 @@ __global__ void __launch_bounds__(T, 1)
         }
         ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
       }
-      if (warp < 4 * NOUT) {
-        // The read-out. Warps w, w + 4 and w + 8 have a quarter of the heads, as tensor memory has it, and every
-        // third 32 columns. The columns are ordered so that a lane's fragments are eight consecutive dims of each of
+      if (warp < ISSUER) {
+        // The read-out. Warps w and w + 4 have a quarter of the heads, as tensor memory has it, and every
+        // second 32 columns. The columns are ordered so that a lane's fragments are eight consecutive dims of each of
         // four rows, and four lanes have 32 dims of a row. The warps that have nothing else to do wait at a barrier of
-        // the hardware, not at the mbarriers.
-        ok = sync_and(ok, 32 * 4 * NOUT);
+        // the hardware, not at the mbarriers; the corrector meets them there and goes on to the next tile.
+        ok = sync_and(ok, 32 * ISSUER);
         if (!ok) break;  // (all of them: one that gave up further down comes here once more)
-        const int set = warp >> 2;
+        if (warp < OUT) continue;
+        const int set = (warp - OUT) >> 2;
         float l = 0.f, m = -INFINITY, sl2 = 0.f;
         if (nblk > 0) {
           const int k = full % NF;
-          if (tid == 0) bar_arrive_tx(&bs.fin[k], min(nblk, NS) * FIN_WG + MH * 4);
+          if (tid == 32 * OUT) bar_arrive_tx(&bs.fin[k], min(nblk, NS) * FIN_WG + MH * 4);
           ok = ready_or_wait<true>(bs.fin, NF, full, abort) && ready_or_wait(&bs.o_full, 1, full, abort);
           ok = __all_sync(0xffffffffu, ok);
           tc_after();
@@ -851,39 +852,49 @@ __global__ void __launch_bounds__(T, 1)
         const int row = (warp & 3) * 32 + (lane >> 2);  // and 8, 16, 24 after it
         const size_t at = (out0 + row) * DL + 8 * (lane & 3);
 #pragma unroll 1
-        for (int c = 32 * set; ok && c < DL; c += 32 * NOUT) {
-          float v[2][16] = {};
-          if (nblk > 0) tmem_ld_frag(tbase + lane_off + c, v);
+        for (int i = set; ok && i < DL / 32; i += 2 * NOUT) {  // two of the set's 32 columns at a time
+          float v[2][2][16] = {};
+          const bool two = i + NOUT < DL / 32;
+          if (nblk > 0) {
+            tmem_ld_frag(tbase + lane_off + 32 * i, v[0]);
+            if (two) tmem_ld_frag(tbase + lane_off + 32 * (i + NOUT), v[1]);
+            asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+            // the columns below 256, or all, are in registers
+            tc_before();
+            __syncwarp();
+            if (lane == 0 && i < DL / 64 && i + 2 * NOUT >= DL / 64) bar_arrive(&bs.o_free[0]);
+            if (lane == 0 && i + 2 * NOUT >= DL / 32) bar_arrive(&bs.o_free[1]);
+          }
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {  // rows 8 k after the first
-            const float f = __shfl_sync(0xffffffffu, inv, 8 * k + (lane >> 2));
-            uint32_t x[8];
+          for (int e = 0; e < 2; ++e) {
+            const int c = 32 * (i + e * NOUT);
+            if (e == 1 && !two) break;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = __float_as_uint(v[k >> 1][4 * (i >> 1) + 2 * (k & 1) + (i & 1)] * f);
-            if (row + 8 * k >= un.live) {  // no query head
-            } else if (un.whole) {
-              uint32_t h[4];
+            for (int k = 0; k < 4; ++k) {  // rows 8 k after the first
+              const float f = __shfl_sync(0xffffffffu, inv, 8 * k + (lane >> 2));
+              uint32_t x[8];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const __nv_bfloat162 y = __floats2bfloat162_rn(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
-                h[i] = *reinterpret_cast<const uint32_t*>(&y);
+              for (int q = 0; q < 8; ++q) x[q] = __float_as_uint(v[e][k >> 1][4 * (q >> 1) + 2 * (k & 1) + (q & 1)] * f);
+              if (row + 8 * k >= un.live) {  // no query head
+              } else if (un.whole) {
+                uint32_t h[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  const __nv_bfloat162 y = __floats2bfloat162_rn(__uint_as_float(x[2 * q]), __uint_as_float(x[2 * q + 1]));
+                  h[q] = *reinterpret_cast<const uint32_t*>(&y);
+                }
+                *reinterpret_cast<uint4*>(a.o + at + 8 * k * DL + c) = make_uint4(h[0], h[1], h[2], h[3]);
+              } else {
+                store8(reinterpret_cast<uint32_t*>(w.part_o + at + 8 * k * DL + c), x, true);
               }
-              *reinterpret_cast<uint4*>(a.o + at + 8 * k * DL + c) = make_uint4(h[0], h[1], h[2], h[3]);
-            } else {
-              store8(reinterpret_cast<uint32_t*>(w.part_o + at + 8 * k * DL + c), x, true);
             }
           }
-          __syncwarp();
         }
         if (ok && set == 0 && head < un.live)
           (un.whole ? a.lse : w.part_lse)[out0 + head] = l == 0.f ? -INFINITY : (m * sl2 + (log2f(l) - kRefLog2)) * 0.6931471805599453f;
         __syncwarp();
-        if (ok && nblk > 0) {
-          tc_before();
-          if (lane == 0) bar_arrive(&bs.o_free);
-        }
       }
-      if (!ok && warp >= 4 * NOUT) break;
+      if (!ok && warp >= ISSUER) break;
     }
     if (!ok && rank == 0) break;
   }

@@ -889,7 +889,10 @@ __global__ void __launch_bounds__(T, 1)
 #pragma unroll 1
         for (int c = 32 * set; ok && c < DL; c += 32 * NOUT) {
           float v[2][16] = {};
-          if (nblk > 0) tmem_ld_frag(tbase + lane_off + c, v);
+          if (nblk > 0) {
+            tmem_ld_frag(tbase + lane_off + c, v);
+            asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+          }
 #pragma unroll
           for (int k = 0; k < 4; ++k) {  // rows 8 k after the first
             const float f = __shfl_sync(0xffffffffu, inv, 8 * k + (lane >> 2));

@@ -273,7 +273,7 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 // 32 accumulator columns of 32 rows, spread over the warp as matrix fragments are: v[h][4 j + 2 s + e]
-// is row 16 h + 8 s + lane / 4, column 8 j + 2 (lane % 4) + e.
+// is row 16 h + 8 s + lane / 4, column 8 j + 2 (lane % 4) + e. The caller waits for the loads.
 __device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, float (&v)[2][16]) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -284,7 +284,6 @@ __device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, float (&v)[2][16]) 
           "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(taddr + ((uint32_t)(16 * h) << 16)));
   }
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 // 32 consecutive bytes of a lane: one store (a whole sector) where they are aligned.
 __device__ __forceinline__ void store8(uint32_t* dst, const uint32_t (&w)[8], bool aligned) {
