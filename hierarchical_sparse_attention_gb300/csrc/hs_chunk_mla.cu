@@ -54,8 +54,9 @@ constexpr int MH = 128;  // MMA M: query heads of a tile (what is there of the n
 constexpr int BJ = 64;   // rows per block
 constexpr int DQK = kFp8Dims, DL = kFp8Latent;
 constexpr int QATOMS = DQK / 64, ATOMS = DL / 64;  // swizzle atoms of 64 values in a block of K and of V
-constexpr int NS = 3;    // S buffers, softmax warpgroups and P buffers: a block each in turn
-constexpr int NK = 3, NV = 5;  // slots of the S-CTA's ring (a block, or half of Q) and of the O-CTA's (half of V's block)
+constexpr int NS = 3;    // S buffers and softmax warpgroups: a block each in turn
+constexpr int NP = 4;    // P buffers
+constexpr int NK = 3, NV = 4;  // slots of the S-CTA's ring (a block, or half of Q) and of the O-CTA's (half of V's block)
 // Barriers of V's slots: two to a slot in turn, as a use of an odd slot count is the other half's use before, whose issuer
 // waits on the other barrier: so each issuer waits on every phase of its own.
 constexpr int NVF = 2 * NV;
@@ -81,10 +82,10 @@ constexpr uint32_t O_RING = 0;
 constexpr uint32_t O_P = NV * HALF_V;
 constexpr uint32_t P_BUF = MH * BJ * 2, P_BYTES = P_BUF + MH * 4;  // P and the rescale factors of a block
 constexpr uint32_t FIN_WG = 2 * MH * 4;            // a softmax warpgroup's sums and references of a tile
-constexpr uint32_t O_ALPHA = O_P + NS * P_BUF;
-constexpr int NF = NS + 1;  // tiles whose totals are kept: P's buffers let the S-CTA be three tiles ahead, of one block each
+constexpr uint32_t O_ALPHA = O_P + NP * P_BUF;
+constexpr int NF = NP + 1;  // tiles whose totals are kept: P's buffers let the S-CTA be four tiles ahead, of one block each
 constexpr uint32_t FIN = NS * FIN_WG + MH * 4;     // of a tile: the warpgroups', and what a unit of a score is
-constexpr uint32_t O_FIN = O_ALPHA + NS * MH * 4;
+constexpr uint32_t O_FIN = O_ALPHA + NP * MH * 4;
 constexpr uint32_t O_END = O_FIN + NF * FIN;
 constexpr uint32_t SMEM_BYTES = S_END > O_END ? S_END : O_END;
 constexpr uint32_t STATIC_BYTES = 1024;  // barriers and flags, one block of a tile's alignment
@@ -377,14 +378,15 @@ struct Barriers {
   uint64_t q_full[NQ], q_done;     // S-CTA: Q in tensor memory; the tile's last S is done
   // per softmax warpgroup, so that whoever waits on one waits on every phase of it (parities repeat):
   uint64_t s_full[NS], s_free[NS]; // S-CTA: S written; S read
+  uint64_t s_next[NS];             // S-CTA: the block's MMAs have been issued
   uint64_t m_set[NS][4];           // S-CTA: the block's reference maxima of a warp's heads are set
-  uint64_t p_free[NS];             // both, arrived by the O-CTA's issuers: P . V of the block is done
-  uint64_t p_full[NS];             // O-CTA, completed by the S-CTA's stores
-  uint64_t pv_go[NS];              // O-CTA: O is ready for P . V of the block
+  uint64_t p_free[NP];             // both, arrived by the O-CTA's issuers: P . V of the block is done
+  uint64_t p_full[NP];             // O-CTA, completed by the S-CTA's stores
+  uint64_t pv_go[NP];              // O-CTA: O is ready for P . V of the block
   uint64_t fin[NF];                // O-CTA: the S-CTA's totals of a tile are here
   uint64_t o_full, o_free[2];      // O-CTA: a tile's last P . V is done; a half of O has been read
 };
-static_assert(NK <= NV, "the rings' barriers");
+static_assert(NK <= NV && NP == NS + 1, "the rings' barriers; softmax's waits for P's buffers");
 
 struct __align__(STATIC_BYTES) Control {
   Barriers bs;
@@ -464,8 +466,11 @@ __global__ void __launch_bounds__(T, 1)
     bar_init(&bs.q_done, NS);
     for (int k = 0; k < NS; ++k) {
       bar_init(&bs.s_full[k], 1);
+      bar_init(&bs.s_next[k], 1);
       bar_init(&bs.s_free[k], 4);  // the warps of the block's softmax warpgroup
       for (int x = 0; x < 4; ++x) bar_init(&bs.m_set[k][x], 1);
+    }
+    for (int k = 0; k < NP; ++k) {
       bar_init(&bs.p_free[k], 2);
       bar_init(&bs.p_full[k], 1);  // the O-CTA's expect_tx; the S-CTA's stores complete it
       bar_init(&bs.pv_go[k], 4);
@@ -478,7 +483,7 @@ __global__ void __launch_bounds__(T, 1)
     ctl.requested = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     if (rank == 1)
-      for (int k = 0; k < NS; ++k) bar_arrive_tx(&bs.p_full[k], P_BYTES);
+      for (int k = 0; k < NP; ++k) bar_arrive_tx(&bs.p_full[k], P_BYTES);
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&ctl.taddr)),
@@ -528,8 +533,8 @@ __global__ void __launch_bounds__(T, 1)
         // is rounded by whole units from 2^24 on.
         float m_own = -INFINITY, l_own = 0.f;  // the sum of this thread's blocks, under this reference
         float* s_ref = reinterpret_cast<float*>(base + S_REF);
-        const uint32_t pbuf = remote(base + O_P + wg * P_BUF + 16 * head, partner);  // (block g's buffer is g % NS = wg)
-        const uint32_t r_alpha = remote(base + O_ALPHA + 4 * (wg * MH + head), partner), rbar = remote(&bs.p_full[wg], partner);
+        const uint32_t pbuf0 = remote(base + O_P + 16 * head, partner);
+        const uint32_t alpha0 = remote(base + O_ALPHA + 4 * head, partner), rbar0 = remote(&bs.p_full[0], partner);
         // what a unit of S is; a scale of zero stays above it, so that -inf stays -inf
         const float sl2 = fminf(fmaxf(score_log2(a) * up, 1e-37f), 3e38f);
         const uint32_t s_at = tbase + lane_off + S_COL + BJ * wg;
@@ -591,10 +596,12 @@ __global__ void __launch_bounds__(T, 1)
           const float ref = m_new == -INFINITY ? 0.f : m_new;  // a NaN score stays one, an unseen row's weight is 0
           l_own *= m_new == -INFINITY ? 1.f : ex2((m_own - m_new) * sl2);
           m_own = m_new;
-          // the O-CTA's P buffer is free once P . V of block g - 3 is done
-          ok = __all_sync(0xffffffffu, g < NS || ready_or_wait<true>(bs.p_free, NS, g - NS, abort));
+          // the O-CTA's P buffer is free once P . V of block g - NP is done (that of g - 2 NP is known to be: the warpgroup
+          // of block g - NP = g - 1 - NS has waited for it and was then at block g - 1, whose m_set has been seen)
+          ok = __all_sync(0xffffffffu, g < NP || ready_or_wait<true>(bs.p_free, NP, g - NP, abort));
           if (!ok) break;
-          st_async_f32(r_alpha, alpha, rbar);
+          const uint32_t pbuf = pbuf0 + (g % NP) * P_BUF, rbar = rbar0 + (g % NP) * 8;
+          st_async_f32(alpha0 + (g % NP) * (MH * 4), alpha, rbar);
           float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
           for (int q = 0; q < BJ / 8; ++q) {  // 16-B chunks of 8 f16
@@ -728,6 +735,9 @@ __global__ void __launch_bounds__(T, 1)
             const int use = use0 + 2 + b;
             go = ready_or_wait(bs.full, NK, use, abort);
             go = go && (turn == 0 || ready_or_wait(&bs.s_free[wg], 1, turn - 1, abort));
+            // blocks in their order: issued side by side, two would take as long as both and leave their slots together
+            const int before = done + b - 1;
+            go = go && (before < 0 || ready_or_wait(bs.s_next, NS, before, abort));
             go = __all_sync(0xffffffffu, go);
             if (!go) break;
             tc_after();
@@ -737,6 +747,7 @@ __global__ void __launch_bounds__(T, 1)
 #pragma unroll
               for (int kk = 0; kk < QATOMS * 4; ++kk)
                 mma_ta(d, Q_COL + 8 * kk, dk0 + (uint64_t)(((kk >> 2) * ATOM + (kk & 3) * 32) >> 4), kIdescQK, kk > 0);
+              bar_arrive(&bs.s_next[wg]);
               commit(&bs.s_full[wg]);
               commit(&bs.free[use % NK]);
               if (b + NS >= nblk) commit(&bs.q_done);
@@ -756,13 +767,13 @@ __global__ void __launch_bounds__(T, 1)
 #pragma unroll 1
         for (int b = 0; ok && b < nblk; ++b) {
           const int g = done + b;
-          ok = __all_sync(0xffffffffu, ready_or_wait<true>(bs.p_full, NS, g, abort));
+          ok = __all_sync(0xffffffffu, ready_or_wait<true>(bs.p_full, NP, g, abort));
           if (!ok) break;
-          const float f = alpha_buf[g % NS * MH + head];
-          // this buffer's next phase is block g + 3: its bytes come only after P . V of block g
-          if (tid == 0) bar_arrive_tx(&bs.p_full[g % NS], P_BYTES);
+          const float f = alpha_buf[g % NP * MH + head];
+          // this buffer's next phase is block g + NP: its bytes come only after P . V of block g
+          if (tid == 0) bar_arrive_tx(&bs.p_full[g % NP], P_BYTES);
           if (__any_sync(0xffffffffu, b > 0 && f != 1.f)) {
-            ok = __all_sync(0xffffffffu, ready_or_wait(bs.p_free, NS, g - 1, abort));
+            ok = __all_sync(0xffffffffu, ready_or_wait(bs.p_free, NP, g - 1, abort));
             if (!ok) break;
             tc_after();
 #pragma unroll 1
@@ -776,7 +787,7 @@ __global__ void __launch_bounds__(T, 1)
             tc_before();
           }
           __syncwarp();
-          if (lane == 0) bar_arrive(&bs.pv_go[g % NS]);
+          if (lane == 0) bar_arrive(&bs.pv_go[g % NP]);
         }
       } else if (warp == ISSUER || warp == ISSUER + 1) {
         const int nh = warp - ISSUER;  // this issuer's 256 columns
@@ -785,21 +796,21 @@ __global__ void __launch_bounds__(T, 1)
 #pragma unroll 1
         for (int b = 0; ok && b < nblk; ++b) {
           const int g = done + b, use = 2 * g + nh;
-          bool go = ready_or_wait(bs.pv_go, NS, g, abort);
+          bool go = ready_or_wait(bs.pv_go, NP, g, abort);
           if (b == 0) go = go && (full == 0 || ready_or_wait(&bs.o_free[nh], 1, full - 1, abort));
           go = go && ready_or_wait(bs.full, NVF, use, abort);
           ok = __all_sync(0xffffffffu, go);
           if (!ok) break;
           tc_after();
           fence_async_smem();  // P's writes, seen through their barrier, before the tensor core's reads
-          const uint64_t dp0 = p0 + (uint64_t)((g % NS) * (P_BUF >> 4)), dv0 = v0 + (uint64_t)((use % NV) * (HALF_V >> 4));
+          const uint64_t dp0 = p0 + (uint64_t)((g % NP) * (P_BUF >> 4)), dv0 = v0 + (uint64_t)((use % NV) * (HALF_V >> 4));
           if (one) {
 #pragma unroll
             for (int kk = 0; kk < BJ / 16; ++kk)
               mma_ss(256 * nh, dp0 + (uint64_t)((kk * 2 * MH * 16) >> 4), dv0 + (uint64_t)((kk * 2048) >> 4), kIdescPV,
                      (b > 0 || kk > 0) ? 1u : 0u);
             commit(&bs.free[use % NV]);
-            commit_multicast(&bs.p_free[g % NS], (uint16_t)3);
+            commit_multicast(&bs.p_free[g % NP], (uint16_t)3);
             if (b == nblk - 1) commit(&bs.o_full);
             ctl.issued[nh] = g + 1;
           }
@@ -905,10 +916,10 @@ __global__ void __launch_bounds__(T, 1)
     if (rank == 0) {
       for (int k = max(done + 2 * full - NK, 0); k < done + 2 * full; ++k) ok = ok && pipe_wait(bs.free, NK, k, abort);
       ok = ok && pipe_wait(&bs.q_done, 1, full - 1, abort);
-      for (int b = done >= NS ? done - NS : 0; b < done; ++b) ok = ok && pipe_wait<true>(bs.p_free, NS, b, abort);
+      for (int b = done >= NP ? done - NP : 0; b < done; ++b) ok = ok && pipe_wait<true>(bs.p_free, NP, b, abort);
     } else {
       ok = pipe_wait(bs.free, NV, 2 * done - 2, abort) && pipe_wait(bs.free, NV, 2 * done - 1, abort) &&
-           pipe_wait(bs.p_free, NS, done - 1, abort);
+           pipe_wait(bs.p_free, NP, done - 1, abort);
     }
   }
   ok = __syncthreads_and(ok && !*abort);
