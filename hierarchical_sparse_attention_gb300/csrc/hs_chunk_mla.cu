@@ -71,6 +71,10 @@ constexpr int ISSUER = 12, COPIER = 15, OUT = 4, NOUT = 2;  // NOUT warps read o
 
 constexpr uint32_t ATOM = BJ * 128, BLOCK = QATOMS * ATOM, HALF_V = ATOMS / 2 * ATOM;
 constexpr uint32_t S_RING = 0;
+// A slot of K is filled and handed back in two parts (values 0 - 319, and the rest), so that the next block's copies start while
+// the tensor core is at the second: three slots cover a copy's way (measured, clocks: 860 from a commit to the copy's
+// start, 1,680 to its end) and a block's MMAs (1,150) only so.
+constexpr uint32_t PART = 5 * ATOM;
 constexpr uint32_t S_REF = NK * BLOCK;             // the reference maxima, handed from block to block
 constexpr uint32_t S_UP = S_REF + MH * 4;          // what a head's Q was divided by, of the last NQ tiles
 // A softmax warpgroup that is at a block may find S computed up to five blocks on (its next one and the two after that), and
@@ -374,7 +378,8 @@ static_assert(kRowsThreads / 32 * 3 == 32 + BJ / 16, "three tasks a warp");
 // ---------------------------------------------------------------- the attention
 
 struct Barriers {
-  uint64_t full[NVF], free[NV];    // a ring slot's bytes are there; it has been read
+  uint64_t k_full[2][NK], k_free[2][NK];  // S-CTA: each part of a ring slot: its bytes are there; it has been read
+  uint64_t v_full[NVF], v_free[NV];       // O-CTA: the same of a slot
   uint64_t q_full[NQ], q_done;     // S-CTA: Q in tensor memory; the tile's last S is done
   // per softmax warpgroup, so that whoever waits on one waits on every phase of it (parities repeat):
   uint64_t s_full[NS], s_free[NS]; // S-CTA: S written; S read
@@ -386,14 +391,16 @@ struct Barriers {
   uint64_t fin[NF];                // O-CTA: the S-CTA's totals of a tile are here
   uint64_t o_full, o_free[2];      // O-CTA: a tile's last P . V is done; a half of O has been read
 };
-static_assert(NK <= NV && NP == NS + 1, "the rings' barriers; softmax's waits for P's buffers");
+static_assert(NP == NS + 1, "softmax's waits for P's buffers");
 
 struct __align__(STATIC_BYTES) Control {
   Barriers bs;
   uint32_t taddr;
   int abort;
   int issued[NS];  // blocks whose MMAs each issuer started (the last commit to wait for)
-  int requested;  // ring slots whose copies were started
+  int uses[NS];    // S-CTA: the ring's use of the last one
+  int whole[NS];   // S-CTA: blocks whose MMAs it started all
+  int requested;   // ring slots (S-CTA: parts of them) whose copies were started
 };
 static_assert(sizeof(Control) == STATIC_BYTES, "one block");
 
@@ -460,8 +467,12 @@ __global__ void __launch_bounds__(T, 1)
   const int pair = blockIdx.x >> 1;
 
   if (tid == 0) {
-    for (int k = 0; k < NVF; ++k) bar_init(&bs.full[k], 1);
-    for (int k = 0; k < NV; ++k) bar_init(&bs.free[k], 1);
+    for (int k = 0; k < 2 * NK; ++k) {
+      bar_init(&bs.k_full[0][k], 1);
+      bar_init(&bs.k_free[0][k], 1);
+    }
+    for (int k = 0; k < NVF; ++k) bar_init(&bs.v_full[k], 1);
+    for (int k = 0; k < NV; ++k) bar_init(&bs.v_free[k], 1);
     for (int k = 0; k < NQ; ++k) bar_init(&bs.q_full[k], 4);  // one arrival per warp that brings Q
     bar_init(&bs.q_done, NS);
     for (int k = 0; k < NS; ++k) {
@@ -479,7 +490,7 @@ __global__ void __launch_bounds__(T, 1)
     bar_init(&bs.o_full, 2);
     for (int k = 0; k < 2; ++k) bar_init(&bs.o_free[k], 4 * NOUT);
     ctl.abort = 0;
-    for (int k = 0; k < NS; ++k) ctl.issued[k] = 0;
+    for (int k = 0; k < NS; ++k) ctl.issued[k] = ctl.uses[k] = ctl.whole[k] = 0;
     ctl.requested = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     if (rank == 1)
@@ -631,22 +642,26 @@ __global__ void __launch_bounds__(T, 1)
         const uint64_t k0 = mdesc(smem_u32(base + S_RING), 16, 1024);
         const auto copy = [&](int i) {  // one thread: half of Q (64 rows, in boxes of 64 values), or a block
           const int use = use0 + i;
-          if (use >= NK && !ready_or_wait(bs.free, NK, use - NK, abort)) return false;
-          uint64_t* bar = &bs.full[use % NK];
-          const uint32_t dst = smem_u32(base + S_RING + (use % NK) * BLOCK);
-          bar_arrive_tx(bar, BLOCK);
-          ctl.requested = use + 1;
-          if (i < 2) {
-            for (int bx = 0; bx < QATOMS; ++bx)
-              asm volatile(
-                  "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-                      dst + bx * ATOM),
-                  "l"(&tm_q), "r"(64 * bx), "r"((int)un.row0 + BJ * i), "r"(smem_u32(bar))
-                  : "memory");
-          } else {
-            asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-                         "l"(w.kv + (size_t)(un.kv + i - 2) * BLOCK), "r"(BLOCK), "r"(smem_u32(bar))
-                         : "memory");
+#pragma unroll 1
+          for (int part = 0; part < 2; ++part) {
+            if (use >= NK && !ready_or_wait(bs.k_free[part], NK, use - NK, abort)) return false;
+            uint64_t* bar = &bs.k_full[part][use % NK];
+            const uint32_t from = part ? PART : 0, size = part ? BLOCK - PART : PART;
+            const uint32_t dst = smem_u32(base + S_RING + (use % NK) * BLOCK) + from;
+            bar_arrive_tx(bar, size);
+            ctl.requested = 2 * use + part + 1;
+            if (i < 2) {
+              for (uint32_t at = 0; at < size; at += ATOM)
+                asm volatile(
+                    "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+                        dst + at),
+                    "l"(&tm_q), "r"((int)((from + at) / ATOM) * 64), "r"((int)un.row0 + BJ * i), "r"(smem_u32(bar))
+                    : "memory");
+            } else {
+              asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                           "l"(w.kv + (size_t)(un.kv + i - 2) * BLOCK + from), "r"(size), "r"(smem_u32(bar))
+                           : "memory");
+            }
           }
           return true;
         };
@@ -660,7 +675,7 @@ __global__ void __launch_bounds__(T, 1)
         // be in the softmax: it needs its S only, all of which is done.
         go = go && (full == 0 || ready_or_wait(&bs.q_done, 1, full - 1, abort));
         const int q_use = use0 + (head >> 6);
-        go = go && ready_or_wait(bs.full, NK, q_use, abort);
+        go = go && ready_or_wait(bs.k_full[0], NK, q_use, abort) && ready_or_wait(bs.k_full[1], NK, q_use, abort);
         go = __all_sync(0xffffffffu, go);
         if (go) {
           tc_after();
@@ -722,8 +737,7 @@ __global__ void __launch_bounds__(T, 1)
           const bool one = elected();
           go = __all_sync(0xffffffffu, go && ready_or_wait(bs.q_full, NQ, full, abort));
           if (go && one && wg == 0) {  // Q has left its slots
-            bar_arrive(&bs.free[use0 % NK]);
-            bar_arrive(&bs.free[(use0 + 1) % NK]);
+            for (int k = 0; k < 4; ++k) bar_arrive(&bs.k_free[k & 1][(use0 + (k >> 1)) % NK]);
           }
           tc_after();
           int b = wg - done % NS;
@@ -733,7 +747,7 @@ __global__ void __launch_bounds__(T, 1)
 #pragma unroll 1
           for (; go && b < nblk; b += NS, ++turn) {
             const int use = use0 + 2 + b;
-            go = ready_or_wait(bs.full, NK, use, abort);
+            go = ready_or_wait(bs.k_full[0], NK, use, abort);
             go = go && (turn == 0 || ready_or_wait(&bs.s_free[wg], 1, turn - 1, abort));
             // blocks in their order: issued side by side, two would take as long as both and leave their slots together
             const int before = done + b - 1;
@@ -743,15 +757,30 @@ __global__ void __launch_bounds__(T, 1)
             tc_after();
             const uint64_t dk0 = k0 + (uint64_t)((use % NK) * (BLOCK >> 4));
             const uint32_t d = S_COL + BJ * wg;
-            if (one) {
+            const auto mmas = [&](auto first, auto end) {
 #pragma unroll
-              for (int kk = 0; kk < QATOMS * 4; ++kk)
+              for (int kk = decltype(first)::value; kk < decltype(end)::value; ++kk)
                 mma_ta(d, Q_COL + 8 * kk, dk0 + (uint64_t)(((kk >> 2) * ATOM + (kk & 3) * 32) >> 4), kIdescQK, kk > 0);
+            };
+            using First = std::integral_constant<int, 0>;
+            using Middle = std::integral_constant<int, PART / ATOM * 4>;
+            using End = std::integral_constant<int, QATOMS * 4>;
+            if (one) {
+              mmas(First{}, Middle{});
+              commit(&bs.k_free[0][use % NK]);
+              ctl.issued[wg] = turn + 1;
+              ctl.uses[wg] = use;
+            }
+            __syncwarp();
+            go = __all_sync(0xffffffffu, ready_or_wait(bs.k_full[1], NK, use, abort));
+            if (!go) break;
+            if (one) {
+              mmas(Middle{}, End{});
               bar_arrive(&bs.s_next[wg]);
               commit(&bs.s_full[wg]);
-              commit(&bs.free[use % NK]);
+              commit(&bs.k_free[1][use % NK]);
               if (b + NS >= nblk) commit(&bs.q_done);
-              ctl.issued[wg] = turn + 1;
+              ctl.whole[wg] = turn + 1;
             }
             __syncwarp();
           }
@@ -798,7 +827,7 @@ __global__ void __launch_bounds__(T, 1)
           const int g = done + b, use = 2 * g + nh;
           bool go = ready_or_wait(bs.pv_go, NP, g, abort);
           if (b == 0) go = go && (full == 0 || ready_or_wait(&bs.o_free[nh], 1, full - 1, abort));
-          go = go && ready_or_wait(bs.full, NVF, use, abort);
+          go = go && ready_or_wait(bs.v_full, NVF, use, abort);
           ok = __all_sync(0xffffffffu, go);
           if (!ok) break;
           tc_after();
@@ -809,7 +838,7 @@ __global__ void __launch_bounds__(T, 1)
             for (int kk = 0; kk < BJ / 16; ++kk)
               mma_ss(256 * nh, dp0 + (uint64_t)((kk * 2 * MH * 16) >> 4), dv0 + (uint64_t)((kk * 2048) >> 4), kIdescPV,
                      (b > 0 || kk > 0) ? 1u : 0u);
-            commit(&bs.free[use % NV]);
+            commit(&bs.v_free[use % NV]);
             commit_multicast(&bs.p_free[g % NP], (uint16_t)3);
             if (b == nblk - 1) commit(&bs.o_full);
             ctl.issued[nh] = g + 1;
@@ -820,9 +849,9 @@ __global__ void __launch_bounds__(T, 1)
 #pragma unroll 1
         for (int i = 0; lane == 0 && ok && i < 2 * nblk; ++i) {
           const int use = 2 * done + i;
-          ok = use < NV || ready_or_wait(bs.free, NV, use - NV, abort);
+          ok = use < NV || ready_or_wait(bs.v_free, NV, use - NV, abort);
           if (!ok) break;
-          uint64_t* bar = &bs.full[use % NVF];
+          uint64_t* bar = &bs.v_full[use % NVF];
           bar_arrive_tx(bar, HALF_V);
           ctl.requested = use + 1;
           asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
@@ -914,11 +943,12 @@ __global__ void __launch_bounds__(T, 1)
   // MMAs and their arrivals in this CTA are over, and the S-CTA has the O-CTA's last P-buffer releases
   if (ok && done > 0) {
     if (rank == 0) {
-      for (int k = max(done + 2 * full - NK, 0); k < done + 2 * full; ++k) ok = ok && pipe_wait(bs.free, NK, k, abort);
+      for (int k = max(done + 2 * full - NK, 0); k < done + 2 * full; ++k)
+        ok = ok && pipe_wait(bs.k_free[0], NK, k, abort) && pipe_wait(bs.k_free[1], NK, k, abort);
       ok = ok && pipe_wait(&bs.q_done, 1, full - 1, abort);
       for (int b = done >= NP ? done - NP : 0; b < done; ++b) ok = ok && pipe_wait<true>(bs.p_free, NP, b, abort);
     } else {
-      ok = pipe_wait(bs.free, NV, 2 * done - 2, abort) && pipe_wait(bs.free, NV, 2 * done - 1, abort) &&
+      ok = pipe_wait(bs.v_free, NV, 2 * done - 2, abort) && pipe_wait(bs.v_free, NV, 2 * done - 1, abort) &&
            pipe_wait(bs.p_free, NP, done - 1, abort);
     }
   }
@@ -932,14 +962,18 @@ __global__ void __launch_bounds__(T, 1)
     __syncthreads();
     const int m = ctl.requested;
     if (rank == 0) {
-      for (int k = m >= NK ? m - NK : 0; k < m; ++k) pipe_wait(bs.full, NK, k, abort);
+      for (int k = m >= 2 * NK ? m - 2 * NK : 0; k < m; ++k) pipe_wait(bs.k_full[k & 1], NK, k >> 1, abort);
+      // an issuer commits a block's first MMAs to their part of its slot, and all of them to s_full: block g of issuer k
       for (int k = 0; k < NS; ++k)
-        if (ctl.issued[k] > 0) pipe_wait(&bs.s_full[k], 1, ctl.issued[k] - 1, abort);
+        if (const int g = k + NS * (ctl.issued[k] - 1); g >= 0) {
+          pipe_wait(bs.k_free[0], NK, ctl.uses[k], abort);
+          if (ctl.whole[k] == ctl.issued[k]) pipe_wait(&bs.s_full[k], 1, ctl.issued[k] - 1, abort);
+        }
     } else {
-      for (int k = m >= NV ? m - NV : 0; k < m; ++k) pipe_wait(bs.full, NVF, k, abort);
+      for (int k = m >= NV ? m - NV : 0; k < m; ++k) pipe_wait(bs.v_full, NVF, k, abort);
       // (each issuer's last block; a block that only one of them issued completes no phase: its slot's does)
       for (int k = 0; k < 2; ++k)
-        if (ctl.issued[k] > 0) pipe_wait(bs.free, NV, 2 * (ctl.issued[k] - 1) + k, abort);
+        if (ctl.issued[k] > 0) pipe_wait(bs.v_free, NV, 2 * (ctl.issued[k] - 1) + k, abort);
     }
   }
   tc_before();
