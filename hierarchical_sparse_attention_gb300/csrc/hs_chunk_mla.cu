@@ -180,6 +180,7 @@ __device__ __forceinline__ int64_t cost_of(int64_t before, int per_tile, int64_t
 __device__ __forceinline__ int blocks_of(int64_t tokens) { return tokens > 0 ? (int)((tokens + BJ - 1) / BJ) : 0; }
 
 __global__ void __launch_bounds__(kListThreads) chunk_list_kernel(const ChunkArgs a, const Work w, int pairs, uint32_t* __restrict__ err) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   pdl_wait();
   const int tid = threadIdx.x, per_tile = MH / a.num_heads;
   int64_t blocks = 0, listed = 0, cost = 0;
@@ -256,110 +257,141 @@ __global__ void __launch_bounds__(kListThreads) chunk_list_kernel(const ChunkArg
 
 constexpr int kRowsThreads = 384;
 
-// Two values to an f16 pair; those that it does not hold become zeros and set `bad`.
-__device__ __forceinline__ uint32_t to_f16(float2 v, bool& bad) {
-  const __half2 h = __floats2half2_rn(v.x, v.y);
-  uint32_t x = *reinterpret_cast<const uint32_t*>(&h);
-  const bool lo = (x & 0x7C00u) == 0x7C00u, hi = (x & 0x7C000000u) == 0x7C000000u;
-  if (lo) x &= 0xFFFF0000u;
-  if (hi) x &= 0x0000FFFFu;
-  bad |= lo || hi;
+// Pairs of f16 values: those that are not finite become zeros.
+__device__ __forceinline__ uint32_t without_bad(uint32_t x) {
+  if ((x & 0x7C00u) == 0x7C00u) x &= 0xFFFF0000u;
+  if ((x & 0x7C000000u) == 0x7C000000u) x &= 0x0000FFFFu;
   return x;
 }
+__device__ __forceinline__ uint32_t bits(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 
-// A CTA per block at a time. A thread has 32 values of a row, a warp eight rows of 128 (or 16 of 32) at a time, placed so
-// that eight lanes' stores meet every bank once. Within 32 values, chunk j of four takes pair j of each, the order of
-// columns that the read-out of O wants (and Q's values have); the place of chunk c of row x of a line's eight is c ^ x.
+// A CTA takes a run of blocks, one after the other. A thread has 32 values of a row, a warp eight rows of 128 (or 16 of 64) at
+// a time, placed so that eight lanes' stores meet every bank once. Within 32 values, chunk j of four takes pair j of each,
+// the order of columns that the read-out of O wants (and Q's values have); the place of chunk c of row x of a line's eight
+// is c ^ x. A scale that f16 holds (a power of two, say) multiplies in f16, which rounds the exact product; others in 32 bits.
 __global__ void __launch_bounds__(kRowsThreads) chunk_rows_kernel(const ChunkArgs a, const Work w, uint32_t* __restrict__ err) {
   extern __shared__ __align__(1024) uint8_t image[];
   __shared__ int s_entry;
   __shared__ int32_t s_row[BJ];
   __shared__ uint32_t s_there[2], s_bad[2];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   pdl_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int count = *w.count, total = *w.blocks;
-  for (int b = blockIdx.x; b < total; b += gridDim.x) {
-    // the last entry whose first block is at or before b
-    int lo = 0;
-    for (int n = count; n > 1;) {
-      const int step = (n + kRowsThreads - 1) / kRowsThreads, i = lo + tid * step;
-      if (i < lo + n && w.entries[i].block <= b && (i + step >= lo + n || w.entries[i + step].block > b)) s_entry = i;
-      __syncthreads();
-      n = min(step, lo + n - s_entry);
-      lo = s_entry;
-      __syncthreads();
+  const int from = (int)((int64_t)total * blockIdx.x / gridDim.x), end = (int)((int64_t)total * (blockIdx.x + 1) / gridDim.x);
+  if (from >= end) return;
+  // the last entry whose first block is at or before `from`
+  int at = 0;
+  for (int n = count; n > 1;) {
+    const int step = (n + kRowsThreads - 1) / kRowsThreads, i = at + tid * step;
+    if (i < at + n && w.entries[i].block <= from && (i + step >= at + n || w.entries[i + step].block > from)) s_entry = i;
+    __syncthreads();
+    n = min(step, at + n - s_entry);
+    at = s_entry;
+    __syncthreads();
+  }
+  Entry e = w.entries[at];
+  int next = at + 1 < count ? w.entries[at + 1].block : total;  // the entry's end
+  // the pool row of this thread's row of block b (-1: none; -2: none, where one should be)
+  const auto row_of = [&](int b) -> int32_t {
+    while (b >= next && at + 1 < count) {
+      e = w.entries[++at];
+      next = at + 1 < count ? w.entries[at + 1].block : total;
     }
-    const Entry e = w.entries[lo];
+    const int64_t t = (int64_t)(b - e.block) * BJ + tid;
+    if (t >= e.seq) return -1;
+    const int32_t p = (int32_t)t / a.page_size, page = a.block_tables[(int64_t)e.table * a.max_blocks + p];
+    const int64_t r = (int64_t)page * a.page_size + ((int32_t)t - p * a.page_size);
+    return page >= 0 && r < a.pool_rows ? (int32_t)r : -2;
+  };
+  int32_t mine = tid < BJ ? row_of(from) : -1;
+  bool missing = false;
+  for (int b = from; b < end; ++b) {
     if (tid < BJ) {
-      const int64_t t = (int64_t)(b - e.block) * BJ + tid;
-      int32_t row = -1;
-      if (t < e.seq) {
-        const int32_t p = (int32_t)t / a.page_size, page = a.block_tables[(int64_t)e.table * a.max_blocks + p];
-        const int64_t r = (int64_t)page * a.page_size + ((int32_t)t - p * a.page_size);
-        if (page >= 0 && r < a.pool_rows) row = (int32_t)r;
-        else atomicOr(err, HS_FLAG_DEVROW);
-      }
-      s_row[tid] = row;
-      const uint32_t there = __ballot_sync(0xffffffffu, row >= 0);
+      s_row[tid] = mine;
+      missing |= mine == -2;
+      const uint32_t there = __ballot_sync(0xffffffffu, mine >= 0);
       if (lane == 0) {
         s_there[warp] = there;
         s_bad[warp] = 0;
       }
+      if (b + 1 < end) mine = row_of(b + 1);
     }
     if (tid == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the last block has left
     __syncthreads();
-    const auto put = [&](int row, int g, int j, uint32_t x0, uint32_t x1, uint32_t x2, uint32_t x3) {
+    const auto put = [&](int row, int g, int j, const uint32_t (&x)[4]) {
       *reinterpret_cast<uint4*>(image + (g >> 1) * ATOM + (row >> 3) * 1024 + (row & 7) * 128 + ((((g & 1) * 4 + j) ^ (row & 7)) << 4)) =
-          make_uint4(x0, x1, x2, x3);
+          make_uint4(x[0], x[1], x[2], x[3]);
     };
+    // the codes of a thread's three tasks are on their way at once
+    uint32_t c[3][8];
+    float s[3];
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
       const int task = warp + k * (kRowsThreads / 32);
-      bool bad = false;
-      int row;
-      if (task < 32) {  // latents: rows 8 (task / 4) .., 128 values of scale task % 4
-        row = 8 * (task >> 2) + (lane & 7);
-        const int g = 4 * (task & 3) + (lane >> 3);
-        const int32_t r = s_row[row];
-        uint32_t c[8] = {};
-        float s = 0.f;
-        if (r >= 0) {
-          const uint8_t* src = a.pool + (int64_t)r * kFp8Row;
-          *reinterpret_cast<uint4*>(c) = __ldg(reinterpret_cast<const uint4*>(src + 32 * g));
-          *reinterpret_cast<uint4*>(c + 4) = __ldg(reinterpret_cast<const uint4*>(src + 32 * g) + 1);
-          s = __ldg(reinterpret_cast<const float*>(src + kFp8Scales) + (task & 3));
-        }
+      if (task >= 32) break;
+      // latents: rows 8 (task / 4) .., 128 values of scale task % 4
+      const int32_t r = s_row[8 * (task >> 2) + (lane & 7)];
+      const uint8_t* src = a.pool + (int64_t)max(r, 0) * kFp8Row;
+      const uint4* codes = reinterpret_cast<const uint4*>(src + 32 * (4 * (task & 3) + (lane >> 3)));
+      const uint4 zero = make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4*>(c[k]) = r >= 0 ? __ldg(codes) : zero;
+      *reinterpret_cast<uint4*>(c[k] + 4) = r >= 0 ? __ldg(codes + 1) : zero;
+      s[k] = r >= 0 ? __ldg(reinterpret_cast<const float*>(src + kFp8Scales) + (task & 3)) : 0.f;
+    }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint32_t x[4];
+    for (int k = 0; k < 3; ++k) {
+      const int task = warp + k * (kRowsThreads / 32);
+      __half2 top = __float2half2_rn(0.f);
+      uint32_t x[4][4];
+      int row, g;
+      if (task < 32) {
+        row = 8 * (task >> 2) + (lane & 7);
+        g = 4 * (task & 3) + (lane >> 3);
+        const __half one = __float2half_rn(s[k]);
+        const bool in_f16 = __half2float(one) == s[k];
+        const __half2 pair = __half2half2(one);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
-            const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c[2 * u + (j >> 1)] >> (16 * (j & 1))), __NV_E4M3);
-            const float2 v = __half22float2(__half2(h));
-            x[u] = to_f16(make_float2(v.x * s, v.y * s), bad);
+            const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c[k][2 * u + (j >> 1)] >> (16 * (j & 1))), __NV_E4M3);
+            __half2 v = __hmul2(__half2(h), pair);
+            if (!in_f16) {
+              const float2 f = __half22float2(__half2(h));
+              v = __floats2half2_rn(f.x * s[k], f.y * s[k]);
+            }
+            top = __hmax2_nan(top, __habs2(v));
+            x[j][u] = bits(v);
           }
-          put(row, g, j, x[0], x[1], x[2], x[3]);
-        }
       } else {  // RoPE: 16 rows, 64 values
         row = 16 * (task - 32) + 8 * (lane >> 4) + (lane & 7);
-        const int g = 16 + ((lane >> 3) & 1);
+        g = 16 + ((lane >> 3) & 1);
         const int32_t r = s_row[row];
-        uint32_t c[16] = {};
+        uint32_t y[16] = {};
         if (r >= 0) {
           const uint4* src = reinterpret_cast<const uint4*>(a.pool + (int64_t)r * kFp8Row + kFp8RopeAt + 64 * (g - 16));
 #pragma unroll
-          for (int u = 0; u < 4; ++u) *reinterpret_cast<uint4*>(c + 4 * u) = __ldg(src + u);
+          for (int u = 0; u < 4; ++u) *reinterpret_cast<uint4*>(y + 4 * u) = __ldg(src + u);
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint32_t x[4];
+        for (int j = 0; j < 4; ++j)
 #pragma unroll
-          for (int u = 0; u < 4; ++u)
-            x[u] = to_f16(make_float2(__uint_as_float(c[4 * u + j] << 16), __uint_as_float(c[4 * u + j] & 0xFFFF0000u)), bad);
-          put(row, g, j, x[0], x[1], x[2], x[3]);
-        }
+          for (int u = 0; u < 4; ++u) {
+            const __half2 v = __floats2half2_rn(__uint_as_float(y[4 * u + j] << 16), __uint_as_float(y[4 * u + j] & 0xFFFF0000u));
+            top = __hmax2_nan(top, __habs2(v));
+            x[j][u] = bits(v);
+          }
       }
-      if (bad) atomicOr(&s_bad[row >> 5], 1u << (row & 31));
+      if (without_bad(bits(top)) != bits(top)) {  // few
+        atomicOr(&s_bad[row >> 5], 1u << (row & 31));
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int u = 0; u < 4; ++u) x[j][u] = without_bad(x[j][u]);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) put(row, g, j, x[j]);
     }
     fence_async_smem();
     __syncthreads();
@@ -372,6 +404,7 @@ __global__ void __launch_bounds__(kRowsThreads) chunk_rows_kernel(const ChunkArg
     }
   }
   if (tid == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+  if (missing) atomicOr(err, HS_FLAG_DEVROW);
 }
 static_assert(kRowsThreads / 32 * 3 == 32 + BJ / 16, "three tasks a warp");
 
@@ -988,49 +1021,68 @@ __global__ void __launch_bounds__(T, 1)
 
 // ---------------------------------------------------------------- the join
 
-// The parts of a tile that pair blockIdx.y began and did not end, joined in their order as an online softmax over their
-// log-sum-exps. A thread per eight output dims.
-constexpr int kMergeThreads = 256;
+// The parts of a tile that pair blockIdx.y began and did not end, joined in their order, weighed by their log-sum-exps.
+// A CTA has kMergeRows query heads, a thread eight output dims of one; what it asks of memory it asks for at once (parts
+// one after the other, each found from the one before, took 47 us where a tile has 32).
+constexpr int kMergeRows = 4, kMergeThreads = kMergeRows * DL / 8;
+static_assert(kMergeThreads > kPairs, "a thread per pair");
 __global__ void __launch_bounds__(kMergeThreads) chunk_merge_kernel(const ChunkArgs a, const Work w, int pairs) {
+  __shared__ Pos s_start[kPairs + 1];
+  __shared__ int s_slot[kPairs];
+  __shared__ float s_lse[kMergeRows][kPairs], s_weight[kMergeRows][kPairs];
   pdl_wait();
-  const int p = blockIdx.y;
+  const int p = blockIdx.y, tid = threadIdx.x;
   const Pos from = w.starts[p], cut = w.starts[p + 1];
   if (cut.blk == 0 || (from.ent == cut.ent && from.tile == cut.tile && from.blk > 0)) return;
+  if (tid <= pairs) s_start[tid] = w.starts[tid];
   const Entry e = w.entries[cut.ent];
+  __syncthreads();
+  // pair q > p has a part if its work begins inside the tile and is not nothing: so many before it, in order
+  int n = 1;
+  {
+    bool part = false;
+    if (tid > p && tid < pairs) {
+      const Pos b = s_start[tid], c = s_start[tid + 1];
+      part = b.ent == cut.ent && b.tile == cut.tile && b.blk > 0 && !(b.ent == c.ent && b.tile == c.tile && b.blk == c.blk);
+    }
+    int at = 1;
+#pragma unroll
+    for (int k = 0; k < (kPairs + 31) / 32; ++k) {
+      const int here = __syncthreads_count(part && tid >> 5 == k);
+      if (tid >> 5 > k) at += here;
+      n += here;
+    }
+    at += __popc(__ballot_sync(0xffffffffu, part) & ((1u << (tid & 31)) - 1u));
+    if (part) s_slot[at] = 2 * tid;
+    if (tid == 0) s_slot[0] = 2 * p + 1;
+  }
+  __syncthreads();
   const int per_tile = MH / a.num_heads, first = cut.tile * per_tile, live = min(per_tile, e.nq - first) * a.num_heads;
-  const int m = (blockIdx.x * kMergeThreads + threadIdx.x) / (DL / 8), c8 = threadIdx.x % (DL / 8);
+  const int r = tid / (DL / 8), c8 = tid % (DL / 8), m = blockIdx.x * kMergeRows + r;
+  if (m < live)
+    for (int k = c8; k < n; k += DL / 8) s_lse[r][k] = w.part_lse[s_slot[k] * MH + m];
+  __syncthreads();
+  float top = -INFINITY;  // (a NaN leaves the maximum alone)
+  for (int k = 0; k < n; ++k) top = fmaxf(top, s_lse[r][k]);
+  const float ref = top == -INFINITY ? 0.f : top;
+  for (int k = c8; k < n; k += DL / 8) s_weight[r][k] = expf(s_lse[r][k] - ref);
+  __syncthreads();
   if (m >= live) return;
-  float acc[8] = {}, z = 0.f, top = -INFINITY;
-  Pos at = cut;
-  for (int q = p; q < pairs;) {
-    const int slot = 2 * q + (q == p ? 1 : 0);
-    const float x = w.part_lse[slot * MH + m];
-    const float4* src = reinterpret_cast<const float4*>(w.part_o + ((size_t)slot * MH + m) * DL) + 2 * c8;
+  float acc[8] = {}, z = 0.f;
+#pragma unroll 4
+  for (int k = 0; k < n; ++k) {
+    const float4* src = reinterpret_cast<const float4*>(w.part_o + ((size_t)s_slot[k] * MH + m) * DL) + 2 * c8;
     const float4 u = src[0], v = src[1];
-    const float mx = fmaxf(top, x), ref = mx == -INFINITY ? 0.f : mx;  // (a NaN leaves the maximum alone)
-    const float keep = expf(top - ref), f = expf(x - ref);
-    top = mx;
-    z = z * keep + f;
-    acc[0] = acc[0] * keep + f * u.x;
-    acc[1] = acc[1] * keep + f * u.y;
-    acc[2] = acc[2] * keep + f * u.z;
-    acc[3] = acc[3] * keep + f * u.w;
-    acc[4] = acc[4] * keep + f * v.x;
-    acc[5] = acc[5] * keep + f * v.y;
-    acc[6] = acc[6] * keep + f * v.z;
-    acc[7] = acc[7] * keep + f * v.w;
-    // the next pair with a part: one whose work begins here, and is not nothing
-    bool more = true;
-    do {
-      if (++q >= pairs) break;
-      const Pos next = w.starts[q + 1];
-      more = !(next.ent == at.ent && next.tile == at.tile && next.blk == at.blk);
-      if (more) {
-        // (pair q's part begins at `at`, inside the tile, if the part before it was cut there)
-        if (at.ent != cut.ent || at.tile != cut.tile || at.blk == 0) q = pairs;
-        at = next;
-      }
-    } while (!more);
+    const float f = s_weight[r][k];
+    z += f;
+    acc[0] += f * u.x;
+    acc[1] += f * u.y;
+    acc[2] += f * u.z;
+    acc[3] += f * u.w;
+    acc[4] += f * v.x;
+    acc[5] += f * v.y;
+    acc[6] += f * v.z;
+    acc[7] += f * v.w;
   }
   const float inv = z == 0.f ? 0.f : 1.f / z;
   uint32_t h[4];
@@ -1120,7 +1172,7 @@ cudaError_t launch_chunk_mla(const ChunkArgs& a, void* workspace, uint32_t* err,
     return e;
   }
   const int rows = MH / a.num_heads * a.num_heads;
-  return launch(chunk_merge_kernel, dim3((unsigned)((rows * (DL / 8) + kMergeThreads - 1) / kMergeThreads), (unsigned)pairs),
+  return launch(chunk_merge_kernel, dim3((unsigned)((rows + kMergeRows - 1) / kMergeRows), (unsigned)pairs),
                 kMergeThreads, 0, stream, a, w, pairs);
 }
 
