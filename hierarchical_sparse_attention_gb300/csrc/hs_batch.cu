@@ -55,22 +55,24 @@ __global__ void __launch_bounds__(kThreads) batch_plan_kernel(const BatchArgs a,
       if (r < 0 || flag) r = -1, from = to = 0;
       flags |= flag;
     }
-    int64_t sum;
-    const int64_t before = asked + cta_prefix<kThreads>(to - from, &sum);
-    asked += sum;
+    int64_t at[1] = {to - from}, sums[1];
+    cta_prefix<kThreads>(at, sums);
+    const int64_t before = asked + at[0];
+    asked += sums[0];
     if (to > from && before + (to - from) > a.max_tokens) {
       flags |= HS_FLAG_FULL;
       r = -1;
       from = to = 0;
     }
-    // (tokens that fit are those before some entry: the prefix over the accepted ones is the same sum)
-    const int64_t at = cta_prefix<kThreads>(to - from, &sum);
-    s_at[tid] = (int32_t)at;
+    at[0] = to - from;
+    cta_prefix<kThreads>(at, sums);
+    const int64_t sum = sums[0];
+    s_at[tid] = (int32_t)at[0];
     s_req[tid] = r;
     s_old[tid] = from;
     s_new[tid] = to;
     if (first_cta && i < a.n) {
-      a.token_offsets[i] = taken + (int32_t)at;
+      a.token_offsets[i] = taken + (int32_t)at[0];
       if (a.seq_lens) a.seq_lens[i] = to;
     }
     __syncthreads();

@@ -62,33 +62,42 @@ struct ChunkArgs {
 size_t chunk_workspace_bytes(int32_t n, int32_t num_heads, int32_t max_tokens, int64_t max_kv_tokens);
 cudaError_t launch_chunk_mla(const ChunkArgs& a, void* workspace, uint32_t* err, cudaStream_t stream);
 
-// Exclusive prefix sum of v over the CTA's kThreads threads; *total gets the sum. Called by every thread. Sums
+// Exclusive prefix sums of N values over the CTA's kThreads threads; total gets the sums. Called by every thread. Sums
 // are 64-bit.
-template <int kThreads>
-__device__ __forceinline__ int64_t cta_prefix(int64_t v, int64_t* total) {
+template <int kThreads, int N>
+__device__ __forceinline__ void cta_prefix(int64_t (&v)[N], int64_t (&total)[N]) {
   constexpr int kWarps = kThreads / 32;
-  static_assert(kThreads % 32 == 0 && kWarps <= 32, "one warp sums the warps");
-  __shared__ int64_t s_warp[kWarps];
+  static_assert(kThreads % 32 == 0, "whole warps");
+  __shared__ int64_t s_warp[N][kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int64_t x = v;
+  int64_t x[N];
 #pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
-    if (lane >= d) x += y;
-  }
+  for (int i = 0; i < N; ++i) x[i] = v[i];
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, x[i], d);
+      if (lane >= d) x[i] += y;
+    }
   __syncthreads();  // the last call's readers are done with s_warp
-  if (lane == 31) s_warp[warp] = x;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (lane == 31) s_warp[i][warp] = x[i];
   __syncthreads();
   // every thread sums the warps before its own (few: no second scan and barrier)
-  int64_t before = 0, all = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    const int64_t y = s_warp[w];
-    before += w < warp ? y : 0;
-    all += y;
+  for (int i = 0; i < N; ++i) {
+    int64_t before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const int64_t y = s_warp[i][w];
+      before += w < warp ? y : 0;
+      all += y;
+    }
+    total[i] = all;
+    v[i] = before + x[i] - v[i];
   }
-  *total = all;
-  return before + x - v;
 }
 
 }  // namespace hs

@@ -183,6 +183,7 @@ __global__ void __launch_bounds__(kListThreads) chunk_list_kernel(const ChunkArg
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   pdl_wait();
   const int tid = threadIdx.x, per_tile = MH / a.num_heads;
+  __shared__ Entry s_entry[kListThreads];  // the first ones
   int64_t blocks = 0, listed = 0, cost = 0;
   uint32_t flags = 0;
   for (int base = 0; base < a.n; base += kListThreads) {
@@ -199,21 +200,27 @@ __global__ void __launch_bounds__(kListThreads) chunk_list_kernel(const ChunkArg
         seq = 0;
       }
     }
+    // blocks asked for, and entries, in one sum: up to 2^41 and 2^10
+    constexpr int kBits = 20;
+    static_assert(kListThreads < (1 << kBits), "the entries of a run");
     const int64_t need = nq > 0 ? blocks_of(seq) : 0;
-    int64_t sum;
-    const int64_t before = blocks + cta_prefix<kListThreads>(need, &sum);
-    blocks += sum;
+    // (an entry that does not fit is given its cost all the same: which ones fit is not known yet)
+    int64_t at[2] = {need << kBits | (nq > 0), nq > 0 ? cost_of((int64_t)seq - nq, per_tile, (nq + per_tile - 1) / per_tile) : 0};
+    int64_t sum[2];
+    cta_prefix<kListThreads>(at, sum);
+    const int64_t before = blocks + (at[0] >> kBits), slot = listed + (at[0] & ((1 << kBits) - 1));
     if (need > 0 && (before + need) * BJ > a.max_kv_tokens) {
       flags |= HS_FLAG_FULL;
       seq = 0;
     }
-    const int64_t slot = listed + cta_prefix<kListThreads>(nq > 0, &sum);
-    listed += sum;
-    const int64_t mine = nq > 0 ? cost_of((int64_t)seq - nq, per_tile, (nq + per_tile - 1) / per_tile) : 0;
-    const int64_t cost0 = cost + cta_prefix<kListThreads>(mine, &sum);
-    cost += sum;
-    // (entries that fit are those before some entry: the sums over all that asked are theirs)
-    if (nq > 0) w.entries[slot] = {q0, nq, seq, i, cost0, (int32_t)min(before, a.max_kv_tokens / BJ), 0};
+    if (nq > 0) {
+      const Entry e = {q0, nq, seq, i, cost + at[1], (int32_t)min(before, a.max_kv_tokens / BJ), 0};
+      w.entries[slot] = e;
+      if (slot < kListThreads) s_entry[slot] = e;
+    }
+    blocks += sum[0] >> kBits;
+    listed += sum[0] & ((1 << kBits) - 1);
+    cost += sum[1];
   }
   if (flags) atomicOr(err, flags);
   if (tid == 0) {
@@ -222,21 +229,23 @@ __global__ void __launch_bounds__(kListThreads) chunk_list_kernel(const ChunkArg
   }
   __syncthreads();  // (the entries, which any thread reads now)
   if (tid > pairs) return;
+  const auto entry = [&](int i) -> Entry { return i < kListThreads ? s_entry[i] : w.entries[i]; };
+  const int used = (int)max(min((int64_t)pairs, cost / (kLeastPart * BJ)), (int64_t)1);  // pairs that get anything
   Pos at = {(int32_t)listed, 0, 0, 0};
-  if (tid < pairs && listed > 0) {
-    const int64_t x = cost / pairs * tid + cost % pairs * tid / pairs;
+  if (tid < used && listed > 0) {
+    const int64_t x = cost / used * tid + cost % used * tid / used;
     int lo = 0, hi = (int)listed - 1;  // the last entry that begins at or before x
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (w.entries[mid].cost <= x) lo = mid;
+      if (entry(mid).cost <= x) lo = mid;
       else hi = mid - 1;
     }
-    const Entry e = w.entries[lo];
+    const Entry e = entry(lo);
     const int tiles = (e.nq + per_tile - 1) / per_tile;
     const int64_t before = (int64_t)e.seq - e.nq, y = x - e.cost;
     // the last tile that begins at or before y: the root of the cost, a quadratic, put right by what rounding took
-    const double b = (double)(max(before, (int64_t)0) + kTileCost * BJ) + 0.5 * per_tile;
-    int64_t t = (int64_t)(2.0 * (double)y / (b + sqrt(b * b + 2.0 * per_tile * (double)y)));
+    const float b = (float)(max(before, (int64_t)0) + kTileCost * BJ) + 0.5f * per_tile;
+    int64_t t = (int64_t)(2.f * (float)y / (b + sqrtf(b * b + 2.f * per_tile * (float)y)));
     t = min(max(t, (int64_t)0), (int64_t)tiles - 1);
     while (t > 0 && cost_of(before, per_tile, t) > y) --t;
     while (t < tiles - 1 && cost_of(before, per_tile, t + 1) <= y) ++t;
@@ -269,7 +278,7 @@ __device__ __forceinline__ uint32_t bits(__half2 h) { return *reinterpret_cast<c
 // a time, placed so that eight lanes' stores meet every bank once. Within 32 values, chunk j of four takes pair j of each,
 // the order of columns that the read-out of O wants (and Q's values have); the place of chunk c of row x of a line's eight
 // is c ^ x. A scale that f16 holds (a power of two, say) multiplies in f16, which rounds the exact product; others in 32 bits.
-__global__ void __launch_bounds__(kRowsThreads) chunk_rows_kernel(const ChunkArgs a, const Work w, uint32_t* __restrict__ err) {
+__global__ void __launch_bounds__(kRowsThreads, 3) chunk_rows_kernel(const ChunkArgs a, const Work w, uint32_t* __restrict__ err) {
   extern __shared__ __align__(1024) uint8_t image[];
   __shared__ int s_entry;
   __shared__ int32_t s_row[BJ];
