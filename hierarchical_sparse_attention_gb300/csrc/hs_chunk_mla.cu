@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(kListThreads) chunk_list_kernel(const ChunkArg
 
 // ---------------------------------------------------------------- the rows
 
-constexpr int kRowsThreads = 384;
+constexpr int kRowsThreads = 192, HB = BJ / 2;  // a CTA has half a block at a time
 
 // Pairs of f16 values: those that are not finite become zeros.
 __device__ __forceinline__ uint32_t without_bad(uint32_t x) {
@@ -274,26 +274,28 @@ __device__ __forceinline__ uint32_t without_bad(uint32_t x) {
 }
 __device__ __forceinline__ uint32_t bits(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 
-// A CTA takes a run of blocks, one after the other. A thread has 32 values of a row, a warp eight rows of 128 (or 16 of 64) at
-// a time, placed so that eight lanes' stores meet every bank once. Within 32 values, chunk j of four takes pair j of each,
-// the order of columns that the read-out of O wants (and Q's values have); the place of chunk c of row x of a line's eight
-// is c ^ x. A scale that f16 holds (a power of two, say) multiplies in f16, which rounds the exact product; others in 32 bits.
-__global__ void __launch_bounds__(kRowsThreads, 3) chunk_rows_kernel(const ChunkArgs a, const Work w, uint32_t* __restrict__ err) {
-  extern __shared__ __align__(1024) uint8_t image[];
+// A CTA takes a run of half blocks (32 rows), one after the other. A thread has 32 values of a row, a warp eight rows of 128 (or 16
+// of 64) at a time. Within 32 values, chunk j of four takes pair j of each, the order of columns that the read-out of O
+// wants (and Q's values have); the place of chunk c of row x of a line's eight is c ^ x, so that a thread's four chunks are
+// half a line, two whole sectors. A scale that f16 holds (a power of two, say) multiplies in f16, which rounds the exact
+// product; others in 32 bits.
+// Bound by memory: 656 bytes read and 1,152 written a row. (Blocks of 64 rows through shared memory and a bulk copy each
+// were bound by their way, at 4.2 TB/s.)
+__global__ void __launch_bounds__(kRowsThreads, 6) chunk_rows_kernel(const ChunkArgs a, const Work w, uint32_t* __restrict__ err) {
   __shared__ int s_entry;
-  __shared__ int32_t s_row[BJ];
+  __shared__ int32_t s_row[2][HB];
   __shared__ uint32_t s_there[2], s_bad[2];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   pdl_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int count = *w.count, total = *w.blocks;
+  const int count = *w.count, total = 2 * *w.blocks;  // (below 2^26)
   const int from = (int)((int64_t)total * blockIdx.x / gridDim.x), end = (int)((int64_t)total * (blockIdx.x + 1) / gridDim.x);
   if (from >= end) return;
-  // the last entry whose first block is at or before `from`
+  // the last entry whose first block is at or before the run's
   int at = 0;
   for (int n = count; n > 1;) {
     const int step = (n + kRowsThreads - 1) / kRowsThreads, i = at + tid * step;
-    if (i < at + n && w.entries[i].block <= from && (i + step >= at + n || w.entries[i + step].block > from)) s_entry = i;
+    if (i < at + n && w.entries[i].block <= from >> 1 && (i + step >= at + n || w.entries[i + step].block > from >> 1)) s_entry = i;
     __syncthreads();
     n = min(step, at + n - s_entry);
     at = s_entry;
@@ -301,46 +303,47 @@ __global__ void __launch_bounds__(kRowsThreads, 3) chunk_rows_kernel(const Chunk
   }
   Entry e = w.entries[at];
   int next = at + 1 < count ? w.entries[at + 1].block : total;  // the entry's end
-  // the pool row of this thread's row of block b (-1: none; -2: none, where one should be)
-  const auto row_of = [&](int b) -> int32_t {
-    while (b >= next && at + 1 < count) {
+  // the pool row of lane's row of half block h (-1: none; -2: none, where one should be)
+  const auto row_of = [&](int h) -> int32_t {
+    while (h >> 1 >= next && at + 1 < count) {
       e = w.entries[++at];
       next = at + 1 < count ? w.entries[at + 1].block : total;
     }
-    const int64_t t = (int64_t)(b - e.block) * BJ + tid;
+    const int64_t t = (int64_t)(h - 2 * e.block) * HB + lane;
     if (t >= e.seq) return -1;
     const int32_t p = (int32_t)t / a.page_size, page = a.block_tables[(int64_t)e.table * a.max_blocks + p];
     const int64_t r = (int64_t)page * a.page_size + ((int32_t)t - p * a.page_size);
     return page >= 0 && r < a.pool_rows ? (int32_t)r : -2;
   };
-  int32_t mine = tid < BJ ? row_of(from) : -1;
+  uint32_t* state = reinterpret_cast<uint32_t*>(w.state);  // of half block h: words 4 (h / 2) + h % 2, and two after it
+  int32_t mine = warp == 0 ? row_of(from) : -1;
   bool missing = false;
-  for (int b = from; b < end; ++b) {
-    if (tid < BJ) {
-      s_row[tid] = mine;
+  for (int h = from; h < end; ++h) {
+    const int turn = h & 1;
+    if (warp == 0) {
+      s_row[turn][lane] = mine;
       missing |= mine == -2;
       const uint32_t there = __ballot_sync(0xffffffffu, mine >= 0);
       if (lane == 0) {
-        s_there[warp] = there;
-        s_bad[warp] = 0;
+        s_there[turn] = there;
+        s_bad[turn] = 0;
       }
-      if (b + 1 < end) mine = row_of(b + 1);
+      if (h + 1 < end) mine = row_of(h + 1);
     }
-    if (tid == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the last block has left
     __syncthreads();
-    const auto put = [&](int row, int g, int j, const uint32_t (&x)[4]) {
-      *reinterpret_cast<uint4*>(image + (g >> 1) * ATOM + (row >> 3) * 1024 + (row & 7) * 128 + ((((g & 1) * 4 + j) ^ (row & 7)) << 4)) =
-          make_uint4(x[0], x[1], x[2], x[3]);
-    };
+    if (tid == 0 && h > from) {
+      state[4 * ((h - 1) >> 1) + (turn ^ 1)] = s_there[turn ^ 1];
+      state[4 * ((h - 1) >> 1) + (turn ^ 1) + 2] = s_bad[turn ^ 1];
+    }
     // the codes of a thread's three tasks are on their way at once
     uint32_t c[3][8];
     float s[3];
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
       const int task = warp + k * (kRowsThreads / 32);
-      if (task >= 32) break;
+      if (task >= 16) break;
       // latents: rows 8 (task / 4) .., 128 values of scale task % 4
-      const int32_t r = s_row[8 * (task >> 2) + (lane & 7)];
+      const int32_t r = s_row[turn][8 * (task >> 2) + (lane & 7)];
       const uint8_t* src = a.pool + (int64_t)max(r, 0) * kFp8Row;
       const uint4* codes = reinterpret_cast<const uint4*>(src + 32 * (4 * (task & 3) + (lane >> 3)));
       const uint4 zero = make_uint4(0, 0, 0, 0);
@@ -354,7 +357,7 @@ __global__ void __launch_bounds__(kRowsThreads, 3) chunk_rows_kernel(const Chunk
       __half2 top = __float2half2_rn(0.f);
       uint32_t x[4][4];
       int row, g;
-      if (task < 32) {
+      if (task < 16) {
         row = 8 * (task >> 2) + (lane & 7);
         g = 4 * (task & 3) + (lane >> 3);
         const __half one = __float2half_rn(s[k]);
@@ -364,19 +367,19 @@ __global__ void __launch_bounds__(kRowsThreads, 3) chunk_rows_kernel(const Chunk
         for (int j = 0; j < 4; ++j)
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
-            const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c[k][2 * u + (j >> 1)] >> (16 * (j & 1))), __NV_E4M3);
-            __half2 v = __hmul2(__half2(h), pair);
+            const __half2_raw q = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c[k][2 * u + (j >> 1)] >> (16 * (j & 1))), __NV_E4M3);
+            __half2 v = __hmul2(__half2(q), pair);
             if (!in_f16) {
-              const float2 f = __half22float2(__half2(h));
+              const float2 f = __half22float2(__half2(q));
               v = __floats2half2_rn(f.x * s[k], f.y * s[k]);
             }
             top = __hmax2_nan(top, __habs2(v));
             x[j][u] = bits(v);
           }
       } else {  // RoPE: 16 rows, 64 values
-        row = 16 * (task - 32) + 8 * (lane >> 4) + (lane & 7);
+        row = 16 * (task - 16) + 8 * (lane >> 4) + (lane & 7);
         g = 16 + ((lane >> 3) & 1);
-        const int32_t r = s_row[row];
+        const int32_t r = s_row[turn][row];
         uint32_t y[16] = {};
         if (r >= 0) {
           const uint4* src = reinterpret_cast<const uint4*>(a.pool + (int64_t)r * kFp8Row + kFp8RopeAt + 64 * (g - 16));
@@ -393,29 +396,36 @@ __global__ void __launch_bounds__(kRowsThreads, 3) chunk_rows_kernel(const Chunk
           }
       }
       if (without_bad(bits(top)) != bits(top)) {  // few
-        atomicOr(&s_bad[row >> 5], 1u << (row & 31));
+        atomicOr(&s_bad[turn], 1u << row);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
           for (int u = 0; u < 4; ++u) x[j][u] = without_bad(x[j][u]);
       }
+      uint8_t* line = w.kv + (size_t)(h >> 1) * BLOCK + (g >> 1) * ATOM + turn * (HB * 128) + row * 128;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) put(row, g, j, x[j]);
-    }
-    fence_async_smem();
-    __syncthreads();
-    if (tid == 0) {
-      w.state[b] = make_uint4(s_there[0], s_there[1], s_bad[0], s_bad[1]);
-      asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n\tcp.async.bulk.commit_group;" ::"l"(
-                       w.kv + (size_t)b * BLOCK),
-                   "r"(smem_u32(image)), "r"(BLOCK)
-                   : "memory");
+      for (int j = 0; j < 4; j += 2) {  // two chunks: a sector
+        const int place = ((g & 1) * 4 + j) ^ (row & 7);
+        const bool swap = row & 1;
+        uint32_t y[8];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          y[u] = swap ? x[j + 1][u] : x[j][u];
+          y[4 + u] = swap ? x[j][u] : x[j + 1][u];
+        }
+        store8(reinterpret_cast<uint32_t*>(line + (place & 6) * 16), y, true);
+      }
     }
   }
-  if (tid == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+  __syncthreads();
+  if (tid == 0) {
+    const int h = end - 1;
+    state[4 * (h >> 1) + (h & 1)] = s_there[h & 1];
+    state[4 * (h >> 1) + (h & 1) + 2] = s_bad[h & 1];
+  }
   if (missing) atomicOr(err, HS_FLAG_DEVROW);
 }
-static_assert(kRowsThreads / 32 * 3 == 32 + BJ / 16, "three tasks a warp");
+static_assert(kRowsThreads / 32 * 3 == 16 + HB / 16, "three tasks a warp");
 
 // ---------------------------------------------------------------- the attention
 
@@ -549,7 +559,10 @@ __global__ void __launch_bounds__(T, 1)
   tc_after();
   // both CTAs' barriers are initialised before either arrives on the other's
   asm volatile("barrier.cluster.arrive.relaxed;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+  // the merge kernel may launch where SMs come free; it waits for this grid's completion before reading
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   pdl_wait();
+  asm volatile("fence.proxy.async;" ::: "memory");  // what the kernels before wrote, before this one's bulk copies of it
   const uint32_t tbase = ctl.taddr;
   const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
   const int head = (warp & 3) * 32 + lane;  // this thread's row of the tile = its tensor-memory lane
@@ -1022,8 +1035,6 @@ __global__ void __launch_bounds__(T, 1)
   __syncthreads();
   if (warp == 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tbase), "r"(TMEM_COLS) : "memory");
-  // the merge kernel may launch; it waits for this grid's completion before reading
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   cluster_sync_all();  // the partner no longer reads or arrives on this CTA's shared memory
   if (!ok && tid == 0) stay();
 }
@@ -1130,7 +1141,6 @@ cudaError_t pairs_resident(int* pairs) {
   if (e == cudaSuccess && dev < kDevices && (*pairs = known[dev].load(std::memory_order_acquire)) > 0) return e;
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(chunk_mla_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(chunk_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, BLOCK);
   *pairs = sms / 2 < 1 ? 1 : sms / 2 < kPairs ? sms / 2 : kPairs;
   if (e != cudaSuccess)
     (void)cudaGetLastError();
@@ -1154,9 +1164,9 @@ cudaError_t launch_chunk_mla(const ChunkArgs& a, void* workspace, uint32_t* err,
   CUtensorMap tm_q;
   if (e == cudaSuccess) e = q_map(&tm_q, a.q, (int64_t)a.max_tokens * a.num_heads);
   if (e == cudaSuccess) e = launch(chunk_list_kernel, dim3(1), kListThreads, 0, stream, a, w, pairs, err);
-  const int64_t blocks = a.max_kv_tokens / BJ, ctas = 6 * (int64_t)pairs;
+  const int64_t blocks = a.max_kv_tokens / HB, ctas = 12 * (int64_t)pairs;
   if (e == cudaSuccess && blocks > 0)
-    e = launch(chunk_rows_kernel, dim3((unsigned)(blocks < ctas ? blocks : ctas)), kRowsThreads, BLOCK, stream, a, w, err);
+    e = launch(chunk_rows_kernel, dim3((unsigned)(blocks < ctas ? blocks : ctas)), kRowsThreads, 0, stream, a, w, err);
   if (e != cudaSuccess) {
     (void)cudaGetLastError();
     return e;
