@@ -1018,9 +1018,9 @@ __global__ void __launch_bounds__(T, 1)
     const int m = ctl.requested;
     if (rank == 0) {
       for (int k = m >= 2 * NK ? m - 2 * NK : 0; k < m; ++k) pipe_wait(bs.k_full[k & 1], NK, k >> 1, abort);
-      // an issuer commits a block's first MMAs to their part of its slot, and all of them to s_full: block g of issuer k
+      // (an issuer commits a block's first MMAs to their part of its slot, and all of them to s_full)
       for (int k = 0; k < NS; ++k)
-        if (const int g = k + NS * (ctl.issued[k] - 1); g >= 0) {
+        if (ctl.issued[k] > 0) {
           pipe_wait(bs.k_free[0], NK, ctl.uses[k], abort);
           if (ctl.whole[k] == ctl.issued[k]) pipe_wait(&bs.s_full[k], 1, ctl.issued[k] - 1, abort);
         }
