@@ -9,8 +9,10 @@
 // that the hardware's rounding to e4m3 and the scale's comparison see which side of a border y is on. Rounded to nearest
 // at 24 bits instead, one code of some 300,000 falls on the other side, by a whole step (2^-3 of the value).
 //
-// What bounds them: memory; 1,816 bytes a token written (and its position's 256 bytes of the table, mostly in L2),
-// 1,812 a row read.
+// What bounds them, at 32,768 tokens written and 65,536 read back (42.9 us in a row; the bytes take 27.5): reading back, memory
+// (20.5 us, 5.9 TB/s); writing, the instructions of exact rounding (25.5 us, 74 % of the issue slots; its bytes take 10).
+// Tried: tokens in a loop, the next one's loads ahead (26.6); in 32 bits first, and exactly where values 2^-20 lower and
+// higher have other codes (25 to 27: the second conversion costs what it saves).
 #include "hs_chunk.h"
 
 #include <cuda_bf16.h>
@@ -41,11 +43,10 @@ __device__ __forceinline__ Pair add(Pair a, Pair b) {
 
 // v r.hi + v r.lo, rounded to odd: cut to 24 bits, the last one set where anything was cut off.
 __device__ __forceinline__ float times_odd(float v, Pair r) {
-  const float p = __fmul_rn(v, r.hi);
-  const float e = __fmaf_rn(v, r.lo, __fmaf_rn(v, r.hi, -p));
-  uint32_t b = __float_as_uint(p);
-  if (e < 0.f || e > 0.f) b = (b - ((__float_as_uint(e) ^ b) >> 31)) | 1u;  // (an e of the other sign: one below p)
-  return __uint_as_float(b);
+  const float c = __fmul_rn(v, r.lo), q = __fmaf_rz(v, r.hi, c);
+  const float left = __fadd_rn(__fmaf_rn(v, r.hi, -q), c);
+  // (r > 0: the sign is v's, a zero's too)
+  return __uint_as_float(__float_as_uint(q) | (__float_as_uint(v) & 0x80000000u) | (left != 0.f && fabsf(q) < INFINITY ? 1u : 0u));
 }
 
 __global__ void __launch_bounds__(kRowsThreads) fp8_pack_kernel(const Fp8RowsArgs a, uint32_t* __restrict__ err) {
@@ -65,15 +66,11 @@ __global__ void __launch_bounds__(kRowsThreads) fp8_pack_kernel(const Fp8RowsArg
     if (row >= 0 && lane == 0) atomicOr(err, bad_row ? HS_FLAG_DEVROW : HS_FLAG_SEQLEN);
     return;
   }
+  float cosine = 1.f, sine = 0.f;  // (on their way while the latents are worked on)
   if (a.rope_table) {
     const float* t = a.rope_table + (int64_t)pos * kFp8Rope + lane;
-    const float c = __ldg(t), s = __ldg(t + kFp8Rope / 2), x = bf16_lo(rope), y = bf16_hi(rope);
-    // each product's rounding error goes into the sum, so that cancellation does not show it
-    const float ys = __fmul_rn(y, s), yc = __fmul_rn(y, c);
-    const float u = __fsub_rn(__fmaf_rn(x, c, -ys), __fmaf_rn(y, s, -ys));
-    const float w = __fadd_rn(__fmaf_rn(x, s, yc), __fmaf_rn(y, c, -yc));
-    const __nv_bfloat162 h = __floats2bfloat162_rn(u, w);
-    rope = *reinterpret_cast<const uint32_t*>(&h);
+    cosine = __ldg(t);
+    sine = __ldg(t + kFp8Rope / 2);
   }
   const uint32_t xs[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
   float y[16];
@@ -89,14 +86,17 @@ __global__ void __launch_bounds__(kRowsThreads) fp8_pack_kernel(const Fp8RowsArg
     const bool finite = top < 0x7F80u;
     const int down = min(max(max((int)(top >> 7), (int)(__float_as_uint(sqrtf(a.norm_eps)) >> 23)) - 127, -125), 125);
     const float unit = __uint_as_float((uint32_t)(127 - down) << 23);
-    Pair sum = {0.f, 0.f};
+    // A lane's 16 squares (below 4, of 16 bits, exact in the product): their sum from 4 on, which no square is larger than, so that
+    // what each addition rounds off is what the square is over the difference, exactly. It is summed by itself.
+    float total = 4.f, off = 0.f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      y[2 * k] = __fmul_rn(bf16_lo(xs[k]), unit);
-      y[2 * k + 1] = __fmul_rn(bf16_hi(xs[k]), unit);
-      sum = add(sum, {__fmul_rn(y[2 * k], y[2 * k]), 0.f});  // squares of 8 bits: exact
-      sum = add(sum, {__fmul_rn(y[2 * k + 1], y[2 * k + 1]), 0.f});
+    for (int k = 0; k < 16; ++k) {
+      y[k] = __fmul_rn(k & 1 ? bf16_hi(xs[k >> 1]) : bf16_lo(xs[k >> 1]), unit);
+      const float more = __fmaf_rn(y[k], y[k], total);
+      off = __fadd_rn(off, __fmaf_rn(y[k], y[k], -__fsub_rn(more, total)));
+      total = more;
     }
+    Pair sum = add({total - 4.f, 0.f}, {off, 0.f});
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) {
       const Pair other = {__shfl_xor_sync(0xffffffffu, sum.hi, d), __shfl_xor_sync(0xffffffffu, sum.lo, d)};
@@ -139,6 +139,15 @@ __global__ void __launch_bounds__(kRowsThreads) fp8_pack_kernel(const Fp8RowsArg
     for (int k = 0; k < 8; ++k)
       c[k >> 1] |= (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(y[2 * k] * inv, y[2 * k + 1] * inv), __NV_SATFINITE, __NV_E4M3)
                    << (16 * (k & 1));
+  }
+  if (a.rope_table) {
+    // each product's rounding error goes into the sum, so that cancellation does not show it
+    const float x = bf16_lo(rope), z = bf16_hi(rope);
+    const float zs = __fmul_rn(z, sine), zc = __fmul_rn(z, cosine);
+    const float u = __fsub_rn(__fmaf_rn(x, cosine, -zs), __fmaf_rn(z, sine, -zs));
+    const float v = __fadd_rn(__fmaf_rn(x, sine, zc), __fmaf_rn(z, cosine, -zc));
+    const __nv_bfloat162 h = __floats2bfloat162_rn(u, v);
+    rope = *reinterpret_cast<const uint32_t*>(&h);
   }
   uint8_t* dst = a.pool + (int64_t)row * kFp8Row;
   *reinterpret_cast<uint4*>(dst + 16 * lane) = make_uint4(c[0], c[1], c[2], c[3]);
