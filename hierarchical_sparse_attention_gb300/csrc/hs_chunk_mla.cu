@@ -41,6 +41,7 @@
 #include <cuda_fp8.h>
 
 #include <atomic>
+#include <climits>
 #include <type_traits>
 
 namespace hs {
@@ -105,7 +106,9 @@ constexpr uint32_t kIdescPV = idesc(256, MH, true);
 constexpr int kTileCost = 5, kLeastPart = 4;
 constexpr int kPairs = 76;  // of CTAs, at most
 constexpr int kListThreads = 512;
-static_assert(kPairs < kListThreads, "a thread per pair");
+constexpr int kRowsThreads = 192, HB = BJ / 2;  // chunk_rows: a CTA has half a block at a time
+constexpr int kFoldEntries = 1024;  // up to so many entries each CTA of chunk_rows goes over them itself
+static_assert(kPairs < kRowsThreads && kPairs < kListThreads, "a thread per pair");
 
 // An entry with queries.
 struct __align__(16) Entry {
@@ -179,35 +182,39 @@ __device__ __forceinline__ int64_t cost_of(int64_t before, int per_tile, int64_t
 }
 __device__ __forceinline__ int blocks_of(int64_t tokens) { return tokens > 0 ? (int)((tokens + BJ - 1) / BJ) : 0; }
 
-__global__ void __launch_bounds__(kListThreads) chunk_list_kernel(const ChunkArgs a, const Work w, int pairs, uint32_t* __restrict__ err) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  pdl_wait();
+// What the call says of entry i: its first flat token, queries, and tokens.
+__device__ __forceinline__ uint32_t look_up(const ChunkArgs& a, int i, int32_t& q0, int32_t& nq, int32_t& seq) {
+  nq = seq = q0 = 0;
+  if (i >= a.n) return 0;
+  q0 = a.token_offsets[i];
+  const int32_t q1 = a.token_offsets[i + 1];
+  seq = a.seq_lens[i];
+  if (q0 < 0 || q1 < q0 || q1 > a.max_tokens) return HS_FLAG_SEQLEN;
+  nq = q1 - q0;
+  if (nq == 0 || (seq >= 0 && seq <= (int64_t)a.max_blocks * a.page_size)) return 0;
+  seq = 0;
+  return HS_FLAG_SEQLEN;
+}
+
+// The list, by a CTA of kThreads threads.
+template <int kThreads>
+__device__ __forceinline__ void list_entries(const ChunkArgs& a, const Work& w, int pairs, uint32_t* __restrict__ err) {
   const int tid = threadIdx.x, per_tile = MH / a.num_heads;
-  __shared__ Entry s_entry[kListThreads];  // the first ones
+  __shared__ Entry s_entry[kThreads];  // the first ones
   int64_t blocks = 0, listed = 0, cost = 0;
   uint32_t flags = 0;
-  for (int base = 0; base < a.n; base += kListThreads) {
+  for (int base = 0; base < a.n; base += kThreads) {
     const int i = base + tid;
-    int32_t q0 = 0, nq = 0, seq = 0;
-    if (i < a.n) {
-      q0 = a.token_offsets[i];
-      const int32_t q1 = a.token_offsets[i + 1];
-      seq = a.seq_lens[i];
-      if (q0 < 0 || q1 < q0 || q1 > a.max_tokens) flags |= HS_FLAG_SEQLEN;
-      else nq = q1 - q0;
-      if (nq > 0 && (seq < 0 || seq > (int64_t)a.max_blocks * a.page_size)) {
-        flags |= HS_FLAG_SEQLEN;
-        seq = 0;
-      }
-    }
+    int32_t q0, nq, seq;
+    flags |= look_up(a, i, q0, nq, seq);
     // blocks asked for, and entries, in one sum: up to 2^41 and 2^10
     constexpr int kBits = 20;
-    static_assert(kListThreads < (1 << kBits), "the entries of a run");
+    static_assert(kThreads < (1 << kBits), "the entries of a run");
     const int64_t need = nq > 0 ? blocks_of(seq) : 0;
     // (an entry that does not fit is given its cost all the same: which ones fit is not known yet)
     int64_t at[2] = {need << kBits | (nq > 0), nq > 0 ? cost_of((int64_t)seq - nq, per_tile, (nq + per_tile - 1) / per_tile) : 0};
     int64_t sum[2];
-    cta_prefix<kListThreads>(at, sum);
+    cta_prefix<kThreads>(at, sum);
     const int64_t before = blocks + (at[0] >> kBits), slot = listed + (at[0] & ((1 << kBits) - 1));
     if (need > 0 && (before + need) * BJ > a.max_kv_tokens) {
       flags |= HS_FLAG_FULL;
@@ -216,7 +223,7 @@ __global__ void __launch_bounds__(kListThreads) chunk_list_kernel(const ChunkArg
     if (nq > 0) {
       const Entry e = {q0, nq, seq, i, cost + at[1], (int32_t)min(before, a.max_kv_tokens / BJ), 0};
       w.entries[slot] = e;
-      if (slot < kListThreads) s_entry[slot] = e;
+      if (slot < kThreads) s_entry[slot] = e;
     }
     blocks += sum[0] >> kBits;
     listed += sum[0] & ((1 << kBits) - 1);
@@ -229,7 +236,7 @@ __global__ void __launch_bounds__(kListThreads) chunk_list_kernel(const ChunkArg
   }
   __syncthreads();  // (the entries, which any thread reads now)
   if (tid > pairs) return;
-  const auto entry = [&](int i) -> Entry { return i < kListThreads ? s_entry[i] : w.entries[i]; };
+  const auto entry = [&](int i) -> Entry { return i < kThreads ? s_entry[i] : w.entries[i]; };
   const int used = (int)max(min((int64_t)pairs, cost / (kLeastPart * BJ)), (int64_t)1);  // pairs that get anything
   Pos at = {(int32_t)listed, 0, 0, 0};
   if (tid < used && listed > 0) {
@@ -262,9 +269,14 @@ __global__ void __launch_bounds__(kListThreads) chunk_list_kernel(const ChunkArg
   w.starts[tid] = at;
 }
 
-// ---------------------------------------------------------------- the rows
+// (a call of many entries: otherwise a CTA of chunk_rows does it)
+__global__ void __launch_bounds__(kListThreads) chunk_list_kernel(const ChunkArgs a, const Work w, int pairs, uint32_t* __restrict__ err) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  pdl_wait();
+  list_entries<kListThreads>(a, w, pairs, err);
+}
 
-constexpr int kRowsThreads = 192, HB = BJ / 2;  // a CTA has half a block at a time
+// ---------------------------------------------------------------- the rows
 
 // Pairs of f16 values: those that are not finite become zeros.
 __device__ __forceinline__ uint32_t without_bad(uint32_t x) {
@@ -281,33 +293,82 @@ __device__ __forceinline__ uint32_t bits(__half2 h) { return *reinterpret_cast<c
 // product; others in 32 bits.
 // Bound by memory: 656 bytes read and 1,152 written a row. (Blocks of 64 rows through shared memory and a bulk copy each
 // were bound by their way, at 4.2 TB/s.)
-__global__ void __launch_bounds__(kRowsThreads, 6) chunk_rows_kernel(const ChunkArgs a, const Work w, uint32_t* __restrict__ err) {
+// kFold: the entries are not listed yet. The last CTA lists them, and the others find the run's in the call's arrays: the same few
+// loads as from a list, and a launch less (4 us of a call).
+template <bool kFold>
+__global__ void __launch_bounds__(kRowsThreads, 5) chunk_rows_kernel(const ChunkArgs a, const Work w, int pairs, uint32_t* __restrict__ err) {
   __shared__ int s_entry;
+  __shared__ int32_t s_first[kFold ? kFoldEntries : 1], s_seq[kFold ? kFoldEntries : 1];  // first blocks, tokens
   __shared__ int32_t s_row[2][HB];
   __shared__ uint32_t s_there[2], s_bad[2];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   pdl_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int count = *w.count, total = 2 * *w.blocks;  // (below 2^26)
-  const int from = (int)((int64_t)total * blockIdx.x / gridDim.x), end = (int)((int64_t)total * (blockIdx.x + 1) / gridDim.x);
+  if (kFold && blockIdx.x == gridDim.x - 1) {
+    list_entries<kRowsThreads>(a, w, pairs, err);
+    return;
+  }
+  const int ctas = gridDim.x - (kFold ? 1 : 0);
+  int count, total;  // entries (kFold: of the call), half blocks (below 2^26)
+  if (kFold) {
+    int64_t blocks = 0;
+    for (int base = 0; base < a.n; base += kRowsThreads) {
+      const int i = base + tid;
+      int32_t q0, nq, seq;
+      look_up(a, i, q0, nq, seq);
+      const int64_t need = nq > 0 ? blocks_of(seq) : 0;
+      int64_t before[1] = {need}, sum[1];
+      cta_prefix<kRowsThreads>(before, sum);
+      before[0] += blocks;
+      blocks += sum[0];
+      if (i < a.n) {
+        s_first[i] = (int32_t)min(before[0], a.max_kv_tokens / BJ);
+        s_seq[i] = nq > 0 && (before[0] + need) * BJ <= a.max_kv_tokens ? seq : 0;
+      }
+    }
+    __syncthreads();
+    count = a.n;
+    total = 2 * (int)min(blocks, a.max_kv_tokens / BJ);
+  } else {
+    count = *w.count;
+    total = 2 * *w.blocks;
+  }
+  const int from = (int)((int64_t)total * blockIdx.x / ctas), end = (int)((int64_t)total * (blockIdx.x + 1) / ctas);
   if (from >= end) return;
+  const auto first_of = [&](int i) { return i >= count ? INT_MAX : kFold ? s_first[i] : w.entries[i].block; };
   // the last entry whose first block is at or before the run's
   int at = 0;
-  for (int n = count; n > 1;) {
-    const int step = (n + kRowsThreads - 1) / kRowsThreads, i = at + tid * step;
-    if (i < at + n && w.entries[i].block <= from >> 1 && (i + step >= at + n || w.entries[i + step].block > from >> 1)) s_entry = i;
-    __syncthreads();
-    n = min(step, at + n - s_entry);
-    at = s_entry;
-    __syncthreads();
+  if (kFold) {
+    for (int hi = count - 1; at < hi;) {
+      const int mid = (at + hi + 1) >> 1;
+      if (s_first[mid] <= from >> 1) at = mid;
+      else hi = mid - 1;
+    }
+  } else {
+    for (int n = count; n > 1;) {
+      const int step = (n + kRowsThreads - 1) / kRowsThreads, i = at + tid * step;
+      if (i < at + n && first_of(i) <= from >> 1 && (i + step >= at + n || first_of(i + step) > from >> 1)) s_entry = i;
+      __syncthreads();
+      n = min(step, at + n - s_entry);
+      at = s_entry;
+      __syncthreads();
+    }
   }
-  Entry e = w.entries[at];
-  int next = at + 1 < count ? w.entries[at + 1].block : total;  // the entry's end
+  struct Run {
+    int block, seq, table;
+  };
+  const auto run_of = [&](int i) -> Run {
+    if (kFold) return {s_first[i], s_seq[i], i};
+    const Entry e = w.entries[i];
+    return {e.block, e.seq, e.table};
+  };
+  Run e = run_of(at);
+  int next = first_of(at + 1);  // the entry's end
   // the pool row of lane's row of half block h (-1: none; -2: none, where one should be)
   const auto row_of = [&](int h) -> int32_t {
-    while (h >> 1 >= next && at + 1 < count) {
-      e = w.entries[++at];
-      next = at + 1 < count ? w.entries[at + 1].block : total;
+    while (h >> 1 >= next) {
+      e = run_of(++at);
+      next = first_of(at + 1);
     }
     const int64_t t = (int64_t)(h - 2 * e.block) * HB + lane;
     if (t >= e.seq) return -1;
@@ -1163,10 +1224,12 @@ cudaError_t launch_chunk_mla(const ChunkArgs& a, void* workspace, uint32_t* err,
   cudaError_t e = pairs_resident(&pairs);
   CUtensorMap tm_q;
   if (e == cudaSuccess) e = q_map(&tm_q, a.q, (int64_t)a.max_tokens * a.num_heads);
-  if (e == cudaSuccess) e = launch(chunk_list_kernel, dim3(1), kListThreads, 0, stream, a, w, pairs, err);
-  const int64_t blocks = a.max_kv_tokens / HB, ctas = 12 * (int64_t)pairs;
-  if (e == cudaSuccess && blocks > 0)
-    e = launch(chunk_rows_kernel, dim3((unsigned)(blocks < ctas ? blocks : ctas)), kRowsThreads, 0, stream, a, w, err);
+  const bool fold = a.n <= kFoldEntries;
+  const int64_t blocks = a.max_kv_tokens / HB, ctas = 10 * (int64_t)pairs;
+  const unsigned rows_ctas = (unsigned)(blocks < ctas ? blocks : ctas);
+  if (e == cudaSuccess && !fold) e = launch(chunk_list_kernel, dim3(1), kListThreads, 0, stream, a, w, pairs, err);
+  if (e == cudaSuccess && (fold || rows_ctas > 0))
+    e = launch(fold ? chunk_rows_kernel<true> : chunk_rows_kernel<false>, dim3(rows_ctas + (fold ? 1 : 0)), kRowsThreads, 0, stream, a, w, pairs, err);
   if (e != cudaSuccess) {
     (void)cudaGetLastError();
     return e;
@@ -1190,6 +1253,9 @@ cudaError_t launch_chunk_mla(const ChunkArgs& a, void* workspace, uint32_t* err,
     (void)cudaGetLastError();
     return e;
   }
+  // a tile that has less than two of the least parts is not cut
+  constexpr int64_t kWhole = (2 * kLeastPart - 1) * BJ;
+  if ((int64_t)a.max_blocks * a.page_size <= kWhole || a.max_kv_tokens <= kWhole) return cudaSuccess;
   const int rows = MH / a.num_heads * a.num_heads;
   return launch(chunk_merge_kernel, dim3((unsigned)((rows + kMergeRows - 1) / kMergeRows), (unsigned)pairs),
                 kMergeThreads, 0, stream, a, w, pairs);
