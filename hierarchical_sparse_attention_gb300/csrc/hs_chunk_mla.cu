@@ -828,7 +828,7 @@ __global__ void __launch_bounds__(T, 1)
           };
           float up = 1.f;
           const float largest = take(std::false_type{}, 1.f);
-          if (__any_sync(0xffffffffu, !(largest >= 1.f && largest < 65504.f)) || a.sm_scale < 0.f) {
+          if (__any_sync(0xffffffffu, head < un.live && !(largest >= 1.f && largest < 65504.f)) || a.sm_scale < 0.f) {
             uint32_t top = 0;
 #pragma unroll 1
             for (int c = 0; c < 8 * QATOMS; ++c) top = max_bf16x2(top, *reinterpret_cast<const uint4*>(src + (c >> 3) * ATOM + ((c & 7) << 4)));
@@ -1060,12 +1060,12 @@ __global__ void __launch_bounds__(T, 1)
   if (ok && done > 0) {
     if (rank == 0) {
       for (int k = max(done + 2 * full - NK, 0); k < done + 2 * full; ++k)
-        ok = ok && pipe_wait(bs.k_free[0], NK, k, abort) && pipe_wait(bs.k_free[1], NK, k, abort);
-      ok = ok && pipe_wait(&bs.q_done, 1, full - 1, abort);
-      for (int b = done >= NP ? done - NP : 0; b < done; ++b) ok = ok && pipe_wait<true>(bs.p_free, NP, b, abort);
+        ok = ok && ready_or_wait(bs.k_free[0], NK, k, abort) && ready_or_wait(bs.k_free[1], NK, k, abort);
+      ok = ok && ready_or_wait(&bs.q_done, 1, full - 1, abort);
+      for (int b = done >= NP ? done - NP : 0; b < done; ++b) ok = ok && ready_or_wait<true>(bs.p_free, NP, b, abort);
     } else {
-      ok = pipe_wait(bs.v_free, NV, 2 * done - 2, abort) && pipe_wait(bs.v_free, NV, 2 * done - 1, abort) &&
-           pipe_wait(bs.p_free, NP, done - 1, abort);
+      ok = ready_or_wait(bs.v_free, NV, 2 * done - 2, abort) && ready_or_wait(bs.v_free, NV, 2 * done - 1, abort) &&
+           ready_or_wait(bs.p_free, NP, done - 1, abort);
     }
   }
   ok = __syncthreads_and(ok && !*abort);
