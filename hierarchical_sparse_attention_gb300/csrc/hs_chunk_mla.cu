@@ -103,7 +103,7 @@ constexpr uint32_t kIdescQK = idesc(BJ, MH, false);
 constexpr uint32_t kIdescPV = idesc(256, MH, true);
 
 // How the work is dealt out, in blocks: what a tile takes besides its blocks, and the least part of a tile.
-constexpr int kTileCost = 5, kLeastPart = 4;
+constexpr int kTileCost = 6, kLeastPart = 4;
 constexpr int kPairs = 76;  // of CTAs, at most
 constexpr int kListThreads = 512;
 constexpr int kRowsThreads = 192, HB = BJ / 2;  // chunk_rows: a CTA has half a block at a time
