@@ -765,7 +765,7 @@ HS_API hs_status hs_fp8_unpack_rows(int32_t n, const uint8_t* pool, int64_t pool
  * row is past the pool are left out, with HS_FLAG_DEVROW. An entry with more queries than seq_lens[i] has first
  * queries at negative positions, which see nothing. seq_lens[i] outside [0, max_blocks * page_size] makes its queries
  * see nothing (HS_FLAG_SEQLEN); token_offsets that are negative, fall or pass max_tokens leave the entry out
- * (HS_FLAG_SEQLEN). Flat tokens behind the last entry's keep what o and lse held.
+ * (HS_FLAG_SEQLEN); of flat tokens that two entries name, either's outputs stay. Flat tokens of no entry keep what o and lse held.
  *   q [max_tokens, num_heads, 576] bf16 bits, o [max_tokens, num_heads, 512] bf16 bits, kv_pool [pool_rows, 656] with
  *   pool_rows < 2^31: device, 16-byte aligned; lse [max_tokens, num_heads] fp32; token_offsets [n + 1], seq_lens [n],
  *   block_tables [n, max_blocks]: device; n <= HS_MAX_BATCH_ENTRIES, max_tokens <= HS_MAX_BATCH_TOKENS
@@ -774,8 +774,16 @@ HS_API hs_status hs_fp8_unpack_rows(int32_t n, const uint8_t* pool, int64_t pool
  *   sees nothing, like every later one that has tokens (HS_FLAG_FULL). A multiple of 64.
  *   workspace: hs_chunk_mla_workspace_bytes(n, num_heads, max_tokens, max_kv_tokens) device bytes, 256-byte aligned,
  *   contents of no matter; calls that share it must be ordered. error_flags: device uint32, HS_FLAG_* bits OR-ed in.
- * No allocation, no synchronisation; graph-capturable: lengths are read on the device, so that a captured call serves
- * every batch that its sizes hold. n == 0 or max_tokens == 0 is a no-op. */
+ *   Latents and RoPE values go through f16: exact where the scale is a power of two (hs_fp8_pack_rows writes such), else off by
+ *   2^-11 of themselves, and by 2^-25 where they are below 2^-14. A row with a value that is not finite, or above 65504, makes
+ *   the outputs of the queries that see it NaN, and only theirs. q goes through f16 over a power of two where that is needed:
+ *   any size, off by up to 2^-25 of the head's largest value. A row's weight is off by up to 2^-11 of itself, and by up to
+ *   2^-32 of the query's largest weight (of a part of the sequence) where it is below 2^-21 of that; lse takes weights as
+ *   they are. q . row and sm_scale x log2(e) x q . row have to be finite in fp32. An MMA pipeline that stands still for 100 ms
+ *   sets HS_FLAG_TIMEOUT and ends the call, its outputs not valid.
+ * The workspace is 40 MB for the parts of tiles that are cut, and 1,152 bytes per token of max_kv_tokens. Up to four kernel
+ * launches; no allocation, no synchronisation; the same arguments give the same result. Graph-capturable: lengths are read on the
+ * device, so that a captured call serves every batch that its sizes hold. n == 0 or max_tokens == 0 is a no-op. */
 HS_API size_t hs_chunk_mla_workspace_bytes(int32_t n, int32_t num_heads, int32_t max_tokens, int64_t max_kv_tokens);
 HS_API hs_status hs_chunk_mla(int32_t n, int32_t num_heads, int32_t max_tokens, const int32_t* token_offsets,
                               const int32_t* seq_lens, const uint16_t* q, const uint8_t* kv_pool, int64_t pool_rows,

@@ -2,8 +2,9 @@
 
 Per output element, with A_i = sum_j p_j |latent_ji|, B = max_j |sm| sum_d |q_d k_jd| of the head and C_i = sum_j
 |latent_ji| over the rows that it sees:
-* q goes through f16 over a power of two: off by up to 2^-25 where the head's largest is 2^14 .. 2^15, so 2^-39 of the
-  largest; under 2^-16 of B for heads and rows whose values are of like sizes, as here;
+* q goes through f16, over a power of two where the head's largest is below 1 or above 65504: off by up to 2^-25 of the
+  head's largest, and only where a value is below 2^-14 of it; under 2^-16 of B for heads and rows whose values are of like
+  sizes, as here;
 * latents go through f16: exact where the scale is a power of two (4 bits of code), else off by 2^-11 of themselves, and
   by 2^-25 where they are under 2^-14: r = 2^-11 of each, and nothing for powers of two. RoPE values of 8 bits: exact
   but for those under 2^-14, off by up to 2^-25 (their products are under 2^-16 of B);
@@ -304,6 +305,41 @@ def test_more_tiles_than_pairs():
     b = Batch(np.random.default_rng(52), 16, [(65 * i % 400 + 1, min(65 * i % 400 + 1, 5)) for i in range(1300)], 64)
     o, lse, _ = b.call(hs)
     b.check(o, lse, range(0, 1300, 29))
+
+
+def test_many_entries_few_of_them_with_tokens():
+    """More entries than one CTA of the kernels looks over at once, and few with queries; with and without room for all."""
+    hs = _gpu()
+    rng = np.random.default_rng(58)
+    for n in (1024, 1025, 5000):
+        entries = [(0, 0)] * n
+        for i in rng.permutation(n)[:25]:
+            entries[i] = (int(rng.integers(1, 700)), 1)
+        entries[n - 1], entries[0] = (130, 3), (65, 2)
+        entries = [(s, min(q, s)) for s, q in entries]
+        b = Batch(rng, 16, entries, 64)
+        o, lse, err = b.call(hs)
+        b.check(o, lse)
+        assert int(err.item()) == 0
+        o, lse, err = b.call(hs, kv_room=b.kv_room + 64 * 50)
+        b.check(o, lse)
+        o, lse, err = b.call(hs, kv_room=b.kv_room - 64)  # all but the last one
+        b.check(o, lse, [i for i in range(n - 1) if b.count[i]])
+        assert (lse[-3:] == -np.inf).all() and int(err.item()) == hs.HS_FLAG_FULL
+
+
+def test_sequences_around_the_shortest_that_is_cut():
+    """Seven, eight and nine blocks: below eight nothing is cut, and no join is launched where the sizes allow none."""
+    hs = _gpu()
+    for seq in (447, 448, 449, 511, 512, 513, 577):
+        b = Batch(np.random.default_rng(seq), 128, [(seq, 1)], 64)
+        b.max_blocks = -(-seq // 64)
+        b.tables = np.ascontiguousarray(b.tables[:, :b.max_blocks])
+        o, lse, err = b.call(hs)
+        b.check(o, lse)
+        b = Batch(np.random.default_rng(seq), 16, [(seq, 9), (seq - 3, 1)], 1)
+        o, lse, err = b.call(hs)
+        b.check(o, lse)
 
 
 def test_captured_and_replayed_with_other_lengths_and_two_graphs_of_one_workspace():
