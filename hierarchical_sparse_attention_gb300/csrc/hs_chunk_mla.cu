@@ -511,8 +511,6 @@ struct __align__(STATIC_BYTES) Control {
   uint32_t taddr;
   int abort;
   int issued[NS];  // blocks whose MMAs each issuer started (the last commit to wait for)
-  int uses[NS];    // S-CTA: the ring's use of the last one
-  int whole[NS];   // S-CTA: blocks whose MMAs it started all
   int requested;   // ring slots (S-CTA: parts of them) whose copies were started
 };
 static_assert(sizeof(Control) == STATIC_BYTES, "one block");
@@ -603,7 +601,7 @@ __global__ void __launch_bounds__(T, 1)
     bar_init(&bs.o_full, 2);
     for (int k = 0; k < 2; ++k) bar_init(&bs.o_free[k], 4 * NOUT);
     ctl.abort = 0;
-    for (int k = 0; k < NS; ++k) ctl.issued[k] = ctl.uses[k] = ctl.whole[k] = 0;
+    for (int k = 0; k < NS; ++k) ctl.issued[k] = 0;
     ctl.requested = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     if (rank == 1)
@@ -863,7 +861,7 @@ __global__ void __launch_bounds__(T, 1)
 #pragma unroll 1
           for (; go && b < nblk; b += NS, ++turn) {
             const int use = use0 + 2 + b;
-            go = ready_or_wait(bs.k_full[0], NK, use, abort);
+            go = ready_or_wait(bs.k_full[0], NK, use, abort) && ready_or_wait(bs.k_full[1], NK, use, abort);
             go = go && (turn == 0 || ready_or_wait(&bs.s_free[wg], 1, turn - 1, abort));
             // blocks in their order: issued side by side, two would take as long as both and leave their slots together
             const int before = done + b - 1;
@@ -882,21 +880,14 @@ __global__ void __launch_bounds__(T, 1)
             using Middle = std::integral_constant<int, PART / ATOM * 4>;
             using End = std::integral_constant<int, QATOMS * 4>;
             if (one) {
+              ctl.issued[wg] = turn + 1;
               mmas(First{}, Middle{});
               commit(&bs.k_free[0][use % NK]);
-              ctl.issued[wg] = turn + 1;
-              ctl.uses[wg] = use;
-            }
-            __syncwarp();
-            go = __all_sync(0xffffffffu, ready_or_wait(bs.k_full[1], NK, use, abort));
-            if (!go) break;
-            if (one) {
               mmas(Middle{}, End{});
               bar_arrive(&bs.s_next[wg]);
               commit(&bs.s_full[wg]);
               commit(&bs.k_free[1][use % NK]);
               if (b + NS >= nblk) commit(&bs.q_done);
-              ctl.whole[wg] = turn + 1;
             }
             __syncwarp();
           }
@@ -1079,12 +1070,8 @@ __global__ void __launch_bounds__(T, 1)
     const int m = ctl.requested;
     if (rank == 0) {
       for (int k = m >= 2 * NK ? m - 2 * NK : 0; k < m; ++k) pipe_wait(bs.k_full[k & 1], NK, k >> 1, abort);
-      // (an issuer commits a block's first MMAs to their part of its slot, and all of them to s_full)
       for (int k = 0; k < NS; ++k)
-        if (ctl.issued[k] > 0) {
-          pipe_wait(bs.k_free[0], NK, ctl.uses[k], abort);
-          if (ctl.whole[k] == ctl.issued[k]) pipe_wait(&bs.s_full[k], 1, ctl.issued[k] - 1, abort);
-        }
+        if (ctl.issued[k] > 0) pipe_wait(&bs.s_full[k], 1, ctl.issued[k] - 1, abort);
     } else {
       for (int k = m >= NV ? m - NV : 0; k < m; ++k) pipe_wait(bs.v_full, NVF, k, abort);
       // (each issuer's last block; a block that only one of them issued completes no phase: its slot's does)
