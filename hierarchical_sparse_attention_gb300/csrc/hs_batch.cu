@@ -8,6 +8,9 @@
 // Every CTA goes over all entries (three words each) in runs of its threads, with the run's prefix sums in shared
 // memory, and writes its share of the run's tokens and table rows: one launch, no workspace, nothing handed from CTA to
 // CTA. A step has tens to a thousand entries; up to kThreads of them are one run.
+//
+// What bounds it: the host. A call is 9 us of the caller's thread (19 arguments, one launch), the kernel 4 to 5 us of
+// dependent loads and barriers for 32 entries as for 1,024 with 47,000 tokens and 4 MB of block tables.
 #include "hs_chunk.h"
 
 namespace hs {

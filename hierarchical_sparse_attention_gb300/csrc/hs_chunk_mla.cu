@@ -4,9 +4,8 @@
 // Per query head of the token at position p, over the tokens t <= p of its sequence:
 //   s_t = sm_scale (q[:512] . latent_t + q[512:] . rope_t),  o = softmax(s) . latent,  lse = log sum_t exp s_t
 //
-// Four kernels:
-//   - chunk_list: the entries with queries, where each sequence's rows go in the workspace, and the work dealt out evenly;
-//   - chunk_rows: every sequence's rows once, from their pages, as f16 in blocks of 64 rows laid out as the tensor cores
+// Three kernels (four for more than 1,024 entries):
+//   - chunk_rows: the list of the entries with queries and the work dealt out evenly; and every sequence's rows once, from their pages, as f16 in blocks of 64 rows laid out as the tensor cores
 //     read them, so that the attention brings a block in with one bulk copy and no arithmetic;
 //   - chunk_mla: tiles of 128 query heads (all heads of as many tokens of an entry as fit) over their blocks;
 //   - chunk_merge: joins the parts of tiles that were cut.
@@ -24,11 +23,27 @@
 // The roles hand blocks over through mbarriers with bounded waits, and run on from tile to tile: Q comes through the ring of
 // K's slots (a slot holds a block of 64 rows of 576 values, or half of Q), V through a ring of half blocks.
 //
+// What bounds it (256 tokens x 128 heads behind 48,000: 1.95 ms, 1,760 TFLOP/s, 0.91 of cuBLAS's bf16 burst and above what it
+// sustains): a block takes a pair 0.77 us, 1,400 clocks at the 1.8 GHz that the power limit leaves, of which the S-CTA's 36 MMAs are
+// 1,150 and the O-CTA's 8 are 1,024. Then a tile's change, 3.7 us (the last S 0.9, Q's copy and its way to tensor memory 2.4,
+// K's ring, which Q has taken, full again), a third of a first chunk's time. What each part brought
+// (256 tokens behind 48,000, or a first chunk of 2,048):
+//   P stored 512 bytes a warp instead of 16 bytes a line (see pdesc)       2,712 -> 2,025 us
+//   S with an issuer per buffer: a commit holds its thread up, 500 clocks with a block's MMAs queued before it, and the waits
+//   for the next block 300 more, in which another thread's MMAs keep the tensor core busy    2,744 -> 2,712
+//   P . V with an issuer per half of O, K's slots in two parts, four P buffers, blocks in order    2,051 -> 1,966
+//   Q brought by the issuing warps while the softmax is at the tile before    650 -> 531
+//   the read-out by eight warps, halves of O handed back as they are read, the corrector at the next tile    531 -> 485
+//   a block's MMAs issued in one go, a tile's own cost of six blocks    471 -> 444
+// Tried, not kept: rows fetched into L2 six blocks ahead (2,470 us); a look at a barrier and a branch between a block's MMAs
+// (2,640: their operands leave the uniform registers); slots in three parts (no change); rows of short batches brought by
+// the pair itself, through the O-CTA's reading-out warps (a decode step 68 -> 142 us: too few loads in flight).
+//
 // Precision. Latents (e4m3 x scale) and RoPE values go through f16: exact where the scale is a power of two, else off by 2^-11
 // of themselves, and by 2^-25 where they are below 2^-14. Q goes through f16, over a power of two where its head's
-// largest value is below 1 or above 65504, which goes into its scores' scale: off by 2^-25 of the head's largest. P, whose reference weighs 2^7, is rounded to f16: by up to
-// 2^-11 of a weight, and by 2^-32 of the largest weight where it is below 2^-21 of that; its sum takes weights
-// unrounded, so lse does not see it. Scores, maxima, sums and O are in 32 bits.
+// largest value is below 1 or above 65504, which goes into its scores' scale: off by 2^-25 of the head's largest. P, whose
+// reference weighs 2^7, is rounded to f16: by up to 2^-11 of a weight, and by 2^-32 of the largest weight where it is below
+// 2^-21 of that; its sum takes weights unrounded, so lse does not see it. Scores, maxima, sums and O are in 32 bits.
 //
 // NaN, infinities and values that f16 does not hold. A row that a query does not see gets P = 0, and 0 x NaN must not reach O:
 // such values are zeros in the blocks, and a mark for their row makes its score NaN for the queries that see it, and so
@@ -65,16 +80,14 @@ constexpr uint32_t TMEM_COLS = 512, Q_COL = 0, S_COL = 288;
 static_assert(S_COL + NS * BJ <= TMEM_COLS, "Q and the S buffers fit tensor memory");
 // S-CTA warps: 0-11 softmax, 12-14 issuers, 15 copies, and 12-15 bring Q; O-CTA: 0-3 corrector, 4-11 read out, 12 and 13
 // issuers, 15 copies.
-// S has an issuer per buffer: a commit takes its thread some 500 clocks with a block's MMAs before it, and the waits for
-// the next block 300 more, in which another thread's MMAs keep the tensor core busy (one issuer for all of S: 2,050 clocks
-// a block, of which its 36 MMAs are 1,150).
+// S has an issuer per buffer, P . V one per half of O.
 constexpr int ISSUER = 12, COPIER = 15, OUT = 4, NOUT = 2;  // NOUT warps read out a quarter of the heads
 
 constexpr uint32_t ATOM = BJ * 128, BLOCK = QATOMS * ATOM, HALF_V = ATOMS / 2 * ATOM;
 constexpr uint32_t S_RING = 0;
 // A slot of K is filled and handed back in two parts (values 0 - 319, and the rest), so that the next block's copies start while
-// the tensor core is at the second: three slots cover a copy's way (measured, clocks: 860 from a commit to the copy's
-// start, 1,680 to its end) and a block's MMAs (1,150) only so.
+// the tensor core is at the second: three slots cover a copy's way (860 clocks from a commit to the copy's start, 1,680 to
+// its end) and a block's MMAs (1,150) only so.
 constexpr uint32_t PART = 5 * ATOM;
 constexpr uint32_t S_REF = NK * BLOCK;             // the reference maxima, handed from block to block
 constexpr uint32_t S_UP = S_REF + MH * 4;          // what a head's Q was divided by, of the last NQ tiles
